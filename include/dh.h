@@ -321,6 +321,109 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
                     void* stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Distillation from a teacher's top logits: the loss of a student's logits and its gradient
+ * (training the candidate head).
+ *
+ * The pages describe the low-rank head, not how it is trained.  The head's own two stages give what
+ * a teacher needs: candidate ids and their exact logits (idx_out and logits_out of dh_draft_head)
+ * are the top logits of the full-rank head, and the student's logits are the low-rank head's scores
+ * over the whole vocabulary.  Row n has student logits z[0..vocab) and teacher entries
+ * (idx[n,k], teacher[n,k]) for k < n_valid[n] (n_valid NULL: all K; values outside [0, K] are
+ * clamped); an entry whose id is outside [0, vocab) is left out.  At temperature T:
+ *   p = softmax over the row's entries of teacher / T,    q = softmax over the vocabulary of z / T
+ *   loss[n]   = T^2 sum_k p_k (log p_k - log q[idx_k])              (0 log 0 = 0)
+ *   grad[n,v] = grad_loss[n] T (q[v] - sum of the p_k with idx_k = v)   (the gradient of
+ *               sum_n grad_loss[n] loss[n]; an id may come more than once)
+ *   stats[n]  = (m, s): m = max_v z[v] and s = sum_v exp((z[v] - m)/T)
+ * Sums, exponents and loss in fp32; the gradient is rounded once to `dtype`.
+ * - A row without entries (or with none above -inf) has loss 0 and gradient 0.  A row with
+ *   grad_loss 0 has gradient 0.  The gradient reads neither kind's logits.
+ * - A student logit of -inf has q = 0; where the teacher's p is positive there the loss is +inf and
+ *   the gradient grad_loss T (-p).  A row of -inf: stats (-inf, 0), q = 0 everywhere.
+ * - A NaN or +inf student logit, or a NaN or +inf teacher entry, makes that row's loss and gradient
+ *   NaN; other rows are not affected.
+ *
+ * dh_distill_topk: loss_out [N] and stats_out [N x 2] (may be NULL).
+ * dh_distill_topk_backward: grad_out from the stats of a forward call on the same inputs.
+ * dh_distill_topk_step: loss_out and grad_out in one call, for a caller that knows grad_loss.
+ *
+ * logits [N x vocab], `dtype`, rows row_stride elements apart (>= 0; any element alignment); idx
+ * int32, teacher fp32 [N x K]; n_valid int32 [N]; grad_loss fp32 [N]; loss_out fp32 [N]; stats fp32
+ * [N x 2], 8-byte aligned; grad_out `dtype`, rows grad_stride >= vocab elements apart: all device.
+ * grad_out may be the logits themselves (same address and stride); otherwise the two must not
+ * overlap.  Elements between the rows are left as they were.  Rows that start on 16 bytes (address
+ * and strides) are the fastest.  K <= DH_MAX_K, vocab <= DH_MAX_VOCAB, temperature > 0 and finite.
+ * Workspaces: 256-byte aligned, not zeroed, not shared by calls that overlap in time.  N = 0 is a
+ * no-op.  Results repeat bit for bit.
+ * ------------------------------------------------------------------------------------------- */
+size_t dh_distill_topk_workspace(int N, int vocab, int dtype);
+int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                    const int32_t* n_valid, int N, int vocab, int K, int dtype, float temperature, float* loss_out,
+                    float* stats_out, void* workspace, size_t ws_bytes, void* stream);
+int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                             const int32_t* n_valid, const float* stats, const float* grad_loss, int N, int vocab,
+                             int K, int dtype, float temperature, void* grad_out, int64_t grad_stride, void* stream);
+size_t dh_distill_topk_step_workspace(int N, int vocab, int dtype);
+int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                         const int32_t* n_valid, const float* grad_loss, int N, int vocab, int K, int dtype,
+                         float temperature, float* loss_out, void* grad_out, int64_t grad_stride, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Beam selection over whole vocabulary rows.
+ *
+ * AlphaSignal page, section "Runtime-sized speculation": a top-k of 1 drafts a chain, larger k a
+ * tree.  dh_expand_children chooses per node among its candidates and dh_size_level among few
+ * children; this call chooses, per request, among every continuation of its W beams:
+ *   s[r,w,v] = score[r,w] + z[r,w,v]/T - log sum_v' exp(z[r,w,v']/T)
+ *   the M best (w, v) by (s desc, w asc, v asc) -> parent_out = w, token_out = v, score_out = s
+ * - finished[r,w] != 0 (NULL: none): the beam has one candidate, token pad_token at score[r,w], and
+ *   its logits are not read; among equal scores it ranks as its beam's first token.
+ * - A beam whose score is not finite (-inf: an unused one) has no candidate, nor has one whose row
+ *   holds a NaN or +inf or nothing above -inf, nor a logit of -inf.
+ * - Where fewer than M candidates exist the rest is parent -1, token -1, score -inf.
+ * Candidates are ordered by their scores in 64 bits (the normalisers' sums carry the error of fp32
+ * exponentials, about 1e-8); score_out is the score rounded to fp32.
+ *
+ * logits `dtype`: request r's beam w at logits + r request_stride + w beam_stride (elements, >= 0,
+ * any element alignment; 0: shared rows); score fp32, finished int32 [R x W]; parent_out, token_out
+ * int32, score_out fp32 [R x M]: device.  W <= DH_MAX_BEAMS, M <= DH_MAX_BEAM_OUT, vocab <=
+ * DH_MAX_VOCAB, temperature > 0 and finite.  Workspace: dh_beam_select_workspace bytes, 256-byte
+ * aligned, not zeroed, not shared by calls that overlap in time.  R = 0 is a no-op.
+ * ------------------------------------------------------------------------------------------- */
+#define DH_MAX_BEAMS 128
+#define DH_MAX_BEAM_OUT 256
+size_t dh_beam_select_workspace(int R, int W, int vocab, int dtype);
+int dh_beam_select(const void* logits, int64_t request_stride, int64_t beam_stride, const float* score,
+                   const int32_t* finished, int R, int W, int vocab, int M, int dtype, float temperature,
+                   int pad_token, int32_t* parent_out, int32_t* token_out, float* score_out, void* workspace,
+                   size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Reordering states after a selection.
+ *
+ * AlphaSignal page, section "Runtime-sized speculation" (the draft's key-value cache is extended
+ * between rounds instead of rebuilt): the drafter's states follow the beams that a selection kept
+ * (parent_out of dh_beam_select), and the states of a draft tree's accepted path (path_out of
+ * dh_tree_accept) are appended to the committed ones.  For every a < A, r < R, j < M, h < H and
+ * t < min(T, lengths[r]):
+ *   dst[a, r, dst_base[r] + j, h, t] = src[a, r, src_base[r] + idx[r,j], h, t]
+ * where idx[r,j] >= 0 and both slots exist (source in [0, src_slots), target in [0, dst_slots));
+ * everything else of dst stays as it was.  Each [a, r, slot, h, t] is unit_bytes contiguous bytes;
+ * src_strides and dst_strides (host arrays) are the byte strides of (a, r, slot, h, t).
+ * In place (dst == src, equal strides and slots): as if every source were read before any target is
+ * written.  Otherwise the memory that src and dst span must not overlap.
+ * idx int32 [R x M]; lengths, src_base, dst_base int32 [R] or NULL (T, 0, 0): device.  The elements
+ * of dst must be distinct.  M <= DH_MAX_SLOTS.  Fastest where addresses, strides and unit_bytes are
+ * multiples of 16.  No workspace.  A zero size is a no-op.
+ * ------------------------------------------------------------------------------------------- */
+#define DH_MAX_SLOTS 1024
+int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, const int64_t* dst_strides,
+                      const int32_t* idx, const int32_t* lengths, const int32_t* src_base, const int32_t* dst_base,
+                      int A, int R, int src_slots, int dst_slots, int M, int H, int T, int64_t unit_bytes,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Greedy draft-tree acceptance without a caller-provided workspace (no counterpart on the pages:
  * it is an interface for callers, not part of the method).
  *

@@ -8,7 +8,11 @@ __version__ = "1.0.0"
 
 def __getattr__(name):
     if name in ("lowrank_topk", "exact_rescore", "tree_accept", "prof_enable", "prof_read",
-                "load_library", "DhError", "Workspace"):
+                "load_library", "DhError", "Workspace", "distill_topk", "distill_topk_backward", "distill_topk_step",
+                "beam_select", "reorder_states"):
         from . import binding
         return getattr(binding, name)
+    if name == "distill_loss":
+        from . import distill
+        return distill.distill_loss
     raise AttributeError(name)

@@ -27,7 +27,12 @@ EXPORTS = ["dh_status_string", "dh_version", "dh_last_error", "dh_lowrank_topk_w
            "dh_tree_accept", "dh_tree_accept_noalloc", "dh_workspace_status", "dh_selftest_wait_timeout", "dh_prof_enable", "dh_prof_read",
            "dh_set_tuning", "dh_verify_chain_workspace", "dh_verify_chain", "dh_size_level",
            "dh_lowrank_topk_shard", "dh_merge_topk", "dh_exact_rescore_shard_workspace", "dh_exact_rescore_shard",
-           "dh_combine_softmax"]
+           "dh_combine_softmax",
+           "dh_distill_topk_workspace", "dh_distill_topk", "dh_distill_topk_backward",
+           "dh_distill_topk_step_workspace", "dh_distill_topk_step",
+           "dh_beam_select_workspace", "dh_beam_select", "dh_reorder_states"]
+
+MAX_K, MAX_BEAMS, MAX_BEAM_OUT, MAX_SLOTS = 1024, 128, 256, 1024  # DH_MAX_*
 
 _lib = None
 _lock = threading.Lock()
@@ -100,6 +105,23 @@ def load_library(path: str | None = None):
         lib.dh_exact_rescore_shard.restype = I
         lib.dh_combine_softmax.argtypes = [P, P, I, I, I, P, P, P]
         lib.dh_combine_softmax.restype = I
+        L, F = ctypes.c_int64, ctypes.c_float
+        lib.dh_distill_topk_workspace.argtypes = [I, I, I]
+        lib.dh_distill_topk_workspace.restype = Z
+        lib.dh_distill_topk.argtypes = [P, L, P, P, P, I, I, I, I, F, P, P, P, Z, P]
+        lib.dh_distill_topk.restype = I
+        lib.dh_distill_topk_backward.argtypes = [P, L, P, P, P, P, P, I, I, I, I, F, P, L, P]
+        lib.dh_distill_topk_backward.restype = I
+        lib.dh_distill_topk_step_workspace.argtypes = [I, I, I]
+        lib.dh_distill_topk_step_workspace.restype = Z
+        lib.dh_distill_topk_step.argtypes = [P, L, P, P, P, P, I, I, I, I, F, P, P, L, P, Z, P]
+        lib.dh_distill_topk_step.restype = I
+        lib.dh_beam_select_workspace.argtypes = [I, I, I, I]
+        lib.dh_beam_select_workspace.restype = Z
+        lib.dh_beam_select.argtypes = [P, L, L, P, P, I, I, I, I, I, F, I, P, P, P, P, Z, P]
+        lib.dh_beam_select.restype = I
+        lib.dh_reorder_states.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, L, P]
+        lib.dh_reorder_states.restype = I
         lib.dh_set_tuning.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
         lib.dh_set_tuning.restype = I
         if path is None:
@@ -429,6 +451,295 @@ def verify_chain(logits, cand_idx, cand_prob, draft_token, u_accept, u_sample, *
                                _ptr(u_sample), B, L, vocab, K, dt, float(temperature), _ptr(n_accept_out),
                                _ptr(token_out), _ptr(ws), nbytes, _stream(stream)), "dh_verify_chain")
     return n_accept_out, token_out
+
+
+# ---------------------------------------------------------------- training, search and state operators
+#
+# These calls take strided rows and run on the device of their tensors, whichever is current.  Their
+# scratch needs no zeroing, so without `workspace` each call takes its own from the caching allocator
+# on its stream: calls on different streams, and graphs captured from them, share nothing.  With an
+# explicit `stream` the results belong to that stream, and the inputs are kept from being reused by
+# the allocator until the stream has passed the call (the caller orders the stream behind whatever
+# wrote the inputs).
+
+
+class _On:
+    """The device and stream of a call: the tensors' device, `stream` or the current one."""
+
+    def __init__(self, dev, stream, inputs):
+        for name, t in inputs.items():
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.dev, self.given, self.inputs = dev, stream, inputs
+        self.ctx = None
+
+    def __enter__(self):
+        if self.given is not None:
+            self.ctx = torch.cuda.stream(self.given)
+        elif self.dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        self.stream = self.given if self.given is not None else torch.cuda.current_stream(self.dev)
+        return self
+
+    def __exit__(self, *exc):
+        if self.given is not None and not torch.cuda.is_current_stream_capturing():
+            for t in self.inputs.values():
+                if t is not None:
+                    t.record_stream(self.given)
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def scratch(self, nbytes, workspace, kind):
+        """nbytes of device memory, not zeroed: the caller's workspace object's, else fresh."""
+        if workspace is not None:
+            return workspace.get(nbytes, self.dev, kind, self.given)
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.dev)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+
+def _typed(t, name, dtype, shape):
+    """A contiguous CUDA tensor of one dtype and shape."""
+    _dev(t, name)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    return t
+
+
+def _rows(t, name):
+    """Checks of a [.., vocab] tensor of logits whose elements of a row are adjacent."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _dtype_code(t)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent (last stride 1)")
+    return code
+
+
+def _distill_inputs(logits, idx, teacher, n_valid, grad_loss=None):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, vocab]")
+    dt = _rows(logits, "logits")
+    N, vocab = logits.shape
+    if idx.dim() != 2:
+        raise ValueError("idx must be [N, K]")
+    K = idx.shape[1]
+    _typed(idx, "idx", torch.int32, (N, K))
+    _typed(teacher, "teacher", torch.float32, (N, K))
+    if n_valid is not None:
+        _typed(n_valid, "n_valid", torch.int32, (N,))
+    if grad_loss is not None:
+        _typed(grad_loss, "grad_loss", torch.float32, (N,))
+    return dt, N, vocab, K
+
+
+def _grad_like(logits):
+    """Memory for the gradient of `logits`, in rows as far apart (where those do not overlap)."""
+    N, vocab = logits.shape
+    ld = logits.stride(0) if N > 1 else vocab
+    if ld <= vocab:
+        return torch.empty(N, vocab, dtype=logits.dtype, device=logits.device)
+    return torch.empty(N, ld, dtype=logits.dtype, device=logits.device)[:, :vocab]
+
+
+def _check_grad(grad_out, logits):
+    if grad_out.dtype != logits.dtype or grad_out.shape != logits.shape:
+        raise ValueError("grad_out must have the logits' dtype and shape")
+    _rows(grad_out, "grad_out")
+    if grad_out.shape[0] > 1 and grad_out.stride(0) < grad_out.shape[1]:
+        raise ValueError("the rows of grad_out must not overlap")
+
+
+def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_out=None, stats_out=None, workspace=None,
+                 stream=None):
+    """The loss of a student's logits [N, vocab] (bf16 or fp32, rows may be strided) against a
+    teacher's top logits: ids idx int32 and values teacher fp32 [N, K], of which the first n_valid
+    int32 [N] count (dh_distill_topk).  Returns (loss fp32 [N], stats fp32 [N, 2]: each row's
+    maximum and sum of exp((z - max) / T), which the gradient takes)."""
+    lib = load_library()
+    dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
+    with _On(logits.device, stream, dict(logits=logits, idx=idx, teacher=teacher, n_valid=n_valid, loss_out=loss_out,
+                                         stats_out=stats_out)) as on:
+        if loss_out is None:
+            loss_out = torch.empty(N, dtype=torch.float32, device=on.dev)
+        if stats_out is None:
+            stats_out = torch.empty(N, 2, dtype=torch.float32, device=on.dev)
+        _typed(loss_out, "loss_out", torch.float32, (N,)), _typed(stats_out, "stats_out", torch.float32, (N, 2))
+        nbytes = lib.dh_distill_topk_workspace(N, vocab, dt)
+        ws = on.scratch(nbytes, workspace, "distill")
+        _check(lib.dh_distill_topk(_ptr(logits), logits.stride(0), _ptr(idx), _ptr(teacher), _ptr(n_valid), N, vocab, K,
+                                   dt, float(temperature), _ptr(loss_out), _ptr(stats_out), _ptr(ws), nbytes,
+                                   on.handle), "dh_distill_topk")
+    return loss_out, stats_out
+
+
+def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=None, temperature=1.0, grad_out=None,
+                          stream=None):
+    """The gradient of sum(grad_loss * loss) with respect to the logits, from the stats that
+    distill_topk returned for the same inputs (dh_distill_topk_backward).  grad_out may be the
+    logits themselves.  Returns it, in the logits' dtype."""
+    lib = load_library()
+    dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid, grad_loss)
+    _typed(stats, "stats", torch.float32, (N, 2))
+    with _On(logits.device, stream, dict(logits=logits, idx=idx, teacher=teacher, n_valid=n_valid, stats=stats,
+                                         grad_loss=grad_loss, grad_out=grad_out)) as on:
+        if grad_out is None:
+            grad_out = _grad_like(logits)
+        _check_grad(grad_out, logits)
+        _check(lib.dh_distill_topk_backward(_ptr(logits), logits.stride(0), _ptr(idx), _ptr(teacher), _ptr(n_valid),
+                                            _ptr(stats), _ptr(grad_loss), N, vocab, K, dt, float(temperature),
+                                            _ptr(grad_out), grad_out.stride(0), on.handle), "dh_distill_topk_backward")
+    return grad_out
+
+
+def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperature=1.0, loss_out=None, grad_out=None,
+                      workspace=None, stream=None):
+    """distill_topk and distill_topk_backward in one call, for rows whose weights grad_loss fp32 [N]
+    are known beforehand (dh_distill_topk_step).  grad_out may be the logits themselves.  Returns
+    (loss fp32 [N], gradient)."""
+    lib = load_library()
+    dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid, grad_loss)
+    with _On(logits.device, stream, dict(logits=logits, idx=idx, teacher=teacher, n_valid=n_valid, grad_loss=grad_loss,
+                                         loss_out=loss_out, grad_out=grad_out)) as on:
+        if loss_out is None:
+            loss_out = torch.empty(N, dtype=torch.float32, device=on.dev)
+        if grad_out is None:
+            grad_out = _grad_like(logits)
+        _typed(loss_out, "loss_out", torch.float32, (N,)), _check_grad(grad_out, logits)
+        nbytes = lib.dh_distill_topk_step_workspace(N, vocab, dt)
+        ws = on.scratch(nbytes, workspace, "distill_step")
+        _check(lib.dh_distill_topk_step(_ptr(logits), logits.stride(0), _ptr(idx), _ptr(teacher), _ptr(n_valid),
+                                        _ptr(grad_loss), N, vocab, K, dt, float(temperature), _ptr(loss_out),
+                                        _ptr(grad_out), grad_out.stride(0), _ptr(ws), nbytes, on.handle),
+               "dh_distill_topk_step")
+    return loss_out, grad_out
+
+
+def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0, parent_out=None, token_out=None,
+                score_out=None, workspace=None, stream=None):
+    """The M best continuations of each request's beams over the whole vocabulary (dh_beam_select).
+    logits [R, W, vocab] (bf16 or fp32, beams and requests may be strided or shared); score fp32
+    [R, W], -inf for unused beams; finished int32 [R, W].  Returns (parent int32 [R, M], token int32
+    [R, M], score fp32 [R, M])."""
+    lib = load_library()
+    if logits.dim() != 3:
+        raise ValueError("logits must be [R, W, vocab]")
+    dt = _rows(logits, "logits")
+    R, W, vocab = logits.shape
+    _typed(score, "score", torch.float32, (R, W))
+    if finished is not None:
+        _typed(finished, "finished", torch.int32, (R, W))
+    M = int(M)
+    with _On(logits.device, stream, dict(logits=logits, score=score, finished=finished, parent_out=parent_out,
+                                         token_out=token_out, score_out=score_out)) as on:
+        size = (R, max(M, 0))
+        if parent_out is None:
+            parent_out = torch.empty(size, dtype=torch.int32, device=on.dev)
+        if token_out is None:
+            token_out = torch.empty(size, dtype=torch.int32, device=on.dev)
+        if score_out is None:
+            score_out = torch.empty(size, dtype=torch.float32, device=on.dev)
+        _typed(parent_out, "parent_out", torch.int32, size), _typed(token_out, "token_out", torch.int32, size)
+        _typed(score_out, "score_out", torch.float32, size)
+        nbytes = lib.dh_beam_select_workspace(R, W, vocab, dt)
+        ws = on.scratch(nbytes, workspace, "beam")
+        _check(lib.dh_beam_select(_ptr(logits), logits.stride(0), logits.stride(1), _ptr(score), _ptr(finished), R, W,
+                                  vocab, M, dt, float(temperature), int(pad_token), _ptr(parent_out), _ptr(token_out),
+                                  _ptr(score_out), _ptr(ws), nbytes, on.handle), "dh_beam_select")
+    return parent_out, token_out, score_out
+
+
+def _copy_dims(dims, unit):
+    """(size, source stride, target stride) of the free dimensions, outer to inner, with those that
+    lie next to each other in both tensors made one; the innermost ones that are contiguous become
+    part of the unit (bytes).  Returns (unit, dims)."""
+    dims = [d for d in dims if d[0] != 1]
+    while dims and dims[-1][1] == unit and dims[-1][2] == unit:
+        unit *= dims.pop()[0]
+    out = []
+    for d in dims:
+        if out and out[-1][1] == d[0] * d[1] and out[-1][2] == d[0] * d[2]:
+            out[-1] = (out[-1][0] * d[0], d[1], d[2])
+        else:
+            out.append(d)
+    return unit, out
+
+
+def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_base=None, dst_base=None, request_dim=1,
+                   slot_dim=2, out_slot_dim=None, stream=None):
+    """Slot dst_base[r] + j of request r takes slot src_base[r] + idx[r, j] (dh_reorder_states):
+    beams' states after a selection, or an accepted path's states appended to the committed ones.
+
+    states: any dtype, any dimensions among them requests (request_dim) and slots (slot_dim), e.g.
+    [layers, R, beams, heads, positions, head size].  idx int32 [R, M]; negative entries and slots
+    that do not exist are passed over.  lengths int32 [R] with length_dim: only the first lengths[r]
+    entries of that dimension (the positions that a cache holds) are moved.  out: the tensor written
+    (None: `states` itself, in place), whose slots are dimension out_slot_dim (slot_dim if not given)
+    and whose other dimensions are those of `states`; what is not a target stays as it was.  Returns
+    out."""
+    lib = load_library()
+    if not states.is_cuda:
+        raise ValueError("states must be a CUDA tensor")
+    dst = states if out is None else out
+    if dst.dtype != states.dtype or dst.dim() != states.dim():
+        raise ValueError("out must have the dtype and the number of dimensions of states")
+    n = states.dim()
+    if out_slot_dim is None:
+        out_slot_dim = slot_dim
+    for name, d in (("request_dim", request_dim), ("slot_dim", slot_dim), ("out_slot_dim", out_slot_dim),
+                    ("length_dim", 0 if length_dim is None else length_dim)):
+        if not 0 <= d < n:
+            raise ValueError(f"{name} must be in [0, {n})")
+    if (lengths is None) != (length_dim is None):
+        raise ValueError("lengths and length_dim come together")
+    if len({request_dim, slot_dim, length_dim}) != 3 or out_slot_dim == request_dim:
+        raise ValueError("the request, slot and length dimensions must differ")
+    R = states.shape[request_dim]
+    if idx.dim() != 2:
+        raise ValueError("idx must be [R, M]")
+    M = idx.shape[1]
+    _typed(idx, "idx", torch.int32, (R, M))
+    for t, name in ((lengths, "lengths"), (src_base, "src_base"), (dst_base, "dst_base")):
+        if t is not None:
+            _typed(t, name, torch.int32, (R,))
+    free_s = [d for d in range(n) if d not in (request_dim, slot_dim)]
+    free_d = [d for d in range(n) if d not in (request_dim, out_slot_dim)]
+    if [states.shape[d] for d in free_s] != [dst.shape[d] for d in free_d] or dst.shape[request_dim] != R:
+        raise ValueError("states and out differ in more than their slots")
+    size = states.element_size()
+    span = sorted((st, s) for st, s in zip(dst.stride(), dst.shape) if s > 1)
+    reach = 0
+    for st, s in span:
+        if st <= reach:
+            raise ValueError("the elements of out must be distinct (it is expanded or overlaps itself)")
+        reach += st * (s - 1)
+    dims = [(states.shape[a], states.stride(a) * size, dst.stride(b) * size) for a, b in zip(free_s, free_d)]
+    T, ts, td = 1, 0, 0
+    if length_dim is not None:
+        at = free_s.index(length_dim)
+        (T, ts, td), inner = dims[at], dims[at + 1:]
+        unit, rest = _copy_dims(inner, size)
+        outer = _copy_dims(dims[:at] + rest, None)[1]  # nothing more joins the unit
+    else:
+        unit, outer = _copy_dims(dims, size)
+    if len(outer) > 2:
+        raise ValueError("states: more than two separate dimensions besides requests, slots, positions and the "
+                         "contiguous part; make the inner ones contiguous")
+    (A, sa, da), (H, sh, dh_) = ([(1, 0, 0)] * (2 - len(outer)) + outer)
+    ss = (ctypes.c_int64 * 5)(sa, states.stride(request_dim) * size, states.stride(slot_dim) * size, sh, ts)
+    ds = (ctypes.c_int64 * 5)(da, dst.stride(request_dim) * size, dst.stride(out_slot_dim) * size, dh_, td)
+    with _On(states.device, stream, dict(states=states, out=dst, idx=idx, lengths=lengths, src_base=src_base,
+                                         dst_base=dst_base)) as on:
+        _check(lib.dh_reorder_states(_ptr(states), ss, _ptr(dst), ds, _ptr(idx), _ptr(lengths), _ptr(src_base),
+                                     _ptr(dst_base), A, R, states.shape[slot_dim], dst.shape[out_slot_dim], M, H, T,
+                                     unit, on.handle), "dh_reorder_states")
+    return dst
 
 
 def workspace_status(workspace: "Workspace | None" = None, device=None, stream=None) -> int:

@@ -1,4 +1,5 @@
 // C ABI of libdh: argument validation, workspace layout and kernel sequencing (see include/dh.h).
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -627,6 +628,225 @@ int dh_prof_read(char* names, int name_len, double* total_ms, int* launches, int
     if (launches) launches[k] = cnt[k];
   }
   return n;
+}
+
+// ------------------------------------------------------------------ distillation
+
+namespace {
+
+bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
+bool good_temperature(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(1.f / t); }
+
+// Bytes of the segment statistics of `rows` rows.
+size_t seg_bytes(long long rows, int vocab, int dtype) {
+  return align_up((size_t)rows * row_segments(vocab, dtype) * sizeof(float2), 256);
+}
+
+// Whether the rows [n x vocab] at p and q (strides in elements) may share memory, other than being
+// the same rows.
+bool rows_clash(const void* p, long long ps, const void* q, long long qs, int n, int vocab, int dtype) {
+  if (p == q && (ps == qs || n == 1)) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  const uintptr_t an = ((uintptr_t)(n - 1) * (uintptr_t)ps + (uintptr_t)vocab) * elem_bytes(dtype);
+  const uintptr_t bn = ((uintptr_t)(n - 1) * (uintptr_t)qs + (uintptr_t)vocab) * elem_bytes(dtype);
+  return a < b + bn && b < a + an;
+}
+
+// The checks that the three calls share; DH_OK to go on.
+int check_distill(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher, int N, int vocab,
+                  int K, int dtype, float temperature) {
+  if (N < 0 || vocab <= 0 || K < 1 || K > DH_MAX_K || row_stride < 0) return DH_ERR_INVALID_ARG;
+  if (!good_temperature(temperature)) return DH_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype) || vocab > DH_MAX_VOCAB) return DH_ERR_UNSUPPORTED;
+  if (N == 0) return DH_OK;
+  if (!logits || !idx || !teacher) return DH_ERR_INVALID_ARG;
+  if (!aligned_to(logits, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
+  return DH_OK;
+}
+
+DistillArgs distill_args(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                         const int32_t* n_valid, int N, int vocab, int K, int dtype, float temperature) {
+  DistillArgs a = {};
+  a.logits = logits;
+  a.ld = row_stride;
+  a.idx = idx;
+  a.teacher = teacher;
+  a.n_valid = n_valid;
+  a.N = N;
+  a.vocab = vocab;
+  a.K = K;
+  a.n_seg = row_segments(vocab, dtype);
+  a.temperature = temperature;
+  a.inv_t = 1.f / temperature;
+  a.c = (float)(1.4426950408889634 / (double)temperature);
+  return a;
+}
+
+// Loss (and statistics) after validation: the rows' segments, then the rows.
+int run_distill_loss(const Ctx& c, DistillArgs a, int dtype, float2* seg) {
+  if (note_error(launch_row_stats(c, a.logits, a.ld, 0, a.N, 1, a.vocab, dtype, a.temperature, nullptr, nullptr, seg),
+                 "row statistics") != cudaSuccess)
+    return DH_ERR_CUDA;
+  a.seg = seg;
+  return note_error(launch_distill_loss(c, a, dtype), "distillation loss") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t dh_distill_topk_workspace(int N, int vocab, int dtype) {
+  if (N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
+  return seg_bytes(N, vocab, dtype);
+}
+
+int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                    const int32_t* n_valid, int N, int vocab, int K, int dtype, float temperature, float* loss_out,
+                    float* stats_out, void* workspace, size_t ws_bytes, void* stream) {
+  const int st = check_distill(logits, row_stride, idx, teacher, N, vocab, K, dtype, temperature);
+  if (st != DH_OK || N == 0) return st;
+  if (!loss_out) return DH_ERR_INVALID_ARG;
+  if (!aligned_to(stats_out, 8)) return DH_ERR_UNSUPPORTED;
+  if (!workspace || !aligned256(workspace) || ws_bytes < dh_distill_topk_workspace(N, vocab, dtype))
+    return DH_ERR_WORKSPACE;
+  Ctx c;
+  if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
+  DistillArgs a = distill_args(logits, row_stride, idx, teacher, n_valid, N, vocab, K, dtype, temperature);
+  a.loss_out = loss_out;
+  a.stats_out = reinterpret_cast<float2*>(stats_out);
+  return run_distill_loss(c, a, dtype, static_cast<float2*>(workspace));
+}
+
+int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                             const int32_t* n_valid, const float* stats, const float* grad_loss, int N, int vocab,
+                             int K, int dtype, float temperature, void* grad_out, int64_t grad_stride, void* stream) {
+  const int st = check_distill(logits, row_stride, idx, teacher, N, vocab, K, dtype, temperature);
+  if (st != DH_OK || N == 0) return st;
+  if (!stats || !grad_loss || !grad_out || (N > 1 && grad_stride < vocab)) return DH_ERR_INVALID_ARG;
+  if (rows_clash(logits, row_stride, grad_out, grad_stride, N, vocab, dtype)) return DH_ERR_INVALID_ARG;
+  if (!aligned_to(stats, 8) || !aligned_to(grad_out, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
+  Ctx c;
+  if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
+  DistillArgs a = distill_args(logits, row_stride, idx, teacher, n_valid, N, vocab, K, dtype, temperature);
+  a.stats = reinterpret_cast<const float2*>(stats);
+  a.weight = grad_loss;
+  a.grad = grad_out;
+  a.gld = grad_stride;
+  return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+}
+
+size_t dh_distill_topk_step_workspace(int N, int vocab, int dtype) {
+  if (N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
+  return seg_bytes(N, vocab, dtype) + align_up((size_t)N * sizeof(float2), 256);
+}
+
+int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                         const int32_t* n_valid, const float* grad_loss, int N, int vocab, int K, int dtype,
+                         float temperature, float* loss_out, void* grad_out, int64_t grad_stride, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  int st = check_distill(logits, row_stride, idx, teacher, N, vocab, K, dtype, temperature);
+  if (st != DH_OK || N == 0) return st;
+  if (!loss_out || !grad_loss || !grad_out || (N > 1 && grad_stride < vocab)) return DH_ERR_INVALID_ARG;
+  if (rows_clash(logits, row_stride, grad_out, grad_stride, N, vocab, dtype)) return DH_ERR_INVALID_ARG;
+  if (!aligned_to(grad_out, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
+  if (!workspace || !aligned256(workspace) || ws_bytes < dh_distill_topk_step_workspace(N, vocab, dtype))
+    return DH_ERR_WORKSPACE;
+  Ctx c;
+  if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
+  DistillArgs a = distill_args(logits, row_stride, idx, teacher, n_valid, N, vocab, K, dtype, temperature);
+  a.weight = grad_loss;
+  a.grad = grad_out;
+  a.gld = grad_stride;
+  a.loss_out = loss_out;
+  float2* stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + seg_bytes(N, vocab, dtype));
+  a.stats_out = stats;
+  st = run_distill_loss(c, a, dtype, static_cast<float2*>(workspace));
+  if (st != DH_OK) return st;
+  a.stats = stats;
+  return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ beam selection
+
+size_t dh_beam_select_workspace(int R, int W, int vocab, int dtype) {
+  if (R <= 0 || W <= 0 || W > DH_MAX_BEAMS || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
+  return seg_bytes((long long)R * W, vocab, dtype);
+}
+
+int dh_beam_select(const void* logits, int64_t request_stride, int64_t beam_stride, const float* score,
+                   const int32_t* finished, int R, int W, int vocab, int M, int dtype, float temperature,
+                   int pad_token, int32_t* parent_out, int32_t* token_out, float* score_out, void* workspace,
+                   size_t ws_bytes, void* stream) {
+  if (R < 0 || W < 1 || vocab <= 0 || M < 1 || request_stride < 0 || beam_stride < 0) return DH_ERR_INVALID_ARG;
+  if (!good_temperature(temperature)) return DH_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype) || W > DH_MAX_BEAMS || M > DH_MAX_BEAM_OUT || vocab > DH_MAX_VOCAB) return DH_ERR_UNSUPPORTED;
+  if (R == 0) return DH_OK;
+  if (!logits || !score || !parent_out || !token_out || !score_out) return DH_ERR_INVALID_ARG;
+  if (!aligned_to(logits, elem_bytes(dtype)) || (long long)R * W > 0x7FFFFFFFLL) return DH_ERR_UNSUPPORTED;
+  if (!workspace || !aligned256(workspace) || ws_bytes < dh_beam_select_workspace(R, W, vocab, dtype))
+    return DH_ERR_WORKSPACE;
+  Ctx c;
+  if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
+  float2* seg = static_cast<float2*>(workspace);
+  if (note_error(launch_row_stats(c, logits, request_stride, beam_stride, R, W, vocab, dtype, temperature, score,
+                                  finished, seg),
+                 "row statistics") != cudaSuccess)
+    return DH_ERR_CUDA;
+  return note_error(launch_beam_select(c, logits, request_stride, beam_stride, score, finished, seg, R, W, vocab, M,
+                                       dtype, temperature, pad_token, parent_out, token_out, score_out),
+                    "beam selection") == cudaSuccess
+             ? DH_OK
+             : DH_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ reordering states
+
+int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, const int64_t* dst_strides,
+                      const int32_t* idx, const int32_t* lengths, const int32_t* src_base, const int32_t* dst_base,
+                      int A, int R, int src_slots, int dst_slots, int M, int H, int T, int64_t unit_bytes,
+                      void* stream) {
+  if (A < 0 || R < 0 || src_slots < 0 || dst_slots < 0 || M < 0 || H < 0 || T < 0 || unit_bytes < 0)
+    return DH_ERR_INVALID_ARG;
+  if (M > DH_MAX_SLOTS) return DH_ERR_UNSUPPORTED;
+  if (A == 0 || R == 0 || src_slots == 0 || dst_slots == 0 || M == 0 || H == 0 || T == 0 || unit_bytes == 0)
+    return DH_OK;
+  if (!src || !dst || !src_strides || !dst_strides || !idx) return DH_ERR_INVALID_ARG;
+  ReorderArgs a = {};
+  a.src = static_cast<const char*>(src);
+  a.dst = static_cast<char*>(dst);
+  const int sn[5] = {A, R, src_slots, H, T}, dn[5] = {A, R, dst_slots, H, T};
+  uintptr_t s_end = (uintptr_t)unit_bytes, d_end = (uintptr_t)unit_bytes;
+  bool same = src == dst && src_slots == dst_slots;
+  for (int i = 0; i < 5; ++i) {
+    if (src_strides[i] < 0 || dst_strides[i] < 0) return DH_ERR_INVALID_ARG;
+    // a dimension of one has no stride
+    a.ss[i] = sn[i] > 1 ? src_strides[i] : 0;
+    a.ds[i] = dn[i] > 1 ? dst_strides[i] : 0;
+    if (dn[i] > 1 && dst_strides[i] < unit_bytes) return DH_ERR_INVALID_ARG;  // targets would overlap
+    same = same && a.ss[i] == a.ds[i];
+    s_end += (uintptr_t)(sn[i] - 1) * (uintptr_t)a.ss[i];
+    d_end += (uintptr_t)(dn[i] - 1) * (uintptr_t)a.ds[i];
+  }
+  const uintptr_t sp = reinterpret_cast<uintptr_t>(src), dp = reinterpret_cast<uintptr_t>(dst);
+  if (!same && sp < dp + d_end && dp < sp + s_end) return DH_ERR_INVALID_ARG;
+  a.in_place = same;
+  a.idx = idx;
+  a.lengths = lengths;
+  a.src_base = src_base;
+  a.dst_base = dst_base;
+  a.A = A;
+  a.R = R;
+  a.src_slots = src_slots;
+  a.dst_slots = dst_slots;
+  a.M = M;
+  a.H = H;
+  a.T = T;
+  a.unit = unit_bytes;
+  if (unit_bytes > 0x7FFFFFFFLL || (long long)H * T > 0x7FFFFFFFLL / unit_bytes * 16 ||
+      reorder_columns(a) > 0x7FFFFF00LL || (double)A * R * (double)reorder_columns(a) > 256.0 * 0x7FFFFFFFLL ||
+      reorder_blocks(a) > 0x7FFFFFFFLL)
+    return DH_ERR_UNSUPPORTED;
+  Ctx c;
+  if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
+  return note_error(launch_reorder(c, a), "reordering states") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
 }
 
 }  // extern "C"

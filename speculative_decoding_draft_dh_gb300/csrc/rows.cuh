@@ -1,0 +1,170 @@
+// Rows of vocabulary logits, shared by the operators that reduce them (distill.cu, beam.cu).
+//
+// A row has `vocab` logits of type T at any element-aligned address (rows may be strided and a
+// vocabulary need not be a multiple of anything).  A vector is 16 bytes of elements counted from
+// the row's first one, so which elements a lane holds, and with it the order of every sum, depends
+// on the position in the row alone, not on the row's address: equal rows give equal sums.
+#pragma once
+
+#include "dh_internal.cuh"
+
+namespace dh {
+
+// 2^x on the special-function unit, subnormal results flushed to zero (the terms it flushes are
+// below 2^-126 of the largest term's and do not move a sum).
+__device__ __forceinline__ float row_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float ROW_LOG2E = 1.4426950408889634f;
+
+// The 16 bytes at an address of any alignment s = address mod 16, taken from the one or two aligned
+// 16-byte words that hold them (both hold bytes of the vector, so neither lies outside the row's
+// memory by a whole word).
+__device__ __forceinline__ uint4 ld16_any(const void* p) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  const unsigned s = (unsigned)a & 15u;
+  const uint4* w = reinterpret_cast<const uint4*>(a - s);
+  const uint4 lo = __ldg(w);
+  if (s == 0) return lo;
+  const uint4 hi = __ldg(w + 1);
+  // words q .. q + 4 of the eight, then a shift by the bytes within a word
+  const unsigned q = s >> 2, b = (s & 3u) * 8u;
+  uint32_t x0, x1, x2, x3, x4;
+  if (q == 0) { x0 = lo.x; x1 = lo.y; x2 = lo.z; x3 = lo.w; x4 = hi.x; }
+  else if (q == 1) { x0 = lo.y; x1 = lo.z; x2 = lo.w; x3 = hi.x; x4 = hi.y; }
+  else if (q == 2) { x0 = lo.z; x1 = lo.w; x2 = hi.x; x3 = hi.y; x4 = hi.z; }
+  else { x0 = lo.w; x1 = hi.x; x2 = hi.y; x3 = hi.z; x4 = hi.w; }
+  return make_uint4(__funnelshift_r(x0, x1, b), __funnelshift_r(x1, x2, b), __funnelshift_r(x2, x3, b),
+                    __funnelshift_r(x3, x4, b));
+}
+
+// Two elements of type T equal to -inf, as a 32-bit word (fp32: one element).
+template <typename T> struct NegInf;
+template <> struct NegInf<float> { static constexpr uint32_t WORD = 0xFF800000u; };
+template <> struct NegInf<__nv_bfloat16> { static constexpr uint32_t WORD = 0xFF80FF80u; };
+
+__device__ __forceinline__ uint32_t elem_bits(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t elem_bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
+
+// Elements id .. id + PER16 - 1 of a row, -inf past its end.  ALIGNED: the row starts on 16 bytes.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 row_vec(const T* row, int id, int vocab) {
+  constexpr int PER = Elem<T>::PER16;
+  if (id + PER <= vocab) return ALIGNED ? ld_nc_v4(row + id) : ld16_any(row + id);
+  uint32_t w[4] = {NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD};
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    if (id + e < vocab) {
+      const uint32_t b = elem_bits(row[id + e]);
+      if (sizeof(T) == 4) w[e] = b;
+      else w[e / 2] = (e & 1) ? ((w[e / 2] & 0xFFFFu) | (b << 16)) : ((w[e / 2] & 0xFFFF0000u) | b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Maximum that a NaN passes through, so that a row which holds one is found out.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Largest element of N vectors, NaN if there is one.
+template <typename T, int N>
+__device__ __forceinline__ float vec_max(const uint4 (&u)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      m = max_nan(m, max_nan(max_nan(__uint_as_float(u[v].x), __uint_as_float(u[v].y)),
+                             max_nan(__uint_as_float(u[v].z), __uint_as_float(u[v].w))));
+    return m;
+  } else {
+    // pairwise in bf16: the maximum of bf16 values is one of them, so nothing is rounded
+    auto b2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    __nv_bfloat162 m = b2(NegInf<T>::WORD);
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(b2(u[v].x), b2(u[v].y)), __hmax2_nan(b2(u[v].z), b2(u[v].w))));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+}
+
+// sum 2^((z - m) c) over the elements of a vector, in a fixed tree.  z - m is exact for the terms
+// near the maximum, so the dominating terms carry only the error of 2^x itself.
+template <typename T>
+__device__ __forceinline__ float vec_expsum(const uint4& u, float m, float c) {
+  constexpr int PER = Elem<T>::PER16;
+  float z[PER];
+  Elem<T>::unpack(u, z);
+#pragma unroll
+  for (int e = 0; e < PER; ++e) z[e] = row_ex2((z[e] - m) * c);
+#pragma unroll
+  for (int o = PER / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e)
+      if (e < o) z[e] += z[e + o];
+  return z[0];
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+// Segments of a row: ROW_SEG_VECS vectors per lane of one warp (1024 bf16 or 512 fp32 ids), lane l
+// holding vectors l, l + 32, ...  k_row_stats leaves each segment's (max, sum of exp((z - max)/T)).
+constexpr int ROW_SEG_VECS = 4;
+template <typename T> constexpr int row_seg() { return 32 * Elem<T>::PER16 * ROW_SEG_VECS; }
+
+// A sum of positive terms held as a rounded value and the part that rounding left out (the
+// two-term sum of Knuth): combining the segments' sums in any number adds no error that counts.
+struct Sum2 {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, b = s - hi;
+    lo += (hi - (s - b)) + (x - b);
+    hi = s;
+  }
+};
+
+// A row's (max, sum) from its segments' pairs, by one warp; every lane gets the result.  The sum
+// is relative to exp((z - max)/T); a row of -inf gives (-inf, 0).  A NaN logit gives
+// (NaN, NaN), a +inf one (+inf, NaN).  inv_t = 1 / T.
+__device__ __forceinline__ void row_combine(const float2* __restrict__ seg, int n_seg, float inv_t, float* m_out,
+                                            Sum2* sum_out) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY;
+  for (int i = lane; i < n_seg; i += 32) m = max_nan(m, __ldcg(&seg[i]).x);
+  m = warp_max(m);
+  Sum2 s;
+  for (int i = lane; i < n_seg; i += 32) {
+    const float2 q = __ldcg(&seg[i]);
+    // a segment of -inf alone adds nothing; a NaN sum stays one
+    if (q.x != -INFINITY) s.add(q.y * expf((q.x - m) * inv_t));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float h = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o), l = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
+    // the lower lane's first, so that both lanes compute the same
+    Sum2 a = (threadIdx.x & o) ? Sum2{h, l} : s;
+    const Sum2 b = (threadIdx.x & o) ? s : Sum2{h, l};
+    a.add(b.hi);
+    a.lo += b.lo;
+    s = a;
+  }
+  *m_out = m;
+  *sum_out = s;
+}
+
+}  // namespace dh
