@@ -363,7 +363,7 @@ int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, 
 int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
                              const int32_t* n_valid, const float* stats, const float* grad_loss, int N, int vocab,
                              int K, int dtype, float temperature, void* grad_out, int64_t grad_stride, void* stream);
-size_t dh_distill_topk_step_workspace(int N, int vocab, int dtype);
+size_t dh_distill_topk_step_workspace(int N, int vocab, int K, int dtype);
 int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
                          const int32_t* n_valid, const float* grad_loss, int N, int vocab, int K, int dtype,
                          float temperature, float* loss_out, void* grad_out, int64_t grad_stride, void* workspace,

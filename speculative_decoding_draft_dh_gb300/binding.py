@@ -7,6 +7,7 @@ loaded the call raises (there is no fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -112,7 +113,7 @@ def load_library(path: str | None = None):
         lib.dh_distill_topk.restype = I
         lib.dh_distill_topk_backward.argtypes = [P, L, P, P, P, P, P, I, I, I, I, F, P, L, P]
         lib.dh_distill_topk_backward.restype = I
-        lib.dh_distill_topk_step_workspace.argtypes = [I, I, I]
+        lib.dh_distill_topk_step_workspace.argtypes = [I, I, I, I]
         lib.dh_distill_topk_step_workspace.restype = Z
         lib.dh_distill_topk_step.argtypes = [P, L, P, P, P, P, I, I, I, I, F, P, P, L, P, Z, P]
         lib.dh_distill_topk_step.restype = I
@@ -463,52 +464,53 @@ def verify_chain(logits, cand_idx, cand_prob, draft_token, u_accept, u_sample, *
 # wrote the inputs).
 
 
-class _On:
-    """The device and stream of a call: the tensors' device, `stream` or the current one."""
-
-    def __init__(self, dev, stream, inputs):
-        for name, t in inputs.items():
-            if t is not None and t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, not on {dev}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.dev, self.given, self.inputs = dev, stream, inputs
-        self.ctx = None
-
-    def __enter__(self):
-        if self.given is not None:
-            self.ctx = torch.cuda.stream(self.given)
-        elif self.dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.dev)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.stream = self.given if self.given is not None else torch.cuda.current_stream(self.dev)
-        return self
-
-    def __exit__(self, *exc):
-        if self.given is not None and not torch.cuda.is_current_stream_capturing():
-            for t in self.inputs.values():
+def _run_on(stream, tensors, call):
+    """call(raw stream, device) on the first tensor's device and on `stream` (None: that device's
+    current one).  tensors: (name, tensor or None) pairs; all have to be on that device."""
+    first = tensors[0][1]
+    index = first.get_device()
+    for name, t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(torch.cuda.current_stream(index).cuda_stream, first.device)
+        with torch.cuda.device(index):
+            return call(torch.cuda.current_stream(index).cuda_stream, first.device)
+    if stream.device != first.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+    with torch.cuda.stream(stream):
+        out = call(stream.cuda_stream, first.device)
+        if not torch.cuda.is_current_stream_capturing():
+            for _, t in tensors:
                 if t is not None:
-                    t.record_stream(self.given)
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+                    t.record_stream(stream)
+    return out
 
-    def scratch(self, nbytes, workspace, kind):
-        """nbytes of device memory, not zeroed: the caller's workspace object's, else fresh."""
-        if workspace is not None:
-            return workspace.get(nbytes, self.dev, kind, self.given)
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.dev)
 
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(query, *sizes):
+    return getattr(load_library(), query)(*sizes)
+
+
+def _scratch(nbytes, workspace, kind, dev, stream):
+    """The address of nbytes of device memory, not zeroed, and what keeps it: the caller's workspace
+    object's, else fresh."""
+    t = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev) if workspace is None else \
+        workspace.get(nbytes, dev, kind, stream)
+    return t.data_ptr(), t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _typed(t, name, dtype, shape):
-    """A contiguous CUDA tensor of one dtype and shape."""
-    _dev(t, name)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    """Checks a contiguous CUDA tensor of one dtype and shape."""
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
     return t
 
 
@@ -517,18 +519,16 @@ def _rows(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     code = _dtype_code(t)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent (last stride 1)")
     return code
 
 
 def _distill_inputs(logits, idx, teacher, n_valid, grad_loss=None):
-    if logits.dim() != 2:
-        raise ValueError("logits must be [N, vocab]")
+    if logits.dim() != 2 or idx.dim() != 2:
+        raise ValueError("logits must be [N, vocab] and idx [N, K]")
     dt = _rows(logits, "logits")
     N, vocab = logits.shape
-    if idx.dim() != 2:
-        raise ValueError("idx must be [N, K]")
     K = idx.shape[1]
     _typed(idx, "idx", torch.int32, (N, K))
     _typed(teacher, "teacher", torch.float32, (N, K))
@@ -539,21 +539,25 @@ def _distill_inputs(logits, idx, teacher, n_valid, grad_loss=None):
     return dt, N, vocab, K
 
 
-def _grad_like(logits):
-    """Memory for the gradient of `logits`, in rows as far apart (where those do not overlap)."""
+def _grad_rows(logits, grad_out):
+    """grad_out checked, or memory for the gradient in rows as far apart as those of `logits` (where
+    they do not overlap)."""
     N, vocab = logits.shape
-    ld = logits.stride(0) if N > 1 else vocab
-    if ld <= vocab:
-        return torch.empty(N, vocab, dtype=logits.dtype, device=logits.device)
-    return torch.empty(N, ld, dtype=logits.dtype, device=logits.device)[:, :vocab]
-
-
-def _check_grad(grad_out, logits):
+    if grad_out is None:
+        ld = logits.stride(0)
+        if ld <= vocab or N <= 1:
+            return torch.empty((N, vocab), dtype=logits.dtype, device=logits.device)
+        return torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
     if grad_out.dtype != logits.dtype or grad_out.shape != logits.shape:
         raise ValueError("grad_out must have the logits' dtype and shape")
     _rows(grad_out, "grad_out")
-    if grad_out.shape[0] > 1 and grad_out.stride(0) < grad_out.shape[1]:
+    if N > 1 and grad_out.stride(0) < vocab:
         raise ValueError("the rows of grad_out must not overlap")
+    return grad_out
+
+
+def _out(t, name, dtype, shape, dev):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _typed(t, name, dtype, shape)
 
 
 def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_out=None, stats_out=None, workspace=None,
@@ -564,19 +568,18 @@ def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_ou
     maximum and sum of exp((z - max) / T), which the gradient takes)."""
     lib = load_library()
     dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
-    with _On(logits.device, stream, dict(logits=logits, idx=idx, teacher=teacher, n_valid=n_valid, loss_out=loss_out,
-                                         stats_out=stats_out)) as on:
-        if loss_out is None:
-            loss_out = torch.empty(N, dtype=torch.float32, device=on.dev)
-        if stats_out is None:
-            stats_out = torch.empty(N, 2, dtype=torch.float32, device=on.dev)
-        _typed(loss_out, "loss_out", torch.float32, (N,)), _typed(stats_out, "stats_out", torch.float32, (N, 2))
-        nbytes = lib.dh_distill_topk_workspace(N, vocab, dt)
-        ws = on.scratch(nbytes, workspace, "distill")
-        _check(lib.dh_distill_topk(_ptr(logits), logits.stride(0), _ptr(idx), _ptr(teacher), _ptr(n_valid), N, vocab, K,
-                                   dt, float(temperature), _ptr(loss_out), _ptr(stats_out), _ptr(ws), nbytes,
-                                   on.handle), "dh_distill_topk")
-    return loss_out, stats_out
+
+    def call(raw, dev):
+        loss = _out(loss_out, "loss_out", torch.float32, (N,), dev)
+        stats = _out(stats_out, "stats_out", torch.float32, (N, 2), dev)
+        nbytes = _workspace_bytes("dh_distill_topk_workspace", N, vocab, dt)
+        ws, _keep = _scratch(nbytes, workspace, "distill", dev, stream)
+        _check(lib.dh_distill_topk(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
+                                   _addr(n_valid), N, vocab, K, dt, temperature, loss.data_ptr(), stats.data_ptr(), ws,
+                                   nbytes, raw), "dh_distill_topk")
+        return loss, stats
+    return _run_on(stream, (("logits", logits), ("idx", idx), ("teacher", teacher), ("n_valid", n_valid),
+                            ("loss_out", loss_out), ("stats_out", stats_out)), call)
 
 
 def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=None, temperature=1.0, grad_out=None,
@@ -587,15 +590,16 @@ def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=Non
     lib = load_library()
     dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid, grad_loss)
     _typed(stats, "stats", torch.float32, (N, 2))
-    with _On(logits.device, stream, dict(logits=logits, idx=idx, teacher=teacher, n_valid=n_valid, stats=stats,
-                                         grad_loss=grad_loss, grad_out=grad_out)) as on:
-        if grad_out is None:
-            grad_out = _grad_like(logits)
-        _check_grad(grad_out, logits)
-        _check(lib.dh_distill_topk_backward(_ptr(logits), logits.stride(0), _ptr(idx), _ptr(teacher), _ptr(n_valid),
-                                            _ptr(stats), _ptr(grad_loss), N, vocab, K, dt, float(temperature),
-                                            _ptr(grad_out), grad_out.stride(0), on.handle), "dh_distill_topk_backward")
-    return grad_out
+
+    def call(raw, dev):
+        grad = _grad_rows(logits, grad_out)
+        _check(lib.dh_distill_topk_backward(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
+                                            _addr(n_valid), stats.data_ptr(), grad_loss.data_ptr(), N, vocab, K, dt,
+                                            temperature, grad.data_ptr(), grad.stride(0), raw),
+               "dh_distill_topk_backward")
+        return grad
+    return _run_on(stream, (("logits", logits), ("idx", idx), ("teacher", teacher), ("n_valid", n_valid),
+                            ("stats", stats), ("grad_loss", grad_loss), ("grad_out", grad_out)), call)
 
 
 def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperature=1.0, loss_out=None, grad_out=None,
@@ -605,20 +609,19 @@ def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperat
     (loss fp32 [N], gradient)."""
     lib = load_library()
     dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid, grad_loss)
-    with _On(logits.device, stream, dict(logits=logits, idx=idx, teacher=teacher, n_valid=n_valid, grad_loss=grad_loss,
-                                         loss_out=loss_out, grad_out=grad_out)) as on:
-        if loss_out is None:
-            loss_out = torch.empty(N, dtype=torch.float32, device=on.dev)
-        if grad_out is None:
-            grad_out = _grad_like(logits)
-        _typed(loss_out, "loss_out", torch.float32, (N,)), _check_grad(grad_out, logits)
-        nbytes = lib.dh_distill_topk_step_workspace(N, vocab, dt)
-        ws = on.scratch(nbytes, workspace, "distill_step")
-        _check(lib.dh_distill_topk_step(_ptr(logits), logits.stride(0), _ptr(idx), _ptr(teacher), _ptr(n_valid),
-                                        _ptr(grad_loss), N, vocab, K, dt, float(temperature), _ptr(loss_out),
-                                        _ptr(grad_out), grad_out.stride(0), _ptr(ws), nbytes, on.handle),
+
+    def call(raw, dev):
+        loss = _out(loss_out, "loss_out", torch.float32, (N,), dev)
+        grad = _grad_rows(logits, grad_out)
+        nbytes = _workspace_bytes("dh_distill_topk_step_workspace", N, vocab, K, dt)
+        ws, _keep = _scratch(nbytes, workspace, "distill_step", dev, stream)
+        _check(lib.dh_distill_topk_step(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
+                                        _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, temperature,
+                                        loss.data_ptr(), grad.data_ptr(), grad.stride(0), ws, nbytes, raw),
                "dh_distill_topk_step")
-    return loss_out, grad_out
+        return loss, grad
+    return _run_on(stream, (("logits", logits), ("idx", idx), ("teacher", teacher), ("n_valid", n_valid),
+                            ("grad_loss", grad_loss), ("loss_out", loss_out), ("grad_out", grad_out)), call)
 
 
 def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0, parent_out=None, token_out=None,
@@ -636,23 +639,20 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     if finished is not None:
         _typed(finished, "finished", torch.int32, (R, W))
     M = int(M)
-    with _On(logits.device, stream, dict(logits=logits, score=score, finished=finished, parent_out=parent_out,
-                                         token_out=token_out, score_out=score_out)) as on:
+
+    def call(raw, dev):
         size = (R, max(M, 0))
-        if parent_out is None:
-            parent_out = torch.empty(size, dtype=torch.int32, device=on.dev)
-        if token_out is None:
-            token_out = torch.empty(size, dtype=torch.int32, device=on.dev)
-        if score_out is None:
-            score_out = torch.empty(size, dtype=torch.float32, device=on.dev)
-        _typed(parent_out, "parent_out", torch.int32, size), _typed(token_out, "token_out", torch.int32, size)
-        _typed(score_out, "score_out", torch.float32, size)
-        nbytes = lib.dh_beam_select_workspace(R, W, vocab, dt)
-        ws = on.scratch(nbytes, workspace, "beam")
-        _check(lib.dh_beam_select(_ptr(logits), logits.stride(0), logits.stride(1), _ptr(score), _ptr(finished), R, W,
-                                  vocab, M, dt, float(temperature), int(pad_token), _ptr(parent_out), _ptr(token_out),
-                                  _ptr(score_out), _ptr(ws), nbytes, on.handle), "dh_beam_select")
-    return parent_out, token_out, score_out
+        parent = _out(parent_out, "parent_out", torch.int32, size, dev)
+        token = _out(token_out, "token_out", torch.int32, size, dev)
+        best = _out(score_out, "score_out", torch.float32, size, dev)
+        nbytes = _workspace_bytes("dh_beam_select_workspace", R, W, vocab, dt)
+        ws, _keep = _scratch(nbytes, workspace, "beam", dev, stream)
+        _check(lib.dh_beam_select(logits.data_ptr(), logits.stride(0), logits.stride(1), score.data_ptr(),
+                                  _addr(finished), R, W, vocab, M, dt, temperature, int(pad_token), parent.data_ptr(),
+                                  token.data_ptr(), best.data_ptr(), ws, nbytes, raw), "dh_beam_select")
+        return parent, token, best
+    return _run_on(stream, (("logits", logits), ("score", score), ("finished", finished), ("parent_out", parent_out),
+                            ("token_out", token_out), ("score_out", score_out)), call)
 
 
 def _copy_dims(dims, unit):
@@ -671,6 +671,46 @@ def _copy_dims(dims, unit):
     return unit, out
 
 
+@functools.lru_cache(maxsize=256)
+def _reorder_plan(shape, stride, out_shape, out_stride, size, request_dim, slot_dim, out_slot_dim, length_dim):
+    """What the library is told of a layout: (A, R, source slots, target slots, H, T, unit bytes, byte
+    strides of the source, of the target).  Goes by shapes and strides alone."""
+    n = len(shape)
+    if len(out_shape) != n:
+        raise ValueError("out must have the number of dimensions of states")
+    for name, d in (("request_dim", request_dim), ("slot_dim", slot_dim), ("out_slot_dim", out_slot_dim),
+                    ("length_dim", 0 if length_dim is None else length_dim)):
+        if not 0 <= d < n:
+            raise ValueError(f"{name} must be in [0, {n})")
+    if len({request_dim, slot_dim, length_dim}) != 3 or out_slot_dim == request_dim:
+        raise ValueError("the request, slot and length dimensions must differ")
+    free = [d for d in range(n) if d not in (request_dim, slot_dim)]
+    out_free = [d for d in range(n) if d not in (request_dim, out_slot_dim)]
+    if [shape[d] for d in free] != [out_shape[d] for d in out_free] or out_shape[request_dim] != shape[request_dim]:
+        raise ValueError("states and out differ in more than their slots")
+    reach = 0
+    for st, s in sorted((st, s) for st, s in zip(out_stride, out_shape) if s > 1):
+        if st <= reach:
+            raise ValueError("the elements of out must be distinct (it is expanded or overlaps itself)")
+        reach += st * (s - 1)
+    dims = [(shape[a], stride[a] * size, out_stride[b] * size) for a, b in zip(free, out_free)]
+    T, ts, td = 1, 0, 0
+    if length_dim is not None:
+        at = free.index(length_dim)
+        T, ts, td = dims[at]
+        unit, rest = _copy_dims(dims[at + 1:], size)
+        outer = _copy_dims(dims[:at] + rest, None)[1]  # nothing more joins the unit
+    else:
+        unit, outer = _copy_dims(dims, size)
+    if len(outer) > 2:
+        raise ValueError("states: more than two separate dimensions besides requests, slots, positions and the "
+                         "contiguous part; make the inner ones contiguous")
+    (A, sa, da), (H, sh, dh) = [(1, 0, 0)] * (2 - len(outer)) + outer
+    ss = (ctypes.c_int64 * 5)(sa, stride[request_dim] * size, stride[slot_dim] * size, sh, ts)
+    ds = (ctypes.c_int64 * 5)(da, out_stride[request_dim] * size, out_stride[out_slot_dim] * size, dh, td)
+    return A, shape[request_dim], shape[slot_dim], out_shape[out_slot_dim], H, T, unit, ss, ds
+
+
 def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_base=None, dst_base=None, request_dim=1,
                    slot_dim=2, out_slot_dim=None, stream=None):
     """Slot dst_base[r] + j of request r takes slot src_base[r] + idx[r, j] (dh_reorder_states):
@@ -684,23 +724,16 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     and whose other dimensions are those of `states`; what is not a target stays as it was.  Returns
     out."""
     lib = load_library()
+    dst = states if out is None else out
     if not states.is_cuda:
         raise ValueError("states must be a CUDA tensor")
-    dst = states if out is None else out
-    if dst.dtype != states.dtype or dst.dim() != states.dim():
-        raise ValueError("out must have the dtype and the number of dimensions of states")
-    n = states.dim()
-    if out_slot_dim is None:
-        out_slot_dim = slot_dim
-    for name, d in (("request_dim", request_dim), ("slot_dim", slot_dim), ("out_slot_dim", out_slot_dim),
-                    ("length_dim", 0 if length_dim is None else length_dim)):
-        if not 0 <= d < n:
-            raise ValueError(f"{name} must be in [0, {n})")
+    if dst.dtype != states.dtype:
+        raise ValueError("out must have the dtype of states")
     if (lengths is None) != (length_dim is None):
         raise ValueError("lengths and length_dim come together")
-    if len({request_dim, slot_dim, length_dim}) != 3 or out_slot_dim == request_dim:
-        raise ValueError("the request, slot and length dimensions must differ")
-    R = states.shape[request_dim]
+    plan = _reorder_plan(states.shape, states.stride(), dst.shape, dst.stride(), states.element_size(), request_dim,
+                         slot_dim, slot_dim if out_slot_dim is None else out_slot_dim, length_dim)
+    A, R, slots, out_slots, H, T, unit, ss, ds = plan
     if idx.dim() != 2:
         raise ValueError("idx must be [R, M]")
     M = idx.shape[1]
@@ -708,37 +741,13 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     for t, name in ((lengths, "lengths"), (src_base, "src_base"), (dst_base, "dst_base")):
         if t is not None:
             _typed(t, name, torch.int32, (R,))
-    free_s = [d for d in range(n) if d not in (request_dim, slot_dim)]
-    free_d = [d for d in range(n) if d not in (request_dim, out_slot_dim)]
-    if [states.shape[d] for d in free_s] != [dst.shape[d] for d in free_d] or dst.shape[request_dim] != R:
-        raise ValueError("states and out differ in more than their slots")
-    size = states.element_size()
-    span = sorted((st, s) for st, s in zip(dst.stride(), dst.shape) if s > 1)
-    reach = 0
-    for st, s in span:
-        if st <= reach:
-            raise ValueError("the elements of out must be distinct (it is expanded or overlaps itself)")
-        reach += st * (s - 1)
-    dims = [(states.shape[a], states.stride(a) * size, dst.stride(b) * size) for a, b in zip(free_s, free_d)]
-    T, ts, td = 1, 0, 0
-    if length_dim is not None:
-        at = free_s.index(length_dim)
-        (T, ts, td), inner = dims[at], dims[at + 1:]
-        unit, rest = _copy_dims(inner, size)
-        outer = _copy_dims(dims[:at] + rest, None)[1]  # nothing more joins the unit
-    else:
-        unit, outer = _copy_dims(dims, size)
-    if len(outer) > 2:
-        raise ValueError("states: more than two separate dimensions besides requests, slots, positions and the "
-                         "contiguous part; make the inner ones contiguous")
-    (A, sa, da), (H, sh, dh_) = ([(1, 0, 0)] * (2 - len(outer)) + outer)
-    ss = (ctypes.c_int64 * 5)(sa, states.stride(request_dim) * size, states.stride(slot_dim) * size, sh, ts)
-    ds = (ctypes.c_int64 * 5)(da, dst.stride(request_dim) * size, dst.stride(out_slot_dim) * size, dh_, td)
-    with _On(states.device, stream, dict(states=states, out=dst, idx=idx, lengths=lengths, src_base=src_base,
-                                         dst_base=dst_base)) as on:
-        _check(lib.dh_reorder_states(_ptr(states), ss, _ptr(dst), ds, _ptr(idx), _ptr(lengths), _ptr(src_base),
-                                     _ptr(dst_base), A, R, states.shape[slot_dim], dst.shape[out_slot_dim], M, H, T,
-                                     unit, on.handle), "dh_reorder_states")
+
+    def call(raw, _dev):
+        _check(lib.dh_reorder_states(states.data_ptr(), ss, dst.data_ptr(), ds, idx.data_ptr(), _addr(lengths),
+                                     _addr(src_base), _addr(dst_base), A, R, slots, out_slots, M, H, T, unit, raw),
+               "dh_reorder_states")
+    _run_on(stream, (("states", states), ("out", dst), ("idx", idx), ("lengths", lengths), ("src_base", src_base),
+                     ("dst_base", dst_base)), call)
     return dst
 
 

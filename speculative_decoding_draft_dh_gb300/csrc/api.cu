@@ -688,14 +688,21 @@ int run_distill_loss(const Ctx& c, DistillArgs a, int dtype, float2* seg) {
                  "row statistics") != cudaSuccess)
     return DH_ERR_CUDA;
   a.seg = seg;
-  return note_error(launch_distill_loss(c, a, dtype), "distillation loss") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+  return note_error(launch_distill_finish(c, a, dtype, true, false), "distillation loss") == cudaSuccess ? DH_OK
+                                                                                                         : DH_ERR_CUDA;
+}
+
+// Whether the gradient's rows lie like the logits' on 16 bytes, so that whole vectors can be copied.
+bool lie_alike(const DistillArgs& a, int dtype) {
+  const uintptr_t off = reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.grad);
+  return (off & 15u) == 0 && (a.N == 1 || (a.ld - a.gld) * elem_bytes(dtype) % 16 == 0);
 }
 
 }  // namespace
 
 size_t dh_distill_topk_workspace(int N, int vocab, int dtype) {
   if (N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
-  return seg_bytes(N, vocab, dtype);
+  return WS_HEADER + seg_bytes(N, vocab, dtype);
 }
 
 int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
@@ -712,7 +719,7 @@ int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, 
   DistillArgs a = distill_args(logits, row_stride, idx, teacher, n_valid, N, vocab, K, dtype, temperature);
   a.loss_out = loss_out;
   a.stats_out = reinterpret_cast<float2*>(stats_out);
-  return run_distill_loss(c, a, dtype, static_cast<float2*>(workspace));
+  return run_distill_loss(c, a, dtype, reinterpret_cast<float2*>(static_cast<char*>(workspace) + WS_HEADER));
 }
 
 int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
@@ -730,12 +737,18 @@ int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32
   a.weight = grad_loss;
   a.grad = grad_out;
   a.gld = grad_stride;
-  return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+  if (a.grad == a.logits || !lie_alike(a, dtype))
+    return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+  if (note_error(launch_distill_dense(c, a, dtype), "distillation gradient") != cudaSuccess) return DH_ERR_CUDA;
+  return note_error(launch_distill_finish(c, a, dtype, false, true), "distillation entries") == cudaSuccess
+             ? DH_OK
+             : DH_ERR_CUDA;
 }
 
-size_t dh_distill_topk_step_workspace(int N, int vocab, int dtype) {
-  if (N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
-  return seg_bytes(N, vocab, dtype) + align_up((size_t)N * sizeof(float2), 256);
+size_t dh_distill_topk_step_workspace(int N, int vocab, int K, int dtype) {
+  if (K < 1 || K > DH_MAX_K || N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
+  return WS_HEADER + seg_bytes(N, vocab, dtype) + align_up((size_t)N * sizeof(float2), 256) +
+         align_up((size_t)N * K * sizeof(float), 256);
 }
 
 int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
@@ -747,7 +760,7 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
   if (!loss_out || !grad_loss || !grad_out || (N > 1 && grad_stride < vocab)) return DH_ERR_INVALID_ARG;
   if (rows_clash(logits, row_stride, grad_out, grad_stride, N, vocab, dtype)) return DH_ERR_INVALID_ARG;
   if (!aligned_to(grad_out, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
-  if (!workspace || !aligned256(workspace) || ws_bytes < dh_distill_topk_step_workspace(N, vocab, dtype))
+  if (!workspace || !aligned256(workspace) || ws_bytes < dh_distill_topk_step_workspace(N, vocab, K, dtype))
     return DH_ERR_WORKSPACE;
   Ctx c;
   if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
@@ -756,11 +769,28 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
   a.grad = grad_out;
   a.gld = grad_stride;
   a.loss_out = loss_out;
-  float2* stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + seg_bytes(N, vocab, dtype));
+  char* ws = static_cast<char*>(workspace);
+  float2* seg = reinterpret_cast<float2*>(ws + WS_HEADER);
+  float2* stats = reinterpret_cast<float2*>(ws + WS_HEADER + seg_bytes(N, vocab, dtype));
+  a.status = static_cast<int*>(workspace);
   a.stats_out = stats;
-  st = run_distill_loss(c, a, dtype, static_cast<float2*>(workspace));
-  if (st != DH_OK) return st;
   a.stats = stats;
+  if (lie_alike(a, dtype)) {
+    DistillArgs b = a;
+    if (a.grad == a.logits) {
+      b.gathered = reinterpret_cast<float*>(ws + WS_HEADER + seg_bytes(N, vocab, dtype) +
+                                            align_up((size_t)N * sizeof(float2), 256));
+      if (note_error(launch_distill_gather(c, b, dtype), "distillation entries") != cudaSuccess) return DH_ERR_CUDA;
+    }
+    bool done = false;
+    if (note_error(launch_distill_ring(c, b, dtype, &done), "distillation step") != cudaSuccess) return DH_ERR_CUDA;
+    if (done)
+      return note_error(launch_distill_finish(c, b, dtype, true, true), "distillation entries") == cudaSuccess
+                 ? DH_OK
+                 : DH_ERR_CUDA;
+  }
+  st = run_distill_loss(c, a, dtype, seg);
+  if (st != DH_OK) return st;
   return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
 }
 
@@ -768,7 +798,7 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
 
 size_t dh_beam_select_workspace(int R, int W, int vocab, int dtype) {
   if (R <= 0 || W <= 0 || W > DH_MAX_BEAMS || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
-  return seg_bytes((long long)R * W, vocab, dtype);
+  return WS_HEADER + seg_bytes((long long)R * W, vocab, dtype);
 }
 
 int dh_beam_select(const void* logits, int64_t request_stride, int64_t beam_stride, const float* score,
@@ -785,7 +815,7 @@ int dh_beam_select(const void* logits, int64_t request_stride, int64_t beam_stri
     return DH_ERR_WORKSPACE;
   Ctx c;
   if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
-  float2* seg = static_cast<float2*>(workspace);
+  float2* seg = reinterpret_cast<float2*>(static_cast<char*>(workspace) + WS_HEADER);
   if (note_error(launch_row_stats(c, logits, request_stride, beam_stride, R, W, vocab, dtype, temperature, score,
                                   finished, seg),
                  "row statistics") != cudaSuccess)

@@ -26,6 +26,7 @@ constexpr int BP_THREADS = 512;
 constexpr int BP_WARPS = BP_THREADS / 32;
 constexpr int BP_CAP = 2048;      // candidates held at once (at least DH_MAX_BEAM_OUT + one segment)
 constexpr int BP_SEGS = 1024;     // segments held at once
+constexpr int BP_STAGE = 2560;    // segment maxima in shared memory: 16 beams of 152K bf16 logits
 
 // Order-preserving map of a double onto uint64 (-0 is folded onto +0).
 __device__ __forceinline__ unsigned long long dkey(double x) {
@@ -44,6 +45,7 @@ struct BeamArgs {
   const float2* seg;
   int W, vocab, M, n_seg, pad_token;
   float temperature, inv_t;
+  double inv_t64;
   int32_t* parent;
   int32_t* token;
   float* score_out;
@@ -55,7 +57,10 @@ struct BeamSmem {
   double base[DH_MAX_BEAMS];   // score of the row's largest logit; -inf: no candidates of its own
   float base32[DH_MAX_BEAMS];
   float top[DH_MAX_BEAMS];     // the row's largest logit
+  float sum_hi[DH_MAX_BEAMS], sum_lo[DH_MAX_BEAMS], score[DH_MAX_BEAMS];
+  bool done[DH_MAX_BEAMS];     // finished, with a score
   float zthr[DH_MAX_BEAMS];    // logits from here on reach the bound
+  float seg_max[BP_STAGE];
   uint32_t segs[BP_SEGS];
   int count[2][BP_WARPS];
   unsigned long long last_key;
@@ -84,7 +89,7 @@ __device__ __forceinline__ float score_below(float b, float top, float z, float 
 
 // The score of logit z of beam w, in 64 bits.
 __device__ __forceinline__ double exact_score(const BeamSmem& s, const BeamArgs& a, int w, float z) {
-  return s.base[w] + ((double)z - (double)s.top[w]) / (double)a.temperature;
+  return s.base[w] + ((double)z - (double)s.top[w]) * a.inv_t64;
 }
 
 // The bound's lowest logit per beam: z >= zthr[w] for every z whose score is tau or more.  The
@@ -153,15 +158,8 @@ __device__ __forceinline__ void keep_best(BeamSmem& s, int M) {
   __syncthreads();
 }
 
-__device__ __forceinline__ void push(BeamSmem& s, unsigned long long key, uint32_t pos) {
-  const int at = atomicAdd(&s.n, 1);
-  if (at < BP_CAP) {
-    s.key[at] = key;
-    s.pos[at] = pos;
-  }
-}
-
-// Adds the elements of vector u (ids id ..) of beam w that reach the bound.
+// Adds the elements of vector u (ids id ..) of beam w that reach the bound.  Their logits stand where
+// the keys will (score_pushed).
 template <typename T>
 __device__ __forceinline__ void push_vec(BeamSmem& s, const BeamArgs& a, const uint4& u, int id, int w, float zthr) {
   constexpr int PER = Elem<T>::PER16;
@@ -169,8 +167,19 @@ __device__ __forceinline__ void push_vec(BeamSmem& s, const BeamArgs& a, const u
   Elem<T>::unpack(u, z);
 #pragma unroll
   for (int e = 0; e < PER; ++e)
-    if (z[e] >= zthr && z[e] > -INFINITY)
-      push(s, dkey(exact_score(s, a, w, z[e])), (uint32_t)w * (uint32_t)a.vocab + (uint32_t)(id + e));
+    if (z[e] >= zthr && z[e] > -INFINITY) {
+      const int at = atomicAdd(&s.n, 1);
+      if (at < BP_CAP) {
+        s.key[at] = __float_as_uint(z[e]);
+        s.pos[at] = (uint32_t)w * (uint32_t)a.vocab + (uint32_t)(id + e);
+      }
+    }
+}
+
+// The keys of the candidates from number `first` on, whose logits were pushed.
+__device__ __forceinline__ void score_pushed(BeamSmem& s, const BeamArgs& a, int first) {
+  for (int i = first + (int)threadIdx.x; i < s.n; i += BP_THREADS)
+    s.key[i] = dkey(exact_score(s, a, (int)(s.pos[i] / (uint32_t)a.vocab), __uint_as_float((uint32_t)s.key[i])));
 }
 
 template <typename T, bool ALIGNED>
@@ -188,29 +197,41 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // 1. the beams
+  // 1. the beams: a warp each for the sums, then a lane each for the logarithms (64-bit operations take
+  // a warp 16 cycles whatever its active lanes, so they are done 32 at a time)
   if (tid == 0) s.n = s.n_segs = 0;
+  const bool staged = n_all <= BP_STAGE;  // the segments' maxima fit shared memory
   for (int w = warp; w < W; w += BP_WARPS) {
     const float sc = __ldg(score + w);
-    double base = -INFINITY;
-    float top = 0.f;
-    if (fabsf(sc) < INFINITY && !(finished && __ldg(finished + w) != 0)) {
-      float m;
+    const bool fin = finished && __ldg(finished + w) != 0;
+    const float2* sg = seg + (size_t)w * n_seg;
+    const bool live = fabsf(sc) < INFINITY && !fin;
+    float m = -INFINITY, total = 0.f, rest = 0.f;
+    if (live) {
       Sum2 sum;
-      row_combine(seg + (size_t)w * n_seg, n_seg, a.inv_t, &m, &sum);
-      const float fs = sum.hi + sum.lo;
-      // a row of -inf, and one with a NaN or +inf, has no distribution
-      if (fabsf(m) < INFINITY && fs < INFINITY)
-        base = (double)sc - log((double)sum.hi + (double)sum.lo);
-      top = m;
+      row_combine(sg, n_seg, a.inv_t, &m, &sum, staged ? &s.seg_max[w * n_seg] : nullptr);
+      total = sum.hi;
+      rest = sum.lo;
     }
     if (lane == 0) {
-      s.base[w] = base;
-      s.base32[w] = (float)base;
-      s.top[w] = top;
+      // a row of -inf, and one with a NaN or +inf, has no distribution
+      const bool good = live && fabsf(m) < INFINITY && total + rest < INFINITY;
+      s.top[w] = good ? m : 0.f;
+      s.sum_hi[w] = good ? total : 0.f;  // 0: no candidates of its own
+      s.sum_lo[w] = rest;
+      s.score[w] = sc;
+      s.done[w] = fin && fabsf(sc) < INFINITY;
     }
   }
   __syncthreads();
+  for (int w = tid; w < W; w += BP_THREADS) {
+    const double b = s.sum_hi[w] > 0.f ? (double)s.score[w] - log((double)s.sum_hi[w] + (double)s.sum_lo[w])
+                                       : -(double)INFINITY;
+    s.base[w] = b;
+    s.base32[w] = (float)b;
+  }
+  __syncthreads();
+  auto seg_max = [&](int i) { return staged ? s.seg_max[i] : __ldg(&seg[i]).x; };
 
   // 2. the bound.  Few segments: the threads' best elements instead of their best segments
   const bool by_elem = n_all < 4 * M;
@@ -227,12 +248,12 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   } else {
     for (int i = tid; i < n_all; i += BP_THREADS) {
       const int w = i / n_seg;
-      if (s.base32[w] != -INFINITY) best = fmaxf(best, score_below(s.base32[w], s.top[w], __ldcg(&seg[i]).x, a.inv_t));
+      if (s.base32[w] != -INFINITY) best = fmaxf(best, score_below(s.base32[w], s.top[w], seg_max(i), a.inv_t));
     }
   }
   if (finished)
     for (int w = tid; w < W; w += BP_THREADS)
-      if (__ldg(finished + w) != 0 && fabsf(__ldg(score + w)) < INFINITY) best = fmaxf(best, __ldg(score + w));
+      if (s.done[w]) best = fmaxf(best, s.score[w]);
   const uint32_t mine = fkey(best);
   uint32_t t = 0;
   for (int b = 31; b >= 12; --b) {  // the leading bits give a lower bound already
@@ -249,7 +270,7 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   for (int i = tid; i < n_all; i += BP_THREADS) {
     const int w = i / n_seg;
     if (s.base32[w] == -INFINITY) continue;
-    const float m = __ldcg(&seg[i]).x;
+    const float m = seg_max(i);
     if (m >= s.zthr[w] && m > -INFINITY) {
       const int at = atomicAdd(&s.n_segs, 1);
       if (at < BP_SEGS) s.segs[at] = (uint32_t)i;
@@ -257,8 +278,11 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   }
   if (finished)
     for (int w = tid; w < W; w += BP_THREADS)
-      if (__ldg(finished + w) != 0 && fabsf(__ldg(score + w)) < INFINITY)
-        push(s, dkey((double)__ldg(score + w)), (uint32_t)w * (uint32_t)a.vocab);
+      if (s.done[w]) {
+        const int at = atomicAdd(&s.n, 1);
+        s.pos[at] = (uint32_t)w * (uint32_t)a.vocab;
+        s.key[at] = dkey((double)s.score[w]);
+      }
   __syncthreads();
   const int n_fin = s.n;  // a finished beam's candidate each (W <= DH_MAX_BEAMS: they fit)
   const bool many = s.n_segs > BP_SEGS;
@@ -275,7 +299,11 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
     }
   }
   __syncthreads();
-  if (many || s.n > BP_CAP) {
+  if (!many && s.n <= BP_CAP) {
+    score_pushed(s, a, n_fin);
+    __syncthreads();
+    if (s.n > 256 && s.n > M) keep_best(s, M);  // ranking below compares all pairs
+  } else {
     // too many level with the bound: walk the segments in (beam, token) order, keeping the M best.
     // Once M are held a segment enters only if its maximum at its first id would rank before the
     // M-th best (a finished beam's candidate may be held ahead of its turn).
@@ -288,7 +316,8 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
       // the M-th best pair, once M are held (s.n == M then)
       unsigned long long last = 0;
       uint32_t last_pos = 0xFFFFFFFFu;
-      if (s.n >= M) {
+      const int held = s.n;
+      if (held >= M) {
         __syncthreads();
         if (tid == 0) {
           s.last_key = ~0ull;
@@ -309,10 +338,13 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
         bool ok = false;
         if (i < n_all) {
           const int w = i / n_seg;
-          const float m = __ldcg(&seg[i]).x;
-          if (s.base32[w] != -INFINITY && m > -INFINITY && m >= s.zthr[w]) {
-            const unsigned long long k = dkey(exact_score(s, a, w, m));
-            ok = k > last || (k == last && (uint32_t)w * (uint32_t)a.vocab + (uint32_t)((i - w * n_seg) * SEG) < last_pos);
+          if (s.base32[w] != -INFINITY) {
+            const float m = seg_max(i);
+            if (m > -INFINITY && m >= s.zthr[w]) {
+              const unsigned long long k = dkey(exact_score(s, a, w, m));
+              ok = k > last ||
+                   (k == last && (uint32_t)w * (uint32_t)a.vocab + (uint32_t)((i - w * n_seg) * SEG) < last_pos);
+            }
           }
         }
         if (tid == 0) s.next = n_all;
@@ -331,11 +363,11 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
         push_vec<T>(s, a, u, id, w, s.zthr[w]);
       }
       __syncthreads();
+      score_pushed(s, a, held);
+      __syncthreads();
       if (s.n > M) keep_best(s, M);
       at = found + 1;
     }
-  } else if (s.n > 256 && s.n > M) {
-    keep_best(s, M);  // ranking below compares all pairs
   }
   __syncthreads();
 
@@ -352,7 +384,7 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
     if (rank < M) {
       const int w = (int)(p / (uint32_t)a.vocab);
       parent[rank] = w;
-      token[rank] = finished && __ldg(finished + w) != 0 ? a.pad_token : (int)(p - (uint32_t)w * (uint32_t)a.vocab);
+      token[rank] = s.done[w] ? a.pad_token : (int)(p - (uint32_t)w * (uint32_t)a.vocab);
       out[rank] = (float)dkey_inv(k);
     }
   }
@@ -387,7 +419,7 @@ cudaError_t launch_beam_select(const Ctx& c, const void* logits, long long rs, l
                                const int32_t* finished, const float2* seg, int R, int W, int vocab, int M, int dtype,
                                float temperature, int pad_token, int32_t* parent, int32_t* token, float* score_out) {
   BeamArgs a{logits, rs, ws, score, finished, seg, W, vocab, M, row_segments(vocab, dtype), pad_token, temperature,
-             1.f / temperature, parent, token, score_out};
+             1.f / temperature, 1.0 / (double)temperature, parent, token, score_out};
   return dtype == DH_BF16 ? run<__nv_bfloat16>(c, a, R) : run<float>(c, a, R);
 }
 

@@ -383,6 +383,8 @@ struct DistillArgs {
   const float2* seg;       // [N x n_seg] (max, sum) of the segments
   float2* stats_out;
   float* loss_out;
+  float* gathered;         // [N x K] the entries' logits, where the gradient overwrites them; or null
+  int* status;             // device status word, or null
   int N, vocab, K, n_seg, splits;
   float temperature, inv_t, c;  // c = log2(e) / T
 };
@@ -393,7 +395,13 @@ bool rows_aligned(const void* logits, long long rs, long long ws, int R, int W, 
 // are left out.
 cudaError_t launch_row_stats(const Ctx& c, const void* logits, long long rs, long long ws, int R, int W, int vocab,
                              int dtype, float temperature, const float* score, const int32_t* finished, float2* seg);
-cudaError_t launch_distill_loss(const Ctx& c, const DistillArgs& a, int dtype);
+// The kernels of distill.cu and distill_ring.cu; which of them a call takes is api.cu's choice.
+// launch_distill_ring: statistics (stats_out) and dense gradient; *done is false, and nothing was
+// launched, where the rows are too long.
+cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done);
+cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype);
+cudaError_t launch_distill_dense(const Ctx& c, const DistillArgs& a, int dtype);
+cudaError_t launch_distill_finish(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad);
 cudaError_t launch_distill_grad(const Ctx& c, const DistillArgs& a, int dtype);
 
 // Beam selection (beam.cu).

@@ -4,21 +4,29 @@
 // With p = softmax(y / T) over the teacher's entries and q = softmax(z / T) over the vocabulary,
 //   loss = T^2 sum_k p_k (log p_k - log q[id_k]),   dz[v] = g T (q[v] - sum of the p_k with id_k = v).
 // Only the normaliser of q needs the whole row; the entries are a sparse correction of the dense
-// term g T q.  So the loss reads the row once (row_stats.cu) and finishes with K gathered logits,
-// and the gradient reads it once and writes it once: both are bound by HBM.
+// term g T q.  So every form is a statistics pass, a dense pass (both bound by HBM) and a small
+// kernel for the entries:
+//   loss              k_row_stats (row_stats.cu), k_distill_finish
+//   gradient          k_distill_dense, k_distill_finish
+//   both              k_distill_ring (distill_ring.cu: statistics and dense term in one pass over the
+//                     logits), k_distill_finish
+//   gradient where the rows do not lie like their logits, or in the logits' place: k_distill_grad
 //
-// k_distill_loss: one block per row; the segments' pairs -> (max, sum), the teacher's softmax, the
-//   loss.
-// k_distill_grad: `splits` blocks per row, each streaming its part of the row.  The logits of the
-//   part's entries are read before the dense pass writes anything (the gradient may overwrite the
-//   logits); after the pass the same block writes the entries' values, one writer per id: the first
-//   entry of an id adds up the others' p in order, so repeated ids repeat bit for bit.
+// k_distill_dense: every vector of a row times one factor; `splits` blocks per row.
+// k_distill_finish: one warp per row: the teacher's softmax, the loss, and the entries' values over
+//   the dense ones, one writer per id: the first entry of an id adds up the others' p in order, so
+//   repeated ids repeat bit for bit.  A hash table in shared memory finds out whether there are any.
+//   Latency-bound: a chain of four dependent loads per row, all rows at once.
+// k_distill_grad: dense term and entries in one kernel; the logits of a part's entries are read
+//   before its dense pass writes anything.
+
 #include "rows.cuh"
 
 namespace dh {
 namespace {
 
-constexpr int DL_THREADS = 128;
+constexpr int DF_WARPS = 4;
+constexpr int DF_BATCH = 4;
 constexpr int DG_THREADS = 256;
 constexpr int DG_UNROLL = 4;
 
@@ -81,54 +89,6 @@ __device__ __forceinline__ Teacher teacher_row(const int32_t* __restrict__ idx, 
   return t;
 }
 
-// T^2 sum_k p_k (log p_k - log q_k) of one row, by the whole block (every thread gets it).
-template <typename T, int NT>
-__device__ __forceinline__ float row_loss(const T* row, const float* __restrict__ y, int nk, const Teacher& t,
-                                          const int32_t* s_id, const float* s_p, float m, float sum, float temperature,
-                                          float inv_t, float* red) {
-  const float log_sum = logf(sum);
-  float part = 0.f;
-  for (int k = threadIdx.x; k < nk; k += NT) {
-    const float p = s_p[k];
-    if (s_id[k] < 0 || p == 0.f) continue;  // 0 log 0 = 0
-    const float z = Elem<T>::to_f(row[s_id[k]]);
-    const float log_q = m == -INFINITY ? -INFINITY : (z - m) * inv_t - log_sum;
-    part += p * (((__ldg(y + k) - t.top) * inv_t - t.log_total) - log_q);
-  }
-  return temperature * temperature * block_sum<NT>(part, red);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(DL_THREADS) k_distill_loss(DistillArgs a) {
-  __shared__ int32_t s_id[DH_MAX_K];
-  __shared__ float s_p[DH_MAX_K];
-  __shared__ float red[DL_THREADS / 32];
-  __shared__ float s_m, s_s;
-  const int row = blockIdx.x;
-  const int32_t* idx = a.idx + (size_t)row * a.K;
-  const float* y = a.teacher + (size_t)row * a.K;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int nk = a.n_valid ? min(max(__ldg(a.n_valid + row), 0), a.K) : a.K;
-  if (threadIdx.x < 32) {
-    float m;
-    Sum2 s;
-    row_combine(a.seg + (size_t)row * a.n_seg, a.n_seg, a.inv_t, &m, &s);
-    if (threadIdx.x == 0) {
-      s_m = m;
-      s_s = s.hi + s.lo;
-      if (a.stats_out) a.stats_out[row] = make_float2(m, s_s);
-    }
-  }
-  const Teacher t = teacher_row<DL_THREADS>(idx, y, nk, a.vocab, a.inv_t, s_id, s_p, red);
-  __syncthreads();
-  float loss = 0.f;
-  if (t.any)
-    loss = row_loss<T, DL_THREADS>(static_cast<const T*>(a.logits) + (size_t)row * a.ld, y, nk, t, s_id, s_p, s_m, s_s,
-                                   a.temperature, a.inv_t, red);
-  if (threadIdx.x == 0) a.loss_out[row] = loss;
-}
-
 // Loads that may see memory which this kernel writes later (the gradient in the logits' place).
 __device__ __forceinline__ uint4 ld16_rw(const void* p) {
   uint4 r;
@@ -149,27 +109,6 @@ __device__ __forceinline__ uint4 ld16_elems(const T* p) {
   for (int e = 0; e < PER; ++e) {
     if constexpr (sizeof(T) == 4) w[e] = elem_bits(*(const volatile float*)(p + e));
     else w[e / 2] |= (uint32_t)(*(const volatile unsigned short*)(p + e)) << (16 * (e & 1));
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// a 2^((z - m) c) for the elements of a vector, rounded once to the logits' type.
-template <typename T>
-__device__ __forceinline__ uint4 grad_vec(const uint4& u, float m, float c, float a) {
-  constexpr int PER = Elem<T>::PER16;
-  float z[PER];
-  Elem<T>::unpack(u, z);
-#pragma unroll
-  for (int e = 0; e < PER; ++e) z[e] = a * row_ex2((z[e] - m) * c);
-  uint32_t w[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if constexpr (sizeof(T) == 4) {
-      w[q] = __float_as_uint(z[q]);
-    } else {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(z[2 * q], z[2 * q + 1]);
-      w[q] = *reinterpret_cast<const uint32_t*>(&b);
-    }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -217,10 +156,11 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_grad(DistillArgs a) {
   // a row of -inf has q = 0 everywhere
   const bool nothing = m == -INFINITY;
   // a NaN among the teacher's entries (its total then is one) makes the whole row NaN
-  const float aq = t.log_total != t.log_total ? t.log_total : (nothing ? 0.f : g / sum), mm = nothing ? 0.f : m;
+  const ExpRef ref(nothing ? 0.f : m, a.c);
+  const float aq = t.log_total != t.log_total ? t.log_total : (nothing ? 0.f : ref.by_max(g / sum, a.c));
   const T* zv = z + pre;
   const bool same = ((reinterpret_cast<uintptr_t>(zv)) & 15u) == 0;
-  auto scalar = [&](int i) { out[i] = Elem<T>::from_f(aq * row_ex2((Elem<T>::to_f(z[i]) - mm) * a.c)); };
+  auto scalar = [&](int i) { out[i] = Elem<T>::from_f(aq * one_exp(Elem<T>::to_f(z[i]), ref, a.c)); };
   if (part == 0)
     for (int i = tid; i < pre; i += DG_THREADS) scalar(i);
   if (part == a.splits - 1)
@@ -235,7 +175,7 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_grad(DistillArgs a) {
 #pragma unroll
     for (int q = 0; q < DG_UNROLL; ++q) {
       const int jj = j + q * DG_THREADS;
-      if (jj < vhi) st16(out + pre + (long long)jj * PER, grad_vec<T>(u[q], mm, a.c, aq));
+      if (jj < vhi) st16(out + pre + (long long)jj * PER, grad_vec<T>(u[q], ref, a.c, aq));
     }
   }
   __syncthreads();  // the entries' values below come after the dense ones
@@ -249,7 +189,199 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_grad(DistillArgs a) {
       if (j < k) { first = false; break; }
       p += s_p[j];
     }
-    if (first) out[id] = Elem<T>::from_f(aq * row_ex2((s_z[k] - mm) * a.c) - g * p);
+    if (first) out[id] = Elem<T>::from_f(aq * one_exp(s_z[k], ref, a.c) - g * p);
+  }
+}
+
+// ---------------------------------------------------------------- dense term
+
+template <typename T>
+__global__ void __launch_bounds__(DG_THREADS) k_distill_dense(DistillArgs a) {
+  constexpr int PER = Elem<T>::PER16;
+  const int row = blockIdx.x / a.splits, part = blockIdx.x - row * a.splits;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const T* z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
+  T* out = static_cast<T*>(a.grad) + (long long)row * a.gld;
+  const int tid = threadIdx.x;
+  const int pre = min(a.vocab, (int)(((16u - (unsigned)(reinterpret_cast<uintptr_t>(z) & 15u)) & 15u) / sizeof(T)));
+  const int nvec = (a.vocab - pre) / PER;
+  const int vlo = (int)((long long)nvec * part / a.splits), vhi = (int)((long long)nvec * (part + 1) / a.splits);
+  const float2 st = __ldg(a.stats + row);
+  const float g = __ldg(a.weight + row) * a.temperature;
+  const bool zero = g == 0.f || (a.n_valid && __ldg(a.n_valid + row) <= 0);
+  const bool nothing = st.x == -INFINITY;  // a row of -inf has q = 0 everywhere
+  const ExpRef ref(nothing ? 0.f : st.x, a.c);
+  const float aq = nothing ? 0.f : ref.by_max(g / st.y, a.c);
+  const T* zv = z + pre;
+  T* ov = out + pre;
+  if (part == 0) {
+    const int behind = pre + nvec * PER;
+    const int i = tid < pre ? tid : behind + tid - pre;
+    if (i < a.vocab) out[i] = Elem<T>::from_f(zero ? 0.f : aq * one_exp(Elem<T>::to_f(z[i]), ref, a.c));
+  }
+  if (zero) {
+    for (int j = vlo + tid; j < vhi; j += DG_THREADS) st16(ov + (long long)j * PER, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  for (int j = vlo + tid; j < vhi; j += DG_THREADS * DG_UNROLL) {
+    uint4 u[DG_UNROLL];
+#pragma unroll
+    for (int q = 0; q < DG_UNROLL; ++q)
+      if (j + q * DG_THREADS < vhi) u[q] = ld_nc_v4(zv + (long long)(j + q * DG_THREADS) * PER);
+#pragma unroll
+    for (int q = 0; q < DG_UNROLL; ++q)
+      if (j + q * DG_THREADS < vhi)
+        st16(ov + (long long)(j + q * DG_THREADS) * PER, grad_vec<T>(u[q], ref, a.c, aq));
+  }
+}
+
+// ---------------------------------------------------------------- entries
+
+// The logits of all entries (0 where there is none), for a gradient that overwrites them.
+template <typename T>
+__global__ void __launch_bounds__(256) k_distill_gather(DistillArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)a.N * a.K) return;
+  const int id = __ldg(a.idx + i);
+  const long long row = i / a.K;
+  a.gathered[i] =
+      id >= 0 && id < a.vocab ? Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.ld + id]) : 0.f;
+}
+
+// LOSS: write the loss (and stats_out).  GRAD: write the entries' gradient.  SEG: the row's statistics
+// come as its segments' pairs.
+template <typename T, bool LOSS, bool GRAD, bool SEG>
+__global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a, int table) {
+  // per warp: the entries' ids, p and logits [K], then the hash table (a power of two of at least 2 K)
+  extern __shared__ int32_t df_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * DF_WARPS + warp;
+  int32_t* const s_id = df_smem + warp * (3 * a.K + table);
+  float* const s_p = reinterpret_cast<float*>(s_id + a.K);
+  float* const s_z = s_p + a.K;
+  int32_t* const s_t = s_id + 3 * a.K;
+  if (GRAD)
+    for (int i = lane; i < table; i += 32) s_t[i] = -1;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (row >= a.N) return;
+  const T* const z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
+  const long long e0 = (long long)row * a.K;
+  const int nk = a.n_valid ? min(max(__ldg(a.n_valid + row), 0), a.K) : a.K;
+  const float g = GRAD ? __ldg(a.weight + row) * a.temperature : 0.f;
+
+  float m, sum;
+  if (SEG) {
+    Sum2 s;
+    row_combine(a.seg + (long long)row * a.n_seg, a.n_seg, a.inv_t, &m, &s);
+    sum = s.hi + s.lo;
+    if (a.stats_out && lane == 0) a.stats_out[row] = make_float2(m, sum);
+  } else {
+    const float2 st = __ldcg(a.stats + row);
+    m = st.x;
+    sum = st.y;
+  }
+  // DF_BATCH entries per lane at a time: their loads, which hang on nothing, are in flight together
+  float top = -INFINITY;
+  for (int k0 = lane; k0 < a.K; k0 += 32 * DF_BATCH) {
+    int id[DF_BATCH];
+    float y[DF_BATCH], zk[DF_BATCH];
+#pragma unroll
+    for (int e = 0; e < DF_BATCH; ++e) {
+      const int k = k0 + e * 32;
+      id[e] = k < a.K ? __ldg(a.idx + e0 + k) : -1;
+      y[e] = k < a.K ? __ldg(a.teacher + e0 + k) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < DF_BATCH; ++e) {
+      const int k = k0 + e * 32;
+      if (k >= nk || id[e] < 0 || id[e] >= a.vocab) id[e] = -1;
+      zk[e] = 0.f;
+      if (id[e] >= 0) zk[e] = a.gathered ? __ldcg(a.gathered + e0 + k) : Elem<T>::to_f(__ldg(z + id[e]));
+    }
+#pragma unroll
+    for (int e = 0; e < DF_BATCH; ++e) {
+      const int k = k0 + e * 32;
+      if (k >= nk) continue;
+      if (id[e] < 0) y[e] = -INFINITY;
+      s_id[k] = id[e];
+      s_p[k] = y[e];
+      s_z[k] = zk[e];
+      top = max_nan(top, y[e]);
+    }
+  }
+  top = warp_max(top);
+  T* const out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.gld : nullptr;
+  if (top == -INFINITY) {  // no entries
+    if (LOSS && lane == 0) a.loss_out[row] = 0.f;
+    // the dense pass knows a row without entries by its count alone
+    if (GRAD && nk > 0 && g != 0.f)
+      for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(0.f);
+    return;
+  }
+  float total = 0.f;
+  for (int k = lane; k < nk; k += 32) {
+    const float e = expf((s_p[k] - top) * a.inv_t);
+    total += e;
+  }
+  total = warp_sum(total);
+  const float inv = 1.f / total, log_total = logf(total), log_sum = logf(sum);
+  if (GRAD && g != 0.f && total != total) {  // a NaN among the entries
+    for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(total);
+    if (LOSS && lane == 0) a.loss_out[row] = total;
+    return;
+  }
+  const bool write = GRAD && g != 0.f;
+  float loss = 0.f;
+  bool twice = false;
+  for (int k = lane; k < nk; k += 32) {
+    const int id = s_id[k];
+    const float ak = (s_p[k] - top) * a.inv_t, p = expf(ak) * inv;
+    s_p[k] = p;
+    if (id < 0) continue;
+    if (LOSS && p != 0.f) {  // 0 log 0 = 0
+      const float log_q = m == -INFINITY ? -INFINITY : (s_z[k] - m) * a.inv_t - log_sum;
+      loss += p * ((ak - log_total) - log_q);
+    }
+    if (write) {
+      for (uint32_t h = (uint32_t)id * 0x9E3779B1u;; ++h) {  // at most half full: ends
+        const int old = atomicCAS(&s_t[h & (uint32_t)(table - 1)], -1, id);
+        if (old == -1) break;
+        if (old == id) {
+          twice = true;
+          break;
+        }
+      }
+    }
+  }
+  if (LOSS) {
+    loss = a.temperature * a.temperature * warp_sum(loss);
+    if (lane == 0) a.loss_out[row] = loss;
+  }
+  if (!write) return;
+  twice = __any_sync(0xFFFFFFFFu, twice);
+  const bool nothing = m == -INFINITY;
+  const ExpRef ref(nothing ? 0.f : m, a.c);
+  const float aq = nothing ? 0.f : ref.by_max(g / sum, a.c);
+  for (int k = lane; k < nk; k += 32) {
+    const int id = s_id[k];
+    if (id < 0) continue;
+    float p = s_p[k];
+    bool first = true;
+    if (twice)
+      for (int j = 0; j < nk; ++j) {
+        if (s_id[j] != id || j == k) continue;
+        if (j < k) {
+          first = false;
+          break;
+        }
+        p += s_p[j];
+      }
+    if (!first) continue;
+    out[id] = Elem<T>::from_f(aq * one_exp(s_z[k], ref, a.c) - g * p);
   }
 }
 
@@ -263,16 +395,6 @@ cudaLaunchConfig_t pdl_config(const Ctx& c, unsigned grid, unsigned block, cudaL
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cfg;
-}
-
-template <typename T>
-cudaError_t run_loss(const Ctx& c, const DistillArgs& a) {
-  cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)a.N, DL_THREADS, &at);
-  prof_before("distill_loss", c.stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_distill_loss<T>, a);
-  prof_after(c.stream);
-  return e;
 }
 
 template <typename T>
@@ -290,10 +412,64 @@ cudaError_t run_grad(const Ctx& c, DistillArgs a) {
   return e;
 }
 
+template <typename T>
+cudaError_t run_dense(const Ctx& c, DistillArgs a) {
+  const long long vecs = (a.vocab + Elem<T>::PER16 - 1) / Elem<T>::PER16;
+  long long splits = (8LL * c.num_sms + a.N - 1) / a.N;
+  splits = splits < vecs / 1024 ? splits : vecs / 1024;
+  a.splits = (int)(splits > 1 ? splits : 1);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)((long long)a.N * a.splits), DG_THREADS, &at);
+  prof_before("distill_dense", c.stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_distill_dense<T>, a);
+  prof_after(c.stream);
+  return e;
+}
+
+template <typename T>
+cudaError_t run_finish(const Ctx& c, const DistillArgs& a, bool loss, bool grad) {
+  int table = 0;
+  if (grad)
+    for (table = 32; table < 2 * a.K;) table *= 2;
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)((a.N + DF_WARPS - 1) / DF_WARPS), DF_WARPS * 32, &at);
+  cfg.dynamicSmemBytes = (size_t)DF_WARPS * (3 * a.K + table) * 4;  // 80 KB at most
+  auto go = [&](auto* kernel, unsigned long long* done) {
+    cudaError_t e = cfg.dynamicSmemBytes > 48 * 1024 ? allow_max_smem(kernel, c.device, done) : cudaSuccess;
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, a, table);
+    return e;
+  };
+  static unsigned long long done[4] = {};
+  prof_before("distill_finish", c.stream);
+  cudaError_t e;
+  if (loss && grad) e = go(k_distill_finish<T, true, true, false>, &done[0]);
+  else if (grad) e = go(k_distill_finish<T, false, true, false>, &done[1]);
+  else if (a.seg) e = go(k_distill_finish<T, true, false, true>, &done[2]);
+  else e = go(k_distill_finish<T, true, false, false>, &done[3]);
+  prof_after(c.stream);
+  return e;
+}
+
+template <typename T>
+cudaError_t run_gather(const Ctx& c, const DistillArgs& a) {
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)(((long long)a.N * a.K + 255) / 256), 256, &at);
+  prof_before("distill_gather", c.stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_distill_gather<T>, a);
+  prof_after(c.stream);
+  return e;
+}
+
 }  // namespace
 
-cudaError_t launch_distill_loss(const Ctx& c, const DistillArgs& a, int dtype) {
-  return dtype == DH_BF16 ? run_loss<__nv_bfloat16>(c, a) : run_loss<float>(c, a);
+cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype) {
+  return dtype == DH_BF16 ? run_gather<__nv_bfloat16>(c, a) : run_gather<float>(c, a);
+}
+cudaError_t launch_distill_dense(const Ctx& c, const DistillArgs& a, int dtype) {
+  return dtype == DH_BF16 ? run_dense<__nv_bfloat16>(c, a) : run_dense<float>(c, a);
+}
+cudaError_t launch_distill_finish(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad) {
+  return dtype == DH_BF16 ? run_finish<__nv_bfloat16>(c, a, loss, grad) : run_finish<float>(c, a, loss, grad);
 }
 cudaError_t launch_distill_grad(const Ctx& c, const DistillArgs& a, int dtype) {
   return dtype == DH_BF16 ? run_grad<__nv_bfloat16>(c, a) : run_grad<float>(c, a);

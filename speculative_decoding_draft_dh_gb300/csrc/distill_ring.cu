@@ -1,0 +1,361 @@
+// Distillation, statistics and dense gradient in one pass over the logits (definitions at
+// dh_distill_topk in dh.h; distill.cu has the other kernels).
+//
+// The gradient g T (q - p) needs the row's normaliser, so a row is read to its end before its first
+// gradient can be written.  Here a row stays in the shared memory of a cluster of C CTAs from its one
+// read to its one write: 4 bytes of traffic per bf16 logit instead of the 6 of two passes.
+//
+// k_distill_ring: persistent clusters, each walking rows; CTA c holds the c-th slice.
+//   producer (one thread)   bulk-copies the slices, chunk by chunk and row after row, into a ring of
+//                           slots; it runs ahead of the row at work by what the ring holds beyond a
+//                           slice, so memory stays busy through the reductions.
+//   consumers (16 warps)    pass A: maximum and sum of exp of the chunks as they arrive, each thread
+//                           with a running maximum; every warp puts its pair into all CTAs of the
+//                           cluster (a marked 64-bit word, no barrier) and combines all pairs in one
+//                           order.  Pass B: the dense term g T q from the slots, which
+//                           are handed back one by one.
+#include "rows.cuh"
+#include "sm100.cuh"
+
+namespace dh {
+namespace {
+
+constexpr int DR_WARPS = 16;
+constexpr int DR_NT = DR_WARPS * 32;            // consumers
+constexpr int DR_THREADS = DR_NT + 32;          // and the producer's warp
+constexpr int DR_CTAS = 1;                      // per SM
+constexpr int DR_MAX_C = 8;
+constexpr int DR_MAX_SLOTS = 32;
+constexpr int DR_CHUNK = 2 * DR_NT;             // vectors per chunk at most: two per thread
+constexpr long long DR_LIMIT = 4000000000ll;    // cycles (two seconds) after which a wait gives up
+
+struct RingArgs {
+  DistillArgs d;
+  int lg;       // C = 2^lg
+  int slots;    // ring slots
+  int slot;     // vectors per slot (a multiple of 32)
+  bool loose;   // rows may have elements beside their 16-byte grid
+};
+
+__device__ __forceinline__ void st16(void* p, const uint4& v) {
+  asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint32_t remote_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(sm100::smem_u32(p)), "r"(rank));
+  return r;
+}
+// The pairs that the warps exchange, in one 64-bit word each: the maximum's bits, and the sum's with
+// its last bit (2^-24 of it) given to a mark that changes whenever the slot is used again.  A word is
+// written and read whole, so it carries its own arrival: no fence has to wait for the gradient's
+// stores in flight, which one at cluster scope does (3 us per row).
+__device__ __forceinline__ unsigned long long pair_word(float m, float s, uint32_t mark) {
+  return (unsigned long long)__float_as_uint(m) << 32 | ((__float_as_uint(s) & ~1u) | mark);
+}
+__device__ __forceinline__ void put_word(uint32_t dst, unsigned long long w) {
+  asm volatile("st.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(dst), "l"(w) : "memory");
+}
+__device__ __forceinline__ unsigned long long get_word(const unsigned long long* p) {
+  unsigned long long w;
+  asm volatile("ld.relaxed.cluster.shared::cta.b64 %0, [%1];" : "=l"(w) : "r"(sm100::smem_u32(p)) : "memory");
+  return w;
+}
+// The wait of sm100::mbar_wait with its limit in SM cycles.
+__device__ __forceinline__ bool wait_cycles(uint64_t* bar, uint32_t parity) {
+  if (sm100::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (clock64() - t0 > DR_LIMIT) return false;
+  }
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A CTA's share of a row: vectors [lo, hi) of the row's 16-byte grid, which starts at element `pre`
+// and ends before element `behind`.  The first CTA also has the elements beside the grid.
+struct Slice {
+  int pre, behind, lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Slice slice_of(const T* z, int vocab, int part, int lg) {
+  Slice s;
+  s.pre = min(vocab, (int)(((16u - (unsigned)(reinterpret_cast<uintptr_t>(z) & 15u)) & 15u) / sizeof(T)));
+  const unsigned nvec = (unsigned)(vocab - s.pre) / Elem<T>::PER16;
+  s.behind = s.pre + (int)nvec * Elem<T>::PER16;
+  s.lo = (int)(nvec * (unsigned)part >> lg);
+  s.hi = (int)(nvec * (unsigned)(part + 1) >> lg);
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a) {
+  const DistillArgs& d = a.d;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  uint4* const ring = reinterpret_cast<uint4*>(ring_smem);         // [slots][slot]
+  __shared__ __align__(16) unsigned long long s_pair[2][DR_MAX_C * DR_WARPS];  // every warp's pair
+  __shared__ uint64_t full[DR_MAX_SLOTS], empty[DR_MAX_SLOTS];
+
+  const int lg = a.lg, C = 1 << lg, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cl = blockIdx.x >> lg, part = blockIdx.x & (C - 1), ncl = gridDim.x >> lg;
+  const T* const logits = static_cast<const T*>(d.logits);
+
+  if (tid == 0) {
+    for (int i = 0; i < a.slots; ++i) {
+      sm100::mbar_init(&full[i], 1);
+      sm100::mbar_init(&empty[i], DR_WARPS);
+    }
+    sm100::fence_barrier_init();
+  }
+  for (int i = tid; i < 2 * DR_MAX_C * DR_WARPS; i += DR_THREADS) (&s_pair[0][0])[i] = 1ull;  // marked as not yet put
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
+  if (C > 1) cluster_barrier();  // the others' slots are there before anything is put
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  bool failed = false;
+  auto give_up = [&] {
+    failed = true;
+    if (d.status) atomicOr(d.status, 1 << DH_ERR_TIMEOUT);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!failed && !wait_cycles(bar, parity)) give_up();
+  };
+
+  if (warp == DR_WARPS) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t phase = 1;  // the first round finds the slots free
+      for (long long row = cl; row < d.N; row += ncl) {
+        const T* z = logits + row * d.ld;
+        const Slice s = slice_of(z, d.vocab, part, lg);
+        const uint4* src = reinterpret_cast<const uint4*>(z + s.pre) + s.lo;
+        for (int v = 0; v < s.hi - s.lo; v += a.slot) {
+          const uint32_t bytes = (uint32_t)min(a.slot, s.hi - s.lo - v) * 16u;
+          wait(&empty[slot], phase);
+          sm100::mbar_arrive_expect_tx(&full[slot], bytes);
+          sm100::bulk_load(ring + (size_t)slot * a.slot, src + v, bytes, &full[slot]);
+          if (++slot == a.slots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (failed)  // no copy is left in flight
+        for (int i = 0; i < a.slots; ++i)
+          for (int k = 0; k < 2; ++k) (void)sm100::mbar_wait(&full[i], k, 10000000ull);
+    }
+  } else {
+    // ---------------------------------------------------------------- consumers
+    int slot_a = 0, slot_b = 0, it = 0;
+    uint32_t ph_a = 0;
+    constexpr uint32_t NEG = NegInf<T>::WORD;
+    // the element beside the grid that this thread holds, or -1
+    auto beside = [&](const Slice& s) {
+      if (!a.loose || part != 0 || warp != 0) return -1;
+      const int at = tid < s.pre ? tid : s.behind + tid - s.pre;
+      return at < d.vocab ? at : -1;
+    };
+    for (long long row = cl; row < d.N; row += ncl, ++it) {
+      const int par = it & 1;
+      const T* const z = logits + row * d.ld;
+      const Slice sl = slice_of(z, d.vocab, part, lg);
+      const int nl = sl.hi - sl.lo, lone = beside(sl);
+      const float x = lone >= 0 ? Elem<T>::to_f(*(const volatile T*)(z + lone)) : -INFINITY;
+      const float g = __ldg(d.weight + row) * d.temperature;
+      const bool zero = g == 0.f || (d.n_valid && __ldg(d.n_valid + row) <= 0);
+      float m = x, s = x == -INFINITY ? 0.f : row_ex2((x - x) * d.c);  // 1, or NaN
+      // two chunks at a time: four independent vectors per thread
+      for (int v = 0; v < nl; v += 2 * a.slot) {
+        uint4 u[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = min(a.slot, nl - v - h * a.slot);  // may be negative: no chunk
+          const uint4* const b = ring + (size_t)slot_a * a.slot;
+          if (n > 0) wait(&full[slot_a], ph_a);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            u[2 * h + i] = tid + i * DR_NT < n ? b[tid + i * DR_NT] : make_uint4(NEG, NEG, NEG, NEG);
+          if (n > 0 && ++slot_a == a.slots) {
+            slot_a = 0;
+            ph_a ^= 1;
+          }
+        }
+        const float mn = max_nan(m, vec_max<T>(u));
+        if (mn != m) {
+          s = m == -INFINITY ? 0.f : s * row_ex2((m - mn) * d.c);
+          m = mn;
+        }
+        if (m != -INFINITY) {
+          const ExpRef ref(m, d.c);
+          float t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = vec_expsum<T>(u[i], ref, d.c);
+          s += ref.by_max((t[0] + t[1]) + (t[2] + t[3]), d.c);
+        }
+      }
+      // the warp's pair, then everybody's
+      const float wm = warp_max(m);
+      s = m == -INFINITY ? 0.f : s * row_ex2((m - wm) * d.c);
+      s = warp_sum(s);
+      const uint32_t mark = (it >> 1) & 1;
+      if (lane < C) {
+        const unsigned long long word = pair_word(wm, s, mark);
+        if (C == 1) *reinterpret_cast<volatile unsigned long long*>(&s_pair[par][warp]) = word;
+        else put_word(remote_addr(&s_pair[par][part * DR_WARPS + warp], lane), word);
+      }
+      float pm[DR_MAX_C * DR_WARPS / 32], ps[DR_MAX_C * DR_WARPS / 32];
+      const long long t0 = clock64();
+#pragma unroll
+      for (int q = 0; q < DR_MAX_C * DR_WARPS / 32; ++q) {
+        const int i = lane + q * 32;
+        pm[q] = -INFINITY;
+        ps[q] = 0.f;
+        if (i >= C * DR_WARPS) continue;
+        unsigned long long word = get_word(&s_pair[par][i]);
+        while (((uint32_t)word & 1u) != mark && !failed) {
+          if (clock64() - t0 > DR_LIMIT) give_up();
+          word = get_word(&s_pair[par][i]);
+        }
+        pm[q] = __uint_as_float((uint32_t)(word >> 32));
+        ps[q] = __uint_as_float((uint32_t)word & ~1u);
+      }
+      __syncwarp();
+      failed = __any_sync(0xFFFFFFFFu, failed);
+      m = pm[0];
+#pragma unroll
+      for (int q = 1; q < DR_MAX_C * DR_WARPS / 32; ++q) m = max_nan(m, pm[q]);
+      m = warp_max(m);
+      s = 0.f;
+#pragma unroll
+      for (int q = 0; q < DR_MAX_C * DR_WARPS / 32; ++q)
+        if (pm[q] != -INFINITY) s += ps[q] * row_ex2((pm[q] - m) * d.c);
+      s = warp_sum(s);
+      // a wait that gave up leaves nothing that looks like a result
+      if (part == 0 && tid == 0) d.stats_out[row] = failed ? make_float2(NAN, NAN) : make_float2(m, s);
+
+      T* const out = static_cast<T*>(d.grad) + row * d.gld;
+      const bool nothing = m == -INFINITY;  // a row of -inf has q = 0
+      const ExpRef ref(nothing ? 0.f : m, d.c);
+      const float aq = nothing ? 0.f : ref.by_max(g / s, d.c);
+      uint4* o = reinterpret_cast<uint4*>(out + sl.pre) + sl.lo;
+      for (int v = 0; v < nl; v += 2 * a.slot) {
+        uint4 u[4];
+        const int slot_0 = slot_b;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = min(a.slot, nl - v - h * a.slot);
+          const uint4* const b = ring + (size_t)slot_b * a.slot;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (tid + i * DR_NT < n) u[2 * h + i] = b[tid + i * DR_NT];
+          if (n > 0 && ++slot_b == a.slots) slot_b = 0;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          sm100::mbar_arrive(&empty[slot_0]);
+          if (v + a.slot < nl) sm100::mbar_arrive(&empty[slot_0 + 1 == a.slots ? 0 : slot_0 + 1]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = min(a.slot, nl - v - h * a.slot);
+          uint4* const oh = o + v + h * a.slot;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (tid + i * DR_NT < n)
+              st16(oh + tid + i * DR_NT, zero ? make_uint4(0, 0, 0, 0) : grad_vec<T>(u[2 * h + i], ref, d.c, aq));
+        }
+      }
+      if (lone >= 0) out[lone] = Elem<T>::from_f(zero ? 0.f : aq * one_exp(x, ref, d.c));
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_barrier();  // no CTA leaves while another may still put something into it
+}
+
+template <typename T>
+cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
+  *done = false;
+  auto* kernel = k_distill_ring<T>;
+  static unsigned long long smem_done = 0;
+  cudaError_t e = allow_max_smem(kernel, c.device, &smem_done);
+  if (e == cudaSuccess) e = carveout_max_shared((const void*)kernel, c.device);
+  if (e != cudaSuccess) return e;
+  static int dyn_max[64] = {};
+  const int dv = c.device < 64 ? c.device : 0;
+  if (dyn_max[dv] == 0 || c.device >= 64) {
+    // each CTA's part of an SM's shared memory, of which every CTA takes 1 KB for itself
+    int per_sm = 0, most = max_dynamic_smem(kernel, c.device);
+    cudaFuncAttributes fa;
+    e = cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, c.device);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    const int share = (per_sm / DR_CTAS - 1024 - (int)fa.sharedSizeBytes) / 128 * 128;
+    dyn_max[dv] = share < most ? share : most;
+  }
+
+  RingArgs a = {};
+  a.d = d;
+  const int vecs = d.vocab / Elem<T>::PER16;
+  // The cut: the fewest CTAs that hold a row with a slot to spare, then more while the rows alone do
+  // not fill the SMs.
+  bool fits = false;
+  static const char* envc = getenv("DH_LG");
+  for (a.lg = 0; a.lg <= 3; ++a.lg) {
+    const int slice = (vecs >> a.lg) > 0 ? (vecs + (1 << a.lg) - 1) >> a.lg : 1;
+    const int chunks = (slice + DR_CHUNK - 1) / DR_CHUNK;
+    a.slot = ((slice + chunks - 1) / chunks + 31) / 32 * 32;
+    const int slots = dyn_max[dv] / (16 * a.slot);
+    a.slots = slots < DR_MAX_SLOTS ? slots : DR_MAX_SLOTS;
+    fits = a.slots >= chunks + 1;
+    if (envc && a.lg < atoi(envc)) continue;
+    if (fits && ((long long)d.N << a.lg >= DR_CTAS * c.num_sms || slice <= 512 || a.lg == 3 || envc)) break;
+  }
+  if (!fits) return cudaSuccess;
+  const int C = 1 << a.lg;
+  a.loose = !rows_aligned(d.logits, d.ld, 0, d.N, 1, (int)sizeof(T)) || d.vocab % Elem<T>::PER16 != 0;
+  *done = true;
+
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)C);
+  cfg.blockDim = dim3(DR_THREADS);
+  cfg.dynamicSmemBytes = (size_t)a.slots * a.slot * 16;
+  cfg.stream = c.stream;
+  cfg.attrs = at;
+  int fit = DR_CTAS * c.num_sms / C;
+  if (C > 1) {
+    static int clusters[64][4] = {};  // that run at once
+    if (clusters[dv][a.lg] == 0 || c.device >= 64) {
+      cudaLaunchConfig_t q = cfg;
+      q.attrs = at + 1;
+      q.numAttrs = 1;
+      q.dynamicSmemBytes = dyn_max[dv];
+      e = cudaOccupancyMaxActiveClusters(&clusters[dv][a.lg], kernel, &q);
+      if (e != cudaSuccess) return e;
+    }
+    fit = clusters[dv][a.lg];
+  }
+  if (fit < 1) fit = 1;
+  cfg.gridDim = dim3((unsigned)((d.N < fit ? d.N : fit) * C));
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  prof_before("distill_ring", c.stream);
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
+  prof_after(c.stream);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done) {
+  return dtype == DH_BF16 ? run<__nv_bfloat16>(c, a, done) : run<float>(c, a, done);
+}
+
+}  // namespace dh

@@ -41,11 +41,12 @@ __global__ void __launch_bounds__(RS_THREADS) k_row_stats(const T* __restrict__ 
     const float m = warp_max(vec_max<T>(u));
     float s = 0.f;
     if (m != -INFINITY) {
+      const ExpRef ref(m, c);
       float p[ROW_SEG_VECS];
 #pragma unroll
-      for (int v = 0; v < ROW_SEG_VECS; ++v) p[v] = vec_expsum<T>(u[v], m, c);
+      for (int v = 0; v < ROW_SEG_VECS; ++v) p[v] = vec_expsum<T>(u[v], ref, c);
       s = (p[0] + p[1]) + (p[2] + p[3]);
-      s = warp_sum(s);
+      s = ref.by_max(warp_sum(s), c);
     }
     if (lane == 0) seg[g] = make_float2(m, s);
   }

@@ -94,21 +94,109 @@ __device__ __forceinline__ float vec_max(const uint4 (&u)[N]) {
   }
 }
 
-// sum 2^((z - m) c) over the elements of a vector, in a fixed tree.  z - m is exact for the terms
-// near the maximum, so the dominating terms carry only the error of 2^x itself.
+// Two fp32 operations in one instruction, each rounded as its scalar form, on a pair in one register
+// pair.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The reference of a row's exponentials, in powers of two: 2^(z c - r) with r the rounded m c, so a
+// term takes one fused multiply-add and its argument one rounding.  What r's rounding leaves out,
+// m c - r, is the same factor for every term: excess() gives it to those who want the sum relative
+// to exp(z/T - m/T).  It is below 2^-15 in the exponent while |m c| < 1024; beyond that (large logits,
+// small temperatures, the type's limits) `far` asks for the terms by (z - m) c instead.
+struct ExpRef {
+  float m, r;
+  bool far;
+  __device__ __forceinline__ ExpRef(float m_, float c) : m(m_), r(m_ * c), far(!(fabsf(m_ * c) < 1024.f)) {
+    if (far) r = 0.f;
+  }
+  // sum 2^((z - m) c) from sum 2^(z c - r): 2^-x for the small x = m c - r by its first two terms
+  __device__ __forceinline__ float by_max(float s, float c) const {
+    return far ? s : fmaf(s, -0.6931471805599453f * fmaf(m, c, -r), s);
+  }
+};
+
+// The exponentials of the elements of a vector, in pairs.
 template <typename T>
-__device__ __forceinline__ float vec_expsum(const uint4& u, float m, float c) {
+__device__ __forceinline__ void vec_exp(const uint4& u, const ExpRef& e, float c, f32x2* z) {
   constexpr int PER = Elem<T>::PER16;
-  float z[PER];
-  Elem<T>::unpack(u, z);
+  float x[PER];
+  Elem<T>::unpack(u, x);
+  if (__builtin_expect(e.far, 0)) {
 #pragma unroll
-  for (int e = 0; e < PER; ++e) z[e] = row_ex2((z[e] - m) * c);
+    for (int q = 0; q < PER; ++q) x[q] = (x[q] - e.m) * c;
+  } else {
+    const f32x2 cc = pack2(c, c), nr = pack2(-e.r, -e.r);
 #pragma unroll
-  for (int o = PER / 2; o > 0; o >>= 1)
+    for (int q = 0; q < PER / 2; ++q) unpack2(fma2(pack2(x[2 * q], x[2 * q + 1]), cc, nr), x[2 * q], x[2 * q + 1]);
+  }
 #pragma unroll
-    for (int e = 0; e < PER / 2; ++e)
-      if (e < o) z[e] += z[e + o];
-  return z[0];
+  for (int q = 0; q < PER / 2; ++q) z[q] = pack2(row_ex2(x[2 * q]), row_ex2(x[2 * q + 1]));
+}
+__device__ __forceinline__ float one_exp(float z, const ExpRef& e, float c) {
+  return row_ex2(e.far ? (z - e.m) * c : fmaf(z, c, -e.r));
+}
+
+// Their sum, in a fixed tree.
+template <typename T>
+__device__ __forceinline__ float vec_expsum(const uint4& u, const ExpRef& e, float c) {
+  f32x2 z[Elem<T>::PER16 / 2];
+  vec_exp<T>(u, e, c, z);
+  f32x2 s = add2(z[0], z[1]);
+  if constexpr (Elem<T>::PER16 == 8) s = add2(s, add2(z[2], z[3]));
+  float a, b;
+  unpack2(s, a, b);
+  return a + b;
+}
+
+// The elements of a vector, each rounded once to the logits' type.
+template <typename T>
+__device__ __forceinline__ uint4 pack_vec(const float* z) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (sizeof(T) == 4) {
+      w[q] = __float_as_uint(z[q]);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(z[2 * q], z[2 * q + 1]);
+      w[q] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// a times the exponentials of a vector's elements, rounded once to the logits' type.
+template <typename T>
+__device__ __forceinline__ uint4 grad_vec(const uint4& u, const ExpRef& e, float c, float a) {
+  f32x2 z[Elem<T>::PER16 / 2];
+  vec_exp<T>(u, e, c, z);
+  const f32x2 aa = pack2(a, a);
+  float x[Elem<T>::PER16];
+#pragma unroll
+  for (int q = 0; q < Elem<T>::PER16 / 2; ++q) unpack2(mul2(z[q], aa), x[2 * q], x[2 * q + 1]);
+  return pack_vec<T>(x);
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -141,18 +229,35 @@ struct Sum2 {
 // A row's (max, sum) from its segments' pairs, by one warp; every lane gets the result.  The sum
 // is relative to exp((z - max)/T); a row of -inf gives (-inf, 0).  A NaN logit gives
 // (NaN, NaN), a +inf one (+inf, NaN).  inv_t = 1 / T.
+// maxima (may be null): takes the segments' maxima.
 __device__ __forceinline__ void row_combine(const float2* __restrict__ seg, int n_seg, float inv_t, float* m_out,
-                                            Sum2* sum_out) {
+                                            Sum2* sum_out, float* maxima = nullptr) {
+  constexpr int HELD = 8;  // pairs per lane that stay in registers, their loads in flight together
   const int lane = threadIdx.x & 31;
+  float2 q[HELD];
   float m = -INFINITY;
-  for (int i = lane; i < n_seg; i += 32) m = max_nan(m, __ldcg(&seg[i]).x);
+#pragma unroll
+  for (int e = 0; e < HELD; ++e)
+    q[e] = lane + e * 32 < n_seg ? __ldg(&seg[lane + e * 32]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+  for (int e = 0; e < HELD; ++e) {
+    m = max_nan(m, q[e].x);
+    if (maxima && lane + e * 32 < n_seg) maxima[lane + e * 32] = q[e].x;
+  }
+  for (int i = lane + HELD * 32; i < n_seg; i += 32) {
+    const float x = __ldg(&seg[i]).x;
+    m = max_nan(m, x);
+    if (maxima) maxima[i] = x;
+  }
   m = warp_max(m);
   Sum2 s;
-  for (int i = lane; i < n_seg; i += 32) {
-    const float2 q = __ldcg(&seg[i]);
-    // a segment of -inf alone adds nothing; a NaN sum stays one
-    if (q.x != -INFINITY) s.add(q.y * expf((q.x - m) * inv_t));
-  }
+  // a segment of -inf alone adds nothing; a NaN sum stays one
+  auto add = [&](const float2& p) {
+    if (p.x != -INFINITY) s.add(p.y * expf((p.x - m) * inv_t));
+  };
+#pragma unroll
+  for (int e = 0; e < HELD; ++e) add(q[e]);
+  for (int i = lane + HELD * 32; i < n_seg; i += 32) add(__ldg(&seg[i]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float h = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o), l = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);

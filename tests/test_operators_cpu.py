@@ -63,10 +63,11 @@ def test_distill_rejects_bad_arguments(lib, which):
 def test_distill_workspaces(lib):
     ws = lib.dh_distill_topk_workspace(512, 151936, binding.BF16)
     assert ws % 256 == 0 and ws >= 512 * 149 * 8  # a pair per 1024 logits
-    assert lib.dh_distill_topk_step_workspace(512, 151936, binding.BF16) >= ws + 512 * 8
+    assert lib.dh_distill_topk_step_workspace(512, 151936, 64, binding.BF16) >= ws + 512 * (8 + 64 * 4)
     for bad in ((0, 100, 0), (-1, 100, 0), (1, 0, 0), (1, 100, 2), (1, (1 << 21) + 1, 0)):
         assert lib.dh_distill_topk_workspace(*bad) == 0
-        assert lib.dh_distill_topk_step_workspace(*bad) == 0
+        assert lib.dh_distill_topk_step_workspace(bad[0], bad[1], 8, bad[2]) == 0
+    assert lib.dh_distill_topk_step_workspace(1, 100, 0, 0) == 0 == lib.dh_distill_topk_step_workspace(1, 100, 1025, 0)
 
 
 def test_beam_select_rejects_bad_arguments(lib):
