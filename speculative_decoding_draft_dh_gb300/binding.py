@@ -464,6 +464,11 @@ def verify_chain(logits, cand_idx, cand_prob, draft_token, u_accept, u_sample, *
 # wrote the inputs).
 
 
+# The current stream's handle (torch.cuda.current_stream(index).cuda_stream without the object).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run_on(stream, tensors, call):
     """call(raw stream, device) on the first tensor's device and on `stream` (None: that device's
     current one).  tensors: (name, tensor or None) pairs; all have to be on that device."""
@@ -474,9 +479,9 @@ def _run_on(stream, tensors, call):
             raise ValueError(f"{name} is on {t.device}, not on {first.device}")
     if stream is None:
         if index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream(index).cuda_stream, first.device)
+            return call(_raw_stream(index), first.device)
         with torch.cuda.device(index):
-            return call(torch.cuda.current_stream(index).cuda_stream, first.device)
+            return call(_raw_stream(index), first.device)
     if stream.device != first.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
     with torch.cuda.stream(stream):

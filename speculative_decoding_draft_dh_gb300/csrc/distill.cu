@@ -16,7 +16,10 @@
 // k_distill_finish: one warp per row: the teacher's softmax, the loss, and the entries' values over
 //   the dense ones, one writer per id: the first entry of an id adds up the others' p in order, so
 //   repeated ids repeat bit for bit.  A hash table in shared memory finds out whether there are any.
-//   Latency-bound: a chain of four dependent loads per row, all rows at once.
+//   Latency-bound (ids, then their logits, then the row's statistics), so it starts under the pass
+//   before it by programmatic dependent launch and waits for that pass only when it needs the
+//   statistics.  What it reads before the wait are the call's inputs: the kernels before it let it
+//   start only after their own wait, when those are complete.
 // k_distill_grad: dense term and entries in one kernel; the logits of a part's entries are read
 //   before its dense pass writes anything.
 
@@ -199,8 +202,9 @@ template <typename T>
 __global__ void __launch_bounds__(DG_THREADS) k_distill_dense(DistillArgs a) {
   constexpr int PER = Elem<T>::PER16;
   const int row = blockIdx.x / a.splits, part = blockIdx.x - row * a.splits;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now: k_distill_finish reads the call's inputs as soon as it may start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const T* z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
   T* out = static_cast<T*>(a.grad) + (long long)row * a.gld;
   const int tid = threadIdx.x;
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_dense(DistillArgs a) {
 // The logits of all entries (0 where there is none), for a gradient that overwrites them.
 template <typename T>
 __global__ void __launch_bounds__(256) k_distill_gather(DistillArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= (long long)a.N * a.K) return;
   const int id = __ldg(a.idx + i);
@@ -266,24 +270,12 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
   if (GRAD)
     for (int i = lane; i < table; i += 32) s_t[i] = -1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row >= a.N) return;
-  const T* const z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
-  const long long e0 = (long long)row * a.K;
-  const int nk = a.n_valid ? min(max(__ldg(a.n_valid + row), 0), a.K) : a.K;
-  const float g = GRAD ? __ldg(a.weight + row) * a.temperature : 0.f;
-
-  float m, sum;
-  if (SEG) {
-    Sum2 s;
-    row_combine(a.seg + (long long)row * a.n_seg, a.n_seg, a.inv_t, &m, &s);
-    sum = s.hi + s.lo;
-    if (a.stats_out && lane == 0) a.stats_out[row] = make_float2(m, sum);
-  } else {
-    const float2 st = __ldcg(a.stats + row);
-    m = st.x;
-    sum = st.y;
-  }
+  const bool mine = row < a.N;
+  const int at = mine ? row : a.N - 1;
+  const T* const z = static_cast<const T*>(a.logits) + (long long)at * a.ld;
+  const long long e0 = (long long)at * a.K;
+  const int nk = a.n_valid ? min(max(__ldg(a.n_valid + at), 0), a.K) : a.K;
+  const float g = GRAD ? __ldg(a.weight + at) * a.temperature : 0.f;
   // DF_BATCH entries per lane at a time: their loads, which hang on nothing, are in flight together
   float top = -INFINITY;
   for (int k0 = lane; k0 < a.K; k0 += 32 * DF_BATCH) {
@@ -314,38 +306,30 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
     }
   }
   top = warp_max(top);
-  T* const out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.gld : nullptr;
-  if (top == -INFINITY) {  // no entries
-    if (LOSS && lane == 0) a.loss_out[row] = 0.f;
-    // the dense pass knows a row without entries by its count alone
-    if (GRAD && nk > 0 && g != 0.f)
-      for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(0.f);
-    return;
-  }
+  const bool any = top != -INFINITY;
   float total = 0.f;
-  for (int k = lane; k < nk; k += 32) {
-    const float e = expf((s_p[k] - top) * a.inv_t);
-    total += e;
-  }
+  if (any)
+    for (int k = lane; k < nk; k += 32) {
+      const float e = expf((s_p[k] - top) * a.inv_t);
+      total += e;
+    }
   total = warp_sum(total);
-  const float inv = 1.f / total, log_total = logf(total), log_sum = logf(sum);
-  if (GRAD && g != 0.f && total != total) {  // a NaN among the entries
-    for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(total);
-    if (LOSS && lane == 0) a.loss_out[row] = total;
-    return;
-  }
-  const bool write = GRAD && g != 0.f;
-  float loss = 0.f;
+  const float inv = 1.f / total, log_total = logf(total);
+  // p, the loss relative to one of the entries' own logits, and whether an id comes twice
+  float zref = -INFINITY;
+  for (int k = lane; k < nk; k += 32)
+    if (s_id[k] >= 0) zref = max_nan(zref, s_z[k]);
+  zref = warp_max(zref);
+  if (!(fabsf(zref) < INFINITY)) zref = 0.f;
+  const bool write = GRAD && any && g != 0.f;
+  float part = 0.f;
   bool twice = false;
-  for (int k = lane; k < nk; k += 32) {
+  for (int k = lane; any && k < nk; k += 32) {
     const int id = s_id[k];
     const float ak = (s_p[k] - top) * a.inv_t, p = expf(ak) * inv;
     s_p[k] = p;
     if (id < 0) continue;
-    if (LOSS && p != 0.f) {  // 0 log 0 = 0
-      const float log_q = m == -INFINITY ? -INFINITY : (s_z[k] - m) * a.inv_t - log_sum;
-      loss += p * ((ak - log_total) - log_q);
-    }
+    if (LOSS && p != 0.f) part += p * ((ak - log_total) - (s_z[k] - zref) * a.inv_t);  // 0 log 0 = 0
     if (write) {
       for (uint32_t h = (uint32_t)id * 0x9E3779B1u;; ++h) {  // at most half full: ends
         const int old = atomicCAS(&s_t[h & (uint32_t)(table - 1)], -1, id);
@@ -357,12 +341,34 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
       }
     }
   }
-  if (LOSS) {
-    loss = a.temperature * a.temperature * warp_sum(loss);
-    if (lane == 0) a.loss_out[row] = loss;
+  if (LOSS) part = warp_sum(part);
+  twice = __any_sync(0xFFFFFFFFu, twice);
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
+  float m, sum;
+  if (SEG) {
+    Sum2 s;
+    row_combine(a.seg + (long long)row * a.n_seg, a.n_seg, a.inv_t, &m, &s);
+    sum = s.hi + s.lo;
+    if (a.stats_out && lane == 0) a.stats_out[row] = make_float2(m, sum);
+  } else {
+    const float2 st = __ldcg(a.stats + row);
+    m = st.x;
+    sum = st.y;
+  }
+  T* const out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.gld : nullptr;
+  if (LOSS && lane == 0) {
+    // sum_k p_k (log p_k - log q_k) with log q_k = (z_k - m)/T - log sum; a row of -inf: infinite
+    const float l = a.temperature * a.temperature * (part + ((m - zref) * a.inv_t + logf(sum)));
+    a.loss_out[row] = !any ? 0.f : (total != total ? total : (m == -INFINITY ? INFINITY : l));
+  }
+  // the dense pass knows a row without entries by its count alone, and no NaN among the entries
+  if (GRAD && nk > 0 && g != 0.f && (!any || total != total)) {
+    for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(any ? total : 0.f);
+    return;
   }
   if (!write) return;
-  twice = __any_sync(0xFFFFFFFFu, twice);
   const bool nothing = m == -INFINITY;
   const ExpRef ref(nothing ? 0.f : m, a.c);
   const float aq = nothing ? 0.f : ref.by_max(g / sum, a.c);
@@ -436,6 +442,9 @@ cudaError_t run_finish(const Ctx& c, const DistillArgs& a, bool loss, bool grad)
   cfg.dynamicSmemBytes = (size_t)DF_WARPS * (3 * a.K + table) * 4;  // 80 KB at most
   auto go = [&](auto* kernel, unsigned long long* done) {
     cudaError_t e = cfg.dynamicSmemBytes > 48 * 1024 ? allow_max_smem(kernel, c.device, done) : cudaSuccess;
+    // under the ring kernel it needs that kernel's carveout to start; under the others theirs, the
+    // default (a changed carveout waits for empty SMs: 68 against 45 us for a loss of 512 rows)
+    if (e == cudaSuccess && loss && grad) e = carveout_max_shared((const void*)kernel, c.device);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, a, table);
     return e;
   };

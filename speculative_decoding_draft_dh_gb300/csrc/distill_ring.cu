@@ -23,17 +23,15 @@ namespace {
 constexpr int DR_WARPS = 16;
 constexpr int DR_NT = DR_WARPS * 32;            // consumers
 constexpr int DR_THREADS = DR_NT + 32;          // and the producer's warp
-constexpr int DR_CTAS = 1;                      // per SM
 constexpr int DR_MAX_C = 8;
 constexpr int DR_MAX_SLOTS = 32;
-constexpr int DR_CHUNK = 2 * DR_NT;             // vectors per chunk at most: two per thread
+constexpr int DR_CHUNK = 2 * DR_NT;             // vectors per chunk: two per thread
 constexpr long long DR_LIMIT = 4000000000ll;    // cycles (two seconds) after which a wait gives up
 
 struct RingArgs {
   DistillArgs d;
   int lg;       // C = 2^lg
   int slots;    // ring slots
-  int slot;     // vectors per slot (a multiple of 32)
   bool loose;   // rows may have elements beside their 16-byte grid
 };
 
@@ -90,10 +88,10 @@ __device__ __forceinline__ Slice slice_of(const T* z, int vocab, int part, int l
 }
 
 template <typename T>
-__global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a) {
+__global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
   const DistillArgs& d = a.d;
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  uint4* const ring = reinterpret_cast<uint4*>(ring_smem);         // [slots][slot]
+  uint4* const ring = reinterpret_cast<uint4*>(ring_smem);         // [slots][DR_CHUNK]
   __shared__ __align__(16) unsigned long long s_pair[2][DR_MAX_C * DR_WARPS];  // every warp's pair
   __shared__ uint64_t full[DR_MAX_SLOTS], empty[DR_MAX_SLOTS];
 
@@ -109,10 +107,11 @@ __global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a
     sm100::fence_barrier_init();
   }
   for (int i = tid; i < 2 * DR_MAX_C * DR_WARPS; i += DR_THREADS) (&s_pair[0][0])[i] = 1ull;  // marked as not yet put
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   if (C > 1) cluster_barrier();  // the others' slots are there before anything is put
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now: the kernel after this one reads the call's inputs as soon as it may start
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   bool failed = false;
   auto give_up = [&] {
@@ -132,11 +131,11 @@ __global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a
         const T* z = logits + row * d.ld;
         const Slice s = slice_of(z, d.vocab, part, lg);
         const uint4* src = reinterpret_cast<const uint4*>(z + s.pre) + s.lo;
-        for (int v = 0; v < s.hi - s.lo; v += a.slot) {
-          const uint32_t bytes = (uint32_t)min(a.slot, s.hi - s.lo - v) * 16u;
+        for (int v = 0; v < s.hi - s.lo; v += DR_CHUNK) {
+          const uint32_t bytes = (uint32_t)min(DR_CHUNK, s.hi - s.lo - v) * 16u;
           wait(&empty[slot], phase);
           sm100::mbar_arrive_expect_tx(&full[slot], bytes);
-          sm100::bulk_load(ring + (size_t)slot * a.slot, src + v, bytes, &full[slot]);
+          sm100::bulk_load(ring + slot * DR_CHUNK, src + v, bytes, &full[slot]);
           if (++slot == a.slots) {
             slot = 0;
             phase ^= 1;
@@ -167,22 +166,8 @@ __global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a
       const float g = __ldg(d.weight + row) * d.temperature;
       const bool zero = g == 0.f || (d.n_valid && __ldg(d.n_valid + row) <= 0);
       float m = x, s = x == -INFINITY ? 0.f : row_ex2((x - x) * d.c);  // 1, or NaN
-      // two chunks at a time: four independent vectors per thread
-      for (int v = 0; v < nl; v += 2 * a.slot) {
-        uint4 u[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = min(a.slot, nl - v - h * a.slot);  // may be negative: no chunk
-          const uint4* const b = ring + (size_t)slot_a * a.slot;
-          if (n > 0) wait(&full[slot_a], ph_a);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            u[2 * h + i] = tid + i * DR_NT < n ? b[tid + i * DR_NT] : make_uint4(NEG, NEG, NEG, NEG);
-          if (n > 0 && ++slot_a == a.slots) {
-            slot_a = 0;
-            ph_a ^= 1;
-          }
-        }
+      // two chunks at a time, four independent vectors per thread; whole ones without bounds checks
+      auto take = [&](const uint4 (&u)[4]) {
         const float mn = max_nan(m, vec_max<T>(u));
         if (mn != m) {
           s = m == -INFINITY ? 0.f : s * row_ex2((m - mn) * d.c);
@@ -195,6 +180,38 @@ __global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a
           for (int i = 0; i < 4; ++i) t[i] = vec_expsum<T>(u[i], ref, d.c);
           s += ref.by_max((t[0] + t[1]) + (t[2] + t[3]), d.c);
         }
+      };
+      auto next_a = [&] {
+        if (++slot_a == a.slots) {
+          slot_a = 0;
+          ph_a ^= 1;
+        }
+      };
+      int v = 0;
+      for (; v + 2 * DR_CHUNK <= nl; v += 2 * DR_CHUNK) {
+        uint4 u[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4* const b = ring + slot_a * DR_CHUNK + tid;
+          wait(&full[slot_a], ph_a);
+          u[2 * h] = b[0];
+          u[2 * h + 1] = b[DR_NT];
+          next_a();
+        }
+        take(u);
+      }
+      if (v < nl) {
+        uint4 u[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = nl - v - h * DR_CHUNK;  // may be negative: no chunk
+          const uint4* const b = ring + slot_a * DR_CHUNK + tid;
+          if (n > 0) wait(&full[slot_a], ph_a);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) u[2 * h + i] = tid + i * DR_NT < n ? b[i * DR_NT] : make_uint4(NEG, NEG, NEG, NEG);
+          if (n > 0) next_a();
+        }
+        take(u);
       }
       // the warp's pair, then everybody's
       const float wm = warp_max(m);
@@ -206,33 +223,26 @@ __global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a
         if (C == 1) *reinterpret_cast<volatile unsigned long long*>(&s_pair[par][warp]) = word;
         else put_word(remote_addr(&s_pair[par][part * DR_WARPS + warp], lane), word);
       }
-      float pm[DR_MAX_C * DR_WARPS / 32], ps[DR_MAX_C * DR_WARPS / 32];
       const long long t0 = clock64();
-#pragma unroll
-      for (int q = 0; q < DR_MAX_C * DR_WARPS / 32; ++q) {
-        const int i = lane + q * 32;
-        pm[q] = -INFINITY;
-        ps[q] = 0.f;
-        if (i >= C * DR_WARPS) continue;
+      m = -INFINITY;
+      s = 0.f;
+      for (int i = lane; i < C * DR_WARPS; i += 32) {  // lane by lane in a fixed order
         unsigned long long word = get_word(&s_pair[par][i]);
         while (((uint32_t)word & 1u) != mark && !failed) {
           if (clock64() - t0 > DR_LIMIT) give_up();
           word = get_word(&s_pair[par][i]);
         }
-        pm[q] = __uint_as_float((uint32_t)(word >> 32));
-        ps[q] = __uint_as_float((uint32_t)word & ~1u);
+        const float pm = __uint_as_float((uint32_t)(word >> 32)), ps = __uint_as_float((uint32_t)word & ~1u);
+        const float mn = max_nan(m, pm);
+        s = (m == -INFINITY ? 0.f : s * row_ex2((m - mn) * d.c)) +
+            (pm == -INFINITY ? 0.f : ps * row_ex2((pm - mn) * d.c));
+        m = mn;
       }
       __syncwarp();
       failed = __any_sync(0xFFFFFFFFu, failed);
-      m = pm[0];
-#pragma unroll
-      for (int q = 1; q < DR_MAX_C * DR_WARPS / 32; ++q) m = max_nan(m, pm[q]);
+      const float lm = m;
       m = warp_max(m);
-      s = 0.f;
-#pragma unroll
-      for (int q = 0; q < DR_MAX_C * DR_WARPS / 32; ++q)
-        if (pm[q] != -INFINITY) s += ps[q] * row_ex2((pm[q] - m) * d.c);
-      s = warp_sum(s);
+      s = warp_sum(lm == -INFINITY ? 0.f : s * row_ex2((lm - m) * d.c));
       // a wait that gave up leaves nothing that looks like a result
       if (part == 0 && tid == 0) d.stats_out[row] = failed ? make_float2(NAN, NAN) : make_float2(m, s);
 
@@ -240,33 +250,37 @@ __global__ void __launch_bounds__(DR_THREADS, DR_CTAS) k_distill_ring(RingArgs a
       const bool nothing = m == -INFINITY;  // a row of -inf has q = 0
       const ExpRef ref(nothing ? 0.f : m, d.c);
       const float aq = nothing ? 0.f : ref.by_max(g / s, d.c);
-      uint4* o = reinterpret_cast<uint4*>(out + sl.pre) + sl.lo;
-      for (int v = 0; v < nl; v += 2 * a.slot) {
+      uint4* o = reinterpret_cast<uint4*>(out + sl.pre) + sl.lo + tid;
+      auto next_b = [&] {  // the slot is read: it goes back to the producer
+        if (lane == 0) sm100::mbar_arrive(&empty[slot_b]);
+        if (++slot_b == a.slots) slot_b = 0;
+      };
+      v = 0;
+      for (; v + 2 * DR_CHUNK <= nl && !zero; v += 2 * DR_CHUNK, o += 2 * DR_CHUNK) {
         uint4 u[4];
-        const int slot_0 = slot_b;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int n = min(a.slot, nl - v - h * a.slot);
-          const uint4* const b = ring + (size_t)slot_b * a.slot;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (tid + i * DR_NT < n) u[2 * h + i] = b[tid + i * DR_NT];
-          if (n > 0 && ++slot_b == a.slots) slot_b = 0;
+          const uint4* const b = ring + slot_b * DR_CHUNK + tid;
+          u[2 * h] = b[0];
+          u[2 * h + 1] = b[DR_NT];
+          __syncwarp();
+          next_b();
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st16(o + i * DR_NT, grad_vec<T>(u[i], ref, d.c, aq));
+      }
+      for (; v < nl; v += DR_CHUNK, o += DR_CHUNK) {
+        const int n = nl - v;
+        uint4 u[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (tid + i * DR_NT < n) u[i] = ring[slot_b * DR_CHUNK + tid + i * DR_NT];
         __syncwarp();
-        if (lane == 0) {
-          sm100::mbar_arrive(&empty[slot_0]);
-          if (v + a.slot < nl) sm100::mbar_arrive(&empty[slot_0 + 1 == a.slots ? 0 : slot_0 + 1]);
-        }
+        next_b();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = min(a.slot, nl - v - h * a.slot);
-          uint4* const oh = o + v + h * a.slot;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (tid + i * DR_NT < n)
-              st16(oh + tid + i * DR_NT, zero ? make_uint4(0, 0, 0, 0) : grad_vec<T>(u[2 * h + i], ref, d.c, aq));
-        }
+        for (int i = 0; i < 2; ++i)
+          if (tid + i * DR_NT < n)
+            st16(o + i * DR_NT, zero ? make_uint4(0, 0, 0, 0) : grad_vec<T>(u[i], ref, d.c, aq));
       }
       if (lone >= 0) out[lone] = Elem<T>::from_f(zero ? 0.f : aq * one_exp(x, ref, d.c));
     }
@@ -286,14 +300,7 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
   static int dyn_max[64] = {};
   const int dv = c.device < 64 ? c.device : 0;
   if (dyn_max[dv] == 0 || c.device >= 64) {
-    // each CTA's part of an SM's shared memory, of which every CTA takes 1 KB for itself
-    int per_sm = 0, most = max_dynamic_smem(kernel, c.device);
-    cudaFuncAttributes fa;
-    e = cudaDeviceGetAttribute(&per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, c.device);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    const int share = (per_sm / DR_CTAS - 1024 - (int)fa.sharedSizeBytes) / 128 * 128;
-    dyn_max[dv] = share < most ? share : most;
+    dyn_max[dv] = max_dynamic_smem(kernel, c.device);
   }
 
   RingArgs a = {};
@@ -302,16 +309,13 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
   // The cut: the fewest CTAs that hold a row with a slot to spare, then more while the rows alone do
   // not fill the SMs.
   bool fits = false;
-  static const char* envc = getenv("DH_LG");
   for (a.lg = 0; a.lg <= 3; ++a.lg) {
     const int slice = (vecs >> a.lg) > 0 ? (vecs + (1 << a.lg) - 1) >> a.lg : 1;
     const int chunks = (slice + DR_CHUNK - 1) / DR_CHUNK;
-    a.slot = ((slice + chunks - 1) / chunks + 31) / 32 * 32;
-    const int slots = dyn_max[dv] / (16 * a.slot);
+    const int slots = dyn_max[dv] / (16 * DR_CHUNK);
     a.slots = slots < DR_MAX_SLOTS ? slots : DR_MAX_SLOTS;
     fits = a.slots >= chunks + 1;
-    if (envc && a.lg < atoi(envc)) continue;
-    if (fits && ((long long)d.N << a.lg >= DR_CTAS * c.num_sms || slice <= 512 || a.lg == 3 || envc)) break;
+    if (fits && ((long long)d.N << a.lg >= c.num_sms || slice <= 512 || a.lg == 3)) break;
   }
   if (!fits) return cudaSuccess;
   const int C = 1 << a.lg;
@@ -327,10 +331,10 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C);
   cfg.blockDim = dim3(DR_THREADS);
-  cfg.dynamicSmemBytes = (size_t)a.slots * a.slot * 16;
+  cfg.dynamicSmemBytes = (size_t)a.slots * DR_CHUNK * 16;
   cfg.stream = c.stream;
   cfg.attrs = at;
-  int fit = DR_CTAS * c.num_sms / C;
+  int fit = c.num_sms / C;
   if (C > 1) {
     static int clusters[64][4] = {};  // that run at once
     if (clusters[dv][a.lg] == 0 || c.device >= 64) {

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(RS_THREADS) k_row_stats(const T* __restrict__ 
   const int lane = threadIdx.x & 31;
   const long long nw = (long long)gridDim.x * (RS_THREADS / 32);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only now: the kernel after this one reads the call's inputs as soon as it may start
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (long long g = (long long)blockIdx.x * (RS_THREADS / 32) + (threadIdx.x >> 5); g < n_items; g += nw) {
     const int row = (int)(g / n_seg), sgi = (int)(g - (long long)row * n_seg);

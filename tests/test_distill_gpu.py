@@ -226,15 +226,17 @@ def test_nan_and_inf_stay_in_their_rows():
     want_l, want_g = dh.distill_topk_step(z, idx, y, gl)
     z[1, 2999], z[2, 5], y[4, 3], y[5, 0] = float("nan"), float("inf"), float("nan"), float("inf")
     z[6] = float("nan")
-    l, stats = dh.distill_topk(z, idx, y)
-    _, g = dh.distill_topk_step(z, idx, y, gl)
+    fwd, stats = dh.distill_topk(z, idx, y)
+    l, g = dh.distill_topk_step(z, idx, y, gl)
+    back = dh.distill_topk_backward(z, idx, y, stats, gl)
     torch.cuda.synchronize()
     for n in (1, 2, 4, 5, 6):
-        assert torch.isnan(l[n]) and torch.isnan(g[n]).all()
+        assert torch.isnan(l[n]) and torch.isnan(fwd[n]) and torch.isnan(back[n]).all() and torch.isnan(g[n]).all()
     for n in (1, 2, 6):
         assert torch.isnan(stats[n, 1])
     for n in (0, 3, 7):
         assert torch.equal(l[n], want_l[n]) and torch.equal(g[n], want_g[n])
+        assert torch.isfinite(fwd[n]) and torch.isfinite(back[n]).all()
 
 
 @pytest.mark.parametrize("std", [0.0, 30.0, 1e4])
