@@ -469,25 +469,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run_on(stream, tensors, call):
-    """call(raw stream, device) on the first tensor's device and on `stream` (None: that device's
-    current one).  tensors: (name, tensor or None) pairs; all have to be on that device."""
-    first = tensors[0][1]
-    index = first.get_device()
-    for name, t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+def _elsewhere(stream, dev, tensors, call):
+    """call() with `dev` current and, if given, `stream`; the tensors (some may be None) are kept for
+    the stream."""
     if stream is None:
-        if index == torch.cuda.current_device():
-            return call(_raw_stream(index), first.device)
-        with torch.cuda.device(index):
-            return call(_raw_stream(index), first.device)
-    if stream.device != first.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.device(dev):
+            return call()
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     with torch.cuda.stream(stream):
-        out = call(stream.cuda_stream, first.device)
+        out = call()
         if not torch.cuda.is_current_stream_capturing():
-            for _, t in tensors:
+            for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
     return out
@@ -498,53 +491,51 @@ def _workspace_bytes(query, *sizes):
     return getattr(load_library(), query)(*sizes)
 
 
-def _scratch(nbytes, workspace, kind, dev, stream):
-    """The address of nbytes of device memory, not zeroed, and what keeps it: the caller's workspace
-    object's, else fresh."""
-    t = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev) if workspace is None else \
-        workspace.get(nbytes, dev, kind, stream)
-    return t.data_ptr(), t
+def _scratch(nbytes, workspace, kind, dev):
+    """nbytes of device memory, not zeroed: the caller's workspace object's, else fresh."""
+    if workspace is not None:
+        return workspace.get(nbytes, dev, kind)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _typed(t, name, dtype, shape):
-    """Checks a contiguous CUDA tensor of one dtype and shape."""
+def _typed(t, name, dtype, shape, index):
+    """Checks a contiguous tensor of one dtype and shape on CUDA device `index`."""
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    return t
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on CUDA device {index}, not on {t.device}")
 
 
 def _rows(t, name):
-    """Checks of a [.., vocab] tensor of logits whose elements of a row are adjacent."""
-    if not t.is_cuda:
+    """Checks a [.., vocab] CUDA tensor of logits whose elements of a row are adjacent; its dtype's
+    code and its device's index."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     code = _dtype_code(t)
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent (last stride 1)")
-    return code
+    return code, index
 
 
-def _distill_inputs(logits, idx, teacher, n_valid, grad_loss=None):
+def _distill_inputs(logits, idx, teacher, n_valid):
     if logits.dim() != 2 or idx.dim() != 2:
         raise ValueError("logits must be [N, vocab] and idx [N, K]")
-    dt = _rows(logits, "logits")
+    dt, index = _rows(logits, "logits")
     N, vocab = logits.shape
     K = idx.shape[1]
-    _typed(idx, "idx", torch.int32, (N, K))
-    _typed(teacher, "teacher", torch.float32, (N, K))
+    _typed(idx, "idx", torch.int32, (N, K), index)
+    _typed(teacher, "teacher", torch.float32, (N, K), index)
     if n_valid is not None:
-        _typed(n_valid, "n_valid", torch.int32, (N,))
-    if grad_loss is not None:
-        _typed(grad_loss, "grad_loss", torch.float32, (N,))
-    return dt, N, vocab, K
+        _typed(n_valid, "n_valid", torch.int32, (N,), index)
+    return dt, index, N, vocab, K
 
 
-def _grad_rows(logits, grad_out):
+def _grad_rows(logits, grad_out, index):
     """grad_out checked, or memory for the gradient in rows as far apart as those of `logits` (where
     they do not overlap)."""
     N, vocab = logits.shape
@@ -555,14 +546,18 @@ def _grad_rows(logits, grad_out):
         return torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
     if grad_out.dtype != logits.dtype or grad_out.shape != logits.shape:
         raise ValueError("grad_out must have the logits' dtype and shape")
-    _rows(grad_out, "grad_out")
+    if _rows(grad_out, "grad_out")[1] != index:
+        raise ValueError(f"grad_out must be on CUDA device {index}")
     if N > 1 and grad_out.stride(0) < vocab:
         raise ValueError("the rows of grad_out must not overlap")
     return grad_out
 
 
 def _out(t, name, dtype, shape, dev):
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _typed(t, name, dtype, shape)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _typed(t, name, dtype, shape, dev.index)
+    return t
 
 
 def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_out=None, stats_out=None, workspace=None,
@@ -572,19 +567,20 @@ def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_ou
     int32 [N] count (dh_distill_topk).  Returns (loss fp32 [N], stats fp32 [N, 2]: each row's
     maximum and sum of exp((z - max) / T), which the gradient takes)."""
     lib = load_library()
-    dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
-
-    def call(raw, dev):
-        loss = _out(loss_out, "loss_out", torch.float32, (N,), dev)
-        stats = _out(stats_out, "stats_out", torch.float32, (N, 2), dev)
-        nbytes = _workspace_bytes("dh_distill_topk_workspace", N, vocab, dt)
-        ws, _keep = _scratch(nbytes, workspace, "distill", dev, stream)
-        _check(lib.dh_distill_topk(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
-                                   _addr(n_valid), N, vocab, K, dt, temperature, loss.data_ptr(), stats.data_ptr(), ws,
-                                   nbytes, raw), "dh_distill_topk")
-        return loss, stats
-    return _run_on(stream, (("logits", logits), ("idx", idx), ("teacher", teacher), ("n_valid", n_valid),
-                            ("loss_out", loss_out), ("stats_out", stats_out)), call)
+    dt, index, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
+    dev = logits.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (logits, idx, teacher, n_valid, loss_out, stats_out), lambda: distill_topk(
+            logits, idx, teacher, n_valid=n_valid, temperature=temperature, loss_out=loss_out, stats_out=stats_out,
+            workspace=workspace))
+    loss = _out(loss_out, "loss_out", torch.float32, (N,), dev)
+    stats = _out(stats_out, "stats_out", torch.float32, (N, 2), dev)
+    nbytes = _workspace_bytes("dh_distill_topk_workspace", N, vocab, dt)
+    ws = _scratch(nbytes, workspace, "distill", dev)
+    _check(lib.dh_distill_topk(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(), _addr(n_valid),
+                               N, vocab, K, dt, temperature, loss.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes,
+                               _raw_stream(index)), "dh_distill_topk")
+    return loss, stats
 
 
 def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=None, temperature=1.0, grad_out=None,
@@ -593,18 +589,19 @@ def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=Non
     distill_topk returned for the same inputs (dh_distill_topk_backward).  grad_out may be the
     logits themselves.  Returns it, in the logits' dtype."""
     lib = load_library()
-    dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid, grad_loss)
-    _typed(stats, "stats", torch.float32, (N, 2))
-
-    def call(raw, dev):
-        grad = _grad_rows(logits, grad_out)
-        _check(lib.dh_distill_topk_backward(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
-                                            _addr(n_valid), stats.data_ptr(), grad_loss.data_ptr(), N, vocab, K, dt,
-                                            temperature, grad.data_ptr(), grad.stride(0), raw),
-               "dh_distill_topk_backward")
-        return grad
-    return _run_on(stream, (("logits", logits), ("idx", idx), ("teacher", teacher), ("n_valid", n_valid),
-                            ("stats", stats), ("grad_loss", grad_loss), ("grad_out", grad_out)), call)
+    dt, index, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
+    _typed(stats, "stats", torch.float32, (N, 2), index)
+    _typed(grad_loss, "grad_loss", torch.float32, (N,), index)
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, logits.device, (logits, idx, teacher, n_valid, stats, grad_loss, grad_out),
+                          lambda: distill_topk_backward(logits, idx, teacher, stats, grad_loss, n_valid=n_valid,
+                                                        temperature=temperature, grad_out=grad_out))
+    grad = _grad_rows(logits, grad_out, index)
+    _check(lib.dh_distill_topk_backward(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
+                                        _addr(n_valid), stats.data_ptr(), grad_loss.data_ptr(), N, vocab, K, dt,
+                                        temperature, grad.data_ptr(), grad.stride(0), _raw_stream(index)),
+           "dh_distill_topk_backward")
+    return grad
 
 
 def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperature=1.0, loss_out=None, grad_out=None,
@@ -613,20 +610,23 @@ def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperat
     are known beforehand (dh_distill_topk_step).  grad_out may be the logits themselves.  Returns
     (loss fp32 [N], gradient)."""
     lib = load_library()
-    dt, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid, grad_loss)
-
-    def call(raw, dev):
-        loss = _out(loss_out, "loss_out", torch.float32, (N,), dev)
-        grad = _grad_rows(logits, grad_out)
-        nbytes = _workspace_bytes("dh_distill_topk_step_workspace", N, vocab, K, dt)
-        ws, _keep = _scratch(nbytes, workspace, "distill_step", dev, stream)
-        _check(lib.dh_distill_topk_step(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
-                                        _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, temperature,
-                                        loss.data_ptr(), grad.data_ptr(), grad.stride(0), ws, nbytes, raw),
-               "dh_distill_topk_step")
-        return loss, grad
-    return _run_on(stream, (("logits", logits), ("idx", idx), ("teacher", teacher), ("n_valid", n_valid),
-                            ("grad_loss", grad_loss), ("loss_out", loss_out), ("grad_out", grad_out)), call)
+    dt, index, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
+    _typed(grad_loss, "grad_loss", torch.float32, (N,), index)
+    dev = logits.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (logits, idx, teacher, n_valid, grad_loss, loss_out, grad_out),
+                          lambda: distill_topk_step(logits, idx, teacher, grad_loss, n_valid=n_valid,
+                                                    temperature=temperature, loss_out=loss_out, grad_out=grad_out,
+                                                    workspace=workspace))
+    loss = _out(loss_out, "loss_out", torch.float32, (N,), dev)
+    grad = _grad_rows(logits, grad_out, index)
+    nbytes = _workspace_bytes("dh_distill_topk_step_workspace", N, vocab, K, dt)
+    ws = _scratch(nbytes, workspace, "distill_step", dev)
+    _check(lib.dh_distill_topk_step(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
+                                    _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, temperature,
+                                    loss.data_ptr(), grad.data_ptr(), grad.stride(0), ws.data_ptr(), nbytes,
+                                    _raw_stream(index)), "dh_distill_topk_step")
+    return loss, grad
 
 
 def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0, parent_out=None, token_out=None,
@@ -638,26 +638,26 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     lib = load_library()
     if logits.dim() != 3:
         raise ValueError("logits must be [R, W, vocab]")
-    dt = _rows(logits, "logits")
+    dt, index = _rows(logits, "logits")
     R, W, vocab = logits.shape
-    _typed(score, "score", torch.float32, (R, W))
+    _typed(score, "score", torch.float32, (R, W), index)
     if finished is not None:
-        _typed(finished, "finished", torch.int32, (R, W))
-    M = int(M)
-
-    def call(raw, dev):
-        size = (R, max(M, 0))
-        parent = _out(parent_out, "parent_out", torch.int32, size, dev)
-        token = _out(token_out, "token_out", torch.int32, size, dev)
-        best = _out(score_out, "score_out", torch.float32, size, dev)
-        nbytes = _workspace_bytes("dh_beam_select_workspace", R, W, vocab, dt)
-        ws, _keep = _scratch(nbytes, workspace, "beam", dev, stream)
-        _check(lib.dh_beam_select(logits.data_ptr(), logits.stride(0), logits.stride(1), score.data_ptr(),
-                                  _addr(finished), R, W, vocab, M, dt, temperature, int(pad_token), parent.data_ptr(),
-                                  token.data_ptr(), best.data_ptr(), ws, nbytes, raw), "dh_beam_select")
-        return parent, token, best
-    return _run_on(stream, (("logits", logits), ("score", score), ("finished", finished), ("parent_out", parent_out),
-                            ("token_out", token_out), ("score_out", score_out)), call)
+        _typed(finished, "finished", torch.int32, (R, W), index)
+    dev = logits.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (logits, score, finished, parent_out, token_out, score_out), lambda: beam_select(
+            logits, score, M, finished=finished, pad_token=pad_token, temperature=temperature, parent_out=parent_out,
+            token_out=token_out, score_out=score_out, workspace=workspace))
+    size = (R, max(M, 0))
+    parent = _out(parent_out, "parent_out", torch.int32, size, dev)
+    token = _out(token_out, "token_out", torch.int32, size, dev)
+    best = _out(score_out, "score_out", torch.float32, size, dev)
+    nbytes = _workspace_bytes("dh_beam_select_workspace", R, W, vocab, dt)
+    ws = _scratch(nbytes, workspace, "beam", dev)
+    _check(lib.dh_beam_select(logits.data_ptr(), logits.stride(0), logits.stride(1), score.data_ptr(), _addr(finished),
+                              R, W, vocab, M, dt, temperature, pad_token, parent.data_ptr(), token.data_ptr(),
+                              best.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(index)), "dh_beam_select")
+    return parent, token, best
 
 
 def _copy_dims(dims, unit):
@@ -742,17 +742,21 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     if idx.dim() != 2:
         raise ValueError("idx must be [R, M]")
     M = idx.shape[1]
-    _typed(idx, "idx", torch.int32, (R, M))
+    index = states.get_device()
+    _typed(idx, "idx", torch.int32, (R, M), index)
     for t, name in ((lengths, "lengths"), (src_base, "src_base"), (dst_base, "dst_base")):
         if t is not None:
-            _typed(t, name, torch.int32, (R,))
-
-    def call(raw, _dev):
-        _check(lib.dh_reorder_states(states.data_ptr(), ss, dst.data_ptr(), ds, idx.data_ptr(), _addr(lengths),
-                                     _addr(src_base), _addr(dst_base), A, R, slots, out_slots, M, H, T, unit, raw),
-               "dh_reorder_states")
-    _run_on(stream, (("states", states), ("out", dst), ("idx", idx), ("lengths", lengths), ("src_base", src_base),
-                     ("dst_base", dst_base)), call)
+            _typed(t, name, torch.int32, (R,), index)
+    if dst.get_device() != index:
+        raise ValueError(f"out must be on {states.device}")
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, states.device, (states, dst, idx, lengths, src_base, dst_base),
+                          lambda: reorder_states(states, idx, out=out, lengths=lengths, length_dim=length_dim,
+                                                 src_base=src_base, dst_base=dst_base, request_dim=request_dim,
+                                                 slot_dim=slot_dim, out_slot_dim=out_slot_dim))
+    _check(lib.dh_reorder_states(states.data_ptr(), ss, dst.data_ptr(), ds, idx.data_ptr(), _addr(lengths),
+                                 _addr(src_base), _addr(dst_base), A, R, slots, out_slots, M, H, T, unit,
+                                 _raw_stream(index)), "dh_reorder_states")
     return dst
 
 
