@@ -684,6 +684,9 @@ DistillArgs distill_args(const void* logits, int64_t row_stride, const int32_t* 
 
 // Loss (and statistics) after validation: the rows' segments, then the rows.
 int run_distill_loss(const Ctx& c, DistillArgs a, int dtype, float2* seg) {
+  if (distill_short(a, c.num_sms, false))
+    return note_error(launch_distill_short(c, a, dtype, true, false), "distillation loss") == cudaSuccess ? DH_OK
+                                                                                                          : DH_ERR_CUDA;
   if (note_error(launch_row_stats(c, a.logits, a.ld, 0, a.N, 1, a.vocab, dtype, a.temperature, nullptr, nullptr, seg),
                  "row statistics") != cudaSuccess)
     return DH_ERR_CUDA;
@@ -737,6 +740,10 @@ int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32
   a.weight = grad_loss;
   a.grad = grad_out;
   a.gld = grad_stride;
+  if (distill_short(a, c.num_sms, false))
+    return note_error(launch_distill_short(c, a, dtype, false, true), "distillation gradient") == cudaSuccess
+               ? DH_OK
+               : DH_ERR_CUDA;
   if (a.grad == a.logits || !lie_alike(a, dtype))
     return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
   if (note_error(launch_distill_dense(c, a, dtype), "distillation gradient") != cudaSuccess) return DH_ERR_CUDA;
@@ -775,6 +782,11 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
   a.status = static_cast<int*>(workspace);
   a.stats_out = stats;
   a.stats = stats;
+  if (distill_short(a, c.num_sms, true)) {
+    a.stats_out = nullptr;
+    return note_error(launch_distill_short(c, a, dtype, true, true), "distillation step") == cudaSuccess ? DH_OK
+                                                                                                         : DH_ERR_CUDA;
+  }
   if (lie_alike(a, dtype)) {
     DistillArgs b = a;
     if (a.grad == a.logits) {

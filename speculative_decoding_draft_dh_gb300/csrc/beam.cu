@@ -26,6 +26,8 @@ constexpr int BP_THREADS = 512;
 constexpr int BP_WARPS = BP_THREADS / 32;
 constexpr int BP_CAP = 2048;      // candidates held at once (at least DH_MAX_BEAM_OUT + one segment)
 constexpr int BP_SEGS = 1024;     // segments held at once
+constexpr int BP_BATCH = 10;      // vectors of a warp in flight
+constexpr int BP_HELD = 5;        // segments of a thread in registers (2560: 16 beams of 152K bf16 logits)
 constexpr int BP_STAGE = 2560;    // segment maxima in shared memory: 16 beams of 152K bf16 logits
 
 // Order-preserving map of a double onto uint64 (-0 is folded onto +0).
@@ -35,6 +37,22 @@ __device__ __forceinline__ unsigned long long dkey(double x) {
 }
 __device__ __forceinline__ double dkey_inv(unsigned long long k) {
   return __longlong_as_double((k >> 63) ? (long long)(k & 0x7FFFFFFFFFFFFFFFull) : (long long)~k);
+}
+
+// log(hi + lo) of a positive sum in two floats, to about 1e-9: the 64-bit logarithm takes 2,600 cycles
+// here, this 300.  With hi = 2^k f, f in [2/3, 4/3), and t = (f - 1)/(f + 1), log f = 2 artanh t
+// = 2 t + 2 t (t^2/3 + t^4/5 + ...): the first term in two floats, the rest, below 0.02 t, in one.
+__device__ __forceinline__ double log_sum(float hi, float lo) {
+  int k = (int)((__float_as_uint(hi) + 0x00555555u) >> 23) - 127;  // rounds to the nearest in [2/3, 4/3)
+  const float scale = __uint_as_float((uint32_t)(127 - k) << 23);
+  const float f = hi * scale, fl = lo * scale;  // exact
+  const float a = f - 1.f;                      // exact; the numerator is a + fl
+  const float b = f + 1.f, bl = (f - (b - 1.f)) + fl;
+  const float t = a / b;
+  const float tl = ((fmaf(-t, b, a) + fl) - t * bl) / b;
+  const float q = t * t;
+  const float r = q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 11.f, 1.f / 9.f), 1.f / 7.f), 1.f / 5.f), 1.f / 3.f);
+  return (double)k * 0.6931471805599453 + ((double)(2.f * t) + (double)(2.f * (tl + t * r)));
 }
 
 struct BeamArgs {
@@ -61,6 +79,7 @@ struct BeamSmem {
   bool done[DH_MAX_BEAMS];     // finished, with a score
   float zthr[DH_MAX_BEAMS];    // logits from here on reach the bound
   float seg_max[BP_STAGE];
+  float tau;
   uint32_t segs[BP_SEGS];
   int count[2][BP_WARPS];
   unsigned long long last_key;
@@ -163,6 +182,8 @@ __device__ __forceinline__ void keep_best(BeamSmem& s, int M) {
 template <typename T>
 __device__ __forceinline__ void push_vec(BeamSmem& s, const BeamArgs& a, const uint4& u, int id, int w, float zthr) {
   constexpr int PER = Elem<T>::PER16;
+  const uint4 one[1] = {u};
+  if (!(vec_max<T>(one) >= zthr)) return;  // most vectors
   float z[PER];
   Elem<T>::unpack(u, z);
 #pragma unroll
@@ -204,15 +225,13 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   for (int w = warp; w < W; w += BP_WARPS) {
     const float sc = __ldg(score + w);
     const bool fin = finished && __ldg(finished + w) != 0;
-    const float2* sg = seg + (size_t)w * n_seg;
     const bool live = fabsf(sc) < INFINITY && !fin;
-    float m = -INFINITY, total = 0.f, rest = 0.f;
-    if (live) {
-      Sum2 sum;
-      row_combine(sg, n_seg, a.inv_t, &m, &sum, staged ? &s.seg_max[w * n_seg] : nullptr);
-      total = sum.hi;
-      rest = sum.lo;
-    }
+    // a beam that is not live has no pairs; what stands in their place is combined all the same, so
+    // that no load waits for another, and not used
+    float m;
+    Sum2 sum;
+    row_combine(seg + (size_t)w * n_seg, n_seg, a.inv_t, &m, &sum, staged ? &s.seg_max[w * n_seg] : nullptr);
+    const float total = sum.hi, rest = sum.lo;
     if (lane == 0) {
       // a row of -inf, and one with a NaN or +inf, has no distribution
       const bool good = live && fabsf(m) < INFINITY && total + rest < INFINITY;
@@ -225,17 +244,26 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   }
   __syncthreads();
   for (int w = tid; w < W; w += BP_THREADS) {
-    const double b = s.sum_hi[w] > 0.f ? (double)s.score[w] - log((double)s.sum_hi[w] + (double)s.sum_lo[w])
-                                       : -(double)INFINITY;
+    const double b =
+        s.sum_hi[w] > 0.f ? (double)s.score[w] - log_sum(s.sum_hi[w], s.sum_lo[w]) : -(double)INFINITY;
     s.base[w] = b;
     s.base32[w] = (float)b;
   }
   __syncthreads();
-  auto seg_max = [&](int i) { return staged ? s.seg_max[i] : __ldg(&seg[i]).x; };
+  auto seg_max = [&](int i) { return staged ? s.seg_max[i] : seg[i].x; };
+  // i / n_seg for i < W n_seg <= 2^19: the quotient is at least 0.5 / n_seg >= 2^-13 away from the next
+  // integer, the error of the product below 2^-16
+  const float inv_seg = 1.f / (float)n_seg;
+  auto beam_of = [&](int i) { return __float2int_rz(((float)i + 0.5f) * inv_seg); };
 
   // 2. the bound.  Few segments: the threads' best elements instead of their best segments
   const bool by_elem = n_all < 4 * M;
   float best = -INFINITY;
+  // a thread's first segments stay in registers: beam and maximum (-inf: not to be looked at)
+  int held_w[BP_HELD] = {};
+  float held_m[BP_HELD];
+#pragma unroll
+  for (int q = 0; q < BP_HELD; ++q) held_m[q] = -INFINITY;
   if (by_elem) {
     for (int i = warp; i < n_all; i += BP_WARPS) {
       const int w = i / n_seg, id0 = (i - w * n_seg) * SEG + lane * PER;
@@ -246,35 +274,78 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
       best = fmaxf(best, score_below(s.base32[w], s.top[w], vec_max<T>(u), a.inv_t));
     }
   } else {
-    for (int i = tid; i < n_all; i += BP_THREADS) {
-      const int w = i / n_seg;
+#pragma unroll
+    for (int q = 0; q < BP_HELD; ++q) {
+      const int i = tid + q * BP_THREADS;
+      if (i >= n_all) break;
+      const int w = beam_of(i);
+      if (s.base32[w] == -INFINITY) continue;
+      held_w[q] = w;
+      held_m[q] = seg_max(i);
+      best = fmaxf(best, score_below(s.base32[w], s.top[w], held_m[q], a.inv_t));
+    }
+    for (int i = tid + BP_HELD * BP_THREADS; i < n_all; i += BP_THREADS) {
+      const int w = beam_of(i);
       if (s.base32[w] != -INFINITY) best = fmaxf(best, score_below(s.base32[w], s.top[w], seg_max(i), a.inv_t));
     }
   }
   if (finished)
     for (int w = tid; w < W; w += BP_THREADS)
       if (s.done[w]) best = fmaxf(best, s.score[w]);
-  const uint32_t mine = fkey(best);
-  uint32_t t = 0;
-  for (int b = 31; b >= 12; --b) {  // the leading bits give a lower bound already
-    const uint32_t u = t | (1u << b);
-    if (__syncthreads_count(mine >= u) >= M) t = u;
+  // The M-th largest: for up to 64 by the ranks of 128 maxima of four threads each (a few more
+  // candidates reach it: 37 where 32 are asked for), else by descent over the leading bits of the
+  // threads' maxima, with a block-wide count each (19 barriers, 2,100 cycles against 500).
+  float tau;
+  if (M <= 64) {
+    best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, 1));
+    best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, 2));
+    float* const four = reinterpret_cast<float*>(s.key);  // [128], not yet in use
+    if ((lane & 3) == 0) four[tid >> 2] = best;
+    __syncthreads();
+    // maximum tid / 4 against a quarter of them per lane
+    const int me = tid >> 2;
+    const float mine = four[me];
+    int rank = 0;
+#pragma unroll
+    for (int q = 0; q < BP_THREADS / 64; ++q) {
+      const int j = q * 16 + (tid & 3) * 4;
+      const float4 o = *reinterpret_cast<const float4*>(four + j);
+      rank += (o.x > mine || (o.x == mine && j < me)) + (o.y > mine || (o.y == mine && j + 1 < me)) +
+              (o.z > mine || (o.z == mine && j + 2 < me)) + (o.w > mine || (o.w == mine && j + 3 < me));
+    }
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 1);
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 2);
+    if ((lane & 3) == 0 && rank == M - 1) s.tau = mine;  // ranks are distinct
+    __syncthreads();
+    tau = s.tau;
+  } else {
+    const uint32_t mine = fkey(best);
+    uint32_t t = 0;
+    for (int b = 31; b >= 13; --b) {
+      const uint32_t u = t | (1u << b);
+      if (__syncthreads_count(mine >= u) >= M) t = u;
+    }
+    tau = t == 0 ? -INFINITY : fkey_inv(t);
   }
-  // a bound at or below -inf, or one that no number has, asks nothing
-  float tau = fkey_inv(t);
-  if (!(tau > -INFINITY && tau < INFINITY) || t == 0) tau = -INFINITY;
+  if (!(tau > -INFINITY && tau < INFINITY)) tau = -INFINITY;  // a bound that no number has asks nothing
   set_thresholds(s, a, tau);
   __syncthreads();
 
   // 3. the segments and elements that reach it
-  for (int i = tid; i < n_all; i += BP_THREADS) {
-    const int w = i / n_seg;
-    if (s.base32[w] == -INFINITY) continue;
-    const float m = seg_max(i);
+  auto reach = [&](int i, int w, float m) {
     if (m >= s.zthr[w] && m > -INFINITY) {
       const int at = atomicAdd(&s.n_segs, 1);
       if (at < BP_SEGS) s.segs[at] = (uint32_t)i;
     }
+  };
+  if (!by_elem) {
+#pragma unroll
+    for (int q = 0; q < BP_HELD; ++q)
+      if (held_m[q] != -INFINITY) reach(tid + q * BP_THREADS, held_w[q], held_m[q]);
+  }
+  for (int i = tid + (by_elem ? 0 : BP_HELD * BP_THREADS); i < n_all; i += BP_THREADS) {
+    const int w = beam_of(i);
+    if (s.base32[w] != -INFINITY) reach(i, w, seg_max(i));
   }
   if (finished)
     for (int w = tid; w < W; w += BP_THREADS)
@@ -288,14 +359,25 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   const bool many = s.n_segs > BP_SEGS;
   __syncthreads();
   if (!many) {
-    for (int i = warp; i < s.n_segs; i += BP_WARPS) {
-      const int sg = (int)s.segs[i], w = sg / n_seg, id0 = (sg - w * n_seg) * SEG + lane * PER;
-      const float zthr = s.zthr[w];
-      uint4 u[ROW_SEG_VECS];
+    // a warp's vectors BP_BATCH at a time, so that up to 40 segments take one trip to memory
+    const int n_rows = s.n_segs * ROW_SEG_VECS;
+    for (int i0 = warp; i0 < n_rows; i0 += BP_WARPS * BP_BATCH) {
+      uint4 u[BP_BATCH];
 #pragma unroll
-      for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec<T, ALIGNED>(rows + w * a.ws, id0 + v * 32 * PER, a.vocab);
+      for (int q = 0; q < BP_BATCH; ++q) {
+        const int i = i0 + q * BP_WARPS;
+        if (i >= n_rows) continue;
+        const int sg = (int)s.segs[i / ROW_SEG_VECS], w = beam_of(sg);
+        u[q] = row_vec<T, ALIGNED>(rows + w * a.ws,
+                                   (sg - w * n_seg) * SEG + (i % ROW_SEG_VECS * 32 + lane) * PER, a.vocab);
+      }
 #pragma unroll
-      for (int v = 0; v < ROW_SEG_VECS; ++v) push_vec<T>(s, a, u[v], id0 + v * 32 * PER, w, zthr);
+      for (int q = 0; q < BP_BATCH; ++q) {
+        const int i = i0 + q * BP_WARPS;
+        if (i >= n_rows) continue;
+        const int sg = (int)s.segs[i / ROW_SEG_VECS], w = beam_of(sg);
+        push_vec<T>(s, a, u[q], (sg - w * n_seg) * SEG + (i % ROW_SEG_VECS * 32 + lane) * PER, w, s.zthr[w]);
+      }
     }
   }
   __syncthreads();
@@ -376,12 +458,17 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   int32_t* parent = a.parent + (size_t)blockIdx.x * M;
   int32_t* token = a.token + (size_t)blockIdx.x * M;
   float* out = a.score_out + (size_t)blockIdx.x * M;
-  for (int i = tid; i < n; i += BP_THREADS) {
-    const unsigned long long k = s.key[i];
-    const uint32_t p = s.pos[i];
+  // a candidate's rank is the number that come before it, counted by eight lanes
+  for (int i0 = 0; i0 < n; i0 += BP_THREADS / 8) {
+    const int i = i0 + (tid >> 3), at = min(i, n - 1);
+    const unsigned long long k = s.key[at];
+    const uint32_t p = s.pos[at];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += s.key[j] > k || (s.key[j] == k && s.pos[j] < p);
-    if (rank < M) {
+    for (int j = tid & 7; j < n; j += 8) rank += s.key[j] > k || (s.key[j] == k && s.pos[j] < p);
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 1);
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 2);
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 4);
+    if (i < n && rank < M && (tid & 7) == 0) {
       const int w = (int)(p / (uint32_t)a.vocab);
       parent[rank] = w;
       token[rank] = s.done[w] ? a.pad_token : (int)(p - (uint32_t)w * (uint32_t)a.vocab);

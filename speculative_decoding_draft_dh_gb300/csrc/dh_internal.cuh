@@ -399,6 +399,8 @@ cudaError_t launch_row_stats(const Ctx& c, const void* logits, long long rs, lon
 // launch_distill_ring: statistics (stats_out) and dense gradient; *done is false, and nothing was
 // launched, where the rows are too long.
 cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done);
+bool distill_short(const DistillArgs& a, int num_sms, bool step);  // rows for launch_distill_short
+cudaError_t launch_distill_short(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad);
 cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype);
 cudaError_t launch_distill_dense(const Ctx& c, const DistillArgs& a, int dtype);
 cudaError_t launch_distill_finish(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad);

@@ -29,6 +29,13 @@ namespace dh {
 namespace {
 
 constexpr int DF_WARPS = 4;
+constexpr int DS_WARPS = 8;
+// Rows for one block and one launch.  Measured in graphs, us, bf16, this against two launches: loss of
+// 16 x 8192 5.7 / 6.8, of 608 x 16384 (16 segments) 10.5 / 10.8, of 2048 x 8192 15.2 / 13.5; gradient
+// of 608 x 16384 16.5 / 17.2, of 2048 x 16384 35.0 / 30.7; step of 16 x 8192 9.0 / 10.8, of 608 x 32768
+// (32 segments) 23.5 / 31.0, of 16 x 32768 12.4 / 11.5, of 2048 x 65536 (64 segments) 123 / 106.
+constexpr int DS_SEG_FEW = 16;
+constexpr int DS_MAX_SEG = 32;
 constexpr int DF_BATCH = 4;
 constexpr int DG_THREADS = 256;
 constexpr int DG_UNROLL = 4;
@@ -255,29 +262,44 @@ __global__ void __launch_bounds__(256) k_distill_gather(DistillArgs a) {
       id >= 0 && id < a.vocab ? Elem<T>::to_f(static_cast<const T*>(a.logits)[row * a.ld + id]) : 0.f;
 }
 
-// LOSS: write the loss (and stats_out).  GRAD: write the entries' gradient.  SEG: the row's statistics
-// come as its segments' pairs.
-template <typename T, bool LOSS, bool GRAD, bool SEG>
-__global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a, int table) {
-  // per warp: the entries' ids, p and logits [K], then the hash table (a power of two of at least 2 K)
-  extern __shared__ int32_t df_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x * DF_WARPS + warp;
-  int32_t* const s_id = df_smem + warp * (3 * a.K + table);
-  float* const s_p = reinterpret_cast<float*>(s_id + a.K);
-  float* const s_z = s_p + a.K;
-  int32_t* const s_t = s_id + 3 * a.K;
+// What one warp knows of a row's entries before it has the row's statistics.
+struct RowEntries {
+  int nk;
+  bool any;      // there is an entry above -inf (or a NaN one)
+  bool twice;    // an id comes more than once
+  float g;       // grad_loss T
+  float total;   // NaN if an entry is
+  float part;    // sum_k p_k (log p_k - (z_k - zref)/T)
+  float zref;    // one of the entries' logits
+};
+
+// Shared memory of a warp: the entries' ids, p and logits [K], then a hash table (a power of two of
+// at least 2 K; only for a gradient).
+struct EntrySmem {
+  int32_t* id;
+  float *p, *z;
+  int32_t* table;
+  int size;
+  __device__ EntrySmem(int32_t* base, int K, int size_) : id(base), size(size_) {
+    p = reinterpret_cast<float*>(base + K);
+    z = p + K;
+    table = base + 3 * K;
+  }
+};
+
+// By one warp: the teacher's softmax and its part of the loss.  Reads nothing but the call's inputs.
+template <typename T, bool LOSS, bool GRAD>
+__device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int row, const EntrySmem& s) {
+  const int lane = threadIdx.x & 31;
+  const T* const z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
+  const long long e0 = (long long)row * a.K;
+  RowEntries r;
   if (GRAD)
-    for (int i = lane; i < table; i += 32) s_t[i] = -1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const bool mine = row < a.N;
-  const int at = mine ? row : a.N - 1;
-  const T* const z = static_cast<const T*>(a.logits) + (long long)at * a.ld;
-  const long long e0 = (long long)at * a.K;
-  const int nk = a.n_valid ? min(max(__ldg(a.n_valid + at), 0), a.K) : a.K;
-  const float g = GRAD ? __ldg(a.weight + at) * a.temperature : 0.f;
+    for (int i = lane; i < s.size; i += 32) s.table[i] = -1;
+  const int nk = r.nk = a.n_valid ? min(max(__ldg(a.n_valid + row), 0), a.K) : a.K;
+  r.g = GRAD ? __ldg(a.weight + row) * a.temperature : 0.f;
   // DF_BATCH entries per lane at a time: their loads, which hang on nothing, are in flight together
-  float top = -INFINITY;
+  float top = -INFINITY, zref = -INFINITY;
   for (int k0 = lane; k0 < a.K; k0 += 32 * DF_BATCH) {
     int id[DF_BATCH];
     float y[DF_BATCH], zk[DF_BATCH];
@@ -292,47 +314,45 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
       const int k = k0 + e * 32;
       if (k >= nk || id[e] < 0 || id[e] >= a.vocab) id[e] = -1;
       zk[e] = 0.f;
-      if (id[e] >= 0) zk[e] = a.gathered ? __ldcg(a.gathered + e0 + k) : Elem<T>::to_f(__ldg(z + id[e]));
+      if (id[e] >= 0)
+        zk[e] = a.gathered ? __ldcg(a.gathered + e0 + k) : Elem<T>::to_f(*(const volatile T*)(z + id[e]));
     }
 #pragma unroll
     for (int e = 0; e < DF_BATCH; ++e) {
       const int k = k0 + e * 32;
       if (k >= nk) continue;
       if (id[e] < 0) y[e] = -INFINITY;
-      s_id[k] = id[e];
-      s_p[k] = y[e];
-      s_z[k] = zk[e];
+      else zref = max_nan(zref, zk[e]);
+      s.id[k] = id[e];
+      s.p[k] = y[e];
+      s.z[k] = zk[e];
       top = max_nan(top, y[e]);
     }
   }
   top = warp_max(top);
-  const bool any = top != -INFINITY;
+  zref = warp_max(zref);
+  r.zref = fabsf(zref) < INFINITY ? zref : 0.f;
+  r.any = top != -INFINITY;
   float total = 0.f;
-  if (any)
+  if (r.any)
     for (int k = lane; k < nk; k += 32) {
-      const float e = expf((s_p[k] - top) * a.inv_t);
+      const float e = expf((s.p[k] - top) * a.inv_t);
       total += e;
     }
-  total = warp_sum(total);
+  total = r.total = warp_sum(total);
   const float inv = 1.f / total, log_total = logf(total);
-  // p, the loss relative to one of the entries' own logits, and whether an id comes twice
-  float zref = -INFINITY;
-  for (int k = lane; k < nk; k += 32)
-    if (s_id[k] >= 0) zref = max_nan(zref, s_z[k]);
-  zref = warp_max(zref);
-  if (!(fabsf(zref) < INFINITY)) zref = 0.f;
-  const bool write = GRAD && any && g != 0.f;
+  const bool write = GRAD && r.any && r.g != 0.f;
   float part = 0.f;
   bool twice = false;
-  for (int k = lane; any && k < nk; k += 32) {
-    const int id = s_id[k];
-    const float ak = (s_p[k] - top) * a.inv_t, p = expf(ak) * inv;
-    s_p[k] = p;
+  for (int k = lane; r.any && k < nk; k += 32) {
+    const int id = s.id[k];
+    const float ak = (s.p[k] - top) * a.inv_t, p = expf(ak) * inv;
+    s.p[k] = p;
     if (id < 0) continue;
-    if (LOSS && p != 0.f) part += p * ((ak - log_total) - (s_z[k] - zref) * a.inv_t);  // 0 log 0 = 0
+    if (LOSS && p != 0.f) part += p * ((ak - log_total) - (s.z[k] - r.zref) * a.inv_t);  // 0 log 0 = 0
     if (write) {
       for (uint32_t h = (uint32_t)id * 0x9E3779B1u;; ++h) {  // at most half full: ends
-        const int old = atomicCAS(&s_t[h & (uint32_t)(table - 1)], -1, id);
+        const int old = atomicCAS(&s.table[h & (uint32_t)(s.size - 1)], -1, id);
         if (old == -1) break;
         if (old == id) {
           twice = true;
@@ -341,54 +361,151 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
       }
     }
   }
-  if (LOSS) part = warp_sum(part);
-  twice = __any_sync(0xFFFFFFFFu, twice);
+  r.part = LOSS ? warp_sum(part) : 0.f;
+  r.twice = __any_sync(0xFFFFFFFFu, twice);
+  return r;
+}
 
+// The row's loss: sum_k p_k (log p_k - log q_k) with log q_k = (z_k - m)/T - log sum; for a row of
+// -inf infinite.
+__device__ __forceinline__ float entries_loss(const DistillArgs& a, const RowEntries& r, float m, float sum) {
+  const float l = a.temperature * a.temperature * (r.part + ((m - r.zref) * a.inv_t + logf(sum)));
+  return !r.any ? 0.f : (r.total != r.total ? r.total : (m == -INFINITY ? INFINITY : l));
+}
+
+// By the same warp: the entries' values over the dense term.
+template <typename T>
+__device__ __forceinline__ void entries_write(const DistillArgs& a, T* out, const RowEntries& r, const EntrySmem& s,
+                                              float m, float sum) {
+  const bool nothing = m == -INFINITY;
+  const ExpRef ref(nothing ? 0.f : m, a.c);
+  const float aq = nothing ? 0.f : ref.by_max(r.g / sum, a.c);
+  for (int k = threadIdx.x & 31; k < r.nk; k += 32) {
+    const int id = s.id[k];
+    if (id < 0) continue;
+    float p = s.p[k];
+    bool first = true;
+    if (r.twice)
+      for (int j = 0; j < r.nk; ++j) {
+        if (s.id[j] != id || j == k) continue;
+        if (j < k) {
+          first = false;
+          break;
+        }
+        p += s.p[j];
+      }
+    if (first) out[id] = Elem<T>::from_f(aq * one_exp(s.z[k], ref, a.c) - r.g * p);
+  }
+}
+
+// LOSS: write the loss (and stats_out).  GRAD: write the entries' gradient.  SEG: the row's statistics
+// come as its segments' pairs.
+template <typename T, bool LOSS, bool GRAD, bool SEG>
+__global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a, int table) {
+  extern __shared__ int32_t df_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * DF_WARPS + warp;
+  const EntrySmem s(df_smem + warp * (3 * a.K + table), a.K, table);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const RowEntries r = entries_prepare<T, LOSS, GRAD>(a, row < a.N ? row : a.N - 1, s);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!mine) return;
+  if (row >= a.N) return;
   float m, sum;
   if (SEG) {
-    Sum2 s;
-    row_combine(a.seg + (long long)row * a.n_seg, a.n_seg, a.inv_t, &m, &s);
-    sum = s.hi + s.lo;
+    Sum2 t;
+    row_combine(a.seg + (long long)row * a.n_seg, a.n_seg, a.inv_t, &m, &t);
+    sum = t.hi + t.lo;
     if (a.stats_out && lane == 0) a.stats_out[row] = make_float2(m, sum);
   } else {
     const float2 st = __ldcg(a.stats + row);
     m = st.x;
     sum = st.y;
   }
-  T* const out = GRAD ? static_cast<T*>(a.grad) + (long long)row * a.gld : nullptr;
-  if (LOSS && lane == 0) {
-    // sum_k p_k (log p_k - log q_k) with log q_k = (z_k - m)/T - log sum; a row of -inf: infinite
-    const float l = a.temperature * a.temperature * (part + ((m - zref) * a.inv_t + logf(sum)));
-    a.loss_out[row] = !any ? 0.f : (total != total ? total : (m == -INFINITY ? INFINITY : l));
+  if (LOSS && lane == 0) a.loss_out[row] = entries_loss(a, r, m, sum);
+  if (!GRAD || r.g == 0.f) return;
+  T* const out = static_cast<T*>(a.grad) + (long long)row * a.gld;
+  if (r.any && r.total == r.total) {
+    entries_write<T>(a, out, r, s, m, sum);
+  } else if (r.nk > 0) {
+    // the dense pass knows a row without entries by its count alone, and no NaN among the entries
+    for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(r.any ? r.total : 0.f);
   }
-  // the dense pass knows a row without entries by its count alone, and no NaN among the entries
-  if (GRAD && nk > 0 && g != 0.f && (!any || total != total)) {
-    for (int i = lane; i < a.vocab; i += 32) out[i] = Elem<T>::from_f(any ? total : 0.f);
-    return;
+}
+
+// ---------------------------------------------------------------- short rows
+
+// A whole row by one block: DS_WARPS warps take its segments, one more its entries; then all of them
+// the dense term.  One launch instead of two.  STATS: the statistics are given.
+template <typename T, bool LOSS, bool GRAD, bool STATS>
+__global__ void __launch_bounds__(DS_WARPS * 32 + 32) k_distill_short(DistillArgs a, int table) {
+  constexpr int PER = Elem<T>::PER16;
+  constexpr int NT = DS_WARPS * 32 + 32;
+  extern __shared__ int32_t df_smem[];
+  __shared__ float2 s_seg[DS_MAX_SEG];
+  __shared__ float s_any;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
+  const EntrySmem s(df_smem, a.K, table);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const T* const z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
+  RowEntries r = {};
+  if (warp == DS_WARPS) {
+    r = entries_prepare<T, LOSS, GRAD>(a, row, s);
+    if (lane == 0) s_any = !r.any ? 0.f : (r.total == r.total ? 1.f : r.total);
+  } else if (!STATS) {
+    for (int i = warp; i < a.n_seg; i += DS_WARPS) {
+      uint4 u[ROW_SEG_VECS];
+      const int id0 = i * row_seg<T>() + lane * PER;
+#pragma unroll
+      for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec_rw<T>(z, id0 + v * 32 * PER, a.vocab);
+      const float2 p = segment_stats<T>(u, a.c);
+      if (lane == 0) s_seg[i] = p;
+    }
   }
-  if (!write) return;
-  const bool nothing = m == -INFINITY;
+  __syncthreads();
+  float m, sum;
+  if (STATS) {
+    const float2 st = __ldg(a.stats + row);
+    m = st.x;
+    sum = st.y;
+  } else {
+    Sum2 t;
+    row_combine(s_seg, a.n_seg, a.inv_t, &m, &t);
+    sum = t.hi + t.lo;
+  }
+  if (warp == DS_WARPS && lane == 0) {
+    if (LOSS) a.loss_out[row] = entries_loss(a, r, m, sum);
+    if (!STATS && a.stats_out) a.stats_out[row] = make_float2(m, sum);
+  }
+  if (!GRAD) return;
+
+  T* const out = static_cast<T*>(a.grad) + (long long)row * a.gld;
+  const float g = __ldg(a.weight + row) * a.temperature, any = s_any;
+  const bool zero = any == 0.f || g == 0.f, nothing = m == -INFINITY;
   const ExpRef ref(nothing ? 0.f : m, a.c);
-  const float aq = nothing ? 0.f : ref.by_max(g / sum, a.c);
-  for (int k = lane; k < nk; k += 32) {
-    const int id = s_id[k];
-    if (id < 0) continue;
-    float p = s_p[k];
-    bool first = true;
-    if (twice)
-      for (int j = 0; j < nk; ++j) {
-        if (s_id[j] != id || j == k) continue;
-        if (j < k) {
-          first = false;
-          break;
-        }
-        p += s_p[j];
-      }
-    if (!first) continue;
-    out[id] = Elem<T>::from_f(aq * one_exp(s_z[k], ref, a.c) - g * p);
+  // a NaN among the entries makes the whole row NaN; a row of -inf has q = 0
+  const float aq = any != any ? any : (nothing ? 0.f : ref.by_max(g / sum, a.c));
+  // vectors on the output's 16-byte grid and the elements beside it
+  const int pre = min(a.vocab, (int)(((16u - (unsigned)(reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / sizeof(T)));
+  const int nvec = (a.vocab - pre) / PER, behind = pre + nvec * PER;
+  const T* zv = z + pre;
+  const bool same = (reinterpret_cast<uintptr_t>(zv) & 15u) == 0;
+  const int lone = tid < pre ? tid : behind + tid - pre;
+  if (lone < a.vocab)
+    out[lone] = Elem<T>::from_f(zero ? 0.f : aq * one_exp(Elem<T>::to_f(*(const volatile T*)(z + lone)), ref, a.c));
+  for (int j = tid; j < nvec; j += NT * 2) {
+    uint4 u[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (j + q * NT < nvec && !zero)
+        u[q] = same ? ld16_rw(zv + (j + q * NT) * PER) : ld16_elems<T>(zv + (j + q * NT) * PER);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (j + q * NT < nvec)
+        st16(out + pre + (j + q * NT) * PER, zero ? make_uint4(0, 0, 0, 0) : grad_vec<T>(u[q], ref, a.c, aq));
   }
+  __syncthreads();  // the entries' values come after the dense ones
+  if (warp == DS_WARPS && !zero && any == any) entries_write<T>(a, out, r, s, m, sum);
 }
 
 cudaLaunchConfig_t pdl_config(const Ctx& c, unsigned grid, unsigned block, cudaLaunchAttribute* at) {
@@ -460,6 +577,22 @@ cudaError_t run_finish(const Ctx& c, const DistillArgs& a, bool loss, bool grad)
 }
 
 template <typename T>
+cudaError_t run_short(const Ctx& c, const DistillArgs& a, bool loss, bool grad) {
+  int table = 0;
+  if (grad)
+    for (table = 32; table < 2 * a.K;) table *= 2;
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)a.N, DS_WARPS * 32 + 32, &at);
+  cfg.dynamicSmemBytes = (size_t)(3 * a.K + table) * 4;  // 20 KB at most
+  prof_before("distill_short", c.stream);
+  const cudaError_t e = loss && grad ? cudaLaunchKernelEx(&cfg, k_distill_short<T, true, true, false>, a, table)
+                        : grad       ? cudaLaunchKernelEx(&cfg, k_distill_short<T, false, true, true>, a, table)
+                                     : cudaLaunchKernelEx(&cfg, k_distill_short<T, true, false, false>, a, table);
+  prof_after(c.stream);
+  return e;
+}
+
+template <typename T>
 cudaError_t run_gather(const Ctx& c, const DistillArgs& a) {
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)(((long long)a.N * a.K + 255) / 256), 256, &at);
@@ -471,6 +604,13 @@ cudaError_t run_gather(const Ctx& c, const DistillArgs& a) {
 
 }  // namespace
 
+cudaError_t launch_distill_short(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad) {
+  return dtype == DH_BF16 ? run_short<__nv_bfloat16>(c, a, loss, grad) : run_short<float>(c, a, loss, grad);
+}
+bool distill_short(const DistillArgs& a, int num_sms, bool step) {
+  if (step) return a.n_seg <= DS_SEG_FEW || (a.n_seg <= DS_MAX_SEG && a.N >= num_sms);
+  return a.n_seg <= DS_SEG_FEW && a.N <= 8 * num_sms;
+}
 cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype) {
   return dtype == DH_BF16 ? run_gather<__nv_bfloat16>(c, a) : run_gather<float>(c, a);
 }

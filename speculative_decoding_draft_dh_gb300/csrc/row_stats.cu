@@ -39,17 +39,8 @@ __global__ void __launch_bounds__(RS_THREADS) k_row_stats(const T* __restrict__ 
     const int id0 = sgi * row_seg<T>() + lane * PER;
 #pragma unroll
     for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec<T, ALIGNED>(r, id0 + v * 32 * PER, vocab);
-    const float m = warp_max(vec_max<T>(u));
-    float s = 0.f;
-    if (m != -INFINITY) {
-      const ExpRef ref(m, c);
-      float p[ROW_SEG_VECS];
-#pragma unroll
-      for (int v = 0; v < ROW_SEG_VECS; ++v) p[v] = vec_expsum<T>(u[v], ref, c);
-      s = (p[0] + p[1]) + (p[2] + p[3]);
-      s = ref.by_max(warp_sum(s), c);
-    }
-    if (lane == 0) seg[g] = make_float2(m, s);
+    const float2 p = segment_stats<T>(u, c);
+    if (lane == 0) seg[g] = p;
   }
 }
 

@@ -210,10 +210,50 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// row_vec for memory that the kernel may write later (no read-only loads); any alignment.
+template <typename T>
+__device__ __forceinline__ uint4 row_vec_rw(const T* row, int id, int vocab) {
+  constexpr int PER = Elem<T>::PER16;
+  uint4 r;
+  if (id + PER <= vocab && (reinterpret_cast<uintptr_t>(row + id) & 15u) == 0) {
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + id) : "memory");
+    return r;
+  }
+  uint32_t w[4] = {NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD};
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    if (id + e < vocab) {
+      if constexpr (sizeof(T) == 4) {
+        w[e] = __float_as_uint(*(const volatile float*)(row + id + e));
+      } else {
+        const uint32_t b = *(const volatile unsigned short*)(row + id + e);
+        w[e / 2] = (e & 1) ? ((w[e / 2] & 0xFFFFu) | (b << 16)) : ((w[e / 2] & 0xFFFF0000u) | b);
+      }
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Segments of a row: ROW_SEG_VECS vectors per lane of one warp (1024 bf16 or 512 fp32 ids), lane l
 // holding vectors l, l + 32, ...  k_row_stats leaves each segment's (max, sum of exp((z - max)/T)).
 constexpr int ROW_SEG_VECS = 4;
 template <typename T> constexpr int row_seg() { return 32 * Elem<T>::PER16 * ROW_SEG_VECS; }
+
+// A segment's pair from its vectors, by one warp (every lane gets it).
+template <typename T>
+__device__ __forceinline__ float2 segment_stats(const uint4 (&u)[ROW_SEG_VECS], float c) {
+  const float m = warp_max(vec_max<T>(u));
+  float s = 0.f;
+  if (m != -INFINITY) {
+    const ExpRef ref(m, c);
+    float p[ROW_SEG_VECS];
+#pragma unroll
+    for (int v = 0; v < ROW_SEG_VECS; ++v) p[v] = vec_expsum<T>(u[v], ref, c);
+    s = ref.by_max(warp_sum((p[0] + p[1]) + (p[2] + p[3])), c);
+  }
+  return make_float2(m, s);
+}
 
 // A sum of positive terms held as a rounded value and the part that rounding left out (the
 // two-term sum of Knuth): combining the segments' sums in any number adds no error that counts.
@@ -230,7 +270,7 @@ struct Sum2 {
 // is relative to exp((z - max)/T); a row of -inf gives (-inf, 0).  A NaN logit gives
 // (NaN, NaN), a +inf one (+inf, NaN).  inv_t = 1 / T.
 // maxima (may be null): takes the segments' maxima.
-__device__ __forceinline__ void row_combine(const float2* __restrict__ seg, int n_seg, float inv_t, float* m_out,
+__device__ __forceinline__ void row_combine(const float2* seg, int n_seg, float inv_t, float* m_out,
                                             Sum2* sum_out, float* maxima = nullptr) {
   constexpr int HELD = 8;  // pairs per lane that stay in registers, their loads in flight together
   const int lane = threadIdx.x & 31;
@@ -238,14 +278,14 @@ __device__ __forceinline__ void row_combine(const float2* __restrict__ seg, int 
   float m = -INFINITY;
 #pragma unroll
   for (int e = 0; e < HELD; ++e)
-    q[e] = lane + e * 32 < n_seg ? __ldg(&seg[lane + e * 32]) : make_float2(-INFINITY, 0.f);
+    q[e] = lane + e * 32 < n_seg ? seg[lane + e * 32] : make_float2(-INFINITY, 0.f);
 #pragma unroll
   for (int e = 0; e < HELD; ++e) {
     m = max_nan(m, q[e].x);
     if (maxima && lane + e * 32 < n_seg) maxima[lane + e * 32] = q[e].x;
   }
   for (int i = lane + HELD * 32; i < n_seg; i += 32) {
-    const float x = __ldg(&seg[i]).x;
+    const float x = seg[i].x;
     m = max_nan(m, x);
     if (maxima) maxima[i] = x;
   }
@@ -257,7 +297,7 @@ __device__ __forceinline__ void row_combine(const float2* __restrict__ seg, int 
   };
 #pragma unroll
   for (int e = 0; e < HELD; ++e) add(q[e]);
-  for (int i = lane + HELD * 32; i < n_seg; i += 32) add(__ldg(&seg[i]));
+  for (int i = lane + HELD * 32; i < n_seg; i += 32) add(seg[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float h = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o), l = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
