@@ -12,8 +12,8 @@
 //   consumers (16 warps)    pass A: maximum and sum of exp of the chunks as they arrive, each thread
 //                           with a running maximum; every warp puts its pair into all CTAs of the
 //                           cluster (a marked 64-bit word, no barrier) and combines all pairs in one
-//                           order.  Pass B: the dense term g T q from the slots, which
-//                           are handed back one by one.
+//                           order.  Pass B: the dense term g T q from the slots, which are handed
+//                           back one by one.
 #include "rows.cuh"
 #include "sm100.cuh"
 
@@ -127,13 +127,14 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
     if (lane == 0) {
       int slot = 0;
       uint32_t phase = 1;  // the first round finds the slots free
-      for (long long row = cl; row < d.N; row += ncl) {
+      for (long long row = cl; row < d.N && !failed; row += ncl) {
         const T* z = logits + row * d.ld;
         const Slice s = slice_of(z, d.vocab, part, lg);
         const uint4* src = reinterpret_cast<const uint4*>(z + s.pre) + s.lo;
         for (int v = 0; v < s.hi - s.lo; v += DR_CHUNK) {
           const uint32_t bytes = (uint32_t)min(DR_CHUNK, s.hi - s.lo - v) * 16u;
           wait(&empty[slot], phase);
+          if (failed) break;
           sm100::mbar_arrive_expect_tx(&full[slot], bytes);
           sm100::bulk_load(ring + slot * DR_CHUNK, src + v, bytes, &full[slot]);
           if (++slot == a.slots) {
@@ -299,9 +300,7 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
   if (e != cudaSuccess) return e;
   static int dyn_max[64] = {};
   const int dv = c.device < 64 ? c.device : 0;
-  if (dyn_max[dv] == 0 || c.device >= 64) {
-    dyn_max[dv] = max_dynamic_smem(kernel, c.device);
-  }
+  if (dyn_max[dv] == 0 || c.device >= 64) dyn_max[dv] = max_dynamic_smem(kernel, c.device);
 
   RingArgs a = {};
   a.d = d;

@@ -14,26 +14,28 @@ namespace {
 
 constexpr int RS_THREADS = 256;
 
-template <typename T, bool ALIGNED>
+// Index: unsigned where the items' numbers fit, else long long (a 64-bit division per item costs as much
+// as a third of its logits).
+template <typename T, bool ALIGNED, typename Index>
 __global__ void __launch_bounds__(RS_THREADS) k_row_stats(const T* __restrict__ logits, long long rs,
-                                                          long long ws, int W, int vocab, float c, int n_seg, long long n_items,
+                                                          long long ws, int W, int vocab, float c, int n_seg, Index n_items,
                                                           const float* __restrict__ score,
                                                           const int32_t* __restrict__ finished,
                                                           float2* __restrict__ seg) {
   constexpr int PER = Elem<T>::PER16;
   const int lane = threadIdx.x & 31;
-  const long long nw = (long long)gridDim.x * (RS_THREADS / 32);
+  const Index nw = (Index)gridDim.x * (RS_THREADS / 32);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // only now: the kernel after this one reads the call's inputs as soon as it may start
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (long long g = (long long)blockIdx.x * (RS_THREADS / 32) + (threadIdx.x >> 5); g < n_items; g += nw) {
-    const int row = (int)(g / n_seg), sgi = (int)(g - (long long)row * n_seg);
+  for (Index g = (Index)blockIdx.x * (RS_THREADS / 32) + (threadIdx.x >> 5); g < n_items; g += nw) {
+    const int row = (int)(g / (Index)n_seg), sgi = (int)(g - (Index)row * (Index)n_seg);
     if (score) {
       // a beam without candidates of its own: its logits are not read
       const float sc = __ldg(score + row);
       if (!(fabsf(sc) < INFINITY) || (finished && __ldg(finished + row) != 0)) continue;
     }
-    const int rq = row / W;
+    const int rq = W == 1 ? row : row / W;
     const T* r = logits + rq * rs + (row - rq * W) * ws;
     uint4 u[ROW_SEG_VECS];
     const int id0 = sgi * row_seg<T>() + lane * PER;
@@ -65,9 +67,15 @@ cudaError_t run(const Ctx& c, const void* logits, long long rs, long long ws, in
   const bool aligned = rows_aligned(logits, rs, ws, R, W, (int)sizeof(T));
   prof_before("row_stats", c.stream);
   const T* z = static_cast<const T*>(logits);
+  auto go = [&](auto* kernel, auto items) {
+    return cudaLaunchKernelEx(&cfg, kernel, z, rs, ws, W, vocab, cf, n_seg, items, score, finished, seg);
+  };
+  // nw more than the last item's number still has to fit
+  const bool narrow = n_items < 0x7F000000LL;
   const cudaError_t e =
-      aligned ? cudaLaunchKernelEx(&cfg, k_row_stats<T, true>, z, rs, ws, W, vocab, cf, n_seg, n_items, score, finished, seg)
-              : cudaLaunchKernelEx(&cfg, k_row_stats<T, false>, z, rs, ws, W, vocab, cf, n_seg, n_items, score, finished, seg);
+      narrow ? (aligned ? go(k_row_stats<T, true, unsigned>, (unsigned)n_items)
+                        : go(k_row_stats<T, false, unsigned>, (unsigned)n_items))
+             : (aligned ? go(k_row_stats<T, true, long long>, n_items) : go(k_row_stats<T, false, long long>, n_items));
   prof_after(c.stream);
   return e;
 }
