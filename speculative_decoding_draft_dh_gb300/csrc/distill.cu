@@ -36,7 +36,7 @@ constexpr int DS_WARPS = 8;
 // (32 segments) 23.5 / 31.0, of 16 x 32768 12.4 / 11.5, of 2048 x 65536 (64 segments) 123 / 106.
 constexpr int DS_SEG_FEW = 16;
 constexpr int DS_MAX_SEG = 32;
-constexpr int DF_BATCH = 4;
+constexpr int DF_BATCH = 8;
 constexpr int DG_THREADS = 256;
 constexpr int DG_UNROLL = 4;
 
