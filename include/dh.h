@@ -337,7 +337,7 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
  *   stats[n]  = (m, s): m = max_v z[v] and s = sum_v exp((z[v] - m)/T)
  * Sums, exponents and loss in fp32; the gradient is rounded once to `dtype`.
  * - A row without entries (or with none above -inf) has loss 0 and gradient 0.  A row with
- *   grad_loss 0 has gradient 0.  The gradient reads neither kind's logits.
+ *   grad_loss 0 has gradient 0.  Neither kind's gradient depends on its logits, NaN or not.
  * - A student logit of -inf has q = 0; where the teacher's p is positive there the loss is +inf and
  *   the gradient grad_loss T (-p).  A row of -inf: stats (-inf, 0), q = 0 everywhere.
  * - A NaN or +inf student logit, or a NaN or +inf teacher entry, makes that row's loss and gradient
@@ -351,10 +351,14 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
  * int32, teacher fp32 [N x K]; n_valid int32 [N]; grad_loss fp32 [N]; loss_out fp32 [N]; stats fp32
  * [N x 2], 8-byte aligned; grad_out `dtype`, rows grad_stride >= vocab elements apart: all device.
  * grad_out may be the logits themselves (same address and stride); otherwise the two must not
- * overlap.  Elements between the rows are left as they were.  Rows that start on 16 bytes (address
- * and strides) are the fastest.  K <= DH_MAX_K, vocab <= DH_MAX_VOCAB, temperature > 0 and finite.
- * Workspaces: 256-byte aligned, not zeroed, not shared by calls that overlap in time.  N = 0 is a
- * no-op.  Results repeat bit for bit.
+ * overlap.  Elements between the rows are left as they were.  The fastest are rows that start on 16
+ * bytes (address and strides), with gradient rows that lie like the logits'.  K <= DH_MAX_K, vocab <=
+ * DH_MAX_VOCAB, temperature > 0 with temperature^2 neither overflowing nor underflowing fp32.
+ * Workspaces: 256-byte aligned, need not be zeroed, not shared by calls that overlap in time.  N = 0
+ * is a no-op.  Results repeat bit for bit from call to call; the three calls sum in different orders,
+ * so they agree with one another to rounding.
+ * dh_distill_topk_step waits on on-chip barriers; one that gives up leaves NaN losses and raises the
+ * workspace's status bit (dh_workspace_status; the word has to be zeroed before the first use).
  * ------------------------------------------------------------------------------------------- */
 size_t dh_distill_topk_workspace(int N, int vocab, int dtype);
 int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,

@@ -636,6 +636,8 @@ namespace {
 
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
 bool good_temperature(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(1.f / t); }
+// the losses are scaled by its square
+bool good_square(float t) { return good_temperature(t) && std::isnormal(t * t); }
 
 // Bytes of the segment statistics of `rows` rows.
 size_t seg_bytes(long long rows, int vocab, int dtype) {
@@ -656,7 +658,7 @@ bool rows_clash(const void* p, long long ps, const void* q, long long qs, int n,
 int check_distill(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher, int N, int vocab,
                   int K, int dtype, float temperature) {
   if (N < 0 || vocab <= 0 || K < 1 || K > DH_MAX_K || row_stride < 0) return DH_ERR_INVALID_ARG;
-  if (!good_temperature(temperature)) return DH_ERR_INVALID_ARG;
+  if (!good_square(temperature)) return DH_ERR_INVALID_ARG;
   if (!valid_dtype(dtype) || vocab > DH_MAX_VOCAB) return DH_ERR_UNSUPPORTED;
   if (N == 0) return DH_OK;
   if (!logits || !idx || !teacher) return DH_ERR_INVALID_ARG;

@@ -39,6 +39,8 @@ constexpr int DS_MAX_SEG = 32;
 constexpr int DF_BATCH = 8;
 constexpr int DG_THREADS = 256;
 constexpr int DG_UNROLL = 4;
+constexpr int DD_THREADS = 512;
+constexpr int DD_UNROLL = 8;
 
 template <int NT>
 __device__ __forceinline__ float block_max(float x, float* red) {
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_grad(DistillArgs a) {
 // ---------------------------------------------------------------- dense term
 
 template <typename T>
-__global__ void __launch_bounds__(DG_THREADS) k_distill_dense(DistillArgs a) {
+__global__ void __launch_bounds__(DD_THREADS) k_distill_dense(DistillArgs a) {
   constexpr int PER = Elem<T>::PER16;
   const int row = blockIdx.x / a.splits, part = blockIdx.x - row * a.splits;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -232,18 +234,18 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_dense(DistillArgs a) {
     if (i < a.vocab) out[i] = Elem<T>::from_f(zero ? 0.f : aq * one_exp(Elem<T>::to_f(z[i]), ref, a.c));
   }
   if (zero) {
-    for (int j = vlo + tid; j < vhi; j += DG_THREADS) st16(ov + (long long)j * PER, make_uint4(0, 0, 0, 0));
+    for (int j = vlo + tid; j < vhi; j += DD_THREADS) st16(ov + (long long)j * PER, make_uint4(0, 0, 0, 0));
     return;
   }
-  for (int j = vlo + tid; j < vhi; j += DG_THREADS * DG_UNROLL) {
-    uint4 u[DG_UNROLL];
+  for (int j = vlo + tid; j < vhi; j += DD_THREADS * DD_UNROLL) {
+    uint4 u[DD_UNROLL];
 #pragma unroll
-    for (int q = 0; q < DG_UNROLL; ++q)
-      if (j + q * DG_THREADS < vhi) u[q] = ld_nc_v4(zv + (long long)(j + q * DG_THREADS) * PER);
+    for (int q = 0; q < DD_UNROLL; ++q)
+      if (j + q * DD_THREADS < vhi) u[q] = ld_nc_v4(zv + (long long)(j + q * DD_THREADS) * PER);
 #pragma unroll
-    for (int q = 0; q < DG_UNROLL; ++q)
-      if (j + q * DG_THREADS < vhi)
-        st16(ov + (long long)(j + q * DG_THREADS) * PER, grad_vec<T>(u[q], ref, a.c, aq));
+    for (int q = 0; q < DD_UNROLL; ++q)
+      if (j + q * DD_THREADS < vhi)
+        st16(ov + (long long)(j + q * DD_THREADS) * PER, grad_vec<T>(u[q], ref, a.c, aq));
   }
 }
 
@@ -542,7 +544,7 @@ cudaError_t run_dense(const Ctx& c, DistillArgs a) {
   splits = splits < vecs / 1024 ? splits : vecs / 1024;
   a.splits = (int)(splits > 1 ? splits : 1);
   cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)((long long)a.N * a.splits), DG_THREADS, &at);
+  const cudaLaunchConfig_t cfg = pdl_config(c, (unsigned)((long long)a.N * a.splits), DD_THREADS, &at);
   prof_before("distill_dense", c.stream);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_distill_dense<T>, a);
   prof_after(c.stream);

@@ -9,7 +9,7 @@
 //   producer (one thread)   bulk-copies the slices, chunk by chunk and row after row, into a ring of
 //                           slots; it runs ahead of the row at work by what the ring holds beyond a
 //                           slice, so memory stays busy through the reductions.
-//   consumers (16 warps)    pass A: maximum and sum of exp of the chunks as they arrive, each thread
+//   consumers (20 warps)    pass A: maximum and sum of exp of the chunks as they arrive, each thread
 //                           with a running maximum; every warp puts its pair into all CTAs of the
 //                           cluster (a marked 64-bit word, no barrier) and combines all pairs in one
 //                           order.  Pass B: the dense term g T q from the slots, which are handed
@@ -20,7 +20,7 @@
 namespace dh {
 namespace {
 
-constexpr int DR_WARPS = 16;
+constexpr int DR_WARPS = 20;
 constexpr int DR_NT = DR_WARPS * 32;            // consumers
 constexpr int DR_THREADS = DR_NT + 32;          // and the producer's warp
 constexpr int DR_MAX_C = 8;

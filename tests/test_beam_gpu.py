@@ -193,6 +193,21 @@ def test_far_scores_and_temperatures():
     assert torch.isfinite(sc[:, 0]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,W,V,M", [(1, 128, 60001, 200), (1, 2, 2 ** 21, 16), (40, 3, 1500, 6), (2, 17, 151936, 20)])
+def test_many_segments(R, W, V, M, dtype):
+    """More segments than are staged, held in registers, or looked at in one round."""
+    check(*make(R, W, V, dtype, seed=V), M)
+
+
+def test_offsets_beyond_32_bits():
+    z, score = make(2, 2, 3000, "bf16", seed=27)
+    far = torch.empty(4 * 1_200_000_000, dtype=torch.bfloat16, device=DEV).view(2, 2, 1_200_000_000)[:, :, :3000]
+    far.copy_(z)
+    for a, b in zip(dh.beam_select(z, score, 6), dh.beam_select(far, score, 6)):
+        assert torch.equal(a, b)
+
+
 def test_m_of_a_single_row_is_its_log_probabilities():
     z, _ = make(3, 1, 20011, "bf16", seed=21)
     par, tok, sc = dh.beam_select(z, torch.zeros(3, 1, device=DEV), 64)

@@ -239,6 +239,56 @@ def test_nan_and_inf_stay_in_their_rows():
         assert torch.isfinite(fwd[n]) and torch.isfinite(back[n]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,V,K", [(2, 1024, 1024), (3, 40000, 1024), (200, 20001, 257), (2, 2 ** 21, 40)])
+def test_the_largest_teachers_and_vocabularies(N, V, K, dtype):
+    z, idx, y, gl = make(N, V, K, dtype, seed=K)
+    check_all(z, idx, y, gl)
+    idx[:, 1::3] = idx[:, ::3][:, :idx[:, 1::3].shape[1]]  # repeated ids in a long list
+    check_all(z, idx, y, gl)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,V", [(152, 12000), (160, 30000), (310, 33000), (77, 151936)])
+def test_more_rows_than_clusters_run_at_once(N, V, dtype):
+    """The forms that walk several rows per block: ragged teachers, weights of 0, packed odd rows."""
+    z, idx, y, gl = make(N, V + 1, 6, dtype, seed=N)
+    gl[::7] = 0.0
+    nv = (torch.arange(N, device=DEV) % 7).int()
+    check_all(z, idx, y, gl, n_valid=nv)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2.4 GB apart."""
+    N, V, ld = 3, 5000, 1_200_000_000
+    small, idx, y, gl = make(N, V, 8, "bf16", seed=47)
+    z = torch.empty(N * ld, dtype=torch.bfloat16, device=DEV).view(N, ld)[:, :V]
+    z.copy_(small)
+    want = dh.distill_topk_step(small, idx, y, gl)
+    got = dh.distill_topk_step(z, idx, y, gl)
+    back = dh.distill_topk_backward(z, idx, y, dh.distill_topk(z, idx, y)[1], gl)
+    assert got[1].stride(0) == ld and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert near(back, want[1], small, idx, y, gl)
+    wide = make(N, 40000, 8, "bf16", seed=48)  # the form for long rows
+    z = torch.empty(N * ld, dtype=torch.bfloat16, device=DEV).view(N, ld)[:, :40000]
+    z.copy_(wide[0])
+    got = dh.distill_topk_step(z, *wide[1:], grad_out=z)
+    want = dh.distill_topk_step(wide[0], *wide[1:])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T", [1e-18, 1e18, 1e-3, 1e3])
+def test_extreme_temperatures(T):
+    z, idx, y, gl = make(3, 9000, 12, "f32", seed=53)
+    loss, grad = dh.distill_topk_step(z, idx, y, gl, temperature=T)
+    ref = reference(z, idx, y, float(np.float32(T)), None, gl)
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    # terms below 2^-126 of the largest are flushed; the rest within the bounds
+    assert (np.abs(loss.double().cpu().numpy() - ref[0]) <= ref[1] + 1e-37).all()
+    g = grad.double().cpu().numpy()
+    assert (np.abs(g - ref[3]) <= ref[4] + 2.0 ** -24 * np.abs(ref[3]) + 2.0 ** -120 * abs(T) + 1e-37).all()
+
+
 @pytest.mark.parametrize("std", [0.0, 30.0, 1e4])
 def test_flat_and_peaked_rows(std):
     check_all(*make(3, 6000, 32, "f32", seed=19, std=std))

@@ -37,7 +37,7 @@ def test_distill_rejects_bad_arguments(lib, which):
     assert call(V=0) == INVALID
     assert call(K=0) == INVALID and call(K=1025) == INVALID
     assert call(ld=-1) == INVALID
-    for T in (0.0, -1.0, float("nan"), float("inf"), 1e-45):
+    for T in (0.0, -1.0, float("nan"), float("inf"), 1e-45, 1e-20, 1e20):
         assert call(T=T) == INVALID
     assert call(dt=2) == UNSUPPORTED
     assert call(V=(1 << 21) + 1, ld=1 << 22, gld=1 << 22) == UNSUPPORTED

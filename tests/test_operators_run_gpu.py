@@ -1,0 +1,114 @@
+"""The operators together, as a drafter uses them: beams are selected over the vocabulary, their states
+follow, ended beams are carried along, and an accepted path is appended to the committed states; the
+head is trained on the same rows.  Checked step by step against plain lists and 64-bit arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from speculative_decoding_draft_dh_gb300 import binding as dh
+from speculative_decoding_draft_dh_gb300 import distill, inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def test_beam_search_with_states_that_follow():
+    """Six steps of beam search of a toy drafter whose next logits depend on everything its state
+    holds, against the same search over lists of tokens."""
+    R, W, V, d, S, EOS = 3, 4, 2000, 32, 6, 7
+    g = torch.Generator().manual_seed(5)
+    emb = torch.randn(V, d, generator=g).to(DEV)
+    head = (torch.randn(d, V, generator=g) * 0.7).to(DEV)
+    head[:, EOS] += 0.4 * emb.mean(0) + 0.3          # ends now and then
+    cache = torch.zeros(2, R, W, S + 1, d, device=DEV)  # two layers: positions hold what was fed
+    start = torch.tensor([3, 11, 90], device=DEV)
+    cache[:, :, :, 0] = emb[start][None, :, None, :]
+    cache[1] *= 0.5
+    score = torch.full((R, W), -float("inf"), device=DEV)
+    score[:, 0] = 0.0                                # one beam at first
+    finished = torch.zeros(R, W, dtype=torch.int32, device=DEV)
+    # the plain search: per request a list of (tokens, score, finished), by beam
+    plain = [[([int(start[r])], 0.0, False)] + [None] * (W - 1) for r in range(R)]
+
+    def logits_of(tokens):
+        return torch.tanh(torch.stack([emb[t] for t in tokens]).sum(0) * 0.3) @ head
+
+    for step in range(S):
+        held = step + 1
+        h = torch.tanh((cache[0, :, :, :held].sum(2) + 2 * cache[1, :, :, :held].sum(2)) * 0.15)
+        logits = torch.empty(R, W, V, device=DEV)
+        for r in range(R):
+            for w in range(W):
+                logits[r, w] = h[r, w] @ head
+        parent, token, best = dh.beam_select(logits, score, W, finished=finished, pad_token=EOS)
+        dh.reorder_states(cache, parent, lengths=torch.full((R,), held, dtype=torch.int32, device=DEV), length_dim=3)
+        torch.cuda.synchronize()
+        for r in range(R):
+            cands = []
+            for w, beam in enumerate(plain[r]):
+                if beam is None:
+                    continue
+                toks, sc, fin = beam
+                if fin:
+                    cands.append((sc, w, EOS, toks, True))
+                    continue
+                z = logits_of(toks).double().cpu().numpy()
+                # the state that followed is the beam's own history
+                assert np.allclose(z, logits[r, w].double().cpu().numpy(), rtol=1e-4, atol=1e-4)
+                lp = z - z.max() - np.log(np.exp(z - z.max()).sum())
+                for v in np.argsort(-lp, kind="stable")[:W]:
+                    cands.append((sc + lp[v], w, int(v), toks, False))
+            cands.sort(key=lambda c: (-c[0], c[1], c[2]))
+            nxt = []
+            for j, (sc, w, v, toks, fin) in enumerate(cands[:W]):
+                # toy logits of two summation orders differ by 1e-4 at most; the seeds' gaps are wider
+                assert int(parent[r, j]) == w and int(token[r, j]) == v
+                assert abs(float(best[r, j]) - sc) <= 1e-3
+                nxt.append((toks + [v], sc, fin or v == EOS) if not fin else (toks, sc, True))
+            plain[r] = nxt + [None] * (W - len(nxt))
+        was = finished.gather(1, parent.clamp(min=0).long())
+        finished = ((was != 0) | (token == EOS)).int()
+        score = best
+        new = emb[token.clamp(min=0).long()]
+        keep = (was == 0)[..., None].float()
+        cache[0, :, :, held], cache[1, :, :, held] = new * keep, 0.5 * new * keep
+
+
+def test_a_round_of_drafting_and_training():
+    """The head drafts, the tree is accepted, its states are appended, and the rows train the head."""
+    cfg = inputs.head_config("tiny", B=4)
+    x = inputs.make_head(cfg, seed=9, device=DEV)
+    idx, _, exact, probs = dh.draft_head(x["h"], x["U"], x["V"], x["W"], cfg.K)
+    dh.expand_children(probs, idx, 4)
+    t = inputs.make_tree(inputs.TREE_CONFIGS["tiny_tree"], seed=9, device=DEV)
+    acc = dh.tree_accept(t["logits"], t["parent"], t["token"])
+    tree = torch.randn(2, 4, 8, 2, 16, device=DEV, dtype=torch.bfloat16)
+    cache = torch.zeros(2, 4, 2, 32, 16, device=DEV, dtype=torch.bfloat16)
+    held = torch.tensor([0, 5, 9, 20], dtype=torch.int32, device=DEV)
+    dh.reorder_states(tree, acc["path"], out=cache, dst_base=held, out_slot_dim=3)
+    o = oracle.tree_accept(t["logits"].cpu(), t["parent"].cpu(), t["token"].cpu())
+    torch.cuda.synchronize()
+    for r in range(4):
+        path = [p for p in o["path"][r] if p >= 0]
+        for i, p in enumerate(path):
+            assert torch.equal(cache[:, r, :, int(held[r]) + i], tree[:, r, p])
+        rest = cache[:, r].clone()
+        rest[:, :, int(held[r]):int(held[r]) + len(path)] = 0
+        assert not rest.any()
+    # one step of each form of training, and a selection over the trained scores
+    U, V = x["U"].clone().requires_grad_(True), x["V"].clone().requires_grad_(True)
+    scores = (x["h"] @ U) @ V
+    loss = distill.distill_loss(scores, idx, exact, temperature=2.0)
+    loss.mean().backward()
+    w = torch.full((4,), 0.25, device=DEV)
+    l2, grad = dh.distill_topk_step(scores.detach(), idx, exact, w, temperature=2.0)
+    gV = (x["h"] @ U.detach()).t() @ grad
+    assert torch.allclose(l2, loss.detach(), rtol=1e-5, atol=1e-5)
+    assert (gV - V.grad).norm() <= 1e-4 * V.grad.norm()
+    with torch.no_grad():
+        U -= 0.1 * U.grad
+        V -= 0.1 * V.grad
+    parent, token, score = dh.beam_select(((x["h"] @ U) @ V).detach().view(2, 2, -1), torch.zeros(2, 2, device=DEV), 6)
+    assert ((parent >= 0) & (parent < 2)).all() and ((token >= 0) & (token < cfg.vocab)).all()
+    assert (score[:, :-1] >= score[:, 1:]).all()
