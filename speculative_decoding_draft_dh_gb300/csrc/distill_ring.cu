@@ -11,9 +11,9 @@
 //                           slice, so memory stays busy through the reductions.
 //   consumers (20 warps)    pass A: maximum and sum of exp of the chunks as they arrive, each thread
 //                           with a running maximum; every warp puts its pair into all CTAs of the
-//                           cluster (a marked 64-bit word, no barrier) and combines all pairs in one
-//                           order.  Pass B: the dense term g T q from the slots, which are handed
-//                           back one by one.
+//                           cluster (a marked 64-bit word, no barrier), takes the next row's first
+//                           chunks meanwhile, and combines all pairs in one order.  Pass B: the dense
+//                           term g T q from the slots, which are handed back one by one.
 #include "rows.cuh"
 #include "sm100.cuh"
 
@@ -32,6 +32,7 @@ struct RingArgs {
   DistillArgs d;
   int lg;       // C = 2^lg
   int slots;    // ring slots
+  int spare;    // of them not needed by a row
   bool loose;   // rows may have elements beside their 16-byte grid
 };
 
@@ -158,17 +159,33 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
       const int at = tid < s.pre ? tid : s.behind + tid - s.pre;
       return at < d.vocab ? at : -1;
     };
+    // A row's pass A as far as it has come: running maximum and sum, vectors done, and the element
+    // beside the grid.
+    struct RowState {
+      float m, s, x;
+      int v;
+    };
+    auto begin = [&](long long row) {
+      RowState r = {-INFINITY, 0.f, -INFINITY, 0};
+      if (row < d.N && a.loose) {
+        const T* z = logits + row * d.ld;
+        const int at = beside(slice_of(z, d.vocab, part, lg));
+        if (at >= 0) r.m = r.x = Elem<T>::to_f(*(const volatile T*)(z + at));
+        if (r.x != -INFINITY) r.s = row_ex2((r.x - r.x) * d.c);  // 1, or NaN
+      }
+      return r;
+    };
+    RowState next = begin(cl);
     for (long long row = cl; row < d.N; row += ncl, ++it) {
       const int par = it & 1;
-      const T* const z = logits + row * d.ld;
-      const Slice sl = slice_of(z, d.vocab, part, lg);
+      const Slice sl = slice_of(logits + row * d.ld, d.vocab, part, lg);
       const int nl = sl.hi - sl.lo, lone = beside(sl);
-      const float x = lone >= 0 ? Elem<T>::to_f(*(const volatile T*)(z + lone)) : -INFINITY;
       const float g = __ldg(d.weight + row) * d.temperature;
       const bool zero = g == 0.f || (d.n_valid && __ldg(d.n_valid + row) <= 0);
-      float m = x, s = x == -INFINITY ? 0.f : row_ex2((x - x) * d.c);  // 1, or NaN
+      float m = next.m, s = next.s;
+      const float x = next.x;
       // two chunks at a time, four independent vectors per thread; whole ones without bounds checks
-      auto take = [&](const uint4 (&u)[4]) {
+      auto take = [&](const uint4 (&u)[4], float& m, float& s) {
         const float mn = max_nan(m, vec_max<T>(u));
         if (mn != m) {
           s = m == -INFINITY ? 0.f : s * row_ex2((m - mn) * d.c);
@@ -188,8 +205,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
           ph_a ^= 1;
         }
       };
-      int v = 0;
-      for (; v + 2 * DR_CHUNK <= nl; v += 2 * DR_CHUNK) {
+      auto take_two = [&](float& m, float& s) {
         uint4 u[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -199,8 +215,10 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
           u[2 * h + 1] = b[DR_NT];
           next_a();
         }
-        take(u);
-      }
+        take(u, m, s);
+      };
+      int v = next.v;
+      for (; v + 2 * DR_CHUNK <= nl; v += 2 * DR_CHUNK) take_two(m, s);
       if (v < nl) {
         uint4 u[4];
 #pragma unroll
@@ -212,7 +230,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
           for (int i = 0; i < 2; ++i) u[2 * h + i] = tid + i * DR_NT < n ? b[i * DR_NT] : make_uint4(NEG, NEG, NEG, NEG);
           if (n > 0) next_a();
         }
-        take(u);
+        take(u, m, s);
       }
       // the warp's pair, then everybody's
       const float wm = warp_max(m);
@@ -223,6 +241,21 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
         const unsigned long long word = pair_word(wm, s, mark);
         if (C == 1) *reinterpret_cast<volatile unsigned long long*>(&s_pair[par][warp]) = word;
         else put_word(remote_addr(&s_pair[par][part * DR_WARPS + warp], lane), word);
+      }
+      // while the pairs travel: the next row's first chunks, as far as the ring holds them beside this
+      // row's (a.spare) and they are there
+      next = begin(row + ncl);
+      if (a.spare >= 2 && row + ncl < d.N) {
+        const Slice ns = slice_of(logits + (row + ncl) * d.ld, d.vocab, part, lg);
+        const int most = min(ns.hi - ns.lo, a.spare * DR_CHUNK) - 2 * DR_CHUNK;
+        while (next.v <= most) {
+          const int second = slot_a + 1 == a.slots ? 0 : slot_a + 1;
+          const bool there = sm100::mbar_try_wait(&full[slot_a], ph_a) &&
+                             sm100::mbar_try_wait(&full[second], second ? ph_a : ph_a ^ 1);
+          if (!__all_sync(0xFFFFFFFFu, there)) break;
+          take_two(next.m, next.s);
+          next.v += 2 * DR_CHUNK;
+        }
       }
       const long long t0 = clock64();
       m = -INFINITY;
@@ -313,7 +346,8 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
     const int chunks = (slice + DR_CHUNK - 1) / DR_CHUNK;
     const int slots = dyn_max[dv] / (16 * DR_CHUNK);
     a.slots = slots < DR_MAX_SLOTS ? slots : DR_MAX_SLOTS;
-    fits = a.slots >= chunks + 1;
+    a.spare = a.slots - chunks;
+    fits = a.spare >= 1;
     if (fits && ((long long)d.N << a.lg >= c.num_sms || slice <= 512 || a.lg == 3)) break;
   }
   if (!fits) return cudaSuccess;
