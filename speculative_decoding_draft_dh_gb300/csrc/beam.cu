@@ -39,22 +39,6 @@ __device__ __forceinline__ double dkey_inv(unsigned long long k) {
   return __longlong_as_double((k >> 63) ? (long long)(k & 0x7FFFFFFFFFFFFFFFull) : (long long)~k);
 }
 
-// log(hi + lo) of a positive sum in two floats, to about 1e-9: the 64-bit logarithm takes 2,600 cycles
-// here, this 300.  With hi = 2^k f, f in [2/3, 4/3), and t = (f - 1)/(f + 1), log f = 2 artanh t
-// = 2 t + 2 t (t^2/3 + t^4/5 + ...): the first term in two floats, the rest, below 0.02 t, in one.
-__device__ __forceinline__ double log_sum(float hi, float lo) {
-  int k = (int)((__float_as_uint(hi) + 0x00555555u) >> 23) - 127;  // rounds to the nearest in [2/3, 4/3)
-  const float scale = __uint_as_float((uint32_t)(127 - k) << 23);
-  const float f = hi * scale, fl = lo * scale;  // exact
-  const float a = f - 1.f;                      // exact; the numerator is a + fl
-  const float b = f + 1.f, bl = (f - (b - 1.f)) + fl;
-  const float t = a / b;
-  const float tl = ((fmaf(-t, b, a) + fl) - t * bl) / b;
-  const float q = t * t;
-  const float r = q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 11.f, 1.f / 9.f), 1.f / 7.f), 1.f / 5.f), 1.f / 3.f);
-  return (double)k * 0.6931471805599453 + ((double)(2.f * t) + (double)(2.f * (tl + t * r)));
-}
-
 struct BeamArgs {
   const void* logits;
   long long rs, ws;  // strides of a request's and a beam's row, in elements
@@ -244,8 +228,11 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   }
   __syncthreads();
   for (int w = tid; w < W; w += BP_THREADS) {
-    const double b =
-        s.sum_hi[w] > 0.f ? (double)s.score[w] - log_sum(s.sum_hi[w], s.sum_lo[w]) : -(double)INFINITY;
+    double b = -(double)INFINITY;
+    if (s.sum_hi[w] > 0.f) {
+      const Sum2 l = log_sum(s.sum_hi[w], s.sum_lo[w]);
+      b = ((double)s.score[w] - (double)l.hi) - (double)l.lo;
+    }
     s.base[w] = b;
     s.base32[w] = (float)b;
   }

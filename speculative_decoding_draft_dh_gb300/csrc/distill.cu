@@ -271,7 +271,7 @@ struct RowEntries {
   bool twice;    // an id comes more than once
   float g;       // grad_loss T
   float total;   // NaN if an entry is
-  float part;    // sum_k p_k (log p_k - (z_k - zref)/T)
+  float part;    // sum_k p_k ((y_k - top)/T - (z_k - zref)/T)
   float zref;    // one of the entries' logits
 };
 
@@ -342,7 +342,7 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
       total += e;
     }
   total = r.total = warp_sum(total);
-  const float inv = 1.f / total, log_total = logf(total);
+  const float inv = 1.f / total;
   const bool write = GRAD && r.any && r.g != 0.f;
   float part = 0.f;
   bool twice = false;
@@ -351,7 +351,7 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
     const float ak = (s.p[k] - top) * a.inv_t, p = expf(ak) * inv;
     s.p[k] = p;
     if (id < 0) continue;
-    if (LOSS && p != 0.f) part += p * ((ak - log_total) - (s.z[k] - r.zref) * a.inv_t);  // 0 log 0 = 0
+    if (LOSS && p != 0.f) part += p * (ak - (s.z[k] - r.zref) * a.inv_t);  // 0 log 0 = 0
     if (write) {
       for (uint32_t h = (uint32_t)id * 0x9E3779B1u;; ++h) {  // at most half full: ends
         const int old = atomicCAS(&s.table[h & (uint32_t)(s.size - 1)], -1, id);
@@ -368,11 +368,22 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
   return r;
 }
 
-// The row's loss: sum_k p_k (log p_k - log q_k) with log q_k = (z_k - m)/T - log sum; for a row of
-// -inf infinite.
+// The row's loss: sum_k p_k (log p_k - log q_k) with log p_k = (y_k - top)/T - log total and
+// log q_k = (z_k - m)/T - log sum; for a row of -inf infinite.  The logarithms of the two sums are
+// several times the loss and nearly cancel, so they are added in two floats.
 __device__ __forceinline__ float entries_loss(const DistillArgs& a, const RowEntries& r, float m, float sum) {
-  const float l = a.temperature * a.temperature * (r.part + ((m - r.zref) * a.inv_t + logf(sum)));
-  return !r.any ? 0.f : (r.total != r.total ? r.total : (m == -INFINITY ? INFINITY : l));
+  if (!r.any) return 0.f;
+  if (r.total != r.total) return r.total;
+  if (m == -INFINITY) return INFINITY;
+  if (!(fabsf(m) < INFINITY) || !(sum < INFINITY)) return NAN;  // a NaN or +inf in the row
+  const float x = (m - r.zref) * a.inv_t;
+  if (!(fabsf(r.part + x) < INFINITY)) return r.part + x;  // an entry's q is 0: infinite
+  Sum2 l = log_sum(sum, 0.f);
+  const Sum2 t = log_sum(r.total, 0.f);
+  l.add(-t.hi);
+  l.add(x);
+  l.add(r.part);
+  return a.temperature * a.temperature * (l.hi + (l.lo - t.lo));
 }
 
 // By the same warp: the entries' values over the dense term.
