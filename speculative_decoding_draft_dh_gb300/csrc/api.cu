@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "dh_internal.cuh"
+#include "operators.cuh"
 
 namespace dh {
 

@@ -369,64 +369,6 @@ cudaError_t launch_verify(const Ctx& c, const void* logits, int dtype, int B, in
                           const float* u_sample, float temperature, int32_t* n_accept, int32_t* token,
                           float2* seg_stats);
 
-// Distillation from a teacher's top logits (row_stats.cu, distill.cu).
-struct DistillArgs {
-  const void* logits;  // [N] rows of `vocab`, stride ld elements
-  long long ld;
-  void* grad;  // rows of stride gld; may be the logits
-  long long gld;
-  const int32_t* idx;      // [N x K]
-  const float* teacher;    // [N x K]
-  const int32_t* n_valid;  // [N] or null
-  const float* weight;     // [N]
-  const float2* stats;     // [N] (max, sum)
-  const float2* seg;       // [N x n_seg] (max, sum) of the segments
-  float2* stats_out;
-  float* loss_out;
-  float* gathered;         // [N x K] the entries' logits, where the gradient overwrites them; or null
-  int* status;             // device status word, or null
-  int N, vocab, K, n_seg, splits;
-  float temperature, inv_t, c;  // c = log2(e) / T
-};
-int row_segments(int vocab, int dtype);
-bool rows_aligned(const void* logits, long long rs, long long ws, int R, int W, int elem);
-// Statistics of every segment of the rows [r][w] at logits + r rs + w ws, into seg [R W x n_seg].
-// With `score` given, the rows whose score is not finite or whose `finished` (may be null) is not 0
-// are left out.
-cudaError_t launch_row_stats(const Ctx& c, const void* logits, long long rs, long long ws, int R, int W, int vocab,
-                             int dtype, float temperature, const float* score, const int32_t* finished, float2* seg);
-// The kernels of distill.cu and distill_ring.cu; which of them a call takes is api.cu's choice.
-// launch_distill_ring: statistics (stats_out) and dense gradient; *done is false, and nothing was
-// launched, where the rows are too long.
-cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done);
-bool distill_short(const DistillArgs& a, int num_sms, bool step);  // rows for launch_distill_short
-cudaError_t launch_distill_short(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad);
-cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype);
-cudaError_t launch_distill_dense(const Ctx& c, const DistillArgs& a, int dtype);
-cudaError_t launch_distill_finish(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad);
-cudaError_t launch_distill_grad(const Ctx& c, const DistillArgs& a, int dtype);
-
-// Beam selection (beam.cu).
-cudaError_t launch_beam_select(const Ctx& c, const void* logits, long long rs, long long ws, const float* score,
-                               const int32_t* finished, const float2* seg, int R, int W, int vocab, int M, int dtype,
-                               float temperature, int pad_token, int32_t* parent, int32_t* token, float* score_out);
-
-// Reordering of states (states.cu).  Sizes and byte strides of (A, R, slot, H, T) and a contiguous
-// unit of bytes.
-struct ReorderArgs {
-  const char* src;
-  char* dst;
-  long long ss[5], ds[5];
-  const int32_t* idx;                            // [R x M]
-  const int32_t *lengths, *src_base, *dst_base;  // [R] or null
-  int A, R, src_slots, dst_slots, M, H, T;
-  long long unit;
-  bool in_place;
-};
-long long reorder_columns(const ReorderArgs& a);
-long long reorder_blocks(const ReorderArgs& a);
-cudaError_t launch_reorder(const Ctx& c, const ReorderArgs& a);
-
 cudaError_t launch_tree(const Ctx& c, const void* logits, const int32_t* parent, const int32_t* token,
                         int B, int N, int vocab, int dtype, int32_t* argmax_ws, int32_t* argmax_out,
                         int32_t* path, int32_t* len, int32_t* bonus, int32_t* err);

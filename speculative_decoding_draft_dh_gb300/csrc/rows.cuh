@@ -6,7 +6,7 @@
 // on the position in the row alone, not on the row's address: equal rows give equal sums.
 #pragma once
 
-#include "dh_internal.cuh"
+#include "operators.cuh"
 
 namespace dh {
 

@@ -11,7 +11,7 @@
 //   k_reorder_inplace:  up to 16 moves in registers; more are staged in the block's shared memory,
 //                       as many columns at a time as fit.  Slots that stay where they are cost
 //                       nothing.
-#include "dh_internal.cuh"
+#include "operators.cuh"
 
 namespace dh {
 namespace {
