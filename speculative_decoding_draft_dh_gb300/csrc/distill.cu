@@ -11,14 +11,17 @@
 //   both              k_distill_ring (distill_ring.cu: statistics and dense term in one pass over the
 //                     logits), k_distill_finish
 //   gradient where the rows do not lie like their logits, or in the logits' place: k_distill_grad
+//   short rows: k_distill_short, one block per row, everything in one launch
 //
-// k_distill_dense: every vector of a row times one factor; `splits` blocks per row.
+// k_distill_dense: the exponentials of a row's vectors times one factor; `splits` blocks per row.
+//   1024 rows of 151936 bf16 logits, 622 MB: 91 us, 6.4 TB/s with the rows that are not read taken
+//   off.  Eight vectors per thread of 512 in flight; measured against 4 per thread of 256: 98 us.
 // k_distill_finish: one warp per row: the teacher's softmax, the loss, and the entries' values over
 //   the dense ones, one writer per id: the first entry of an id adds up the others' p in order, so
 //   repeated ids repeat bit for bit.  A hash table in shared memory finds out whether there are any.
 //   Latency-bound (ids, then their logits, then the row's statistics), so it starts under the pass
 //   before it by programmatic dependent launch and waits for that pass only when it needs the
-//   statistics.  What it reads before the wait are the call's inputs: the kernels before it let it
+//   statistics (16 us behind the one-pass step of 2048 rows, 7 under it).  What it reads before the wait are the call's inputs: the kernels before it let it
 //   start only after their own wait, when those are complete.
 // k_distill_grad: dense term and entries in one kernel; the logits of a part's entries are read
 //   before its dense pass writes anything.
@@ -353,7 +356,8 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
     if (id < 0) continue;
     if (LOSS && p != 0.f) part += p * (ak - (s.z[k] - r.zref) * a.inv_t);  // 0 log 0 = 0
     if (write) {
-      for (uint32_t h = (uint32_t)id * 0x9E3779B1u;; ++h) {  // at most half full: ends
+      // multiplicative hashing: the product's leading bits; the table is at most half full, so it ends
+      for (uint32_t h = (uint32_t)id * 0x9E3779B1u >> (__clz(s.size) + 1);; ++h) {
         const int old = atomicCAS(&s.table[h & (uint32_t)(s.size - 1)], -1, id);
         if (old == -1) break;
         if (old == id) {
@@ -578,13 +582,12 @@ cudaError_t run_finish(const Ctx& c, const DistillArgs& a, bool loss, bool grad)
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, a, table);
     return e;
   };
-  static unsigned long long done[4] = {};
+  static unsigned long long done[3] = {};
   prof_before("distill_finish", c.stream);
   cudaError_t e;
   if (loss && grad) e = go(k_distill_finish<T, true, true, false>, &done[0]);
   else if (grad) e = go(k_distill_finish<T, false, true, false>, &done[1]);
-  else if (a.seg) e = go(k_distill_finish<T, true, false, true>, &done[2]);
-  else e = go(k_distill_finish<T, true, false, false>, &done[3]);
+  else e = go(k_distill_finish<T, true, false, true>, &done[2]);
   prof_after(c.stream);
   return e;
 }

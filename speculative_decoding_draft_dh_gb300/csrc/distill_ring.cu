@@ -14,6 +14,11 @@
 //                           cluster (a marked 64-bit word, no barrier), takes the next row's first
 //                           chunks meanwhile, and combines all pairs in one order.  Pass B: the dense
 //                           term g T q from the slots, which are handed back one by one.
+// Measured at 2048 rows of 151936 bf16 logits (two CTAs per row, 152 KB each in a ring of 11 slots of
+// 20 KB, one CTA per SM): 206 us for 1.24 GB, 6.0 TB/s, against 278 us for a statistics and a dense
+// pass and 277 for one block per row that reads it twice, the second time from L2.  The consumers'
+// instructions bound it (about nine per logit and lane, and the rows' own work): 16 warps 213 us, 24
+// 219, four CTAs per row 256, eight 500 (each with 16 warps more of per-row work).
 #include "rows.cuh"
 #include "sm100.cuh"
 

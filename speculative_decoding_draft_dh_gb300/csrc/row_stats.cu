@@ -6,7 +6,9 @@
 // A warp holds a whole segment in registers, so the sum is taken relative to the segment's true
 // maximum, without a running rescale, with one reduction pair per 32 elements of a lane.  The
 // warps stream the (row, segment) items of all rows, so a row longer than a warp's share is split
-// over many SMs and few rows still use the whole card.
+// over many SMs and few rows still use the whole card.  64 warps per SM (32 registers) keep enough
+// loads in flight without any in the code: 2048 rows of 151936 bf16 logits, 622 MB, 93 us, 6.7 TB/s;
+// with the next item's loads issued ahead (fewer warps fit) 117, with 32 warps 115.
 #include "rows.cuh"
 
 namespace dh {

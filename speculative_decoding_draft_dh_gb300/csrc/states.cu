@@ -7,6 +7,8 @@
 // the column, so in place needs no more than a thread's own order (all loads before the first
 // store) and no second buffer; a source that several targets share is fetched from HBM once, its
 // loads being issued together.
+// 8 requests of 8 beams, 2.35 GB in caches of up to 4096 positions: 336 us, 7.0 TB/s (the copy's rate);
+// the accepted paths of 64 trees, 12.6 MB: 6 us, a chain of two loads and the launch.
 //   k_reorder:          separate source and target: batches of 8 slots in registers.
 //   k_reorder_inplace:  up to 16 moves in registers; more are staged in the block's shared memory,
 //                       as many columns at a time as fit.  Slots that stay where they are cost
