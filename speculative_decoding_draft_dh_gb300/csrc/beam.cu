@@ -113,7 +113,7 @@ __device__ __forceinline__ void set_thresholds(BeamSmem& s, const BeamArgs& a, f
 
 // Leaves the best M of the list's s.n > M candidates in its first M places (in no order): the M-th
 // key by descent over its bits with block-wide counts, then, among equal keys, the M-th position.
-__device__ __forceinline__ void keep_best(BeamSmem& s, int M) {
+__device__ __noinline__ void keep_best(BeamSmem& s, int M) {
   constexpr int PER = BP_CAP / BP_THREADS;
   unsigned long long k[PER];
   uint32_t p[PER];
@@ -167,10 +167,8 @@ __device__ __forceinline__ void keep_best(BeamSmem& s, int M) {
 // Adds the elements of vector u (ids id ..) of beam w that reach the bound.  Their logits stand where
 // the keys will (score_pushed).
 template <typename T>
-__device__ __forceinline__ void push_vec(BeamSmem& s, const BeamArgs& a, const uint4& u, int id, int w, float zthr) {
+__device__ __noinline__ void push_elems(BeamSmem& s, const BeamArgs& a, uint4 u, int id, int w, float zthr) {
   constexpr int PER = Elem<T>::PER16;
-  const uint4 one[1] = {u};
-  if (!(vec_max<T>(one) >= zthr)) return;  // most vectors
   float z[PER];
   Elem<T>::unpack(u, z);
 #pragma unroll
@@ -183,9 +181,14 @@ __device__ __forceinline__ void push_vec(BeamSmem& s, const BeamArgs& a, const u
       }
     }
 }
+template <typename T>
+__device__ __forceinline__ void push_vec(BeamSmem& s, const BeamArgs& a, const uint4& u, int id, int w, float zthr) {
+  const uint4 one[1] = {u};
+  if (vec_max<T>(one) >= zthr) push_elems<T>(s, a, u, id, w, zthr);  // few vectors
+}
 
 // The keys of the candidates from number `first` on, whose logits were pushed.
-__device__ __forceinline__ void score_pushed(BeamSmem& s, const BeamArgs& a, int first) {
+__device__ __noinline__ void score_pushed(BeamSmem& s, const BeamArgs& a, int first) {
   for (int i = first + (int)threadIdx.x; i < s.n; i += BP_THREADS)
     s.key[i] = dkey(exact_score(s, a, (int)(s.pos[i] / (uint32_t)a.vocab), __uint_as_float((uint32_t)s.key[i])));
 }
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
       if (s.base32[w] == -INFINITY) continue;
       uint4 u[ROW_SEG_VECS];
 #pragma unroll
-      for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec<T, ALIGNED>(rows + w * a.ws, id0 + v * 32 * PER, a.vocab);
+      for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec<T, ALIGNED, true>(rows + w * a.ws, id0 + v * 32 * PER, a.vocab);
       best = fmaxf(best, score_below(s.base32[w], s.top[w], vec_max<T>(u), a.inv_t));
     }
   } else {
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
         const int i = i0 + q * BP_WARPS;
         if (i >= n_rows) continue;
         const int sg = (int)s.segs[i / ROW_SEG_VECS], w = beam_of(sg);
-        u[q] = row_vec<T, ALIGNED>(rows + w * a.ws,
+        u[q] = row_vec<T, ALIGNED, true>(rows + w * a.ws,
                                    (sg - w * n_seg) * SEG + (i % ROW_SEG_VECS * 32 + lane) * PER, a.vocab);
       }
 #pragma unroll
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
       const int w = found / n_seg, id0 = (found - w * n_seg) * SEG;
       if (warp < ROW_SEG_VECS) {
         const int id = id0 + (warp * 32 + lane) * PER;
-        const uint4 u = row_vec<T, ALIGNED>(rows + w * a.ws, id, a.vocab);
+        const uint4 u = row_vec<T, ALIGNED, true>(rows + w * a.ws, id, a.vocab);
         push_vec<T>(s, a, u, id, w, s.zthr[w]);
       }
       __syncthreads();

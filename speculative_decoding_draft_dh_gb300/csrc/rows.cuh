@@ -49,11 +49,10 @@ template <> struct NegInf<__nv_bfloat16> { static constexpr uint32_t WORD = 0xFF
 __device__ __forceinline__ uint32_t elem_bits(float x) { return __float_as_uint(x); }
 __device__ __forceinline__ uint32_t elem_bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 
-// Elements id .. id + PER16 - 1 of a row, -inf past its end.  ALIGNED: the row starts on 16 bytes.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ uint4 row_vec(const T* row, int id, int vocab) {
+// Elements id .. id + PER16 - 1 of a row, -inf past its end: the row's last, partial vector.
+template <typename T>
+__device__ __forceinline__ uint4 row_tail(const T* row, int id, int vocab) {
   constexpr int PER = Elem<T>::PER16;
-  if (id + PER <= vocab) return ALIGNED ? ld_nc_v4(row + id) : ld16_any(row + id);
   uint32_t w[4] = {NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD};
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
@@ -64,6 +63,20 @@ __device__ __forceinline__ uint4 row_vec(const T* row, int id, int vocab) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __noinline__ uint4 row_tail_call(const T* row, int id, int vocab) { return row_tail<T>(row, id, vocab); }
+template <typename T>
+__device__ __noinline__ uint4 ld16_any_call(const T* p) { return ld16_any(p); }
+
+// Elements id .. id + PER16 - 1 of a row, -inf past its end.  ALIGNED: the row starts on 16 bytes.
+// SMALL: the rare paths are calls, for code that is run once and unrolled (its instructions come from
+// memory).
+template <typename T, bool ALIGNED, bool SMALL = false>
+__device__ __forceinline__ uint4 row_vec(const T* row, int id, int vocab) {
+  if (id + Elem<T>::PER16 <= vocab)
+    return ALIGNED ? ld_nc_v4(row + id) : (SMALL ? ld16_any_call<T>(row + id) : ld16_any(row + id));
+  return SMALL ? row_tail_call<T>(row, id, vocab) : row_tail<T>(row, id, vocab);
 }
 
 // Maximum that a NaN passes through, so that a row which holds one is found out.
