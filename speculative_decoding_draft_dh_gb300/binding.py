@@ -492,10 +492,10 @@ def _workspace_bytes(query, *sizes):
 
 
 def _scratch(nbytes, workspace, kind, dev):
-    """nbytes of device memory, not zeroed: the caller's workspace object's, else fresh."""
+    """nbytes of device memory, not zeroed: the caller's workspace object's, else fresh (None: 0 bytes)."""
     if workspace is not None:
         return workspace.get(nbytes, dev, kind)
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
 def _addr(t):
@@ -578,7 +578,7 @@ def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_ou
     nbytes = _workspace_bytes("dh_distill_topk_workspace", N, vocab, dt)
     ws = _scratch(nbytes, workspace, "distill", dev)
     _check(lib.dh_distill_topk(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(), _addr(n_valid),
-                               N, vocab, K, dt, temperature, loss.data_ptr(), stats.data_ptr(), ws.data_ptr(), nbytes,
+                               N, vocab, K, dt, temperature, loss.data_ptr(), stats.data_ptr(), _addr(ws), nbytes,
                                _raw_stream(index)), "dh_distill_topk")
     return loss, stats
 
@@ -624,7 +624,7 @@ def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperat
     ws = _scratch(nbytes, workspace, "distill_step", dev)
     _check(lib.dh_distill_topk_step(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
                                     _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, temperature,
-                                    loss.data_ptr(), grad.data_ptr(), grad.stride(0), ws.data_ptr(), nbytes,
+                                    loss.data_ptr(), grad.data_ptr(), grad.stride(0), _addr(ws), nbytes,
                                     _raw_stream(index)), "dh_distill_topk_step")
     return loss, grad
 
@@ -656,7 +656,7 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     ws = _scratch(nbytes, workspace, "beam", dev)
     _check(lib.dh_beam_select(logits.data_ptr(), logits.stride(0), logits.stride(1), score.data_ptr(), _addr(finished),
                               R, W, vocab, M, dt, temperature, pad_token, parent.data_ptr(), token.data_ptr(),
-                              best.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(index)), "dh_beam_select")
+                              best.data_ptr(), _addr(ws), nbytes, _raw_stream(index)), "dh_beam_select")
     return parent, token, best
 
 

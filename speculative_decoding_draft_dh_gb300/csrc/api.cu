@@ -708,6 +708,7 @@ bool lie_alike(const DistillArgs& a, int dtype) {
 
 size_t dh_distill_topk_workspace(int N, int vocab, int dtype) {
   if (N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
+  if (distill_short_always(N, row_segments(vocab, dtype), false)) return 0;
   return WS_HEADER + seg_bytes(N, vocab, dtype);
 }
 
@@ -718,14 +719,15 @@ int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, 
   if (st != DH_OK || N == 0) return st;
   if (!loss_out) return DH_ERR_INVALID_ARG;
   if (!aligned_to(stats_out, 8)) return DH_ERR_UNSUPPORTED;
-  if (!workspace || !aligned256(workspace) || ws_bytes < dh_distill_topk_workspace(N, vocab, dtype))
-    return DH_ERR_WORKSPACE;
+  const size_t need = dh_distill_topk_workspace(N, vocab, dtype);
+  if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return DH_ERR_WORKSPACE;
   Ctx c;
   if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
   DistillArgs a = distill_args(logits, row_stride, idx, teacher, n_valid, N, vocab, K, dtype, temperature);
   a.loss_out = loss_out;
   a.stats_out = reinterpret_cast<float2*>(stats_out);
-  return run_distill_loss(c, a, dtype, reinterpret_cast<float2*>(static_cast<char*>(workspace) + WS_HEADER));
+  char* ws = static_cast<char*>(workspace);
+  return run_distill_loss(c, a, dtype, need ? reinterpret_cast<float2*>(ws + WS_HEADER) : nullptr);
 }
 
 int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
@@ -757,6 +759,7 @@ int dh_distill_topk_backward(const void* logits, int64_t row_stride, const int32
 
 size_t dh_distill_topk_step_workspace(int N, int vocab, int K, int dtype) {
   if (K < 1 || K > DH_MAX_K || N <= 0 || vocab <= 0 || vocab > DH_MAX_VOCAB || !valid_dtype(dtype)) return 0;
+  if (distill_short_always(N, row_segments(vocab, dtype), true)) return 0;
   return WS_HEADER + seg_bytes(N, vocab, dtype) + align_up((size_t)N * sizeof(float2), 256) +
          align_up((size_t)N * K * sizeof(float), 256);
 }
@@ -770,8 +773,8 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
   if (!loss_out || !grad_loss || !grad_out || (N > 1 && grad_stride < vocab)) return DH_ERR_INVALID_ARG;
   if (rows_clash(logits, row_stride, grad_out, grad_stride, N, vocab, dtype)) return DH_ERR_INVALID_ARG;
   if (!aligned_to(grad_out, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
-  if (!workspace || !aligned256(workspace) || ws_bytes < dh_distill_topk_step_workspace(N, vocab, K, dtype))
-    return DH_ERR_WORKSPACE;
+  const size_t need = dh_distill_topk_step_workspace(N, vocab, K, dtype);
+  if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return DH_ERR_WORKSPACE;
   Ctx c;
   if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
   DistillArgs a = distill_args(logits, row_stride, idx, teacher, n_valid, N, vocab, K, dtype, temperature);
@@ -779,17 +782,15 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
   a.grad = grad_out;
   a.gld = grad_stride;
   a.loss_out = loss_out;
+  if (distill_short(a, c.num_sms, true))
+    return note_error(launch_distill_short(c, a, dtype, true, true), "distillation step") == cudaSuccess ? DH_OK
+                                                                                                         : DH_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
   float2* seg = reinterpret_cast<float2*>(ws + WS_HEADER);
   float2* stats = reinterpret_cast<float2*>(ws + WS_HEADER + seg_bytes(N, vocab, dtype));
   a.status = static_cast<int*>(workspace);
   a.stats_out = stats;
   a.stats = stats;
-  if (distill_short(a, c.num_sms, true)) {
-    a.stats_out = nullptr;
-    return note_error(launch_distill_short(c, a, dtype, true, true), "distillation step") == cudaSuccess ? DH_OK
-                                                                                                         : DH_ERR_CUDA;
-  }
   if (lie_alike(a, dtype)) {
     DistillArgs b = a;
     if (a.grad == a.logits) {

@@ -623,9 +623,10 @@ cudaError_t run_gather(const Ctx& c, const DistillArgs& a) {
 cudaError_t launch_distill_short(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad) {
   return dtype == DH_BF16 ? run_short<__nv_bfloat16>(c, a, loss, grad) : run_short<float>(c, a, loss, grad);
 }
+bool distill_short_always(int N, int n_seg, bool step) { return n_seg <= DS_SEG_FEW && (step || N <= 512); }
 bool distill_short(const DistillArgs& a, int num_sms, bool step) {
-  if (step) return a.n_seg <= DS_SEG_FEW || (a.n_seg <= DS_MAX_SEG && a.N >= num_sms);
-  return a.n_seg <= DS_SEG_FEW && a.N <= 8 * num_sms;
+  if (distill_short_always(a.N, a.n_seg, step)) return true;
+  return step ? a.n_seg <= DS_MAX_SEG && a.N >= num_sms : a.n_seg <= DS_SEG_FEW && a.N <= 8 * num_sms;
 }
 cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype) {
   return dtype == DH_BF16 ? run_gather<__nv_bfloat16>(c, a) : run_gather<float>(c, a);

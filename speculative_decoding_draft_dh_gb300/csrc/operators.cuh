@@ -36,7 +36,10 @@ cudaError_t launch_row_stats(const Ctx& c, const void* logits, long long rs, lon
 // launch_distill_ring: statistics (stats_out) and dense gradient; *done is false, and nothing was
 // launched, where the rows are too long.
 cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done);
-bool distill_short(const DistillArgs& a, int num_sms, bool step);  // rows for launch_distill_short
+// Rows for launch_distill_short: distill_short on a device of num_sms SMs; whatever the device (and so
+// without a workspace) if distill_short_always.
+bool distill_short_always(int N, int n_seg, bool step);
+bool distill_short(const DistillArgs& a, int num_sms, bool step);
 cudaError_t launch_distill_short(const Ctx& c, const DistillArgs& a, int dtype, bool loss, bool grad);
 cudaError_t launch_distill_gather(const Ctx& c, const DistillArgs& a, int dtype);
 cudaError_t launch_distill_dense(const Ctx& c, const DistillArgs& a, int dtype);

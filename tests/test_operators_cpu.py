@@ -46,7 +46,9 @@ def test_distill_rejects_bad_arguments(lib, which):
     assert call(N=0, z=0, idx=0, y=0, loss=0, gl=0, grad=0, ws=0) == DH_OK
     if which != "backward":
         assert call(loss=0) == INVALID
-        assert call(ws=0) == WORKSPACE and call(ws=FAKE * 16 + 16) == WORKSPACE and call(nbytes=15) == WORKSPACE
+        long = dict(V=100000, ld=100000, gld=100000, grad=FAKE << 12)  # short rows need no workspace
+        assert call(**long, ws=0) == WORKSPACE and call(**long, ws=FAKE * 16 + 16) == WORKSPACE
+        assert call(**long, nbytes=15) == WORKSPACE
     if which != "step":
         assert call(stats=FAKE + 4) == UNSUPPORTED
     if which == "backward":
@@ -64,6 +66,9 @@ def test_distill_workspaces(lib):
     ws = lib.dh_distill_topk_workspace(512, 151936, binding.BF16)
     assert ws % 256 == 0 and ws >= 512 * 149 * 8  # a pair per 1024 logits
     assert lib.dh_distill_topk_step_workspace(512, 151936, 64, binding.BF16) >= ws + 512 * (8 + 64 * 4)
+    assert lib.dh_distill_topk_workspace(4, 4096, binding.F32) == 0  # one launch, nothing between
+    assert lib.dh_distill_topk_workspace(600, 4096, binding.F32) > 0
+    assert lib.dh_distill_topk_step_workspace(600, 4096, 16, binding.F32) == 0
     for bad in ((0, 100, 0), (-1, 100, 0), (1, 0, 0), (1, 100, 2), (1, (1 << 21) + 1, 0)):
         assert lib.dh_distill_topk_workspace(*bad) == 0
         assert lib.dh_distill_topk_step_workspace(bad[0], bad[1], 8, bad[2]) == 0
