@@ -18,8 +18,9 @@
 // then enters only with a score above the M-th best (equal ones come behind it in the order), so
 // even constant rows end after the first segments.
 //
-// k_beam_pick is a chain of latencies (128 requests of 16 beams, M = 16: 9 us, of it the combination
-// 1.5, logarithms 0.6, bound 1.5, search of the list 0.6, segments read again 2.5, scores and order 1.5).
+// k_beam_pick is a chain of latencies (128 requests of 16 beams, M = 16: 8 us, of it the combination
+// 1.4, logarithms 0.5, bound 1.5, search of the segments 0.5, elements read again 2, scores and order 2).
+// What runs once is kept out of line: unrolled code has to come from memory first.
 #include "rows.cuh"
 
 namespace dh {

@@ -194,7 +194,7 @@ def test_far_scores_and_temperatures():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("R,W,V,M", [(1, 128, 60001, 200), (1, 2, 2 ** 21, 16), (40, 3, 1500, 6), (2, 17, 151936, 20)])
+@pytest.mark.parametrize("R,W,V,M", [(1, 128, 60001, 200), (1, 2, 2 ** 21, 16), (40, 3, 1500, 6), (3000, 2, 64, 3), (2, 17, 151936, 20)])
 def test_many_segments(R, W, V, M, dtype):
     """More segments than are staged, held in registers, or looked at in one round."""
     check(*make(R, W, V, dtype, seed=V), M)
