@@ -355,8 +355,8 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
  * bytes (address and strides), with gradient rows that lie like the logits'.  K <= DH_MAX_K, vocab <=
  * DH_MAX_VOCAB, temperature > 0 with temperature^2 neither overflowing nor underflowing fp32.
  * Workspaces (0 bytes, then NULL will do, for short rows): 256-byte aligned, need not be zeroed, not
- * shared by calls that overlap in time.  N = 0 is a no-op.  Results repeat bit for bit from call to call; the three calls sum in different orders,
- * so they agree with one another to rounding.
+ * shared by calls that overlap in time.  N = 0 is a no-op.  Results repeat bit for bit from call to
+ * call; the three calls sum in different orders, so they agree with one another to rounding.
  * dh_distill_topk_step waits on on-chip barriers; one that gives up leaves NaN losses and raises the
  * workspace's status bit (dh_workspace_status; the word has to be zeroed before the first use).
  * ------------------------------------------------------------------------------------------- */

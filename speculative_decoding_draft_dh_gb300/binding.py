@@ -578,8 +578,8 @@ def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_ou
     nbytes = _workspace_bytes("dh_distill_topk_workspace", N, vocab, dt)
     ws = _scratch(nbytes, workspace, "distill", dev)
     _check(lib.dh_distill_topk(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(), _addr(n_valid),
-                               N, vocab, K, dt, temperature, loss.data_ptr(), stats.data_ptr(), _addr(ws), nbytes,
-                               _raw_stream(index)), "dh_distill_topk")
+                               N, vocab, K, dt, float(temperature), loss.data_ptr(), stats.data_ptr(), _addr(ws),
+                               nbytes, _raw_stream(index)), "dh_distill_topk")
     return loss, stats
 
 
@@ -599,7 +599,7 @@ def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=Non
     grad = _grad_rows(logits, grad_out, index)
     _check(lib.dh_distill_topk_backward(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
                                         _addr(n_valid), stats.data_ptr(), grad_loss.data_ptr(), N, vocab, K, dt,
-                                        temperature, grad.data_ptr(), grad.stride(0), _raw_stream(index)),
+                                        float(temperature), grad.data_ptr(), grad.stride(0), _raw_stream(index)),
            "dh_distill_topk_backward")
     return grad
 
@@ -623,7 +623,7 @@ def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperat
     nbytes = _workspace_bytes("dh_distill_topk_step_workspace", N, vocab, K, dt)
     ws = _scratch(nbytes, workspace, "distill_step", dev)
     _check(lib.dh_distill_topk_step(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(),
-                                    _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, temperature,
+                                    _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, float(temperature),
                                     loss.data_ptr(), grad.data_ptr(), grad.stride(0), _addr(ws), nbytes,
                                     _raw_stream(index)), "dh_distill_topk_step")
     return loss, grad
@@ -643,6 +643,7 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     _typed(score, "score", torch.float32, (R, W), index)
     if finished is not None:
         _typed(finished, "finished", torch.int32, (R, W), index)
+    M = int(M)
     dev = logits.device
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(stream, dev, (logits, score, finished, parent_out, token_out, score_out), lambda: beam_select(
@@ -655,8 +656,9 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     nbytes = _workspace_bytes("dh_beam_select_workspace", R, W, vocab, dt)
     ws = _scratch(nbytes, workspace, "beam", dev)
     _check(lib.dh_beam_select(logits.data_ptr(), logits.stride(0), logits.stride(1), score.data_ptr(), _addr(finished),
-                              R, W, vocab, M, dt, temperature, pad_token, parent.data_ptr(), token.data_ptr(),
-                              best.data_ptr(), _addr(ws), nbytes, _raw_stream(index)), "dh_beam_select")
+                              R, W, vocab, M, dt, float(temperature), int(pad_token), parent.data_ptr(),
+                              token.data_ptr(), best.data_ptr(), _addr(ws), nbytes, _raw_stream(index)),
+           "dh_beam_select")
     return parent, token, best
 
 
@@ -734,6 +736,8 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
         raise ValueError("states must be a CUDA tensor")
     if dst.dtype != states.dtype:
         raise ValueError("out must have the dtype of states")
+    if (states.requires_grad or dst.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("states are moved outside of autograd: detach them, or call under torch.no_grad()")
     if (lengths is None) != (length_dim is None):
         raise ValueError("lengths and length_dim come together")
     plan = _reorder_plan(states.shape, states.stride(), dst.shape, dst.stride(), states.element_size(), request_dim,

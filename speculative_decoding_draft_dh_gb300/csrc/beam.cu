@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
       if (s.base32[w] == -INFINITY) continue;
       uint4 u[ROW_SEG_VECS];
 #pragma unroll
-      for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec<T, ALIGNED, true>(rows + w * a.ws, id0 + v * 32 * PER, a.vocab);
+      for (int v = 0; v < ROW_SEG_VECS; ++v)
+        u[v] = row_vec<T, ALIGNED, true>(rows + w * a.ws, id0 + v * 32 * PER, a.vocab);
       best = fmaxf(best, score_below(s.base32[w], s.top[w], vec_max<T>(u), a.inv_t));
     }
   } else {

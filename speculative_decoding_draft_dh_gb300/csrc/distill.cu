@@ -21,8 +21,9 @@
 //   repeated ids repeat bit for bit.  A hash table in shared memory finds out whether there are any.
 //   Latency-bound (ids, then their logits, then the row's statistics), so it starts under the pass
 //   before it by programmatic dependent launch and waits for that pass only when it needs the
-//   statistics (16 us behind the one-pass step of 2048 rows, 7 under it).  What it reads before the wait are the call's inputs: the kernels before it let it
-//   start only after their own wait, when those are complete.
+//   statistics (2048 rows of 64 entries: 12 us after a pass, 7 where it can start under it).  What it
+//   reads before the wait are the call's inputs: the kernels before it let it start only after their
+//   own wait, when those are complete.
 // k_distill_grad: dense term and entries in one kernel; the logits of a part's entries are read
 //   before its dense pass writes anything.
 

@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
           const uint4* const b = ring + slot_a * DR_CHUNK + tid;
           if (n > 0) wait(&full[slot_a], ph_a);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) u[2 * h + i] = tid + i * DR_NT < n ? b[i * DR_NT] : make_uint4(NEG, NEG, NEG, NEG);
+          for (int i = 0; i < 2; ++i)
+            u[2 * h + i] = tid + i * DR_NT < n ? b[i * DR_NT] : make_uint4(NEG, NEG, NEG, NEG);
           if (n > 0) next_a();
         }
         take(u, m, s);

@@ -20,7 +20,8 @@ constexpr int RS_THREADS = 256;
 // as a third of its logits).
 template <typename T, bool ALIGNED, typename Index>
 __global__ void __launch_bounds__(RS_THREADS) k_row_stats(const T* __restrict__ logits, long long rs,
-                                                          long long ws, int W, int vocab, float c, int n_seg, Index n_items,
+                                                          long long ws, int W, int vocab, float c, int n_seg,
+                                                          Index n_items,
                                                           const float* __restrict__ score,
                                                           const int32_t* __restrict__ finished,
                                                           float2* __restrict__ seg) {

@@ -46,8 +46,8 @@ __device__ __forceinline__ Place place(const ReorderArgs& p, uint32_t blocks_per
 }
 
 // Offsets of column `col` = (h, t, v) in source and target; false past the last or the length.
-__device__ __forceinline__ bool column(const ReorderArgs& p, uint32_t col, uint32_t cols, uint32_t per_t, int V, int len,
-                                       long long* so, long long* dso) {
+__device__ __forceinline__ bool column(const ReorderArgs& p, uint32_t col, uint32_t cols, uint32_t per_t, int V,
+                                       int len, long long* so, long long* dso) {
   if (col >= cols) return false;
   const uint32_t x = col / per_t, v = col - x * per_t;
   const uint32_t h = x / (uint32_t)p.T, t = x - h * (uint32_t)p.T;
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(RO_THREADS) k_reorder_inplace(ReorderArgs p, u
     if ((int)threadIdx.x >= width || c >= RO_THREADS || !column(p, q.col0 + c, cols, per_t, V, len, &so, &dso))
       continue;
     // a thread's own places in the staging, so no barrier
-    for (int b = 0; b < n; ++b) st[b * width + threadIdx.x] = *reinterpret_cast<const T*>(base + dso + s_from[b] * p.ds[2]);
+    for (int b = 0; b < n; ++b)
+      st[b * width + threadIdx.x] = *reinterpret_cast<const T*>(base + dso + s_from[b] * p.ds[2]);
     for (int b = 0; b < n; ++b) *reinterpret_cast<T*>(base + dso + s_to[b] * p.ds[2]) = st[b * width + threadIdx.x];
   }
 }

@@ -262,4 +262,7 @@ def test_refusals():
     with pytest.raises(dh.DhError):
         dh.beam_select(torch.zeros(1, 129, 4, device=DEV), torch.zeros(1, 129, device=DEV), 2)
     par, tok, sc = dh.beam_select(z[:0], score[:0], 2)
+    same = dh.beam_select(z, score, np.int64(2), temperature=np.float32(1), pad_token=np.int32(3))
+    for a, b in zip(same, dh.beam_select(z, score, 2)):
+        assert torch.equal(a, b)
     assert par.shape == (0, 2) and sc.shape == (0, 2)

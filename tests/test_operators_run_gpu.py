@@ -112,3 +112,39 @@ def test_a_round_of_drafting_and_training():
     parent, token, score = dh.beam_select(((x["h"] @ U) @ V).detach().view(2, 2, -1), torch.zeros(2, 2, device=DEV), 6)
     assert ((parent >= 0) & (parent < 2)).all() and ((token >= 0) & (token < cfg.vocab)).all()
     assert (score[:, :-1] >= score[:, 1:]).all()
+
+
+@pytest.mark.parametrize("own_streams", [False, True])
+def test_calls_from_two_threads(own_streams):
+    """Calls that interleave on one stream, or run on two, give what they give alone."""
+    import threading
+    g = torch.Generator().manual_seed(3)
+    z = torch.randn(40, 30001, generator=g).to(DEV).bfloat16()
+    idx = torch.randint(0, 30001, (40, 12), generator=g).int().to(DEV)
+    y, w = torch.randn(40, 12, generator=g).to(DEV), torch.rand(40, generator=g).to(DEV)
+    score = -torch.rand(10, 4, generator=g).to(DEV)
+    beams = z.view(10, 4, 30001)
+    want_step, want_beam = dh.distill_topk_step(z, idx, y, w), dh.beam_select(beams, score, 8)
+    want_loss = dh.distill_topk(z, idx, y)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(calls):
+        stream = torch.cuda.Stream() if own_streams else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            got = [f() for _ in range(30) for f, _ in calls]
+        stream.synchronize()
+        for i, out in enumerate(got):
+            for a, b in zip(out, calls[i % len(calls)][1]):
+                if not torch.equal(a, b):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(calls,)) for calls in (
+        [(lambda: dh.distill_topk_step(z, idx, y, w), want_step), (lambda: dh.beam_select(beams, score, 8), want_beam)],
+        [(lambda: dh.beam_select(beams, score, 8), want_beam), (lambda: dh.distill_topk(z, idx, y), want_loss)])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong

@@ -196,6 +196,11 @@ def test_refusals():
                 lambda: dh.reorder_states(rand((2, 3, 4, 2, 6, 6), torch.float32)[..., ::2, ::3, ::2], idx)):
         with pytest.raises(ValueError):
             bad()
+    leaf = x.clone().requires_grad_(True)
+    with pytest.raises(ValueError, match="autograd"):
+        dh.reorder_states(leaf, idx)
+    with torch.no_grad():
+        assert dh.reorder_states(leaf, idx) is leaf
     with pytest.raises(dh.DhError):  # partly the same memory
         dh.reorder_states(x[:, :, 1:], parents(3, 3, 3), out=x[:, :, :3])
     with pytest.raises(dh.DhError):
