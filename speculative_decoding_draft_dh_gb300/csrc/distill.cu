@@ -139,7 +139,6 @@ __global__ void __launch_bounds__(DG_THREADS) k_distill_grad(DistillArgs a) {
   const int row = blockIdx.x / a.splits, part = blockIdx.x - row * a.splits;
   const int32_t* idx = a.idx + (size_t)row * a.K;
   const float* y = a.teacher + (size_t)row * a.K;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.ld;
   T* out = static_cast<T*>(a.grad) + (size_t)row * a.gld;
@@ -424,7 +423,6 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * DF_WARPS + warp;
   const EntrySmem s(df_smem + warp * (3 * a.K + table), a.K, table);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const RowEntries r = entries_prepare<T, LOSS, GRAD>(a, row < a.N ? row : a.N - 1, s);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= a.N) return;
@@ -463,7 +461,6 @@ __global__ void __launch_bounds__(DS_WARPS * 32 + 32) k_distill_short(DistillArg
   __shared__ float s_any;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
   const EntrySmem s(df_smem, a.K, table);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const T* const z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
   RowEntries r = {};

@@ -1,5 +1,10 @@
 // Internal declarations of the training, search and state operators (row_stats.cu, distill.cu,
 // distill_ring.cu, beam.cu, states.cu).
+//
+// Programmatic dependent launch: the passes over the logits let the next kernel of their call start
+// once they have waited themselves.  The last kernel of a call lets nothing start before it has ended:
+// the rescoring kernels load their hidden rows before their own wait, and a caller may hand them rows
+// that a reordering or a gradient has just written.
 #pragma once
 
 #include "dh_internal.cuh"

@@ -70,7 +70,6 @@ template <int V>
 __global__ void __launch_bounds__(RO_THREADS) k_reorder(ReorderArgs p, uint32_t blocks_per_slice, uint32_t cols,
                                                         uint32_t per_t) {
   using T = typename Unit<V>::T;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Place q = place(p, blocks_per_slice);
   const int len = p.lengths ? min(max(__ldg(p.lengths + q.r), 0), p.T) : p.T;
@@ -102,7 +101,6 @@ __global__ void __launch_bounds__(RO_THREADS) k_reorder_inplace(ReorderArgs p, u
   extern __shared__ __align__(16) unsigned char stage[];
   __shared__ int s_from[DH_MAX_SLOTS], s_to[DH_MAX_SLOTS];
   __shared__ int s_n;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Place q = place(p, blocks_per_slice);
   const int len = p.lengths ? min(max(__ldg(p.lengths + q.r), 0), p.T) : p.T;

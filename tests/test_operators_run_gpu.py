@@ -148,3 +148,51 @@ def test_calls_from_two_threads(own_streams):
         t.join()
     torch.cuda.synchronize()
     assert not wrong
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rescoring_of_states_that_just_moved(in_place):
+    """The hidden rows that a reordering writes last, rescored by the next call on the stream: a kernel
+    that starts under the reordering may not see rows that have not moved yet."""
+    A, B, d, V, K = 2000, 64, 2048, 5000, 16
+    g = torch.Generator(device=DEV).manual_seed(9)
+    states = torch.randn(A, 1, B, d, generator=g, device=DEV).bfloat16()
+    idx = torch.arange(B, dtype=torch.int32, device=DEV).flip(0)[None].contiguous()
+    W = torch.randn(V, d, generator=g, device=DEV).bfloat16()
+    cand = torch.randint(0, V, (B, K), generator=g, device=DEV, dtype=torch.int32)
+    want = dh.exact_rescore(states[-1, 0].flip(0).contiguous(), W, cand)
+    for _ in range(5):
+        out = states.clone() if in_place else torch.zeros_like(states)
+        torch.cuda.synchronize()
+        if in_place:
+            dh.reorder_states(out, idx)
+        else:
+            dh.reorder_states(states, idx, out=out)
+        got = dh.exact_rescore(out[-1, 0], W, cand)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rescoring_of_a_gradient():
+    """The same for rows that a gradient call has just written."""
+    N, d, V, K = 4096, 2048, 5000, 16
+    g = torch.Generator(device=DEV).manual_seed(10)
+    z = torch.randn(N, d, generator=g, device=DEV).bfloat16()
+    idx = torch.randint(0, d, (N, 200), generator=g, device=DEV, dtype=torch.int32)
+    y = torch.randn(N, 200, generator=g, device=DEV)
+    gl = torch.full((N,), 1000.0, device=DEV)
+    W = torch.randn(V, d, generator=g, device=DEV).bfloat16()
+    cand = torch.randint(0, V, (64, K), generator=g, device=DEV, dtype=torch.int32)
+    stats = dh.distill_topk(z, idx, y)[1]
+    for call in (lambda out: dh.distill_topk_step(z, idx, y, gl, grad_out=out)[1],
+                 lambda out: dh.distill_topk_backward(z, idx, y, stats, gl, grad_out=out)):
+        out = torch.zeros_like(z)
+        call(out)
+        torch.cuda.synchronize()
+        want = dh.exact_rescore(out[-64:], W, cand)
+        for _ in range(5):
+            out = torch.zeros_like(z)
+            torch.cuda.synchronize()
+            got = dh.exact_rescore(call(out)[-64:], W, cand)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
