@@ -265,7 +265,8 @@ def test_offsets_beyond_32_bits():
     z = torch.empty(N * ld, dtype=torch.bfloat16, device=DEV).view(N, ld)[:, :V]
     z.copy_(small)
     want = dh.distill_topk_step(small, idx, y, gl)
-    got = dh.distill_topk_step(z, idx, y, gl)
+    out = torch.empty(N * ld, dtype=torch.bfloat16, device=DEV).view(N, ld)[:, :V]
+    got = dh.distill_topk_step(z, idx, y, gl, grad_out=out)
     back = dh.distill_topk_backward(z, idx, y, dh.distill_topk(z, idx, y)[1], gl)
     assert got[1].stride(0) == ld and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert near(back, want[1], small, idx, y, gl)
@@ -441,3 +442,27 @@ def test_teacher_from_the_draft_head():
     assert torch.allclose(loss.double(), ref, rtol=1e-4, atol=1e-4)
     for got, want in ((U.grad, U64.grad), (V.grad, V64.grad)):
         assert (got.double() - want).norm() <= 1e-3 * want.norm()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,ld", [(5000, 5008), (5000, 50003), (40000, 4000001), (1001, 1001)])
+def test_memory_of_the_gradient(V, ld, dtype):
+    """Rows far apart (one position of many) do not make the gradient as large as what they lie in, and
+    its rows still lie like theirs."""
+    N = 6
+    small, idx, y, gl = make(N, V, 8, dtype, seed=53)
+    z = torch.empty(N * ld, dtype=small.dtype, device=DEV).view(N, ld)[:, :V]
+    z.copy_(small)
+    stats = dh.distill_topk(small, idx, y)[1]
+    want = dh.distill_topk_step(small, idx, y, gl)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = dh.distill_topk_step(z, idx, y, gl)[1]
+    back = dh.distill_topk_backward(z, idx, y, stats, gl)
+    torch.cuda.synchronize()
+    size = N * V * z.element_size()
+    # two gradients of at most 9/8 of their rows and 16 bytes each, and small outputs and workspaces
+    assert torch.cuda.max_memory_allocated() - before <= 2 * (size * 9 // 8 + N * 16) + (1 << 16)
+    assert (got.stride(0) - ld) * z.element_size() % 16 == 0 and (back.stride(0) - ld) * z.element_size() % 16 == 0
+    assert near(got, want[1], small, idx, y, gl) and near(back, want[1], small, idx, y, gl)
