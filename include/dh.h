@@ -350,10 +350,11 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
  * logits [N x vocab], `dtype`, rows row_stride elements apart (>= 0; any element alignment); idx
  * int32, teacher fp32 [N x K]; n_valid int32 [N]; grad_loss fp32 [N]; loss_out fp32 [N]; stats fp32
  * [N x 2], 8-byte aligned; grad_out `dtype`, rows grad_stride >= vocab elements apart: all device.
- * grad_out may be the logits themselves (same address and stride); otherwise the two must not
- * overlap.  Elements between the rows are left as they were.  The fastest are rows that start on 16
- * bytes (address and strides), with gradient rows that lie like the logits'.  K <= DH_MAX_K, vocab <=
- * DH_MAX_VOCAB, temperature > 0 with temperature^2 neither overflowing nor underflowing fp32.
+ * grad_out may be the logits themselves (same address and stride); otherwise the memory from the
+ * first row to the last of the two must not overlap.  Elements between the rows are left as they
+ * were.  The fastest are rows that start on 16 bytes (address and strides), with gradient rows that
+ * lie like the logits'.  K <= DH_MAX_K, vocab <= DH_MAX_VOCAB, N <= 2^31 - 256, temperature > 0 with
+ * temperature^2 neither overflowing nor underflowing fp32.
  * Workspaces (0 bytes, then NULL will do, for short rows): 256-byte aligned, need not be zeroed, not
  * shared by calls that overlap in time.  N = 0 is a no-op.  Results repeat bit for bit from call to
  * call; the three calls sum in different orders, so they agree with one another to rounding.
@@ -392,8 +393,9 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
  * logits `dtype`: request r's beam w at logits + r request_stride + w beam_stride (elements, >= 0,
  * any element alignment; 0: shared rows); score fp32, finished int32 [R x W]; parent_out, token_out
  * int32, score_out fp32 [R x M]: device.  W <= DH_MAX_BEAMS, M <= DH_MAX_BEAM_OUT, vocab <=
- * DH_MAX_VOCAB, temperature > 0 and finite.  Workspace: dh_beam_select_workspace bytes, 256-byte
- * aligned, not zeroed, not shared by calls that overlap in time.  R = 0 is a no-op.
+ * DH_MAX_VOCAB, R W <= 2^31 - 256, temperature > 0 with it and 2 / temperature finite in fp32.
+ * Workspace: dh_beam_select_workspace bytes, 256-byte aligned, not zeroed, not shared by calls that
+ * overlap in time.  R = 0 is a no-op.
  * ------------------------------------------------------------------------------------------- */
 #define DH_MAX_BEAMS 128
 #define DH_MAX_BEAM_OUT 256
@@ -418,8 +420,10 @@ int dh_beam_select(const void* logits, int64_t request_stride, int64_t beam_stri
  * In place (dst == src, equal strides and slots): as if every source were read before any target is
  * written.  Otherwise the memory that src and dst span must not overlap.
  * idx int32 [R x M]; lengths, src_base, dst_base int32 [R] or NULL (T, 0, 0): device.  The elements
- * of dst must be distinct.  M <= DH_MAX_SLOTS.  Fastest where addresses, strides and unit_bytes are
- * multiples of 16.  No workspace.  A zero size is a no-op.
+ * of dst must be distinct.  M <= DH_MAX_SLOTS, unit_bytes < 2^31.  The copy's piece is the widest
+ * power of two up to 16 bytes that addresses, strides and unit_bytes are multiples of (16 is the
+ * fastest): H T unit_bytes is at most 2^31 - 256 pieces, and A R times its blocks of 256 pieces below
+ * 2^31.  No workspace.  A zero size is a no-op.
  * ------------------------------------------------------------------------------------------- */
 #define DH_MAX_SLOTS 1024
 int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, const int64_t* dst_strides,

@@ -510,6 +510,9 @@ def _typed(t, name, dtype, shape, index):
         raise ValueError(f"{name} must be contiguous and on CUDA device {index}, not on {t.device}")
 
 
+_INT_MAX = (1 << 31) - 1  # larger sizes would be cut off on their way to the library
+
+
 def _rows(t, name):
     """Checks a [.., vocab] CUDA tensor of logits whose elements of a row are adjacent; its dtype's
     code and its device's index."""
@@ -528,6 +531,8 @@ def _distill_inputs(logits, idx, teacher, n_valid):
     dt, index = _rows(logits, "logits")
     N, vocab = logits.shape
     K = idx.shape[1]
+    if N > _INT_MAX or vocab > _INT_MAX or K > _INT_MAX:
+        raise ValueError("logits and idx: N, vocab and K have to fit 32 bits")
     _typed(idx, "idx", torch.int32, (N, K), index)
     _typed(teacher, "teacher", torch.float32, (N, K), index)
     if n_valid is not None:
@@ -646,6 +651,9 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     if finished is not None:
         _typed(finished, "finished", torch.int32, (R, W), index)
     M = int(M)
+    pad_token = int(pad_token)
+    if R > _INT_MAX or W > _INT_MAX or vocab > _INT_MAX or abs(M) > _INT_MAX or abs(pad_token) > _INT_MAX:
+        raise ValueError("R, W, vocab, M and pad_token have to fit 32 bits")
     dev = logits.device
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(stream, dev, (logits, score, finished, parent_out, token_out, score_out), lambda: beam_select(
@@ -658,7 +666,7 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
     nbytes = _workspace_bytes("dh_beam_select_workspace", R, W, vocab, dt)
     ws = _scratch(nbytes, workspace, "beam", dev)
     _check(lib.dh_beam_select(logits.data_ptr(), logits.stride(0), logits.stride(1), score.data_ptr(), _addr(finished),
-                              R, W, vocab, M, dt, float(temperature), int(pad_token), parent.data_ptr(),
+                              R, W, vocab, M, dt, float(temperature), pad_token, parent.data_ptr(),
                               token.data_ptr(), best.data_ptr(), _addr(ws), nbytes, _raw_stream(index)),
            "dh_beam_select")
     return parent, token, best
@@ -715,6 +723,8 @@ def _reorder_plan(shape, stride, out_shape, out_stride, size, request_dim, slot_
         raise ValueError("states: more than two separate dimensions besides requests, slots, positions and the "
                          "contiguous part; make the inner ones contiguous")
     (A, sa, da), (H, sh, dh) = [(1, 0, 0)] * (2 - len(outer)) + outer
+    if max(A, H, T, shape[request_dim], shape[slot_dim], out_shape[out_slot_dim]) > _INT_MAX:
+        raise ValueError("states: a dimension, or dimensions that lie together, of 2^31 elements or more")
     ss = (ctypes.c_int64 * 5)(sa, stride[request_dim] * size, stride[slot_dim] * size, sh, ts)
     ds = (ctypes.c_int64 * 5)(da, out_stride[request_dim] * size, out_stride[out_slot_dim] * size, dh, td)
     return A, shape[request_dim], shape[slot_dim], out_shape[out_slot_dim], H, T, unit, ss, ds
@@ -736,8 +746,8 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     dst = states if out is None else out
     if not states.is_cuda:
         raise ValueError("states must be a CUDA tensor")
-    if dst.dtype != states.dtype:
-        raise ValueError("out must have the dtype of states")
+    if dst.dtype != states.dtype or dst.is_conj() != states.is_conj() or dst.is_neg() != states.is_neg():
+        raise ValueError("out must have the dtype of states (and be a conjugate or negated view only if they are)")
     if (states.requires_grad or dst.requires_grad) and torch.is_grad_enabled():
         raise ValueError("states are moved outside of autograd: detach them, or call under torch.no_grad()")
     if (lengths is None) != (length_dim is None):
@@ -748,6 +758,8 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     if idx.dim() != 2:
         raise ValueError("idx must be [R, M]")
     M = idx.shape[1]
+    if M > _INT_MAX:
+        raise ValueError("idx: M has to fit 32 bits")
     index = states.get_device()
     _typed(idx, "idx", torch.int32, (R, M), index)
     for t, name in ((lengths, "lengths"), (src_base, "src_base"), (dst_base, "dst_base")):

@@ -636,9 +636,13 @@ int dh_prof_read(char* names, int name_len, double* total_ms, int* launches, int
 namespace {
 
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
-bool good_temperature(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(1.f / t); }
+// 2 / t bounds the log2(e) / t of the exponents
+bool good_temperature(float t) { return t > 0.f && std::isfinite(t) && std::isfinite(2.f / t); }
 // the losses are scaled by its square
 bool good_square(float t) { return good_temperature(t) && std::isnormal(t * t); }
+
+// Rows of a call: their numbers, rounded up to a block's, stay below 2^31.
+constexpr int MAX_ROWS = 0x7FFFFF00;
 
 // Bytes of the segment statistics of `rows` rows.
 size_t seg_bytes(long long rows, int vocab, int dtype) {
@@ -660,7 +664,7 @@ int check_distill(const void* logits, int64_t row_stride, const int32_t* idx, co
                   int K, int dtype, float temperature) {
   if (N < 0 || vocab <= 0 || K < 1 || K > DH_MAX_K || row_stride < 0) return DH_ERR_INVALID_ARG;
   if (!good_square(temperature)) return DH_ERR_INVALID_ARG;
-  if (!valid_dtype(dtype) || vocab > DH_MAX_VOCAB) return DH_ERR_UNSUPPORTED;
+  if (!valid_dtype(dtype) || vocab > DH_MAX_VOCAB || N > MAX_ROWS) return DH_ERR_UNSUPPORTED;
   if (N == 0) return DH_OK;
   if (!logits || !idx || !teacher) return DH_ERR_INVALID_ARG;
   if (!aligned_to(logits, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
@@ -826,7 +830,7 @@ int dh_beam_select(const void* logits, int64_t request_stride, int64_t beam_stri
   if (!valid_dtype(dtype) || W > DH_MAX_BEAMS || M > DH_MAX_BEAM_OUT || vocab > DH_MAX_VOCAB) return DH_ERR_UNSUPPORTED;
   if (R == 0) return DH_OK;
   if (!logits || !score || !parent_out || !token_out || !score_out) return DH_ERR_INVALID_ARG;
-  if (!aligned_to(logits, elem_bytes(dtype)) || (long long)R * W > 0x7FFFFFFFLL) return DH_ERR_UNSUPPORTED;
+  if (!aligned_to(logits, elem_bytes(dtype)) || (long long)R * W > MAX_ROWS) return DH_ERR_UNSUPPORTED;
   if (!workspace || !aligned256(workspace) || ws_bytes < dh_beam_select_workspace(R, W, vocab, dtype))
     return DH_ERR_WORKSPACE;
   Ctx c;
@@ -886,7 +890,7 @@ int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, co
   a.H = H;
   a.T = T;
   a.unit = unit_bytes;
-  if (unit_bytes > 0x7FFFFFFFLL || (long long)H * T > 0x7FFFFFFFLL / unit_bytes * 16 ||
+  if (unit_bytes > 0x7FFFFFFFLL || (double)H * T * (double)unit_bytes > 16.0 * 0x7FFFFFFFLL ||
       reorder_columns(a) > 0x7FFFFF00LL || (double)A * R * (double)reorder_columns(a) > 256.0 * 0x7FFFFFFFLL ||
       reorder_blocks(a) > 0x7FFFFFFFLL)
     return DH_ERR_UNSUPPORTED;

@@ -294,7 +294,8 @@ __device__ __forceinline__ Sum2 log_sum(float hi, float lo) {
   const float q = t * t;
   const float r = q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.f / 11.f, 1.f / 9.f), 1.f / 7.f), 1.f / 5.f), 1.f / 3.f);
   Sum2 s;
-  s.add((float)k * 0.693359375f);  // log 2 in a part of ten bits, whose product is exact, and the rest
+  // log 2 as 355/512, whose product with k is exact, and the rest (the split of Cody and Waite)
+  s.add((float)k * 0.693359375f);
   s.add(2.f * t);
   s.lo += (float)k * -2.12194440e-4f + 2.f * (tl + t * r);
   return s;

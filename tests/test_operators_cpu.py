@@ -147,3 +147,52 @@ def test_copy_dimensions():
 def test_public_names(name):
     import speculative_decoding_draft_dh_gb300 as pkg
     assert callable(getattr(pkg, name))
+
+
+def test_largest_sizes_and_smallest_temperatures(lib):
+    """Row numbers that would leave 32 bits, and temperatures whose exponents' factor would overflow."""
+    for which in ("loss", "backward", "step"):
+        assert distill_call(lib, which, N=(1 << 31) - 1, V=1, ld=1, gld=1, K=1, grad=1 << 45) == UNSUPPORTED
+    beam = lambda R, W, T: lib.dh_beam_select(  # noqa: E731
+        P(FAKE), 1, 1, P(FAKE), None, R, W, 1, 1, binding.F32, F(T), 0, P(FAKE), P(FAKE), P(FAKE), P(FAKE * 16), 15,
+        None)
+    assert beam((1 << 31) - 1, 1, 1.0) == UNSUPPORTED and beam(1 << 24, 128, 1.0) == UNSUPPORTED
+    assert beam(1, 1, 3e-39) == INVALID and beam(1, 1, 1e-38) == WORKSPACE
+
+
+def test_binding_refuses_sizes_beyond_32_bits():
+    n = (1 << 31) + 5
+    plan = binding._reorder_plan.__wrapped__
+    with pytest.raises(ValueError, match="2\\^31"):  # positions
+        plan((2, 1, 2, n, 4), (2 * n * 8, 2 * n * 8, n * 8, 8, 1), (2, 1, 2, n, 4), (2 * n * 8, 2 * n * 8, n * 8, 8, 1),
+             2, 1, 2, 2, 3)
+    with pytest.raises(ValueError, match="2\\^31"):  # dimensions that lie together
+        plan((1, 1, 2, 1 << 16, 1 << 16, 4), (1 << 36, 1 << 36, 1 << 35, 1 << 19, 8, 1), (1, 1, 2, 1 << 16, 1 << 16, 4),
+             (1 << 36, 1 << 36, 1 << 35, 1 << 19, 8, 1), 2, 1, 2, 2, None)
+
+    class Rows:  # what the check looks at of a tensor of logits that no memory here would hold
+        dtype, device = torch.float32, torch.device("cuda", 0)
+
+        def __init__(self, *shape):
+            self.shape = torch.Size(shape)
+
+        def dim(self):
+            return len(self.shape)
+
+        def get_device(self):
+            return 0
+
+        def stride(self, d):
+            return 1
+
+    with pytest.raises(ValueError, match="32 bits"):
+        binding._distill_inputs(Rows(n, 1), Rows(n, 1), None, None)
+    score = Rows(n, 1)
+    score.is_contiguous = lambda: True
+    with pytest.raises(ValueError, match="32 bits"):
+        binding.beam_select(Rows(n, 1, 4), score, 1)
+    score = Rows(1, 1)
+    score.is_contiguous = lambda: True
+    for m, pad in ((1 << 33, 0), (1, 1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            binding.beam_select(Rows(1, 1, 4), score, m, pad_token=pad)

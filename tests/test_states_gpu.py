@@ -205,3 +205,15 @@ def test_refusals():
         dh.reorder_states(x[:, :, 1:], parents(3, 3, 3), out=x[:, :, :3])
     with pytest.raises(dh.DhError):
         dh.reorder_states(x, torch.zeros(3, 1025, dtype=torch.int32, device=DEV))
+
+
+def test_conjugate_views():
+    """A conjugate view holds other bits than it shows: it moves among such views alone."""
+    x = torch.randn(1, 1, 3, 4, dtype=torch.complex64, device=DEV)
+    idx = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV)
+    out = torch.empty_like(x)
+    with pytest.raises(ValueError, match="conjugate"):
+        dh.reorder_states(x.conj(), idx, out=out)
+    got = dh.reorder_states(x.conj(), idx, out=out.conj())
+    torch.cuda.synchronize()
+    assert torch.equal(got.resolve_conj(), x.conj().resolve_conj()[:, :, [2, 0, 1]])
