@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(BP_THREADS) k_beam_pick(BeamArgs a) {
   const float2* seg = a.seg + row0 * n_seg;
   const float* score = a.score + row0;
   const int32_t* finished = a.finished ? a.finished + row0 : nullptr;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // 1. the beams: a warp each for the sums, then a lane each for the logarithms (64-bit operations take

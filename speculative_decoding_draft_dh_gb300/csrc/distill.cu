@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(DF_WARPS * 32) k_distill_finish(DistillArgs a,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * DF_WARPS + warp;
   const EntrySmem s(df_smem + warp * (3 * a.K + table), a.K, table);
+  if (!GRAD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const RowEntries r = entries_prepare<T, LOSS, GRAD>(a, row < a.N ? row : a.N - 1, s);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= a.N) return;
@@ -461,6 +462,7 @@ __global__ void __launch_bounds__(DS_WARPS * 32 + 32) k_distill_short(DistillArg
   __shared__ float s_any;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
   const EntrySmem s(df_smem, a.K, table);
+  if (!GRAD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const T* const z = static_cast<const T*>(a.logits) + (long long)row * a.ld;
   RowEntries r = {};

@@ -2,9 +2,10 @@
 // distill_ring.cu, beam.cu, states.cu).
 //
 // Programmatic dependent launch: the passes over the logits let the next kernel of their call start
-// once they have waited themselves.  The last kernel of a call lets nothing start before it has ended:
-// the rescoring kernels load their hidden rows before their own wait, and a caller may hand them rows
-// that a reordering or a gradient has just written.
+// once they have waited themselves, and a call's last kernel lets the next call's start where it writes
+// losses or a selection.  One that writes states or a gradient lets nothing start before it has ended:
+// the rescoring kernels load their hidden rows before their own wait, and those may be rows that a
+// reordering or a gradient has just written.
 #pragma once
 
 #include "dh_internal.cuh"
