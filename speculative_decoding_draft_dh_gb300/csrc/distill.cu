@@ -347,6 +347,7 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
   total = r.total = warp_sum(total);
   const float inv = 1.f / total;
   const bool write = GRAD && r.any && r.g != 0.f;
+  __syncwarp();  // the table is cleared before any lane looks into it (shuffles order no memory)
   float part = 0.f;
   bool twice = false;
   for (int k = lane; r.any && k < nk; k += 32) {
@@ -369,6 +370,7 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
   }
   r.part = LOSS ? warp_sum(part) : 0.f;
   r.twice = __any_sync(0xFFFFFFFFu, twice);
+  __syncwarp();  // entries_write reads the other lanes' ids and p
   return r;
 }
 

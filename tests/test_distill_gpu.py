@@ -466,3 +466,14 @@ def test_memory_of_the_gradient(V, ld, dtype):
     assert torch.cuda.max_memory_allocated() - before <= 2 * (size * 9 // 8 + N * 16) + (1 << 16)
     assert (got.stride(0) - ld) * z.element_size() % 16 == 0 and (back.stride(0) - ld) * z.element_size() % 16 == 0
     assert near(got, want[1], small, idx, y, gl) and near(back, want[1], small, idx, y, gl)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,V,K", [(1300, 500, 33), (300, 33001, 96), (40, 70000, 1024)])
+def test_repeated_ids_of_many_rows(N, V, K, dtype):
+    """Every row's ids repeat in another way: pairs held by one lane, by neighbouring and by far lanes."""
+    z, idx, y, gl = make(N, V, K if K < V else V, dtype, seed=61)
+    g = torch.Generator().manual_seed(67)
+    pick = torch.stack([torch.randint(0, 1 + (n * 7) % K, (K,), generator=g) for n in range(N)]).to(DEV)
+    idx = idx.gather(1, pick).contiguous()
+    check_all(z, idx, y, gl)
