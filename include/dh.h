@@ -358,8 +358,9 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
  * Workspaces (0 bytes, then NULL will do, for short rows): 256-byte aligned, need not be zeroed, not
  * shared by calls that overlap in time.  N = 0 is a no-op.  Results repeat bit for bit from call to
  * call; the three calls sum in different orders, so they agree with one another to rounding.
- * dh_distill_topk_step waits on on-chip barriers; one that gives up leaves NaN losses and raises the
- * workspace's status bit (dh_workspace_status; the word has to be zeroed before the first use).
+ * dh_distill_topk_step waits on on-chip barriers.  Where a wait gives up, the rows that share its
+ * blocks are left with NaN losses (rows without entries apart) and NaN gradients, and the workspace's
+ * status bit is raised (dh_workspace_status; the word has to be zeroed before the first use).
  * ------------------------------------------------------------------------------------------- */
 size_t dh_distill_topk_workspace(int N, int vocab, int dtype);
 int dh_distill_topk(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
@@ -470,6 +471,21 @@ int dh_workspace_status(void* workspace, void* stream, int* status_out);
  * workspace: a zero-filled device buffer of at least 256 bytes, 256-byte aligned.
  * ------------------------------------------------------------------------------------------- */
 int dh_selftest_wait_timeout(int mode, int limit_us, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Self-test of the waits of dh_distill_topk_step (no counterpart on the pages).
+ *
+ * The step of fp32 rows, with its waits limited to limit_us microseconds (1..1000000).  From row `row`
+ * on, the last block of every group that shares a row holds something back, so that a wait gives up:
+ *   mode 0: nothing     1: the copies of its logits     2: a warp's statistics     3: a warp's buffers
+ * The call returns and the CUDA context stays usable.  Rows too short or too long for the one-pass
+ * kernel, and gradients that do not lie like their logits, take the other kernels and hold nothing back.
+ * Arguments as for dh_distill_topk_step; workspace: dh_distill_topk_step_workspace bytes, zero-filled.
+ * ------------------------------------------------------------------------------------------- */
+int dh_selftest_distill_timeout(int mode, int row, int limit_us, const float* logits, int64_t row_stride,
+                                const int32_t* idx, const float* teacher, const float* grad_loss, int N, int vocab,
+                                int K, float temperature, float* loss_out, float* grad_out, int64_t grad_stride,
+                                void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Kernel timing for measurement (no counterpart on the pages).

@@ -30,7 +30,7 @@ EXPORTS = ["dh_status_string", "dh_version", "dh_last_error", "dh_lowrank_topk_w
            "dh_lowrank_topk_shard", "dh_merge_topk", "dh_exact_rescore_shard_workspace", "dh_exact_rescore_shard",
            "dh_combine_softmax",
            "dh_distill_topk_workspace", "dh_distill_topk", "dh_distill_topk_backward",
-           "dh_distill_topk_step_workspace", "dh_distill_topk_step",
+           "dh_distill_topk_step_workspace", "dh_distill_topk_step", "dh_selftest_distill_timeout",
            "dh_beam_select_workspace", "dh_beam_select", "dh_reorder_states"]
 
 MAX_K, MAX_BEAMS, MAX_BEAM_OUT, MAX_SLOTS = 1024, 128, 256, 1024  # DH_MAX_*
@@ -117,6 +117,8 @@ def load_library(path: str | None = None):
         lib.dh_distill_topk_step_workspace.restype = Z
         lib.dh_distill_topk_step.argtypes = [P, L, P, P, P, P, I, I, I, I, F, P, P, L, P, Z, P]
         lib.dh_distill_topk_step.restype = I
+        lib.dh_selftest_distill_timeout.argtypes = [I, I, I, P, L, P, P, P, I, I, I, F, P, P, L, P, Z, P]
+        lib.dh_selftest_distill_timeout.restype = I
         lib.dh_beam_select_workspace.argtypes = [I, I, I, I]
         lib.dh_beam_select_workspace.restype = Z
         lib.dh_beam_select.argtypes = [P, L, L, P, P, I, I, I, I, I, F, I, P, P, P, P, Z, P]
@@ -614,8 +616,9 @@ def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=Non
 def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperature=1.0, loss_out=None, grad_out=None,
                       workspace=None, stream=None):
     """distill_topk and distill_topk_backward in one call, for rows whose weights grad_loss fp32 [N]
-    are known beforehand (dh_distill_topk_step).  grad_out may be the logits themselves.  Returns
-    (loss fp32 [N], gradient)."""
+    are known beforehand (dh_distill_topk_step).  grad_out may be the logits themselves.  A wait of the
+    kernel that gives up shows as NaN losses and gradients, with `workspace` also in workspace_status.
+    Returns (loss fp32 [N], gradient)."""
     lib = load_library()
     dt, index, N, vocab, K = _distill_inputs(logits, idx, teacher, n_valid)
     _typed(grad_loss, "grad_loss", torch.float32, (N,), index)
@@ -803,6 +806,29 @@ def selftest_wait_timeout(limit_us: int = 50000, stream=None) -> int:
     out = ctypes.c_int(0)
     _check(lib.dh_workspace_status(_ptr(ws), _stream(stream), ctypes.byref(out)), "dh_workspace_status")
     return out.value
+
+
+def selftest_distill_timeout(mode, row, limit_us, logits, idx, teacher, grad_loss):
+    """distill_topk_step on fp32 rows with something held back from row `row` on and its waits limited to
+    limit_us (dh_selftest_distill_timeout).  Returns (loss, gradient, status word; expected 1 <<
+    DH_ERR_TIMEOUT where a wait gave up)."""
+    lib = load_library()
+    dt, index, N, vocab, K = _distill_inputs(logits, idx, teacher, None)
+    _typed(grad_loss, "grad_loss", torch.float32, (N,), index)
+    if dt != F32:
+        raise TypeError("the self-test takes fp32 logits")
+    dev = logits.device
+    nbytes = lib.dh_distill_topk_step_workspace(N, vocab, K, dt)
+    loss, grad = torch.empty(N, device=dev), _grad_rows(logits, None, index)
+    ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    _check(lib.dh_selftest_distill_timeout(mode, row, limit_us, logits.data_ptr(), logits.stride(0), idx.data_ptr(),
+                                           teacher.data_ptr(), grad_loss.data_ptr(), N, vocab, K, 1.0, loss.data_ptr(),
+                                           grad.data_ptr(), grad.stride(0), ws.data_ptr(), nbytes, _raw_stream(index)),
+           "dh_selftest_distill_timeout")
+    out = ctypes.c_int(0)
+    _check(lib.dh_workspace_status(_ptr(ws), ctypes.c_void_p(_raw_stream(index)), ctypes.byref(out)),
+           "dh_workspace_status")
+    return loss, grad, out.value
 
 
 def set_tuning(name: str, value: str | None):

@@ -768,10 +768,13 @@ size_t dh_distill_topk_step_workspace(int N, int vocab, int K, int dtype) {
          align_up((size_t)N * K * sizeof(float), 256);
 }
 
-int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
-                         const int32_t* n_valid, const float* grad_loss, int N, int vocab, int K, int dtype,
-                         float temperature, float* loss_out, void* grad_out, int64_t grad_stride, void* workspace,
-                         size_t ws_bytes, void* stream) {
+namespace {
+
+// The step; `test`: through the one-pass kernel's self-test.
+int distill_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                 const int32_t* n_valid, const float* grad_loss, int N, int vocab, int K, int dtype, float temperature,
+                 float* loss_out, void* grad_out, int64_t grad_stride, void* workspace, size_t ws_bytes, void* stream,
+                 const RingTest* test) {
   int st = check_distill(logits, row_stride, idx, teacher, N, vocab, K, dtype, temperature);
   if (st != DH_OK || N == 0) return st;
   if (!loss_out || !grad_loss || !grad_out || (N > 1 && grad_stride < vocab)) return DH_ERR_INVALID_ARG;
@@ -803,7 +806,8 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
       if (note_error(launch_distill_gather(c, b, dtype), "distillation entries") != cudaSuccess) return DH_ERR_CUDA;
     }
     bool done = false;
-    if (note_error(launch_distill_ring(c, b, dtype, &done), "distillation step") != cudaSuccess) return DH_ERR_CUDA;
+    if (note_error(launch_distill_ring(c, b, dtype, &done, test), "distillation step") != cudaSuccess)
+      return DH_ERR_CUDA;
     if (done)
       return note_error(launch_distill_finish(c, b, dtype, true, true), "distillation entries") == cudaSuccess
                  ? DH_OK
@@ -812,6 +816,26 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
   st = run_distill_loss(c, a, dtype, seg);
   if (st != DH_OK) return st;
   return note_error(launch_distill_grad(c, a, dtype), "distillation gradient") == cudaSuccess ? DH_OK : DH_ERR_CUDA;
+}
+
+}  // namespace
+
+int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* idx, const float* teacher,
+                         const int32_t* n_valid, const float* grad_loss, int N, int vocab, int K, int dtype,
+                         float temperature, float* loss_out, void* grad_out, int64_t grad_stride, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  return distill_step(logits, row_stride, idx, teacher, n_valid, grad_loss, N, vocab, K, dtype, temperature, loss_out,
+                      grad_out, grad_stride, workspace, ws_bytes, stream, nullptr);
+}
+
+int dh_selftest_distill_timeout(int mode, int row, int limit_us, const float* logits, int64_t row_stride,
+                                const int32_t* idx, const float* teacher, const float* grad_loss, int N, int vocab,
+                                int K, float temperature, float* loss_out, float* grad_out, int64_t grad_stride,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  if (mode < 0 || mode > 3 || row < 0 || limit_us <= 0 || limit_us > 1000000) return DH_ERR_INVALID_ARG;
+  const RingTest test{mode, row, limit_us};
+  return distill_step(logits, row_stride, idx, teacher, nullptr, grad_loss, N, vocab, K, DH_F32, temperature, loss_out,
+                      grad_out, grad_stride, workspace, ws_bytes, stream, &test);
 }
 
 // ------------------------------------------------------------------ beam selection

@@ -19,6 +19,11 @@
 // pass and 277 for one block per row that reads it twice, the second time from L2.  The consumers'
 // instructions bound it (about nine per logit and lane, and each row's own work per warp): 16 warps
 // 213 us, 24 219, four CTAs per row 256.
+//
+// Every wait has a limit.  A warp whose wait gave up waits no more and hands no slot back, so the
+// producer and those that need its pairs end at their own limits; it walks the rest of its rows with
+// whatever the slots hold (leaving the loop instead costs the kernel a third of its speed: 290 us).  At
+// the end its whole cluster waits for the copies in flight and leaves all of its rows NaN.
 #include "rows.cuh"
 #include "sm100.cuh"
 
@@ -39,6 +44,8 @@ struct RingArgs {
   int slots;    // ring slots
   int spare;    // of them not needed by a row
   bool loose;   // rows may have elements beside their 16-byte grid
+  long long limit;  // cycles after which a wait gives up
+  RingTest test;
 };
 
 __device__ __forceinline__ void st16(void* p, const uint4& v) {
@@ -64,15 +71,6 @@ __device__ __forceinline__ unsigned long long get_word(const unsigned long long*
   asm volatile("ld.relaxed.cluster.shared::cta.b64 %0, [%1];" : "=l"(w) : "r"(sm100::smem_u32(p)) : "memory");
   return w;
 }
-// The wait of sm100::mbar_wait with its limit in SM cycles.
-__device__ __forceinline__ bool wait_cycles(uint64_t* bar, uint32_t parity) {
-  if (sm100::mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
-    if (clock64() - t0 > DR_LIMIT) return false;
-  }
-}
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -93,19 +91,49 @@ __device__ __forceinline__ Slice slice_of(const T* z, int vocab, int part, int l
   return s;
 }
 
+// What a CTA does when a wait of its cluster has given up: it waits for its copies in flight (of slot i
+// the last one was of parity `phase`, or the other one for i < slot) and leaves NaN in its part of the
+// cluster's rows and in their statistics, whatever was written there.
 template <typename T>
+__device__ __noinline__ void abandon(const RingArgs& a, uint64_t* full, int slot, uint32_t phase, int part) {
+  const DistillArgs& d = a.d;
+  if (threadIdx.x == 0 && d.status) atomicOr(d.status, 1 << DH_ERR_TIMEOUT);
+  if ((int)threadIdx.x < a.slots) {
+    const uint32_t parity = (int)threadIdx.x < slot ? phase ^ 1u : phase;
+    const long long t0 = clock64();
+    while (!sm100::mbar_try_wait(&full[threadIdx.x], parity) && clock64() - t0 <= DR_LIMIT) {
+    }
+  }
+  __syncthreads();
+  const T nan = Elem<T>::from_f(NAN);
+  for (long long row = blockIdx.x >> a.lg; row < d.N; row += gridDim.x >> a.lg) {
+    const Slice s = slice_of(static_cast<const T*>(d.logits) + row * d.ld, d.vocab, part, a.lg);
+    T* const out = static_cast<T*>(d.grad) + row * d.gld;
+    const int lo = part == 0 ? 0 : s.pre + s.lo * Elem<T>::PER16, hi = s.pre + s.hi * Elem<T>::PER16;
+    for (int i = lo + (int)threadIdx.x; i < hi; i += DR_THREADS) out[i] = nan;
+    if (part != 0) continue;
+    for (int i = s.behind + (int)threadIdx.x; i < d.vocab; i += DR_THREADS) out[i] = nan;
+    if (threadIdx.x == 0) d.stats_out[row] = make_float2(NAN, NAN);
+  }
+}
+
+// TEST: the form that the self-test runs (RingTest).
+template <typename T, bool TEST>
 __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
   const DistillArgs& d = a.d;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   uint4* const ring = reinterpret_cast<uint4*>(ring_smem);         // [slots][DR_CHUNK]
   __shared__ __align__(16) unsigned long long s_pair[2][DR_MAX_C * DR_WARPS];  // every warp's pair
   __shared__ uint64_t full[DR_MAX_SLOTS], empty[DR_MAX_SLOTS];
+  __shared__ uint32_t s_stop;         // a wait of the cluster has given up
+  __shared__ uint32_t s_last[2];      // the producer's next slot and phase, once it is done
 
   const int lg = a.lg, C = 1 << lg, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cl = blockIdx.x >> lg, part = blockIdx.x & (C - 1), ncl = gridDim.x >> lg;
   const T* const logits = static_cast<const T*>(d.logits);
 
   if (tid == 0) {
+    s_stop = 0;
     for (int i = 0; i < a.slots; ++i) {
       sm100::mbar_init(&full[i], 1);
       sm100::mbar_init(&empty[i], DR_WARPS);
@@ -120,12 +148,22 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   bool failed = false;
-  auto give_up = [&] {
+  // In a wait that started at t0: whether it is to end without what it waits for.
+  auto give_up = [&](long long t0) {
+    if (!failed && clock64() - t0 <= a.limit) return false;
     failed = true;
-    if (d.status) atomicOr(d.status, 1 << DH_ERR_TIMEOUT);
+    *(volatile uint32_t*)&s_stop = 1;
+    return true;
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!failed && !wait_cycles(bar, parity)) give_up();
+    if (failed || sm100::mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!sm100::mbar_try_wait(bar, parity))
+      if (give_up(t0)) return;
+  };
+  // What the self-test holds back, from a row on, in the cluster's last CTA
+  auto held = [&](int what, long long row) {
+    return TEST && a.test.hold == what && part == C - 1 && row >= a.test.row;
   };
 
   if (warp == DR_WARPS) {
@@ -134,6 +172,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
       int slot = 0;
       uint32_t phase = 1;  // the first round finds the slots free
       for (long long row = cl; row < d.N && !failed; row += ncl) {
+        if (held(RingTest::COPIES, row)) break;
         const T* z = logits + row * d.ld;
         const Slice s = slice_of(z, d.vocab, part, lg);
         const uint4* src = reinterpret_cast<const uint4*>(z + s.pre) + s.lo;
@@ -149,9 +188,8 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
           }
         }
       }
-      if (failed)  // no copy is left in flight
-        for (int i = 0; i < a.slots; ++i)
-          for (int k = 0; k < 2; ++k) (void)sm100::mbar_wait(&full[i], k, 10000000ull);
+      s_last[0] = (uint32_t)slot;
+      s_last[1] = phase;
     }
   } else {
     // ---------------------------------------------------------------- consumers
@@ -243,7 +281,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
       s = m == -INFINITY ? 0.f : s * row_ex2((m - wm) * d.c);
       s = warp_sum(s);
       const uint32_t mark = (it >> 1) & 1;
-      if (lane < C) {
+      if (lane < C && !(held(RingTest::PAIRS, row) && warp == 0)) {
         const unsigned long long word = pair_word(wm, s, mark);
         if (C == 1) *reinterpret_cast<volatile unsigned long long*>(&s_pair[par][warp]) = word;
         else put_word(remote_addr(&s_pair[par][part * DR_WARPS + warp], lane), word);
@@ -268,10 +306,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
       s = 0.f;
       for (int i = lane; i < C * DR_WARPS; i += 32) {  // lane by lane in a fixed order
         unsigned long long word = get_word(&s_pair[par][i]);
-        while (((uint32_t)word & 1u) != mark && !failed) {
-          if (clock64() - t0 > DR_LIMIT) give_up();
-          word = get_word(&s_pair[par][i]);
-        }
+        while (((uint32_t)word & 1u) != mark && !give_up(t0)) word = get_word(&s_pair[par][i]);
         const float pm = __uint_as_float((uint32_t)(word >> 32)), ps = __uint_as_float((uint32_t)word & ~1u);
         const float mn = max_nan(m, pm);
         s = (m == -INFINITY ? 0.f : s * row_ex2((m - mn) * d.c)) +
@@ -283,8 +318,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
       const float lm = m;
       m = warp_max(m);
       s = warp_sum(lm == -INFINITY ? 0.f : s * row_ex2((lm - m) * d.c));
-      // a wait that gave up leaves nothing that looks like a result
-      if (part == 0 && tid == 0) d.stats_out[row] = failed ? make_float2(NAN, NAN) : make_float2(m, s);
+      if (part == 0 && tid == 0) d.stats_out[row] = make_float2(m, s);
 
       T* const out = static_cast<T*>(d.grad) + row * d.gld;
       const bool nothing = m == -INFINITY;  // a row of -inf has q = 0
@@ -292,7 +326,7 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
       const float aq = nothing ? 0.f : ref.by_max(g / s, d.c);
       uint4* o = reinterpret_cast<uint4*>(out + sl.pre) + sl.lo + tid;
       auto next_b = [&] {  // the slot is read: it goes back to the producer
-        if (lane == 0) sm100::mbar_arrive(&empty[slot_b]);
+        if (lane == 0 && !failed && !(held(RingTest::SLOTS, row) && warp == 0)) sm100::mbar_arrive(&empty[slot_b]);
         if (++slot_b == a.slots) slot_b = 0;
       };
       v = 0;
@@ -326,13 +360,19 @@ __global__ void __launch_bounds__(DR_THREADS, 1) k_distill_ring(RingArgs a) {
     }
   }
   __syncthreads();
-  if (C > 1) cluster_barrier();  // no CTA leaves while another may still put something into it
+  if (C > 1) {
+    if (*(const volatile uint32_t*)&s_stop != 0 && tid < C)
+      asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(remote_addr(&s_stop, tid)), "r"(1)
+                   : "memory");
+    cluster_barrier();  // no CTA leaves while another may still put something into it
+  }
+  if (*(const volatile uint32_t*)&s_stop != 0) abandon<T>(a, full, (int)s_last[0], s_last[1], part);
 }
 
-template <typename T>
-cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
+template <typename T, bool TEST>
+cudaError_t run(const Ctx& c, const DistillArgs& d, const RingTest* test, bool* done) {
   *done = false;
-  auto* kernel = k_distill_ring<T>;
+  auto* kernel = k_distill_ring<T, TEST>;
   static unsigned long long smem_done = 0;
   cudaError_t e = allow_max_smem(kernel, c.device, &smem_done);
   if (e == cudaSuccess) e = carveout_max_shared((const void*)kernel, c.device);
@@ -343,6 +383,11 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
 
   RingArgs a = {};
   a.d = d;
+  a.limit = DR_LIMIT;
+  if (TEST) {
+    a.test = *test;
+    a.limit = 2000ll * test->limit_us;  // about 2 GHz
+  }
   const int vecs = d.vocab / Elem<T>::PER16;
   // The cut: the fewest CTAs that hold a row with a slot to spare, then more while the rows alone do
   // not fill the SMs.
@@ -397,8 +442,9 @@ cudaError_t run(const Ctx& c, const DistillArgs& d, bool* done) {
 
 }  // namespace
 
-cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done) {
-  return dtype == DH_BF16 ? run<__nv_bfloat16>(c, a, done) : run<float>(c, a, done);
+cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done, const RingTest* test) {
+  if (test) return dtype == DH_F32 ? run<float, true>(c, a, test, done) : cudaErrorInvalidValue;
+  return dtype == DH_BF16 ? run<__nv_bfloat16, false>(c, a, nullptr, done) : run<float, false>(c, a, nullptr, done);
 }
 
 }  // namespace dh

@@ -40,8 +40,14 @@ cudaError_t launch_row_stats(const Ctx& c, const void* logits, long long rs, lon
                              int dtype, float temperature, const float* score, const int32_t* finished, float2* seg);
 // The kernels of distill.cu and distill_ring.cu; which of them a call takes is api.cu's choice.
 // launch_distill_ring: statistics (stats_out) and dense gradient; *done is false, and nothing was
-// launched, where the rows are too long.
-cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done);
+// launched, where the rows are too long.  `test` (fp32 only): what the self-test of its waits holds back
+// in the last CTA of every cluster, from row `row` on, and the waits' limit.
+struct RingTest {
+  enum Hold { NOTHING = 0, COPIES, PAIRS, SLOTS };
+  int hold, row, limit_us;
+};
+cudaError_t launch_distill_ring(const Ctx& c, const DistillArgs& a, int dtype, bool* done,
+                                const RingTest* test = nullptr);
 // Rows for launch_distill_short: distill_short on a device of num_sms SMs; whatever the device (and so
 // without a workspace) if distill_short_always.
 bool distill_short_always(int N, int n_seg, bool step);

@@ -477,3 +477,29 @@ def test_repeated_ids_of_many_rows(N, V, K, dtype):
     pick = torch.stack([torch.randint(0, 1 + (n * 7) % K, (K,), generator=g) for n in range(N)]).to(DEV)
     idx = idx.gather(1, pick).contiguous()
     check_all(z, idx, y, gl)
+
+
+@pytest.mark.parametrize("mode", [1, 2, 3])
+@pytest.mark.parametrize("N,V", [(400, 65540), (333, 40001)])  # rows held by two blocks and by one
+def test_a_wait_that_gives_up_leaves_no_result(N, V, mode):
+    """Something held back from a row on (the copies, a warp's statistics, its buffers): the status bit is
+    raised, every row that shares its blocks is NaN in loss and gradient, the others are as ever, and the
+    next call works."""
+    z, idx, y, gl = make(N, V, 8, "f32", seed=59)
+    gl[:] = 0.5
+    want_l, want_g = dh.distill_topk_step(z, idx, y, gl)
+    loss, grad, status = dh.selftest_distill_timeout(0, 0, 100000, z, idx, y, gl)
+    assert status == 0 and torch.equal(loss, want_l) and torch.equal(grad, want_g)
+    # a block that has no more rows to load waits for no buffer, so those are held back from the start
+    for row in ((0,) if mode == 3 else (0, N - 5)):
+        loss, grad, status = dh.selftest_distill_timeout(mode, row, 3000, z, idx, y, gl)
+        assert status == 1 << 5
+        lost = torch.isnan(loss)
+        assert lost[row:].all() and torch.isnan(grad[lost]).all()
+        assert torch.equal(loss[~lost], want_l[~lost]) and torch.equal(grad[~lost], want_g[~lost])
+        if row:
+            assert lost.sum() <= 5 * (N // 60)  # five groups of blocks, of 76 or 152
+    again = dh.distill_topk_step(z, idx, y, gl)
+    assert torch.equal(again[0], want_l) and torch.equal(again[1], want_g)
+    with pytest.raises(TypeError):
+        dh.selftest_distill_timeout(1, 0, 3000, z.bfloat16(), idx, y, gl)

@@ -196,3 +196,12 @@ def test_binding_refuses_sizes_beyond_32_bits():
     for m, pad in ((1 << 33, 0), (1, 1 << 32)):
         with pytest.raises(ValueError, match="32 bits"):
             binding.beam_select(Rows(1, 1, 4), score, m, pad_token=pad)
+
+
+def test_distill_selftest_rejects_bad_arguments(lib):
+    def call(mode=1, row=0, us=1000, z=FAKE, nbytes=1 << 30):
+        return lib.dh_selftest_distill_timeout(mode, row, us, P(z), 100000, P(FAKE), P(FAKE), P(FAKE), 2, 100000, 8,
+                                               F(1.0), P(FAKE), P(FAKE << 12), 100000, P(FAKE * 16), nbytes, None)
+    assert call(mode=-1) == INVALID and call(mode=4) == INVALID and call(row=-1) == INVALID
+    assert call(us=0) == INVALID and call(us=1000001) == INVALID and call(z=0) == INVALID
+    assert call(nbytes=15) == WORKSPACE
