@@ -21,6 +21,8 @@
 // k_beam_pick is a chain of latencies (128 requests of 16 beams, M = 16: 8 us, of it the combination
 // 1.4, logarithms 0.5, bound 1.5, search of the segments 0.5, elements read again 2, scores and order 2).
 // What runs once is kept out of line: unrolled code has to come from memory first.
+#include <cstddef>
+
 #include "rows.cuh"
 
 namespace dh {
@@ -58,7 +60,7 @@ struct BeamArgs {
 };
 
 struct BeamSmem {
-  unsigned long long key[BP_CAP];
+  alignas(16) unsigned long long key[BP_CAP];
   uint32_t pos[BP_CAP];
   double base[DH_MAX_BEAMS];   // score of the row's largest logit; -inf: no candidates of its own
   float base32[DH_MAX_BEAMS];
@@ -74,6 +76,8 @@ struct BeamSmem {
   uint32_t last_pos;
   int n, n_segs, next;
 };
+// the keys' place is read 16 bytes at a time before they stand there (k_beam_pick, part 2)
+static_assert(alignof(BeamSmem) % 16 == 0 && offsetof(BeamSmem, key) % 16 == 0, "16-byte loads from BeamSmem::key");
 
 // Sum of x over the block.  `turn` alternates between calls, so one barrier per call is enough.
 __device__ __forceinline__ int block_count(BeamSmem& s, int x, int& turn) {
