@@ -388,8 +388,10 @@ int dh_distill_topk_step(const void* logits, int64_t row_stride, const int32_t* 
  * - A beam whose score is not finite (-inf: an unused one) has no candidate, nor has one whose row
  *   holds a NaN or +inf or nothing above -inf, nor a logit of -inf.
  * - Where fewer than M candidates exist the rest is parent -1, token -1, score -inf.
- * Candidates are ordered by their scores in 64 bits (the normalisers' sums carry the error of fp32
- * exponentials, about 1e-8); score_out is the score rounded to fp32.
+ * Candidates are ordered by their scores in 64 bits, with normalisers from fp32 exponentials: a row's
+ * logarithm is off by about 2^-24 (1 + the mean of (max - z)/T under the row's softmax), which is 1e-7 on
+ * rows of random logits (3e-7 the most seen, 2^-18 at the worst).  Candidates of different beams that are
+ * nearer to one another may come in either order.  score_out is the score rounded to fp32.
  *
  * logits `dtype`: request r's beam w at logits + r request_stride + w beam_stride (elements, >= 0,
  * any element alignment; 0: shared rows); score fp32, finished int32 [R x W]; parent_out, token_out

@@ -4,8 +4,8 @@
 // The pass over the logits (row_stats.cu, the step's traffic: HBM-bound) leaves a (max, sum) pair
 // per segment of a row.  k_beam_pick then works from those pairs, one block per request:
 //   1. each beam's normaliser, hence base[w] = score[w] - log sum exp((z - max)/T), in 64 bits: two
-//      candidates of different beams are ordered by it, so its error decides which of two near ones
-//      comes first;
+//      candidates of different beams are ordered by it, so its error (about 1e-7, from the sums' fp32
+//      exponentials) decides which of two near ones comes first;
 //   2. a bound: every thread's best segment maximum is the score of some candidate, so the M-th
 //      largest of them is one that at least M candidates reach.  It only has to be a lower bound, so
 //      it is taken in fp32, each score lowered by more than its rounding;

@@ -16,6 +16,11 @@ namespace {
 
 constexpr int RS_THREADS = 256;
 
+// The factor c = log2(e)/T is one float, so a row's sum has the error of a temperature that is off by
+// 2^-24: up to 1e-7 in its logarithm, as much as the 2^x unit's own (5e-8 on average).  A second
+// multiply-add by the rest of c takes that part away and leaves the unit's: the errors of random rows then
+// are 0 to 7e-8 instead of -8e-8 to 1e-7, for 9 us more at 2048 rows of 151936 bf16 logits.
+
 // Index: unsigned where the items' numbers fit, else long long (a 64-bit division per item costs as much
 // as a third of its logits).
 template <typename T, bool ALIGNED, typename Index>

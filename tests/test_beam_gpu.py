@@ -266,3 +266,31 @@ def test_refusals():
     for a, b in zip(same, dh.beam_select(z, score, 2)):
         assert torch.equal(a, b)
     assert par.shape == (0, 2) and sc.shape == (0, 2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [50257, 151936])
+@pytest.mark.parametrize("std", [0.5, 1.0, 3.0])
+def test_normalisers_at_their_stated_error(std, V, dtype):
+    """The logarithm of a row's sum, by the score of its first token at a score of about its negative.
+
+    With d = (max - z)/T and q the row's probabilities the error is at most, all of one sign, the rounding
+    of log2(e)/T and 1/T to fp32, 2^-24 of the exponent: 2^-24 E_q[d]; the mean error of the 2^x unit,
+    5.1e-8 over a range of exponents of one (1.5e-7 the largest); and, independent of each other, the
+    terms' argument (2^-24 d) and 2^x, and the sums' roundings within a segment: its tree has 2^j additions
+    of weight 2^-j at depth j, so their variance is below two of 2^-24 / sqrt 3.  Those count six
+    deviations.  That is 1e-7 to 4e-7 here; scores are rounded once."""
+    g = torch.Generator().manual_seed(71)
+    z = (std * torch.randn(16, 1, V, generator=g)).to(DT[dtype])
+    for T in (1.0, 0.7, 1.047, 1.27, 0.55, 4.0):
+        d = (z.double().amax(2, keepdim=True) - z.double())[:, 0].numpy() / np.float64(np.float32(T))
+        total = np.exp(-d).sum(1)
+        q = np.exp(-d) / total[:, None]
+        seg = 512 if dtype == "f32" else 1024
+        share = np.add.reduceat(q, np.arange(0, V, seg), axis=1)
+        u = 2.0 ** -24
+        noise = np.sqrt((q * q * ((u * d) ** 2 / 3 + 1.5e-7 ** 2)).sum(1) + (share * share).sum(1) * 2 * u * u / 3)
+        score = torch.from_numpy(np.log(total)).float()
+        _, _, out = dh.beam_select(z.to(DEV), score[:, None].to(DEV), 1, temperature=T)
+        err = out[:, 0].double().cpu().numpy() - (score.double().numpy() - np.log(total))
+        assert (np.abs(err) <= u * (q * d).sum(1) + 5.1e-8 + 6 * noise + u * np.abs(out[:, 0].cpu().numpy())).all(), T

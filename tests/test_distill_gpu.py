@@ -503,3 +503,32 @@ def test_a_wait_that_gives_up_leaves_no_result(N, V, mode):
     assert torch.equal(again[0], want_l) and torch.equal(again[1], want_g)
     with pytest.raises(TypeError):
         dh.selftest_distill_timeout(1, 0, 3000, z.bfloat16(), idx, y, gl)
+
+
+@pytest.mark.parametrize("T", [1.0, 1.27])
+@pytest.mark.parametrize("K", [512, 1024])
+def test_small_losses(K, T):
+    """Losses of a student near its teacher, the difference of two logarithms many times their size: the
+    deviation over 512 rows.  With d = (max - z)/T, a = (max - y)/T and u = 2^-24 a row's error is, always
+    the same way, u (E_q[d] + E_p[a]) by the factors 1/T (log2(e)/T alone at T = 1) and the 2^x unit's
+    mean of 5.1e-8; and at random the roundings of the terms (u d and 1.5e-7 for q; 2 u a and four steps'
+    half, 2^-22 for p), of two sums' trees (variance below two of u / sqrt 3 each) and of the losses'
+    own terms p (a - d).  A quarter more for the deviation of the deviation."""
+    N, u = 512, 2.0 ** -24
+    g = torch.Generator().manual_seed(73)
+    z = 0.3 * torch.randn(N, K, generator=g)
+    y = z + 0.3 * torch.randn(N, K, generator=g)
+    idx = torch.arange(K, dtype=torch.int32).expand(N, K).contiguous()
+    loss, _ = dh.distill_topk(z.to(DEV), idx.to(DEV), y.to(DEV), temperature=T)
+    t = np.float64(np.float32(T))
+    d = (z.double().amax(1, keepdim=True) - z.double()).numpy() / t
+    a = (y.double().amax(1, keepdim=True) - y.double()).numpy() / t
+    q, p = np.exp(-d) / np.exp(-d).sum(1)[:, None], np.exp(-a) / np.exp(-a).sum(1)[:, None]
+    logq, logp = -d - np.log(np.exp(-d).sum(1))[:, None], -a - np.log(np.exp(-a).sum(1))[:, None]
+    want = (p * (logp - logq)).sum(1)
+    f = u if T != 1.0 else abs(float(np.float32(np.log2(np.e))) / np.log2(np.e) - 1)
+    always = f * ((q * d).sum(1) + (p * a).sum(1) * (T != 1.0)) + 5.1e-8
+    var = ((q * q * ((u * d) ** 2 / 3 + 1.5e-7 ** 2)).sum(1) + (p * p * ((2 * u * a) ** 2 / 3 + 2.0 ** -44)).sum(1)
+           + 4 * u * u / 3 + (p * p * (u * (a + d)) ** 2).sum(1) + (u * want) ** 2)
+    err = loss.double().cpu().numpy() / (t * t) - want
+    assert np.sqrt((err ** 2).mean()) <= 1.25 * np.sqrt((always ** 2 + var).mean())
