@@ -463,7 +463,9 @@ def verify_chain(logits, cand_idx, cand_prob, draft_token, u_accept, u_sample, *
 # on its stream: calls on different streams, and graphs captured from them, share nothing.  With an
 # explicit `stream` the results belong to that stream, and the inputs are kept from being reused by
 # the allocator until the stream has passed the call (the caller orders the stream behind whatever
-# wrote the inputs).
+# wrote the inputs).  They are outside of autograd (distill.distill_loss is the differentiable form):
+# results have no graph, whether or not the inputs require grad.  Tensors of the caller's that a call
+# writes count as modified, so that autograd notices where it saved them.
 
 
 # The current stream's handle (torch.cuda.current_stream(index).cuda_stream without the object).
@@ -502,6 +504,16 @@ def _scratch(nbytes, workspace, kind, dev):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+_bump = torch.autograd.graph.increment_version
+
+
+def _written(*tensors):
+    """Raises the version of the caller's tensors (None: not given) that a call has written."""
+    for t in tensors:
+        if t is not None:
+            _bump((t,))
 
 
 def _typed(t, name, dtype, shape, index):
@@ -589,6 +601,8 @@ def distill_topk(logits, idx, teacher, *, n_valid=None, temperature=1.0, loss_ou
     _check(lib.dh_distill_topk(logits.data_ptr(), logits.stride(0), idx.data_ptr(), teacher.data_ptr(), _addr(n_valid),
                                N, vocab, K, dt, float(temperature), loss.data_ptr(), stats.data_ptr(), _addr(ws),
                                nbytes, _raw_stream(index)), "dh_distill_topk")
+    if loss_out is not None or stats_out is not None:
+        _written(loss_out, stats_out)
     return loss, stats
 
 
@@ -610,6 +624,8 @@ def distill_topk_backward(logits, idx, teacher, stats, grad_loss, *, n_valid=Non
                                         _addr(n_valid), stats.data_ptr(), grad_loss.data_ptr(), N, vocab, K, dt,
                                         float(temperature), grad.data_ptr(), grad.stride(0), _raw_stream(index)),
            "dh_distill_topk_backward")
+    if grad_out is not None:
+        _written(grad_out)
     return grad
 
 
@@ -636,6 +652,8 @@ def distill_topk_step(logits, idx, teacher, grad_loss, *, n_valid=None, temperat
                                     _addr(n_valid), grad_loss.data_ptr(), N, vocab, K, dt, float(temperature),
                                     loss.data_ptr(), grad.data_ptr(), grad.stride(0), _addr(ws), nbytes,
                                     _raw_stream(index)), "dh_distill_topk_step")
+    if loss_out is not None or grad_out is not None:
+        _written(loss_out, grad_out)
     return loss, grad
 
 
@@ -672,6 +690,8 @@ def beam_select(logits, score, M, *, finished=None, pad_token=0, temperature=1.0
                               R, W, vocab, M, dt, float(temperature), pad_token, parent.data_ptr(),
                               token.data_ptr(), best.data_ptr(), _addr(ws), nbytes, _raw_stream(index)),
            "dh_beam_select")
+    if parent_out is not None or token_out is not None or score_out is not None:
+        _written(parent_out, token_out, score_out)
     return parent, token, best
 
 
@@ -747,9 +767,11 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     out."""
     lib = load_library()
     dst = states if out is None else out
-    if not states.is_cuda:
+    index = states.get_device()
+    if index < 0:
         raise ValueError("states must be a CUDA tensor")
-    if dst.dtype != states.dtype or dst.is_conj() != states.is_conj() or dst.is_neg() != states.is_neg():
+    if dst is not states and (dst.dtype != states.dtype or dst.is_neg() != states.is_neg()
+                              or (dst.is_complex() and dst.is_conj() != states.is_conj())):
         raise ValueError("out must have the dtype of states (and be a conjugate or negated view only if they are)")
     if (states.requires_grad or dst.requires_grad) and torch.is_grad_enabled():
         raise ValueError("states are moved outside of autograd: detach them, or call under torch.no_grad()")
@@ -763,21 +785,27 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
     M = idx.shape[1]
     if M > _INT_MAX:
         raise ValueError("idx: M has to fit 32 bits")
-    index = states.get_device()
     _typed(idx, "idx", torch.int32, (R, M), index)
-    for t, name in ((lengths, "lengths"), (src_base, "src_base"), (dst_base, "dst_base")):
-        if t is not None:
-            _typed(t, name, torch.int32, (R,), index)
-    if dst.get_device() != index:
+    n = sb = db = None
+    if lengths is not None:
+        _typed(lengths, "lengths", torch.int32, (R,), index)
+        n = lengths.data_ptr()
+    if src_base is not None:
+        _typed(src_base, "src_base", torch.int32, (R,), index)
+        sb = src_base.data_ptr()
+    if dst_base is not None:
+        _typed(dst_base, "dst_base", torch.int32, (R,), index)
+        db = dst_base.data_ptr()
+    if dst is not states and dst.get_device() != index:
         raise ValueError(f"out must be on {states.device}")
     if stream is not None or index != torch.cuda.current_device():
         return _elsewhere(stream, states.device, (states, dst, idx, lengths, src_base, dst_base),
                           lambda: reorder_states(states, idx, out=out, lengths=lengths, length_dim=length_dim,
                                                  src_base=src_base, dst_base=dst_base, request_dim=request_dim,
                                                  slot_dim=slot_dim, out_slot_dim=out_slot_dim))
-    _check(lib.dh_reorder_states(states.data_ptr(), ss, dst.data_ptr(), ds, idx.data_ptr(), _addr(lengths),
-                                 _addr(src_base), _addr(dst_base), A, R, slots, out_slots, M, H, T, unit,
-                                 _raw_stream(index)), "dh_reorder_states")
+    _check(lib.dh_reorder_states(states.data_ptr(), ss, dst.data_ptr(), ds, idx.data_ptr(), n, sb, db, A, R, slots,
+                                 out_slots, M, H, T, unit, _raw_stream(index)), "dh_reorder_states")
+    _bump((dst,))
     return dst
 
 

@@ -196,3 +196,53 @@ def test_rescoring_of_a_gradient():
             got = dh.exact_rescore(call(out)[-64:], W, cand)
             torch.cuda.synchronize()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_memory_that_is_written_counts_as_modified():
+    """Autograd notices that what it saved was overwritten: outputs that the caller gives raise their version."""
+    g = torch.Generator().manual_seed(13)
+    z = torch.randn(4, 5000, generator=g).to(DEV)
+    idx, y = torch.randint(0, 5000, (4, 6), generator=g).int().to(DEV), torch.randn(4, 6, generator=g).to(DEV)
+    w, score = torch.ones(4, device=DEV), torch.zeros(2, 2, device=DEV)
+    parents = torch.tensor([[1, 0], [0, 0], [1, 1], [0, 1]], dtype=torch.int32, device=DEV)
+    loss, stats = dh.distill_topk(z, idx, y)
+    out = dict(loss_out=torch.empty_like(loss), stats_out=torch.empty_like(stats))
+    picks = dict(parent_out=torch.empty(2, 3, dtype=torch.int32, device=DEV),
+                 token_out=torch.empty(2, 3, dtype=torch.int32, device=DEV), score_out=torch.empty(2, 3, device=DEV))
+    grad, moved, side = torch.empty_like(z), torch.zeros(1, 4, 2, 8, device=DEV), torch.cuda.Stream()
+    calls = [(lambda s: dh.distill_topk(z, idx, y, stream=s, **out), list(out.values())),
+             (lambda s: dh.distill_topk_backward(z, idx, y, stats, w, grad_out=grad, stream=s), [grad]),
+             (lambda s: dh.distill_topk_step(z, idx, y, w, loss_out=out["loss_out"], grad_out=grad, stream=s),
+              [out["loss_out"], grad]),
+             (lambda s: dh.beam_select(z.view(2, 2, 5000), score, 3, stream=s, **picks), list(picks.values())),
+             (lambda s: dh.reorder_states(moved, parents, stream=s), [moved]),
+             (lambda s: dh.reorder_states(moved.clone(), parents, out=moved, stream=s), [moved])]
+    for call, written in calls:
+        for stream in (None, side):
+            side.wait_stream(torch.cuda.current_stream())
+            before = [t._version for t in written], z._version
+            call(stream)
+            torch.cuda.current_stream().wait_stream(side)
+            assert all(t._version > v for t, v in zip(written, before[0])) and z._version == before[1]
+
+    # the gradient in the place of logits that a backward pass still needs
+    for call in (lambda t: dh.distill_topk_step(t, idx, y, w, grad_out=t),
+                 lambda t: dh.distill_topk_backward(t, idx, y, stats, w, grad_out=t)):
+        capped = torch.tanh(z.clone().requires_grad_(True))
+        loss = distill.distill_loss(capped, idx, y)
+        call(capped.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.sum().backward()
+    # states that moved under one
+    held = torch.tanh(torch.randn(1, 4, 2, 8, device=DEV).requires_grad_(True))
+    with torch.no_grad():
+        dh.reorder_states(held, parents)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        held.sum().backward()
+    # tensors of inference mode have no version
+    with torch.inference_mode():
+        free = z.clone()
+        want = dh.distill_topk_step(z, idx, y, w)
+    got = dh.distill_topk_step(free, idx, y, w, grad_out=free)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and got[1] is free
