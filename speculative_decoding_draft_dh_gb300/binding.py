@@ -555,16 +555,23 @@ def _distill_inputs(logits, idx, teacher, n_valid):
 
 
 def _grad_rows(logits, grad_out, index):
-    """grad_out checked, or memory for the gradient: rows that lie like those of `logits` on 16 bytes, as
-    far apart as they are where that takes at most an eighth more memory."""
+    """grad_out checked, or memory for the gradient: rows that lie like those of `logits` on 16 bytes, the
+    first one and the distance between them, which is theirs where that takes at most an eighth more memory.
+    Rows that share memory get packed ones."""
     N, vocab = logits.shape
     if grad_out is None:
         ld = logits.stride(0)
         if ld <= vocab or N <= 1:
-            return torch.empty((N, vocab), dtype=logits.dtype, device=logits.device)
-        if ld - vocab > vocab // 8:
+            ld = vocab
+        elif ld - vocab > vocab // 8:
             ld = vocab + (ld - vocab) % (16 // logits.element_size())
-        return torch.empty((N, ld), dtype=logits.dtype, device=logits.device)[:, :vocab]
+        beside = logits.data_ptr() & 15
+        if beside:
+            first = beside // logits.element_size()
+            rows = torch.empty(N * ld + first, dtype=logits.dtype, device=logits.device)[first:].view(N, ld)
+        else:
+            rows = torch.empty((N, ld), dtype=logits.dtype, device=logits.device)
+        return rows if ld == vocab else rows[:, :vocab]
     if grad_out.dtype != logits.dtype or grad_out.shape != logits.shape:
         raise ValueError("grad_out must have the logits' dtype and shape")
     if _rows(grad_out, "grad_out")[1] != index:

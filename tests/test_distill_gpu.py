@@ -532,3 +532,20 @@ def test_small_losses(K, T):
            + 4 * u * u / 3 + (p * p * (u * (a + d)) ** 2).sum(1) + (u * want) ** 2)
     err = loss.double().cpu().numpy() / (t * t) - want
     assert np.sqrt((err ** 2).mean()) <= 1.25 * np.sqrt((always ** 2 + var).mean())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,V,ld,base", [(5, 40001, 40001, 1), (5, 40001, 40004, 3), (1, 40000, 40000, 2),
+                                         (3, 40001, 40001, 0), (4, 1001, 4000001, 5)])
+def test_gradient_lies_like_logits_off_16_bytes(N, V, ld, base, dtype):
+    """Logits that start anywhere (the rows behind the first of an odd vocabulary, a part of wider rows)
+    get a gradient that starts at the same place of 16 bytes, and the results of contiguous ones."""
+    z, idx, y, gl = make(N, V, 8, dtype, seed=79, ld=ld, base=base)
+    got = dh.distill_topk_step(z, idx, y, gl)[1]
+    back = dh.distill_topk_backward(z, idx, y, dh.distill_topk(z, idx, y)[1], gl)
+    torch.cuda.synchronize()
+    for x in (got, back):
+        assert (x.data_ptr() - z.data_ptr()) % 16 == 0
+        assert N == 1 or (x.stride(0) - ld) * x.element_size() % 16 == 0
+        assert x.untyped_storage().nbytes() <= N * (V * 9 // 8 + 8) * x.element_size() + 16
+        assert near(x, dh.distill_topk_step(z.contiguous(), idx, y, gl)[1], z, idx, y, gl)
