@@ -7,8 +7,9 @@
 // maximum, without a running rescale, with one reduction pair per 32 elements of a lane.  The
 // warps stream the (row, segment) items of all rows, so a row longer than a warp's share is split
 // over many SMs and few rows still use the whole card.  64 warps per SM (32 registers) keep enough
-// loads in flight without any in the code: 2048 rows of 151936 bf16 logits, 622 MB, 93 us, 6.7 TB/s;
-// with the next item's loads issued ahead (fewer warps fit) 117, with 32 warps 115.
+// loads in flight without any in the code: 2048 rows of 151936 bf16 logits, 622 MB, 95 us, 6.5 TB/s.  A
+// beam step over them takes 103 us; with the next item's loads issued ahead (48 registers, fewer warps) 110.
+// With 32 warps it takes 121 instead of 105, each step waited for.
 #include "rows.cuh"
 
 namespace dh {

@@ -13,6 +13,10 @@
 //   k_reorder_inplace:  up to 16 moves in registers; more are staged in the block's shared memory,
 //                       as many columns at a time as fit.  Slots that stay where they are cost
 //                       nothing.
+// In place, caches of 1.07 GB, bf16: 8 beams 314 us (223 for the bytes of the slots that move: the loaded
+// slots take 80 registers, with spills), 24 beams, staged, 865 us (256: 128 KB per block, so one block per
+// SM).  With lengths, positions innermost (a transposed cache) are moved one element at a time: 1285 us and
+// 5220; put the positions before the contiguous part.
 #include "operators.cuh"
 
 namespace dh {
