@@ -338,7 +338,7 @@ int dh_verify_chain(const void* logits, const int32_t* cand_idx, const float* ca
  * Sums, exponents and loss in fp32; the gradient is rounded once to `dtype`.
  * - A row without entries (or with none above -inf) has loss 0 and gradient 0.  A row with
  *   grad_loss 0 has gradient 0.  Neither kind's gradient depends on its logits, NaN or not.
- * - A student logit of -inf has q = 0; where the teacher's p is positive there the loss is +inf and
+ * - A student logit of -inf has q = 0; where the teacher's p is positive in fp32 there the loss is +inf and
  *   the gradient grad_loss T (-p).  A row of -inf: stats (-inf, 0), q = 0 everywhere.
  * - A NaN or +inf student logit, or a NaN or +inf teacher entry, makes that row's loss and gradient
  *   NaN; other rows are not affected.

@@ -275,6 +275,7 @@ struct RowEntries {
   float g;       // grad_loss T
   float total;   // NaN if an entry is
   float part;    // sum_k p_k ((y_k - top)/T - (z_k - zref)/T)
+  float pa, pz;  // where that has no finite value: sum_k p_k (y_k - top)/T and sum_k p_k (zref - z_k)
   float zref;    // one of the entries' logits
 };
 
@@ -368,7 +369,21 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
       }
     }
   }
-  r.part = LOSS ? warp_sum(part) : 0.f;
+  r.part = r.pa = LOSS ? warp_sum(part) : 0.f;
+  r.pz = 0.f;
+  if (LOSS && !(fabsf(r.part) < INFINITY)) {
+    // -inf at an entry, or a logit near the type's lowest value, whose quotient by T overflows: the two
+    // sums apart, the logits' before it is divided
+    float pa = 0.f, pz = 0.f;
+    for (int k = lane; k < nk; k += 32) {
+      const float p = s.p[k];
+      if (s.id[k] < 0 || p == 0.f) continue;
+      pa += p * ((__ldg(a.teacher + e0 + k) - top) * a.inv_t);
+      pz += p * (r.zref - s.z[k]);
+    }
+    r.pa = warp_sum(pa);
+    r.pz = warp_sum(pz);
+  }
   r.twice = __any_sync(0xFFFFFFFFu, twice);
   __syncwarp();  // entries_write reads the other lanes' ids and p
   return r;
@@ -383,9 +398,11 @@ __device__ __forceinline__ float entries_loss(const DistillArgs& a, const RowEnt
   if (m == -INFINITY) return INFINITY;
   if (!(fabsf(m) < INFINITY) || !(sum < INFINITY)) return NAN;  // a NaN or +inf in the row
   const float x = (m - r.zref) * a.inv_t;
-  if (!(fabsf(r.part + x) < INFINITY)) return r.part + x;  // an entry's q is 0: infinite
   Sum2 l = log_sum(sum, 0.f);
   const Sum2 t = log_sum(r.total, 0.f);
+  if (!(fabsf(r.part + x) < INFINITY))  // infinite where an entry's q is 0
+    return a.temperature * a.temperature * (r.pa + ((l.hi - t.hi) + (l.lo - t.lo))) +
+           a.temperature * (r.pz + (m - r.zref));
   l.add(-t.hi);
   l.add(x);
   l.add(r.part);

@@ -549,3 +549,30 @@ def test_gradient_lies_like_logits_off_16_bytes(N, V, ld, base, dtype):
         assert N == 1 or (x.stride(0) - ld) * x.element_size() % 16 == 0
         assert x.untyped_storage().nbytes() <= N * (V * 9 // 8 + 8) * x.element_size() + 16
         assert near(x, dh.distill_topk_step(z.contiguous(), idx, y, gl)[1], z, idx, y, gl)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [900, 70001])
+@pytest.mark.parametrize("T", [0.1, 0.5, 0.8])
+def test_entries_at_the_lowest_value_below_one(T, V, dtype):
+    """Logits masked by the type's lowest value at the teacher's entries, divided by a temperature below
+    one: the quotient has no fp32, the loss (T^2 times it) has one, and a share near nothing leaves little."""
+    N, K = 6, 24
+    z, idx, y, gl = make(N, V, K, dtype, seed=83)
+    low = torch.finfo(DT[dtype]).min
+    col = lambda n, k: (n, idx[n, k].long())  # noqa: E731
+    z[col(0, 0)] = low                         # the likeliest entry
+    y[1, 5] = y[1].max() - 90.0 * T            # a share of e^-90
+    z[col(1, 5)] = low
+    z[2, idx[2].long()] = low                  # all entries
+    z[3] = low                                 # the whole row: q is flat
+    y[4, 5:] = -float("inf")                   # entries without a share, and an unlikely one
+    z[4, idx[4, 5:].long()] = low
+    y[4, 4] = y[4].max() - 40.0 * T
+    z[col(4, 4)] = low
+    ref = reference(z, idx, y, float(np.float32(T)))[0]
+    assert np.isfinite(ref).all() and (ref < 3.4e38).all() and ref[0] > 1e36 and ref[1] < 100
+    loss, grad = check_all(z, idx, y, gl, T=float(np.float32(T)))
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    z[col(0, 0)] = -float("inf")
+    assert torch.isinf(dh.distill_topk(z, idx, y, temperature=T)[0][0])
