@@ -275,7 +275,7 @@ struct RowEntries {
   float g;       // grad_loss T
   float total;   // NaN if an entry is
   float part;    // sum_k p_k ((y_k - top)/T - (z_k - zref)/T)
-  float pa, pz;  // where that has no finite value: sum_k p_k (y_k - top)/T and sum_k p_k (zref - z_k)
+  float pa, pz;  // where that has no finite value: sum_k p_k (y_k - top)/T and sum_k p_k (zref - z_k)/4
   float zref;    // one of the entries' logits
 };
 
@@ -373,13 +373,15 @@ __device__ __forceinline__ RowEntries entries_prepare(const DistillArgs& a, int 
   r.pz = 0.f;
   if (LOSS && !(fabsf(r.part) < INFINITY)) {
     // -inf at an entry, or a logit near the type's lowest value, whose quotient by T overflows: the two
-    // sums apart, the logits' before it is divided
+    // sums apart, the logits' before it is divided (a quarter of it: the shares may add up to more than 1).
+    // A share below fp32's normal numbers counts there, so it is taken as a square of exp(a / 2)
     float pa = 0.f, pz = 0.f;
     for (int k = lane; k < nk; k += 32) {
       const float p = s.p[k];
       if (s.id[k] < 0 || p == 0.f) continue;
-      pa += p * ((__ldg(a.teacher + e0 + k) - top) * a.inv_t);
-      pz += p * (r.zref - s.z[k]);
+      const float ak = (__ldg(a.teacher + e0 + k) - top) * a.inv_t, half = expf(0.5f * ak);
+      pa += p * ak;
+      pz += half * inv * (half * (0.25f * r.zref - 0.25f * s.z[k]));
     }
     r.pa = warp_sum(pa);
     r.pz = warp_sum(pz);
@@ -402,7 +404,7 @@ __device__ __forceinline__ float entries_loss(const DistillArgs& a, const RowEnt
   const Sum2 t = log_sum(r.total, 0.f);
   if (!(fabsf(r.part + x) < INFINITY))  // infinite where an entry's q is 0
     return a.temperature * a.temperature * (r.pa + ((l.hi - t.hi) + (l.lo - t.lo))) +
-           a.temperature * (r.pz + (m - r.zref));
+           4.f * a.temperature * (r.pz + (0.25f * m - 0.25f * r.zref));
   l.add(-t.hi);
   l.add(x);
   l.add(r.part);

@@ -576,3 +576,21 @@ def test_entries_at_the_lowest_value_below_one(T, V, dtype):
     assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
     z[col(0, 0)] = -float("inf")
     assert torch.isinf(dh.distill_topk(z, idx, y, temperature=T)[0][0])
+
+
+def test_entries_at_the_lowest_value_at_their_limits():
+    """Shares that round up, at losses next to the largest fp32, and shares below the normal numbers."""
+    low = torch.finfo(torch.float32).min
+    for seed, N, V, K, T in ((89, 200, 197, 140, 0.1), (97, 60, 1290, 7, 0.1), (101, 60, 9000, 40, 0.25)):
+        z, idx, y, gl = make(N, V, K, "f32", seed=seed)
+        n = torch.arange(N, device=DEV)
+        best = y.argmax(dim=1)
+        z[n[::2], idx[n[::2], best[::2]].long()] = low           # the whole share of some rows, nearly
+        for m in range(1, N, 2):                                  # e^-88 to e^-103 in the others
+            k = int((best[m] + 1) % K)
+            y[m, k] = y[m, best[m]] - (88.0 + 15.0 * m / N) * T
+            z[m, idx[m, k].long()] = low
+        t = float(np.float32(T))
+        assert (reference(z, idx, y, t)[0] < 3.4e38).all()
+        loss, _ = check_all(z, idx, y, gl, T=t)
+        assert torch.isfinite(loss).all()
