@@ -853,6 +853,9 @@ def selftest_distill_timeout(mode, row, limit_us, logits, idx, teacher, grad_los
     if dt != F32:
         raise TypeError("the self-test takes fp32 logits")
     dev = logits.device
+    if index != torch.cuda.current_device():
+        return _elsewhere(None, dev, (), lambda: selftest_distill_timeout(mode, row, limit_us, logits, idx, teacher,
+                                                                          grad_loss))
     nbytes = lib.dh_distill_topk_step_workspace(N, vocab, K, dt)
     loss, grad = torch.empty(N, device=dev), _grad_rows(logits, None, index)
     ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
