@@ -435,6 +435,104 @@ int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, co
                       void* stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Sampling one token per row of logits.
+ *
+ * EAGLE-4 summary page, section "Distribution preservation has algorithmic and implementation
+ * conditions": at positive temperature a drafter draws its tokens, and verification needs the
+ * probability with which each was drawn.  dh_verify_chain draws from a target's whole distribution;
+ * this call draws with the filters that a serving request sets.  Row n has logits z[0..vocab), its
+ * tokens ordered by (z desc, id asc), and w_i = exp((z_i - z_0) / T):
+ *   top-k   the first top_k tokens (0, or vocab and more: all); M = their sum of w
+ *   top-p   of those the first ones, up to and with the one at which the running sum reaches top_p M
+ *           (at least one; 1: all)
+ *   min-p   of those the ones with w >= min_p (0: all)
+ * The kept tokens are a prefix of the order; with K their mass,
+ *   token_out[n] = the first token at which the running sum exceeds u[n] K
+ *   prob_out[n]  = its w / K, the probability with which it is drawn
+ * T = 0 takes the first token, with probability 1.  The same inputs give the same token.
+ * - Weights are fixed-point numbers whose sums are exact: a running sum is off by about 2^-30 of
+ *   itself, and weights below about 2^-41 (2^-44 for a vocabulary of up to 2^18) of the largest
+ *   count as 0.
+ * - A logit of -inf is never drawn.  A row with a NaN or +inf logit, or with nothing above -inf, has
+ *   token -1 and probability 0; so has one whose temperature is not finite and >= 0 or whose u, top_p
+ *   or min_p is NaN.  Other settings beyond their range count as the nearest end of it.
+ *
+ * temperature, top_p, min_p fp32, top_k int32 [N]: device; NULL: the value *_all for every row, which
+ * is checked on the host (temperature_all finite and >= 0, top_k_all >= 0, top_p_all and min_p_all in
+ * [0, 1]).  logits `dtype`, rows row_stride elements apart (>= 0; any element alignment); u fp32 [N];
+ * token_out int32 [N], prob_out fp32 [N] (may be NULL): device.  vocab <= DH_MAX_VOCAB,
+ * N <= 2^31 - 256.  Workspace: dh_sample_workspace bytes (0: NULL will do), 256-byte aligned, need not
+ * be zeroed, not shared by calls that overlap in time.  N = 0 is a no-op.
+ * ------------------------------------------------------------------------------------------- */
+size_t dh_sample_workspace(int N, int vocab, int dtype);
+int dh_sample(const void* logits, int64_t row_stride, const float* u, const float* temperature, const int32_t* top_k,
+              const float* top_p, const float* min_p, float temperature_all, int top_k_all, float top_p_all,
+              float min_p_all, int N, int vocab, int dtype, int32_t* token_out, float* prob_out, void* workspace,
+              size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Embedding of the drafted tokens, and the table's gradient.
+ *
+ * AlphaSignal page, section "Runtime-sized speculation" (the draft extends its own state token by
+ * token): a drafted token enters the drafter as a row of a table.
+ *   out[n,:]        = scale table[tokens[n],:]
+ *   grad_table[v,:] = scale sum over the n with tokens[n] = v of grad_out[n,:]
+ * each rounded once to `dtype`.  A token outside [0, vocab) (padding) has a row of zeros and no
+ * gradient.  The gradient's sums are fp32, in the order of n in groups that depend on the sorted
+ * tokens, so they repeat bit for bit.  accumulate = 1: the gradient is added to grad_table, whose
+ * rows without a token stay as they were; 0: every row is written.
+ *
+ * tokens int32 [N]; rows of d elements, *_stride elements apart (any element alignment; rows read
+ * may overlap or be one, stride 0; rows written may not: stride >= d): all device.  What is written
+ * must not overlap what is read.  The fastest are rows of whole 16-byte vectors that start on 16
+ * bytes.  d <= DH_MAX_WIDTH, vocab <= DH_MAX_VOCAB, N <= DH_MAX_TOKENS.
+ * Workspace: dh_embed_backward_workspace bytes, 256-byte aligned, need not be zeroed, not shared by
+ * calls that overlap in time.  N = 0 writes nothing, or the gradient's zeros where accumulate = 0.
+ * ------------------------------------------------------------------------------------------- */
+#define DH_MAX_WIDTH 65536
+#define DH_MAX_TOKENS (1 << 24)
+int dh_embed(const void* table, int64_t table_stride, const int32_t* tokens, int N, int vocab, int d, int dtype,
+             float scale, void* out, int64_t out_stride, void* stream);
+size_t dh_embed_backward_workspace(int N, int vocab, int d, int dtype);
+int dh_embed_backward(const void* grad_out, int64_t grad_stride, const int32_t* tokens, int N, int vocab, int d,
+                      int dtype, float scale, int accumulate, void* grad_table, int64_t table_stride, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Layer norm of the hidden rows that the head takes, and its gradients.
+ *
+ * The pages leave the drafter's body open; a norm ahead of the head (h of dh_draft_head) is what
+ * such bodies end with.  For a row x of d elements, with var the mean of (x - mean)^2:
+ *   y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(var + eps)
+ *   stats = (mean, rstd)
+ * and with xhat = (x - mean) rstd, h = grad_out weight:
+ *   grad_x = rstd (h - mean(h) - xhat mean(h xhat))
+ *   grad_weight = sum over the rows of grad_out xhat,   grad_bias = sum over the rows of grad_out
+ * Sums, statistics and products in fp32, each result rounded once to its type.  weight, bias: [d] of
+ * param_dtype (DH_F32, or `dtype`), NULL for 1 and 0.  Infinite or NaN elements make their row NaN,
+ * and the sums of the gradients that it enters; other rows are not affected.
+ *
+ * dh_layer_norm: stats_out fp32 [N x 2] (may be NULL).  y may be x itself (same address and stride).
+ * dh_layer_norm_backward: from the stats of a forward call on the same x.  grad_x, grad_weight,
+ * grad_bias (param_dtype): each may be NULL.  grad_x may be x or grad_out itself.  N = 0 writes the
+ * zeros of grad_weight and grad_bias.
+ * Rows *_stride elements apart (any element alignment; rows read may overlap, rows written may not:
+ * stride >= d); stats 8-byte aligned: all device.  Apart from the cases above what is written must
+ * not overlap what is read.  The fastest are rows of whole 16-byte vectors that start on 16 bytes, of
+ * up to 8192 elements.  d <= DH_MAX_WIDTH, N <= 2^31 - 256, eps finite and >= 0.
+ * Workspace (where grad_weight or grad_bias is wanted): dh_layer_norm_backward_workspace bytes,
+ * 256-byte aligned, need not be zeroed, not shared by calls that overlap in time.  Results repeat bit
+ * for bit on one kind of device.
+ * ------------------------------------------------------------------------------------------- */
+int dh_layer_norm(const void* x, int64_t row_stride, const void* weight, const void* bias, int N, int d, int dtype,
+                  int param_dtype, float eps, void* y, int64_t y_stride, float* stats_out, void* stream);
+size_t dh_layer_norm_backward_workspace(int N, int d, int dtype);
+int dh_layer_norm_backward(const void* grad_out, int64_t grad_stride, const void* x, int64_t row_stride,
+                           const float* stats, const void* weight, int N, int d, int dtype, int param_dtype,
+                           void* grad_x, int64_t grad_x_stride, void* grad_weight, void* grad_bias, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Greedy draft-tree acceptance without a caller-provided workspace (no counterpart on the pages:
  * it is an interface for callers, not part of the method).
  *

@@ -9,10 +9,14 @@ __version__ = "1.0.0"
 def __getattr__(name):
     if name in ("lowrank_topk", "exact_rescore", "tree_accept", "prof_enable", "prof_read",
                 "load_library", "DhError", "Workspace", "distill_topk", "distill_topk_backward", "distill_topk_step",
-                "beam_select", "reorder_states"):
+                "beam_select", "reorder_states", "sample", "embed", "embed_backward", "layer_norm",
+                "layer_norm_backward"):
         from . import binding
         return getattr(binding, name)
     if name == "distill_loss":
         from . import distill
         return distill.distill_loss
+    if name == "embedding":
+        from . import layers
+        return layers.embedding
     raise AttributeError(name)

@@ -31,7 +31,9 @@ EXPORTS = ["dh_status_string", "dh_version", "dh_last_error", "dh_lowrank_topk_w
            "dh_combine_softmax",
            "dh_distill_topk_workspace", "dh_distill_topk", "dh_distill_topk_backward",
            "dh_distill_topk_step_workspace", "dh_distill_topk_step", "dh_selftest_distill_timeout",
-           "dh_beam_select_workspace", "dh_beam_select", "dh_reorder_states"]
+           "dh_beam_select_workspace", "dh_beam_select", "dh_reorder_states",
+           "dh_sample_workspace", "dh_sample", "dh_embed", "dh_embed_backward_workspace", "dh_embed_backward",
+           "dh_layer_norm", "dh_layer_norm_backward_workspace", "dh_layer_norm_backward"]
 
 MAX_K, MAX_BEAMS, MAX_BEAM_OUT, MAX_SLOTS = 1024, 128, 256, 1024  # DH_MAX_*
 
@@ -125,6 +127,22 @@ def load_library(path: str | None = None):
         lib.dh_beam_select.restype = I
         lib.dh_reorder_states.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, L, P]
         lib.dh_reorder_states.restype = I
+        lib.dh_sample_workspace.argtypes = [I, I, I]
+        lib.dh_sample_workspace.restype = Z
+        lib.dh_sample.argtypes = [P, L, P, P, P, P, P, F, I, F, F, I, I, I, P, P, P, Z, P]
+        lib.dh_sample.restype = I
+        lib.dh_embed.argtypes = [P, L, P, I, I, I, I, F, P, L, P]
+        lib.dh_embed.restype = I
+        lib.dh_embed_backward_workspace.argtypes = [I, I, I, I]
+        lib.dh_embed_backward_workspace.restype = Z
+        lib.dh_embed_backward.argtypes = [P, L, P, I, I, I, I, F, I, P, L, P, Z, P]
+        lib.dh_embed_backward.restype = I
+        lib.dh_layer_norm.argtypes = [P, L, P, P, I, I, I, I, F, P, L, P, P]
+        lib.dh_layer_norm.restype = I
+        lib.dh_layer_norm_backward_workspace.argtypes = [I, I, I]
+        lib.dh_layer_norm_backward_workspace.restype = Z
+        lib.dh_layer_norm_backward.argtypes = [P, L, P, L, P, P, I, I, I, I, P, L, P, P, P, Z, P]
+        lib.dh_layer_norm_backward.restype = I
         lib.dh_set_tuning.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
         lib.dh_set_tuning.restype = I
         if path is None:
@@ -814,6 +832,213 @@ def reorder_states(states, idx, *, out=None, lengths=None, length_dim=None, src_
                                  out_slots, M, H, T, unit, _raw_stream(index)), "dh_reorder_states")
     _bump((dst,))
     return dst
+
+
+# ---------------------------------------------------------------- sampling, embedding and layer norm
+#
+# As the training, search and state operators: strided rows, the tensors' own device, fresh scratch, outside
+# of autograd (layers.embedding and layers.layer_norm are the differentiable forms).
+
+
+def _setting(value, name, dtype, N, index):
+    """A setting of all rows, or a tensor of one per row: (address or None, value of all rows)."""
+    if isinstance(value, torch.Tensor):
+        _typed(value, name, dtype, (N,), index)
+        return value.data_ptr(), 0
+    return None, value
+
+
+def _given(*values):
+    return [v for v in values if isinstance(v, torch.Tensor)]
+
+
+def sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token_out=None, prob_out=None, workspace=None,
+           stream=None):
+    """One token per row of logits [N, vocab] (bf16 or fp32, rows may be strided), drawn with the uniform u
+    fp32 [N] after top-k, top-p and min-p (dh_sample).  temperature, top_p, min_p: a number, or fp32 [N] on the
+    device; top_k: a number (0: all), or int32 [N].  Temperature 0 takes the likeliest token.  Returns (token int32
+    [N], prob fp32 [N]: the probability with which it is drawn); -1 and 0 for a row that is no distribution."""
+    lib = load_library()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, vocab]")
+    dt, index = _rows(logits, "logits")
+    N, vocab = logits.shape
+    if N > _INT_MAX or vocab > _INT_MAX:
+        raise ValueError("N and vocab have to fit 32 bits")
+    _typed(u, "u", torch.float32, (N,), index)
+    t_ptr, t = _setting(temperature, "temperature", torch.float32, N, index)
+    k_ptr, k = _setting(top_k, "top_k", torch.int32, N, index)
+    p_ptr, p = _setting(top_p, "top_p", torch.float32, N, index)
+    m_ptr, m = _setting(min_p, "min_p", torch.float32, N, index)
+    k = int(k)
+    if abs(k) > _INT_MAX:
+        raise ValueError("top_k has to fit 32 bits")
+    dev = logits.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, _given(logits, u, temperature, top_k, top_p, min_p, token_out, prob_out),
+                          lambda: sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p,
+                                         token_out=token_out, prob_out=prob_out, workspace=workspace))
+    token = _out(token_out, "token_out", torch.int32, (N,), dev)
+    prob = _out(prob_out, "prob_out", torch.float32, (N,), dev)
+    nbytes = _workspace_bytes("dh_sample_workspace", N, vocab, dt)
+    ws = _scratch(nbytes, workspace, "sample", dev)
+    _check(lib.dh_sample(logits.data_ptr(), logits.stride(0), u.data_ptr(), t_ptr, k_ptr, p_ptr, m_ptr, float(t), k,
+                         float(p), float(m), N, vocab, dt, token.data_ptr(), prob.data_ptr(), _addr(ws), nbytes,
+                         _raw_stream(index)), "dh_sample")
+    if token_out is not None or prob_out is not None:
+        _written(token_out, prob_out)
+    return token, prob
+
+
+def _hidden(t, name, shape, dtype=None, index=None):
+    """Checks a CUDA tensor of rows whose elements are adjacent, [N, d]; its dtype's code and device's index."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'[rows, d]' if shape is None else list(shape)}, not {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    code, at = _rows(t, name)
+    if index is not None and at != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, not on {t.device}")
+    if t.shape[0] > _INT_MAX or t.shape[1] > _INT_MAX:
+        raise ValueError(f"{name}: its sizes have to fit 32 bits")
+    return code, at
+
+
+def _hidden_out(t, name, shape, dtype, dev):
+    """The rows that a call writes: the caller's, checked, or new ones."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _hidden(t, name, shape, dtype, dev.index)
+    if shape[0] > 1 and t.stride(0) < shape[1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t
+
+
+def embed(table, tokens, *, scale=1.0, out=None, stream=None):
+    """scale * table[tokens] (dh_embed): table [vocab, d] (bf16 or fp32, rows may be strided), tokens int32 [N]; a
+    token outside the vocabulary (padding) has a row of zeros.  Returns [N, d] in the table's dtype."""
+    lib = load_library()
+    dt, index = _hidden(table, "table", None)
+    vocab, d = table.shape
+    if tokens.dim() != 1:
+        raise ValueError("tokens must be [N]")
+    N = tokens.shape[0]
+    _typed(tokens, "tokens", torch.int32, (N,), index)
+    if N > _INT_MAX:
+        raise ValueError("tokens: N has to fit 32 bits")
+    dev = table.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (table, tokens, out), lambda: embed(table, tokens, scale=scale, out=out))
+    rows = _hidden_out(out, "out", (N, d), table.dtype, dev)
+    _check(lib.dh_embed(table.data_ptr(), table.stride(0), tokens.data_ptr(), N, vocab, d, dt, float(scale),
+                        rows.data_ptr(), rows.stride(0), _raw_stream(index)), "dh_embed")
+    if out is not None:
+        _written(out)
+    return rows
+
+
+def embed_backward(grad_out, tokens, vocab, *, scale=1.0, grad_table=None, accumulate=False, workspace=None,
+                   stream=None):
+    """The gradient of a table [vocab, d] from that of the rows looked up, grad_out [N, d] (dh_embed_backward), in
+    grad_out's dtype.  accumulate: it is added to grad_table, whose other rows stay as they were.  Returns it."""
+    lib = load_library()
+    dt, index = _hidden(grad_out, "grad_out", None)
+    N, d = grad_out.shape
+    _typed(tokens, "tokens", torch.int32, (N,), index)
+    vocab = int(vocab)
+    if not 0 < vocab <= _INT_MAX:
+        raise ValueError("vocab must be positive and fit 32 bits")
+    if accumulate and grad_table is None:
+        raise ValueError("accumulate adds to a grad_table that is given")
+    dev = grad_out.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (grad_out, tokens, grad_table), lambda: embed_backward(
+            grad_out, tokens, vocab, scale=scale, grad_table=grad_table, accumulate=accumulate, workspace=workspace))
+    grad = _hidden_out(grad_table, "grad_table", (vocab, d), grad_out.dtype, dev)
+    nbytes = _workspace_bytes("dh_embed_backward_workspace", N, vocab, d, dt)
+    ws = _scratch(nbytes, workspace, "embed", dev)
+    _check(lib.dh_embed_backward(grad_out.data_ptr(), grad_out.stride(0), tokens.data_ptr(), N, vocab, d, dt,
+                                 float(scale), 1 if accumulate else 0, grad.data_ptr(), grad.stride(0), _addr(ws),
+                                 nbytes, _raw_stream(index)), "dh_embed_backward")
+    if grad_table is not None:
+        _written(grad_table)
+    return grad
+
+
+def _norm_params(x, index, weight, bias, dtype=None):
+    """The dtype of the parameters (fp32 or that of the rows) and its code."""
+    d = x.shape[1]
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dtype != torch.float32 and t.dtype != x.dtype:
+            raise ValueError(f"{name} must be fp32 or {x.dtype}, not {t.dtype}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError("weight and bias must share a dtype")
+        dtype = t.dtype
+        _typed(t, name, dtype, (d,), index)
+    dtype = x.dtype if dtype is None else dtype
+    return dtype, BF16 if dtype == torch.bfloat16 else F32
+
+
+def layer_norm(x, weight=None, bias=None, *, eps=1e-5, with_stats=False, out=None, stats_out=None, stream=None):
+    """Layer norm of the rows x [N, d] (bf16 or fp32, rows may be strided; dh_layer_norm); weight and bias [d] in
+    fp32 or x's dtype.  out may be x itself.  Returns (y in x's dtype, stats fp32 [N, 2] or None: each row's mean and
+    1 / sqrt(variance + eps), which the gradient takes)."""
+    lib = load_library()
+    dt, index = _hidden(x, "x", None)
+    N, d = x.shape
+    _, pt = _norm_params(x, index, weight, bias)
+    dev = x.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (x, weight, bias, out, stats_out), lambda: layer_norm(
+            x, weight, bias, eps=eps, with_stats=with_stats, out=out, stats_out=stats_out))
+    y = _hidden_out(out, "out", (N, d), x.dtype, dev)
+    stats = None
+    if with_stats or stats_out is not None:
+        stats = _out(stats_out, "stats_out", torch.float32, (N, 2), dev)
+    _check(lib.dh_layer_norm(x.data_ptr(), x.stride(0), _addr(weight), _addr(bias), N, d, dt, pt, float(eps),
+                             y.data_ptr(), y.stride(0), _addr(stats), _raw_stream(index)), "dh_layer_norm")
+    if out is not None or stats_out is not None:
+        _written(out, stats_out)
+    return y, stats
+
+
+def layer_norm_backward(grad_out, x, stats, weight=None, *, param_dtype=None, with_x=True, with_weight=True,
+                        with_bias=True, grad_x=None, grad_weight=None, grad_bias=None, workspace=None, stream=None):
+    """The gradients of layer_norm's x, weight and bias (dh_layer_norm_backward) from that of y, grad_out [N, d], and
+    the stats of a forward call on the same x.  Those of the parameters have the weight's dtype (param_dtype where
+    there is no weight; x's if not given).  grad_x may be x or grad_out itself.  Returns (grad_x, grad_weight,
+    grad_bias), None where not wanted."""
+    lib = load_library()
+    dt, index = _hidden(x, "x", None)
+    N, d = x.shape
+    _hidden(grad_out, "grad_out", (N, d), x.dtype, index)
+    _typed(stats, "stats", torch.float32, (N, 2), index)
+    if param_dtype is not None and param_dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"param_dtype must be fp32 or {x.dtype}")
+    ptype, pt = _norm_params(x, index, weight, None, param_dtype)
+    dev = x.device
+    if stream is not None or index != torch.cuda.current_device():
+        return _elsewhere(stream, dev, (grad_out, x, stats, weight, grad_x, grad_weight, grad_bias),
+                          lambda: layer_norm_backward(
+                              grad_out, x, stats, weight, param_dtype=param_dtype, with_x=with_x,
+                              with_weight=with_weight, with_bias=with_bias, grad_x=grad_x, grad_weight=grad_weight,
+                              grad_bias=grad_bias, workspace=workspace))
+    dx = _hidden_out(grad_x, "grad_x", (N, d), x.dtype, dev) if with_x or grad_x is not None else None
+    dw = _out(grad_weight, "grad_weight", ptype, (d,), dev) if with_weight or grad_weight is not None else None
+    db = _out(grad_bias, "grad_bias", ptype, (d,), dev) if with_bias or grad_bias is not None else None
+    nbytes, ws = 0, None
+    if dw is not None or db is not None:
+        nbytes = _workspace_bytes("dh_layer_norm_backward_workspace", N, d, dt)
+        ws = _scratch(nbytes, workspace, "norm", dev)
+    _check(lib.dh_layer_norm_backward(grad_out.data_ptr(), grad_out.stride(0), x.data_ptr(), x.stride(0),
+                                      stats.data_ptr(), _addr(weight), N, d, dt, pt, _addr(dx),
+                                      d if dx is None else dx.stride(0), _addr(dw), _addr(db), _addr(ws), nbytes,
+                                      _raw_stream(index)), "dh_layer_norm_backward")
+    if grad_x is not None or grad_weight is not None or grad_bias is not None:
+        _written(grad_x, grad_weight, grad_bias)
+    return dx, dw, db
 
 
 def workspace_status(workspace: "Workspace | None" = None, device=None, stream=None) -> int:

@@ -1,0 +1,434 @@
+// Embedding lookup with scaling, and the table's gradient by sorted tokens (definitions at dh_embed and
+// dh_embed_backward in dh.h).
+//
+// Lookup: out[n] = scale table[token[n]].  Nothing but the copy's traffic: a thread moves VECS vectors of 16
+// bytes, all loads issued before the first store.
+//
+// Gradient: grad[v] = scale sum over the n with token[n] = v, in fp32.  The positions are first sorted by
+// (token, n), so that a row's terms stand together and are added in one fixed order, without atomics on
+// values:
+//   k_token_sort   a stable radix sort of the N (token, n) pairs by one cluster, in a single launch; also marks
+//                  the tokens that occur in a bitmap
+//   k_embed_grad   blocks over chunks of the sorted pairs, each for a tile of columns: a run of one token that
+//                  lies within its chunk is summed and written; of a run that leaves its chunk, the part is
+//                  written to the workspace.  More blocks write the zeros of the rows that do not occur.
+//   k_embed_join   adds the parts of the runs that span chunks, in order.
+// The split by chunks of pairs, not by rows, keeps the work even however often one token comes.
+#include <type_traits>
+
+#include "layers.cuh"
+
+namespace dh {
+namespace {
+
+constexpr int EM_THREADS = 256;
+constexpr int EM_VECS = 4;
+
+// A unit is 16 bytes of a row (VEC), else one element; `units` of them make a row.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned units) {
+  using U = typename std::conditional<VEC, uint4, T>::type;
+  constexpr int PER = Elem<T>::PER16, UNIT = VEC ? PER : 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const T* table = static_cast<const T*>(a.src);
+  T* out = static_cast<T*>(a.dst);
+  const unsigned long long items = (unsigned long long)a.N * units;
+  const unsigned long long i0 = (unsigned long long)blockIdx.x * (EM_THREADS * EM_VECS) + threadIdx.x;
+  U x[EM_VECS];
+  int row[EM_VECS], at[EM_VECS];
+#pragma unroll
+  for (int q = 0; q < EM_VECS; ++q) {
+    const unsigned long long i = i0 + q * EM_THREADS;
+    row[q] = -1;
+    if (i < items) {
+      const unsigned long long r = i / units;
+      row[q] = (int)r;
+      at[q] = (int)(i - r * units) * UNIT;
+      const int t = __ldg(a.tokens + r);
+      x[q] = U{};
+      if (t >= 0 && t < a.vocab) x[q] = *reinterpret_cast<const U*>(table + (long long)t * a.src_ld + at[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < EM_VECS; ++q) {
+    if (row[q] < 0) continue;
+    if (a.scale != 1.f) {
+      if constexpr (VEC) {
+        float z[PER];
+        Elem<T>::unpack(x[q], z);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) z[e] *= a.scale;
+        x[q] = round_vec<T>(z);
+      } else {
+        x[q] = Elem<T>::from_f(Elem<T>::to_f(x[q]) * a.scale);
+      }
+    }
+    *reinterpret_cast<U*>(out + row[q] * a.dst_ld + at[q]) = x[q];
+  }
+}
+
+// ------------------------------------------------------------------ sorting the tokens
+
+constexpr int TS_THREADS = 1024;
+constexpr int TS_WARPS = TS_THREADS / 32;
+constexpr int TS_BITS = 9;  // at most, per pass
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The word at `p` of this block's shared memory, in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+  return v;
+}
+
+// Sorts (token, n) by token, stable in n, into buf[passes & 1 ? 1 : 0]; tokens outside [0, vocab) get the key
+// vocab and so come last.  A least-significant-digit radix sort: each warp owns a contiguous run of pairs, counts
+// its digits, and after an exclusive scan over (digit, block, warp) places its pairs in order.
+__global__ void __launch_bounds__(TS_THREADS) k_token_sort(const int32_t* __restrict__ tokens, int N, int vocab,
+                                                           int bits, int passes, uint2* __restrict__ buf0,
+                                                           uint2* __restrict__ buf1, uint32_t* __restrict__ present) {
+  extern __shared__ uint32_t ts_smem[];
+  __shared__ uint32_t s_total[1 << TS_BITS], s_scan[TS_WARPS];
+  const int nb = 1 << bits;
+  uint32_t* cnt = ts_smem;  // [warp][digit]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int words = (vocab + 31) / 32;
+  for (int i = rank * TS_THREADS + threadIdx.x; i < words; i += ranks * TS_THREADS) present[i] = 0u;
+  // pairs of a warp: a multiple of 32, contiguous
+  const unsigned warps = ranks * TS_WARPS;
+  const long long per_warp = ((long long)N + 32LL * warps - 1) / (32LL * warps) * 32;
+  const long long w0 = per_warp * (rank * TS_WARPS + warp);
+  const int p0 = (int)(w0 < N ? w0 : N), p1 = (int)(w0 + per_warp < N ? w0 + per_warp : N);
+  for (int pass = 0; pass < passes; ++pass) {
+    const uint2* src = (pass & 1) ? buf0 : buf1;
+    uint2* dst = (pass & 1) ? buf1 : buf0;
+    const int sh = pass * bits;
+    const uint32_t mask = (uint32_t)nb - 1u;
+    auto pair = [&](int i) -> uint2 {
+      if (pass == 0) {
+        const int t = __ldg(tokens + i);
+        return make_uint2((uint32_t)t < (uint32_t)vocab ? (uint32_t)t : (uint32_t)vocab, (uint32_t)i);
+      }
+      return __ldcg(src + i);
+    };
+    for (int i = threadIdx.x; i < nb * TS_WARPS; i += TS_THREADS) cnt[i] = 0u;
+    __syncthreads();
+    uint32_t* mine = cnt + warp * nb;
+    for (int i = p0; i < p1; i += 32) {
+      const bool on = i + lane < p1;
+      const uint32_t dg = on ? (pair(i + lane).x >> sh) & mask : 0xFFFFFFFFu;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
+      if (on && (same & ((1u << lane) - 1u)) == 0) mine[dg] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // per digit: the warps' counts to exclusive sums, and the block's total
+    for (int b = threadIdx.x; b < nb; b += TS_THREADS) {
+      uint32_t s = 0;
+      for (int w = 0; w < TS_WARPS; ++w) {
+        const uint32_t x = cnt[w * nb + b];
+        cnt[w * nb + b] = s;
+        s += x;
+      }
+      s_total[b] = s;
+    }
+    cluster_sync();
+    // the digit's first place of this block: lower digits of all blocks, the same digit of lower blocks
+    uint32_t all = 0, before = 0;
+    if (threadIdx.x < nb) {
+      for (uint32_t r = 0; r < ranks; ++r) {
+        const uint32_t x = ld_cluster(s_total + threadIdx.x, r);
+        all += x;
+        if (r < rank) before += x;
+      }
+    }
+    uint32_t inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    uint32_t lower = 0;
+    for (int w = 0; w < warp; ++w) lower += s_scan[w];
+    if (threadIdx.x < nb) {
+      const uint32_t base = lower + inc - all + before;
+      for (int w = 0; w < TS_WARPS; ++w) cnt[w * nb + threadIdx.x] += base;
+    }
+    __syncthreads();
+    for (int i = p0; i < p1; i += 32) {
+      const bool on = i + lane < p1;
+      uint2 x = make_uint2(0u, 0u);
+      if (on) x = pair(i + lane);
+      const uint32_t dg = on ? (x.x >> sh) & mask : 0xFFFFFFFFu;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
+      const uint32_t below = same & ((1u << lane) - 1u);
+      if (on) dst[mine[dg] + __popc(below)] = x;
+      __syncwarp();
+      if (on && below == 0) mine[dg] += __popc(same);
+      __syncwarp();
+      if (pass == 0 && on && x.x < (uint32_t)vocab) {
+        // the bitmap was zeroed before the cluster's barrier; a bit that is set needs no second atomic
+        const uint32_t bit = 1u << (x.x & 31u);
+        if (!(__ldcg(present + (x.x >> 5)) & bit)) atomicOr(present + (x.x >> 5), bit);
+      }
+    }
+    // the pairs are in place for the whole cluster, and the totals have been read
+    cluster_sync();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ summing the runs
+
+constexpr int EG_THREADS = 128;
+constexpr int EG_CHUNK = 64;   // pairs of a chunk, at most
+constexpr int EG_AHEAD = 8;    // loads of a thread in flight
+constexpr int EG_ZERO_ROWS = 8;
+
+struct GradPlan {
+  int chunk, n_chunks, tiles;
+  unsigned run_blocks, zero_blocks;
+  const uint2* pairs;
+  const uint32_t* present;
+  // [chunk][2][part_ld]: the sums of the run that comes from the chunk before, and of the one that goes on; a
+  // tile's in the order of its threads
+  float* parts;
+  long long part_ld;
+};
+
+// The columns of a tile: EG_THREADS vectors.  `col0` is the tile's first one.
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_grad(const EmbedArgs& a, uint32_t token, int col0, const float* sum) {
+  using C = Cols<T, VEC>;
+  T* row = static_cast<T*>(a.dst) + (long long)token * a.dst_ld + col0;
+  float z[C::PER];
+#pragma unroll
+  for (int e = 0; e < C::PER; ++e) z[e] = sum[e] * a.scale;
+  if (a.accumulate) {
+    float old[C::PER];
+    Elem<T>::unpack(C::load(row, threadIdx.x, EG_THREADS, 0, a.d - col0), old);
+#pragma unroll
+    for (int e = 0; e < C::PER; ++e) z[e] += old[e];
+  }
+  C::store(row, threadIdx.x, EG_THREADS, 0, a.d - col0, round_vec<T>(z));
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(EG_THREADS) k_embed_grad(EmbedArgs a, GradPlan p) {
+  using C = Cols<T, VEC>;
+  constexpr int PER = C::PER;
+  __shared__ uint2 s_pair[EG_CHUNK + 2];  // the pair before the chunk, the chunk, the pair after it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.n_chunks > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel follows
+  if (blockIdx.x >= p.run_blocks) {
+    const long long v0 = (long long)(blockIdx.x - p.run_blocks) * EG_ZERO_ROWS;
+    for (int r = 0; r < EG_ZERO_ROWS; ++r) {
+      const long long v = v0 + r;
+      if (v >= a.vocab) return;
+      if ((__ldg(p.present + (v >> 5)) >> (v & 31)) & 1u) continue;
+      T* row = static_cast<T*>(a.dst) + v * a.dst_ld;
+      for (int col0 = 0; col0 < a.d; col0 += EG_THREADS * PER)
+        C::store(row + col0, threadIdx.x, EG_THREADS, 0, a.d - col0, make_uint4(0u, 0u, 0u, 0u));
+    }
+    return;
+  }
+  const int c = blockIdx.x / p.tiles, tile = blockIdx.x - c * p.tiles;
+  const int i0 = c * p.chunk, n = min(p.chunk, a.N - i0);
+  const uint2 none = make_uint2(0xFFFFFFFFu, 0u);
+  for (int i = threadIdx.x; i < n + 2; i += EG_THREADS) {
+    const int g = i0 + i - 1;
+    s_pair[i] = g >= 0 && g < a.N ? __ldg(p.pairs + g) : none;
+  }
+  __syncthreads();
+  const int col0 = tile * EG_THREADS * PER;
+  const T* grad = static_cast<const T*>(a.src) + col0;
+  float sum[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) sum[e] = 0.f;
+  bool from_before = s_pair[0].x == s_pair[1].x;
+  for (int j = 0; j < n; j += EG_AHEAD) {
+    uint4 x[EG_AHEAD];
+#pragma unroll
+    for (int q = 0; q < EG_AHEAD; ++q) {
+      x[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (j + q < n && s_pair[j + q + 1].x < (uint32_t)a.vocab)
+        x[q] = C::load(grad + (long long)s_pair[j + q + 1].y * a.src_ld, threadIdx.x, EG_THREADS, 0, a.d - col0);
+    }
+#pragma unroll
+    for (int q = 0; q < EG_AHEAD; ++q) {
+      if (j + q >= n) break;
+      const uint32_t token = s_pair[j + q + 1].x;
+      if (token >= (uint32_t)a.vocab) return;  // the padding, behind every token
+      float z[PER];
+      Elem<T>::unpack(x[q], z);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) sum[e] += z[e];
+      const bool goes_on = s_pair[j + q + 2].x == token;
+      if (goes_on && j + q + 1 < n) continue;
+      if (from_before || goes_on) {
+        float* part = p.parts + ((long long)c * 2 + (from_before ? 0 : 1)) * p.part_ld + col0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) part[e * EG_THREADS + threadIdx.x] = sum[e];
+      } else {
+        write_grad<T, VEC>(a, token, col0, sum);
+      }
+      from_before = false;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) sum[e] = 0.f;
+    }
+  }
+}
+
+// A run that starts in chunk c and goes on: its parts, in order.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(EG_THREADS) k_embed_join(EmbedArgs a, GradPlan p) {
+  constexpr int PER = Elem<T>::PER16;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x / p.tiles, tile = blockIdx.x - c * p.tiles;
+  const long long end = (long long)(c + 1) * p.chunk;
+  if (end >= a.N) return;
+  const uint32_t token = __ldg(p.pairs + end - 1).x;
+  if (token >= (uint32_t)a.vocab || __ldg(p.pairs + end).x != token) return;
+  // from the chunk before: not its first part
+  const long long start = (long long)c * p.chunk;
+  if (start > 0 && __ldg(p.pairs + start - 1).x == token) return;
+  const int col0 = tile * EG_THREADS * PER;
+  float sum[PER];
+  const float* part = p.parts + ((long long)c * 2 + 1) * p.part_ld + col0 + threadIdx.x;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) sum[e] = part[e * EG_THREADS];
+  for (int k = c + 1; k < p.n_chunks && __ldg(p.pairs + (long long)k * p.chunk).x == token; ++k) {
+    part = p.parts + (long long)k * 2 * p.part_ld + col0 + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) sum[e] += part[e * EG_THREADS];
+  }
+  write_grad<T, VEC>(a, token, col0, sum);
+}
+
+// Pairs per chunk: 64, fewer where that leaves SMs without a block.
+int chunk_of(int N) { return N >= 64 * 304 ? 64 : N >= 16 * 304 ? 16 : 8; }
+
+// Columns of a part, whole tiles of either type.
+size_t part_width(int d) { return align_up((size_t)d, EG_THREADS * 8); }
+
+struct GradLayout {
+  size_t buf0, buf1, present, parts, total;
+};
+GradLayout grad_layout(int N, int vocab, int d) {
+  GradLayout L;
+  size_t off = WS_HEADER;
+  L.buf0 = off;
+  off = align_up(off + (size_t)N * 8, 256);
+  L.buf1 = off;
+  off = align_up(off + (size_t)N * 8, 256);
+  L.present = off;
+  off = align_up(off + ((size_t)vocab + 31) / 32 * 4, 256);
+  L.parts = off;
+  const int chunk = chunk_of(N);
+  off = align_up(off + ((size_t)N + chunk - 1) / chunk * 2 * part_width(d) * 4, 256);
+  L.total = off;
+  return L;
+}
+
+template <typename T>
+cudaError_t run_embed(const Ctx& c, const EmbedArgs& a) {
+  constexpr int PER = Elem<T>::PER16;
+  const bool vec = whole_vectors(a.src, a.src_ld, a.vocab, a.d, sizeof(T)) &&
+                   whole_vectors(a.dst, a.dst_ld, a.N, a.d, sizeof(T));
+  const unsigned units = vec ? (unsigned)(a.d / PER) : (unsigned)a.d;
+  const unsigned long long items = (unsigned long long)a.N * units;
+  const unsigned grid = (unsigned)((items + EM_THREADS * EM_VECS - 1) / (EM_THREADS * EM_VECS));
+  return launch_pdl(c, "embed", vec ? k_embed<T, true> : k_embed<T, false>, dim3(grid), dim3(EM_THREADS), 0, a,
+                    units);
+}
+
+// No tokens: rows of zeros.
+template <typename T>
+cudaError_t launch_zeros(const Ctx& c, const EmbedArgs& a) {
+  return note_error(cudaMemset2DAsync(a.dst, (size_t)(a.vocab > 1 ? a.dst_ld : a.d) * sizeof(T), 0,
+                                      (size_t)a.d * sizeof(T), (size_t)a.vocab, c.stream),
+                    "cudaMemset2DAsync");
+}
+
+template <typename T>
+cudaError_t run_embed_backward(const Ctx& c, const EmbedArgs& a) {
+  constexpr int PER = Elem<T>::PER16;
+  const GradLayout L = grad_layout(a.N, a.vocab, a.d);
+  uint2* buf[2] = {reinterpret_cast<uint2*>(a.ws + L.buf0), reinterpret_cast<uint2*>(a.ws + L.buf1)};
+  uint32_t* present = reinterpret_cast<uint32_t*>(a.ws + L.present);
+  int key_bits = 0;
+  while (a.vocab >> key_bits) ++key_bits;  // the largest key is vocab
+  const int passes = (key_bits + TS_BITS - 1) / TS_BITS, bits = (key_bits + passes - 1) / passes;
+  if (a.N == 0) return launch_zeros<T>(c, a);
+  static unsigned long long smem_done = 0;
+  cudaError_t e = allow_max_smem(k_token_sort, c.device, &smem_done);
+  if (e != cudaSuccess) return e;
+  {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    const unsigned ranks = a.N > 4 * TS_THREADS ? 8 : 1;
+    at[1].val.clusterDim.x = ranks;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(TS_THREADS);
+    cfg.dynamicSmemBytes = (size_t)TS_WARPS * (1u << bits) * 4;
+    cfg.stream = c.stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    prof_before("token_sort", c.stream);
+    e = cudaLaunchKernelEx(&cfg, k_token_sort, a.tokens, a.N, a.vocab, bits, passes, buf[0], buf[1], present);
+    prof_after(c.stream);
+    if (e != cudaSuccess) return e;
+  }
+  const bool vec = whole_vectors(a.src, a.src_ld, a.N, a.d, sizeof(T)) &&
+                   whole_vectors(a.dst, a.dst_ld, a.vocab, a.d, sizeof(T));
+  GradPlan p = {};
+  p.chunk = chunk_of(a.N);
+  p.n_chunks = (int)(((long long)a.N + p.chunk - 1) / p.chunk);
+  p.tiles = (a.d + EG_THREADS * PER - 1) / (EG_THREADS * PER);
+  p.run_blocks = (unsigned)p.n_chunks * (unsigned)p.tiles;
+  p.zero_blocks = a.accumulate ? 0u : (unsigned)((a.vocab + EG_ZERO_ROWS - 1) / EG_ZERO_ROWS);
+  p.pairs = buf[(passes - 1) & 1];
+  p.present = present;
+  p.parts = reinterpret_cast<float*>(a.ws + L.parts);
+  p.part_ld = (long long)part_width(a.d);
+  e = launch_pdl(c, "embed_grad", vec ? k_embed_grad<T, true> : k_embed_grad<T, false>,
+                 dim3(p.run_blocks + p.zero_blocks), dim3(EG_THREADS), 0, a, p);
+  if (e != cudaSuccess || p.n_chunks == 1) return e;
+  return launch_pdl(c, "embed_join", vec ? k_embed_join<T, true> : k_embed_join<T, false>, dim3(p.run_blocks),
+                    dim3(EG_THREADS), 0, a, p);
+}
+
+}  // namespace
+
+size_t embed_backward_workspace(int N, int vocab, int d, int) { return grad_layout(N, vocab, d).total; }
+
+cudaError_t launch_embed(const Ctx& c, const EmbedArgs& a, int dtype) {
+  return dtype == DH_BF16 ? run_embed<__nv_bfloat16>(c, a) : run_embed<float>(c, a);
+}
+cudaError_t launch_embed_backward(const Ctx& c, const EmbedArgs& a, int dtype) {
+  return dtype == DH_BF16 ? run_embed_backward<__nv_bfloat16>(c, a) : run_embed_backward<float>(c, a);
+}
+
+}  // namespace dh
