@@ -223,11 +223,11 @@ __device__ __forceinline__ void write_grad(const EmbedArgs& a, uint32_t token, i
   for (int e = 0; e < C::PER; ++e) z[e] = sum[e] * a.scale;
   if (a.accumulate) {
     float old[C::PER];
-    Elem<T>::unpack(C::load(row, threadIdx.x, EG_THREADS, 0, a.d - col0), old);
+    Elem<T>::unpack(C::load(row, threadIdx.x, 0, a.d - col0), old);
 #pragma unroll
     for (int e = 0; e < C::PER; ++e) z[e] += old[e];
   }
-  C::store(row, threadIdx.x, EG_THREADS, 0, a.d - col0, round_vec<T>(z));
+  C::store(row, threadIdx.x, 0, a.d - col0, round_vec<T>(z));
 }
 
 template <typename T, bool VEC>
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(EG_THREADS) k_embed_grad(EmbedArgs a, GradPlan
       if ((__ldg(p.present + (v >> 5)) >> (v & 31)) & 1u) continue;
       T* row = static_cast<T*>(a.dst) + v * a.dst_ld;
       for (int col0 = 0; col0 < a.d; col0 += EG_THREADS * PER)
-        C::store(row + col0, threadIdx.x, EG_THREADS, 0, a.d - col0, make_uint4(0u, 0u, 0u, 0u));
+        C::store(row + col0, threadIdx.x, 0, a.d - col0, make_uint4(0u, 0u, 0u, 0u));
     }
     return;
   }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(EG_THREADS) k_embed_grad(EmbedArgs a, GradPlan
     for (int q = 0; q < EG_AHEAD; ++q) {
       x[q] = make_uint4(0u, 0u, 0u, 0u);
       if (j + q < n && s_pair[j + q + 1].x < (uint32_t)a.vocab)
-        x[q] = C::load(grad + (long long)s_pair[j + q + 1].y * a.src_ld, threadIdx.x, EG_THREADS, 0, a.d - col0);
+        x[q] = C::load(grad + (long long)s_pair[j + q + 1].y * a.src_ld, threadIdx.x, 0, a.d - col0);
     }
 #pragma unroll
     for (int q = 0; q < EG_AHEAD; ++q) {

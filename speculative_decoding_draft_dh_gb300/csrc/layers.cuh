@@ -58,6 +58,7 @@ struct NormArgs {
   long long grad_ld;
   void *grad_weight, *grad_bias;
   int N, d;
+  int part_ld;  // columns of a block's sums in ws
   float* ws;
 };
 size_t norm_backward_workspace(int N, int d, int dtype);
@@ -87,25 +88,27 @@ cudaError_t launch_pdl(const Ctx& c, const char* name, void (*kernel)(P...), dim
 
 // ------------------------------------------------------------------ rows of hidden states
 
-// Which columns of a row a thread (one of `width`) holds, PER16 of them per vector v.  VEC, for rows of whole
-// vectors that start on 16 bytes: PER16 adjacent ones, in one access.  Otherwise every width-th one, so that
-// neighbouring threads access neighbouring elements whatever the row's alignment.  Columns past the row's end
-// read as 0 and are not written.
-template <typename T, bool VEC>
+// Which columns of a row a thread holds: NV vectors of PER16 of them.  A warp's columns are contiguous, so that a
+// thread's vectors lie at constant distances.  VEC, for rows of whole vectors that start on 16 bytes: a vector is
+// adjacent columns, in one access, and a warp's vectors v stand together.  Otherwise a thread has every 32nd column
+// of its warp's, so that neighbouring threads access neighbouring elements whatever the row's alignment.  Columns
+// past the row's end read as 0 and are not written.
+template <typename T, bool VEC, int NV = 1>
 struct Cols {
   static constexpr int PER = Elem<T>::PER16;
-  __device__ __forceinline__ static int col(int thread, int width, int v, int e) {
-    return VEC ? (thread + v * width) * PER + e : (v * PER + e) * width + thread;
+  static constexpr int WARP = 32 * NV * PER;  // columns of a warp
+  __device__ __forceinline__ static int col(int thread, int v, int e) {
+    return (thread >> 5) * WARP + (VEC ? (v * 32 + (thread & 31)) * PER + e : (v * PER + e) * 32 + (thread & 31));
   }
-  __device__ __forceinline__ static uint4 load(const T* row, int thread, int width, int v, int d) {
+  __device__ __forceinline__ static uint4 load(const T* row, int thread, int v, int d) {
     if constexpr (VEC) {
-      const int id = col(thread, width, v, 0);
+      const int id = col(thread, v, 0);
       return id < d ? *reinterpret_cast<const uint4*>(row + id) : make_uint4(0u, 0u, 0u, 0u);
     } else {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        const int id = col(thread, width, v, e);
+        const int id = col(thread, v, e);
         if (id < d) {
           if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(row[id]);
           else w[e / 2] |= (uint32_t)__bfloat16_as_ushort(row[id]) << (16 * (e & 1));
@@ -114,15 +117,15 @@ struct Cols {
       return make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  __device__ __forceinline__ static void store(T* row, int thread, int width, int v, int d, const uint4& u) {
+  __device__ __forceinline__ static void store(T* row, int thread, int v, int d, const uint4& u) {
     if constexpr (VEC) {
-      const int id = col(thread, width, v, 0);
+      const int id = col(thread, v, 0);
       if (id < d) *reinterpret_cast<uint4*>(row + id) = u;
     } else {
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
-        const int id = col(thread, width, v, e);
+        const int id = col(thread, v, e);
         if (id < d) {
           if constexpr (sizeof(T) == 4) row[id] = __uint_as_float(w[e]);
           else row[id] = __ushort_as_bfloat16((unsigned short)(w[e / 2] >> (16 * (e & 1))));

@@ -12,54 +12,26 @@
 // blocks leave their sums in the workspace and a second kernel adds them in order.
 // Rows of more than NM_HELD columns are read again for each step instead, by k_norm_wide and
 // k_norm_backward_wide, and k_norm_columns sums their dw and db.
+#include <mutex>
+#include <utility>
+#include <vector>
+
 #include "layers.cuh"
+#include "rows.cuh"
 
 namespace dh {
 namespace {
 
 constexpr int NM_HELD = 8192;  // columns of a row that registers hold
 
-// N parameters of type P at the columns of Cols<T, VEC>'s vector v (0 past the end).
-template <typename P, int N>
-struct Params {
-  uint4 raw[N * sizeof(P) / 16];
-  __device__ __forceinline__ void unpack(float* z) const {
-    constexpr int PER = Elem<P>::PER16;
-#pragma unroll
-    for (int q = 0; q < N / PER; ++q) Elem<P>::unpack(raw[q], z + q * PER);
-  }
-};
-template <typename T, typename P, bool VEC>
-__device__ __forceinline__ void load_params(Params<P, Elem<T>::PER16>& u, const P* p, int thread, int width, int v,
-                                            int d) {
-  constexpr int N = Elem<T>::PER16, PER = Elem<P>::PER16;
-  if constexpr (VEC) {
-    const int id = Cols<T, VEC>::col(thread, width, v, 0);
-#pragma unroll
-    for (int q = 0; q < N / PER; ++q)
-      u.raw[q] = id < d ? __ldg(reinterpret_cast<const uint4*>(p + id) + q) : make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    float z[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int id = Cols<T, VEC>::col(thread, width, v, e);
-      z[e] = id < d ? Elem<P>::to_f(p[id]) : 0.f;
-    }
-#pragma unroll
-    for (int q = 0; q < N / PER; ++q) u.raw[q] = round_vec<P>(z + q * PER);  // exact: they are P values
-  }
-}
-
-// Sums of a and b over the row's group, a warp or the block; every thread gets them.  `turn` alternates, so that
-// one barrier per call is enough.
-template <bool WARP>
-__device__ __forceinline__ float2 group_sum(float a, float b, float2 (*sh)[32], int& turn) {
+// Sums of a and b over the block, every thread gets them.  `turn` alternates, so that one barrier per call is
+// enough.
+__device__ __forceinline__ float2 block_sum(float a, float b, float2 (*sh)[32], int& turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
     b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
   }
-  if (WARP) return make_float2(a, b);
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) sh[turn][warp] = make_float2(a, b);
   __syncthreads();
@@ -73,6 +45,13 @@ __device__ __forceinline__ float2 group_sum(float a, float b, float2 (*sh)[32], 
   return s;
 }
 
+// One step of a reduction of several values at once: a lane keeps one of two, hands the other to the lane across,
+// and takes that lane's share of what it keeps, so that K values cost K/2 + K/4 + ... exchanges.
+__device__ __forceinline__ float fold(float low, float high, int o) {
+  const bool up = threadIdx.x & o;
+  return (up ? high : low) + __shfl_xor_sync(0xFFFFFFFFu, up ? low : high, o);
+}
+
 // Mean (as mean0 + delta) and 1 / sqrt(variance + eps) from the second pass's sums.
 struct Moments {
   float mean0, delta, rstd;
@@ -84,192 +63,474 @@ __device__ __forceinline__ Moments moments(float mean0, float2 q, float inv_d, f
   return {mean0, delta, 1.f / sqrtf(var + eps)};
 }
 
-constexpr int NF_WARPS = 4;  // rows of a block where a row belongs to a warp
-
-template <typename T, typename P, int NV, bool WARP, bool VEC>
-__global__ void __launch_bounds__(WARP ? 32 * NF_WARPS : 1024) k_norm(NormArgs a) {
-  using C = Cols<T, VEC>;
-  constexpr int PER = C::PER;
-  __shared__ float2 sh[2][32];
-  const int me = WARP ? (threadIdx.x & 31) : threadIdx.x, width = WARP ? 32 : blockDim.x;
-  const long long groups = WARP ? (long long)gridDim.x * NF_WARPS : gridDim.x;
-  long long n = WARP ? (long long)blockIdx.x * NF_WARPS + (threadIdx.x >> 5) : blockIdx.x;
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.y);
-  const float inv_d = 1.f / (float)a.d;
-  int turn = 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n >= a.N) return;  // a whole group
-  uint4 u[NV], next[NV];
-  Params<P, PER> w[NV], b[NV];
+// Rows on their way: SLOTS rows in shared memory, of which a thread copies its own vectors by cp.async and reads them
+// itself, so that no barrier is needed.  Copies are 16 bytes (VEC) or 4 (fp32 rows of any alignment); bf16 rows off
+// 16 bytes are loaded when they are used.
+template <typename T, bool VEC, int NV>
+struct Ring {
+  using C = Cols<T, VEC, NV>;
+  static constexpr bool COPIED = VEC || sizeof(T) == 4;
+  static constexpr int COPIES = VEC ? NV : NV * C::PER;  // of a thread and row
+  static constexpr int STEP = VEC ? 32 * C::PER : 32;    // columns between them
+  uint32_t mine;  // this thread's place in slot 0, a shared-memory address
+  uint32_t slot;  // bytes of a slot
+  int held;       // copies within the row
+  int first;      // this thread's first column (0 where it has none)
+  __device__ __forceinline__ Ring(void* smem, int me, int d)
+      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * (NV * 512) + (threadIdx.x & 31) * 16),
+        slot(blockDim.x * NV * 16), held(min(max((d - C::col(me, 0, 0) + STEP - 1) / STEP, 0), COPIES)),
+        first(held ? C::col(me, 0, 0) : 0) {}
+  static constexpr __host__ __device__ size_t bytes(int threads) { return COPIED ? (size_t)NV * threads * 16 : 0; }
+  // A row on its way to slot s (`on`: there is one), from its column `first` on.  A group of copies.
+  __device__ __forceinline__ void fetch(const T* mine_of_row, bool on, int s) const {
+    if constexpr (COPIED) {
+      const uint32_t to = mine + s * slot;
+      if (on) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) u[v] = C::load(x + n * a.ld, me, width, v, a.d);
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    if (a.weight) load_params<T, P, VEC>(w[v], static_cast<const P*>(a.weight), me, width, v, a.d);
-    if (a.bias) load_params<T, P, VEC>(b[v], static_cast<const P*>(a.bias), me, width, v, a.d);
+        for (int k = 0; k < COPIES; ++k) {
+          if constexpr (VEC) {
+            // past the row's end: zeros, and the address is not used
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * 512),
+                         "l"(mine_of_row + (k < held ? k * STEP : 0)), "r"(k < held ? 16 : 0)
+                         : "memory");
+          } else {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (k / 4) * 512 + (k % 4) * 4),
+                         "l"(mine_of_row + (k < held ? k * STEP : 0)), "r"(k < held ? 4 : 0)
+                         : "memory");
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
   }
-  for (; n < a.N; n += groups) {
-    if (n + groups < a.N) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) next[v] = C::load(x + (n + groups) * a.ld, me, width, v, a.d);
+  // Waits for this thread's copies, up to the LATER youngest groups.
+  template <int LATER>
+  __device__ __forceinline__ void wait() const {
+    if constexpr (COPIED) asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+  }
+  // Vector v of the row in slot s.
+  __device__ __forceinline__ uint4 get(const T* row, int s, int v, int me, int d) const {
+    if constexpr (COPIED) {
+      uint4 u;
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                   : "r"(mine + s * slot + v * 512)
+                   : "memory");
+      return u;
+    } else {
+      return C::load(row, me, v, d);
     }
-    float s = 0.f;
+  }
+};
+
+// The elements of a vector in pairs.
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& u, f32x2* z) {
+  float x[Elem<T>::PER16];
+  Elem<T>::unpack(u, x);
+#pragma unroll
+  for (int q = 0; q < Elem<T>::PER16 / 2; ++q) z[q] = pack2(x[2 * q], x[2 * q + 1]);
+}
+// The parameters of a thread's columns, 0 past the row's end.
+template <typename T, typename P, bool VEC, int NV>
+__device__ __forceinline__ void load_pairs(f32x2* w, const P* p, int thread, int v, int d) {
+  using C = Cols<T, VEC, NV>;
+  constexpr int PER = C::PER, PP = Elem<P>::PER16;
+  float t[PER];
+  if constexpr (VEC) {
+    const int id = C::col(thread, v, 0);
+#pragma unroll
+    for (int q = 0; q < PER / PP; ++q) {
+      const uint4 u = id < d ? __ldg(reinterpret_cast<const uint4*>(p + id) + q) : make_uint4(0u, 0u, 0u, 0u);
+      Elem<P>::unpack(u, t + q * PP);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int id = C::col(thread, v, e);
+      t[e] = id < d ? Elem<P>::to_f(p[id]) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < PER / 2; ++e) w[e] = pack2(t[2 * e], t[2 * e + 1]);
+}
+// Parameters in shared memory, as fp32 in the order in which the threads read them: each warp's vectors v, and of
+// them the first four columns of all lanes before the other four (bank conflicts otherwise).
+template <typename T, typename P, bool VEC, int NV>
+struct SharedParams {
+  using C = Cols<T, VEC, NV>;
+  static constexpr int PER = C::PER;
+  float* p;
+  static constexpr __host__ __device__ size_t bytes(int width) { return (size_t)width * NV * PER * sizeof(float); }
+  __device__ __forceinline__ explicit SharedParams(void* smem) : p(static_cast<float*>(smem)) {}
+  __device__ __forceinline__ static int place(int col) {
+    if (!VEC || PER == 4) return col;
+    return (col & ~255) + ((col >> 3) & 31) * 4 + (col & 3) + ((col & 4) << 5);
+  }
+  __device__ __forceinline__ void fill(const P* src, int width, int d) const {
+    if constexpr (VEC) {
+      constexpr int PP = Elem<P>::PER16;
+#pragma unroll 4
+      for (int i = threadIdx.x * PP; i < width * NV * PER; i += blockDim.x * PP) {
+        float t[PP];
+        Elem<P>::unpack(i < d ? __ldg(reinterpret_cast<const uint4*>(src + i)) : make_uint4(0u, 0u, 0u, 0u), t);
+#pragma unroll
+        for (int h = 0; h < PP; h += 4)
+          *reinterpret_cast<float4*>(p + place(i + h)) = make_float4(t[h], t[h + 1], t[h + 2], t[h + 3]);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < width * NV * PER; i += blockDim.x) p[i] = i < d ? Elem<P>::to_f(src[i]) : 0.f;
+    }
+  }
+  // The columns of vector v, in pairs.
+  __device__ __forceinline__ void pairs(f32x2* w, int thread, int v) const {
+    if constexpr (VEC) {
+      const float* q = p + (thread >> 5) * C::WARP + v * 32 * PER + (thread & 31) * 4;
+#pragma unroll
+      for (int h = 0; h < PER / 4; ++h) {
+        const float4 t = *reinterpret_cast<const float4*>(q + h * 128);
+        w[2 * h] = pack2(t.x, t.y);
+        w[2 * h + 1] = pack2(t.z, t.w);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) w[e / 2] = pack2(p[C::col(thread, v, e)], p[C::col(thread, v, e + 1)]);
+    }
+  }
+};
+// Each rounded once to T.
+template <typename T>
+__device__ __forceinline__ uint4 round_pairs(const f32x2* z) {
+  float x[Elem<T>::PER16];
+#pragma unroll
+  for (int q = 0; q < Elem<T>::PER16 / 2; ++q) unpack2(z[q], x[2 * q], x[2 * q + 1]);
+  return round_vec<T>(x);
+}
+__device__ __forceinline__ f32x2 both(float x) { return pack2(x, x); }
+__device__ __forceinline__ float half_of(f32x2 v, int high) {
+  float a, b;
+  unpack2(v, a, b);
+  return high ? b : a;
+}
+__device__ __forceinline__ float pair_sum(f32x2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
+}
+
+constexpr int NF_STAGES = 3;
+constexpr int NF_WARPS = 16;  // of a row, at most
+// Registers of a thread with NV vectors.
+constexpr int norm_regs(int nv) { return nv == 1 ? 64 : nv == 2 ? 80 : 128; }
+
+// A block holds blockDim / width groups of `width` threads, each of which walks over rows of its own; the groups
+// share the parameters (SHARED: in shared memory).  Barriers are a group's.
+// Each thread takes its elements relative to the mean of its first vector (z = x - s): with at most NV vectors the
+// sum of z^2 is at most NV + 1 times that of the squares about the thread's own mean, so nothing is lost to a mean
+// far from 0 or to an outlier.  The threads' sums are joined relative to the shift of a warp's first lane, the
+// warps' relative to that of the first warp (the formulas of Chan, Golub and LeVeque).
+template <typename T, typename P, int NV, bool VEC, bool SHARED>
+__global__ void __maxnreg__(norm_regs(NV)) k_norm(NormArgs a, int width) {
+  using C = Cols<T, VEC, NV>;
+  using S = SharedParams<T, P, VEC, NV>;
+  constexpr int PER = C::PER, HALF = PER / 2;
+  extern __shared__ __align__(16) unsigned char norm_smem[];
+  __shared__ float sh[2][32][4];
+  const int group = threadIdx.x / width, groups = blockDim.x / width, me = threadIdx.x - group * width;
+  const int warp = me >> 5, lane = me & 31, warps = width >> 5, warp0 = (threadIdx.x >> 5) - warp;
+  const float inv_d = 1.f / (float)a.d;
+  // elements of this thread's first vector, of this thread, and of the warp whose sums this lane joins
+  int first = 0, mine = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      mine += C::col(me, v, e) < a.d;
+      if (v == 0) first = mine;
+    }
+  const float inv_first = first ? 1.f / (float)first : 0.f;
+  const float count = (float)mine, their_count = (float)min(max(a.d - (lane & 15) * C::WARP, 0), C::WARP);
+  int turn = 0;
+  const S w_shared(norm_smem), b_shared(norm_smem + S::bytes(width));
+  const Ring<T, VEC, NV> ring(norm_smem + (SHARED ? 2 * S::bytes(width) : 0), me, a.d);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const unsigned rows = a.N, step = gridDim.x * groups;
+  unsigned n = blockIdx.x * groups + group;
+  const long long x_step = step * a.ld, y_step = step * a.y_ld;
+  const T* row = static_cast<const T*>(a.x) + n * a.ld;
+  const T* next = row + ring.first;  // the next row to fetch
+  T* out = static_cast<T*>(a.y) + n * a.y_ld;
+#pragma unroll
+  for (int s = 0; s < NF_STAGES - 1; ++s) {
+    ring.fetch(next, n + s * step < rows, s);
+    next += x_step;
+  }
+  if constexpr (SHARED) {
+    if (a.weight) w_shared.fill(static_cast<const P*>(a.weight), width, a.d);
+    if (a.bias) b_shared.fill(static_cast<const P*>(a.bias), width, a.d);
+    __syncthreads();
+  }
+  int stage = 0;
+  for (; n < rows; n += step) {
+    f32x2 z[NV][HALF];
+    ring.template wait<NF_STAGES - 2>();
+#pragma unroll
+    for (int v = 0; v < NV; ++v) unpack_pairs<T>(ring.get(row, stage, v, me, a.d), z[v]);
+    ring.fetch(next, n + (NF_STAGES - 1) * step < rows, stage == 0 ? NF_STAGES - 1 : stage - 1);
+    next += x_step;
+    row += x_step;
+    stage = stage + 1 == NF_STAGES ? 0 : stage + 1;
+    // past the row's end the elements are 0
+    f32x2 f = add2(z[0][0], z[0][1]);
+    if constexpr (HALF == 4) f = add2(f, add2(z[0][2], z[0][3]));
+    const float s = pair_sum(f) * inv_first;
+    f32x2 d1[2] = {0, 0}, d2[2] = {0, 0};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float z[PER];
-      Elem<T>::unpack(u[v], z);
+      // and stay 0
+      const f32x2 shift = both(!VEC || v * PER < mine ? -s : 0.f);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) s += z[e];
-    }
-    const float mean0 = group_sum<WARP>(s, 0.f, sh, turn).x * inv_d;
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float z[PER];
-      Elem<T>::unpack(u[v], z);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const float t = C::col(me, width, v, e) < a.d ? z[e] - mean0 : 0.f;
-        s1 += t;
-        s2 = fmaf(t, t, s2);
+      for (int e = 0; e < HALF; ++e) {
+        f32x2 t = add2(z[v][e], shift);
+        if constexpr (!VEC) {
+          float p, q;
+          unpack2(t, p, q);
+          t = pack2(v * PER + 2 * e < mine ? p : 0.f, v * PER + 2 * e + 1 < mine ? q : 0.f);
+        }
+        z[v][e] = t;
+        d1[e & 1] = add2(d1[e & 1], t);
+        d2[e & 1] = fma2(t, t, d2[e & 1]);
       }
     }
-    const Moments q = moments(mean0, group_sum<WARP>(s1, s2, sh, turn), inv_d, a.eps);
-    if (a.stats_out && me == 0) a.stats_out[n] = make_float2(q.mean0 + q.delta, q.rstd);
+    // sums of x - c and of its square, c the first lane's shift
+    const float c = __shfl_sync(0xFFFFFFFFu, s, 0), r = s - c;
+    const float p1 = pair_sum(add2(d1[0], d1[1])), p2 = pair_sum(add2(d2[0], d2[1]));
+    float part = fold(fmaf(count, r, p1), fmaf(r, fmaf(count, r, 2.f * p1), p2), 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+    float c0 = c;
+    if (warps > 1) {
+      // lanes 0 and 16 have the warp's sums
+      if ((lane & 15) == 0) sh[turn][warp0 + warp][lane >> 4] = part;
+      if (lane == 1) sh[turn][warp0 + warp][2] = c;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(width) : "memory");
+      c0 = sh[turn][warp0][2];
+      part = 0.f;
+      if ((lane & 15) < warps) {
+        const float* q = sh[turn][warp0 + (lane & 15)];
+        const float g = q[2] - c0, k = their_count * g;
+        part = lane < 16 ? q[0] + k : fmaf(g, fmaf(2.f, q[0], k), q[1]);
+      }
+      turn ^= 1;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+    }
+    const float sum1 = __shfl_sync(0xFFFFFFFFu, part, 0), sum2 = __shfl_sync(0xFFFFFFFFu, part, 16);
+    const float delta = sum1 * inv_d;
+    float var = (sum2 - sum1 * delta) * inv_d;
+    if (var < 0.f) var = 0.f;  // a NaN stays
+    const float rs = 1.f / sqrtf(var + a.eps);
+    if (a.stats_out && me == 0) a.stats_out[n] = make_float2(c0 + delta, rs);
+    const f32x2 rstd = both(rs), back = both(((s - c0) - delta) * rs);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float z[PER], wv[PER], bv[PER];
-      Elem<T>::unpack(u[v], z);
-      if (a.weight) w[v].unpack(wv);
-      if (a.bias) b[v].unpack(bv);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        z[e] = ((z[e] - q.mean0) - q.delta) * q.rstd;
-        if (a.weight) z[e] = a.bias ? fmaf(z[e], wv[e], bv[e]) : z[e] * wv[e];
-        else if (a.bias) z[e] += bv[e];
+      f32x2 w[HALF], b[HALF];
+      if (a.weight) {
+        if constexpr (SHARED) w_shared.pairs(w, me, v);
+        else load_pairs<T, P, VEC, NV>(w, static_cast<const P*>(a.weight), me, v, a.d);
       }
-      C::store(y + n * a.y_ld, me, width, v, a.d, round_vec<T>(z));
-      u[v] = next[v];
+      if (a.bias) {
+        if constexpr (SHARED) b_shared.pairs(b, me, v);
+        else load_pairs<T, P, VEC, NV>(b, static_cast<const P*>(a.bias), me, v, a.d);
+      }
+#pragma unroll
+      for (int e = 0; e < HALF; ++e) {
+        f32x2 o = fma2(z[v][e], rstd, back);
+        if (a.weight) o = a.bias ? fma2(o, w[e], b[e]) : mul2(o, w[e]);
+        else if (a.bias) o = add2(o, b[e]);
+        z[v][e] = o;
+      }
+      C::store(out, me, v, a.d, round_pairs<T>(z[v]));
     }
+    out += y_step;
   }
 }
 
-constexpr int NB_WARPS = 8;  // backward: rows of a block where a row belongs to a warp
-constexpr int NB_THREADS = 512;
-
-template <typename T, typename P, int NV, bool WARP, bool VEC>
-__global__ void __launch_bounds__(WARP ? 32 * NB_WARPS : NB_THREADS) k_norm_backward(NormArgs a, bool sums) {
-  using C = Cols<T, VEC>;
-  constexpr int PER = C::PER;
-  __shared__ float2 sh[2][32];
-  __shared__ float s_sum[WARP ? 2 * 32 * NV * PER : 1];
-  const int me = WARP ? (threadIdx.x & 31) : threadIdx.x, width = WARP ? 32 : blockDim.x;
-  const long long groups = WARP ? (long long)gridDim.x * NB_WARPS : gridDim.x;
-  const T* x = static_cast<const T*>(a.x);
-  const T* g = static_cast<const T*>(a.grad);
-  T* dx = static_cast<T*>(a.y);
+constexpr int NB_REGS = 128, NB_THREADS = 65536 / NB_REGS;
+constexpr int NB_STAGES = 2;
+// Groups of threads as in k_norm, each on R rows at a time (2 of bf16, 1 of fp32), so that their exchanges and the
+// weights are shared.
+template <typename T, typename P, int NV, bool VEC>
+__global__ void __maxnreg__(NB_REGS) k_norm_backward(NormArgs a, int width, bool sums) {
+  constexpr int R = sizeof(T) == 4 ? 1 : 2;
+  using C = Cols<T, VEC, NV>;
+  using S = SharedParams<T, P, VEC, NV>;
+  constexpr int PER = C::PER, HALF = PER / 2;
+  extern __shared__ __align__(16) unsigned char norm_smem[];
+  __shared__ float sh[2][NB_THREADS / 32][2 * R];
+  const int group = threadIdx.x / width, groups = blockDim.x / width, me = threadIdx.x - group * width;
+  const int warp = threadIdx.x >> 5, lane = me & 31, warps = width >> 5, warp0 = warp - (me >> 5);
   const float inv_d = 1.f / (float)a.d;
   int turn = 0;
+  const S w_shared(norm_smem);
+  const Ring<T, VEC, NV> ring(norm_smem + S::bytes(width), me, a.d);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (sums) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel follows
-  long long n = WARP ? (long long)blockIdx.x * NB_WARPS + (threadIdx.x >> 5) : blockIdx.x;
-  uint4 u[NV], h[NV], un[NV], hn[NV];
-  Params<P, PER> w[NV];
-  float dw[NV][PER], db[NV][PER];
-  float2 st = make_float2(0.f, 0.f), stn = st;
+  f32x2 dw[NV][HALF], db[NV][HALF];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
+  for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int e = 0; e < PER; ++e) dw[v][e] = db[v][e] = 0.f;
-    if (n < a.N) {
-      u[v] = C::load(x + n * a.ld, me, width, v, a.d);
-      h[v] = C::load(g + n * a.grad_ld, me, width, v, a.d);
+    for (int e = 0; e < HALF; ++e) dw[v][e] = db[v][e] = 0;
+  const unsigned rows = a.N, step = gridDim.x * groups * R;
+  unsigned n = (blockIdx.x * groups + group) * R;
+  const long long x_step = step * a.ld, g_step = step * a.grad_ld, dx_step = step * a.y_ld;
+  const T* x_row = static_cast<const T*>(a.x) + n * a.ld;
+  const T* g_row = static_cast<const T*>(a.grad) + n * a.grad_ld;
+  const T *x_next = x_row + ring.first, *g_next = g_row + ring.first;  // the next rows to fetch
+  T* out = a.y ? static_cast<T*>(a.y) + n * a.y_ld : nullptr;
+  const float2* st_next = a.stats + n;
+  float2 stn[R];
+  auto fetch = [&](unsigned first, int s) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      ring.fetch(x_next + i * a.ld, first + i < rows, (s * R + i) * 2);
+      ring.fetch(g_next + i * a.grad_ld, first + i < rows, (s * R + i) * 2 + 1);
     }
-    if (a.weight) load_params<T, P, VEC>(w[v], static_cast<const P*>(a.weight), me, width, v, a.d);
-  }
-  if (n < a.N) st = __ldg(a.stats + n);
-  for (; n < a.N; n += groups) {
-    const long long m = n + groups;
-    if (m < a.N) {
+    x_next += x_step;
+    g_next += g_step;
+  };
+  auto fetch_stats = [&](unsigned first) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        un[v] = C::load(x + m * a.ld, me, width, v, a.d);
-        hn[v] = C::load(g + m * a.grad_ld, me, width, v, a.d);
-      }
-      stn = __ldg(a.stats + m);
-    }
-    float s1 = 0.f, s2 = 0.f;
+    for (int i = 0; i < R; ++i) stn[i] = first + i < rows ? __ldg(st_next + i) : make_float2(0.f, 0.f);
+    st_next += step;
+  };
+#pragma unroll
+  for (int s = 0; s < NB_STAGES - 1; ++s) fetch(n + s * step, s);
+  fetch_stats(n);
+  if (a.weight) w_shared.fill(static_cast<const P*>(a.weight), width, a.d);
+  __syncthreads();
+  int stage = 0;
+  for (; n < rows; n += step) {
+    float2 st[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i] = stn[i];
+    ring.template wait<2 * R * (NB_STAGES - 2)>();
+    fetch(n + (NB_STAGES - 1) * step, stage == 0 ? NB_STAGES - 1 : stage - 1);
+    fetch_stats(n + step);
+    const bool pair = R == 1 || n + 1 < rows;  // the last row may be alone
+    // x - mean and g of vector v of row i; past the row's end g is 0 and x - mean counts for nothing
+    auto terms = [&](int i, int v, f32x2* z, f32x2* q) {
+      const f32x2 shift = both(-st[i].x);
+      unpack_pairs<T>(ring.get(x_row + i * a.ld, (stage * R + i) * 2, v, me, a.d), z);
+      unpack_pairs<T>(ring.get(g_row + i * a.grad_ld, (stage * R + i) * 2 + 1, v, me, a.d), q);
+#pragma unroll
+      for (int e = 0; e < HALF; ++e) z[e] = add2(z[e], shift);
+    };
+    f32x2 s1[R], s2[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) s1[i] = s2[i] = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float z[PER], q[PER], wv[PER];
-      Elem<T>::unpack(u[v], z);
-      Elem<T>::unpack(h[v], q);
-      if (a.weight) w[v].unpack(wv);
+      f32x2 w[HALF];
+      if (a.weight) w_shared.pairs(w, me, v);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        // past the row's end g is 0, and so is what it is multiplied with (the row's statistics may be NaN)
-        const float hat = C::col(me, width, v, e) < a.d ? (z[e] - st.x) * st.y : 0.f;
-        dw[v][e] = fmaf(q[e], hat, dw[v][e]);
-        db[v][e] += q[e];
-        const float t = a.weight ? q[e] * wv[e] : q[e];
-        s1 += t;
-        s2 = fmaf(t, hat, s2);
-      }
-    }
-    if (dx) {
-      const float2 c = group_sum<WARP>(s1, s2, sh, turn);
-      const float c1 = c.x * inv_d, c2 = c.y * inv_d;
+      for (int i = 0; i < R; ++i) {
+        if (i > 0 && !pair) continue;
+        f32x2 z[HALF], q[HALF];
+        const f32x2 rstd = both(st[i].y);
+        terms(i, v, z, q);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float z[PER], q[PER], wv[PER];
-        Elem<T>::unpack(u[v], z);
-        Elem<T>::unpack(h[v], q);
-        if (a.weight) w[v].unpack(wv);
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          const float hat = (z[e] - st.x) * st.y;
-          const float t = a.weight ? q[e] * wv[e] : q[e];
-          z[e] = st.y * fmaf(-hat, c2, t - c1);
+        for (int e = 0; e < HALF; ++e) {
+          dw[v][e] = fma2(q[e], mul2(z[e], rstd), dw[v][e]);
+          db[v][e] = add2(db[v][e], q[e]);
+          const f32x2 t = a.weight ? mul2(q[e], w[e]) : q[e];
+          s1[i] = add2(s1[i], t);
+          s2[i] = fma2(t, z[e], s2[i]);
         }
-        C::store(dx + n * a.y_ld, me, width, v, a.d, round_vec<T>(z));
       }
     }
+    if (out) {
+      // the rows' sums: 2 R values over the block
+      float part;
+      if constexpr (R == 2) {
+        const float p = fold(pair_sum(s1[0]), pair_sum(s1[1]), 16), q = fold(pair_sum(s2[0]), pair_sum(s2[1]), 16);
+        part = fold(p, q, 8);
+      } else {
+        part = fold(pair_sum(s1[0]), pair_sum(s2[0]), 16);
+        part += __shfl_xor_sync(0xFFFFFFFFu, part, 8);
+      }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      u[v] = un[v];
-      h[v] = hn[v];
+      for (int o = 4; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+      // this lane's value: (row, sum) = (lane bit 4, lane bit 3), or for one row the sum = lane bit 4
+      constexpr int LANES = R == 2 ? 8 : 16;
+      const int which = lane / LANES, k0 = lane % LANES;
+      if (warps > 1) {
+        if (k0 == 0) sh[turn][warp][which] = part;
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(width) : "memory");
+        part = 0.f;
+#pragma unroll
+        for (int k = 0; k < NB_THREADS / 32; k += LANES)
+          if (k0 + k < warps) part += sh[turn][warp0 + k0 + k][which];
+        turn ^= 1;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+      }
+      // dx = rstd t + (x - mean) c2 + c1
+      f32x2 c1[R], c2[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float m1 = -inv_d * __shfl_sync(0xFFFFFFFFu, part, 2 * i * LANES);
+        const float m2 = -inv_d * __shfl_sync(0xFFFFFFFFu, part, (2 * i + 1) * LANES);
+        c1[i] = both(m1 * st[i].y);
+        c2[i] = both(((m2 * st[i].y) * st[i].y) * st[i].y);
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        f32x2 w[HALF];
+        if (a.weight) w_shared.pairs(w, me, v);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (i > 0 && !pair) continue;
+          f32x2 z[HALF], t[HALF];
+          const f32x2 rstd = both(st[i].y);
+          terms(i, v, z, t);
+#pragma unroll
+          for (int e = 0; e < HALF; ++e) {
+            if (a.weight) t[e] = mul2(t[e], w[e]);
+            t[e] = fma2(t[e], rstd, fma2(z[e], c2[i], c1[i]));
+          }
+          C::store(out + i * a.y_ld, me, v, a.d, round_pairs<T>(t));
+        }
+      }
+      out += dx_step;
     }
-    st = stn;
+    x_row += x_step;
+    g_row += g_step;
+    stage = stage + 1 == NB_STAGES ? 0 : stage + 1;
   }
   if (!sums) return;
-  float* part = a.ws + (long long)blockIdx.x * 2 * a.d;
-  if (WARP) {
-    // the warps add theirs one after another
-    for (int r = 0; r < NB_WARPS; ++r) {
-      if ((int)(threadIdx.x >> 5) == r) {
+  // the block's sums: the groups add theirs one after another, in shared memory, the last one on its way out; in the
+  // order of the threads' columns, (v, e) major
+  float* part = a.ws + (long long)blockIdx.x * 2 * a.part_ld;
+  float* all = reinterpret_cast<float*>(norm_smem);
+  ring.template wait<0>();
+  for (int k = 0; k < groups; ++k) {
+    if (groups > 1) __syncthreads();
+    if (group != k) continue;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
 #pragma unroll
-          for (int e = 0; e < PER; ++e) {
-            float* q = s_sum + ((v * PER + e) * 32 + me) * 2;
-            q[0] = (r ? q[0] : 0.f) + dw[v][e];
-            q[1] = (r ? q[1] : 0.f) + db[v][e];
-          }
-      }
-      __syncthreads();
-    }
-    if (threadIdx.x >= 32) return;
-  }
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      const int id = C::col(me, width, v, e);
-      const float* q = s_sum + ((v * PER + e) * 32 + me) * 2;
-      if (id < a.d) {
-        part[id] = WARP ? q[0] : dw[v][e];
-        part[a.d + id] = WARP ? q[1] : db[v][e];
+      for (int e = 0; e < PER; ++e) {
+        float x = half_of(dw[v][e / 2], e & 1), y = half_of(db[v][e / 2], e & 1);
+        const int at = (v * PER + e) * width + me, other = NV * PER * width;
+        if (k > 0) {
+          x += all[at];
+          y += all[other + at];
+        }
+        float* to = k + 1 < groups ? all : part;
+        to[at] = x;
+        to[(k + 1 < groups ? other : a.part_ld) + at] = y;
       }
     }
   }
@@ -292,14 +553,14 @@ __global__ void __launch_bounds__(NW_THREADS) k_norm_wide(NormArgs a) {
     T* y = static_cast<T*>(a.y) + n * a.y_ld;
     float s = 0.f;
     for (int i = threadIdx.x; i < a.d; i += NW_THREADS) s += Elem<T>::to_f(x[i]);
-    const float mean0 = group_sum<false>(s, 0.f, sh, turn).x * inv_d;
+    const float mean0 = block_sum(s, 0.f, sh, turn).x * inv_d;
     float s1 = 0.f, s2 = 0.f;
     for (int i = threadIdx.x; i < a.d; i += NW_THREADS) {
       const float t = Elem<T>::to_f(x[i]) - mean0;
       s1 += t;
       s2 = fmaf(t, t, s2);
     }
-    const Moments q = moments(mean0, group_sum<false>(s1, s2, sh, turn), inv_d, a.eps);
+    const Moments q = moments(mean0, block_sum(s1, s2, sh, turn), inv_d, a.eps);
     if (a.stats_out && threadIdx.x == 0) a.stats_out[n] = make_float2(q.mean0 + q.delta, q.rstd);
     for (int i = threadIdx.x; i < a.d; i += NW_THREADS) {
       float z = ((Elem<T>::to_f(x[i]) - q.mean0) - q.delta) * q.rstd;
@@ -333,7 +594,7 @@ __global__ void __launch_bounds__(NW_THREADS) k_norm_backward_wide(NormArgs a, b
       s1 += t;
       s2 = fmaf(t, hat, s2);
     }
-    const float2 c = group_sum<false>(s1, s2, sh, turn);
+    const float2 c = block_sum(s1, s2, sh, turn);
     const float c1 = c.x * inv_d, c2 = c.y * inv_d;
     for (int i = threadIdx.x; i < a.d; i += NW_THREADS) {
       const float t = terms(i, &hat);
@@ -359,70 +620,141 @@ __global__ void __launch_bounds__(NC_THREADS) k_norm_columns(NormArgs a) {
     dw = fmaf(q, (Elem<T>::to_f(x[n * a.ld]) - st.x) * st.y, dw);
     db += q;
   }
-  float* part = a.ws + (long long)blockIdx.y * 2 * a.d;
+  float* part = a.ws + (long long)blockIdx.y * 2 * a.part_ld;
   part[col] = dw;
-  part[a.d + col] = db;
+  part[a.part_ld + col] = db;
 }
 
-// The blocks' sums, added in a fixed order and rounded once.
-constexpr int NJ_COLS = 32, NJ_ROWS = 16;
+// The blocks' sums, added in a fixed order and rounded once.  They stand in the order of the threads' columns, nv
+// vectors of `per` of a thread and `width` threads (nv 0: in the order of the columns).
+constexpr int NJ_COLS = 32, NJ_ROWS = 32;
 template <typename P>
-__global__ void __launch_bounds__(NJ_COLS * NJ_ROWS) k_norm_join(NormArgs a, int parts) {
-  __shared__ float sh[NJ_ROWS][NJ_COLS];
+__global__ void __launch_bounds__(NJ_COLS * NJ_ROWS) k_norm_join(NormArgs a, int parts, int width, int nv, int per,
+                                                                 bool vec) {
+  __shared__ float sh[NJ_ROWS][NJ_COLS + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int col = blockIdx.x * NJ_COLS + (threadIdx.x & 31), row = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, at = blockIdx.x * NJ_COLS + lane;
   P* out = static_cast<P*>(blockIdx.y ? a.grad_bias : a.grad_weight);
   if (!out) return;
+  const float* from = a.ws + blockIdx.y * a.part_ld + at;
   float s = 0.f;
-  if (col < a.d)
-    for (int i = row; i < parts; i += NJ_ROWS) s += a.ws[((long long)i * 2 + blockIdx.y) * a.d + col];
-  sh[row][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (row == 0 && col < a.d) {
-    float t = 0.f;
-#pragma unroll
-    for (int r = 0; r < NJ_ROWS; ++r) t += sh[r][threadIdx.x];
-    out[col] = Elem<P>::from_f(t);
+  if (at < a.part_ld) {
+#pragma unroll 8
+    for (int i = row; i < parts; i += NJ_ROWS) s += from[(long long)i * 2 * a.part_ld];
   }
+  sh[row][lane] = s;
+  __syncthreads();
+  // warp r adds up column r: lane l has part l's sum
+  const float t = warp_sum(sh[lane][row]);
+  if (lane != 0) return;
+  const int mine = blockIdx.x * NJ_COLS + row;
+  int id = mine;
+  if (nv > 0) {
+    const int thread = mine % width, ve = mine / width;
+    id = (thread >> 5) * (32 * nv * per) +
+         (vec ? ((ve / per) * 32 + (thread & 31)) * per + ve % per : ve * 32 + (thread & 31));
+  }
+  if (id < a.d) out[id] = Elem<P>::from_f(t);
 }
 
-constexpr int NM_PARTS = 512;  // blocks that leave sums, at most
+// Blocks that leave sums, at most: 2^22 columns of them, or 512.
+int norm_parts(int d) { return (1 << 22) / d < 512 ? (1 << 22) / d : 512; }
 
 int round32(int x) { return (x + 31) / 32 * 32; }
 unsigned least(long long a, long long b) { return (unsigned)(a < b ? a : b); }
+
+// Lets a kernel take as much shared memory as the device has, once per (kernel, device).
+cudaError_t allow_ring(const void* kernel, int device) {
+  static std::mutex mu;
+  static std::vector<std::pair<const void*, int>> done;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const auto& d : done)
+    if (d.first == kernel && d.second == device) return cudaSuccess;
+  int most = 0;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return note_error(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
+  done.emplace_back(kernel, device);
+  return cudaSuccess;
+}
+// Launches a kernel whose ring takes `smem` bytes of shared memory.
+template <class Kernel, class... A>
+cudaError_t launch_ring(const Ctx& c, const char* name, Kernel* kernel, unsigned grid, unsigned threads, size_t smem,
+                        A... args) {
+  const cudaError_t e = smem > 0 ? allow_ring(reinterpret_cast<const void*>(kernel), c.device) : cudaSuccess;
+  return e != cudaSuccess ? e : launch_pdl(c, name, kernel, dim3(grid), dim3(threads), smem, args...);
+}
+
+constexpr int SM_SMEM = 220 * 1024;  // of an SM's shared memory, for the rings of its blocks
+
+template <typename T, typename P, bool VEC, int NV>
+cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
+  const int width = round32((nvec + NV - 1) / NV);
+  const size_t ring = NF_STAGES * Ring<T, VEC, NV>::bytes(width), shared = 2 * SharedParams<T, P, VEC, NV>::bytes(width);
+  if (few)
+    return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false>, (unsigned)a.N, (unsigned)width, ring, a, width);
+  long long groups = least(1024, 65536 / norm_regs(NV)) / width;
+  if (ring && shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
+  groups = least(groups < 1 ? 1 : groups, 15);  // a barrier each
+  const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
+  return launch_ring(c, "norm", k_norm<T, P, NV, VEC, true>, grid, (unsigned)(width * groups), shared + ring * groups, a,
+                     width);
+}
 
 template <typename T, typename P, bool VEC>
 cudaError_t run_norm(const Ctx& c, const NormArgs& a) {
   constexpr int PER = Elem<T>::PER16;
   const int nvec = (a.d + PER - 1) / PER;
-  auto go = [&](auto* kernel, unsigned grid, unsigned threads) {
-    return launch_pdl(c, "norm", kernel, dim3(grid), dim3(threads), 0, a);
-  };
-  const unsigned by_warp = least(((long long)a.N + NF_WARPS - 1) / NF_WARPS, 12LL * c.num_sms);
-  if (nvec <= 32) return go(k_norm<T, P, 1, true, VEC>, by_warp, 32 * NF_WARPS);
-  if (nvec <= 128) return go(k_norm<T, P, 4, true, VEC>, by_warp, 32 * NF_WARPS);
-  const int nv = nvec <= 640 ? 1 : 2, threads = round32((nvec + nv - 1) / nv);
-  const unsigned by_block = least(a.N, (long long)c.num_sms * (2048 / threads > 8 ? 8 : 2048 / threads));
-  return nv == 1 ? go(k_norm<T, P, 1, false, VEC>, by_block, (unsigned)threads)
-                 : go(k_norm<T, P, 2, false, VEC>, by_block, (unsigned)threads);
+  // one row per block and no parameters in shared memory where there are few rows
+  const bool few = a.N <= 2 * c.num_sms;
+  if (nvec <= 32) return run_norm_nv<T, P, VEC, 1>(c, a, nvec, few);
+  if (nvec <= 64 || (few && nvec <= 2 * 32 * NF_WARPS)) return run_norm_nv<T, P, VEC, 2>(c, a, nvec, few);
+  return run_norm_nv<T, P, VEC, 4>(c, a, nvec, few);
+}
+
+// How the backward pass left its sums.
+struct JoinPlan {
+  int parts, width, nv, per;
+  bool vec;
+};
+
+template <typename T, typename P, bool VEC, int NV>
+cudaError_t run_backward_nv(const Ctx& c, NormArgs& a, bool sums, JoinPlan* join, int nvec) {
+  constexpr int PER = Elem<T>::PER16, R = sizeof(T) == 4 ? 1 : 2;
+  const int width = round32((nvec + NV - 1) / NV);
+  const size_t ring = NB_STAGES * 2 * R * Ring<T, VEC, NV>::bytes(width), shared = SharedParams<T, P, VEC, NV>::bytes(width);
+  const long long units = ((long long)a.N + R - 1) / R;
+  long long groups = NB_THREADS / width;
+  if (ring && shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
+  groups = least(groups < 1 ? 1 : groups, 15);  // a barrier each
+  // few rows: on as many SMs as there are
+  if (units < c.num_sms * groups) groups = (units + c.num_sms - 1) / c.num_sms;
+  size_t smem = shared + ring * groups;
+  const size_t joined = (size_t)width * NV * PER * 2 * sizeof(float);  // the groups' sums
+  if (groups > 1 && joined > smem) smem = joined;
+  *join = {(int)least((units + groups - 1) / groups, least(norm_parts(a.d), c.num_sms)), width, NV, PER, VEC};
+  a.part_ld = width * NV * PER;
+  return launch_ring(c, "norm_backward", k_norm_backward<T, P, NV, VEC>, (unsigned)join->parts,
+                     (unsigned)(width * groups), smem, a, width, sums);
 }
 
 template <typename T, typename P, bool VEC>
-cudaError_t run_norm_backward(const Ctx& c, const NormArgs& a, bool sums, int* parts) {
-  constexpr int PER = Elem<T>::PER16;
-  const int nvec = (a.d + PER - 1) / PER;
-  auto go = [&](auto* kernel, unsigned grid, unsigned threads) {
-    *parts = (int)grid;
-    return launch_pdl(c, "norm_backward", kernel, dim3(grid), dim3(threads), 0, a, sums);
-  };
-  const unsigned by_warp = least(((long long)a.N + NB_WARPS - 1) / NB_WARPS, least(NM_PARTS, 3LL * c.num_sms));
-  if (nvec <= 32) return go(k_norm_backward<T, P, 1, true, VEC>, by_warp, 32 * NB_WARPS);
-  const int nv = nvec <= NB_THREADS ? 1 : nvec <= 2 * NB_THREADS ? 2 : 4, threads = round32((nvec + nv - 1) / nv);
-  const unsigned by_block = least(a.N, least(NM_PARTS, (long long)c.num_sms * (1024 / threads > 8 ? 8 : 1024 / threads)));
-  if (nv == 1) return go(k_norm_backward<T, P, 1, false, VEC>, by_block, (unsigned)threads);
-  if (nv == 2) return go(k_norm_backward<T, P, 2, false, VEC>, by_block, (unsigned)threads);
-  if constexpr (sizeof(T) == 4) return go(k_norm_backward<T, P, 4, false, VEC>, by_block, (unsigned)threads);
-  return cudaErrorInvalidValue;  // not reached: 8192 bf16 columns are 1024 vectors
+cudaError_t run_norm_backward(const Ctx& c, NormArgs& a, bool sums, JoinPlan* join) {
+  const int nvec = (a.d + Elem<T>::PER16 - 1) / Elem<T>::PER16;
+  if constexpr (sizeof(T) == 4) {
+    if (nvec <= 512) return run_backward_nv<T, P, VEC, 2>(c, a, sums, join, nvec);
+    return run_backward_nv<T, P, VEC, 4>(c, a, sums, join, nvec);
+  } else {
+    const int two = round32((nvec + 1) / 2), three = round32((nvec + 2) / 3);
+    if (NB_THREADS / two * two * 5 / 4 >= NB_THREADS / three * three)
+      return run_backward_nv<T, P, VEC, 2>(c, a, sums, join, nvec);
+    return run_backward_nv<T, P, VEC, 3>(c, a, sums, join, nvec);
+  }
 }
 
 bool params16(const void* w, const void* b) {
@@ -439,9 +771,10 @@ cudaError_t pick_norm(const Ctx& c, const NormArgs& a) {
 }
 
 template <typename T, typename P>
-cudaError_t pick_backward(const Ctx& c, const NormArgs& a) {
+cudaError_t pick_backward(const Ctx& c, NormArgs a) {
   const bool sums = a.grad_weight || a.grad_bias;
-  int parts = 0;
+  JoinPlan join = {};
+  a.part_ld = a.d;
   cudaError_t e = cudaSuccess;
   if (a.N == 0) {
     // sums of no rows: the joining kernel writes zeros
@@ -449,13 +782,13 @@ cudaError_t pick_backward(const Ctx& c, const NormArgs& a) {
     const bool vec = params16(a.weight, nullptr) && whole_vectors(a.x, a.ld, a.N, a.d, sizeof(T)) &&
                      whole_vectors(a.grad, a.grad_ld, a.N, a.d, sizeof(T)) &&
                      (!a.y || whole_vectors(a.y, a.y_ld, a.N, a.d, sizeof(T)));
-    e = vec ? run_norm_backward<T, P, true>(c, a, sums, &parts) : run_norm_backward<T, P, false>(c, a, sums, &parts);
+    e = vec ? run_norm_backward<T, P, true>(c, a, sums, &join) : run_norm_backward<T, P, false>(c, a, sums, &join);
   } else {
     // the columns' sums first: the gradient may overwrite the rows
     if (sums) {
       const int tiles = (a.d + NC_THREADS - 1) / NC_THREADS, shares = 8 * c.num_sms / tiles;
-      parts = (int)least(a.N, least(NM_PARTS, shares < 1 ? 1 : shares));
-      e = launch_pdl(c, "norm_columns", k_norm_columns<T>, dim3((unsigned)tiles, (unsigned)parts), dim3(NC_THREADS), 0,
+      join.parts = (int)least(a.N, least(norm_parts(a.d), shares < 1 ? 1 : shares));
+      e = launch_pdl(c, "norm_columns", k_norm_columns<T>, dim3((unsigned)tiles, (unsigned)join.parts), dim3(NC_THREADS), 0,
                      a);
     }
     if (e == cudaSuccess && a.y)
@@ -463,14 +796,15 @@ cudaError_t pick_backward(const Ctx& c, const NormArgs& a) {
                      dim3(NW_THREADS), 0, a, sums);
   }
   if (e != cudaSuccess || !sums) return e;
-  return launch_pdl(c, "norm_join", k_norm_join<P>, dim3((unsigned)((a.d + NJ_COLS - 1) / NJ_COLS), 2u),
-                    dim3(NJ_COLS * NJ_ROWS), 0, a, parts);
+  return launch_pdl(c, "norm_join", k_norm_join<P>, dim3((unsigned)((a.part_ld + NJ_COLS - 1) / NJ_COLS), 2u),
+                    dim3(NJ_COLS * NJ_ROWS), 0, a, join.parts, join.width, join.nv, join.per, join.vec);
 }
 
 }  // namespace
 
+// (a block's threads have up to 1024 columns more than the row)
 size_t norm_backward_workspace(int N, int d, int) {
-  return WS_HEADER + align_up((size_t)(N < NM_PARTS ? N : NM_PARTS) * 2 * d * sizeof(float), 256);
+  return WS_HEADER + align_up((size_t)least(N, norm_parts(d)) * 2 * (d + 1024) * sizeof(float), 256);
 }
 
 cudaError_t launch_norm(const Ctx& c, const NormArgs& a, int dtype, int param_dtype) {
