@@ -2,16 +2,22 @@
 // at dh_sample in dh.h).
 //
 // In the order of a row's tokens by (logit desc, id asc) every filter keeps a prefix, and the drawn token is the
-// one at which the prefix's running sum of weights passes u times its mass.  So everything is a search for a
-// place in that order: by count (top-k) or by mass (top-p, the draw).  A search descends over the order-preserving
-// keys of the logits: a histogram of at most 2048 bins over a range of keys (counts and masses), the bin that holds
-// the place, then that bin's keys, until one key is left; tokens of one key have one weight, so the place among
-// them is a division, and their order is that of the ids.
+// one at which the prefix's running sum of weights passes u times its mass.  So a token far down the order matters
+// only by its share of the row's mass, and that only where no top-k leaves it out.
+//   k_sample_scan   the one pass over the logits: the largest of every group of 16 vectors and, of rows whose mass
+//                   is needed, every segment's mass.  Its bound is HBM; with masses, the instructions of the weights.
+//   k_sample_pick   a block per row.  A bound below which nothing can be drawn: the top_k-th largest group maximum,
+//                   or a histogram of masses.  The tokens that reach it are listed, sorted, weighted and summed, and
+//                   the filters and the draw are places in that list.
+// Rows whose list would not fit are searched instead: a histogram (counts and masses) over a range of
+// order-preserving keys, the bin that holds the place, then that bin's keys, until one key is left; tokens of one
+// key have one weight, so the place among them is a division, and their order is that of the ids.
+// Rows of few segments are scanned by the block that picks, in one launch.
 //
 // Which token a uniform falls on hangs on the running sums, so the weights exp((z - max)/T) are integers: fixed
-// point with S fraction bits relative to a power of two near the largest, S = 62 - log2(vocab), so that a row's
-// masses fit 64 bits.  Their sums are exact, whatever the order of the atomics.  2^(z c), c = log2(e)/T, is taken as
-// 2^(k/64) 2^r with k the rounded 64 z c: 2^(k/64) from a table, exact to 2^-29, and 2^r - 1, |r| < 2^-7 + 2^-9,
+// point with `frac` fraction bits relative to a power of two near the largest, frac = 62 - log2(vocab) (52 at most),
+// so that a row's masses fit 64 bits.  Their sums are exact, whatever their order.  2^(z c), c = log2(e)/T, is taken
+// as 2^(k/64) 2^r with k the rounded 64 z c: 2^(k/64) from a table, exact to 2^-29, and 2^r - 1, |r| < 2^-7 + 2^-9,
 // by a cubic in fp32 whose rounding is below 2^-29 of the weight; c in two floats, so that z c is exact to 2^-31.
 #include "layers.cuh"
 #include "rows.cuh"
@@ -22,6 +28,10 @@ namespace {
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 2048;
+constexpr int SP_LIST = 4096;    // tokens listed, at most
+constexpr int SP_GROUPS = 2048;  // groups listed, at most
+constexpr int SEG_GROUPS = 8;    // groups of a segment: four lanes' vectors each
+constexpr int SEG_FRAC = 52;     // fraction bits of a segment's mass, relative to 2^e of its own largest weight
 
 using u64 = unsigned long long;
 
@@ -51,51 +61,88 @@ __device__ const ExpTable g_exp_table = make_table();
 constexpr float EXP_MAGIC = 196608.f;  // 1.5 2^17: adding it rounds to multiples of 1/64
 constexpr int EXP_MAGIC_BITS = 0x48400000;
 
-// The weights of a row whose largest logit is m at temperature t.  z c has to stay below 2^15 for the fp32 form;
-// beyond that (huge logits, tiny temperatures) `far` takes 64-bit arithmetic.
+// log2(e) / t in two floats.
+struct Rate {
+  float hi, lo;
+  __device__ __forceinline__ explicit Rate(float t) : hi(1.44269502f / t) {
+    lo = (fmaf(-hi, t, 1.44269502f) + 1.92596299e-8f) / t;
+  }
+};
+
+// The weights of a row whose largest logit is m at temperature t.  z c has to stay below 2^15 for the fp32 form, and
+// the logits whose weights count above the type's lowest; beyond that (huge logits, tiny and huge temperatures)
+// `far` takes 64-bit arithmetic.
 struct Weights {
-  float ch, cl, zlow;
+  Rate c;
+  float m, t, zlow;
   int e_ref, frac;  // the largest weight is in [2^frac, 2^(frac + 1)]
   bool far;
-  double m, c;
   const ExpTable* tab;  // in shared memory
-  __device__ Weights(float m_, float t, int frac_, const ExpTable* tab_) : frac(frac_), m(m_), tab(tab_) {
-    c = 1.4426950408889634 / (double)t;
-    ch = (float)c;
-    cl = (float)(c - (double)ch);
-    far = !(fabs(m * c) < 32000.0 && c < 1e38);
-    const double low = m - (frac + 2) / c;  // weights below 2^-(frac + 1)
-    zlow = low < -3.4e38 ? -3.4028234e38f : (float)low;
-    e_ref = 0;
-    if (!far) e_ref = (__float_as_int(fmaf(m_, ch, EXP_MAGIC)) - EXP_MAGIC_BITS) >> 6;
+  __device__ __forceinline__ Weights(float m_, float t_, int frac_, const ExpTable* tab_)
+      : c(t_), m(m_), t(t_), frac(frac_), tab(tab_) {
+    const float reach = (float)(frac + 2) / c.hi;  // what is lower than m by that much weighs below 2^-(frac + 1)
+    far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e38f && reach + fabsf(m) < 1.5e38f);
+    zlow = far ? -3.4028234e38f : m - reach;
+    e_ref = far ? 0 : (__float_as_int(fmaf(m, c.hi, EXP_MAGIC)) - EXP_MAGIC_BITS) >> 6;
+  }
+  // far: the weight's 28 bits and how far down they are (64 and more: 0)
+  __device__ __noinline__ static uint32_t slow(float z, float m, float t, int* down) {
+    const double x = ((double)z - (double)m) * (1.4426950408889634 / (double)t), e = floor(x);
+    if (!(e > -64.0)) {
+      *down = 64;
+      return 0;
+    }
+    *down = -(int)e;
+    return (uint32_t)rint(exp2(x - e) * 268435456.0);
   }
   __device__ __forceinline__ u64 operator()(float z) const {
     if (!(z >= zlow)) return 0;
     uint32_t q;
     int down;
     if (__builtin_expect(far, 0)) {
-      const double x = ((double)z - m) * c, e = floor(x);
-      if (!(e > -64.0)) return 0;
-      q = (uint32_t)rint(exp2(x - e) * 268435456.0);
-      down = -(int)e;
+      q = slow(z, m, t, &down);
     } else {
-      const float k = fmaf(z, ch, EXP_MAGIC), kf = k - EXP_MAGIC;
-      const float r = fmaf(z, cl, fmaf(z, ch, -kf));
+      const float k = fmaf(z, c.hi, EXP_MAGIC), kf = k - EXP_MAGIC;
+      const float r = fmaf(z, c.lo, fmaf(z, c.hi, -kf));
       const int ki = __float_as_int(k) - EXP_MAGIC_BITS, j = ki & 63;
       // 2^r - 1 by its series
       const float x = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
       // added to 1.5 2^23, which rounds to an integer in the low bits; |tab.f x| < 2^22
       q = tab->q[j] + (uint32_t)(__float_as_int(fmaf(tab->f[j], x, 12582912.f)) - 0x4B400000);
-      down = min(e_ref - (ki >> 6), 63);
+      down = e_ref - (ki >> 6);
     }
-    return ((u64)q << (frac - 28)) >> down;
+    // 28 fraction bits to frac, and down; rounded
+    const int left = frac - 28 - down;
+    if (left >= 0) return (u64)q << left;
+    return left < -31 ? 0 : (q + (1u << (-left - 1))) >> -left;
   }
 };
+
+// x mass rounded down, and whether something was left over, exactly, for 0 <= x < 1.
+__device__ __forceinline__ u64 times(float x, u64 mass, bool* rest) {
+  const uint32_t bits = __float_as_uint(x);
+  const u64 n = (bits & 0x7FFFFFu) | 0x800000u;
+  const int s = 150 - (int)(bits >> 23);  // x = n 2^-s
+  const u64 lo = n * mass, hi = __umul64hi(n, mass);
+  *rest = x > 0.f;
+  if (bits < 0x00800000u || s > 87) return 0;  // below 2^-87
+  if (s >= 64) {
+    *rest = lo != 0 || (s > 64 && (hi << (128 - s)) != 0);
+    return hi >> (s - 64);
+  }
+  *rest = (lo << (64 - s)) != 0;
+  return (hi << (64 - s)) | (lo >> s);
+}
 
 // Order-preserving keys: of fp32 logits 32 bits, of bf16 logits 16.
 template <typename T>
 __device__ __forceinline__ uint32_t key_of(float z) {
   return sizeof(T) == 4 ? fkey(z) : fkey(z) >> 16;
+}
+template <typename T>
+__device__ __forceinline__ float value_of(uint32_t key) {
+  if (sizeof(T) == 4) return fkey_inv(key);
+  return fkey_inv((key & 0x8000u) ? key << 16 : (key << 16) | 0xFFFFu);
 }
 // The smallest key of T whose value is at least x.
 template <typename T>
@@ -106,18 +153,142 @@ __device__ __forceinline__ uint32_t key_at_least(float x) {
   return (k & 0x80000000u) ? (k + 0xFFFFu) >> 16 : k >> 16;
 }
 
+// ------------------------------------------------------------------ the pass over the logits
+
+// A segment's mass, in units of 2^(e - SEG_FRAC).
+struct SegMass {
+  u64 mass;
+  int e;
+  int pad;
+};
+
+// What of a row's settings asks for: its whole mass (no top-k bounds what is kept, and what is kept or drawn is a
+// share of all).
+__device__ __forceinline__ bool needs_mass(float t, int top_k, float top_p, float min_p, int vocab) {
+  return t > 0.f && !(top_k >= 1 && top_k < vocab) && top_p > 0.f && (top_p < 1.f || !(min_p > 0.f));
+}
+
+// The table of 2^(j/64), a copy for each of 16 lanes so that a warp's look-ups do not meet in a bank.
+struct ScanTable {
+  uint2 e[64 * 16];
+};
+__device__ __forceinline__ void fill_table(ScanTable& t, int threads) {
+  for (int i = threadIdx.x; i < 64 * 16; i += threads)
+    t.e[i] = make_uint2(g_exp_table.q[i >> 4], __float_as_uint(g_exp_table.f[i >> 4]));
+}
+
+// Segment sgi of a row by one warp: the maxima of its groups (lanes 4 g .. 4 g + 3 have group g's) and, if `mass`,
+// its mass at temperature t.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, float t, bool mass, const ScanTable& tab,
+                                             float* gmax, SegMass* seg) {
+  constexpr int PER = Elem<T>::PER16;
+  const int lane = threadIdx.x & 31;
+  const int id0 = sgi * row_seg<T>() + lane * PER;
+  uint4 u[ROW_SEG_VECS];
+#pragma unroll
+  for (int v = 0; v < ROW_SEG_VECS; ++v) u[v] = row_vec<T, ALIGNED>(row, id0 + v * 32 * PER, vocab);
+  float m = vec_max<T>(u);
+  m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  if ((lane & 3) == 0) gmax[sgi * SEG_GROUPS + (lane >> 2)] = m;
+  if (!mass) return;
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const Rate c(t);
+  const float ch = c.hi, cl = c.lo, reach = (float)(SEG_FRAC + 2) / ch;  // what is lower than m by that much counts as 0
+  u64 sum = 0;
+  int e_ref = -0x40000000;
+  // beyond, and so beyond the limits of Weights: the row's weights are taken in 64 bits by the block that picks, or
+  // its largest logit is so far above this segment's that their weights are 0
+  if (fabsf(m * ch) < 32700.f && ch < 1e38f && reach + fabsf(m) < 3.3e38f) {
+    e_ref = (__float_as_int(fmaf(m, ch, EXP_MAGIC)) - EXP_MAGIC_BITS) >> 6;
+    const float low = m - reach;
+    const uint2* tb = tab.e + (lane & 15);
+    const f32x2 cc = pack2(ch, ch), cd = pack2(cl, cl), magic = pack2(EXP_MAGIC, EXP_MAGIC);
+    const f32x2 nmagic = pack2(-EXP_MAGIC, -EXP_MAGIC), none = pack2(-1.f, -1.f);
+    const f32x2 c3 = pack2(0.0555041087f, 0.0555041087f), c2 = pack2(0.240226507f, 0.240226507f),
+                c1 = pack2(0.693147181f, 0.693147181f);
+    const int base = e_ref + (EXP_MAGIC_BITS >> 6) + 8;  // with 2^24 of the 2^52, counted from bit 32
+#pragma unroll
+    for (int v = 0; v < ROW_SEG_VECS; ++v) {
+      float x[PER];
+      Elem<T>::unpack(u[v], x);
+#pragma unroll
+      for (int q = 0; q < PER; q += 2) {
+        const f32x2 z = pack2(fmaxf(x[q], low), fmaxf(x[q + 1], low));
+        const f32x2 k = fma2(z, cc, magic), kf = add2(k, nmagic);
+        const f32x2 r = fma2(z, cd, fma2(z, cc, mul2(kf, none)));
+        const f32x2 y = mul2(r, fma2(r, fma2(r, c3, c2), c1));
+        float ka, kb, ya, yb;
+        unpack2(k, ka, kb);
+        unpack2(y, ya, yb);
+        auto one = [&](float kx, float yx) {
+          const int ki = __float_as_int(kx);
+          const uint2 w = tb[(ki & 63) * 16];
+          const uint32_t n = w.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(w.y), yx, 12582912.f)) - 0x4B400000);
+          // n 2^24 >> (e_ref - e), from n 2^32
+          sum += ((u64)n << 32) >> min(base - (ki >> 6), 63);
+        };
+        one(ka, ya);
+        one(kb, yb);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) seg[sgi] = {sum, e_ref, 0};
+}
+
+constexpr int SC_THREADS = 256;
+
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(SC_THREADS) k_sample_scan(SampleArgs a, int n_seg, float* gmax, SegMass* segs) {
+  __shared__ ScanTable tab;
+  fill_table(tab, SC_THREADS);
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the picking kernel follows
+  const unsigned nw = gridDim.x * (SC_THREADS / 32);
+  const unsigned long long items = (unsigned long long)a.N * n_seg;
+  for (unsigned long long g = blockIdx.x * (SC_THREADS / 32) + (threadIdx.x >> 5); g < items; g += nw) {
+    int n, sgi;
+    if (items < 0x7F000000ull) {
+      n = (int)((unsigned)g / (unsigned)n_seg);
+      sgi = (int)((unsigned)g - (unsigned)n * (unsigned)n_seg);
+    } else {
+      n = (int)(g / n_seg);
+      sgi = (int)(g - (unsigned long long)n * n_seg);
+    }
+    const float t = a.temperature ? __ldg(a.temperature + n) : a.temperature0;
+    const bool mass = needs_mass(t, a.top_k ? __ldg(a.top_k + n) : a.top_k0, a.top_p ? __ldg(a.top_p + n) : a.top_p0,
+                                 a.min_p ? __ldg(a.min_p + n) : a.min_p0, a.vocab);
+    scan_segment<T, ALIGNED>(static_cast<const T*>(a.logits) + n * a.ld, sgi, a.vocab, t, mass, tab,
+                             gmax + (long long)n * n_seg * SEG_GROUPS, segs + (long long)n * n_seg);
+  }
+}
+
 // ------------------------------------------------------------------ the search
 
 struct SampleSmem {
-  u64 mass[SP_BINS];
-  uint32_t count[SP_BINS];
+  union {
+    struct {
+      u64 mass[SP_BINS];
+      uint32_t count[SP_BINS];
+    };
+    u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
+  };
+  uint32_t groups[SP_GROUPS];
   ExpTable tab;
   u64 warp_mass[SP_WARPS];
   uint32_t warp_count[SP_WARPS];
-  float warp_max[SP_WARPS];
+  float warp_max[SP_WARPS], warp_min[SP_WARPS];
   int bin, last;
   u64 bin_mass, above_mass;
   uint32_t bin_count, above_count;
+  uint32_t n_list, n_groups;
+  u64 found_mass, found_w;
+  uint32_t found_at, found_id;
 };
 
 // A place in the order: all tokens above `key`, of which there are `above` with mass `above_mass`, and the tokens
@@ -127,7 +298,7 @@ struct Place {
   u64 above_mass, w;
 };
 
-// f(value, id) of every logit of the row.
+// f(value) of every logit of the row (-inf past its end).
 template <typename T, bool ALIGNED, typename F>
 __device__ __forceinline__ void each(const T* row, int vocab, F f) {
   constexpr int PER = Elem<T>::PER16;
@@ -139,111 +310,127 @@ __device__ __forceinline__ void each(const T* row, int vocab, F f) {
   }
 }
 
+// The bin, of 2^sh keys from the top down, of the keys [lo, hi] in which `want` is reached: tokens (BY_COUNT) or a
+// mass of want or more (STRICT: more than want), counted on from `above` tokens of `above_mass`; the last bin with a
+// token where it is not.
+struct Histogram {
+  int bin, sh;
+  uint32_t above, count;
+  u64 above_mass, mass;
+};
+template <typename T, bool ALIGNED, bool BY_COUNT, bool STRICT>
+__device__ __noinline__ Histogram histogram(SampleSmem& s, const T* row, int vocab, uint32_t lo, uint32_t hi,
+                                            uint32_t above, u64 above_mass, u64 want, const Weights& weight) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bits = 32 - __clz(hi - lo), sh = bits > 11 ? bits - 11 : 0;
+  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) {
+    s.mass[b] = 0;
+    s.count[b] = 0;
+  }
+  if (threadIdx.x == 0) s.bin = s.last = -1;
+  __syncthreads();
+  each<T, ALIGNED>(row, vocab, [&](float z) {
+    const uint32_t k = key_of<T>(z);
+    if (k >= lo && k <= hi) {
+      const uint32_t b = (hi - k) >> sh;
+      atomicAdd(&s.count[b], 1u);
+      const u64 w = weight(z);
+      if (w) atomicAdd(&s.mass[b], w);
+    }
+  });
+  __syncthreads();
+  // inclusive sums over the bins, four to a thread
+  constexpr int OWN = SP_BINS / SP_THREADS;
+  u64 m = 0;
+  uint32_t c = 0;
+  const int b0 = threadIdx.x * OWN;
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    m += s.mass[b0 + q];
+    c += s.count[b0 + q];
+  }
+  u64 mi = m;
+  uint32_t ci = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 x = __shfl_up_sync(0xFFFFFFFFu, mi, o);
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, ci, o);
+    if (lane >= o) {
+      mi += x;
+      ci += y;
+    }
+  }
+  if (lane == 31) {
+    s.warp_mass[warp] = mi;
+    s.warp_count[warp] = ci;
+  }
+  __syncthreads();
+  u64 ma = above_mass + mi - m;
+  uint32_t ca = above + ci - c;
+  for (int w = 0; w < warp; ++w) {
+    ma += s.warp_mass[w];
+    ca += s.warp_count[w];
+  }
+  auto reached = [&](u64 mass, uint32_t count) {
+    return BY_COUNT ? count >= want : STRICT ? mass > want : mass >= want;
+  };
+  int last = -1;
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    const u64 mb = s.mass[b0 + q];
+    const uint32_t cb = s.count[b0 + q];
+    if (cb) last = b0 + q;
+    if (!reached(ma, ca) && reached(ma + mb, ca + cb)) {
+      s.bin = b0 + q;
+      s.bin_mass = mb;
+      s.bin_count = cb;
+      s.above_mass = ma;
+      s.above_count = ca;
+    }
+    ma += mb;
+    ca += cb;
+  }
+  if (last >= 0) atomicMax(&s.last, last);
+  __syncthreads();
+  if (s.bin < 0) {
+    // the sums never reach it: the last bin that holds a token
+    if (s.last >= b0 && s.last < b0 + OWN) {
+      for (int q = OWN - 1; b0 + q > s.last; --q) {
+        ma -= s.mass[b0 + q];
+        ca -= s.count[b0 + q];
+      }
+      s.bin_mass = s.mass[s.last];
+      s.bin_count = s.count[s.last];
+      s.above_mass = ma - s.bin_mass;
+      s.above_count = ca - s.bin_count;
+    }
+    __syncthreads();
+  }
+  const Histogram h = {s.bin < 0 ? s.last : s.bin, sh, s.above_count, s.bin_count, s.above_mass, s.bin_mass};
+  __syncthreads();
+  return h;
+}
+
 // The first place with `want` tokens or more (BY_COUNT), or with a mass of want or more (STRICT: more than want),
 // among the keys [lo, hi]; the last place where there is none.  hi is the row's largest key.
 template <typename T, bool ALIGNED, bool BY_COUNT, bool STRICT>
 __device__ __noinline__ Place descend(SampleSmem& s, const T* row, int vocab, uint32_t lo, uint32_t hi, u64 want,
                                       const Weights& weight) {
-  u64 above_mass = 0;
-  uint32_t above = 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Place p = {};
   for (;;) {
-    const int bits = 32 - __clz(hi - lo), sh = bits > 11 ? bits - 11 : 0;
-    for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) {
-      s.mass[b] = 0;
-      s.count[b] = 0;
-    }
-    if (threadIdx.x == 0) s.bin = s.last = -1;
-    __syncthreads();
-    each<T, ALIGNED>(row, vocab, [&](float z) {
-      const uint32_t k = key_of<T>(z);
-      if (k >= lo && k <= hi) {
-        const uint32_t b = (hi - k) >> sh;
-        atomicAdd(&s.count[b], 1u);
-        const u64 w = weight(z);
-        if (w) atomicAdd(&s.mass[b], w);
-      }
-    });
-    __syncthreads();
-    // inclusive sums over the bins, four to a thread
-    constexpr int OWN = SP_BINS / SP_THREADS;
-    u64 m = 0;
-    uint32_t c = 0;
-    const int b0 = threadIdx.x * OWN;
-#pragma unroll
-    for (int q = 0; q < OWN; ++q) {
-      m += s.mass[b0 + q];
-      c += s.count[b0 + q];
-    }
-    u64 mi = m;
-    uint32_t ci = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 x = __shfl_up_sync(0xFFFFFFFFu, mi, o);
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, ci, o);
-      if (lane >= o) {
-        mi += x;
-        ci += y;
-      }
-    }
-    if (lane == 31) {
-      s.warp_mass[warp] = mi;
-      s.warp_count[warp] = ci;
-    }
-    __syncthreads();
-    u64 ma = above_mass + mi - m;
-    uint32_t ca = above + ci - c;
-    for (int w = 0; w < warp; ++w) {
-      ma += s.warp_mass[w];
-      ca += s.warp_count[w];
-    }
-    auto reached = [&](u64 mass, uint32_t count) {
-      return BY_COUNT ? count >= want : STRICT ? mass > want : mass >= want;
-    };
-    int last = -1;
-#pragma unroll
-    for (int q = 0; q < OWN; ++q) {
-      const u64 mb = s.mass[b0 + q];
-      const uint32_t cb = s.count[b0 + q];
-      if (cb) last = b0 + q;
-      if (!reached(ma, ca) && reached(ma + mb, ca + cb)) {
-        s.bin = b0 + q;
-        s.bin_mass = mb;
-        s.bin_count = cb;
-        s.above_mass = ma;
-        s.above_count = ca;
-      }
-      ma += mb;
-      ca += cb;
-    }
-    if (last >= 0) atomicMax(&s.last, last);
-    __syncthreads();
-    if (s.bin < 0) {
-      // the sums never reach it: the last bin that holds a token
-      if (s.last >= b0 && s.last < b0 + OWN) {
-        for (int q = OWN - 1; b0 + q > s.last; --q) {
-          ma -= s.mass[b0 + q];
-          ca -= s.count[b0 + q];
-        }
-        s.bin_mass = s.mass[s.last];
-        s.bin_count = s.count[s.last];
-        s.above_mass = ma - s.bin_mass;
-        s.above_count = ca - s.bin_count;
-      }
-      __syncthreads();
-    }
-    const uint32_t b = (uint32_t)(s.bin < 0 ? s.last : s.bin);
-    above_mass = s.above_mass;
-    above = s.above_count;
-    hi -= b << sh;
-    const uint32_t reach = (1u << sh) - 1u;
+    const Histogram h =
+        histogram<T, ALIGNED, BY_COUNT, STRICT>(s, row, vocab, lo, hi, p.above, p.above_mass, want, weight);
+    p.above_mass = h.above_mass;
+    p.above = h.above;
+    hi -= (uint32_t)h.bin << h.sh;
+    const uint32_t reach = (1u << h.sh) - 1u;
     if (hi - lo > reach) lo = hi - reach;
     if (lo == hi) {
-      const Place p = {hi, above, s.bin_count, above_mass, s.bin_mass / s.bin_count};
-      __syncthreads();
+      p.key = hi;
+      p.n_equal = h.count;
+      p.w = h.mass / h.count;
       return p;
     }
-    __syncthreads();
   }
 }
 
@@ -299,94 +486,464 @@ __device__ __noinline__ int find_token(SampleSmem& s, const T* row, int vocab, u
   return s.bin;
 }
 
+// w / mass; in 64 bits by one warp, whose result counts (the units are few).
+__device__ __forceinline__ float share(u64 w, u64 mass) {
+  return threadIdx.x < 32 ? (float)((double)w / (double)mass) : 0.f;
+}
+
+// Sum over the block; every thread gets it.
+__device__ __forceinline__ u64 block_mass(SampleSmem& s, u64 x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  if ((threadIdx.x & 31) == 0) s.warp_mass[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+  for (int w = 0; w < SP_WARPS; ++w) x += s.warp_mass[w];
+  __syncthreads();
+  return x;
+}
+// Sum over the threads before this one.
+__device__ __forceinline__ u64 mass_before(SampleSmem& s, u64 x) {
+  u64 inc = x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) s.warp_mass[warp] = inc;
+  __syncthreads();
+  u64 before = inc - x;
+  for (int w = 0; w < warp; ++w) before += s.warp_mass[w];
+  return before;
+}
+
+// The settings of a row and what is known of it.
+struct RowState {
+  uint32_t top;    // key of the largest logit
+  uint32_t low;    // of the smallest logit with a weight
+  uint32_t least;  // of the smallest logit that min-p keeps (0: it leaves out none)
+  int top_k;       // 0: none
+  float top_p, u;
+  u64 mass;        // of the row, where no top-k bounds it
+};
+
+// The place of a draw in a mass: the token whose running sum is the first above it.
+__device__ __forceinline__ u64 draw_at(float u, u64 mass) {
+  if (!(u > 0.f)) return 0;
+  bool rest;
+  return u < 1.f ? times(u, mass, &rest) : mass - 1;
+}
+__device__ __forceinline__ u64 share_of(float p, u64 mass) {
+  bool rest;
+  const u64 want = times(p, mass, &rest);
+  return want + rest;
+}
+
+// Token and probability by searches over the whole row.
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(SP_THREADS) k_sample(SampleArgs a) {
+__device__ __noinline__ void pick_by_search(SampleSmem& s, const T* row, int vocab, const RowState& r,
+                                            const Weights& weight, int* token, float* prob) {
+  // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
+  uint32_t key = r.low, equal = 0xFFFFFFFFu;
+  u64 mass = r.mass;
+  if (r.top_k) {
+    const Place p = descend<T, ALIGNED, true, false>(s, row, vocab, r.low, r.top, (u64)r.top_k, weight);
+    key = p.key;
+    equal = min((uint32_t)r.top_k - min(p.above, (uint32_t)r.top_k), p.n_equal);
+    mass = p.above_mass + equal * p.w;
+  }
+  if (r.top_p < 1.f) {
+    const u64 want = share_of(r.top_p, mass);
+    const Place p = descend<T, ALIGNED, false, false>(s, row, vocab, key, r.top, want, weight);
+    uint32_t j = p.n_equal;
+    if (p.w && p.above_mass < want) j = (uint32_t)min((u64)j, (want - p.above_mass + p.w - 1) / p.w);
+    if (p.key == key) j = min(j, equal);
+    key = p.key;
+    equal = j;
+    mass = p.above_mass + j * p.w;
+  }
+  if (r.least > key || mass == 0) {
+    // min-p alone (the mass is not known yet), or above what top-k and top-p keep
+    key = max(key, r.least);
+    equal = 0xFFFFFFFFu;
+    u64 sum = 0;
+    each<T, ALIGNED>(row, vocab, [&](float z) {
+      if (key_of<T>(z) >= key) sum += weight(z);
+    });
+    mass = block_mass(s, sum);
+  }
+  const u64 want = draw_at(r.u, mass);
+  const Place p = descend<T, ALIGNED, false, true>(s, row, vocab, key, r.top, want, weight);
+  uint32_t j = p.n_equal;
+  if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
+  if (p.key == key) j = min(j, equal);
+  *token = find_token<T, ALIGNED>(s, row, vocab, p.key, j);
+  *prob = share(p.w, mass);
+}
+
+// The lower edge of the histogram bin that holds the k-th largest of the groups' maxima, of which the smallest above
+// -inf has the key lo: at least k tokens reach it.
+struct Bound {
+  uint32_t lo;
+};
+template <typename T>
+__device__ __noinline__ Bound bound_by_count(SampleSmem& s, const float* gmax, int n_groups, uint32_t lo, uint32_t top,
+                                             uint32_t k) {
+  constexpr int OWN = SP_BINS / SP_THREADS;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bits = 32 - __clz(top - lo), sh = bits > 11 ? bits - 11 : 0;
+  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.count[b] = 0;
+  if (threadIdx.x == 0) s.bin = -1;
+  __syncthreads();
+  for (int g = threadIdx.x; g < n_groups; g += SP_THREADS) {
+    const uint32_t x = key_of<T>(gmax[g]);
+    if (x >= lo) atomicAdd(&s.count[(top - x) >> sh], 1u);
+  }
+  __syncthreads();
+  uint32_t c = 0;
+  const int b0 = threadIdx.x * OWN;
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) c += s.count[b0 + q];
+  uint32_t inc = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) s.warp_count[warp] = inc;
+  __syncthreads();
+  uint32_t at = inc - c;
+  for (int w = 0; w < warp; ++w) at += s.warp_count[w];
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    if (at < k && at + s.count[b0 + q] >= k) s.bin = b0 + q;
+    at += s.count[b0 + q];
+  }
+  __syncthreads();
+  // fewer groups than k above -inf: no bound
+  const int b = s.bin;
+  __syncthreads();
+  if (b < 0) return {0};
+  const uint32_t hi = top - ((uint32_t)b << sh), reach = (1u << sh) - 1u;
+  return {hi - lo > reach ? hi - reach : lo};
+}
+
+// The lower edge of the histogram bin in which the running sum reaches `want`; false where the tokens that reach the
+// edge are too many to list.
+template <typename T, bool ALIGNED>
+__device__ __noinline__ bool bound_by_mass(SampleSmem& s, const T* row, int vocab, const Weights& weight,
+                                           const RowState& r, u64 want, uint32_t* lo) {
+  // what lies below weighs less than the rest of the mass, even if it were the whole vocabulary
+  uint32_t floor_key = r.low;
+  if (!weight.far) {
+    const float rest = (float)(r.mass - min(want, r.mass)) / (float)vocab;  // of a token, in the weights' units
+    if (rest > 1.f) {
+      const float z = (log2f(rest) + (float)(weight.e_ref - weight.frac)) / weight.c.hi;
+      // a little lower: the weights' and this value's rounding
+      floor_key = max(floor_key, min(key_of<T>(z - 1e-5f * fabsf(z) - 1e-3f / weight.c.hi), r.top));
+    }
+  }
+  const Histogram h = histogram<T, ALIGNED, false, false>(s, row, vocab, floor_key, r.top, 0, 0, want, weight);
+  const uint32_t reach = (1u << h.sh) - 1u;
+  const uint32_t hi = r.top - ((uint32_t)h.bin << h.sh);
+  *lo = hi - floor_key > reach ? hi - reach : floor_key;
+  return h.above + h.count <= SP_LIST;
+}
+
+// Lists the tokens whose keys reach `lo`, from the groups whose maxima do; false where they are too many.
+template <typename T, bool ALIGNED>
+__device__ __noinline__ bool list_tokens(SampleSmem& s, const T* row, int vocab, const float* gmax, int n_groups,
+                                         uint32_t lo) {
+  constexpr int PER = Elem<T>::PER16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s.n_list = s.n_groups = 0;
+  __syncthreads();
+  for (int g = threadIdx.x; g < n_groups; g += SP_THREADS) {
+    if (key_of<T>(gmax[g]) >= lo) {
+      const uint32_t at = atomicAdd(&s.n_groups, 1u);
+      if (at < SP_GROUPS) s.groups[at] = g;
+    }
+  }
+  __syncthreads();
+  const uint32_t n = s.n_groups;
+  if (n > SP_GROUPS) return false;
+  // two groups to a warp, 16 vectors each
+  for (uint32_t i = warp * 2; i < n; i += SP_WARPS * 2) {
+    uint32_t hits = 0, id = 0;
+    float x[PER];
+    if (i + (lane >> 4) < n) {
+      const uint32_t g = s.groups[i + (lane >> 4)];
+      id = (g / SEG_GROUPS) * row_seg<T>() + (((lane >> 2) & 3) * 32 + (g % SEG_GROUPS) * 4 + (lane & 3)) * PER;
+      if ((int)id < vocab) {
+        Elem<T>::unpack(row_vec<T, ALIGNED>(row, (int)id, vocab), x);
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+          if (key_of<T>(x[e]) >= lo && (int)id + e < vocab) hits |= 1u << e;
+      }
+    }
+    uint32_t inc = __popc(hits);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    uint32_t at = 0;
+    if (lane == 31 && inc) at = atomicAdd(&s.n_list, inc);
+    at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - __popc(hits);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      if ((hits >> e) & 1u) {
+        if (at < SP_LIST) s.list[at] = ((u64)key_of<T>(x[e]) << 32) | (uint32_t)~(id + e);
+        ++at;
+      }
+    }
+  }
+  __syncthreads();
+  return s.n_list <= SP_LIST;
+}
+
+// The list in descending order (its numbers are distinct).
+__device__ __noinline__ void sort_list(SampleSmem& s) {
+  const int n = (int)s.n_list;
+  if (n <= SP_THREADS) {
+    // by ranks
+    u64 x = 0;
+    int rank = 0;
+    if ((int)threadIdx.x < n) {
+      x = s.list[threadIdx.x];
+      for (int i = 0; i < n; ++i) rank += s.list[i] > x;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < n) s.list[rank] = x;
+    __syncthreads();
+    return;
+  }
+  int size = 2 * SP_THREADS;
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += SP_THREADS) s.list[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2) {
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int t = threadIdx.x; t < size / 2; t += SP_THREADS) {
+        const int i = 2 * t - (t & (j - 1)), o = i + j;
+        const u64 x = s.list[i], y = s.list[o];
+        if ((x < y) == ((i & k) == 0)) {
+          s.list[i] = y;
+          s.list[o] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Token and probability from the sorted list, which holds all tokens down to the last that can be drawn.
+template <typename T>
+__device__ __noinline__ void pick_from_list(SampleSmem& s, const RowState& r, const Weights& weight, int* token,
+                                            float* prob) {
+  constexpr int OWN = SP_LIST / SP_THREADS;
+  const int n = (int)s.n_list, own = (n + SP_THREADS - 1) / SP_THREADS, i0 = threadIdx.x * own;
+  u64 w[OWN], sum = 0;
+  int n_min = 0;
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    w[q] = 0;
+    if (q < own && i0 + q < n) {
+      const uint32_t k = (uint32_t)(s.list[i0 + q] >> 32);
+      w[q] = weight(value_of<T>(k));
+      n_min += k >= r.least;
+      sum += w[q];
+    }
+  }
+  const u64 before = mass_before(s, sum);
+  // f(running sum before, with, index) of this thread's tokens
+  auto walk = [&](auto f) {
+    u64 at = before;
+#pragma unroll
+    for (int q = 0; q < OWN; ++q) {
+      if (q < own && i0 + q < n) {
+        f(at, at + w[q], i0 + q, w[q]);
+        at += w[q];
+      }
+    }
+  };
+  if (threadIdx.x == 0) {
+    s.found_mass = r.mass;
+    s.found_at = n;
+    s.n_groups = 0;  // counts the tokens that min-p keeps
+  }
+  __syncthreads();
+  int keep = n;
+  u64 mass = r.mass;
+  if (r.least) {
+    n_min = __reduce_add_sync(0xFFFFFFFFu, n_min);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s.n_groups, (unsigned)n_min);
+  }
+  if (r.top_k) {
+    keep = min(n, r.top_k);
+    walk([&](u64, u64 with, int i, u64) {
+      if (i == keep - 1) s.found_mass = with;
+    });
+    __syncthreads();
+    mass = s.found_mass;
+  }
+  if (r.top_p < 1.f) {
+    const u64 want = share_of(r.top_p, mass);
+    walk([&](u64 b, u64 with, int i, u64) {
+      if (b < want && with >= want) s.found_at = i + 1;
+    });
+  }
+  __syncthreads();
+  keep = min(keep, (int)s.found_at);
+  if (r.least) keep = min(keep, max(1, (int)s.n_groups));
+  if (r.top_p < 1.f || r.least) {
+    walk([&](u64, u64 with, int i, u64) {
+      if (i == keep - 1) s.found_mass = with;
+    });
+    __syncthreads();
+    mass = s.found_mass;
+  }
+  const u64 want = draw_at(r.u, mass);
+  if (threadIdx.x == 0) s.found_id = 0xFFFFFFFFu;
+  __syncthreads();
+  walk([&](u64 b, u64 with, int i, u64 x) {
+    // the last kept one where rounding leaves no other
+    if (i < keep && b <= want && (with > want || i == keep - 1)) {
+      s.found_id = ~(uint32_t)s.list[i];
+      s.found_w = x;
+    }
+  });
+  __syncthreads();
+  *token = (int)s.found_id;
+  *prob = share(s.found_w, mass);
+}
+
+template <typename T, bool ALIGNED, bool SHORT>
+__global__ void __launch_bounds__(SP_THREADS) k_sample_pick(SampleArgs a, int n_seg, const float* gmax_all,
+                                                            const SegMass* segs_all) {
   __shared__ SampleSmem s;
+  __shared__ float s_gmax[SHORT ? SP_WARPS * SEG_GROUPS : 1];
+  __shared__ SegMass s_seg[SHORT ? SP_WARPS : 1];
+  const int n = blockIdx.x, vocab = a.vocab, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < (int)(sizeof(ExpTable) / 4); i += SP_THREADS)
+    reinterpret_cast<uint32_t*>(&s.tab)[i] = reinterpret_cast<const uint32_t*>(&g_exp_table)[i];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = blockIdx.x, vocab = a.vocab;
   const T* row = static_cast<const T*>(a.logits) + n * a.ld;
   const float t = a.temperature ? __ldg(a.temperature + n) : a.temperature0;
   const float top_p = a.top_p ? __ldg(a.top_p + n) : a.top_p0, min_p = a.min_p ? __ldg(a.min_p + n) : a.min_p0;
   const int top_k = a.top_k ? __ldg(a.top_k + n) : a.top_k0;
   const float u = __ldg(a.u + n);
-  for (int i = threadIdx.x; i < (int)(sizeof(ExpTable) / 4); i += SP_THREADS)
-    reinterpret_cast<uint32_t*>(&s.tab)[i] = reinterpret_cast<const uint32_t*>(&g_exp_table)[i];
-  float m = -INFINITY;
-  each<T, ALIGNED>(row, vocab, [&](float z) { m = max_nan(m, z); });
+  const bool whole = needs_mass(t, top_k, top_p, min_p, vocab);
+  const float* gmax = gmax_all + (long long)n * n_seg * SEG_GROUPS;
+  const SegMass* segs = segs_all + (long long)n * n_seg;
+  if constexpr (SHORT) {
+    ScanTable& table = *reinterpret_cast<ScanTable*>(s.list);  // not used before
+    if (whole) {
+      fill_table(table, SP_THREADS);
+      __syncthreads();
+    }
+    if (warp < n_seg) scan_segment<T, ALIGNED>(row, warp, vocab, t, whole, table, s_gmax, s_seg);
+    gmax = s_gmax;
+    segs = s_seg;
+    __syncthreads();
+  }
+  const int n_groups = n_seg * SEG_GROUPS;
+  // the row's largest logit, and the smallest of the groups' maxima above -inf
+  float m = -INFINITY, least_max = INFINITY;
+  for (int g = threadIdx.x; g < n_groups; g += SP_THREADS) {
+    const float x = gmax[g];
+    m = max_nan(m, x);
+    if (x > -INFINITY) least_max = fminf(least_max, x);
+  }
   m = warp_max(m);
-  if ((threadIdx.x & 31) == 0) s.warp_max[threadIdx.x >> 5] = m;
+  for (int o = 16; o > 0; o >>= 1) least_max = fminf(least_max, __shfl_xor_sync(0xFFFFFFFFu, least_max, o));
+  if (lane == 0) {
+    s.warp_max[warp] = m;
+    s.warp_min[warp] = least_max;
+  }
   __syncthreads();
-  for (int w = 0; w < SP_WARPS; ++w) m = max_nan(m, s.warp_max[w]);
+  for (int w = 0; w < SP_WARPS; ++w) {
+    m = max_nan(m, s.warp_max[w]);
+    least_max = fminf(least_max, s.warp_min[w]);
+  }
+  __syncthreads();
   int token = -1;
   float prob = 0.f;
   // no distribution: a NaN or +inf logit, nothing above -inf, settings or uniforms that are not numbers
   if (fabsf(m) < INFINITY && t >= 0.f && t < INFINITY && top_p == top_p && min_p == min_p && u == u) {
-    const uint32_t top = key_of<T>(m);
+    RowState r;
+    r.top = key_of<T>(m);
     if (t == 0.f || top_k == 1 || top_p <= 0.f) {
-      token = find_token<T, ALIGNED>(s, row, vocab, top, 1);
+      if (list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, r.top)) {
+        // the lowest of the ids that share the largest logit
+        uint32_t id = 0xFFFFFFFFu;
+        for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS) id = min(id, ~(uint32_t)s.list[i]);
+        id = __reduce_min_sync(0xFFFFFFFFu, id);
+        if (lane == 0) s.warp_count[warp] = id;
+        __syncthreads();
+        for (int w = 0; w < SP_WARPS; ++w) id = min(id, s.warp_count[w]);
+        token = (int)id;
+      } else {
+        __syncthreads();
+        token = find_token<T, ALIGNED>(s, row, vocab, r.top, 1);
+      }
       prob = 1.f;
     } else {
-      const Weights weight(m, t, 62 - (32 - __clz(vocab - 1)), &s.tab);
-      const uint32_t low = key_of<T>(weight.zlow);
-      // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
-      uint32_t key = low, equal = 0xFFFFFFFFu;
-      u64 mass = 0;
-      if (top_k > 1 && top_k < vocab) {
-        const Place p = descend<T, ALIGNED, true, false>(s, row, vocab, low, top, (u64)top_k, weight);
-        key = p.key;
-        equal = min((uint32_t)top_k - p.above, p.n_equal);
-        mass = p.above_mass + equal * p.w;
-      } else {
-        u64 sum = 0;
-        each<T, ALIGNED>(row, vocab, [&](float z) { sum += weight(z); });
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if ((threadIdx.x & 31) == 0) s.warp_mass[threadIdx.x >> 5] = sum;
-        __syncthreads();
-        for (int w = 0; w < SP_WARPS; ++w) mass += s.warp_mass[w];
-        __syncthreads();
-      }
-      if (top_p < 1.f) {
-        u64 want = (u64)ceil((double)top_p * (double)mass);
-        if (want < 1) want = 1;
-        const Place p = descend<T, ALIGNED, false, false>(s, row, vocab, key, top, want, weight);
-        uint32_t j = p.n_equal;
-        if (p.w && p.above_mass < want) j = (uint32_t)min((u64)j, (want - p.above_mass + p.w - 1) / p.w);
-        if (p.key == key) j = min(j, equal);
-        key = p.key;
-        equal = j;
-        mass = p.above_mass + j * p.w;
-      }
+      const Weights weight(m, t, min(62 - (32 - __clz(vocab - 1)), SEG_FRAC), &s.tab);
+      r.low = key_of<T>(weight.zlow);
+      r.top_k = top_k > 1 && top_k < vocab ? top_k : 0;
+      r.top_p = top_p;
+      r.u = u;
+      r.mass = 0;
+      r.least = 0;
       if (min_p > 0.f) {
-        // the lowest logit whose weight is min_p of the largest one's
-        const double x = (double)m + (double)t * log((double)fminf(min_p, 1.f));
-        float f = (float)x;
-        if ((double)f < x) f = nextafterf(f, INFINITY);
-        const uint32_t least = min(key_at_least<T>(f), top);
-        if (least > key) {
-          u64 sum = 0;
-          each<T, ALIGNED>(row, vocab, [&](float z) {
-            if (key_of<T>(z) >= least) sum += weight(z);
-          });
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-          if ((threadIdx.x & 31) == 0) s.warp_mass[threadIdx.x >> 5] = sum;
-          __syncthreads();
-          mass = 0;
-          for (int w = 0; w < SP_WARPS; ++w) mass += s.warp_mass[w];
-          __syncthreads();
-          key = least;
-          equal = 0xFFFFFFFFu;
+        // the lowest logit whose weight is min_p of the largest one's, in 64 bits by one warp (the units are few)
+        if (threadIdx.x < 32) {
+          const double x = (double)m + (double)t * log((double)fminf(min_p, 1.f));
+          float f = (float)x;
+          if ((double)f < x) f = nextafterf(f, INFINITY);
+          if (threadIdx.x == 0) s.warp_max[0] = f;
         }
+        __syncthreads();
+        r.least = min(key_at_least<T>(s.warp_max[0]), r.top);
+        __syncthreads();
       }
-      const double at = fmax((double)u, 0.0) * (double)mass;
-      const u64 want = at < (double)mass ? min((u64)at, mass - 1) : mass - 1;
-      const Place p = descend<T, ALIGNED, false, true>(s, row, vocab, key, top, want, weight);
-      uint32_t j = p.n_equal;
-      if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
-      if (p.key == key) j = min(j, equal);
-      token = find_token<T, ALIGNED>(s, row, vocab, p.key, j);
-      prob = (float)((double)p.w / (double)mass);
+      if (whole || (!r.top_k && r.top_p < 1.f)) {
+        u64 sum = 0;
+        if (weight.far) {
+          each<T, ALIGNED>(row, vocab, [&](float z) { sum += weight(z); });
+        } else {
+          for (int i = threadIdx.x; i < n_seg; i += SP_THREADS) {
+            const SegMass q = segs[i];
+            const long long down = (long long)(SEG_FRAC - weight.frac) + weight.e_ref - q.e;
+            if (down <= 0) sum += q.mass;
+            else if (down < 64) sum += (q.mass + (1ull << (down - 1))) >> down;
+          }
+        }
+        r.mass = block_mass(s, sum);
+      }
+      // the key below which nothing can be kept and drawn
+      uint32_t lo = r.low;
+      bool listed = true;
+      if (r.top_k) {
+        if (r.top_k <= n_groups) {
+          const Bound b = bound_by_count<T>(s, gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
+          lo = max(lo, b.lo);
+        }
+      } else if (whole) {
+        const u64 want = r.top_p < 1.f ? share_of(r.top_p, r.mass) : draw_at(r.u, r.mass) + 1;
+        listed = bound_by_mass<T, ALIGNED>(s, row, vocab, weight, r, want, &lo);
+      } else {
+        lo = max(lo, r.least);
+      }
+      if (listed && list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, lo)) {
+        sort_list(s);
+        pick_from_list<T>(s, r, weight, &token, &prob);
+      } else {
+        __syncthreads();
+        pick_by_search<T, ALIGNED>(s, row, vocab, r, weight, &token, &prob);
+      }
     }
   }
   if (threadIdx.x == 0) {
@@ -397,16 +954,47 @@ __global__ void __launch_bounds__(SP_THREADS) k_sample(SampleArgs a) {
 
 }  // namespace
 
-size_t sample_workspace(int, int, int) { return 0; }
+namespace {
+
+struct SampleLayout {
+  size_t gmax, segs, total;
+  int n_seg;
+};
+SampleLayout sample_layout(int N, int vocab, int dtype) {
+  const int seg = dtype == DH_BF16 ? row_seg<__nv_bfloat16>() : row_seg<float>();
+  SampleLayout L;
+  L.n_seg = (vocab + seg - 1) / seg;
+  L.gmax = WS_HEADER;
+  L.segs = L.gmax + align_up((size_t)N * L.n_seg * SEG_GROUPS * sizeof(float), 256);
+  L.total = L.n_seg <= SP_WARPS ? 0 : L.segs + align_up((size_t)N * L.n_seg * sizeof(SegMass), 256);
+  return L;
+}
+
+template <typename T, bool ALIGNED>
+cudaError_t run_sample(const Ctx& c, const SampleArgs& a, int dtype) {
+  const SampleLayout L = sample_layout(a.N, a.vocab, dtype);
+  const dim3 grid((unsigned)a.N), block(SP_THREADS);
+  if (L.total == 0)
+    return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, true>, grid, block, 0, a, L.n_seg, nullptr, nullptr);
+  float* gmax = reinterpret_cast<float*>(static_cast<char*>(a.ws) + L.gmax);
+  SegMass* segs = reinterpret_cast<SegMass*>(static_cast<char*>(a.ws) + L.segs);
+  const long long want = ((long long)a.N * L.n_seg + SC_THREADS / 32 - 1) / (SC_THREADS / 32), most = 6LL * c.num_sms;
+  const cudaError_t e = launch_pdl(c, "sample_scan", k_sample_scan<T, ALIGNED>, dim3((unsigned)(want < most ? want : most)),
+                                   dim3(SC_THREADS), 0, a, L.n_seg, gmax, segs);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, false>, grid, block, 0, a, L.n_seg, gmax, segs);
+}
+
+}  // namespace
+
+size_t sample_workspace(int N, int vocab, int dtype) { return sample_layout(N, vocab, dtype).total; }
 
 cudaError_t launch_sample(const Ctx& c, const SampleArgs& a, int dtype) {
   const int elem = dtype == DH_BF16 ? 2 : 4;
   const bool al = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && (a.N == 1 || a.ld * elem % 16 == 0);
-  auto go = [&](auto* kernel) {
-    return launch_pdl(c, "sample", kernel, dim3((unsigned)a.N), dim3(SP_THREADS), 0, a);
-  };
-  if (dtype == DH_BF16) return al ? go(k_sample<__nv_bfloat16, true>) : go(k_sample<__nv_bfloat16, false>);
-  return al ? go(k_sample<float, true>) : go(k_sample<float, false>);
+  if (dtype == DH_BF16)
+    return al ? run_sample<__nv_bfloat16, true>(c, a, dtype) : run_sample<__nv_bfloat16, false>(c, a, dtype);
+  return al ? run_sample<float, true>(c, a, dtype) : run_sample<float, false>(c, a, dtype);
 }
 
 }  // namespace dh
