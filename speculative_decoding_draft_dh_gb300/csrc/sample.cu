@@ -30,6 +30,12 @@ constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 2048;
 constexpr int SP_LIST = 4096;    // tokens listed, at most
 constexpr int SP_GROUPS = 2048;  // groups listed, at most
+// Groups with which a row whose mass is needed is tried, and how many times more each time.
+#ifndef SP_F
+#define SP_F 64
+#define SP_S 4
+#endif
+constexpr int SP_TRY_FIRST = SP_F, SP_TRY_STEP = SP_S;
 constexpr int SEG_GROUPS = 8;    // groups of a segment: four lanes' vectors each
 constexpr int SEG_FRAC = 52;     // fraction bits of a segment's mass, relative to 2^e of its own largest weight
 
@@ -270,13 +276,25 @@ __global__ void __launch_bounds__(SC_THREADS) k_sample_scan(SampleArgs a, int n_
 
 // ------------------------------------------------------------------ the search
 
+// A histogram over a range of keys: masses in two words, counts.
+struct Bins {
+  uint32_t lo[SP_BINS], hi[SP_BINS], count[SP_BINS];
+  __device__ __forceinline__ u64 mass(int b) const { return ((u64)hi[b] << 32) | lo[b]; }
+  __device__ __forceinline__ void add(uint32_t b, u64 w) {
+    atomicAdd(&count[b], 1u);
+    const uint32_t x = (uint32_t)w;
+    uint32_t h = (uint32_t)(w >> 32);
+    // (there is no 64-bit addition in shared memory)
+    if (x) h += atomicAdd(&lo[b], x) > ~x;
+    if (h) atomicAdd(&hi[b], h);
+  }
+};
+
 struct SampleSmem {
   union {
-    struct {
-      u64 mass[SP_BINS];
-      uint32_t count[SP_BINS];
-    };
+    Bins bins[2];       // of the whole range, of a part of it
     u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
+    uint32_t group_count[SP_BINS];
   };
   uint32_t groups[SP_GROUPS];
   ExpTable tab;
@@ -298,47 +316,57 @@ struct Place {
   u64 above_mass, w;
 };
 
-// f(value) of every logit of the row (-inf past its end).
+// f(value) of every logit of the row that is in [from, to] (finite numbers).
 template <typename T, bool ALIGNED, typename F>
-__device__ __forceinline__ void each(const T* row, int vocab, F f) {
-  constexpr int PER = Elem<T>::PER16;
-  for (int id = threadIdx.x * PER; id < vocab; id += SP_THREADS * PER) {
-    float x[PER];
-    Elem<T>::unpack(row_vec<T, ALIGNED>(row, id, vocab), x);
+__device__ __forceinline__ void each(const T* row, int vocab, float from, float to, F f) {
+  constexpr int PER = Elem<T>::PER16, AHEAD = 4;
+  for (int id0 = threadIdx.x * PER; id0 < vocab; id0 += AHEAD * SP_THREADS * PER) {
+    uint4 u[AHEAD];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) f(x[e]);
+    for (int q = 0; q < AHEAD; ++q) {
+      const int id = id0 + q * SP_THREADS * PER;
+      u[q] = make_uint4(NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD);
+      if (id < vocab) u[q] = row_vec<T, ALIGNED>(row, id, vocab);
+    }
+#pragma unroll 1
+    for (int q = 0; q < AHEAD; ++q) {
+      float x[PER];
+      Elem<T>::unpack(q == 0 ? u[0] : q == 1 ? u[1] : q == 2 ? u[2] : u[3], x);
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (x[e] >= from && x[e] <= to) f(x[e]);
+    }
   }
 }
 
-// The bin, of 2^sh keys from the top down, of the keys [lo, hi] in which `want` is reached: tokens (BY_COUNT) or a
-// mass of want or more (STRICT: more than want), counted on from `above` tokens of `above_mass`; the last bin with a
-// token where it is not.
+// The bin, of 2^sh keys from the top down, in which `want` is reached: tokens (BY_COUNT) or a mass of want or more
+// (STRICT: more than want), counted on from `above` tokens of `above_mass`; the last bin with a token where it is
+// not.
 struct Histogram {
   int bin, sh;
   uint32_t above, count;
   u64 above_mass, mass;
 };
-template <typename T, bool ALIGNED, bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Histogram histogram(SampleSmem& s, const T* row, int vocab, uint32_t lo, uint32_t hi,
-                                            uint32_t above, u64 above_mass, u64 want, const Weights& weight) {
+__device__ __forceinline__ int bin_shift(uint32_t lo, uint32_t hi) {
+  const int bits = 32 - __clz(hi - lo);
+  return bits > 11 ? bits - 11 : 0;
+}
+// The tokens with keys [lo, hi].
+template <typename T, bool ALIGNED>
+__device__ __noinline__ void fill_bins(Bins& bins, const T* row, int vocab, uint32_t lo, uint32_t hi,
+                                       const Weights& weight) {
+  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) bins.lo[b] = bins.hi[b] = bins.count[b] = 0;
+  __syncthreads();
+  const int sh = bin_shift(lo, hi);
+  each<T, ALIGNED>(row, vocab, value_of<T>(lo), value_of<T>(hi),
+                   [&](float z) { bins.add((hi - key_of<T>(z)) >> sh, weight(z)); });
+  __syncthreads();
+}
+template <bool BY_COUNT, bool STRICT>
+__device__ __noinline__ Histogram find_bin(SampleSmem& s, const Bins& bins, int sh, uint32_t above, u64 above_mass,
+                                           u64 want) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int bits = 32 - __clz(hi - lo), sh = bits > 11 ? bits - 11 : 0;
-  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) {
-    s.mass[b] = 0;
-    s.count[b] = 0;
-  }
   if (threadIdx.x == 0) s.bin = s.last = -1;
-  __syncthreads();
-  each<T, ALIGNED>(row, vocab, [&](float z) {
-    const uint32_t k = key_of<T>(z);
-    if (k >= lo && k <= hi) {
-      const uint32_t b = (hi - k) >> sh;
-      atomicAdd(&s.count[b], 1u);
-      const u64 w = weight(z);
-      if (w) atomicAdd(&s.mass[b], w);
-    }
-  });
-  __syncthreads();
   // inclusive sums over the bins, four to a thread
   constexpr int OWN = SP_BINS / SP_THREADS;
   u64 m = 0;
@@ -346,8 +374,8 @@ __device__ __noinline__ Histogram histogram(SampleSmem& s, const T* row, int voc
   const int b0 = threadIdx.x * OWN;
 #pragma unroll
   for (int q = 0; q < OWN; ++q) {
-    m += s.mass[b0 + q];
-    c += s.count[b0 + q];
+    m += bins.mass(b0 + q);
+    c += bins.count[b0 + q];
   }
   u64 mi = m;
   uint32_t ci = c;
@@ -374,52 +402,49 @@ __device__ __noinline__ Histogram histogram(SampleSmem& s, const T* row, int voc
   auto reached = [&](u64 mass, uint32_t count) {
     return BY_COUNT ? count >= want : STRICT ? mass > want : mass >= want;
   };
+  auto found = [&](int b, u64 mass_before, uint32_t count_before) {
+    s.bin_mass = bins.mass(b);
+    s.bin_count = bins.count[b];
+    s.above_mass = mass_before;
+    s.above_count = count_before;
+  };
   int last = -1;
+  u64 last_mass = 0;
+  uint32_t last_count = 0;
 #pragma unroll
   for (int q = 0; q < OWN; ++q) {
-    const u64 mb = s.mass[b0 + q];
-    const uint32_t cb = s.count[b0 + q];
-    if (cb) last = b0 + q;
+    const u64 mb = bins.mass(b0 + q);
+    const uint32_t cb = bins.count[b0 + q];
+    if (cb) {
+      last = b0 + q;
+      last_mass = ma;
+      last_count = ca;
+    }
     if (!reached(ma, ca) && reached(ma + mb, ca + cb)) {
       s.bin = b0 + q;
-      s.bin_mass = mb;
-      s.bin_count = cb;
-      s.above_mass = ma;
-      s.above_count = ca;
+      found(b0 + q, ma, ca);
     }
     ma += mb;
     ca += cb;
   }
   if (last >= 0) atomicMax(&s.last, last);
   __syncthreads();
-  if (s.bin < 0) {
-    // the sums never reach it: the last bin that holds a token
-    if (s.last >= b0 && s.last < b0 + OWN) {
-      for (int q = OWN - 1; b0 + q > s.last; --q) {
-        ma -= s.mass[b0 + q];
-        ca -= s.count[b0 + q];
-      }
-      s.bin_mass = s.mass[s.last];
-      s.bin_count = s.count[s.last];
-      s.above_mass = ma - s.bin_mass;
-      s.above_count = ca - s.bin_count;
-    }
-    __syncthreads();
-  }
+  // where the sums never reach it: the last bin that holds a token
+  if (s.bin < 0 && last >= 0 && last == s.last) found(last, last_mass, last_count);
+  __syncthreads();
   const Histogram h = {s.bin < 0 ? s.last : s.bin, sh, s.above_count, s.bin_count, s.above_mass, s.bin_mass};
   __syncthreads();
   return h;
 }
 
 // The first place with `want` tokens or more (BY_COUNT), or with a mass of want or more (STRICT: more than want),
-// among the keys [lo, hi]; the last place where there is none.  hi is the row's largest key.
+// among the keys [lo, hi], whose histogram is in bins[0]; the last place where there is none.
 template <typename T, bool ALIGNED, bool BY_COUNT, bool STRICT>
 __device__ __noinline__ Place descend(SampleSmem& s, const T* row, int vocab, uint32_t lo, uint32_t hi, u64 want,
                                       const Weights& weight) {
   Place p = {};
+  Histogram h = find_bin<BY_COUNT, STRICT>(s, s.bins[0], bin_shift(lo, hi), 0, 0, want);
   for (;;) {
-    const Histogram h =
-        histogram<T, ALIGNED, BY_COUNT, STRICT>(s, row, vocab, lo, hi, p.above, p.above_mass, want, weight);
     p.above_mass = h.above_mass;
     p.above = h.above;
     hi -= (uint32_t)h.bin << h.sh;
@@ -431,6 +456,8 @@ __device__ __noinline__ Place descend(SampleSmem& s, const T* row, int vocab, ui
       p.w = h.mass / h.count;
       return p;
     }
+    fill_bins<T, ALIGNED>(s.bins[1], row, vocab, lo, hi, weight);
+    h = find_bin<BY_COUNT, STRICT>(s, s.bins[1], bin_shift(lo, hi), p.above, p.above_mass, want);
   }
 }
 
@@ -544,6 +571,7 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
 template <typename T, bool ALIGNED>
 __device__ __noinline__ void pick_by_search(SampleSmem& s, const T* row, int vocab, const RowState& r,
                                             const Weights& weight, int* token, float* prob) {
+  fill_bins<T, ALIGNED>(s.bins[0], row, vocab, r.low, r.top, weight);
   // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
   uint32_t key = r.low, equal = 0xFFFFFFFFu;
   u64 mass = r.mass;
@@ -555,7 +583,7 @@ __device__ __noinline__ void pick_by_search(SampleSmem& s, const T* row, int voc
   }
   if (r.top_p < 1.f) {
     const u64 want = share_of(r.top_p, mass);
-    const Place p = descend<T, ALIGNED, false, false>(s, row, vocab, key, r.top, want, weight);
+    const Place p = descend<T, ALIGNED, false, false>(s, row, vocab, r.low, r.top, want, weight);
     uint32_t j = p.n_equal;
     if (p.w && p.above_mass < want) j = (uint32_t)min((u64)j, (want - p.above_mass + p.w - 1) / p.w);
     if (p.key == key) j = min(j, equal);
@@ -568,43 +596,38 @@ __device__ __noinline__ void pick_by_search(SampleSmem& s, const T* row, int voc
     key = max(key, r.least);
     equal = 0xFFFFFFFFu;
     u64 sum = 0;
-    each<T, ALIGNED>(row, vocab, [&](float z) {
-      if (key_of<T>(z) >= key) sum += weight(z);
-    });
+    each<T, ALIGNED>(row, vocab, value_of<T>(key), weight.m, [&](float z) { sum += weight(z); });
     mass = block_mass(s, sum);
   }
   const u64 want = draw_at(r.u, mass);
-  const Place p = descend<T, ALIGNED, false, true>(s, row, vocab, key, r.top, want, weight);
+  const Place p = descend<T, ALIGNED, false, true>(s, row, vocab, r.low, r.top, want, weight);
   uint32_t j = p.n_equal;
   if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
   if (p.key == key) j = min(j, equal);
+  // (p.key < key, below the kept prefix, is not reached: the searches go by the same sums)
   *token = find_token<T, ALIGNED>(s, row, vocab, p.key, j);
   *prob = share(p.w, mass);
 }
 
 // The lower edge of the histogram bin that holds the k-th largest of the groups' maxima, of which the smallest above
-// -inf has the key lo: at least k tokens reach it.
-struct Bound {
-  uint32_t lo;
-};
+// -inf has the key lo: at least k tokens reach it.  0 where fewer than k groups are above -inf.
 template <typename T>
-__device__ __noinline__ Bound bound_by_count(SampleSmem& s, const float* gmax, int n_groups, uint32_t lo, uint32_t top,
-                                             uint32_t k) {
+__device__ __noinline__ uint32_t bound_by_count(SampleSmem& s, const float* gmax, int n_groups, uint32_t lo,
+                                                uint32_t top, uint32_t k) {
   constexpr int OWN = SP_BINS / SP_THREADS;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int bits = 32 - __clz(top - lo), sh = bits > 11 ? bits - 11 : 0;
-  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.count[b] = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sh = bin_shift(lo, top);
+  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.group_count[b] = 0;
   if (threadIdx.x == 0) s.bin = -1;
   __syncthreads();
   for (int g = threadIdx.x; g < n_groups; g += SP_THREADS) {
     const uint32_t x = key_of<T>(gmax[g]);
-    if (x >= lo) atomicAdd(&s.count[(top - x) >> sh], 1u);
+    if (x >= lo) atomicAdd(&s.group_count[(top - x) >> sh], 1u);
   }
   __syncthreads();
   uint32_t c = 0;
   const int b0 = threadIdx.x * OWN;
 #pragma unroll
-  for (int q = 0; q < OWN; ++q) c += s.count[b0 + q];
+  for (int q = 0; q < OWN; ++q) c += s.group_count[b0 + q];
   uint32_t inc = c;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -617,38 +640,15 @@ __device__ __noinline__ Bound bound_by_count(SampleSmem& s, const float* gmax, i
   for (int w = 0; w < warp; ++w) at += s.warp_count[w];
 #pragma unroll
   for (int q = 0; q < OWN; ++q) {
-    if (at < k && at + s.count[b0 + q] >= k) s.bin = b0 + q;
-    at += s.count[b0 + q];
+    if (at < k && at + s.group_count[b0 + q] >= k) s.bin = b0 + q;
+    at += s.group_count[b0 + q];
   }
   __syncthreads();
-  // fewer groups than k above -inf: no bound
   const int b = s.bin;
   __syncthreads();
-  if (b < 0) return {0};
+  if (b < 0) return 0;
   const uint32_t hi = top - ((uint32_t)b << sh), reach = (1u << sh) - 1u;
-  return {hi - lo > reach ? hi - reach : lo};
-}
-
-// The lower edge of the histogram bin in which the running sum reaches `want`; false where the tokens that reach the
-// edge are too many to list.
-template <typename T, bool ALIGNED>
-__device__ __noinline__ bool bound_by_mass(SampleSmem& s, const T* row, int vocab, const Weights& weight,
-                                           const RowState& r, u64 want, uint32_t* lo) {
-  // what lies below weighs less than the rest of the mass, even if it were the whole vocabulary
-  uint32_t floor_key = r.low;
-  if (!weight.far) {
-    const float rest = (float)(r.mass - min(want, r.mass)) / (float)vocab;  // of a token, in the weights' units
-    if (rest > 1.f) {
-      const float z = (log2f(rest) + (float)(weight.e_ref - weight.frac)) / weight.c.hi;
-      // a little lower: the weights' and this value's rounding
-      floor_key = max(floor_key, min(key_of<T>(z - 1e-5f * fabsf(z) - 1e-3f / weight.c.hi), r.top));
-    }
-  }
-  const Histogram h = histogram<T, ALIGNED, false, false>(s, row, vocab, floor_key, r.top, 0, 0, want, weight);
-  const uint32_t reach = (1u << h.sh) - 1u;
-  const uint32_t hi = r.top - ((uint32_t)h.bin << h.sh);
-  *lo = hi - floor_key > reach ? hi - reach : floor_key;
-  return h.above + h.count <= SP_LIST;
+  return hi - lo > reach ? hi - reach : lo;
 }
 
 // Lists the tokens whose keys reach `lo`, from the groups whose maxima do; false where they are too many.
@@ -701,6 +701,14 @@ __device__ __noinline__ bool list_tokens(SampleSmem& s, const T* row, int vocab,
   }
   __syncthreads();
   return s.n_list <= SP_LIST;
+}
+
+// The mass of the list.
+template <typename T>
+__device__ __noinline__ u64 list_mass(SampleSmem& s, const Weights& weight) {
+  u64 sum = 0;
+  for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS) sum += weight(value_of<T>((uint32_t)(s.list[i] >> 32)));
+  return block_mass(s, sum);
 }
 
 // The list in descending order (its numbers are distinct).
@@ -820,9 +828,10 @@ __device__ __noinline__ void pick_from_list(SampleSmem& s, const RowState& r, co
 }
 
 template <typename T, bool ALIGNED, bool SHORT>
-__global__ void __launch_bounds__(SP_THREADS) k_sample_pick(SampleArgs a, int n_seg, const float* gmax_all,
+__global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int n_seg, const float* gmax_all,
                                                             const SegMass* segs_all) {
-  __shared__ SampleSmem s;
+  extern __shared__ __align__(16) unsigned char sample_smem[];
+  SampleSmem& s = *reinterpret_cast<SampleSmem*>(sample_smem);
   __shared__ float s_gmax[SHORT ? SP_WARPS * SEG_GROUPS : 1];
   __shared__ SegMass s_seg[SHORT ? SP_WARPS : 1];
   const int n = blockIdx.x, vocab = a.vocab, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -912,7 +921,7 @@ __global__ void __launch_bounds__(SP_THREADS) k_sample_pick(SampleArgs a, int n_
       if (whole || (!r.top_k && r.top_p < 1.f)) {
         u64 sum = 0;
         if (weight.far) {
-          each<T, ALIGNED>(row, vocab, [&](float z) { sum += weight(z); });
+          each<T, ALIGNED>(row, vocab, weight.zlow, weight.m, [&](float z) { sum += weight(z); });
         } else {
           for (int i = threadIdx.x; i < n_seg; i += SP_THREADS) {
             const SegMass q = segs[i];
@@ -923,21 +932,24 @@ __global__ void __launch_bounds__(SP_THREADS) k_sample_pick(SampleArgs a, int n_
         }
         r.mass = block_mass(s, sum);
       }
-      // the key below which nothing can be kept and drawn
-      uint32_t lo = r.low;
-      bool listed = true;
-      if (r.top_k) {
-        if (r.top_k <= n_groups) {
-          const Bound b = bound_by_count<T>(s, gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
-          lo = max(lo, b.lo);
-        }
-      } else if (whole) {
+      // a list of the tokens from a key on below which nothing can be kept and drawn
+      bool listed = false;
+      if (whole) {
+        // the mass that the list has to hold; the more groups, the lower the key
         const u64 want = r.top_p < 1.f ? share_of(r.top_p, r.mass) : draw_at(r.u, r.mass) + 1;
-        listed = bound_by_mass<T, ALIGNED>(s, row, vocab, weight, r, want, &lo);
+        for (int k = SP_TRY_FIRST; !listed && k <= SP_GROUPS; k *= SP_TRY_STEP) {
+          const uint32_t lo =
+              k < n_groups ? bound_by_count<T>(s, gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)k) : 0;
+          if (!list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, max(lo, r.low))) break;
+          listed = lo <= r.low || list_mass<T>(s, weight) >= want;
+        }
       } else {
-        lo = max(lo, r.least);
+        uint32_t lo = r.top_k ? 0 : r.least;
+        if (r.top_k && r.top_k <= n_groups)
+          lo = bound_by_count<T>(s, gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
+        listed = list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, max(lo, r.low));
       }
-      if (listed && list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, lo)) {
+      if (listed) {
         sort_list(s);
         pick_from_list<T>(s, r, weight, &token, &prob);
       } else {
@@ -974,15 +986,23 @@ template <typename T, bool ALIGNED>
 cudaError_t run_sample(const Ctx& c, const SampleArgs& a, int dtype) {
   const SampleLayout L = sample_layout(a.N, a.vocab, dtype);
   const dim3 grid((unsigned)a.N), block(SP_THREADS);
-  if (L.total == 0)
-    return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, true>, grid, block, 0, a, L.n_seg, nullptr, nullptr);
+  const size_t smem = sizeof(SampleSmem);
+  if (L.total == 0) {
+    static unsigned long long short_done = 0;
+    const cudaError_t e = allow_max_smem(k_sample_pick<T, ALIGNED, true>, c.device, &short_done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, true>, grid, block, smem, a, L.n_seg, nullptr, nullptr);
+  }
+  static unsigned long long long_done = 0;
+  cudaError_t e = allow_max_smem(k_sample_pick<T, ALIGNED, false>, c.device, &long_done);
+  if (e != cudaSuccess) return e;
   float* gmax = reinterpret_cast<float*>(static_cast<char*>(a.ws) + L.gmax);
   SegMass* segs = reinterpret_cast<SegMass*>(static_cast<char*>(a.ws) + L.segs);
   const long long want = ((long long)a.N * L.n_seg + SC_THREADS / 32 - 1) / (SC_THREADS / 32), most = 6LL * c.num_sms;
-  const cudaError_t e = launch_pdl(c, "sample_scan", k_sample_scan<T, ALIGNED>, dim3((unsigned)(want < most ? want : most)),
-                                   dim3(SC_THREADS), 0, a, L.n_seg, gmax, segs);
+  e = launch_pdl(c, "sample_scan", k_sample_scan<T, ALIGNED>, dim3((unsigned)(want < most ? want : most)),
+                 dim3(SC_THREADS), 0, a, L.n_seg, gmax, segs);
   if (e != cudaSuccess) return e;
-  return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, false>, grid, block, 0, a, L.n_seg, gmax, segs);
+  return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, false>, grid, block, smem, a, L.n_seg, gmax, segs);
 }
 
 }  // namespace
