@@ -71,7 +71,9 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned unit
 
 constexpr int TS_THREADS = 1024;
 constexpr int TS_WARPS = TS_THREADS / 32;
-constexpr int TS_BITS = 9;  // at most, per pass
+constexpr int TS_BITS = 9;   // at most, per pass
+constexpr int TS_ITEMS = 8;  // rows of 32 pairs of a warp at a time
+constexpr int TS_RANKS = 8;  // blocks of the cluster, at most
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -94,18 +96,34 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank)
   return v;
 }
 
-// Sorts (token, n) by token, stable in n, into buf[passes & 1 ? 1 : 0]; tokens outside [0, vocab) get the key
+// The lanes whose digit is this lane's, among those that have one.  By a ballot per bit: a match instruction takes
+// an SM many times as long (a sort of 32768 tokens 27 us with it).
+template <int BITS>
+__device__ __forceinline__ uint32_t same_digit(uint32_t dg, bool on) {
+  uint32_t same = __ballot_sync(0xFFFFFFFFu, on);
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const bool bit = (dg >> b) & 1u;
+    const uint32_t ones = __ballot_sync(0xFFFFFFFFu, bit);
+    same &= bit ? ones : ~ones;
+  }
+  return same;
+}
+
+// Sorts (token, n) by token, stable in n, into buf0 after an odd number of passes, else buf1; tokens outside [0, vocab) get the key
 // vocab and so come last.  A least-significant-digit radix sort: each warp owns a contiguous run of pairs, counts
-// its digits, and after an exclusive scan over (digit, block, warp) places its pairs in order.
+// its digits, and after an exclusive scan over (digit, block, warp) places its pairs in order.  What bounds it are
+// latencies, so a warp's loads are issued TS_ITEMS at a time, and up to that many pairs per lane stay in registers
+// between counting and placing.
+template <int BITS>
 __global__ void __launch_bounds__(TS_THREADS) k_token_sort(const int32_t* __restrict__ tokens, int N, int vocab,
-                                                           int bits, int passes, uint2* __restrict__ buf0,
+                                                           int passes, uint2* __restrict__ buf0,
                                                            uint2* __restrict__ buf1, uint32_t* __restrict__ present) {
-  extern __shared__ uint32_t ts_smem[];
-  __shared__ uint32_t s_total[1 << TS_BITS], s_scan[TS_WARPS];
-  const int nb = 1 << bits;
-  uint32_t* cnt = ts_smem;  // [warp][digit]
+  constexpr int NB = 1 << BITS;
+  extern __shared__ uint32_t cnt[];  // [warp][digit]
+  __shared__ uint32_t s_total[NB], s_base[NB], s_scan[TS_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const uint32_t rank = cluster_rank(), ranks = cluster_size(), under = (1u << lane) - 1u;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int words = (vocab + 31) / 32;
   for (int i = rank * TS_THREADS + threadIdx.x; i < words; i += ranks * TS_THREADS) present[i] = 0u;
@@ -114,83 +132,108 @@ __global__ void __launch_bounds__(TS_THREADS) k_token_sort(const int32_t* __rest
   const long long per_warp = ((long long)N + 32LL * warps - 1) / (32LL * warps) * 32;
   const long long w0 = per_warp * (rank * TS_WARPS + warp);
   const int p0 = (int)(w0 < N ? w0 : N), p1 = (int)(w0 + per_warp < N ? w0 + per_warp : N);
+  const bool once = per_warp <= 32 * TS_ITEMS;
+  uint32_t* mine = cnt + warp * NB;
+  uint2 x[TS_ITEMS];
   for (int pass = 0; pass < passes; ++pass) {
     const uint2* src = (pass & 1) ? buf0 : buf1;
     uint2* dst = (pass & 1) ? buf1 : buf0;
-    const int sh = pass * bits;
-    const uint32_t mask = (uint32_t)nb - 1u;
-    auto pair = [&](int i) -> uint2 {
-      if (pass == 0) {
-        const int t = __ldg(tokens + i);
-        return make_uint2((uint32_t)t < (uint32_t)vocab ? (uint32_t)t : (uint32_t)vocab, (uint32_t)i);
+    const int sh = pass * BITS;
+    // the pairs from i on, TS_ITEMS rows of 32; past the end the digit is none
+    auto load = [&](int i) {
+#pragma unroll
+      for (int q = 0; q < TS_ITEMS; ++q) {
+        const int at = i + q * 32 + lane;
+        x[q] = make_uint2(0xFFFFFFFFu, 0u);
+        if (at < p1) {
+          if (pass == 0) {
+            const int t = __ldg(tokens + at);
+            x[q] = make_uint2((uint32_t)t < (uint32_t)vocab ? (uint32_t)t : (uint32_t)vocab, (uint32_t)at);
+          } else {
+            x[q] = __ldcg(src + at);
+          }
+        }
       }
-      return __ldcg(src + i);
     };
-    for (int i = threadIdx.x; i < nb * TS_WARPS; i += TS_THREADS) cnt[i] = 0u;
+    for (int i = threadIdx.x; i < NB * TS_WARPS / 4; i += TS_THREADS)
+      reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p0 < p1) load(p0);
     __syncthreads();
-    uint32_t* mine = cnt + warp * nb;
-    for (int i = p0; i < p1; i += 32) {
-      const bool on = i + lane < p1;
-      const uint32_t dg = on ? (pair(i + lane).x >> sh) & mask : 0xFFFFFFFFu;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
-      if (on && (same & ((1u << lane) - 1u)) == 0) mine[dg] += __popc(same);
-      __syncwarp();
+    for (int i = p0; i < p1; i += 32 * TS_ITEMS) {
+      if (i > p0) load(i);
+#pragma unroll
+      for (int q = 0; q < TS_ITEMS; ++q) {
+        if (i + q * 32 >= p1) break;
+        const bool on = x[q].x != 0xFFFFFFFFu;
+        const uint32_t dg = (x[q].x >> sh) & (NB - 1u), same = same_digit<BITS>(dg, on);
+        if (on && (same & under) == 0) mine[dg] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
     // per digit: the warps' counts to exclusive sums, and the block's total
-    for (int b = threadIdx.x; b < nb; b += TS_THREADS) {
+    for (int b = threadIdx.x; b < NB; b += TS_THREADS) {
       uint32_t s = 0;
-      for (int w = 0; w < TS_WARPS; ++w) {
-        const uint32_t x = cnt[w * nb + b];
-        cnt[w * nb + b] = s;
-        s += x;
+#pragma unroll
+      for (int w0 = 0; w0 < TS_WARPS; w0 += 8) {
+        uint32_t c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = cnt[(w0 + w) * NB + b];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          cnt[(w0 + w) * NB + b] = s;
+          s += c[w];
+        }
       }
       s_total[b] = s;
     }
     cluster_sync();
     // the digit's first place of this block: lower digits of all blocks, the same digit of lower blocks
     uint32_t all = 0, before = 0;
-    if (threadIdx.x < nb) {
-      for (uint32_t r = 0; r < ranks; ++r) {
-        const uint32_t x = ld_cluster(s_total + threadIdx.x, r);
-        all += x;
-        if (r < rank) before += x;
+    if (threadIdx.x < NB) {
+#pragma unroll
+      for (uint32_t r = 0; r < TS_RANKS; ++r) {
+        const uint32_t c = r < ranks ? ld_cluster(s_total + threadIdx.x, r) : 0u;
+        all += c;
+        if (r < rank) before += c;
       }
     }
     uint32_t inc = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += x;
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
     }
     if (lane == 31) s_scan[warp] = inc;
     __syncthreads();
-    uint32_t lower = 0;
-    for (int w = 0; w < warp; ++w) lower += s_scan[w];
-    if (threadIdx.x < nb) {
-      const uint32_t base = lower + inc - all + before;
-      for (int w = 0; w < TS_WARPS; ++w) cnt[w * nb + threadIdx.x] += base;
+    if (threadIdx.x < NB) {
+      uint32_t base = inc - all + before;
+      for (int w = 0; w < warp; ++w) base += s_scan[w];
+      s_base[threadIdx.x] = base;
     }
     __syncthreads();
-    for (int i = p0; i < p1; i += 32) {
-      const bool on = i + lane < p1;
-      uint2 x = make_uint2(0u, 0u);
-      if (on) x = pair(i + lane);
-      const uint32_t dg = on ? (x.x >> sh) & mask : 0xFFFFFFFFu;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, dg);
-      const uint32_t below = same & ((1u << lane) - 1u);
-      if (on) dst[mine[dg] + __popc(below)] = x;
-      __syncwarp();
-      if (on && below == 0) mine[dg] += __popc(same);
-      __syncwarp();
-      if (pass == 0 && on && x.x < (uint32_t)vocab) {
-        // the bitmap was zeroed before the cluster's barrier; a bit that is set needs no second atomic
-        const uint32_t bit = 1u << (x.x & 31u);
-        if (!(__ldcg(present + (x.x >> 5)) & bit)) atomicOr(present + (x.x >> 5), bit);
+    for (int i = p0; i < p1; i += 32 * TS_ITEMS) {
+      if (!once) load(i);
+#pragma unroll
+      for (int q = 0; q < TS_ITEMS; ++q) {
+        if (i + q * 32 >= p1) break;
+        const bool on = x[q].x != 0xFFFFFFFFu;
+        const uint32_t dg = (x[q].x >> sh) & (NB - 1u), same = same_digit<BITS>(dg, on);
+        const uint32_t below = same & under;
+        if (on) dst[s_base[dg] + mine[dg] + __popc(below)] = x[q];
+        __syncwarp();
+        if (on && below == 0) mine[dg] += __popc(same);
+        __syncwarp();
       }
     }
     // the pairs are in place for the whole cluster, and the totals have been read
     cluster_sync();
+  }
+  // the tokens that occur, each once: where a run starts
+  const uint2* sorted = (passes & 1) ? buf0 : buf1;
+  for (int i = rank * TS_THREADS + threadIdx.x; i < N; i += ranks * TS_THREADS) {
+    const uint32_t t = __ldcg(sorted + i).x;
+    if (t < (uint32_t)vocab && (i == 0 || __ldcg(sorted + i - 1).x != t)) atomicOr(present + (t >> 5), 1u << (t & 31u));
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -207,10 +250,10 @@ struct GradPlan {
   unsigned run_blocks, zero_blocks;
   const uint2* pairs;
   const uint32_t* present;
-  // [chunk][2][part_ld]: the sums of the run that comes from the chunk before, and of the one that goes on; a
-  // tile's in the order of its threads
+  // [chunk][2][part_ld]: the sums of the run that comes from the chunk before, and of the one that goes on
   float* parts;
   long long part_ld;
+  int join_tiles;
 };
 
 // The columns of a tile: EG_THREADS vectors.  `col0` is the tile's first one.
@@ -284,8 +327,15 @@ __global__ void __launch_bounds__(EG_THREADS) k_embed_grad(EmbedArgs a, GradPlan
       if (goes_on && j + q + 1 < n) continue;
       if (from_before || goes_on) {
         float* part = p.parts + ((long long)c * 2 + (from_before ? 0 : 1)) * p.part_ld + col0;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int e = 0; e < PER; ++e) part[e * EG_THREADS + threadIdx.x] = sum[e];
+          for (int e = 0; e < PER; e += 4)
+            *reinterpret_cast<float4*>(part + threadIdx.x * PER + e) =
+                make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) part[C::col(threadIdx.x, 0, e)] = sum[e];
+        }
       } else {
         write_grad<T, VEC>(a, token, col0, sum);
       }
@@ -296,30 +346,61 @@ __global__ void __launch_bounds__(EG_THREADS) k_embed_grad(EmbedArgs a, GradPlan
   }
 }
 
-// A run that starts in chunk c and goes on: its parts, in order.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(EG_THREADS) k_embed_join(EmbedArgs a, GradPlan p) {
-  constexpr int PER = Elem<T>::PER16;
+// A run that starts in chunk c and goes on: the sum of its parts, for a tile of columns.  Warp w adds the parts w,
+// w + 8, ..., and the warps' sums are added in order.
+constexpr int EJ_WARPS = 8, EJ_VECS = 4, EJ_COLS = 128 * EJ_VECS;
+template <typename T>
+__global__ void __launch_bounds__(32 * EJ_WARPS) k_embed_join(EmbedArgs a, GradPlan p) {
+  __shared__ float s_sum[EJ_WARPS][EJ_COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x / p.tiles, tile = blockIdx.x - c * p.tiles;
-  const long long end = (long long)(c + 1) * p.chunk;
+  const int c = blockIdx.x / p.join_tiles, tile = blockIdx.x - c * p.join_tiles;
+  const long long end = (long long)(c + 1) * p.chunk, start = end - p.chunk;
   if (end >= a.N) return;
-  const uint32_t token = __ldg(p.pairs + end - 1).x;
-  if (token >= (uint32_t)a.vocab || __ldg(p.pairs + end).x != token) return;
-  // from the chunk before: not its first part
-  const long long start = (long long)c * p.chunk;
-  if (start > 0 && __ldg(p.pairs + start - 1).x == token) return;
-  const int col0 = tile * EG_THREADS * PER;
-  float sum[PER];
-  const float* part = p.parts + ((long long)c * 2 + 1) * p.part_ld + col0 + threadIdx.x;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) sum[e] = part[e * EG_THREADS];
-  for (int k = c + 1; k < p.n_chunks && __ldg(p.pairs + (long long)k * p.chunk).x == token; ++k) {
-    part = p.parts + (long long)k * 2 * p.part_ld + col0 + threadIdx.x;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) sum[e] += part[e * EG_THREADS];
+  const uint32_t token = __ldg(p.pairs + end - 1).x, next = __ldg(p.pairs + end).x;
+  const uint32_t prev = start > 0 ? __ldg(p.pairs + start - 1).x : 0xFFFFFFFFu;
+  // no run goes on, or it comes from the chunk before
+  if (token >= (uint32_t)a.vocab || next != token || (prev == token && __ldg(p.pairs + start).x == token)) return;
+  // its last chunk: the last whose first pair has the token
+  int last = c + 1;
+  for (int k0 = c + 2;; k0 += 32) {
+    const int k = k0 + lane;
+    const bool same = k < p.n_chunks && __ldg(p.pairs + (long long)k * p.chunk).x == token;
+    const uint32_t run = __ballot_sync(0xFFFFFFFFu, same);
+    last += run == 0xFFFFFFFFu ? 32 : __ffs(~run) - 1;
+    if (run != 0xFFFFFFFFu) break;
   }
-  write_grad<T, VEC>(a, token, col0, sum);
+  // part 0: of chunk c; part i: of chunk c + i
+  const int n = last - c + 1;
+  const float* from = p.parts + (long long)c * 2 * p.part_ld + tile * EJ_COLS + lane * 4;
+  float4 sum[EJ_VECS];
+#pragma unroll
+  for (int v = 0; v < EJ_VECS; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = warp; i < n; i += EJ_WARPS) {
+#pragma unroll
+    for (int v = 0; v < EJ_VECS; ++v) {
+      const float4 x = *reinterpret_cast<const float4*>(from + (i == 0 ? 1 : 2LL * i) * p.part_ld + v * 128);
+      sum[v].x += x.x;
+      sum[v].y += x.y;
+      sum[v].z += x.z;
+      sum[v].w += x.w;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < EJ_VECS; ++v) *reinterpret_cast<float4*>(&s_sum[warp][v * 128 + lane * 4]) = sum[v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < EJ_COLS; i += 32 * EJ_WARPS) {
+    const int id = tile * EJ_COLS + i;
+    if (id >= a.d) return;
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < EJ_WARPS; ++w) t += s_sum[w][i];
+    T* to = static_cast<T*>(a.dst) + (long long)token * a.dst_ld + id;
+    t *= a.scale;
+    if (a.accumulate) t += Elem<T>::to_f(*to);
+    *to = Elem<T>::from_f(t);
+  }
 }
 
 // Pairs per chunk: 64, fewer where that leaves SMs without a block.
@@ -367,40 +448,46 @@ cudaError_t launch_zeros(const Ctx& c, const EmbedArgs& a) {
                     "cudaMemset2DAsync");
 }
 
+template <int BITS>
+cudaError_t launch_sort(const Ctx& c, const EmbedArgs& a, int passes, uint2* const* buf, uint32_t* present) {
+  static unsigned long long smem_done = 0;
+  cudaError_t e = allow_max_smem(k_token_sort<BITS>, c.device, &smem_done);
+  if (e != cudaSuccess) return e;
+  // one block while a warp of it has no more pairs than it keeps in registers
+  const unsigned ranks = a.N > 32 * TS_WARPS * TS_ITEMS / 2 ? TS_RANKS : 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ranks;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(TS_THREADS);
+  cfg.dynamicSmemBytes = (size_t)TS_WARPS * (1u << BITS) * 4;
+  cfg.stream = c.stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  prof_before("token_sort", c.stream);
+  e = cudaLaunchKernelEx(&cfg, k_token_sort<BITS>, a.tokens, a.N, a.vocab, passes, buf[0], buf[1], present);
+  prof_after(c.stream);
+  return e;
+}
+
 template <typename T>
 cudaError_t run_embed_backward(const Ctx& c, const EmbedArgs& a) {
   constexpr int PER = Elem<T>::PER16;
   const GradLayout L = grad_layout(a.N, a.vocab, a.d);
   uint2* buf[2] = {reinterpret_cast<uint2*>(a.ws + L.buf0), reinterpret_cast<uint2*>(a.ws + L.buf1)};
   uint32_t* present = reinterpret_cast<uint32_t*>(a.ws + L.present);
+  if (a.N == 0) return launch_zeros<T>(c, a);
   int key_bits = 0;
   while (a.vocab >> key_bits) ++key_bits;  // the largest key is vocab
-  const int passes = (key_bits + TS_BITS - 1) / TS_BITS, bits = (key_bits + passes - 1) / passes;
-  if (a.N == 0) return launch_zeros<T>(c, a);
-  static unsigned long long smem_done = 0;
-  cudaError_t e = allow_max_smem(k_token_sort, c.device, &smem_done);
+  const int passes = (key_bits + TS_BITS - 1) / TS_BITS;
+  cudaError_t e = (key_bits + passes - 1) / passes <= 6 ? launch_sort<6>(c, a, passes, buf, present)
+                                                        : launch_sort<TS_BITS>(c, a, passes, buf, present);
   if (e != cudaSuccess) return e;
-  {
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    const unsigned ranks = a.N > 4 * TS_THREADS ? 8 : 1;
-    at[1].val.clusterDim.x = ranks;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks);
-    cfg.blockDim = dim3(TS_THREADS);
-    cfg.dynamicSmemBytes = (size_t)TS_WARPS * (1u << bits) * 4;
-    cfg.stream = c.stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    prof_before("token_sort", c.stream);
-    e = cudaLaunchKernelEx(&cfg, k_token_sort, a.tokens, a.N, a.vocab, bits, passes, buf[0], buf[1], present);
-    prof_after(c.stream);
-    if (e != cudaSuccess) return e;
-  }
   const bool vec = whole_vectors(a.src, a.src_ld, a.N, a.d, sizeof(T)) &&
                    whole_vectors(a.dst, a.dst_ld, a.vocab, a.d, sizeof(T));
   GradPlan p = {};
@@ -413,11 +500,12 @@ cudaError_t run_embed_backward(const Ctx& c, const EmbedArgs& a) {
   p.present = present;
   p.parts = reinterpret_cast<float*>(a.ws + L.parts);
   p.part_ld = (long long)part_width(a.d);
+  p.join_tiles = (a.d + EJ_COLS - 1) / EJ_COLS;
   e = launch_pdl(c, "embed_grad", vec ? k_embed_grad<T, true> : k_embed_grad<T, false>,
                  dim3(p.run_blocks + p.zero_blocks), dim3(EG_THREADS), 0, a, p);
   if (e != cudaSuccess || p.n_chunks == 1) return e;
-  return launch_pdl(c, "embed_join", vec ? k_embed_join<T, true> : k_embed_join<T, false>, dim3(p.run_blocks),
-                    dim3(EG_THREADS), 0, a, p);
+  return launch_pdl(c, "embed_join", k_embed_join<T>, dim3((unsigned)p.n_chunks * (unsigned)p.join_tiles),
+                    dim3(32 * EJ_WARPS), 0, a, p);
 }
 
 }  // namespace
