@@ -75,27 +75,6 @@ constexpr int TS_BITS = 9;   // at most, per pass
 constexpr int TS_ITEMS = 8;  // rows of 32 pairs of a warp at a time
 constexpr int TS_RANKS = 8;  // blocks of the cluster, at most
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// The word at `p` of this block's shared memory, in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {
-  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
-  return v;
-}
-
 // The lanes whose digit is this lane's, among those that have one.  By a ballot per bit: a match instruction takes
 // an SM many times as long (a sort of 32768 tokens 27 us with it).
 template <int BITS>
@@ -451,28 +430,12 @@ cudaError_t launch_zeros(const Ctx& c, const EmbedArgs& a) {
 template <int BITS>
 cudaError_t launch_sort(const Ctx& c, const EmbedArgs& a, int passes, uint2* const* buf, uint32_t* present) {
   static unsigned long long smem_done = 0;
-  cudaError_t e = allow_max_smem(k_token_sort<BITS>, c.device, &smem_done);
+  const cudaError_t e = allow_max_smem(k_token_sort<BITS>, c.device, &smem_done);
   if (e != cudaSuccess) return e;
   // one block while a warp of it has no more pairs than it keeps in registers
   const unsigned ranks = a.N > 32 * TS_WARPS * TS_ITEMS / 2 ? TS_RANKS : 1;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = ranks;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ranks);
-  cfg.blockDim = dim3(TS_THREADS);
-  cfg.dynamicSmemBytes = (size_t)TS_WARPS * (1u << BITS) * 4;
-  cfg.stream = c.stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  prof_before("token_sort", c.stream);
-  e = cudaLaunchKernelEx(&cfg, k_token_sort<BITS>, a.tokens, a.N, a.vocab, passes, buf[0], buf[1], present);
-  prof_after(c.stream);
-  return e;
+  return launch_clusters(c, "token_sort", k_token_sort<BITS>, ranks, dim3(ranks), dim3(TS_THREADS),
+                         (size_t)TS_WARPS * (1u << BITS) * 4, a.tokens, a.N, a.vocab, passes, buf[0], buf[1], present);
 }
 
 template <typename T>

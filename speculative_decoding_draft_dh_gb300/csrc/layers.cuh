@@ -66,24 +66,66 @@ cudaError_t launch_norm(const Ctx& c, const NormArgs& a, int dtype, int param_dt
 cudaError_t launch_norm_backward(const Ctx& c, const NormArgs& a, int dtype, int param_dtype);
 
 // Launches with programmatic stream serialization: the kernel may start while the grid before it ends, and
-// waits for it by griddepcontrol.wait.
+// waits for it by griddepcontrol.wait.  In clusters of `ranks` blocks (1: none).
 template <class... P, class... A>
-cudaError_t launch_pdl(const Ctx& c, const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
-                       A... args) {
-  cudaLaunchAttribute at[1];
+cudaError_t launch_clusters(const Ctx& c, const char* name, void (*kernel)(P...), unsigned ranks, dim3 grid, dim3 block,
+                            size_t smem, A... args) {
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ranks;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
   prof_before(name, c.stream);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
   prof_after(c.stream);
   return e;
+}
+template <class... P, class... A>
+cudaError_t launch_pdl(const Ctx& c, const char* name, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                       A... args) {
+  return launch_clusters(c, name, kernel, 1, grid, block, smem, args...);
+}
+
+// ------------------------------------------------------------------ thread-block clusters
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The word at `p` of this block's shared memory, in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, uint32_t rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_cluster(const uint4* p, uint32_t rank) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(r)
+               : "memory");
+  return v;
 }
 
 // ------------------------------------------------------------------ rows of hidden states

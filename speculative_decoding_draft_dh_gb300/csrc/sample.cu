@@ -101,6 +101,10 @@ struct Weights {
     *down = -(int)e;
     return (uint32_t)rint(exp2(x - e) * 268435456.0);
   }
+  // not far: the weight in 64ths of an octave, rounded
+  __device__ __forceinline__ int step(float z) const {
+    return __float_as_int(fmaf(z, c.hi, EXP_MAGIC)) - EXP_MAGIC_BITS;
+  }
   __device__ __forceinline__ u64 operator()(float z) const {
     if (!(z >= zlow)) return 0;
     uint32_t q;
@@ -110,7 +114,7 @@ struct Weights {
     } else {
       const float k = fmaf(z, c.hi, EXP_MAGIC), kf = k - EXP_MAGIC;
       const float r = fmaf(z, c.lo, fmaf(z, c.hi, -kf));
-      const int ki = __float_as_int(k) - EXP_MAGIC_BITS, j = ki & 63;
+      const int ki = step(z), j = ki & 63;
       // 2^r - 1 by its series
       const float x = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
       // added to 1.5 2^23, which rounds to an integer in the low bits; |tab.f x| < 2^22
@@ -212,7 +216,7 @@ __device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, f
     const float low = m - reach;
     const uint2* tb = tab.e + (lane & 15);
     const f32x2 cc = pack2(ch, ch), cd = pack2(cl, cl), magic = pack2(EXP_MAGIC, EXP_MAGIC);
-    const f32x2 nmagic = pack2(-EXP_MAGIC, -EXP_MAGIC), none = pack2(-1.f, -1.f);
+    const f32x2 none = pack2(-1.f, -1.f);
     const f32x2 c3 = pack2(0.0555041087f, 0.0555041087f), c2 = pack2(0.240226507f, 0.240226507f),
                 c1 = pack2(0.693147181f, 0.693147181f);
     const int base = e_ref + (EXP_MAGIC_BITS >> 6) + 8;  // with 2^24 of the 2^52, counted from bit 32
@@ -223,8 +227,8 @@ __device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, f
 #pragma unroll
       for (int q = 0; q < PER; q += 2) {
         const f32x2 z = pack2(fmaxf(x[q], low), fmaxf(x[q + 1], low));
-        const f32x2 k = fma2(z, cc, magic), kf = add2(k, nmagic);
-        const f32x2 r = fma2(z, cd, fma2(z, cc, mul2(kf, none)));
+        const f32x2 k = fma2(z, cc, magic);
+        const f32x2 r = fma2(z, cd, fma2(z, cc, fma2(k, none, magic)));  // (magic - k is exact)
         const f32x2 y = mul2(r, fma2(r, fma2(r, c3, c2), c1));
         float ka, kb, ya, yb;
         unpack2(k, ka, kb);
@@ -234,7 +238,7 @@ __device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, f
           const uint2 w = tb[(ki & 63) * 16];
           const uint32_t n = w.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(w.y), yx, 12582912.f)) - 0x4B400000);
           // n 2^24 >> (e_ref - e), from n 2^32
-          sum += ((u64)n << 32) >> min(base - (ki >> 6), 63);
+          sum += ((u64)n << 32) >> (base - (ki >> 6));  // at most 63: z is at least low
         };
         one(ka, ya);
         one(kb, yb);
@@ -247,9 +251,13 @@ __device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, f
 }
 
 constexpr int SC_THREADS = 256;
+#ifndef SC_B
+#define SC_B 5
+#endif
+constexpr int SC_BLOCKS = SC_B;  // of an SM
 
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(SC_THREADS) k_sample_scan(SampleArgs a, int n_seg, float* gmax, SegMass* segs) {
+__global__ void __launch_bounds__(SC_THREADS, SC_BLOCKS) k_sample_scan(SampleArgs a, int n_seg, float* gmax, SegMass* segs) {
   __shared__ ScanTable tab;
   fill_table(tab, SC_THREADS);
   __syncthreads();
@@ -277,11 +285,11 @@ __global__ void __launch_bounds__(SC_THREADS) k_sample_scan(SampleArgs a, int n_
 // ------------------------------------------------------------------ the search
 
 // A histogram over a range of keys: masses in two words, counts.
-struct Bins {
+struct __align__(16) Bins {
   uint32_t lo[SP_BINS], hi[SP_BINS], count[SP_BINS];
   __device__ __forceinline__ u64 mass(int b) const { return ((u64)hi[b] << 32) | lo[b]; }
-  __device__ __forceinline__ void add(uint32_t b, u64 w) {
-    atomicAdd(&count[b], 1u);
+  __device__ __forceinline__ void add(uint32_t b, u64 w, bool counted) {
+    if (counted) atomicAdd(&count[b], 1u);
     const uint32_t x = (uint32_t)w;
     uint32_t h = (uint32_t)(w >> 32);
     // (there is no 64-bit addition in shared memory)
@@ -290,13 +298,8 @@ struct Bins {
   }
 };
 
-struct SampleSmem {
-  union {
-    Bins bins[2];       // of the whole range, of a part of it
-    u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
-    uint32_t group_count[SP_BINS];
-  };
-  uint32_t groups[SP_GROUPS];
+// What the steps of a block leave for one another.
+struct Scratch {
   ExpTable tab;
   u64 warp_mass[SP_WARPS];
   uint32_t warp_count[SP_WARPS];
@@ -307,6 +310,19 @@ struct SampleSmem {
   uint32_t n_list, n_groups;
   u64 found_mass, found_w;
   uint32_t found_at, found_id;
+  uint32_t share[2];  // of a sum over a cluster
+};
+struct SampleSmem : Scratch {
+  union {
+    Bins bins[2];       // of the whole range, of a part of it
+    u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
+    uint32_t group_count[SP_BINS];
+  };
+  uint32_t groups[SP_GROUPS];
+};
+struct SearchSmem : Scratch {
+  Bins local;    // of this block's share of the row
+  Bins bins[2];  // of the whole row
 };
 
 // A place in the order: all tokens above `key`, of which there are `above` with mass `above_mass`, and the tokens
@@ -316,17 +332,29 @@ struct Place {
   u64 above_mass, w;
 };
 
-// f(value) of every logit of the row that is in [from, to] (finite numbers).
+// A block's share of a row: the ids [from, to), whole steps of a warp but for the row's end.
+struct Share {
+  int from, to;
+};
+template <typename T, int RANKS>
+__device__ __forceinline__ Share share_of_row(int vocab) {
+  if (RANKS == 1) return {0, vocab};
+  constexpr int STEP = 32 * Elem<T>::PER16;
+  const int each = (vocab + RANKS * STEP - 1) / (RANKS * STEP) * STEP, from = min((int)cluster_rank() * each, vocab);
+  return {from, min(from + each, vocab)};
+}
+
+// f(value) of every logit of the share that is in [from, to] (finite numbers).
 template <typename T, bool ALIGNED, typename F>
-__device__ __forceinline__ void each(const T* row, int vocab, float from, float to, F f) {
+__device__ __forceinline__ void each(const T* row, Share part, float from, float to, F f) {
   constexpr int PER = Elem<T>::PER16, AHEAD = 4;
-  for (int id0 = threadIdx.x * PER; id0 < vocab; id0 += AHEAD * SP_THREADS * PER) {
+  for (int id0 = part.from + threadIdx.x * PER; id0 < part.to; id0 += AHEAD * SP_THREADS * PER) {
     uint4 u[AHEAD];
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       const int id = id0 + q * SP_THREADS * PER;
       u[q] = make_uint4(NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD);
-      if (id < vocab) u[q] = row_vec<T, ALIGNED>(row, id, vocab);
+      if (id < part.to) u[q] = row_vec<T, ALIGNED>(row, id, part.to);
     }
 #pragma unroll 1
     for (int q = 0; q < AHEAD; ++q) {
@@ -339,11 +367,10 @@ __device__ __forceinline__ void each(const T* row, int vocab, float from, float 
   }
 }
 
-// The bin, of 2^sh keys from the top down, in which `want` is reached: tokens (BY_COUNT) or a mass of want or more
-// (STRICT: more than want), counted on from `above` tokens of `above_mass`; the last bin with a token where it is
-// not.
+// The bin, from the top down, in which `want` is reached: tokens (BY_COUNT) or a mass of want or more (STRICT: more
+// than want), counted on from `above` tokens of `above_mass`; the last bin that is not empty where it is not.
 struct Histogram {
-  int bin, sh;
+  int bin;
   uint32_t above, count;
   u64 above_mass, mass;
 };
@@ -351,20 +378,94 @@ __device__ __forceinline__ int bin_shift(uint32_t lo, uint32_t hi) {
   const int bits = 32 - __clz(hi - lo);
   return bits > 11 ? bits - 11 : 0;
 }
-// The tokens with keys [lo, hi].
-template <typename T, bool ALIGNED>
-__device__ __noinline__ void fill_bins(Bins& bins, const T* row, int vocab, uint32_t lo, uint32_t hi,
-                                       const Weights& weight) {
-  for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) bins.lo[b] = bins.hi[b] = bins.count[b] = 0;
-  __syncthreads();
-  const int sh = bin_shift(lo, hi);
-  each<T, ALIGNED>(row, vocab, value_of<T>(lo), value_of<T>(hi),
-                   [&](float z) { bins.add((hi - key_of<T>(z)) >> sh, weight(z)); });
+
+// The bins of a row's first histogram: steps of a 32nd of an octave of the weights (linear in the logits, so that
+// neighbouring tokens seldom meet in a bin), or, where weights are far, ranges of keys.
+struct Coarse {
+  int top;        // step of the largest weight
+  uint32_t lo, hi;
+  int sh;         // far: of the keys
+  bool far;
+  template <typename T>
+  __device__ __forceinline__ int bin(float z, const Weights& weight) const {
+    return far ? (int)((hi - key_of<T>(z)) >> sh) : (top - weight.step(z)) >> 1;
+  }
+  // The range of keys that holds a bin's tokens (and others).
+  template <typename T>
+  __device__ __forceinline__ void keys(int b, const Weights& weight, uint32_t* from, uint32_t* to) const {
+    if (far) {
+      const uint32_t reach = (1u << sh) - 1u;
+      *to = hi - ((uint32_t)b << sh);
+      *from = *to - lo > reach ? *to - reach : lo;
+    } else {
+      // one step more on either side covers the roundings
+      const float z1 = (float)(top - 2 * b + 1) / (64.f * weight.c.hi), z0 = (float)(top - 2 * b - 2) / (64.f * weight.c.hi);
+      *from = max(lo, min(key_of<T>(z0), hi));
+      *to = min(hi, max(key_of<T>(z1), *from));
+    }
+  }
+};
+
+// `out` = the sum of the cluster's `local`.
+template <int RANKS>
+__device__ __forceinline__ void merge_bins(Bins& local, Bins& out) {
+  if constexpr (RANKS == 1) {
+    __syncthreads();  // local is out
+  } else {
+    static_assert(SP_BINS == 4 * SP_THREADS, "a thread has four bins");
+    cluster_sync();
+    const int b = threadIdx.x;
+    u64 m[4] = {0, 0, 0, 0};
+    uint4 c = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (uint32_t r = 0; r < RANKS; ++r) {
+      const uint4 l = ld_cluster(reinterpret_cast<const uint4*>(local.lo) + b, r);
+      const uint4 h = ld_cluster(reinterpret_cast<const uint4*>(local.hi) + b, r);
+      const uint4 n = ld_cluster(reinterpret_cast<const uint4*>(local.count) + b, r);
+      m[0] += ((u64)h.x << 32) | l.x;
+      m[1] += ((u64)h.y << 32) | l.y;
+      m[2] += ((u64)h.z << 32) | l.z;
+      m[3] += ((u64)h.w << 32) | l.w;
+      c.x += n.x;
+      c.y += n.y;
+      c.z += n.z;
+      c.w += n.w;
+    }
+    reinterpret_cast<uint4*>(out.lo)[b] = make_uint4((uint32_t)m[0], (uint32_t)m[1], (uint32_t)m[2], (uint32_t)m[3]);
+    reinterpret_cast<uint4*>(out.hi)[b] =
+        make_uint4((uint32_t)(m[0] >> 32), (uint32_t)(m[1] >> 32), (uint32_t)(m[2] >> 32), (uint32_t)(m[3] >> 32));
+    reinterpret_cast<uint4*>(out.count)[b] = c;
+    cluster_sync();  // `local` has been read
+  }
+}
+__device__ __forceinline__ void clear_bins(Bins& bins) {
+  for (int b = threadIdx.x; b < SP_BINS / 4; b += SP_THREADS)
+    reinterpret_cast<uint4*>(bins.lo)[b] = reinterpret_cast<uint4*>(bins.hi)[b] =
+        reinterpret_cast<uint4*>(bins.count)[b] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 }
+// All tokens with a weight, by the coarse bins.
+template <typename T, bool ALIGNED, int RANKS>
+__device__ __noinline__ void fill_coarse(Bins& local, Bins& out, const T* row, Share part, const Coarse& coarse,
+                                         const Weights& weight, bool counted) {
+  clear_bins(local);
+  each<T, ALIGNED>(row, part, weight.zlow, weight.m,
+                   [&](float z) { local.add(coarse.bin<T>(z, weight), weight(z), counted); });
+  merge_bins<RANKS>(local, out);
+}
+// Those of one coarse bin with keys [lo, hi], by ranges of keys.
+template <typename T, bool ALIGNED, int RANKS>
+__device__ __noinline__ void fill_fine(Bins& local, Bins& out, const T* row, Share part, const Coarse& coarse, int bin,
+                                       uint32_t lo, uint32_t hi, const Weights& weight) {
+  clear_bins(local);
+  const int sh = bin_shift(lo, hi);
+  each<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), [&](float z) {
+    if (coarse.bin<T>(z, weight) == bin) local.add((hi - key_of<T>(z)) >> sh, weight(z), true);
+  });
+  merge_bins<RANKS>(local, out);
+}
 template <bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Histogram find_bin(SampleSmem& s, const Bins& bins, int sh, uint32_t above, u64 above_mass,
-                                           u64 want) {
+__device__ __noinline__ Histogram find_bin(Scratch& s, const Bins& bins, uint32_t above, u64 above_mass, u64 want) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s.bin = s.last = -1;
   // inclusive sums over the bins, four to a thread
@@ -415,7 +516,7 @@ __device__ __noinline__ Histogram find_bin(SampleSmem& s, const Bins& bins, int 
   for (int q = 0; q < OWN; ++q) {
     const u64 mb = bins.mass(b0 + q);
     const uint32_t cb = bins.count[b0 + q];
-    if (cb) {
+    if (cb || mb) {
       last = b0 + q;
       last_mass = ma;
       last_count = ca;
@@ -429,50 +530,57 @@ __device__ __noinline__ Histogram find_bin(SampleSmem& s, const Bins& bins, int 
   }
   if (last >= 0) atomicMax(&s.last, last);
   __syncthreads();
-  // where the sums never reach it: the last bin that holds a token
+  // where the sums never reach it: the last bin that is not empty
   if (s.bin < 0 && last >= 0 && last == s.last) found(last, last_mass, last_count);
   __syncthreads();
-  const Histogram h = {s.bin < 0 ? s.last : s.bin, sh, s.above_count, s.bin_count, s.above_mass, s.bin_mass};
+  const Histogram h = {s.bin < 0 ? s.last : s.bin, s.above_count, s.bin_count, s.above_mass, s.bin_mass};
   __syncthreads();
   return h;
 }
 
-// The first place with `want` tokens or more (BY_COUNT), or with a mass of want or more (STRICT: more than want),
-// among the keys [lo, hi], whose histogram is in bins[0]; the last place where there is none.
-template <typename T, bool ALIGNED, bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Place descend(SampleSmem& s, const T* row, int vocab, uint32_t lo, uint32_t hi, u64 want,
-                                      const Weights& weight) {
+// The first place with `want` tokens or more (BY_COUNT), or with a mass of want or more (STRICT: more than want); the
+// last place where there is none.  `whole` is the row's coarse histogram; `local` and `out` are for finer ones.
+template <typename T, bool ALIGNED, int RANKS, bool BY_COUNT, bool STRICT>
+__device__ __noinline__ Place descend(Scratch& s, const Bins& whole, Bins& local, Bins& out, const T* row, Share part,
+                                      const Coarse& coarse, u64 want, const Weights& weight) {
   Place p = {};
-  Histogram h = find_bin<BY_COUNT, STRICT>(s, s.bins[0], bin_shift(lo, hi), 0, 0, want);
+  Histogram h = find_bin<BY_COUNT, STRICT>(s, whole, 0, 0, want);
+  const int bin = h.bin;
+  uint32_t lo, hi;
+  coarse.keys<T>(bin, weight, &lo, &hi);
   for (;;) {
     p.above_mass = h.above_mass;
     p.above = h.above;
-    hi -= (uint32_t)h.bin << h.sh;
-    const uint32_t reach = (1u << h.sh) - 1u;
+    fill_fine<T, ALIGNED, RANKS>(local, out, row, part, coarse, bin, lo, hi, weight);
+    const int sh = bin_shift(lo, hi);
+    h = find_bin<BY_COUNT, STRICT>(s, out, p.above, p.above_mass, want);
+    hi -= (uint32_t)h.bin << sh;
+    const uint32_t reach = (1u << sh) - 1u;
     if (hi - lo > reach) lo = hi - reach;
     if (lo == hi) {
+      p.above_mass = h.above_mass;
+      p.above = h.above;
       p.key = hi;
       p.n_equal = h.count;
-      p.w = h.mass / h.count;
+      p.w = h.count ? h.mass / h.count : 0;
       return p;
     }
-    fill_bins<T, ALIGNED>(s.bins[1], row, vocab, lo, hi, weight);
-    h = find_bin<BY_COUNT, STRICT>(s, s.bins[1], bin_shift(lo, hi), p.above, p.above_mass, want);
   }
 }
 
-// The id of the j-th token (from 1, by id) whose key is `key`; the last one where there are fewer.
-template <typename T, bool ALIGNED>
-__device__ __noinline__ int find_token(SampleSmem& s, const T* row, int vocab, uint32_t key, uint32_t j) {
+// The id of the j-th token (from 1, by id) whose key is `key`, the last one where there are fewer; -1 in the blocks
+// of a cluster whose share does not hold it.
+template <typename T, bool ALIGNED, int RANKS>
+__device__ __noinline__ int find_token(Scratch& s, const T* row, Share part, uint32_t key, uint32_t j) {
   constexpr int PER = Elem<T>::PER16, STEP = 32 * PER;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int share = (vocab + SP_WARPS * STEP - 1) / (SP_WARPS * STEP) * STEP;
-  const long long from = (long long)warp * share, to = from + share < vocab ? from + share : vocab;
-  auto matches = [&](long long id) -> uint32_t {
+  const int each = (part.to - part.from + SP_WARPS * STEP - 1) / (SP_WARPS * STEP) * STEP;
+  const int from = min(part.from + warp * each, part.to), to = min(from + each, part.to);
+  auto matches = [&](int id) -> uint32_t {
     uint32_t bits = 0;
     if (id < to) {
       float x[PER];
-      Elem<T>::unpack(row_vec<T, ALIGNED>(row, (int)id, vocab), x);
+      Elem<T>::unpack(row_vec<T, ALIGNED>(row, id, to), x);
 #pragma unroll
       for (int e = 0; e < PER; ++e)
         if (id + e < to && key_of<T>(x[e]) == key) bits |= 1u << e;
@@ -480,20 +588,33 @@ __device__ __noinline__ int find_token(SampleSmem& s, const T* row, int vocab, u
     return bits;
   };
   uint32_t n = 0;
-  for (long long i = from; i < to; i += STEP) n += __popc(matches(i + lane * PER));
+#pragma unroll 4
+  for (int i = from; i < to; i += STEP) n += __popc(matches(i + lane * PER));
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   if (lane == 0) s.warp_count[warp] = n;
-  if (threadIdx.x == 0) s.bin = 0;
+  if (threadIdx.x == 0) s.bin = -1;
   __syncthreads();
   uint32_t before = 0, all = 0;
   for (int w = 0; w < SP_WARPS; ++w) {
     if (w < warp) before += s.warp_count[w];
     all += s.warp_count[w];
   }
+  if constexpr (RANKS > 1) {
+    if (threadIdx.x == 0) s.share[0] = all;
+    cluster_sync();
+    uint32_t total = 0;
+    for (uint32_t r = 0; r < RANKS; ++r) {
+      const uint32_t x = ld_cluster(&s.share[0], r);
+      if (r < cluster_rank()) before += x;
+      total += x;
+    }
+    all = total;
+    cluster_sync();
+  }
   if (j > all) j = all;
   if (before < j && j <= before + n) {
     uint32_t want = j - before;
-    for (long long i = from; i < to; i += STEP) {
+    for (int i = from; i < to; i += STEP) {
       const uint32_t bits = matches(i + lane * PER);
       uint32_t inc = __popc(bits);
 #pragma unroll
@@ -503,7 +624,7 @@ __device__ __noinline__ int find_token(SampleSmem& s, const T* row, int vocab, u
       }
       const uint32_t total = __shfl_sync(0xFFFFFFFFu, inc, 31), excl = inc - __popc(bits);
       if (want <= total) {
-        if (excl < want && want <= inc) s.bin = (int)i + lane * PER + __fns(bits, 0, (int)(want - excl));
+        if (excl < want && want <= inc) s.bin = i + lane * PER + __fns(bits, 0, (int)(want - excl));
         break;
       }
       want -= total;
@@ -519,7 +640,7 @@ __device__ __forceinline__ float share(u64 w, u64 mass) {
 }
 
 // Sum over the block; every thread gets it.
-__device__ __forceinline__ u64 block_mass(SampleSmem& s, u64 x) {
+__device__ __forceinline__ u64 block_mass(Scratch& s, u64 x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
   if ((threadIdx.x & 31) == 0) s.warp_mass[threadIdx.x >> 5] = x;
@@ -530,7 +651,7 @@ __device__ __forceinline__ u64 block_mass(SampleSmem& s, u64 x) {
   return x;
 }
 // Sum over the threads before this one.
-__device__ __forceinline__ u64 mass_before(SampleSmem& s, u64 x) {
+__device__ __forceinline__ u64 mass_before(Scratch& s, u64 x) {
   u64 inc = x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -567,23 +688,27 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
   return want + rest;
 }
 
-// Token and probability by searches over the whole row.
-template <typename T, bool ALIGNED>
-__device__ __noinline__ void pick_by_search(SampleSmem& s, const T* row, int vocab, const RowState& r,
-                                            const Weights& weight, int* token, float* prob) {
-  fill_bins<T, ALIGNED>(s.bins[0], row, vocab, r.low, r.top, weight);
+// Token and probability by searches over the whole row, by one block or a cluster; token -1 in the blocks that do
+// not hold it.
+template <typename T, bool ALIGNED, int RANKS>
+__device__ __noinline__ void pick_by_search(Scratch& s, Bins& whole, Bins& local, Bins& fine, const T* row, int vocab,
+                                            const RowState& r, const Weights& weight, int* token, float* prob) {
+  const Share part = share_of_row<T, RANKS>(vocab);
+  const Coarse coarse = {weight.far ? 0 : weight.step(weight.m), r.low, r.top, bin_shift(r.low, r.top), weight.far};
+  fill_coarse<T, ALIGNED, RANKS>(RANKS == 1 ? whole : local, whole, row, part, coarse, weight, r.top_k != 0);
+  Bins& part_bins = RANKS == 1 ? fine : local;
   // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
   uint32_t key = r.low, equal = 0xFFFFFFFFu;
   u64 mass = r.mass;
   if (r.top_k) {
-    const Place p = descend<T, ALIGNED, true, false>(s, row, vocab, r.low, r.top, (u64)r.top_k, weight);
+    const Place p = descend<T, ALIGNED, RANKS, true, false>(s, whole, part_bins, fine, row, part, coarse, (u64)r.top_k, weight);
     key = p.key;
     equal = min((uint32_t)r.top_k - min(p.above, (uint32_t)r.top_k), p.n_equal);
     mass = p.above_mass + equal * p.w;
   }
   if (r.top_p < 1.f) {
     const u64 want = share_of(r.top_p, mass);
-    const Place p = descend<T, ALIGNED, false, false>(s, row, vocab, r.low, r.top, want, weight);
+    const Place p = descend<T, ALIGNED, RANKS, false, false>(s, whole, part_bins, fine, row, part, coarse, want, weight);
     uint32_t j = p.n_equal;
     if (p.w && p.above_mass < want) j = (uint32_t)min((u64)j, (want - p.above_mass + p.w - 1) / p.w);
     if (p.key == key) j = min(j, equal);
@@ -596,16 +721,26 @@ __device__ __noinline__ void pick_by_search(SampleSmem& s, const T* row, int voc
     key = max(key, r.least);
     equal = 0xFFFFFFFFu;
     u64 sum = 0;
-    each<T, ALIGNED>(row, vocab, value_of<T>(key), weight.m, [&](float z) { sum += weight(z); });
+    each<T, ALIGNED>(row, part, value_of<T>(key), weight.m, [&](float z) { sum += weight(z); });
     mass = block_mass(s, sum);
+    if constexpr (RANKS > 1) {
+      if (threadIdx.x == 0) {
+        s.share[0] = (uint32_t)mass;
+        s.share[1] = (uint32_t)(mass >> 32);
+      }
+      cluster_sync();
+      mass = 0;
+      for (uint32_t k = 0; k < RANKS; ++k) mass += ((u64)ld_cluster(&s.share[1], k) << 32) | ld_cluster(&s.share[0], k);
+      cluster_sync();
+    }
   }
   const u64 want = draw_at(r.u, mass);
-  const Place p = descend<T, ALIGNED, false, true>(s, row, vocab, r.low, r.top, want, weight);
+  const Place p = descend<T, ALIGNED, RANKS, false, true>(s, whole, part_bins, fine, row, part, coarse, want, weight);
   uint32_t j = p.n_equal;
   if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
   if (p.key == key) j = min(j, equal);
   // (p.key < key, below the kept prefix, is not reached: the searches go by the same sums)
-  *token = find_token<T, ALIGNED>(s, row, vocab, p.key, j);
+  *token = find_token<T, ALIGNED, RANKS>(s, row, part, p.key, j);
   *prob = share(p.w, mass);
 }
 
@@ -827,9 +962,16 @@ __device__ __noinline__ void pick_from_list(SampleSmem& s, const RowState& r, co
   *prob = share(s.found_w, mass);
 }
 
+// A row that is searched by k_sample_search.
+struct Job {
+  RowState row;
+  float m;
+  int searched;
+};
+
 template <typename T, bool ALIGNED, bool SHORT>
 __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int n_seg, const float* gmax_all,
-                                                            const SegMass* segs_all) {
+                                                               const SegMass* segs_all, Job* jobs) {
   extern __shared__ __align__(16) unsigned char sample_smem[];
   SampleSmem& s = *reinterpret_cast<SampleSmem*>(sample_smem);
   __shared__ float s_gmax[SHORT ? SP_WARPS * SEG_GROUPS : 1];
@@ -838,6 +980,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
   for (int i = threadIdx.x; i < (int)(sizeof(ExpTable) / 4); i += SP_THREADS)
     reinterpret_cast<uint32_t*>(&s.tab)[i] = reinterpret_cast<const uint32_t*>(&g_exp_table)[i];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!SHORT && jobs) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the searching kernel follows
   const T* row = static_cast<const T*>(a.logits) + n * a.ld;
   const float t = a.temperature ? __ldg(a.temperature + n) : a.temperature0;
   const float top_p = a.top_p ? __ldg(a.top_p + n) : a.top_p0, min_p = a.min_p ? __ldg(a.min_p + n) : a.min_p0;
@@ -879,6 +1022,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
   __syncthreads();
   int token = -1;
   float prob = 0.f;
+  bool searched = false;
   // no distribution: a NaN or +inf logit, nothing above -inf, settings or uniforms that are not numbers
   if (fabsf(m) < INFINITY && t >= 0.f && t < INFINITY && top_p == top_p && min_p == min_p && u == u) {
     RowState r;
@@ -895,7 +1039,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
         token = (int)id;
       } else {
         __syncthreads();
-        token = find_token<T, ALIGNED>(s, row, vocab, r.top, 1);
+        token = find_token<T, ALIGNED, 1>(s, row, Share{0, vocab}, r.top, 1);
       }
       prob = 1.f;
     } else {
@@ -921,7 +1065,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
       if (whole || (!r.top_k && r.top_p < 1.f)) {
         u64 sum = 0;
         if (weight.far) {
-          each<T, ALIGNED>(row, vocab, weight.zlow, weight.m, [&](float z) { sum += weight(z); });
+          each<T, ALIGNED>(row, Share{0, vocab}, weight.zlow, weight.m, [&](float z) { sum += weight(z); });
         } else {
           for (int i = threadIdx.x; i < n_seg; i += SP_THREADS) {
             const SegMass q = segs[i];
@@ -952,13 +1096,48 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
       if (listed) {
         sort_list(s);
         pick_from_list<T>(s, r, weight, &token, &prob);
-      } else {
+      } else if (SHORT || !jobs) {
         __syncthreads();
-        pick_by_search<T, ALIGNED>(s, row, vocab, r, weight, &token, &prob);
+        pick_by_search<T, ALIGNED, 1>(s, s.bins[0], s.bins[1], s.bins[1], row, vocab, r, weight, &token, &prob);
+      } else {
+        // left to k_sample_search
+        if (threadIdx.x == 0) jobs[n].row = r;
+        searched = true;
       }
     }
   }
+  if (!SHORT && jobs && threadIdx.x == 0) {
+    jobs[n].m = m;
+    jobs[n].searched = searched;
+  }
+  if (searched) return;
   if (threadIdx.x == 0) {
+    a.token[n] = token;
+    if (a.prob) a.prob[n] = prob;
+  }
+}
+
+// The rows whose lists would have been too long, each by a cluster.
+constexpr int SS_RANKS = 4;
+
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(SP_THREADS, 2) k_sample_search(SampleArgs a, const Job* jobs) {
+  extern __shared__ __align__(16) unsigned char sample_smem[];
+  SearchSmem& s = *reinterpret_cast<SearchSmem*>(sample_smem);
+  const int n = blockIdx.x / SS_RANKS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!__ldcg(&jobs[n].searched)) return;  // the whole cluster
+  for (int i = threadIdx.x; i < (int)(sizeof(ExpTable) / 4); i += SP_THREADS)
+    reinterpret_cast<uint32_t*>(&s.tab)[i] = reinterpret_cast<const uint32_t*>(&g_exp_table)[i];
+  __syncthreads();
+  const RowState r = jobs[n].row;
+  const float t = a.temperature ? __ldg(a.temperature + n) : a.temperature0;
+  const Weights weight(jobs[n].m, t, min(62 - (32 - __clz(a.vocab - 1)), SEG_FRAC), &s.tab);
+  int token;
+  float prob;
+  pick_by_search<T, ALIGNED, SS_RANKS>(s, s.bins[0], s.local, s.bins[1], static_cast<const T*>(a.logits) + n * a.ld,
+                                       a.vocab, r, weight, &token, &prob);
+  if (threadIdx.x == 0 && token >= 0) {
     a.token[n] = token;
     if (a.prob) a.prob[n] = prob;
   }
@@ -969,7 +1148,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
 namespace {
 
 struct SampleLayout {
-  size_t gmax, segs, total;
+  size_t gmax, segs, jobs, total;
   int n_seg;
 };
 SampleLayout sample_layout(int N, int vocab, int dtype) {
@@ -978,8 +1157,15 @@ SampleLayout sample_layout(int N, int vocab, int dtype) {
   L.n_seg = (vocab + seg - 1) / seg;
   L.gmax = WS_HEADER;
   L.segs = L.gmax + align_up((size_t)N * L.n_seg * SEG_GROUPS * sizeof(float), 256);
-  L.total = L.n_seg <= SP_WARPS ? 0 : L.segs + align_up((size_t)N * L.n_seg * sizeof(SegMass), 256);
+  L.jobs = L.segs + align_up((size_t)N * L.n_seg * sizeof(SegMass), 256);
+  L.total = L.n_seg <= SP_WARPS ? 0 : L.jobs + align_up((size_t)N * sizeof(Job), 256);
   return L;
+}
+
+// Rows that the host knows to have a small top-k, or temperature 0: their lists are too long only where thousands of
+// tokens are equal, and then the block that picks searches too.  A third kernel would cost the usual call 2 us.
+bool seldom_searched(const SampleArgs& a) {
+  return (!a.temperature && a.temperature0 == 0.f) || (!a.top_k && a.top_k0 >= 1 && a.top_k0 <= 1024 && a.top_k0 < a.vocab);
 }
 
 template <typename T, bool ALIGNED>
@@ -991,18 +1177,26 @@ cudaError_t run_sample(const Ctx& c, const SampleArgs& a, int dtype) {
     static unsigned long long short_done = 0;
     const cudaError_t e = allow_max_smem(k_sample_pick<T, ALIGNED, true>, c.device, &short_done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, true>, grid, block, smem, a, L.n_seg, nullptr, nullptr);
+    return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, true>, grid, block, smem, a, L.n_seg, nullptr,
+                      nullptr, nullptr);
   }
   static unsigned long long long_done = 0;
   cudaError_t e = allow_max_smem(k_sample_pick<T, ALIGNED, false>, c.device, &long_done);
   if (e != cudaSuccess) return e;
   float* gmax = reinterpret_cast<float*>(static_cast<char*>(a.ws) + L.gmax);
   SegMass* segs = reinterpret_cast<SegMass*>(static_cast<char*>(a.ws) + L.segs);
-  const long long want = ((long long)a.N * L.n_seg + SC_THREADS / 32 - 1) / (SC_THREADS / 32), most = 6LL * c.num_sms;
+  const long long want = ((long long)a.N * L.n_seg + SC_THREADS / 32 - 1) / (SC_THREADS / 32), most = (long long)SC_BLOCKS * c.num_sms;
   e = launch_pdl(c, "sample_scan", k_sample_scan<T, ALIGNED>, dim3((unsigned)(want < most ? want : most)),
                  dim3(SC_THREADS), 0, a, L.n_seg, gmax, segs);
   if (e != cudaSuccess) return e;
-  return launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, false>, grid, block, smem, a, L.n_seg, gmax, segs);
+  Job* jobs = seldom_searched(a) ? nullptr : reinterpret_cast<Job*>(static_cast<char*>(a.ws) + L.jobs);
+  e = launch_pdl(c, "sample_pick", k_sample_pick<T, ALIGNED, false>, grid, block, smem, a, L.n_seg, gmax, segs, jobs);
+  if (e != cudaSuccess || !jobs) return e;
+  static unsigned long long search_done = 0;
+  e = allow_max_smem(k_sample_search<T, ALIGNED>, c.device, &search_done);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(c, "sample_search", k_sample_search<T, ALIGNED>, SS_RANKS, dim3((unsigned)a.N * SS_RANKS), block,
+                         sizeof(SearchSmem), a, jobs);
 }
 
 }  // namespace
