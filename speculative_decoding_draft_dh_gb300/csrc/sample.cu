@@ -48,6 +48,29 @@ struct ExpTable {
   uint32_t q[64];
   float f[64];
 };
+// The block's shared memory as one of the structures below, of which each starts with a Scratch.  Every function
+// takes it from the symbol itself: through a reference that is passed on the compiler would not know that it is
+// shared memory, and atomics and loads on such addresses are several times as slow.
+template <class S>
+__device__ __forceinline__ S& smem() {
+  extern __shared__ __align__(16) unsigned char sample_smem[];
+  return *reinterpret_cast<S*>(sample_smem);
+}
+// What the steps of a block leave for one another.
+struct Scratch {
+  ExpTable tab;
+  u64 warp_mass[SP_WARPS];
+  uint32_t warp_count[SP_WARPS];
+  float warp_max[SP_WARPS], warp_min[SP_WARPS];
+  int bin, last;
+  u64 bin_mass, above_mass;
+  uint32_t bin_count, above_count;
+  uint32_t n_list, n_groups;
+  u64 found_mass, found_w;
+  uint32_t found_at, found_id;
+  uint32_t share[2];  // of a sum over a cluster
+};
+
 constexpr ExpTable make_table() {
   ExpTable t = {};
   for (int j = 0; j < 64; ++j) {
@@ -83,9 +106,7 @@ struct Weights {
   float m, t, zlow;
   int e_ref, frac;  // the largest weight is in [2^frac, 2^(frac + 1)]
   bool far;
-  const ExpTable* tab;  // in shared memory
-  __device__ __forceinline__ Weights(float m_, float t_, int frac_, const ExpTable* tab_)
-      : c(t_), m(m_), t(t_), frac(frac_), tab(tab_) {
+  __device__ __forceinline__ Weights(float m_, float t_, int frac_) : c(t_), m(m_), t(t_), frac(frac_) {
     const float reach = (float)(frac + 2) / c.hi;  // what is lower than m by that much weighs below 2^-(frac + 1)
     far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e38f && reach + fabsf(m) < 1.5e38f);
     zlow = far ? -3.4028234e38f : m - reach;
@@ -118,7 +139,8 @@ struct Weights {
       // 2^r - 1 by its series
       const float x = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
       // added to 1.5 2^23, which rounds to an integer in the low bits; |tab.f x| < 2^22
-      q = tab->q[j] + (uint32_t)(__float_as_int(fmaf(tab->f[j], x, 12582912.f)) - 0x4B400000);
+      const ExpTable& tab = smem<Scratch>().tab;
+      q = tab.q[j] + (uint32_t)(__float_as_int(fmaf(tab.f[j], x, 12582912.f)) - 0x4B400000);
       down = e_ref - (ki >> 6);
     }
     // 28 fraction bits to frac, and down; rounded
@@ -298,21 +320,9 @@ struct __align__(16) Bins {
   }
 };
 
-// What the steps of a block leave for one another.
-struct Scratch {
-  ExpTable tab;
-  u64 warp_mass[SP_WARPS];
-  uint32_t warp_count[SP_WARPS];
-  float warp_max[SP_WARPS], warp_min[SP_WARPS];
-  int bin, last;
-  u64 bin_mass, above_mass;
-  uint32_t bin_count, above_count;
-  uint32_t n_list, n_groups;
-  u64 found_mass, found_w;
-  uint32_t found_at, found_id;
-  uint32_t share[2];  // of a sum over a cluster
-};
 struct SampleSmem : Scratch {
+  static constexpr int RANKS = 1;  // blocks of a search
+  __device__ __forceinline__ Bins& local(int level) { return bins[level]; }
   union {
     Bins bins[2];       // of the whole range, of a part of it
     u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
@@ -320,8 +330,11 @@ struct SampleSmem : Scratch {
   };
   uint32_t groups[SP_GROUPS];
 };
+constexpr int SS_RANKS = 4;
 struct SearchSmem : Scratch {
-  Bins local;    // of this block's share of the row
+  static constexpr int RANKS = SS_RANKS;
+  __device__ __forceinline__ Bins& local(int) { return own; }
+  Bins own;      // of this block's share of the row
   Bins bins[2];  // of the whole row
 };
 
@@ -406,19 +419,22 @@ struct Coarse {
   }
 };
 
-// `out` = the sum of the cluster's `local`.
-template <int RANKS>
-__device__ __forceinline__ void merge_bins(Bins& local, Bins& out) {
-  if constexpr (RANKS == 1) {
-    __syncthreads();  // local is out
+// bins[level] = the sum of the cluster's local bins.
+template <class S>
+__device__ __forceinline__ void merge_bins(int level) {
+  if constexpr (S::RANKS == 1) {
+    __syncthreads();  // they are the same
   } else {
+    S& s = smem<S>();
+    const Bins& local = s.local(level);
+    Bins& out = s.bins[level];
     static_assert(SP_BINS == 4 * SP_THREADS, "a thread has four bins");
     cluster_sync();
     const int b = threadIdx.x;
     u64 m[4] = {0, 0, 0, 0};
     uint4 c = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (uint32_t r = 0; r < RANKS; ++r) {
+    for (uint32_t r = 0; r < S::RANKS; ++r) {
       const uint4 l = ld_cluster(reinterpret_cast<const uint4*>(local.lo) + b, r);
       const uint4 h = ld_cluster(reinterpret_cast<const uint4*>(local.hi) + b, r);
       const uint4 n = ld_cluster(reinterpret_cast<const uint4*>(local.count) + b, r);
@@ -438,34 +454,39 @@ __device__ __forceinline__ void merge_bins(Bins& local, Bins& out) {
     cluster_sync();  // `local` has been read
   }
 }
-__device__ __forceinline__ void clear_bins(Bins& bins) {
+template <class S>
+__device__ __forceinline__ void clear_bins(int level) {
+  Bins& bins = smem<S>().local(level);
   for (int b = threadIdx.x; b < SP_BINS / 4; b += SP_THREADS)
     reinterpret_cast<uint4*>(bins.lo)[b] = reinterpret_cast<uint4*>(bins.hi)[b] =
         reinterpret_cast<uint4*>(bins.count)[b] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 }
-// All tokens with a weight, by the coarse bins.
-template <typename T, bool ALIGNED, int RANKS>
-__device__ __noinline__ void fill_coarse(Bins& local, Bins& out, const T* row, Share part, const Coarse& coarse,
-                                         const Weights& weight, bool counted) {
-  clear_bins(local);
+// All tokens with a weight, by the coarse bins, into bins[0].
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ void fill_coarse(const T* row, Share part, Coarse coarse, Weights weight, bool counted) {
+  clear_bins<S>(0);
+  Bins& local = smem<S>().local(0);
   each<T, ALIGNED>(row, part, weight.zlow, weight.m,
                    [&](float z) { local.add(coarse.bin<T>(z, weight), weight(z), counted); });
-  merge_bins<RANKS>(local, out);
+  merge_bins<S>(0);
 }
-// Those of one coarse bin with keys [lo, hi], by ranges of keys.
-template <typename T, bool ALIGNED, int RANKS>
-__device__ __noinline__ void fill_fine(Bins& local, Bins& out, const T* row, Share part, const Coarse& coarse, int bin,
-                                       uint32_t lo, uint32_t hi, const Weights& weight) {
-  clear_bins(local);
+// Those of one coarse bin with keys [lo, hi], by ranges of keys, into bins[1].
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ void fill_fine(const T* row, Share part, Coarse coarse, int bin, uint32_t lo, uint32_t hi,
+                                       Weights weight) {
+  clear_bins<S>(1);
+  Bins& local = smem<S>().local(1);
   const int sh = bin_shift(lo, hi);
   each<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), [&](float z) {
     if (coarse.bin<T>(z, weight) == bin) local.add((hi - key_of<T>(z)) >> sh, weight(z), true);
   });
-  merge_bins<RANKS>(local, out);
+  merge_bins<S>(1);
 }
-template <bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Histogram find_bin(Scratch& s, const Bins& bins, uint32_t above, u64 above_mass, u64 want) {
+template <class S, bool BY_COUNT, bool STRICT>
+__device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_mass, u64 want) {
+  S& s = smem<S>();
+  const Bins& bins = s.bins[level];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s.bin = s.last = -1;
   // inclusive sums over the bins, four to a thread
@@ -539,21 +560,20 @@ __device__ __noinline__ Histogram find_bin(Scratch& s, const Bins& bins, uint32_
 }
 
 // The first place with `want` tokens or more (BY_COUNT), or with a mass of want or more (STRICT: more than want); the
-// last place where there is none.  `whole` is the row's coarse histogram; `local` and `out` are for finer ones.
-template <typename T, bool ALIGNED, int RANKS, bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Place descend(Scratch& s, const Bins& whole, Bins& local, Bins& out, const T* row, Share part,
-                                      const Coarse& coarse, u64 want, const Weights& weight) {
+// last place where there is none.  bins[0] is the row's coarse histogram.
+template <typename T, bool ALIGNED, class S, bool BY_COUNT, bool STRICT>
+__device__ __noinline__ Place descend(const T* row, Share part, Coarse coarse, u64 want, Weights weight) {
   Place p = {};
-  Histogram h = find_bin<BY_COUNT, STRICT>(s, whole, 0, 0, want);
+  Histogram h = find_bin<S, BY_COUNT, STRICT>(0, 0, 0, want);
   const int bin = h.bin;
   uint32_t lo, hi;
   coarse.keys<T>(bin, weight, &lo, &hi);
   for (;;) {
     p.above_mass = h.above_mass;
     p.above = h.above;
-    fill_fine<T, ALIGNED, RANKS>(local, out, row, part, coarse, bin, lo, hi, weight);
+    fill_fine<T, ALIGNED, S>(row, part, coarse, bin, lo, hi, weight);
     const int sh = bin_shift(lo, hi);
-    h = find_bin<BY_COUNT, STRICT>(s, out, p.above, p.above_mass, want);
+    h = find_bin<S, BY_COUNT, STRICT>(1, p.above, p.above_mass, want);
     hi -= (uint32_t)h.bin << sh;
     const uint32_t reach = (1u << sh) - 1u;
     if (hi - lo > reach) lo = hi - reach;
@@ -571,7 +591,8 @@ __device__ __noinline__ Place descend(Scratch& s, const Bins& whole, Bins& local
 // The id of the j-th token (from 1, by id) whose key is `key`, the last one where there are fewer; -1 in the blocks
 // of a cluster whose share does not hold it.
 template <typename T, bool ALIGNED, int RANKS>
-__device__ __noinline__ int find_token(Scratch& s, const T* row, Share part, uint32_t key, uint32_t j) {
+__device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, uint32_t j) {
+  Scratch& s = smem<Scratch>();
   constexpr int PER = Elem<T>::PER16, STEP = 32 * PER;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (part.to - part.from + SP_WARPS * STEP - 1) / (SP_WARPS * STEP) * STEP;
@@ -640,7 +661,8 @@ __device__ __forceinline__ float share(u64 w, u64 mass) {
 }
 
 // Sum over the block; every thread gets it.
-__device__ __forceinline__ u64 block_mass(Scratch& s, u64 x) {
+__device__ __forceinline__ u64 block_mass(u64 x) {
+  Scratch& s = smem<Scratch>();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
   if ((threadIdx.x & 31) == 0) s.warp_mass[threadIdx.x >> 5] = x;
@@ -651,7 +673,8 @@ __device__ __forceinline__ u64 block_mass(Scratch& s, u64 x) {
   return x;
 }
 // Sum over the threads before this one.
-__device__ __forceinline__ u64 mass_before(Scratch& s, u64 x) {
+__device__ __forceinline__ u64 mass_before(u64 x) {
+  Scratch& s = smem<Scratch>();
   u64 inc = x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -690,25 +713,26 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
 
 // Token and probability by searches over the whole row, by one block or a cluster; token -1 in the blocks that do
 // not hold it.
-template <typename T, bool ALIGNED, int RANKS>
-__device__ __noinline__ void pick_by_search(Scratch& s, Bins& whole, Bins& local, Bins& fine, const T* row, int vocab,
-                                            const RowState& r, const Weights& weight, int* token, float* prob) {
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ void pick_by_search(const T* row, int vocab, RowState r, Weights weight, int* token,
+                                            float* prob) {
+  constexpr int RANKS = S::RANKS;
+  S& s = smem<S>();
   const Share part = share_of_row<T, RANKS>(vocab);
   const Coarse coarse = {weight.far ? 0 : weight.step(weight.m), r.low, r.top, bin_shift(r.low, r.top), weight.far};
-  fill_coarse<T, ALIGNED, RANKS>(RANKS == 1 ? whole : local, whole, row, part, coarse, weight, r.top_k != 0);
-  Bins& part_bins = RANKS == 1 ? fine : local;
+  fill_coarse<T, ALIGNED, S>(row, part, coarse, weight, r.top_k != 0);
   // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
   uint32_t key = r.low, equal = 0xFFFFFFFFu;
   u64 mass = r.mass;
   if (r.top_k) {
-    const Place p = descend<T, ALIGNED, RANKS, true, false>(s, whole, part_bins, fine, row, part, coarse, (u64)r.top_k, weight);
+    const Place p = descend<T, ALIGNED, S, true, false>(row, part, coarse, (u64)r.top_k, weight);
     key = p.key;
     equal = min((uint32_t)r.top_k - min(p.above, (uint32_t)r.top_k), p.n_equal);
     mass = p.above_mass + equal * p.w;
   }
   if (r.top_p < 1.f) {
     const u64 want = share_of(r.top_p, mass);
-    const Place p = descend<T, ALIGNED, RANKS, false, false>(s, whole, part_bins, fine, row, part, coarse, want, weight);
+    const Place p = descend<T, ALIGNED, S, false, false>(row, part, coarse, want, weight);
     uint32_t j = p.n_equal;
     if (p.w && p.above_mass < want) j = (uint32_t)min((u64)j, (want - p.above_mass + p.w - 1) / p.w);
     if (p.key == key) j = min(j, equal);
@@ -722,7 +746,7 @@ __device__ __noinline__ void pick_by_search(Scratch& s, Bins& whole, Bins& local
     equal = 0xFFFFFFFFu;
     u64 sum = 0;
     each<T, ALIGNED>(row, part, value_of<T>(key), weight.m, [&](float z) { sum += weight(z); });
-    mass = block_mass(s, sum);
+    mass = block_mass(sum);
     if constexpr (RANKS > 1) {
       if (threadIdx.x == 0) {
         s.share[0] = (uint32_t)mass;
@@ -735,20 +759,21 @@ __device__ __noinline__ void pick_by_search(Scratch& s, Bins& whole, Bins& local
     }
   }
   const u64 want = draw_at(r.u, mass);
-  const Place p = descend<T, ALIGNED, RANKS, false, true>(s, whole, part_bins, fine, row, part, coarse, want, weight);
+  const Place p = descend<T, ALIGNED, S, false, true>(row, part, coarse, want, weight);
   uint32_t j = p.n_equal;
   if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
   if (p.key == key) j = min(j, equal);
   // (p.key < key, below the kept prefix, is not reached: the searches go by the same sums)
-  *token = find_token<T, ALIGNED, RANKS>(s, row, part, p.key, j);
+  *token = find_token<T, ALIGNED, RANKS>(row, part, p.key, j);
   *prob = share(p.w, mass);
 }
 
 // The lower edge of the histogram bin that holds the k-th largest of the groups' maxima, of which the smallest above
 // -inf has the key lo: at least k tokens reach it.  0 where fewer than k groups are above -inf.
 template <typename T>
-__device__ __noinline__ uint32_t bound_by_count(SampleSmem& s, const float* gmax, int n_groups, uint32_t lo,
+__device__ __noinline__ uint32_t bound_by_count(const float* gmax, int n_groups, uint32_t lo,
                                                 uint32_t top, uint32_t k) {
+  SampleSmem& s = smem<SampleSmem>();
   constexpr int OWN = SP_BINS / SP_THREADS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sh = bin_shift(lo, top);
   for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.group_count[b] = 0;
@@ -788,8 +813,9 @@ __device__ __noinline__ uint32_t bound_by_count(SampleSmem& s, const float* gmax
 
 // Lists the tokens whose keys reach `lo`, from the groups whose maxima do; false where they are too many.
 template <typename T, bool ALIGNED>
-__device__ __noinline__ bool list_tokens(SampleSmem& s, const T* row, int vocab, const float* gmax, int n_groups,
+__device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* gmax, int n_groups,
                                          uint32_t lo) {
+  SampleSmem& s = smem<SampleSmem>();
   constexpr int PER = Elem<T>::PER16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s.n_list = s.n_groups = 0;
@@ -840,14 +866,16 @@ __device__ __noinline__ bool list_tokens(SampleSmem& s, const T* row, int vocab,
 
 // The mass of the list.
 template <typename T>
-__device__ __noinline__ u64 list_mass(SampleSmem& s, const Weights& weight) {
+__device__ __noinline__ u64 list_mass(Weights weight) {
+  SampleSmem& s = smem<SampleSmem>();
   u64 sum = 0;
   for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS) sum += weight(value_of<T>((uint32_t)(s.list[i] >> 32)));
-  return block_mass(s, sum);
+  return block_mass(sum);
 }
 
 // The list in descending order (its numbers are distinct).
-__device__ __noinline__ void sort_list(SampleSmem& s) {
+__device__ __noinline__ void sort_list() {
+  SampleSmem& s = smem<SampleSmem>();
   const int n = (int)s.n_list;
   if (n <= SP_THREADS) {
     // by ranks
@@ -883,8 +911,8 @@ __device__ __noinline__ void sort_list(SampleSmem& s) {
 
 // Token and probability from the sorted list, which holds all tokens down to the last that can be drawn.
 template <typename T>
-__device__ __noinline__ void pick_from_list(SampleSmem& s, const RowState& r, const Weights& weight, int* token,
-                                            float* prob) {
+__device__ __noinline__ void pick_from_list(RowState r, Weights weight, int* token, float* prob) {
+  SampleSmem& s = smem<SampleSmem>();
   constexpr int OWN = SP_LIST / SP_THREADS;
   const int n = (int)s.n_list, own = (n + SP_THREADS - 1) / SP_THREADS, i0 = threadIdx.x * own;
   u64 w[OWN], sum = 0;
@@ -899,7 +927,7 @@ __device__ __noinline__ void pick_from_list(SampleSmem& s, const RowState& r, co
       sum += w[q];
     }
   }
-  const u64 before = mass_before(s, sum);
+  const u64 before = mass_before(sum);
   // f(running sum before, with, index) of this thread's tokens
   auto walk = [&](auto f) {
     u64 at = before;
@@ -972,8 +1000,7 @@ struct Job {
 template <typename T, bool ALIGNED, bool SHORT>
 __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int n_seg, const float* gmax_all,
                                                                const SegMass* segs_all, Job* jobs) {
-  extern __shared__ __align__(16) unsigned char sample_smem[];
-  SampleSmem& s = *reinterpret_cast<SampleSmem*>(sample_smem);
+  SampleSmem& s = smem<SampleSmem>();
   __shared__ float s_gmax[SHORT ? SP_WARPS * SEG_GROUPS : 1];
   __shared__ SegMass s_seg[SHORT ? SP_WARPS : 1];
   const int n = blockIdx.x, vocab = a.vocab, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1028,7 +1055,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
     RowState r;
     r.top = key_of<T>(m);
     if (t == 0.f || top_k == 1 || top_p <= 0.f) {
-      if (list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, r.top)) {
+      if (list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, r.top)) {
         // the lowest of the ids that share the largest logit
         uint32_t id = 0xFFFFFFFFu;
         for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS) id = min(id, ~(uint32_t)s.list[i]);
@@ -1039,11 +1066,11 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
         token = (int)id;
       } else {
         __syncthreads();
-        token = find_token<T, ALIGNED, 1>(s, row, Share{0, vocab}, r.top, 1);
+        token = find_token<T, ALIGNED, 1>(row, Share{0, vocab}, r.top, 1);
       }
       prob = 1.f;
     } else {
-      const Weights weight(m, t, min(62 - (32 - __clz(vocab - 1)), SEG_FRAC), &s.tab);
+      const Weights weight(m, t, min(62 - (32 - __clz(vocab - 1)), SEG_FRAC));
       r.low = key_of<T>(weight.zlow);
       r.top_k = top_k > 1 && top_k < vocab ? top_k : 0;
       r.top_p = top_p;
@@ -1074,7 +1101,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
             else if (down < 64) sum += (q.mass + (1ull << (down - 1))) >> down;
           }
         }
-        r.mass = block_mass(s, sum);
+        r.mass = block_mass(sum);
       }
       // a list of the tokens from a key on below which nothing can be kept and drawn
       bool listed = false;
@@ -1083,22 +1110,22 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
         const u64 want = r.top_p < 1.f ? share_of(r.top_p, r.mass) : draw_at(r.u, r.mass) + 1;
         for (int k = SP_TRY_FIRST; !listed && k <= SP_GROUPS; k *= SP_TRY_STEP) {
           const uint32_t lo =
-              k < n_groups ? bound_by_count<T>(s, gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)k) : 0;
-          if (!list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, max(lo, r.low))) break;
-          listed = lo <= r.low || list_mass<T>(s, weight) >= want;
+              k < n_groups ? bound_by_count<T>(gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)k) : 0;
+          if (!list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, max(lo, r.low))) break;
+          listed = lo <= r.low || list_mass<T>(weight) >= want;
         }
       } else {
         uint32_t lo = r.top_k ? 0 : r.least;
         if (r.top_k && r.top_k <= n_groups)
-          lo = bound_by_count<T>(s, gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
-        listed = list_tokens<T, ALIGNED>(s, row, vocab, gmax, n_groups, max(lo, r.low));
+          lo = bound_by_count<T>(gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
+        listed = list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, max(lo, r.low));
       }
       if (listed) {
-        sort_list(s);
-        pick_from_list<T>(s, r, weight, &token, &prob);
+        sort_list();
+        pick_from_list<T>(r, weight, &token, &prob);
       } else if (SHORT || !jobs) {
         __syncthreads();
-        pick_by_search<T, ALIGNED, 1>(s, s.bins[0], s.bins[1], s.bins[1], row, vocab, r, weight, &token, &prob);
+        pick_by_search<T, ALIGNED, SampleSmem>(row, vocab, r, weight, &token, &prob);
       } else {
         // left to k_sample_search
         if (threadIdx.x == 0) jobs[n].row = r;
@@ -1118,12 +1145,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
 }
 
 // The rows whose lists would have been too long, each by a cluster.
-constexpr int SS_RANKS = 4;
-
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_search(SampleArgs a, const Job* jobs) {
-  extern __shared__ __align__(16) unsigned char sample_smem[];
-  SearchSmem& s = *reinterpret_cast<SearchSmem*>(sample_smem);
+  SearchSmem& s = smem<SearchSmem>();
   const int n = blockIdx.x / SS_RANKS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!__ldcg(&jobs[n].searched)) return;  // the whole cluster
@@ -1132,11 +1156,10 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_search(SampleArgs a, c
   __syncthreads();
   const RowState r = jobs[n].row;
   const float t = a.temperature ? __ldg(a.temperature + n) : a.temperature0;
-  const Weights weight(jobs[n].m, t, min(62 - (32 - __clz(a.vocab - 1)), SEG_FRAC), &s.tab);
+  const Weights weight(jobs[n].m, t, min(62 - (32 - __clz(a.vocab - 1)), SEG_FRAC));
   int token;
   float prob;
-  pick_by_search<T, ALIGNED, SS_RANKS>(s, s.bins[0], s.local, s.bins[1], static_cast<const T*>(a.logits) + n * a.ld,
-                                       a.vocab, r, weight, &token, &prob);
+  pick_by_search<T, ALIGNED, SearchSmem>(static_cast<const T*>(a.logits) + n * a.ld, a.vocab, r, weight, &token, &prob);
   if (threadIdx.x == 0 && token >= 0) {
     a.token[n] = token;
     if (a.prob) a.prob[n] = prob;
