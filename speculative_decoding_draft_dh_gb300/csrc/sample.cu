@@ -31,11 +31,7 @@ constexpr int SP_BINS = 2048;
 constexpr int SP_LIST = 4096;    // tokens listed, at most
 constexpr int SP_GROUPS = 2048;  // groups listed, at most
 // Groups with which a row whose mass is needed is tried, and how many times more each time.
-#ifndef SP_F
-#define SP_F 64
-#define SP_S 4
-#endif
-constexpr int SP_TRY_FIRST = SP_F, SP_TRY_STEP = SP_S;
+constexpr int SP_TRY_FIRST = 64, SP_TRY_STEP = 16;
 constexpr int SEG_GROUPS = 8;    // groups of a segment: four lanes' vectors each
 constexpr int SEG_FRAC = 52;     // fraction bits of a segment's mass, relative to 2^e of its own largest weight
 
@@ -108,7 +104,7 @@ struct Weights {
   bool far;
   __device__ __forceinline__ Weights(float m_, float t_, int frac_) : c(t_), m(m_), t(t_), frac(frac_) {
     const float reach = (float)(frac + 2) / c.hi;  // what is lower than m by that much weighs below 2^-(frac + 1)
-    far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e38f && reach + fabsf(m) < 1.5e38f);
+    far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e38f && 128.f / c.hi + fabsf(m) < 1e38f);
     zlow = far ? -3.4028234e38f : m - reach;
     e_ref = far ? 0 : (__float_as_int(fmaf(m, c.hi, EXP_MAGIC)) - EXP_MAGIC_BITS) >> 6;
   }
@@ -233,7 +229,7 @@ __device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, f
   int e_ref = -0x40000000;
   // beyond, and so beyond the limits of Weights: the row's weights are taken in 64 bits by the block that picks, or
   // its largest logit is so far above this segment's that their weights are 0
-  if (fabsf(m * ch) < 32700.f && ch < 1e38f && reach + fabsf(m) < 3.3e38f) {
+  if (fabsf(m * ch) < 32700.f && ch < 1e38f && 128.f / ch + fabsf(m) < 3.3e38f) {
     e_ref = (__float_as_int(fmaf(m, ch, EXP_MAGIC)) - EXP_MAGIC_BITS) >> 6;
     const float low = m - reach;
     const uint2* tb = tab.e + (lane & 15);
@@ -380,6 +376,68 @@ __device__ __forceinline__ void each(const T* row, Share part, float from, float
   }
 }
 
+// Which elements of a vector are in [from, to], by two comparisons per word.
+template <typename T>
+struct Within {
+  float from, to;
+  __device__ __forceinline__ Within(float f, float t) : from(f), to(t) {}
+  __device__ __forceinline__ uint32_t operator()(const uint4& u) const {
+    float x[4];
+    Elem<T>::unpack(u, x);
+    uint32_t hits = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) hits |= (x[e] >= from && x[e] <= to ? 1u : 0u) << e;
+    return hits;
+  }
+};
+template <>
+struct Within<__nv_bfloat16> {
+  __nv_bfloat162 from, to;  // bf16 values
+  __device__ __forceinline__ Within(float f, float t) : from(__float2bfloat162_rn(f)), to(__float2bfloat162_rn(t)) {}
+  __device__ __forceinline__ uint32_t operator()(const uint4& u) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[q]);
+      m[q] = __hge2_mask(x, from) & __hle2_mask(x, to);
+    }
+    if (!((m[0] | m[1]) | (m[2] | m[3]))) return 0;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) hits |= ((m[q] & 1u) | ((m[q] >> 15) & 2u)) << (2 * q);
+    return hits;
+  }
+};
+// Element e of a vector.
+template <typename T>
+__device__ __forceinline__ float element(const uint4& u, int e) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(e < 2 ? (e == 0 ? u.x : u.y) : (e == 2 ? u.z : u.w));
+  } else {
+    const uint32_t w = e < 4 ? (e < 2 ? u.x : u.y) : (e < 6 ? u.z : u.w);
+    return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
+  }
+}
+// As `each`, where few are: from and to are values of T.
+template <typename T, bool ALIGNED, typename F>
+__device__ __forceinline__ void each_of_few(const T* row, Share part, float from, float to, F f) {
+  constexpr int PER = Elem<T>::PER16, AHEAD = 4;
+  const Within<T> within(from, to);
+  for (int id0 = part.from + threadIdx.x * PER; id0 < part.to; id0 += AHEAD * SP_THREADS * PER) {
+    uint4 u[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const int id = id0 + q * SP_THREADS * PER;
+      u[q] = make_uint4(NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD);
+      if (id < part.to) u[q] = row_vec<T, ALIGNED>(row, id, part.to);
+    }
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q)
+      for (uint32_t hits = within(u[q]); hits; hits &= hits - 1) f(element<T>(u[q], __ffs(hits) - 1));
+  }
+}
+
 // The bin, from the top down, in which `want` is reached: tokens (BY_COUNT) or a mass of want or more (STRICT: more
 // than want), counted on from `above` tokens of `above_mass`; the last bin that is not empty where it is not.
 struct Histogram {
@@ -478,7 +536,7 @@ __device__ __noinline__ void fill_fine(const T* row, Share part, Coarse coarse, 
   clear_bins<S>(1);
   Bins& local = smem<S>().local(1);
   const int sh = bin_shift(lo, hi);
-  each<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), [&](float z) {
+  each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), [&](float z) {
     if (coarse.bin<T>(z, weight) == bin) local.add((hi - key_of<T>(z)) >> sh, weight(z), true);
   });
   merge_bins<S>(1);
@@ -597,17 +655,8 @@ __device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, u
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (part.to - part.from + SP_WARPS * STEP - 1) / (SP_WARPS * STEP) * STEP;
   const int from = min(part.from + warp * each, part.to), to = min(from + each, part.to);
-  auto matches = [&](int id) -> uint32_t {
-    uint32_t bits = 0;
-    if (id < to) {
-      float x[PER];
-      Elem<T>::unpack(row_vec<T, ALIGNED>(row, id, to), x);
-#pragma unroll
-      for (int e = 0; e < PER; ++e)
-        if (id + e < to && key_of<T>(x[e]) == key) bits |= 1u << e;
-    }
-    return bits;
-  };
+  const Within<T> within(value_of<T>(key), value_of<T>(key));  // (a finite number, so not what lies past the row's end)
+  auto matches = [&](int id) -> uint32_t { return id < to ? within(row_vec<T, ALIGNED>(row, id, to)) : 0u; };
   uint32_t n = 0;
 #pragma unroll 4
   for (int i = from; i < to; i += STEP) n += __popc(matches(i + lane * PER));
@@ -696,7 +745,7 @@ struct RowState {
   uint32_t least;  // of the smallest logit that min-p keeps (0: it leaves out none)
   int top_k;       // 0: none
   float top_p, u;
-  u64 mass;        // of the row, where no top-k bounds it
+  u64 mass;        // of the row, where no top-k bounds it (0: not known)
 };
 
 // The place of a draw in a mass: the token whose running sum is the first above it.
@@ -705,10 +754,11 @@ __device__ __forceinline__ u64 draw_at(float u, u64 mass) {
   bool rest;
   return u < 1.f ? times(u, mass, &rest) : mass - 1;
 }
+// The mass that top-p asks for.
 __device__ __forceinline__ u64 share_of(float p, u64 mass) {
   bool rest;
-  const u64 want = times(p, mass, &rest);
-  return want + rest;
+  const u64 want = times(p, mass, &rest) + rest;
+  return want < 1 ? 1 : want;
 }
 
 // Token and probability by searches over the whole row, by one block or a cluster; token -1 in the blocks that do
@@ -820,8 +870,9 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s.n_list = s.n_groups = 0;
   __syncthreads();
+  const float from = value_of<T>(lo);
   for (int g = threadIdx.x; g < n_groups; g += SP_THREADS) {
-    if (key_of<T>(gmax[g]) >= lo) {
+    if (gmax[g] >= from) {
       const uint32_t at = atomicAdd(&s.n_groups, 1u);
       if (at < SP_GROUPS) s.groups[at] = g;
     }
@@ -830,17 +881,16 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
   const uint32_t n = s.n_groups;
   if (n > SP_GROUPS) return false;
   // two groups to a warp, 16 vectors each
+  const Within<T> within(from, INFINITY);  // (a row with +inf does not come here)
   for (uint32_t i = warp * 2; i < n; i += SP_WARPS * 2) {
     uint32_t hits = 0, id = 0;
-    float x[PER];
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (i + (lane >> 4) < n) {
       const uint32_t g = s.groups[i + (lane >> 4)];
       id = (g / SEG_GROUPS) * row_seg<T>() + (((lane >> 2) & 3) * 32 + (g % SEG_GROUPS) * 4 + (lane & 3)) * PER;
       if ((int)id < vocab) {
-        Elem<T>::unpack(row_vec<T, ALIGNED>(row, (int)id, vocab), x);
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-          if (key_of<T>(x[e]) >= lo && (int)id + e < vocab) hits |= 1u << e;
+        u = row_vec<T, ALIGNED>(row, (int)id, vocab);
+        hits = within(u);
       }
     }
     uint32_t inc = __popc(hits);
@@ -852,12 +902,9 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
     uint32_t at = 0;
     if (lane == 31 && inc) at = atomicAdd(&s.n_list, inc);
     at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - __popc(hits);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      if ((hits >> e) & 1u) {
-        if (at < SP_LIST) s.list[at] = ((u64)key_of<T>(x[e]) << 32) | (uint32_t)~(id + e);
-        ++at;
-      }
+    for (; hits; hits &= hits - 1, ++at) {
+      const int e = __ffs(hits) - 1;
+      if (at < SP_LIST) s.list[at] = ((u64)key_of<T>(element<T>(u, e)) << 32) | (uint32_t)~(id + e);
     }
   }
   __syncthreads();
@@ -1112,7 +1159,9 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
           const uint32_t lo =
               k < n_groups ? bound_by_count<T>(gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)k) : 0;
           if (!list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, max(lo, r.low))) break;
-          listed = lo <= r.low || list_mass<T>(weight) >= want;
+          const u64 mass = lo <= r.low ? want : list_mass<T>(weight);
+          listed = mass >= want;
+          if (mass < want / 3) break;  // a longer list would hardly do
         }
       } else {
         uint32_t lo = r.top_k ? 0 : r.least;
