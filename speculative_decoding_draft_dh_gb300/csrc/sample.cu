@@ -139,10 +139,8 @@ struct Weights {
       q = tab.q[j] + (uint32_t)(__float_as_int(fmaf(tab.f[j], x, 12582912.f)) - 0x4B400000);
       down = e_ref - (ki >> 6);
     }
-    // 28 fraction bits to frac, and down; rounded
-    const int left = frac - 28 - down;
-    if (left >= 0) return (u64)q << left;
-    return left < -31 ? 0 : (q + (1u << (-left - 1))) >> -left;
+    // 28 fraction bits to frac, and down, rounded; z is at least zlow, so that the shift is at most 62
+    return ((((u64)q << 32) >> min(59 - frac + down, 63)) + 1) >> 1;
   }
 };
 
@@ -320,11 +318,12 @@ struct SampleSmem : Scratch {
   static constexpr int RANKS = 1;  // blocks of a search
   __device__ __forceinline__ Bins& local(int level) { return bins[level]; }
   union {
-    Bins bins[2];       // of the whole range, of a part of it
-    u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
-    uint32_t group_count[SP_BINS];
+    Bins bins[2];  // of the whole range, of a part of it
+    struct {
+      uint32_t group_count[SP_BINS], groups[SP_GROUPS];
+    };
   };
-  uint32_t groups[SP_GROUPS];
+  u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
 };
 constexpr int SS_RANKS = 4;
 struct SearchSmem : Scratch {
@@ -341,16 +340,27 @@ struct Place {
   u64 above_mass, w;
 };
 
-// A block's share of a row: the ids [from, to), whole steps of a warp but for the row's end.
+// A block's share of a row: the ids [from, to), whole steps of a warp but for the row's end; or the listed tokens.
 struct Share {
   int from, to;
+  bool listed;
 };
 template <typename T, int RANKS>
 __device__ __forceinline__ Share share_of_row(int vocab) {
-  if (RANKS == 1) return {0, vocab};
+  if (RANKS == 1) return {0, vocab, false};
   constexpr int STEP = 32 * Elem<T>::PER16;
   const int each = (vocab + RANKS * STEP - 1) / (RANKS * STEP) * STEP, from = min((int)cluster_rank() * each, vocab);
-  return {from, min(from + each, vocab)};
+  return {from, min(from + each, vocab), false};
+}
+
+// f(value) of every logit of the list that is in [from, to].
+template <typename T, typename F>
+__device__ __forceinline__ void each_listed(float from, float to, F f) {
+  const SampleSmem& s = smem<SampleSmem>();
+  for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS) {
+    const float z = value_of<T>((uint32_t)(s.list[i] >> 32));
+    if (z >= from && z <= to) f(z);
+  }
 }
 
 // f(value) of every logit of the share that is in [from, to] (finite numbers).
@@ -525,8 +535,9 @@ template <typename T, bool ALIGNED, class S>
 __device__ __noinline__ void fill_coarse(const T* row, Share part, Coarse coarse, Weights weight, bool counted) {
   clear_bins<S>(0);
   Bins& local = smem<S>().local(0);
-  each<T, ALIGNED>(row, part, weight.zlow, weight.m,
-                   [&](float z) { local.add(coarse.bin<T>(z, weight), weight(z), counted); });
+  auto add = [&](float z) { local.add(coarse.bin<T>(z, weight), weight(z), counted); };
+  if (S::RANKS == 1 && part.listed) each_listed<T>(weight.zlow, weight.m, add);
+  else each<T, ALIGNED>(row, part, weight.zlow, weight.m, add);
   merge_bins<S>(0);
 }
 // Those of one coarse bin with keys [lo, hi], by ranges of keys, into bins[1].
@@ -536,9 +547,11 @@ __device__ __noinline__ void fill_fine(const T* row, Share part, Coarse coarse, 
   clear_bins<S>(1);
   Bins& local = smem<S>().local(1);
   const int sh = bin_shift(lo, hi);
-  each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), [&](float z) {
+  auto add = [&](float z) {
     if (coarse.bin<T>(z, weight) == bin) local.add((hi - key_of<T>(z)) >> sh, weight(z), true);
-  });
+  };
+  if (S::RANKS == 1 && part.listed) each_listed<T>(value_of<T>(lo), value_of<T>(hi), add);
+  else each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), add);
   merge_bins<S>(1);
 }
 template <class S, bool BY_COUNT, bool STRICT>
@@ -704,6 +717,33 @@ __device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, u
   return s.bin;
 }
 
+// The same of the list: the j-th of the listed tokens whose key is `key`.
+__device__ __noinline__ int find_listed(uint32_t key, uint32_t j) {
+  SampleSmem& s = smem<SampleSmem>();
+  const int n = (int)s.n_list;
+  if (threadIdx.x == 0) {
+    s.bin = -1;
+    s.n_groups = 0;  // of that key
+  }
+  __syncthreads();
+  uint32_t own = 0;
+  for (int i = threadIdx.x; i < n; i += SP_THREADS) own += (uint32_t)(s.list[i] >> 32) == key;
+  if (own) atomicAdd(&s.n_groups, own);
+  __syncthreads();
+  j = min(j, s.n_groups);
+  for (int i = threadIdx.x; i < n; i += SP_THREADS) {
+    const u64 x = s.list[i];
+    if ((uint32_t)(x >> 32) != key) continue;
+    // of one key the larger number has the lower id
+    uint32_t rank = 1;
+    if (s.n_groups > 1)
+      for (int k = 0; k < n; ++k) rank += (uint32_t)(s.list[k] >> 32) == key && s.list[k] > x;
+    if (rank == j) s.bin = (int)~(uint32_t)x;
+  }
+  __syncthreads();
+  return s.bin;
+}
+
 // w / mass; in 64 bits by one warp, whose result counts (the units are few).
 __device__ __forceinline__ float share(u64 w, u64 mass) {
   return threadIdx.x < 32 ? (float)((double)w / (double)mass) : 0.f;
@@ -761,14 +801,13 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
   return want < 1 ? 1 : want;
 }
 
-// Token and probability by searches over the whole row, by one block or a cluster; token -1 in the blocks that do
-// not hold it.
+// Token and probability by searches over the whole row, by one block or a cluster (token -1 in the blocks that do
+// not hold it), or over a list that holds all tokens down to the last that can be drawn.
 template <typename T, bool ALIGNED, class S>
-__device__ __noinline__ void pick_by_search(const T* row, int vocab, RowState r, Weights weight, int* token,
+__device__ __noinline__ void pick_by_search(const T* row, Share part, RowState r, Weights weight, int* token,
                                             float* prob) {
   constexpr int RANKS = S::RANKS;
   S& s = smem<S>();
-  const Share part = share_of_row<T, RANKS>(vocab);
   const Coarse coarse = {weight.far ? 0 : weight.step(weight.m), r.low, r.top, bin_shift(r.low, r.top), weight.far};
   fill_coarse<T, ALIGNED, S>(row, part, coarse, weight, r.top_k != 0);
   // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
@@ -795,7 +834,9 @@ __device__ __noinline__ void pick_by_search(const T* row, int vocab, RowState r,
     key = max(key, r.least);
     equal = 0xFFFFFFFFu;
     u64 sum = 0;
-    each<T, ALIGNED>(row, part, value_of<T>(key), weight.m, [&](float z) { sum += weight(z); });
+    auto add = [&](float z) { sum += weight(z); };
+    if (RANKS == 1 && part.listed) each_listed<T>(value_of<T>(key), weight.m, add);
+    else each<T, ALIGNED>(row, part, value_of<T>(key), weight.m, add);
     mass = block_mass(sum);
     if constexpr (RANKS > 1) {
       if (threadIdx.x == 0) {
@@ -814,7 +855,7 @@ __device__ __noinline__ void pick_by_search(const T* row, int vocab, RowState r,
   if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
   if (p.key == key) j = min(j, equal);
   // (p.key < key, below the kept prefix, is not reached: the searches go by the same sums)
-  *token = find_token<T, ALIGNED, RANKS>(row, part, p.key, j);
+  *token = RANKS == 1 && part.listed ? find_listed(p.key, j) : find_token<T, ALIGNED, RANKS>(row, part, p.key, j);
   *prob = share(p.w, mass);
 }
 
@@ -880,20 +921,28 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
   __syncthreads();
   const uint32_t n = s.n_groups;
   if (n > SP_GROUPS) return false;
-  // two groups to a warp, 16 vectors each
+  // two groups to a warp, 16 vectors each, the loads of AHEAD pairs of groups in flight
+  constexpr int AHEAD = 4;
   const Within<T> within(from, INFINITY);  // (a row with +inf does not come here)
-  for (uint32_t i = warp * 2; i < n; i += SP_WARPS * 2) {
-    uint32_t hits = 0, id = 0;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (i + (lane >> 4) < n) {
-      const uint32_t g = s.groups[i + (lane >> 4)];
-      id = (g / SEG_GROUPS) * row_seg<T>() + (((lane >> 2) & 3) * 32 + (g % SEG_GROUPS) * 4 + (lane & 3)) * PER;
-      if ((int)id < vocab) {
-        u = row_vec<T, ALIGNED>(row, (int)id, vocab);
-        hits = within(u);
+  for (uint32_t i0 = warp * 2; i0 < n; i0 += SP_WARPS * 2 * AHEAD) {
+    uint4 u[AHEAD];
+    uint32_t id[AHEAD], hits[AHEAD], inc = 0;
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const uint32_t i = i0 + q * SP_WARPS * 2 + (lane >> 4);
+      id[q] = (uint32_t)vocab;
+      if (i < n) {
+        const uint32_t g = s.groups[i];
+        id[q] = (g / SEG_GROUPS) * row_seg<T>() + (((lane >> 2) & 3) * 32 + (g % SEG_GROUPS) * 4 + (lane & 3)) * PER;
       }
+      if ((int)id[q] < vocab) u[q] = row_vec<T, ALIGNED>(row, (int)id[q], vocab);
     }
-    uint32_t inc = __popc(hits);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      hits[q] = (int)id[q] < vocab ? within(u[q]) : 0u;
+      inc += __popc(hits[q]);
+    }
+    const uint32_t own = inc;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -901,10 +950,13 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
     }
     uint32_t at = 0;
     if (lane == 31 && inc) at = atomicAdd(&s.n_list, inc);
-    at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - __popc(hits);
-    for (; hits; hits &= hits - 1, ++at) {
-      const int e = __ffs(hits) - 1;
-      if (at < SP_LIST) s.list[at] = ((u64)key_of<T>(element<T>(u, e)) << 32) | (uint32_t)~(id + e);
+    at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - own;
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      for (uint32_t h = hits[q]; h; h &= h - 1, ++at) {
+        const int e = __ffs(h) - 1;
+        if (at < SP_LIST) s.list[at] = ((u64)key_of<T>(element<T>(u[q], e)) << 32) | (uint32_t)~(id[q] + e);
+      }
     }
   }
   __syncthreads();
@@ -920,118 +972,64 @@ __device__ __noinline__ u64 list_mass(Weights weight) {
   return block_mass(sum);
 }
 
-// The list in descending order (its numbers are distinct).
+// A list of at most a token per thread, in descending order (its numbers are distinct), by ranks.
 __device__ __noinline__ void sort_list() {
   SampleSmem& s = smem<SampleSmem>();
   const int n = (int)s.n_list;
-  if (n <= SP_THREADS) {
-    // by ranks
-    u64 x = 0;
-    int rank = 0;
-    if ((int)threadIdx.x < n) {
-      x = s.list[threadIdx.x];
-      for (int i = 0; i < n; ++i) rank += s.list[i] > x;
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < n) s.list[rank] = x;
-    __syncthreads();
-    return;
+  u64 x = 0;
+  int rank = 0;
+  if ((int)threadIdx.x < n) {
+    x = s.list[threadIdx.x];
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) rank += s.list[i] > x;
   }
-  int size = 2 * SP_THREADS;
-  while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += SP_THREADS) s.list[i] = 0;
   __syncthreads();
-  for (int k = 2; k <= size; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int t = threadIdx.x; t < size / 2; t += SP_THREADS) {
-        const int i = 2 * t - (t & (j - 1)), o = i + j;
-        const u64 x = s.list[i], y = s.list[o];
-        if ((x < y) == ((i & k) == 0)) {
-          s.list[i] = y;
-          s.list[o] = x;
-        }
-      }
-      __syncthreads();
-    }
-  }
+  if ((int)threadIdx.x < n) s.list[rank] = x;
+  __syncthreads();
 }
 
-// Token and probability from the sorted list, which holds all tokens down to the last that can be drawn.
+// Token and probability from the sorted list, which holds all tokens down to the last that can be drawn, one to a
+// thread.
 template <typename T>
 __device__ __noinline__ void pick_from_list(RowState r, Weights weight, int* token, float* prob) {
   SampleSmem& s = smem<SampleSmem>();
-  constexpr int OWN = SP_LIST / SP_THREADS;
-  const int n = (int)s.n_list, own = (n + SP_THREADS - 1) / SP_THREADS, i0 = threadIdx.x * own;
-  u64 w[OWN], sum = 0;
-  int n_min = 0;
-#pragma unroll
-  for (int q = 0; q < OWN; ++q) {
-    w[q] = 0;
-    if (q < own && i0 + q < n) {
-      const uint32_t k = (uint32_t)(s.list[i0 + q] >> 32);
-      w[q] = weight(value_of<T>(k));
-      n_min += k >= r.least;
-      sum += w[q];
-    }
-  }
-  const u64 before = mass_before(sum);
-  // f(running sum before, with, index) of this thread's tokens
-  auto walk = [&](auto f) {
-    u64 at = before;
-#pragma unroll
-    for (int q = 0; q < OWN; ++q) {
-      if (q < own && i0 + q < n) {
-        f(at, at + w[q], i0 + q, w[q]);
-        at += w[q];
-      }
-    }
-  };
-  if (threadIdx.x == 0) {
+  const int n = (int)s.n_list, i = threadIdx.x;
+  const bool on = i < n;
+  const u64 x = on ? s.list[i] : 0;
+  const uint32_t key = (uint32_t)(x >> 32);
+  const u64 w = on ? weight(value_of<T>(key)) : 0;
+  if (i == 0) {
     s.found_mass = r.mass;
     s.found_at = n;
-    s.n_groups = 0;  // counts the tokens that min-p keeps
   }
-  __syncthreads();
+  const u64 before = mass_before(w), with = before + w;  // (a barrier inside)
+  // how many the filters keep, and their mass
   int keep = n;
   u64 mass = r.mass;
-  if (r.least) {
-    n_min = __reduce_add_sync(0xFFFFFFFFu, n_min);
-    if ((threadIdx.x & 31) == 0) atomicAdd(&s.n_groups, (unsigned)n_min);
-  }
   if (r.top_k) {
     keep = min(n, r.top_k);
-    walk([&](u64, u64 with, int i, u64) {
-      if (i == keep - 1) s.found_mass = with;
-    });
+    if (i == keep - 1) s.found_mass = with;
     __syncthreads();
     mass = s.found_mass;
   }
   if (r.top_p < 1.f) {
     const u64 want = share_of(r.top_p, mass);
-    walk([&](u64 b, u64 with, int i, u64) {
-      if (b < want && with >= want) s.found_at = i + 1;
-    });
+    if (on && before < want && with >= want) s.found_at = i + 1;
   }
-  __syncthreads();
+  const int above = __syncthreads_count(on && key >= r.least);
   keep = min(keep, (int)s.found_at);
-  if (r.least) keep = min(keep, max(1, (int)s.n_groups));
+  if (r.least) keep = min(keep, max(1, above));
   if (r.top_p < 1.f || r.least) {
-    walk([&](u64, u64 with, int i, u64) {
-      if (i == keep - 1) s.found_mass = with;
-    });
+    if (i == keep - 1) s.found_mass = with;
     __syncthreads();
     mass = s.found_mass;
   }
   const u64 want = draw_at(r.u, mass);
-  if (threadIdx.x == 0) s.found_id = 0xFFFFFFFFu;
-  __syncthreads();
-  walk([&](u64 b, u64 with, int i, u64 x) {
-    // the last kept one where rounding leaves no other
-    if (i < keep && b <= want && (with > want || i == keep - 1)) {
-      s.found_id = ~(uint32_t)s.list[i];
-      s.found_w = x;
-    }
-  });
+  // the last kept one where rounding leaves no other
+  if (on && i < keep && before <= want && (with > want || i == keep - 1)) {
+    s.found_id = ~(uint32_t)x;
+    s.found_w = w;
+  }
   __syncthreads();
   *token = (int)s.found_id;
   *prob = share(s.found_w, mass);
@@ -1064,7 +1062,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
   const float* gmax = gmax_all + (long long)n * n_seg * SEG_GROUPS;
   const SegMass* segs = segs_all + (long long)n * n_seg;
   if constexpr (SHORT) {
-    ScanTable& table = *reinterpret_cast<ScanTable*>(s.list);  // not used before
+    ScanTable& table = *reinterpret_cast<ScanTable*>(s.list);  // (not used before)
     if (whole) {
       fill_table(table, SP_THREADS);
       __syncthreads();
@@ -1113,7 +1111,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
         token = (int)id;
       } else {
         __syncthreads();
-        token = find_token<T, ALIGNED, 1>(row, Share{0, vocab}, r.top, 1);
+        token = find_token<T, ALIGNED, 1>(row, Share{0, vocab, false}, r.top, 1);
       }
       prob = 1.f;
     } else {
@@ -1139,7 +1137,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
       if (whole || (!r.top_k && r.top_p < 1.f)) {
         u64 sum = 0;
         if (weight.far) {
-          each<T, ALIGNED>(row, Share{0, vocab}, weight.zlow, weight.m, [&](float z) { sum += weight(z); });
+          each<T, ALIGNED>(row, Share{0, vocab, false}, weight.zlow, weight.m, [&](float z) { sum += weight(z); });
         } else {
           for (int i = threadIdx.x; i < n_seg; i += SP_THREADS) {
             const SegMass q = segs[i];
@@ -1169,12 +1167,14 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
           lo = bound_by_count<T>(gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
         listed = list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, max(lo, r.low));
       }
-      if (listed) {
+      if (listed && s.n_list <= SP_THREADS) {
         sort_list();
         pick_from_list<T>(r, weight, &token, &prob);
+      } else if (listed) {
+        pick_by_search<T, ALIGNED, SampleSmem>(row, Share{0, vocab, true}, r, weight, &token, &prob);
       } else if (SHORT || !jobs) {
         __syncthreads();
-        pick_by_search<T, ALIGNED, SampleSmem>(row, vocab, r, weight, &token, &prob);
+        pick_by_search<T, ALIGNED, SampleSmem>(row, Share{0, vocab, false}, r, weight, &token, &prob);
       } else {
         // left to k_sample_search
         if (threadIdx.x == 0) jobs[n].row = r;
@@ -1208,7 +1208,8 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_search(SampleArgs a, c
   const Weights weight(jobs[n].m, t, min(62 - (32 - __clz(a.vocab - 1)), SEG_FRAC));
   int token;
   float prob;
-  pick_by_search<T, ALIGNED, SearchSmem>(static_cast<const T*>(a.logits) + n * a.ld, a.vocab, r, weight, &token, &prob);
+  pick_by_search<T, ALIGNED, SearchSmem>(static_cast<const T*>(a.logits) + n * a.ld,
+                                         share_of_row<T, SS_RANKS>(a.vocab), r, weight, &token, &prob);
   if (threadIdx.x == 0 && token >= 0) {
     a.token[n] = token;
     if (a.prob) a.prob[n] = prob;
