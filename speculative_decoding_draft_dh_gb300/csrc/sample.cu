@@ -63,8 +63,11 @@ struct Scratch {
   uint32_t bin_count, above_count;
   uint32_t n_list, n_groups;
   u64 found_mass, found_w;
+  u64 found_token;
   uint32_t found_at, found_id;
   uint32_t share[2];  // of a sum over a cluster
+  uint32_t n_few;
+  u64 few[SP_THREADS], all_few[SP_THREADS];  // tokens as in the lists, of a block's share and of the row
 };
 
 constexpr ExpTable make_table() {
@@ -170,15 +173,6 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   if (sizeof(T) == 4) return fkey_inv(key);
   return fkey_inv((key & 0x8000u) ? key << 16 : (key << 16) | 0xFFFFu);
 }
-// The smallest key of T whose value is at least x.
-template <typename T>
-__device__ __forceinline__ uint32_t key_at_least(float x) {
-  const uint32_t k = fkey(x);
-  if (sizeof(T) == 4) return k;
-  // a negative bf16 value's key has ones where the fp32 key goes on, a positive one's zeros
-  return (k & 0x80000000u) ? (k + 0xFFFFu) >> 16 : k >> 16;
-}
-
 // ------------------------------------------------------------------ the pass over the logits
 
 // A segment's mass, in units of 2^(e - SEG_FRAC).
@@ -353,13 +347,13 @@ __device__ __forceinline__ Share share_of_row(int vocab) {
   return {from, min(from + each, vocab), false};
 }
 
-// f(value) of every logit of the list that is in [from, to].
+// f(value, id) of every token of the list.
 template <typename T, typename F>
-__device__ __forceinline__ void each_listed(float from, float to, F f) {
+__device__ __forceinline__ void each_listed(F f) {
   const SampleSmem& s = smem<SampleSmem>();
   for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS) {
-    const float z = value_of<T>((uint32_t)(s.list[i] >> 32));
-    if (z >= from && z <= to) f(z);
+    const u64 x = s.list[i];
+    f(value_of<T>((uint32_t)(x >> 32)), ~(uint32_t)x);
   }
 }
 
@@ -429,7 +423,7 @@ __device__ __forceinline__ float element(const uint4& u, int e) {
     return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
   }
 }
-// As `each`, where few are: from and to are values of T.
+// f(value, id) as `each`, where few are: from and to are values of T.
 template <typename T, bool ALIGNED, typename F>
 __device__ __forceinline__ void each_of_few(const T* row, Share part, float from, float to, F f) {
   constexpr int PER = Elem<T>::PER16, AHEAD = 4;
@@ -444,12 +438,22 @@ __device__ __forceinline__ void each_of_few(const T* row, Share part, float from
     }
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q)
-      for (uint32_t hits = within(u[q]); hits; hits &= hits - 1) f(element<T>(u[q], __ffs(hits) - 1));
+      for (uint32_t hits = within(u[q]); hits; hits &= hits - 1) {
+        const int e = __ffs(hits) - 1;
+        f(element<T>(u[q], e), (uint32_t)(id0 + q * SP_THREADS * PER + e));
+      }
   }
 }
 
-// The bin, from the top down, in which `want` is reached: tokens (BY_COUNT) or a mass of want or more (STRICT: more
-// than want), counted on from `above` tokens of `above_mass`; the last bin that is not empty where it is not.
+// What a place is searched by: a number of tokens, a mass, or more than a mass.  (Arguments, not template parameters:
+// a row's searches then share their code, which comes from memory the first time.)
+enum Goal { TOKENS, MASS, ABOVE };
+__device__ __forceinline__ bool reached(Goal goal, u64 want, u64 mass, uint32_t count) {
+  return goal == TOKENS ? count >= want : goal == ABOVE ? mass > want : mass >= want;
+}
+
+// The bin, from the top down, in which `want` is reached, counted on from `above` tokens of `above_mass`; the last bin
+// that is not empty where it is not.
 struct Histogram {
   int bin;
   uint32_t above, count;
@@ -535,8 +539,8 @@ template <typename T, bool ALIGNED, class S>
 __device__ __noinline__ void fill_coarse(const T* row, Share part, Coarse coarse, Weights weight, bool counted) {
   clear_bins<S>(0);
   Bins& local = smem<S>().local(0);
-  auto add = [&](float z) { local.add(coarse.bin<T>(z, weight), weight(z), counted); };
-  if (S::RANKS == 1 && part.listed) each_listed<T>(weight.zlow, weight.m, add);
+  auto add = [&](float z, uint32_t = 0) { local.add(coarse.bin<T>(z, weight), weight(z), counted); };
+  if (S::RANKS == 1 && part.listed) each_listed<T>(add);
   else each<T, ALIGNED>(row, part, weight.zlow, weight.m, add);
   merge_bins<S>(0);
 }
@@ -547,15 +551,13 @@ __device__ __noinline__ void fill_fine(const T* row, Share part, Coarse coarse, 
   clear_bins<S>(1);
   Bins& local = smem<S>().local(1);
   const int sh = bin_shift(lo, hi);
-  auto add = [&](float z) {
+  each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), [&](float z, uint32_t) {
     if (coarse.bin<T>(z, weight) == bin) local.add((hi - key_of<T>(z)) >> sh, weight(z), true);
-  };
-  if (S::RANKS == 1 && part.listed) each_listed<T>(value_of<T>(lo), value_of<T>(hi), add);
-  else each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), add);
+  });
   merge_bins<S>(1);
 }
-template <class S, bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_mass, u64 want) {
+template <class S>
+__device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_mass, u64 want, Goal goal) {
   S& s = smem<S>();
   const Bins& bins = s.bins[level];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -592,9 +594,6 @@ __device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_
     ma += s.warp_mass[w];
     ca += s.warp_count[w];
   }
-  auto reached = [&](u64 mass, uint32_t count) {
-    return BY_COUNT ? count >= want : STRICT ? mass > want : mass >= want;
-  };
   auto found = [&](int b, u64 mass_before, uint32_t count_before) {
     s.bin_mass = bins.mass(b);
     s.bin_count = bins.count[b];
@@ -613,7 +612,7 @@ __device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_
       last_mass = ma;
       last_count = ca;
     }
-    if (!reached(ma, ca) && reached(ma + mb, ca + cb)) {
+    if (!reached(goal, want, ma, ca) && reached(goal, want, ma + mb, ca + cb)) {
       s.bin = b0 + q;
       found(b0 + q, ma, ca);
     }
@@ -630,12 +629,11 @@ __device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_
   return h;
 }
 
-// The first place with `want` tokens or more (BY_COUNT), or with a mass of want or more (STRICT: more than want); the
-// last place where there is none.  bins[0] is the row's coarse histogram.
-template <typename T, bool ALIGNED, class S, bool BY_COUNT, bool STRICT>
-__device__ __noinline__ Place descend(const T* row, Share part, Coarse coarse, u64 want, Weights weight) {
+// The first place at which `want` is reached, the last place where it is not.  bins[0] is the row's coarse histogram.
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ Place descend(const T* row, Share part, Coarse coarse, u64 want, Goal goal, Weights weight) {
   Place p = {};
-  Histogram h = find_bin<S, BY_COUNT, STRICT>(0, 0, 0, want);
+  Histogram h = find_bin<S>(0, 0, 0, want, goal);
   const int bin = h.bin;
   uint32_t lo, hi;
   coarse.keys<T>(bin, weight, &lo, &hi);
@@ -644,7 +642,7 @@ __device__ __noinline__ Place descend(const T* row, Share part, Coarse coarse, u
     p.above = h.above;
     fill_fine<T, ALIGNED, S>(row, part, coarse, bin, lo, hi, weight);
     const int sh = bin_shift(lo, hi);
-    h = find_bin<S, BY_COUNT, STRICT>(1, p.above, p.above_mass, want);
+    h = find_bin<S>(1, p.above, p.above_mass, want, goal);
     hi -= (uint32_t)h.bin << sh;
     const uint32_t reach = (1u << sh) - 1u;
     if (hi - lo > reach) lo = hi - reach;
@@ -717,33 +715,6 @@ __device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, u
   return s.bin;
 }
 
-// The same of the list: the j-th of the listed tokens whose key is `key`.
-__device__ __noinline__ int find_listed(uint32_t key, uint32_t j) {
-  SampleSmem& s = smem<SampleSmem>();
-  const int n = (int)s.n_list;
-  if (threadIdx.x == 0) {
-    s.bin = -1;
-    s.n_groups = 0;  // of that key
-  }
-  __syncthreads();
-  uint32_t own = 0;
-  for (int i = threadIdx.x; i < n; i += SP_THREADS) own += (uint32_t)(s.list[i] >> 32) == key;
-  if (own) atomicAdd(&s.n_groups, own);
-  __syncthreads();
-  j = min(j, s.n_groups);
-  for (int i = threadIdx.x; i < n; i += SP_THREADS) {
-    const u64 x = s.list[i];
-    if ((uint32_t)(x >> 32) != key) continue;
-    // of one key the larger number has the lower id
-    uint32_t rank = 1;
-    if (s.n_groups > 1)
-      for (int k = 0; k < n; ++k) rank += (uint32_t)(s.list[k] >> 32) == key && s.list[k] > x;
-    if (rank == j) s.bin = (int)~(uint32_t)x;
-  }
-  __syncthreads();
-  return s.bin;
-}
-
 // w / mass; in 64 bits by one warp, whose result counts (the units are few).
 __device__ __forceinline__ float share(u64 w, u64 mass) {
   return threadIdx.x < 32 ? (float)((double)w / (double)mass) : 0.f;
@@ -782,7 +753,8 @@ __device__ __forceinline__ u64 mass_before(u64 x) {
 struct RowState {
   uint32_t top;    // key of the largest logit
   uint32_t low;    // of the smallest logit with a weight
-  uint32_t least;  // of the smallest logit that min-p keeps (0: it leaves out none)
+  uint32_t least;  // of a logit that is below every one that min-p keeps (0: it leaves out none)
+  u64 w_min;       // the smallest weight that min-p keeps
   int top_k;       // 0: none
   float top_p, u;
   u64 mass;        // of the row, where no top-k bounds it (0: not known)
@@ -801,62 +773,181 @@ __device__ __forceinline__ u64 share_of(float p, u64 mass) {
   return want < 1 ? 1 : want;
 }
 
-// Token and probability by searches over the whole row, by one block or a cluster (token -1 in the blocks that do
-// not hold it), or over a list that holds all tokens down to the last that can be drawn.
+// Sum over the block, or the cluster, that searches a row; every thread gets it.
+template <class S>
+__device__ __forceinline__ u64 row_mass(u64 x) {
+  u64 mass = block_mass(x);
+  if constexpr (S::RANKS > 1) {
+    S& s = smem<S>();
+    if (threadIdx.x == 0) {
+      s.share[0] = (uint32_t)mass;
+      s.share[1] = (uint32_t)(mass >> 32);
+    }
+    cluster_sync();
+    mass = 0;
+    for (uint32_t k = 0; k < S::RANKS; ++k) mass += ((u64)ld_cluster(&s.share[1], k) << 32) | ld_cluster(&s.share[0], k);
+    cluster_sync();
+  }
+  return mass;
+}
+// The mass of the tokens that min-p keeps.
 template <typename T, bool ALIGNED, class S>
-__device__ __noinline__ void pick_by_search(const T* row, Share part, RowState r, Weights weight, int* token,
-                                            float* prob) {
-  constexpr int RANKS = S::RANKS;
+__device__ __noinline__ u64 mass_of_heavy(const T* row, Share part, u64 w_min, uint32_t least, Weights weight) {
+  u64 sum = 0;
+  auto add = [&](float z, uint32_t = 0) {
+    const u64 w = weight(z);
+    if (w >= w_min) sum += w;
+  };
+  if (S::RANKS == 1 && part.listed) each_listed<T>(add);
+  else each<T, ALIGNED>(row, part, fmaxf(value_of<T>(least), weight.zlow), weight.m, add);
+  return row_mass<S>(sum);
+}
+
+// The token (as in the lists) at which `want` is reached, of the tokens of coarse bin h.bin, the running sum up to and
+// with it, and its weight; the bin's last one where it is not.  False where the bin has more tokens than threads.
+struct Cut {
+  u64 token, mass, w;
+};
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Histogram h, u64 want, Goal goal,
+                                     Weights weight, Cut* cut) {
   S& s = smem<S>();
-  const Coarse coarse = {weight.far ? 0 : weight.step(weight.m), r.low, r.top, bin_shift(r.low, r.top), weight.far};
+  if (threadIdx.x == 0) s.n_few = 0;
+  __syncthreads();
+  auto add = [&](float z, uint32_t id) {
+    if (!(z >= weight.zlow) || coarse.bin<T>(z, weight) != h.bin) return;
+    const uint32_t at = atomicAdd(&s.n_few, 1u);
+    if (at < SP_THREADS) s.few[at] = ((u64)key_of<T>(z) << 32) | (uint32_t)~id;
+  };
+  if (S::RANKS == 1 && part.listed) {
+    each_listed<T>(add);
+  } else {
+    uint32_t lo, hi;
+    coarse.keys<T>(h.bin, weight, &lo, &hi);
+    each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), add);
+  }
+  __syncthreads();
+  const int i = threadIdx.x;
+  int n = (int)s.n_few;
+  u64 x = 0;
+  if constexpr (S::RANKS == 1) {
+    if (n > SP_THREADS) return false;
+    if (i < n) x = s.few[i];
+  } else {
+    cluster_sync();
+    int base = 0, mine = -1, at = 0;
+    for (uint32_t r = 0; r < S::RANKS; ++r) {
+      const int c = (int)ld_cluster(&s.n_few, r);
+      if (mine < 0 && i < base + c) {
+        mine = (int)r;
+        at = i - base;
+      }
+      base += c;
+    }
+    n = base;
+    if (n <= SP_THREADS && mine >= 0) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(&s.few[at]);
+      x = ((u64)ld_cluster(from + 1, mine) << 32) | ld_cluster(from, mine);
+    }
+    cluster_sync();  // the other blocks' have been read
+    if (n > SP_THREADS) return false;
+  }
+  if (i < n) s.all_few[i] = x;
+  __syncthreads();
+  int rank = 0;
+  if (i < n) {
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) rank += s.all_few[k] > x;
+  }
+  __syncthreads();
+  if (i < n) s.all_few[rank] = x;
+  if (i == 0) s.found_at = n - 1;
+  __syncthreads();
+  x = i < n ? s.all_few[i] : 0;
+  const u64 w = i < n ? weight(value_of<T>((uint32_t)(x >> 32))) : 0;
+  const u64 before = h.above_mass + mass_before(w);
+  if (i < n && !reached(goal, want, before, h.above + i) && reached(goal, want, before + w, h.above + i + 1))
+    s.found_at = i;
+  __syncthreads();
+  if (i == (int)s.found_at) {
+    s.found_token = x;
+    s.found_mass = before + w;
+    s.found_w = w;
+  }
+  __syncthreads();
+  *cut = {s.found_token, s.found_mass, s.found_w};
+  __syncthreads();
+  return true;
+}
+
+// Token and probability where thousands of tokens are equal, or nearly: a coarse bin's tokens by ranges of their keys,
+// until one key is left.
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ void pick_by_keys(const T* row, Share part, Coarse coarse, RowState r, Weights weight,
+                                          int* token, float* prob) {
+  constexpr int RANKS = S::RANKS;
   fill_coarse<T, ALIGNED, S>(row, part, coarse, weight, r.top_k != 0);
   // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
-  uint32_t key = r.low, equal = 0xFFFFFFFFu;
-  u64 mass = r.mass;
+  uint32_t key = 0, equal = 0xFFFFFFFFu;
+  u64 mass = r.mass, w = 0;
   if (r.top_k) {
-    const Place p = descend<T, ALIGNED, S, true, false>(row, part, coarse, (u64)r.top_k, weight);
+    const Place p = descend<T, ALIGNED, S>(row, part, coarse, (u64)r.top_k, TOKENS, weight);
     key = p.key;
     equal = min((uint32_t)r.top_k - min(p.above, (uint32_t)r.top_k), p.n_equal);
     mass = p.above_mass + equal * p.w;
+    w = p.w;
   }
   if (r.top_p < 1.f) {
     const u64 want = share_of(r.top_p, mass);
-    const Place p = descend<T, ALIGNED, S, false, false>(row, part, coarse, want, weight);
+    const Place p = descend<T, ALIGNED, S>(row, part, coarse, want, MASS, weight);
     uint32_t j = p.n_equal;
     if (p.w && p.above_mass < want) j = (uint32_t)min((u64)j, (want - p.above_mass + p.w - 1) / p.w);
     if (p.key == key) j = min(j, equal);
     key = p.key;
     equal = j;
     mass = p.above_mass + j * p.w;
+    w = p.w;
   }
-  if (r.least > key || mass == 0) {
-    // min-p alone (the mass is not known yet), or above what top-k and top-p keep
-    key = max(key, r.least);
-    equal = 0xFFFFFFFFu;
-    u64 sum = 0;
-    auto add = [&](float z) { sum += weight(z); };
-    if (RANKS == 1 && part.listed) each_listed<T>(value_of<T>(key), weight.m, add);
-    else each<T, ALIGNED>(row, part, value_of<T>(key), weight.m, add);
-    mass = block_mass(sum);
-    if constexpr (RANKS > 1) {
-      if (threadIdx.x == 0) {
-        s.share[0] = (uint32_t)mass;
-        s.share[1] = (uint32_t)(mass >> 32);
-      }
-      cluster_sync();
-      mass = 0;
-      for (uint32_t k = 0; k < RANKS; ++k) mass += ((u64)ld_cluster(&s.share[1], k) << 32) | ld_cluster(&s.share[0], k);
-      cluster_sync();
-    }
+  if (r.w_min > w) {
+    key = 0;
+    mass = mass_of_heavy<T, ALIGNED, S>(row, part, r.w_min, r.least, weight);
   }
   const u64 want = draw_at(r.u, mass);
-  const Place p = descend<T, ALIGNED, S, false, true>(row, part, coarse, want, weight);
+  const Place p = descend<T, ALIGNED, S>(row, part, coarse, want, ABOVE, weight);
   uint32_t j = p.n_equal;
   if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
   if (p.key == key) j = min(j, equal);
-  // (p.key < key, below the kept prefix, is not reached: the searches go by the same sums)
-  *token = RANKS == 1 && part.listed ? find_listed(p.key, j) : find_token<T, ALIGNED, RANKS>(row, part, p.key, j);
+  *token = find_token<T, ALIGNED, RANKS>(row, part, p.key, j);
   *prob = share(p.w, mass);
+}
+
+// Token and probability by searches over the whole row, by one block or a cluster (-1 in the blocks that do not hold
+// the token), or over a list that holds all tokens down to the last that can be drawn.
+template <typename T, bool ALIGNED, class S>
+__device__ __noinline__ void pick_by_search(const T* row, Share part, RowState r, Weights weight, int* token,
+                                            float* prob) {
+  const Coarse coarse = {weight.far ? 0 : weight.step(weight.m), r.low, r.top, bin_shift(r.low, r.top), weight.far};
+  fill_coarse<T, ALIGNED, S>(row, part, coarse, weight, r.top_k != 0);
+  // each filter's last token: its place in the bins, then among its bin's tokens
+  Cut cut = {0, r.mass, 0};
+  auto search = [&](u64 want, Goal goal) {
+    return resolve<T, ALIGNED, S>(row, part, coarse, find_bin<S>(0, 0, 0, want, goal), want, goal, weight, &cut);
+  };
+  bool found = !r.top_k || search((u64)r.top_k, TOKENS);
+  if (found && r.top_p < 1.f) found = search(share_of(r.top_p, cut.mass), MASS);
+  if (found) {
+    // min-p alone (the mass is not known yet), or above what top-k and top-p keep
+    u64 mass = cut.mass;
+    if (r.w_min > cut.w) mass = mass_of_heavy<T, ALIGNED, S>(row, part, r.w_min, r.least, weight);
+    found = search(draw_at(r.u, mass), ABOVE);
+    if (found) {
+      *token = S::RANKS == 1 || cluster_rank() == 0 ? (int)~(uint32_t)cut.token : -1;
+      *prob = share(cut.w, mass);
+      return;
+    }
+  }
+  if constexpr (S::RANKS == 1) part = {0, part.to, false};
+  pick_by_keys<T, ALIGNED, S>(row, part, coarse, r, weight, token, prob);
 }
 
 // The lower edge of the histogram bin that holds the k-th largest of the groups' maxima, of which the smallest above
@@ -1016,10 +1107,10 @@ __device__ __noinline__ void pick_from_list(RowState r, Weights weight, int* tok
     const u64 want = share_of(r.top_p, mass);
     if (on && before < want && with >= want) s.found_at = i + 1;
   }
-  const int above = __syncthreads_count(on && key >= r.least);
+  const int above = __syncthreads_count(on && w >= r.w_min);
   keep = min(keep, (int)s.found_at);
-  if (r.least) keep = min(keep, max(1, above));
-  if (r.top_p < 1.f || r.least) {
+  if (r.w_min) keep = min(keep, max(1, above));
+  if (r.top_p < 1.f || r.w_min) {
     if (i == keep - 1) s.found_mass = with;
     __syncthreads();
     mass = s.found_mass;
@@ -1122,17 +1213,15 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
       r.u = u;
       r.mass = 0;
       r.least = 0;
+      r.w_min = 0;
       if (min_p > 0.f) {
-        // the lowest logit whose weight is min_p of the largest one's, in 64 bits by one warp (the units are few)
-        if (threadIdx.x < 32) {
-          const double x = (double)m + (double)t * log((double)fminf(min_p, 1.f));
-          float f = (float)x;
-          if ((double)f < x) f = nextafterf(f, INFINITY);
-          if (threadIdx.x == 0) s.warp_max[0] = f;
-        }
-        __syncthreads();
-        r.least = min(key_at_least<T>(s.warp_max[0]), r.top);
-        __syncthreads();
+        const u64 most = weight(m);
+        bool rest;
+        r.w_min = min_p < 1.f ? times(min_p, most, &rest) : most;
+        if (min_p < 1.f) r.w_min += rest;
+        // a little lower: this value's and the weights' roundings
+        const float z = m + t * logf(fminf(min_p, 1.f));
+        r.least = min(key_of<T>(z - 1e-5f * (fabsf(z) + fabsf(m)) - 1e-3f * t), r.top);
       }
       if (whole || (!r.top_k && r.top_p < 1.f)) {
         u64 sum = 0;
