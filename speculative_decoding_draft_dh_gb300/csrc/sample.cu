@@ -30,6 +30,7 @@ constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 2048;
 constexpr int SP_LIST = 4096;    // tokens listed, at most
 constexpr int SP_GROUPS = 2048;  // groups listed, at most
+constexpr int SP_FEW = 2 * SP_THREADS;  // tokens of a bin that are sorted, at most
 // Groups with which a row whose mass is needed is tried, and how many times more each time.
 constexpr int SP_TRY_FIRST = 64, SP_TRY_STEP = 16;
 constexpr int SEG_GROUPS = 8;    // groups of a segment: four lanes' vectors each
@@ -67,7 +68,7 @@ struct Scratch {
   uint32_t found_at, found_id;
   uint32_t share[2];  // of a sum over a cluster
   uint32_t n_few;
-  u64 few[SP_THREADS], all_few[SP_THREADS];  // tokens as in the lists, of a block's share and of the row
+  alignas(16) u64 few[SP_FEW], all_few[SP_FEW];  // tokens as in the lists, of a block's share and of the row
 };
 
 constexpr ExpTable make_table() {
@@ -317,7 +318,7 @@ struct SampleSmem : Scratch {
       uint32_t group_count[SP_BINS], groups[SP_GROUPS];
     };
   };
-  u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
+  alignas(16) u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
 };
 constexpr int SS_RANKS = 4;
 struct SearchSmem : Scratch {
@@ -464,8 +465,8 @@ __device__ __forceinline__ int bin_shift(uint32_t lo, uint32_t hi) {
   return bits > 11 ? bits - 11 : 0;
 }
 
-// The bins of a row's first histogram: steps of a 32nd of an octave of the weights (linear in the logits, so that
-// neighbouring tokens seldom meet in a bin), or, where weights are far, ranges of keys.
+// The bins of a row's first histogram: 32nds of an octave of the weights (linear in the logits, so that neighbouring
+// tokens seldom meet in a bin), or, where weights are far, ranges of keys.
 struct Coarse {
   int top;        // step of the largest weight
   uint32_t lo, hi;
@@ -483,7 +484,7 @@ struct Coarse {
       *to = hi - ((uint32_t)b << sh);
       *from = *to - lo > reach ? *to - reach : lo;
     } else {
-      // one step more on either side covers the roundings
+      // half a step more on either side covers the roundings
       const float z1 = (float)(top - 2 * b + 1) / (64.f * weight.c.hi), z0 = (float)(top - 2 * b - 2) / (64.f * weight.c.hi);
       *from = max(lo, min(key_of<T>(z0), hi));
       *to = min(hi, max(key_of<T>(z1), *from));
@@ -803,8 +804,52 @@ __device__ __noinline__ u64 mass_of_heavy(const T* row, Share part, u64 w_min, u
   return row_mass<S>(sum);
 }
 
+constexpr int SP_RANKED = 256;  // tokens: 2 us less than the network at 250, and a tie beyond
+// The first n <= SP_FEW of `a` (shared memory, at 16 bytes) in descending order; they are distinct and not 0, and a holds SP_FEW.
+// By ranks where that is a few steps, else by a bitonic network, whose steps of up to 32 places stay within a warp.
+__device__ __forceinline__ void sort_few(u64* a, int n) {
+  if (n <= SP_RANKED) {
+    const u64 x = (int)threadIdx.x < n ? a[threadIdx.x] : 0;
+    if ((int)threadIdx.x >= n && (int)threadIdx.x < (n + 3) / 4 * 4) a[threadIdx.x] = 0;
+    __syncthreads();
+    int rank = 0;
+    if ((int)threadIdx.x < n) {
+      const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(a);
+      for (int k = 0; k < (n + 3) / 4; ++k) {
+        const ulonglong2 p = pairs[2 * k], q = pairs[2 * k + 1];
+        rank += (p.x > x) + (p.y > x) + (q.x > x) + (q.y > x);
+      }
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < n) a[rank] = x;
+    __syncthreads();
+    return;
+  }
+  int size = 128;
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += SP_THREADS) a[i] = 0;
+  __syncthreads();
+  const int t = threadIdx.x;
+  for (int k = 2; k <= size; k *= 2) {
+    for (int j = k / 2; j > 0; j /= 2) {
+      if (t < size / 2) {
+        const int i = 2 * t - (t & (j - 1)), o = i + j;
+        const u64 x = a[i], y = a[o];
+        if ((x < y) == ((i & k) == 0)) {
+          a[i] = y;
+          a[o] = x;
+        }
+      }
+      // the next step's places: this warp's own 64, or others
+      if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
+      else __syncwarp();
+    }
+  }
+  __syncthreads();
+}
+
 // The token (as in the lists) at which `want` is reached, of the tokens of coarse bin h.bin, the running sum up to and
-// with it, and its weight; the bin's last one where it is not.  False where the bin has more tokens than threads.
+// with it, and its weight; the bin's last one where it is not.  False where the bin has more tokens than are sorted.
 struct Cut {
   u64 token, mass, w;
 };
@@ -817,7 +862,7 @@ __device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Hi
   auto add = [&](float z, uint32_t id) {
     if (!(z >= weight.zlow) || coarse.bin<T>(z, weight) != h.bin) return;
     const uint32_t at = atomicAdd(&s.n_few, 1u);
-    if (at < SP_THREADS) s.few[at] = ((u64)key_of<T>(z) << 32) | (uint32_t)~id;
+    if (at < SP_FEW) s.few[at] = ((u64)key_of<T>(z) << 32) | (uint32_t)~id;
   };
   if (S::RANKS == 1 && part.listed) {
     each_listed<T>(add);
@@ -827,52 +872,65 @@ __device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Hi
     each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), add);
   }
   __syncthreads();
-  const int i = threadIdx.x;
+  // the row's, into all_few; two to a thread
   int n = (int)s.n_few;
-  u64 x = 0;
+  u64 x[2] = {0, 0};
   if constexpr (S::RANKS == 1) {
-    if (n > SP_THREADS) return false;
-    if (i < n) x = s.few[i];
+    if (n > SP_FEW) return false;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if ((int)threadIdx.x + q * SP_THREADS < n) x[q] = s.few[threadIdx.x + q * SP_THREADS];
   } else {
     cluster_sync();
-    int base = 0, mine = -1, at = 0;
-    for (uint32_t r = 0; r < S::RANKS; ++r) {
-      const int c = (int)ld_cluster(&s.n_few, r);
-      if (mine < 0 && i < base + c) {
-        mine = (int)r;
-        at = i - base;
+    int from[S::RANKS + 1];
+    from[0] = 0;
+#pragma unroll
+    for (int r = 0; r < S::RANKS; ++r) from[r + 1] = from[r] + (int)ld_cluster(&s.n_few, r);
+    n = from[S::RANKS];
+    if (n <= SP_FEW) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = threadIdx.x + q * SP_THREADS;
+#pragma unroll
+        for (int r = 0; r < S::RANKS; ++r) {
+          if (i >= from[r] && i < from[r + 1]) {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(&s.few[i - from[r]]);
+            x[q] = ((u64)ld_cluster(p + 1, r) << 32) | ld_cluster(p, r);
+          }
+        }
       }
-      base += c;
-    }
-    n = base;
-    if (n <= SP_THREADS && mine >= 0) {
-      const uint32_t* from = reinterpret_cast<const uint32_t*>(&s.few[at]);
-      x = ((u64)ld_cluster(from + 1, mine) << 32) | ld_cluster(from, mine);
     }
     cluster_sync();  // the other blocks' have been read
-    if (n > SP_THREADS) return false;
+    if (n > SP_FEW) return false;
   }
-  if (i < n) s.all_few[i] = x;
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    if ((int)threadIdx.x + q * SP_THREADS < n) s.all_few[threadIdx.x + q * SP_THREADS] = x[q];
   __syncthreads();
-  int rank = 0;
-  if (i < n) {
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) rank += s.all_few[k] > x;
+  sort_few(s.all_few, n);
+  if (threadIdx.x == 0) s.found_at = n - 1;
+  __syncthreads();
+  u64 w[2];
+  const int i0 = 2 * threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    x[q] = i0 + q < n ? s.all_few[i0 + q] : 0;
+    w[q] = i0 + q < n ? weight(value_of<T>((uint32_t)(x[q] >> 32))) : 0;
+  }
+  u64 run = h.above_mass + mass_before(w[0] + w[1]);
+  const u64 before = run;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (i0 + q < n && !reached(goal, want, run, h.above + i0 + q) && reached(goal, want, run + w[q], h.above + i0 + q + 1))
+      s.found_at = i0 + q;
+    run += w[q];
   }
   __syncthreads();
-  if (i < n) s.all_few[rank] = x;
-  if (i == 0) s.found_at = n - 1;
-  __syncthreads();
-  x = i < n ? s.all_few[i] : 0;
-  const u64 w = i < n ? weight(value_of<T>((uint32_t)(x >> 32))) : 0;
-  const u64 before = h.above_mass + mass_before(w);
-  if (i < n && !reached(goal, want, before, h.above + i) && reached(goal, want, before + w, h.above + i + 1))
-    s.found_at = i;
-  __syncthreads();
-  if (i == (int)s.found_at) {
-    s.found_token = x;
-    s.found_mass = before + w;
-    s.found_w = w;
+  const int at = (int)s.found_at - i0;
+  if (at == 0 || at == 1) {
+    s.found_token = x[at];
+    s.found_mass = before + w[0] + (at ? w[1] : 0);
+    s.found_w = w[at];
   }
   __syncthreads();
   *cut = {s.found_token, s.found_mass, s.found_w};
@@ -1063,63 +1121,65 @@ __device__ __noinline__ u64 list_mass(Weights weight) {
   return block_mass(sum);
 }
 
-// A list of at most a token per thread, in descending order (its numbers are distinct), by ranks.
-__device__ __noinline__ void sort_list() {
-  SampleSmem& s = smem<SampleSmem>();
-  const int n = (int)s.n_list;
-  u64 x = 0;
-  int rank = 0;
-  if ((int)threadIdx.x < n) {
-    x = s.list[threadIdx.x];
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) rank += s.list[i] > x;
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < n) s.list[rank] = x;
-  __syncthreads();
-}
-
-// Token and probability from the sorted list, which holds all tokens down to the last that can be drawn, one to a
-// thread.
+// Token and probability from a list of at most SP_FEW tokens, sorted here, which holds all tokens down to the last that
+// can be drawn; two to a thread.
 template <typename T>
 __device__ __noinline__ void pick_from_list(RowState r, Weights weight, int* token, float* prob) {
   SampleSmem& s = smem<SampleSmem>();
-  const int n = (int)s.n_list, i = threadIdx.x;
-  const bool on = i < n;
-  const u64 x = on ? s.list[i] : 0;
-  const uint32_t key = (uint32_t)(x >> 32);
-  const u64 w = on ? weight(value_of<T>(key)) : 0;
-  if (i == 0) {
+  const int n = (int)s.n_list, i0 = 2 * threadIdx.x;
+  sort_few(s.list, n);
+  u64 x[2], w[2];
+  int heavy = 0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    x[q] = i0 + q < n ? s.list[i0 + q] : 0;
+    w[q] = i0 + q < n ? weight(value_of<T>((uint32_t)(x[q] >> 32))) : 0;
+    heavy += i0 + q < n && w[q] >= r.w_min;
+  }
+  if (threadIdx.x == 0) {
     s.found_mass = r.mass;
     s.found_at = n;
+    s.n_few = 0;  // of the tokens that min-p keeps
   }
-  const u64 before = mass_before(w), with = before + w;  // (a barrier inside)
-  // how many the filters keep, and their mass
+  const u64 before = mass_before(w[0] + w[1]);  // (a barrier inside)
+  const u64 run[3] = {before, before + w[0], before + w[0] + w[1]};  // up to each token, and with it
+  if (r.w_min) {
+    heavy = __reduce_add_sync(0xFFFFFFFFu, heavy);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s.n_few, (unsigned)heavy);
+  }
+  // the mass up to and with the last token that is kept
   int keep = n;
   u64 mass = r.mass;
-  if (r.top_k) {
-    keep = min(n, r.top_k);
-    if (i == keep - 1) s.found_mass = with;
+  auto mass_of_kept = [&]() {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (i0 + q == keep - 1) s.found_mass = run[q + 1];
     __syncthreads();
     mass = s.found_mass;
+  };
+  if (r.top_k) {
+    keep = min(n, r.top_k);
+    mass_of_kept();
   }
   if (r.top_p < 1.f) {
     const u64 want = share_of(r.top_p, mass);
-    if (on && before < want && with >= want) s.found_at = i + 1;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (i0 + q < n && run[q] < want && run[q + 1] >= want) s.found_at = i0 + q + 1;
   }
-  const int above = __syncthreads_count(on && w >= r.w_min);
+  __syncthreads();
   keep = min(keep, (int)s.found_at);
-  if (r.w_min) keep = min(keep, max(1, above));
-  if (r.top_p < 1.f || r.w_min) {
-    if (i == keep - 1) s.found_mass = with;
-    __syncthreads();
-    mass = s.found_mass;
-  }
+  if (r.w_min) keep = min(keep, max(1, (int)s.n_few));
+  if (r.top_p < 1.f || r.w_min) mass_of_kept();
   const u64 want = draw_at(r.u, mass);
   // the last kept one where rounding leaves no other
-  if (on && i < keep && before <= want && (with > want || i == keep - 1)) {
-    s.found_id = ~(uint32_t)x;
-    s.found_w = w;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = i0 + q;
+    if (i < n && i < keep && run[q] <= want && (run[q + 1] > want || i == keep - 1)) {
+      s.found_id = ~(uint32_t)x[q];
+      s.found_w = w[q];
+    }
   }
   __syncthreads();
   *token = (int)s.found_id;
@@ -1256,8 +1316,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
           lo = bound_by_count<T>(gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
         listed = list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, max(lo, r.low));
       }
-      if (listed && s.n_list <= SP_THREADS) {
-        sort_list();
+      if (listed && s.n_list <= SP_FEW) {
         pick_from_list<T>(r, weight, &token, &prob);
       } else if (listed) {
         pick_by_search<T, ALIGNED, SampleSmem>(row, Share{0, vocab, true}, r, weight, &token, &prob);
