@@ -448,8 +448,11 @@ cudaError_t run_embed_backward(const Ctx& c, const EmbedArgs& a) {
   int key_bits = 0;
   while (a.vocab >> key_bits) ++key_bits;  // the largest key is vocab
   const int passes = (key_bits + TS_BITS - 1) / TS_BITS;
-  cudaError_t e = (key_bits + passes - 1) / passes <= 6 ? launch_sort<6>(c, a, passes, buf, present)
-                                                        : launch_sort<TS_BITS>(c, a, passes, buf, present);
+  const int bits = (key_bits + passes - 1) / passes;
+  cudaError_t e = bits <= 6   ? launch_sort<6>(c, a, passes, buf, present)
+                  : bits == 7 ? launch_sort<7>(c, a, passes, buf, present)
+                  : bits == 8 ? launch_sort<8>(c, a, passes, buf, present)
+                              : launch_sort<TS_BITS>(c, a, passes, buf, present);
   if (e != cudaSuccess) return e;
   const bool vec = whole_vectors(a.src, a.src_ld, a.N, a.d, sizeof(T)) &&
                    whole_vectors(a.dst, a.dst_ld, a.vocab, a.d, sizeof(T));
