@@ -220,6 +220,78 @@ def test_draws_follow_the_distribution(s, dtype):
     assert (np.diff(row[token.cpu().numpy()]) <= 0).all()
 
 
+LONG = {  # of V ids i
+    "flat": lambda V, g: 2 * torch.randn(V, generator=g),
+    "narrow": lambda V, g: 1e-3 * torch.randn(V, generator=g),
+    "steps": lambda V, g: torch.floor(torch.arange(V) / 1000.0) / 16,
+    "few values": lambda V, g: (torch.arange(V) % 3).float(),
+    "equal": lambda V, g: torch.full((V,), -2.5),
+    "ramp": lambda V, g: torch.arange(V) * (10.0 / V),
+    "above": lambda V, g: torch.where(torch.arange(V) % 37 == 5, 4.0, 0.0) + 0.25 * torch.randn(V, generator=g),
+    "large": lambda V, g: 1e6 + torch.randn(V, generator=g),
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", LONG)
+def test_long_rows_without_a_short_list(kind, dtype):
+    """Rows of which thousands of tokens are kept, nearly equal or equal.  A weight is rounded to 2^-45 of the largest;
+    of the likeliest tokens' z the others' are 14 T below it at most, so that this is 2^-24.8 of each: with the sums'
+    2^-29 and the result's 2^-24 less than 2^-23."""
+    V, N = 150011, 3
+    g = torch.Generator().manual_seed(len(kind))
+    row = LONG[kind](V, g).to(DT[dtype])
+    for ld in (V, 150016):  # the second in whole vectors
+        buf = torch.full((N, ld), float("nan"), dtype=DT[dtype], device=DEV)
+        z = buf[:, :V]
+        z.copy_(row)
+        u = torch.rand(N, generator=g).to(DEV)
+        for s in [(3.0, 0, 1.0, 0.0), (3.0, 0, 0.99, 0.0), (2.0, 0, 0.5, 0.001), (1.0, 0, 1.0, 0.05), (1.0, 0, 1.0, 0.97),
+                  (1.0, 3000, 1.0, 0.0), (1.0, 1800, 0.9, 0.01), (1.0, 900, 1.0, 0.0), (5.0, 20000, 0.9, 0.0),
+                  (0.0, 0, 1.0, 0.0)]:
+            check(z, u, *s)
+
+
+def test_rows_that_are_searched_beside_others():
+    """Each row of a batch as it is alone, whatever its neighbours need; again with one workspace and given outputs."""
+    V, N = 60000, 40
+    z, u = rows(N, V, "bf16", seed=21)
+    g = torch.Generator().manual_seed(2)
+    z[::3] = (0.5 * torch.randn(V, generator=g)).bfloat16().to(DEV)
+    z[4], z[7, 5] = -float("inf"), float("nan")
+    T = torch.tensor([[0.0, 0.7, 1.0, 2.5][n % 4] for n in range(N)], device=DEV)
+    k = torch.tensor([[0, 30, 4000][n % 3] for n in range(N)], dtype=torch.int32, device=DEV)
+    p = torch.tensor([[1.0, 0.9][n // 3 % 2] for n in range(N)], device=DEV)
+    m = torch.tensor([[0.0, 0.0, 0.02][n // 5 % 3] for n in range(N)], device=DEV)
+    token, prob = check(z, u, T, k, p, m)
+    ws = dh.Workspace()
+    out = torch.empty(N, dtype=torch.int32, device=DEV), torch.empty(N, device=DEV)
+    for n in (N, 7, N):
+        dh.sample(z[:n], u[:n], temperature=T[:n], top_k=k[:n], top_p=p[:n], min_p=m[:n], token_out=out[0][:n],
+                  prob_out=out[1][:n], workspace=ws)
+        assert torch.equal(out[0][:n], token[:n]) and torch.equal(out[1][:n], prob[:n])
+        out[0][:n], out[1][:n] = -5, -5
+    for n in range(N):
+        one = dh.sample(z[n:n + 1], u[n:n + 1], temperature=T[n].item(), top_k=k[n].item(), top_p=p[n].item(),
+                        min_p=m[n].item())
+        assert one[0][0] == token[n] and one[1][0] == prob[n]
+
+
+def test_many_rows():
+    """More rows than blocks can run at once, of both kinds of length."""
+    for N, V in ((70000, 9), (20000, 9000)):
+        g = torch.Generator(device=DEV).manual_seed(N)
+        z = torch.randn(N, V, generator=g, device=DEV).bfloat16()
+        u = torch.rand(N, generator=g, device=DEV)
+        token, prob = dh.sample(z, u, temperature=0.0)
+        first = (z == z.max(1, keepdim=True).values).int().argmax(1)
+        assert torch.equal(token.long(), first) and (prob == 1).all()
+        token, prob = dh.sample(z, u, temperature=1.5)
+        for n in (0, 1, N // 2, N - 1):
+            one = check(z[n:n + 1], u[n:n + 1], 1.5)
+            assert one[0][0] == token[n] and one[1][0] == prob[n]
+
+
 def test_offsets_beyond_32_bits():
     V, ld = 1000, (1 << 31) + 8
     buf = torch.empty(2 * ld + V, dtype=torch.bfloat16, device=DEV)
