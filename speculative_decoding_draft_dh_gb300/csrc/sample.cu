@@ -30,7 +30,7 @@ constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 2048;
 constexpr int SP_LIST = 4096;    // tokens listed, at most
 constexpr int SP_GROUPS = 2048;  // groups listed, at most
-constexpr int SP_FEW = 2 * SP_THREADS;   // tokens of a bin that are sorted, at most
+constexpr int SP_FEW = 4 * SP_THREADS;   // tokens of a bin that are sorted, at most
 constexpr int SP_SORT = 4 * SP_THREADS;  // of a list
 constexpr int SP_RANKED = 128;           // by ranks alone
 // Groups with which a row whose mass is needed is tried, and how many times more each time.
@@ -70,7 +70,7 @@ struct Scratch {
   uint32_t found_at, found_id;
   uint32_t share[2];  // of a sum over a cluster
   uint32_t n_few;
-  u64 few[SP_FEW], all_few[SP_FEW];  // tokens as in the lists, of a block's share and of the row
+  u64 few[SP_FEW];  // tokens as in the lists, of a block's share
 };
 
 constexpr ExpTable make_table() {
@@ -106,9 +106,12 @@ struct Rate {
 struct Weights {
   Rate c;
   float m, t, zlow;
+  int id_bits;      // of the row's ids
   int e_ref, frac;  // the largest weight is in [2^frac, 2^(frac + 1)]
   bool far;
-  __device__ __forceinline__ Weights(float m_, float t_, int frac_) : c(t_), m(m_), t(t_), frac(frac_) {
+  __device__ __forceinline__ Weights(float m_, float t_, int vocab) : c(t_), m(m_), t(t_) {
+    id_bits = 32 - __clz(vocab - 1);
+    frac = min(62 - id_bits, SEG_FRAC);
     const float reach = (float)(frac + 2) / c.hi;  // what is lower than m by that much weighs below 2^-(frac + 1)
     far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e38f && 128.f / c.hi + fabsf(m) < 1e38f);
     zlow = far ? -3.4028234e38f : m - reach;
@@ -128,25 +131,28 @@ struct Weights {
   __device__ __forceinline__ int step(float z) const {
     return __float_as_int(fmaf(z, c.hi, EXP_MAGIC)) - EXP_MAGIC_BITS;
   }
+  // 28 fraction bits to frac, and down, rounded; z is at least zlow, so that the shift is at most 62
+  __device__ __forceinline__ u64 scaled(uint32_t q, int down) const {
+    return ((((u64)q << 32) >> min(59 - frac + down, 63)) + 1) >> 1;
+  }
+  // not far, z at least zlow
+  __device__ __forceinline__ u64 near(float z) const {
+    const float k = fmaf(z, c.hi, EXP_MAGIC), kf = k - EXP_MAGIC;
+    const float r = fmaf(z, c.lo, fmaf(z, c.hi, -kf));
+    const int ki = step(z), j = ki & 63;
+    // 2^r - 1 by its series
+    const float x = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
+    // added to 1.5 2^23, which rounds to an integer in the low bits; |tab.f x| < 2^22
+    const ExpTable& tab = smem<Scratch>().tab;
+    const uint32_t q = tab.q[j] + (uint32_t)(__float_as_int(fmaf(tab.f[j], x, 12582912.f)) - 0x4B400000);
+    return scaled(q, e_ref - (ki >> 6));
+  }
   __device__ __forceinline__ u64 operator()(float z) const {
     if (!(z >= zlow)) return 0;
-    uint32_t q;
+    if (__builtin_expect(!far, 1)) return near(z);
     int down;
-    if (__builtin_expect(far, 0)) {
-      q = slow(z, m, t, &down);
-    } else {
-      const float k = fmaf(z, c.hi, EXP_MAGIC), kf = k - EXP_MAGIC;
-      const float r = fmaf(z, c.lo, fmaf(z, c.hi, -kf));
-      const int ki = step(z), j = ki & 63;
-      // 2^r - 1 by its series
-      const float x = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
-      // added to 1.5 2^23, which rounds to an integer in the low bits; |tab.f x| < 2^22
-      const ExpTable& tab = smem<Scratch>().tab;
-      q = tab.q[j] + (uint32_t)(__float_as_int(fmaf(tab.f[j], x, 12582912.f)) - 0x4B400000);
-      down = e_ref - (ki >> 6);
-    }
-    // 28 fraction bits to frac, and down, rounded; z is at least zlow, so that the shift is at most 62
-    return ((((u64)q << 32) >> min(59 - frac + down, 63)) + 1) >> 1;
+    const uint32_t q = slow(z, m, t, &down);
+    return scaled(q, down);
   }
 };
 
@@ -310,6 +316,7 @@ struct __align__(16) Bins {
 
 struct SampleSmem : Scratch {
   static constexpr int RANKS = 1;  // blocks of a search
+  __device__ __forceinline__ u64* row_few() { return few; }
   __device__ __forceinline__ Bins& local(int level) { return bins[level]; }
   union {
     Bins bins[2];  // of the whole range, of a part of it
@@ -322,6 +329,8 @@ struct SampleSmem : Scratch {
 constexpr int SS_RANKS = 4;
 struct SearchSmem : Scratch {
   static constexpr int RANKS = SS_RANKS;
+  u64 all_few[SP_FEW];  // of the row
+  __device__ __forceinline__ u64* row_few() { return all_few; }
   __device__ __forceinline__ Bins& local(int) { return own; }
   Bins own;      // of this block's share of the row
   Bins bins[2];  // of the whole row
@@ -534,6 +543,48 @@ __device__ __forceinline__ void clear_bins(int level) {
         reinterpret_cast<uint4*>(bins.count)[b] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 }
+// Those of a share with a weight, where weights are near.  A vector's tokens side by side: an atomic's result comes
+// after many instructions, and one after the other a row of 151936 flat logits takes 25 us by four blocks.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void add_near(const T* row, Share part, Coarse coarse, const Weights& weight, Bins& bins,
+                                         bool counted) {
+  constexpr int PER = Elem<T>::PER16, AHEAD = 4;
+  for (int id0 = part.from + threadIdx.x * PER; id0 < part.to; id0 += AHEAD * SP_THREADS * PER) {
+    uint4 u[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const int id = id0 + q * SP_THREADS * PER;
+      u[q] = make_uint4(NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD, NegInf<T>::WORD);
+      if (id < part.to) u[q] = row_vec<T, ALIGNED>(row, id, part.to);
+    }
+#pragma unroll 1
+    for (int q = 0; q < AHEAD; ++q) {
+      float x[PER];
+      Elem<T>::unpack(q == 0 ? u[0] : q == 1 ? u[1] : q == 2 ? u[2] : u[3], x);
+      int b[PER];
+      uint32_t lo[PER], hi[PER];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const float z = fmaxf(x[e], weight.zlow);
+        const u64 w = weight.near(z);
+        b[e] = x[e] >= weight.zlow ? (coarse.top - weight.step(z)) >> 1 : -1;
+        lo[e] = (uint32_t)w;
+        hi[e] = (uint32_t)(w >> 32);
+      }
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (b[e] >= 0) hi[e] += atomicAdd(&bins.lo[b[e]], lo[e]) > ~lo[e];
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (b[e] >= 0 && hi[e]) atomicAdd(&bins.hi[b[e]], hi[e]);
+      if (counted) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+          if (b[e] >= 0) atomicAdd(&bins.count[b[e]], 1u);
+      }
+    }
+  }
+}
 // All tokens with a weight, by the coarse bins, into bins[0].
 template <typename T, bool ALIGNED, class S>
 __device__ __noinline__ void fill_coarse(const T* row, Share part, Coarse coarse, Weights weight, bool counted) {
@@ -541,6 +592,7 @@ __device__ __noinline__ void fill_coarse(const T* row, Share part, Coarse coarse
   Bins& local = smem<S>().local(0);
   auto add = [&](float z, uint32_t = 0) { local.add(coarse.bin<T>(z, weight), weight(z), counted); };
   if (S::RANKS == 1 && part.listed) each_listed<T>(add);
+  else if (!weight.far) add_near<T, ALIGNED>(row, part, coarse, weight, local, counted);
   else each<T, ALIGNED>(row, part, weight.zlow, weight.m, add);
   merge_bins<S>(0);
 }
@@ -807,10 +859,10 @@ __device__ __noinline__ u64 mass_of_heavy(const T* row, Share part, u64 w_min, u
 }
 
 // The first n <= OWN SP_THREADS of `a` (shared memory) in descending order; they are distinct.  A few are ranked among
-// one another; more are counted by ranges of their keys first, of which most have a token or none, and then ranked
-// among their range's.  (100 tokens: 1 us by ranks, 2 by ranges; 565: 6 by ranks, 2 by ranges.)
+// one another; more are counted by ranges of their keys first, of one key by ranges of ids, so that most ranges have a
+// token or none, and then ranked among their range's.  (100 tokens: 1 us by ranks, 2 by ranges; 565: 6 by ranks, 2 by ranges.)
 template <int OWN>
-__device__ __forceinline__ void sort_few(u64* a, int n, Bins& bins) {
+__device__ __forceinline__ void sort_few(u64* a, int n, int id_bits, Bins& bins) {
   Scratch& s = smem<Scratch>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (n <= SP_RANKED) {
@@ -845,11 +897,12 @@ __device__ __forceinline__ void sort_few(u64* a, int n, Bins& bins) {
   const u64 range = lane < SP_WARPS ? s.warp_mass[lane] : 0xFFFFFFFFull;
   lo = __reduce_min_sync(0xFFFFFFFFu, (uint32_t)range);
   hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(range >> 32));
-  const int sh = bin_shift(lo, hi);
+  const int sh = bin_shift(lo, hi), more = max(11 - (32 - __clz(hi - lo)), 0), id_sh = max(id_bits - more, 0);
   uint32_t at[OWN], slot[OWN];
 #pragma unroll
   for (int q = 0; q < OWN; ++q) {
     at[q] = (hi - (uint32_t)(x[q] >> 32)) >> sh;
+    if (more) at[q] = (at[q] << more) + ((~(uint32_t)x[q]) >> id_sh);
     if ((int)threadIdx.x + q * SP_THREADS < n) slot[q] = atomicAdd(&bins.count[at[q]], 1u);
   }
   __syncthreads();
@@ -916,15 +969,12 @@ __device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Hi
     each_of_few<T, ALIGNED>(row, part, value_of<T>(lo), value_of<T>(hi), add);
   }
   __syncthreads();
-  // the row's, into all_few; two to a thread
+  // the row's, together
+  constexpr int OWN = SP_FEW / SP_THREADS;
   int n = (int)s.n_few;
-  u64 x[2] = {0, 0};
-  if constexpr (S::RANKS == 1) {
-    if (n > SP_FEW) return false;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      if ((int)threadIdx.x + q * SP_THREADS < n) x[q] = s.few[threadIdx.x + q * SP_THREADS];
-  } else {
+  u64* few = s.row_few();
+  u64 x[OWN], w[OWN];
+  if constexpr (S::RANKS > 1) {
     cluster_sync();
     int from[S::RANKS + 1];
     from[0] = 0;
@@ -933,48 +983,41 @@ __device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Hi
     n = from[S::RANKS];
     if (n <= SP_FEW) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < OWN; ++q) {
         const int i = threadIdx.x + q * SP_THREADS;
 #pragma unroll
         for (int r = 0; r < S::RANKS; ++r) {
           if (i >= from[r] && i < from[r + 1]) {
             const uint32_t* p = reinterpret_cast<const uint32_t*>(&s.few[i - from[r]]);
-            x[q] = ((u64)ld_cluster(p + 1, r) << 32) | ld_cluster(p, r);
+            few[i] = ((u64)ld_cluster(p + 1, r) << 32) | ld_cluster(p, r);
           }
         }
       }
     }
     cluster_sync();  // the other blocks' have been read
-    if (n > SP_FEW) return false;
   }
+  if (n > SP_FEW) return false;
+  sort_few<OWN>(few, n, weight.id_bits, s.bins[1]);
+  const int i0 = OWN * threadIdx.x;
+  u64 run = 0;
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-    if ((int)threadIdx.x + q * SP_THREADS < n) s.all_few[threadIdx.x + q * SP_THREADS] = x[q];
-  __syncthreads();
-  sort_few<SP_FEW / SP_THREADS>(s.all_few, n, s.bins[1]);
-  if (threadIdx.x == 0) s.found_at = n - 1;
-  __syncthreads();
-  u64 w[2];
-  const int i0 = 2 * threadIdx.x;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    x[q] = i0 + q < n ? s.all_few[i0 + q] : 0;
+  for (int q = 0; q < OWN; ++q) {
+    x[q] = i0 + q < n ? few[i0 + q] : 0;
     w[q] = i0 + q < n ? weight(value_of<T>((uint32_t)(x[q] >> 32))) : 0;
-  }
-  u64 run = h.above_mass + mass_before(w[0] + w[1]);
-  const u64 before = run;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    if (i0 + q < n && !reached(goal, want, run, h.above + i0 + q) && reached(goal, want, run + w[q], h.above + i0 + q + 1))
-      s.found_at = i0 + q;
     run += w[q];
   }
-  __syncthreads();
-  const int at = (int)s.found_at - i0;
-  if (at == 0 || at == 1) {
-    s.found_token = x[at];
-    s.found_mass = before + w[0] + (at ? w[1] : 0);
-    s.found_w = w[at];
+  run = h.above_mass + mass_before(run);
+  auto place = [&](int q) {
+    s.found_token = x[q];
+    s.found_mass = run;
+    s.found_w = w[q];
+  };
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    const bool yet = reached(goal, want, run, h.above + i0 + q);
+    run += w[q];
+    const bool now = reached(goal, want, run, h.above + i0 + q + 1);
+    if ((i0 + q < n && !yet && now) || (i0 + q == n - 1 && !now)) place(q);
   }
   __syncthreads();
   *cut = {s.found_token, s.found_mass, s.found_w};
@@ -988,7 +1031,6 @@ template <typename T, bool ALIGNED, class S>
 __device__ __noinline__ void pick_by_keys(const T* row, Share part, Coarse coarse, RowState r, Weights weight,
                                           int* token, float* prob) {
   constexpr int RANKS = S::RANKS;
-  fill_coarse<T, ALIGNED, S>(row, part, coarse, weight, r.top_k != 0);
   // the kept prefix: the tokens above `key` and the first `equal` of those with it, of mass `mass`
   uint32_t key = 0, equal = 0xFFFFFFFFu;
   u64 mass = r.mass, w = 0;
@@ -1048,7 +1090,10 @@ __device__ __noinline__ void pick_by_search(const T* row, Share part, RowState r
       return;
     }
   }
-  if constexpr (S::RANKS == 1) part = {0, part.to, false};
+  if (S::RANKS == 1 && part.listed) {
+    part.listed = false;
+    fill_coarse<T, ALIGNED, S>(row, part, coarse, weight, r.top_k != 0);
+  }
   pick_by_keys<T, ALIGNED, S>(row, part, coarse, r, weight, token, prob);
 }
 
@@ -1195,7 +1240,7 @@ template <typename T, int OWN>
 __device__ __noinline__ void pick_from_list(RowState r, Weights weight, int* token, float* prob) {
   SampleSmem& s = smem<SampleSmem>();
   const int n = (int)s.n_list, i0 = OWN * threadIdx.x;
-  sort_few<OWN>(s.list, n, s.bins[1]);
+  sort_few<OWN>(s.list, n, weight.id_bits, s.bins[1]);
   u64 run[OWN + 1];  // the sums up to each token
   run[0] = 0;
   int heavy = 0;
@@ -1335,7 +1380,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
       }
       prob = 1.f;
     } else {
-      const Weights weight(m, t, min(62 - (32 - __clz(vocab - 1)), SEG_FRAC));
+      const Weights weight(m, t, vocab);
       r.low = key_of<T>(weight.zlow);
       r.top_k = top_k > 1 && top_k < vocab ? top_k : 0;
       r.top_p = top_p;
@@ -1424,7 +1469,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_search(SampleArgs a, c
   __syncthreads();
   const RowState r = jobs[n].row;
   const float t = a.temperature ? __ldg(a.temperature + n) : a.temperature0;
-  const Weights weight(jobs[n].m, t, min(62 - (32 - __clz(a.vocab - 1)), SEG_FRAC));
+  const Weights weight(jobs[n].m, t, a.vocab);
   int token;
   float prob;
   pick_by_search<T, ALIGNED, SearchSmem>(static_cast<const T*>(a.logits) + n * a.ld,
