@@ -1123,8 +1123,8 @@ __device__ __forceinline__ void each_group(const float* gmax, int n_groups, F f)
   }
 }
 
-// The lower edge of the histogram bin that holds the k-th largest of the groups' maxima, of which the smallest above
-// -inf has the key lo: at least k tokens reach it.  0 where fewer than k groups are above -inf.
+// The lower edge of the histogram bin that holds the k-th largest of the groups' maxima (of the list, without them),
+// of which the smallest above -inf has the key lo: at least k tokens reach it.  0 where fewer than k are above -inf.
 template <typename T>
 __device__ __noinline__ uint32_t bound_by_count(const float* gmax, int n_groups, uint32_t lo,
                                                 uint32_t top, uint32_t k) {
@@ -1134,10 +1134,15 @@ __device__ __noinline__ uint32_t bound_by_count(const float* gmax, int n_groups,
   for (int b = threadIdx.x; b < SP_BINS; b += SP_THREADS) s.group_count[b] = 0;
   if (threadIdx.x == 0) s.bin = -1;
   __syncthreads();
-  each_group(gmax, n_groups, [&](float z, int) {
-    const uint32_t x = key_of<T>(z);
-    if (x >= lo) atomicAdd(&s.group_count[(top - x) >> sh], 1u);
-  });
+  if (gmax) {
+    each_group(gmax, n_groups, [&](float z, int) {
+      const uint32_t x = key_of<T>(z);
+      if (x >= lo) atomicAdd(&s.group_count[(top - x) >> sh], 1u);
+    });
+  } else {
+    for (int i = threadIdx.x; i < (int)s.n_list; i += SP_THREADS)
+      atomicAdd(&s.group_count[(top - (uint32_t)(s.list[i] >> 32)) >> sh], 1u);
+  }
   __syncthreads();
   uint32_t c = 0;
   const int b0 = threadIdx.x * OWN;
@@ -1225,6 +1230,25 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
   }
   __syncthreads();
   return s.n_list <= SP_LIST;
+}
+
+// Leaves those of the list whose keys reach `lo`.
+__device__ __noinline__ void shorten_list(uint32_t lo) {
+  SampleSmem& s = smem<SampleSmem>();
+  constexpr int OWN = SP_LIST / SP_THREADS;
+  u64 x[OWN];
+#pragma unroll
+  for (int q = 0; q < OWN; ++q) {
+    const int i = threadIdx.x + q * SP_THREADS;
+    x[q] = i < (int)s.n_list ? s.list[i] : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.n_list = 0;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < OWN; ++q)
+    if (x[q] && (uint32_t)(x[q] >> 32) >= lo) s.list[atomicAdd(&s.n_list, 1u)] = x[q];
+  __syncthreads();
 }
 
 // The mass of the list.
@@ -1426,7 +1450,11 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
         uint32_t lo = r.top_k ? 0 : r.least;
         if (r.top_k && r.top_k <= n_groups)
           lo = bound_by_count<T>(gmax, n_groups, key_of<T>(least_max), r.top, (uint32_t)r.top_k);
-        listed = list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, max(lo, r.low));
+        lo = max(lo, r.low);
+        listed = list_tokens<T, ALIGNED>(row, vocab, gmax, n_groups, lo);
+        // more tokens than are sorted: only the first top_k of them count (512 rows of top-k 1000: 92 us searched)
+        if (listed && s.n_list > SP_SORT && r.top_k && r.top_k < SP_SORT)
+          shorten_list(bound_by_count<T>(nullptr, 0, lo, r.top, (uint32_t)r.top_k));
       }
       if (listed && s.n_list <= SP_SORT) {
         // (a token to a thread where that does: 512 rows of 50 tokens 46 us, 48 with four)
