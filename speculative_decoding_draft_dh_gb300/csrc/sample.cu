@@ -863,7 +863,7 @@ __device__ __noinline__ u64 mass_of_heavy(const T* row, Share part, u64 w_min, u
 // The first n <= OWN SP_THREADS of `a` (shared memory) in descending order; they are distinct.  A few are ranked among
 // one another; more are counted by ranges of their keys first, of one key by ranges of ids, so that most ranges have a
 // token or none, and then ranked among their range's.  (100 tokens: 1 us by ranks, 2 by ranges; 565: 6 by ranks, 2 by ranges.)
-template <int OWN>
+template <typename T, int OWN>
 __device__ __forceinline__ void sort_few(u64* a, int n, int id_bits, Bins& bins) {
   Scratch& s = smem<Scratch>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -899,12 +899,16 @@ __device__ __forceinline__ void sort_few(u64* a, int n, int id_bits, Bins& bins)
   const u64 range = lane < SP_WARPS ? s.warp_mass[lane] : 0xFFFFFFFFull;
   lo = __reduce_min_sync(0xFFFFFFFFu, (uint32_t)range);
   hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(range >> 32));
+  // by keys and ids where a bin has one key, else by values: a wide range's keys are mostly those of numbers near 0
   const int sh = bin_shift(lo, hi), more = max(11 - (32 - __clz(hi - lo)), 0), id_sh = max(id_bits - more, 0);
+  const float largest = value_of<T>(hi), reach = largest - value_of<T>(lo);
+  const float per_bin = reach < INFINITY ? (SP_BINS - 1) / reach : 0.f;
   uint32_t at[OWN], slot[OWN];
 #pragma unroll
   for (int q = 0; q < OWN; ++q) {
-    at[q] = (hi - (uint32_t)(x[q] >> 32)) >> sh;
-    if (more) at[q] = (at[q] << more) + ((~(uint32_t)x[q]) >> id_sh);
+    const uint32_t key = (uint32_t)(x[q] >> 32);
+    if (sh == 0) at[q] = ((hi - key) << more) + (~(uint32_t)x[q] >> id_sh);
+    else at[q] = min((uint32_t)((largest - value_of<T>(key)) * per_bin), SP_BINS - 1u);
     if ((int)threadIdx.x + q * SP_THREADS < n) slot[q] = atomicAdd(&bins.count[at[q]], 1u);
   }
   __syncthreads();
@@ -999,7 +1003,7 @@ __device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Hi
     cluster_sync();  // the other blocks' have been read
   }
   if (n > SP_FEW) return false;
-  sort_few<OWN>(few, n, weight.id_bits, s.bins[1]);
+  sort_few<T, OWN>(few, n, weight.id_bits, s.bins[1]);
   const int i0 = OWN * threadIdx.x;
   u64 run = 0;
 #pragma unroll
@@ -1266,7 +1270,7 @@ template <typename T, int OWN>
 __device__ __noinline__ void pick_from_list(RowState r, Weights weight, int* token, float* prob) {
   SampleSmem& s = smem<SampleSmem>();
   const int n = (int)s.n_list, i0 = OWN * threadIdx.x;
-  sort_few<OWN>(s.list, n, weight.id_bits, s.bins[1]);
+  sort_few<T, OWN>(s.list, n, weight.id_bits, s.bins[1]);
   u64 run[OWN + 1];  // the sums up to each token
   run[0] = 0;
   int heavy = 0;
