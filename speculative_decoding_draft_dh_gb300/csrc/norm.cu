@@ -63,62 +63,92 @@ __device__ __forceinline__ Moments moments(float mean0, float2 q, float inv_d, f
   return {mean0, delta, 1.f / sqrtf(var + eps)};
 }
 
-// Rows on their way: SLOTS rows in shared memory, of which a thread copies its own vectors by cp.async and reads them
-// itself, so that no barrier is needed.  Copies are 16 bytes (VEC) or 4 (fp32 rows of any alignment); bf16 rows off
-// 16 bytes are loaded when they are used.
+// Rows on their way: SLOTS rows in shared memory.  A thread copies its own vectors by cp.async and reads them itself, so
+// that no barrier is needed: 16 bytes each (VEC) or 4 (fp32 rows of any alignment).  Of bf16 rows of any alignment a
+// warp copies the 16-byte words that hold its columns, and a thread reads its elements from there (20000 rows of 8191:
+// see k_norm and k_norm_backward).
 template <typename T, bool VEC, int NV>
 struct Ring {
   using C = Cols<T, VEC, NV>;
-  static constexpr bool COPIED = VEC || sizeof(T) == 4;
+  static constexpr bool WORDS = !VEC && sizeof(T) == 2;
   static constexpr int COPIES = VEC ? NV : NV * C::PER;  // of a thread and row
   static constexpr int STEP = VEC ? 32 * C::PER : 32;    // columns between them
+  static constexpr int REGION = NV * 512 + (WORDS ? 16 : 0);  // bytes of a warp
   uint32_t mine;  // this thread's place in slot 0, a shared-memory address
   uint32_t slot;  // bytes of a slot
-  int held;       // copies within the row
-  int first;      // this thread's first column (0 where it has none)
+  int held;       // copies within the row (WORDS: columns of the warp)
+  int first;      // this thread's (WORDS: its warp's) first column, 0 where it has none
   __device__ __forceinline__ Ring(void* smem, int me, int d)
-      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * (NV * 512) + (threadIdx.x & 31) * 16),
-        slot(blockDim.x * NV * 16), held(min(max((d - C::col(me, 0, 0) + STEP - 1) / STEP, 0), COPIES)),
-        first(held ? C::col(me, 0, 0) : 0) {}
-  static constexpr __host__ __device__ size_t bytes(int threads) { return COPIED ? (size_t)NV * threads * 16 : 0; }
+      : mine((uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * REGION + (threadIdx.x & 31) * 16),
+        slot(blockDim.x / 32 * REGION) {
+    const int at = WORDS ? (me >> 5) * C::WARP : C::col(me, 0, 0);
+    held = WORDS ? min(max(d - at, 0), C::WARP) : min(max((d - at + STEP - 1) / STEP, 0), COPIES);
+    first = held ? at : 0;
+  }
+  static constexpr __host__ __device__ size_t bytes(int threads) { return (size_t)(threads / 32) * REGION; }
+  __device__ __forceinline__ static void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
   // A row on its way to slot s (`on`: there is one), from its column `first` on.  A group of copies.
   __device__ __forceinline__ void fetch(const T* mine_of_row, bool on, int s) const {
-    if constexpr (COPIED) {
-      const uint32_t to = mine + s * slot;
-      if (on) {
+    const uint32_t to = mine + s * slot;
+    if constexpr (WORDS) {
+      __syncwarp();  // the slot has been read
+      if (on && held) {
+        const int before = (int)(reinterpret_cast<uintptr_t>(mine_of_row) & 15u), lane = threadIdx.x & 31;
+        const char* word = reinterpret_cast<const char*>(mine_of_row) - before;
+        const int end = before + held * 2;
 #pragma unroll
-        for (int k = 0; k < COPIES; ++k) {
-          if constexpr (VEC) {
-            // past the row's end: zeros, and the address is not used
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * 512),
-                         "l"(mine_of_row + (k < held ? k * STEP : 0)), "r"(k < held ? 16 : 0)
-                         : "memory");
-          } else {
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (k / 4) * 512 + (k % 4) * 4),
-                         "l"(mine_of_row + (k < held ? k * STEP : 0)), "r"(k < held ? 4 : 0)
-                         : "memory");
-          }
+        for (int k = 0; k < NV; ++k)
+          if ((lane + 32 * k) * 16 < end) copy16(to + k * 512, word + (lane + 32 * k) * 16);
+        if (lane == 0 && NV * 512 < end) copy16(to + NV * 512, word + NV * 512);
+      }
+    } else if (on) {
+#pragma unroll
+      for (int k = 0; k < COPIES; ++k) {
+        if constexpr (VEC) {
+          // past the row's end: zeros, and the address is not used
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * 512),
+                       "l"(mine_of_row + (k < held ? k * STEP : 0)), "r"(k < held ? 16 : 0)
+                       : "memory");
+        } else {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (k / 4) * 512 + (k % 4) * 4),
+                       "l"(mine_of_row + (k < held ? k * STEP : 0)), "r"(k < held ? 4 : 0)
+                       : "memory");
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  // Waits for this thread's copies, up to the LATER youngest groups.
+  // Waits for this thread's copies (WORDS: its warp's), up to the LATER youngest groups.
   template <int LATER>
   __device__ __forceinline__ void wait() const {
-    if constexpr (COPIED) asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+    if constexpr (WORDS) __syncwarp();
   }
   // Vector v of the row in slot s.
-  __device__ __forceinline__ uint4 get(const T* row, int s, int v, int me, int d) const {
-    if constexpr (COPIED) {
+  __device__ __forceinline__ uint4 get(const T* row, int s, int v) const {
+    if constexpr (WORDS) {
+      const int lane = threadIdx.x & 31;
+      const uint32_t at = mine + s * slot - lane * 16 + (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < C::PER; ++e) {
+        const int i = (v * C::PER + e) * 32 + lane;
+        if (i < held) {
+          unsigned short x;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + i * 2) : "memory");
+          w[e / 2] |= (uint32_t)x << (16 * (e & 1));
+        }
+      }
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
       uint4 u;
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                    : "r"(mine + s * slot + v * 512)
                    : "memory");
       return u;
-    } else {
-      return C::load(row, me, v, d);
     }
   }
 };
@@ -276,7 +306,7 @@ __global__ void __maxnreg__(norm_regs(NV)) k_norm(NormArgs a, int width) {
     f32x2 z[NV][HALF];
     ring.template wait<NF_STAGES - 2>();
 #pragma unroll
-    for (int v = 0; v < NV; ++v) unpack_pairs<T>(ring.get(row, stage, v, me, a.d), z[v]);
+    for (int v = 0; v < NV; ++v) unpack_pairs<T>(ring.get(row, stage, v), z[v]);
     ring.fetch(next, n + (NF_STAGES - 1) * step < rows, stage == 0 ? NF_STAGES - 1 : stage - 1);
     next += x_step;
     row += x_step;
@@ -422,8 +452,8 @@ __global__ void __maxnreg__(NB_REGS) k_norm_backward(NormArgs a, int width, bool
     // x - mean and g of vector v of row i; past the row's end g is 0 and x - mean counts for nothing
     auto terms = [&](int i, int v, f32x2* z, f32x2* q) {
       const f32x2 shift = both(-st[i].x);
-      unpack_pairs<T>(ring.get(x_row + i * a.ld, (stage * R + i) * 2, v, me, a.d), z);
-      unpack_pairs<T>(ring.get(g_row + i * a.grad_ld, (stage * R + i) * 2 + 1, v, me, a.d), q);
+      unpack_pairs<T>(ring.get(x_row + i * a.ld, (stage * R + i) * 2, v), z);
+      unpack_pairs<T>(ring.get(g_row + i * a.grad_ld, (stage * R + i) * 2 + 1, v), q);
 #pragma unroll
       for (int e = 0; e < HALF; ++e) z[e] = add2(z[e], shift);
     };
@@ -699,7 +729,7 @@ cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
   if (few)
     return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false>, (unsigned)a.N, (unsigned)width, ring, a, width);
   long long groups = least(1024, 65536 / norm_regs(NV)) / width;
-  if (ring && shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
+  if (shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
   groups = least(groups < 1 ? 1 : groups, 15);  // a barrier each
   const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
   return launch_ring(c, "norm", k_norm<T, P, NV, VEC, true>, grid, (unsigned)(width * groups), shared + ring * groups, a,
@@ -730,7 +760,7 @@ cudaError_t run_backward_nv(const Ctx& c, NormArgs& a, bool sums, JoinPlan* join
   const size_t ring = NB_STAGES * 2 * R * Ring<T, VEC, NV>::bytes(width), shared = SharedParams<T, P, VEC, NV>::bytes(width);
   const long long units = ((long long)a.N + R - 1) / R;
   long long groups = NB_THREADS / width;
-  if (ring && shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
+  if (shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
   groups = least(groups < 1 ? 1 : groups, 15);  // a barrier each
   // few rows: on as many SMs as there are
   if (units < c.num_sms * groups) groups = (units + c.num_sms - 1) / c.num_sms;
