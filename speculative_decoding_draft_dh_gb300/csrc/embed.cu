@@ -2,7 +2,7 @@
 // dh_embed_backward in dh.h).
 //
 // Lookup: out[n] = scale table[token[n]].  Nothing but the copy's traffic: a thread moves VECS vectors of 16
-// bytes, all loads issued before the first store.
+// bytes, all loads issued before the first store.  32768 rows of 5120 bf16 in 75 us: 455 MB at 6.1 TB/s.
 //
 // Gradient: grad[v] = scale sum over the n with token[n] = v, in fp32.  The positions are first sorted by
 // (token, n), so that a row's terms stand together and are added in one fixed order, without atomics on
@@ -13,7 +13,10 @@
 //                  lies within its chunk is summed and written; of a run that leaves its chunk, the part is
 //                  written to the workspace.  More blocks write the zeros of the rows that do not occur.
 //   k_embed_join   adds the parts of the runs that span chunks, in order.
-// The split by chunks of pairs, not by rows, keeps the work even however often one token comes.
+// The split by chunks of pairs, not by rows, keeps the work even however often one token comes.  The bound is HBM,
+// most of it the zeros of the rows that do not occur: 32768 tokens of 5120 bf16 into 151936 rows, 1.9 GB, in 287 us
+// (6.5 TB/s), of which the sort takes 20.  Of fewer tokens the sort is the larger part: 20011 of 1001 fp32 into 4096
+// rows 41 us, sort 16.
 #include <type_traits>
 
 #include "layers.cuh"
@@ -23,6 +26,8 @@ namespace dh {
 namespace {
 
 constexpr int EM_THREADS = 256;
+// 4 for long calls: 32768 rows of 5120 bf16 75 us, 79 with 2, 78 with 8.  1 where the blocks of such a call are few for
+// the SMs: 8 rows 1.2 us, 1.8 with 4.
 constexpr int EM_VECS = 4;
 
 // Pieces of a row that is written: its 16-byte words in memory, of which the first and the last may hold elements of
@@ -70,18 +75,18 @@ __device__ __forceinline__ void store_piece(T* row, int col, int d, const uint4&
 }
 
 // A unit is 16 bytes of a row, with all rows starting on 16 bytes (VEC), else a piece; `units` of them make a row.
-template <typename T, bool VEC>
+template <typename T, bool VEC, int VECS>
 __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned units) {
   constexpr int PER = Elem<T>::PER16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const T* table = static_cast<const T*>(a.src);
   T* out = static_cast<T*>(a.dst);
   const unsigned long long items = (unsigned long long)a.N * units;
-  const unsigned long long i0 = (unsigned long long)blockIdx.x * (EM_THREADS * EM_VECS) + threadIdx.x;
-  uint4 x[EM_VECS];
-  int row[EM_VECS], at[EM_VECS];
+  const unsigned long long i0 = (unsigned long long)blockIdx.x * (EM_THREADS * VECS) + threadIdx.x;
+  uint4 x[VECS];
+  int row[VECS], at[VECS];
 #pragma unroll
-  for (int q = 0; q < EM_VECS; ++q) {
+  for (int q = 0; q < VECS; ++q) {
     const unsigned long long i = i0 + q * EM_THREADS;
     row[q] = -1;
     if (i < items) {
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned unit
     }
   }
 #pragma unroll
-  for (int q = 0; q < EM_VECS; ++q) {
+  for (int q = 0; q < VECS; ++q) {
     if (row[q] < 0) continue;
     if (a.scale != 1.f) {
       float z[PER];
@@ -135,11 +140,13 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t dg, bool on) {
   return same;
 }
 
-// Sorts (token, n) by token, stable in n, into buf0 after an odd number of passes, else buf1; tokens outside [0, vocab) get the key
-// vocab and so come last.  A least-significant-digit radix sort: each warp owns a contiguous run of pairs, counts
-// its digits, and after an exclusive scan over (digit, block, warp) places its pairs in order.  What bounds it are
-// latencies, so a warp's loads are issued TS_ITEMS at a time, and up to that many pairs per lane stay in registers
-// between counting and placing.
+// Sorts (token, n) by token, stable in n, into buf0 after an odd number of passes, else buf1; tokens outside
+// [0, vocab) get the key vocab and so come last.  A least-significant-digit radix sort: each warp owns a contiguous
+// run of pairs, counts its digits, and after an exclusive scan over (digit, block, warp) places its pairs in order.
+// What bounds it are latencies: of the passes, as few as digits of 9 bits allow (the counts of 32 warps fit shared
+// memory), and of memory, so that a warp's loads are issued TS_ITEMS at a time, and up to that many pairs per lane
+// stay in registers between counting and placing.  One cluster, since a pass then costs two cluster barriers and no
+// launch: 32768 tokens of 18 bits in 22 us by 8 blocks, in 107 by one; 300 tokens 1.5 us less by one block.
 template <int BITS>
 __global__ void __launch_bounds__(TS_THREADS) k_token_sort(const int32_t* __restrict__ tokens, int N, int vocab,
                                                            int passes, uint2* __restrict__ buf0,
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(TS_THREADS) k_token_sort(const int32_t* __rest
 
 constexpr int EG_THREADS = 128;
 constexpr int EG_CHUNK = 64;   // pairs of a chunk, at most
-constexpr int EG_AHEAD = 8;    // loads of a thread in flight
+constexpr int EG_AHEAD = 8;    // loads of a thread in flight (32768 tokens of 5120 bf16: 287 us, 298 with 4)
 constexpr int EG_ZERO_ROWS = 8;
 
 struct GradPlan {
@@ -428,7 +435,8 @@ __global__ void __launch_bounds__(32 * EJ_WARPS) k_embed_join(EmbedArgs a, GradP
   }
 }
 
-// Pairs per chunk: 64, fewer where that leaves SMs without a block.
+// Pairs per chunk: 64, fewer where that leaves SMs without a block.  (1001 columns of fp32, with 64, 16 and 8 in a
+// chunk: 2000 tokens 25, 17.1 and 16.5 us, 5000 tokens 29, 20.2 and 22.6, 20011 tokens 40.5, 44 and 54.)
 int chunk_of(int N) { return N >= 64 * 304 ? 64 : N >= 16 * 304 ? 16 : 8; }
 
 // Columns of a part, whole tiles of either type.
@@ -460,9 +468,12 @@ cudaError_t run_embed(const Ctx& c, const EmbedArgs& a) {
                    whole_vectors(a.dst, a.dst_ld, a.N, a.d, sizeof(T));
   const unsigned units = vec ? (unsigned)(a.d / PER) : (unsigned)pieces(a.d, PER);
   const unsigned long long items = (unsigned long long)a.N * units;
-  const unsigned grid = (unsigned)((items + EM_THREADS * EM_VECS - 1) / (EM_THREADS * EM_VECS));
-  return launch_pdl(c, "embed", vec ? k_embed<T, true> : k_embed<T, false>, dim3(grid), dim3(EM_THREADS), 0, a,
-                    units);
+  const bool few = items <= (unsigned long long)EM_THREADS * EM_VECS * c.num_sms;
+  const unsigned each = EM_THREADS * (few ? 1 : EM_VECS), grid = (unsigned)((items + each - 1) / each);
+  return launch_pdl(c, "embed",
+                    few ? (vec ? k_embed<T, true, 1> : k_embed<T, false, 1>)
+                        : (vec ? k_embed<T, true, EM_VECS> : k_embed<T, false, EM_VECS>),
+                    dim3(grid), dim3(EM_THREADS), 0, a, units);
 }
 
 // No tokens: rows of zeros.

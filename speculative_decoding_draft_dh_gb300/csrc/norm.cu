@@ -1,9 +1,12 @@
 // Layer norm over the last dimension, and its gradients (definitions at dh_layer_norm and
 // dh_layer_norm_backward in dh.h).
 //
-// The bound is HBM: a row is read once, held in registers, and written once.  A row belongs to a warp (up to 128
-// vectors of 16 bytes) or to a block; the groups walk over the rows and load their next row before they reduce
-// the present one.
+// The bound is HBM: a row is read once and written once.  A row belongs to a group of threads, a vector of 16 bytes
+// each or up to four; a block's groups walk over rows of their own, with the next rows on their way in shared memory
+// while the present one is reduced in registers.  Once the memory is kept busy, the instructions count: they are
+// packed in pairs, and the parameters wait in shared memory as fp32.  32768 rows of 5120 bf16: forward 104 us
+// (671 MB, 6.5 TB/s), backward 173 (1.0 GB, 5.8 TB/s).  (The next rows in registers instead: 154 to 215 and 312 to 587;
+// the parameters by way of L1: up to 313 backward.)
 // Forward: the mean first, then the sums of x - mean and of its square, so that the variance loses nothing to a
 // mean far from 0 (the two-pass form with the correction of Chan, Golub and LeVeque).
 // Backward: with xhat = (x - mean) rstd and h = g w,
@@ -11,7 +14,7 @@
 // A thread keeps its columns over all rows that its group walks, so dw and db are summed in its registers;
 // blocks leave their sums in the workspace and a second kernel adds them in order.
 // Rows of more than NM_HELD columns are read again for each step instead, by k_norm_wide and
-// k_norm_backward_wide, and k_norm_columns sums their dw and db.
+// k_norm_backward_wide, and k_norm_columns sums their dw and db (10000 rows of 12288 bf16: 217 us and 453).
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -63,10 +66,10 @@ __device__ __forceinline__ Moments moments(float mean0, float2 q, float inv_d, f
   return {mean0, delta, 1.f / sqrtf(var + eps)};
 }
 
-// Rows on their way: SLOTS rows in shared memory.  A thread copies its own vectors by cp.async and reads them itself, so
-// that no barrier is needed: 16 bytes each (VEC) or 4 (fp32 rows of any alignment).  Of bf16 rows of any alignment a
-// warp copies the 16-byte words that hold its columns, and a thread reads its elements from there (20000 rows of 8191:
-// see k_norm and k_norm_backward).
+// Rows on their way: SLOTS rows in shared memory.  A thread copies its own vectors by cp.async and reads them itself,
+// so that no barrier is needed: 16 bytes each (VEC) or 4 (fp32 rows of any alignment).  Of bf16 rows off 16 bytes a
+// warp copies the 16-byte words that hold its columns, and a thread reads its elements from there (20000 rows of 8191
+// forward 171 us, backward 335; loaded element by element when they are used 283 and 412).
 template <typename T, bool VEC, int NV>
 struct Ring {
   using C = Cols<T, VEC, NV>;
@@ -249,7 +252,7 @@ __device__ __forceinline__ float pair_sum(f32x2 v) {
   return a + b;
 }
 
-constexpr int NF_STAGES = 3;
+constexpr int NF_STAGES = 3;  // 32768 rows of 5120 bf16: 104 us, 109 with 2, 103 with 4
 constexpr int NF_WARPS = 16;  // of a row, at most
 // Registers of a thread with NV vectors.
 constexpr int norm_regs(int nv) { return nv == 1 ? 64 : nv == 2 ? 80 : 128; }
@@ -388,9 +391,10 @@ __global__ void __maxnreg__(norm_regs(NV)) k_norm(NormArgs a, int width) {
 }
 
 constexpr int NB_REGS = 128, NB_THREADS = 65536 / NB_REGS;
-constexpr int NB_STAGES = 2;
+constexpr int NB_STAGES = 2;  // 3 leave room for fewer groups: 32768 rows of 5120 bf16 251 us instead of 173
 // Groups of threads as in k_norm, each on R rows at a time (2 of bf16, 1 of fp32), so that their exchanges and the
-// weights are shared.
+// weights are shared.  One block of 512 threads to an SM, so that a thread has 128 registers for its columns' sums
+// (two blocks of half the groups: 184 us instead of 173).
 template <typename T, typename P, int NV, bool VEC>
 __global__ void __maxnreg__(NB_REGS) k_norm_backward(NormArgs a, int width, bool sums) {
   constexpr int R = sizeof(T) == 4 ? 1 : 2;
@@ -707,7 +711,8 @@ cudaError_t allow_ring(const void* kernel, int device) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             (int)cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return note_error(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
   done.emplace_back(kernel, device);
   return cudaSuccess;
@@ -725,25 +730,28 @@ constexpr int SM_SMEM = 220 * 1024;  // of an SM's shared memory, for the rings 
 template <typename T, typename P, bool VEC, int NV>
 cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
   const int width = round32((nvec + NV - 1) / NV);
-  const size_t ring = NF_STAGES * Ring<T, VEC, NV>::bytes(width), shared = 2 * SharedParams<T, P, VEC, NV>::bytes(width);
+  const size_t ring = NF_STAGES * Ring<T, VEC, NV>::bytes(width);
+  const size_t shared = 2 * SharedParams<T, P, VEC, NV>::bytes(width);
   if (few)
     return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false>, (unsigned)a.N, (unsigned)width, ring, a, width);
   long long groups = least(1024, 65536 / norm_regs(NV)) / width;
   if (shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
   groups = least(groups < 1 ? 1 : groups, 15);  // a barrier each
   const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
-  return launch_ring(c, "norm", k_norm<T, P, NV, VEC, true>, grid, (unsigned)(width * groups), shared + ring * groups, a,
-                     width);
+  return launch_ring(c, "norm", k_norm<T, P, NV, VEC, true>, grid, (unsigned)(width * groups), shared + ring * groups,
+                     a, width);
 }
 
 template <typename T, typename P, bool VEC>
 cudaError_t run_norm(const Ctx& c, const NormArgs& a) {
   constexpr int PER = Elem<T>::PER16;
   const int nvec = (a.d + PER - 1) / PER;
-  // one row per block and no parameters in shared memory where there are few rows
+  // one row per block and no parameters in shared memory where there are few rows (5120 bf16: 8 rows 2.5 us, 3.6 as
+  // many rows are done; 304 rows 3.1 and 3.8; 608 rows 5.7 and 5.2)
   const bool few = a.N <= 2 * c.num_sms;
   if (nvec <= 32) return run_norm_nv<T, P, VEC, 1>(c, a, nvec, few);
   if (nvec <= 64 || (few && nvec <= 2 * 32 * NF_WARPS)) return run_norm_nv<T, P, VEC, 2>(c, a, nvec, few);
+  // (32768 rows of 5120 bf16 with 2 vectors per thread 121 us instead of 104, with 8 129)
   return run_norm_nv<T, P, VEC, 4>(c, a, nvec, few);
 }
 
@@ -757,7 +765,8 @@ template <typename T, typename P, bool VEC, int NV>
 cudaError_t run_backward_nv(const Ctx& c, NormArgs& a, bool sums, JoinPlan* join, int nvec) {
   constexpr int PER = Elem<T>::PER16, R = sizeof(T) == 4 ? 1 : 2;
   const int width = round32((nvec + NV - 1) / NV);
-  const size_t ring = NB_STAGES * 2 * R * Ring<T, VEC, NV>::bytes(width), shared = SharedParams<T, P, VEC, NV>::bytes(width);
+  const size_t ring = NB_STAGES * 2 * R * Ring<T, VEC, NV>::bytes(width);
+  const size_t shared = SharedParams<T, P, VEC, NV>::bytes(width);
   const long long units = ((long long)a.N + R - 1) / R;
   long long groups = NB_THREADS / width;
   if (shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
@@ -780,6 +789,8 @@ cudaError_t run_norm_backward(const Ctx& c, NormArgs& a, bool sums, JoinPlan* jo
     if (nvec <= 512) return run_backward_nv<T, P, VEC, 2>(c, a, sums, join, nvec);
     return run_backward_nv<T, P, VEC, 4>(c, a, sums, join, nvec);
   } else {
+    // two vectors per thread, or three where whole groups of two would leave more than a fifth of the threads out
+    // (32768 rows of 5120: 189 us with two, 173 with three; of 1024: 39 and 53; of 2048: 65 and 76)
     const int two = round32((nvec + 1) / 2), three = round32((nvec + 2) / 3);
     if (NB_THREADS / two * two * 5 / 4 >= NB_THREADS / three * three)
       return run_backward_nv<T, P, VEC, 2>(c, a, sums, join, nvec);
@@ -818,8 +829,8 @@ cudaError_t pick_backward(const Ctx& c, NormArgs a) {
     if (sums) {
       const int tiles = (a.d + NC_THREADS - 1) / NC_THREADS, shares = 8 * c.num_sms / tiles;
       join.parts = (int)least(a.N, least(norm_parts(a.d), shares < 1 ? 1 : shares));
-      e = launch_pdl(c, "norm_columns", k_norm_columns<T>, dim3((unsigned)tiles, (unsigned)join.parts), dim3(NC_THREADS), 0,
-                     a);
+      e = launch_pdl(c, "norm_columns", k_norm_columns<T>, dim3((unsigned)tiles, (unsigned)join.parts),
+                     dim3(NC_THREADS), 0, a);
     }
     if (e == cudaSuccess && a.y)
       e = launch_pdl(c, "norm_backward", k_norm_backward_wide<T, P>, dim3(least(a.N, 2LL * c.num_sms)),

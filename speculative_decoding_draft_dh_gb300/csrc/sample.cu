@@ -5,14 +5,21 @@
 // one at which the prefix's running sum of weights passes u times its mass.  So a token far down the order matters
 // only by its share of the row's mass, and that only where no top-k leaves it out.
 //   k_sample_scan   the one pass over the logits: the largest of every group of 16 vectors and, of rows whose mass
-//                   is needed, every segment's mass.  Its bound is HBM; with masses, the instructions of the weights.
+//                   is needed, every segment's mass.  A warp takes a segment of 64 vectors, so that rows of any
+//                   number fill the SMs.  Its bound is HBM (512 rows of 151936 bf16: 25 us, 156 MB at 6.2 TB/s);
+//                   with masses, the 25 instructions of a weight (72 us, the issue slots 74% full).
 //   k_sample_pick   a block per row.  A bound below which nothing can be drawn: the top_k-th largest group maximum,
-//                   or a histogram of masses.  The tokens that reach it are listed, sorted, weighted and summed, and
-//                   the filters and the draw are places in that list.
-// Rows whose list would not fit are searched instead: a histogram (counts and masses) over a range of
-// order-preserving keys, the bin that holds the place, then that bin's keys, until one key is left; tokens of one
-// key have one weight, so the place among them is a division, and their order is that of the ids.
-// Rows of few segments are scanned by the block that picks, in one launch.
+//                   or, of rows whose mass is needed, that of the SP_TRY-th, if what is above holds the mass.  The
+//                   tokens that reach it are listed, sorted, weighted and summed, and the filters and the draw are
+//                   places in that list.  Its bound is the chain of a block's steps, 5 us in one row.
+//   k_sample_search the rows whose list would be too long, each by a cluster: a histogram of masses over all
+//                   logits, then for each place (of top-k, of top-p, of the draw) the bin that holds it and that
+//                   bin's tokens, sorted as a list's.  Where thousands of tokens are equal, or nearly, a bin's tokens
+//                   by ranges of their keys instead, until one key is left: its tokens have one weight, so the place
+//                   among them is a division, and their order is that of the ids.  Its bound is shared memory's
+//                   atomics, two or three of a logit (one flat row 30 us).
+// Rows of few segments are scanned by the block that picks, in one launch; rows that the host knows to need no mass
+// are searched there too, should they have to be, and a call has two launches.
 //
 // Which token a uniform falls on hangs on the running sums, so the weights exp((z - max)/T) are integers: fixed
 // point with `frac` fraction bits relative to a power of two near the largest, frac = 62 - log2(vocab) (52 at most),
@@ -227,7 +234,8 @@ __device__ __forceinline__ void scan_segment(const T* row, int sgi, int vocab, f
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   const Rate c(t);
-  const float ch = c.hi, cl = c.lo, reach = (float)(SEG_FRAC + 2) / ch;  // what is lower than m by that much counts as 0
+  // (what is lower than m by `reach` counts as 0)
+  const float ch = c.hi, cl = c.lo, reach = (float)(SEG_FRAC + 2) / ch;
   u64 sum = 0;
   int e_ref = -0x40000000;
   // beyond, and so beyond the limits of Weights: the row's weights are taken in 64 bits by the block that picks, or
@@ -275,7 +283,8 @@ constexpr int SC_THREADS = 256;
 constexpr int SC_BLOCKS = 5;  // of an SM
 
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(SC_THREADS, SC_BLOCKS) k_sample_scan(SampleArgs a, int n_seg, float* gmax, SegMass* segs) {
+__global__ void __launch_bounds__(SC_THREADS, SC_BLOCKS) k_sample_scan(SampleArgs a, int n_seg, float* gmax,
+                                                                       SegMass* segs) {
   __shared__ ScanTable tab;
   fill_table(tab, SC_THREADS);
   __syncthreads();
@@ -328,6 +337,8 @@ struct SampleSmem : Scratch {
   };
   u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
 };
+// Blocks of a cluster: 512 flat rows 558 us, one 67, 512 rows at top-p 0.95 189; with 2 433, 81 and 194; with 8 1060,
+// 66 and 199.
 constexpr int SS_RANKS = 4;
 struct SearchSmem : Scratch {
   static constexpr int RANKS = SS_RANKS;
@@ -495,7 +506,8 @@ struct Coarse {
       *from = *to - lo > reach ? *to - reach : lo;
     } else {
       // half a step more on either side covers the roundings
-      const float z1 = (float)(top - 2 * b + 1) / (64.f * weight.c.hi), z0 = (float)(top - 2 * b - 2) / (64.f * weight.c.hi);
+      const float steps = 64.f * weight.c.hi;
+      const float z1 = (float)(top - 2 * b + 1) / steps, z0 = (float)(top - 2 * b - 2) / steps;
       *from = max(lo, min(key_of<T>(z0), hi));
       *to = min(hi, max(key_of<T>(z1), *from));
     }
@@ -842,7 +854,8 @@ __device__ __forceinline__ u64 row_mass(u64 x) {
     }
     cluster_sync();
     mass = 0;
-    for (uint32_t k = 0; k < S::RANKS; ++k) mass += ((u64)ld_cluster(&s.share[1], k) << 32) | ld_cluster(&s.share[0], k);
+    for (uint32_t k = 0; k < S::RANKS; ++k)
+      mass += ((u64)ld_cluster(&s.share[1], k) << 32) | ld_cluster(&s.share[0], k);
     cluster_sync();
   }
   return mass;
@@ -861,8 +874,9 @@ __device__ __noinline__ u64 mass_of_heavy(const T* row, Share part, u64 w_min, u
 }
 
 // The first n <= OWN SP_THREADS of `a` (shared memory) in descending order; they are distinct.  A few are ranked among
-// one another; more are counted by ranges of their keys first, of one key by ranges of ids, so that most ranges have a
-// token or none, and then ranked among their range's.  (100 tokens: 1 us by ranks, 2 by ranges; 565: 6 by ranks, 2 by ranges.)
+// one another; more are counted by ranges of their keys or values first, of one key by ranges of ids, so that most
+// ranges have a token or none, and then ranked among their range's.  (One list of 20: a call of 9.9 us by ranks, 10.4
+// by ranges; 77 lists of 565: 26 us by ranges, 39 by a bitonic network.)
 template <typename T, int OWN>
 __device__ __forceinline__ void sort_few(u64* a, int n, int id_bits, Bins& bins) {
   Scratch& s = smem<Scratch>();
@@ -1194,7 +1208,7 @@ __device__ __noinline__ bool list_tokens(const T* row, int vocab, const float* g
   __syncthreads();
   const uint32_t n = s.n_groups;
   if (n > SP_GROUPS) return false;
-  // two groups to a warp, 16 vectors each, the loads of AHEAD pairs of groups in flight
+  // two groups to a warp, 16 vectors each, the loads of AHEAD pairs of groups in flight (registers for no more)
   constexpr int AHEAD = 4;
   const Within<T> within(from, INFINITY);  // (a row with +inf does not come here)
   for (uint32_t i0 = warp * 2; i0 < n; i0 += SP_WARPS * 2 * AHEAD) {
@@ -1532,7 +1546,8 @@ SampleLayout sample_layout(int N, int vocab, int dtype) {
 // Rows that the host knows to have a small top-k, or temperature 0: their lists are too long only where thousands of
 // tokens are equal, and then the block that picks searches too.  A third kernel would cost the usual call 2 us.
 bool seldom_searched(const SampleArgs& a) {
-  return (!a.temperature && a.temperature0 == 0.f) || (!a.top_k && a.top_k0 >= 1 && a.top_k0 <= 1024 && a.top_k0 < a.vocab);
+  return (!a.temperature && a.temperature0 == 0.f) ||
+         (!a.top_k && a.top_k0 >= 1 && a.top_k0 <= 1024 && a.top_k0 < a.vocab);
 }
 
 template <typename T, bool ALIGNED>
@@ -1552,7 +1567,8 @@ cudaError_t run_sample(const Ctx& c, const SampleArgs& a, int dtype) {
   if (e != cudaSuccess) return e;
   float* gmax = reinterpret_cast<float*>(static_cast<char*>(a.ws) + L.gmax);
   SegMass* segs = reinterpret_cast<SegMass*>(static_cast<char*>(a.ws) + L.segs);
-  const long long want = ((long long)a.N * L.n_seg + SC_THREADS / 32 - 1) / (SC_THREADS / 32), most = (long long)SC_BLOCKS * c.num_sms;
+  const long long want = ((long long)a.N * L.n_seg + SC_THREADS / 32 - 1) / (SC_THREADS / 32);
+  const long long most = (long long)SC_BLOCKS * c.num_sms;
   e = launch_pdl(c, "sample_scan", k_sample_scan<T, ALIGNED>, dim3((unsigned)(want < most ? want : most)),
                  dim3(SC_THREADS), 0, a, L.n_seg, gmax, segs);
   if (e != cudaSuccess) return e;
@@ -1562,8 +1578,8 @@ cudaError_t run_sample(const Ctx& c, const SampleArgs& a, int dtype) {
   static unsigned long long search_done = 0;
   e = allow_max_smem(k_sample_search<T, ALIGNED>, c.device, &search_done);
   if (e != cudaSuccess) return e;
-  return launch_clusters(c, "sample_search", k_sample_search<T, ALIGNED>, SS_RANKS, dim3((unsigned)a.N * SS_RANKS), block,
-                         sizeof(SearchSmem), a, jobs);
+  return launch_clusters(c, "sample_search", k_sample_search<T, ALIGNED>, SS_RANKS, dim3((unsigned)a.N * SS_RANKS),
+                         block, sizeof(SearchSmem), a, jobs);
 }
 
 }  // namespace
