@@ -20,7 +20,12 @@ bool overlap(const void* p, int64_t ps, int64_t n, const void* q, int64_t qs, in
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   const uintptr_t an = ((uintptr_t)(n - 1) * (uintptr_t)ps + (uintptr_t)d) * (uintptr_t)elem;
   const uintptr_t bn = ((uintptr_t)(m - 1) * (uintptr_t)qs + (uintptr_t)d) * (uintptr_t)elem;
-  return a < b + bn && b < a + an;
+  if (!(a < b + bn && b < a + an)) return false;
+  // other columns of the same rows
+  const uintptr_t step = (uintptr_t)ps * (uintptr_t)elem, row = (uintptr_t)d * (uintptr_t)elem;
+  if (ps != qs || step < 2 * row) return true;
+  const uintptr_t apart = (a < b ? b - a : a - b) % step;
+  return apart < row || step - apart < row;
 }
 // The same, other than being the same rows.
 bool clash(const void* p, int64_t ps, const void* q, int64_t qs, int64_t n, int64_t d, int elem) {

@@ -142,6 +142,36 @@ def test_autograd_shapes_and_broadcast():
         y.sum().backward()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 61])
+def test_columns_of_one_buffer(d, dtype):
+    """What is read and what is written may be other columns of the same rows, with the bits of the same call between
+    buffers of that layout (of another layout the order of a row's sums differs); rows that share elements are
+    refused."""
+    g = torch.Generator(device=DEV).manual_seed(d)
+    whole = torch.randn(41, 4 * d + 3, generator=g, device=DEV).to(dtype)
+    tok = torch.randint(-1, 40, (40,), generator=g, device=DEV, dtype=torch.int32)
+    cols = lambda t: (t[:40, :d], t[:40, d:2 * d], t[:40, 2 * d + 1:3 * d + 1])  # noqa: E731
+    x, y, dx = cols(whole)
+    plain, want, want_dx = (cols(whole.clone())[i] for i in range(3))
+    _, stats = dh.layer_norm(plain, out=want, with_stats=True)
+    dh.layer_norm(x, out=y)
+    assert torch.equal(y, want) and torch.equal(x, plain)
+    grads = dh.layer_norm_backward(want, plain, stats, grad_x=want_dx)
+    got = dh.layer_norm_backward(y, x, stats, grad_x=dx)
+    assert all(torch.equal(a, b) for a, b in zip(got, grads)) and torch.equal(x, plain) and torch.equal(y, want)
+    dh.embed(x, tok, out=y)
+    assert torch.equal(y, dh.embed(plain, tok)) and torch.equal(x, plain)
+    dh.embed_backward(x, tok, 40, grad_table=dx)
+    assert torch.equal(dx, dh.embed_backward(plain, tok, 40, grad_table=want_dx)) and torch.equal(x, plain)
+    for col in (d - 1, 1, 3 * d + 4):  # the last one's rows end in the next row's first column
+        out = whole.as_strided(x.shape, x.stride(), col)
+        with pytest.raises(dh.DhError, match="INVALID_ARG"):
+            dh.embed(x, tok, out=out)
+        with pytest.raises(dh.DhError, match="INVALID_ARG"):
+            dh.layer_norm(x, out=out)
+
+
 def test_gradients_are_not_captured():
     table = torch.randn(10, 16, device=DEV, requires_grad=True)
     tok = torch.tensor([1, 2], dtype=torch.int32, device=DEV)
