@@ -1464,6 +1464,8 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_pick(SampleArgs a, int
     } else {
       const Weights weight(m, t, vocab);
       r.low = key_of<T>(weight.zlow);
+      // (the limit itself need not be a value of T: the key is then that of the value below)
+      if (value_of<T>(r.low) < weight.zlow) ++r.low;
       r.top_k = top_k > 1 && top_k < vocab ? top_k : 0;
       r.top_p = top_p;
       r.u = u;

@@ -252,6 +252,19 @@ def test_long_rows_without_a_short_list(kind, dtype):
             check(z, u, *s)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,top", [(0.7, 40.0), (1.0, 40.0), (0.7, 5.0), (0.3, 13.0)])
+def test_fewer_tokens_with_a_weight_than_top_k(T, top, dtype):
+    """Logits that fall by 40 T: of 3500 the last three hundred or so weigh less than 2^-52 of the first and count as
+    none, so top-k reaches past the tokens that count."""
+    V, N = 3500, 24
+    z = torch.linspace(top, top - 40 * T, V)[torch.randperm(V, generator=torch.Generator().manual_seed(1))]
+    z = z.to(DT[dtype]).to(DEV).expand(N, V)
+    u = torch.rand(N, generator=torch.Generator().manual_seed(2)).to(DEV)
+    for s in [(T, 3400, 1.0, 0.0), (T, 3400, 0.99, 0.0), (T, 3400, 0.9, 1e-4), (T, 3400, 1.0, 1.0), (T, 1500, 0.99, 0.0)]:
+        check(z, u, *s)
+
+
 def test_rows_that_are_searched_beside_others():
     """Each row of a batch as it is alone, whatever its neighbours need; again with one workspace and given outputs."""
     V, N = 60000, 40
