@@ -26,9 +26,9 @@ namespace dh {
 namespace {
 
 constexpr int EM_THREADS = 256;
-// 4 for long calls: 32768 rows of 5120 bf16 75 us, 79 with 2, 78 with 8.  1 where the blocks of such a call are few for
-// the SMs: 8 rows 1.2 us, 1.8 with 4.
-constexpr int EM_VECS = 4;
+// 4 for long calls: 32768 rows of 5120 bf16 75 us, 79 with 2, 78 with 8.  1 where those are fewer than EM_FEW blocks per
+// SM: 8 rows 1.2 us, 1.8 with 4; 1000 rows 3.1 and 3.4; 2000 rows 6.2 and 5.4.
+constexpr int EM_VECS = 4, EM_FEW = 8;
 
 // Pieces of a row that is written: its 16-byte words in memory, of which the first and the last may hold elements of
 // its neighbours, so that what is written is whole words whatever the row's alignment.  Piece g starts at column
@@ -468,7 +468,7 @@ cudaError_t run_embed(const Ctx& c, const EmbedArgs& a) {
                    whole_vectors(a.dst, a.dst_ld, a.N, a.d, sizeof(T));
   const unsigned units = vec ? (unsigned)(a.d / PER) : (unsigned)pieces(a.d, PER);
   const unsigned long long items = (unsigned long long)a.N * units;
-  const bool few = items <= (unsigned long long)EM_THREADS * EM_VECS * c.num_sms;
+  const bool few = items <= (unsigned long long)EM_THREADS * EM_VECS * EM_FEW * c.num_sms;
   const unsigned each = EM_THREADS * (few ? 1 : EM_VECS), grid = (unsigned)((items + each - 1) / each);
   return launch_pdl(c, "embed",
                     few ? (vec ? k_embed<T, true, 1> : k_embed<T, false, 1>)
