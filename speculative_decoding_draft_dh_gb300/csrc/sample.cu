@@ -109,9 +109,9 @@ struct Rate {
   }
 };
 
-// The weights of a row whose largest logit is m at temperature t.  z c has to stay below 2^15 for the fp32 form, and
-// the logits whose weights count above the type's lowest; beyond that (huge logits, tiny and huge temperatures)
-// `far` takes 64-bit arithmetic.
+// The weights of a row whose largest logit is m at temperature t.  z c has to stay below 2^15 for the fp32 form, the
+// logits whose weights count above the type's lowest, and 64 c, the steps of a logit, below its largest; beyond that
+// (huge logits, tiny and huge temperatures) `far` takes 64-bit arithmetic.
 struct Weights {
   Rate c;
   float m, t, zlow;
@@ -122,7 +122,7 @@ struct Weights {
     id_bits = 32 - __clz(vocab - 1);
     frac = min(62 - id_bits, SEG_FRAC);
     const float reach = (float)(frac + 2) / c.hi;  // what is lower than m by that much weighs below 2^-(frac + 1)
-    far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e38f && 128.f / c.hi + fabsf(m) < 1e38f);
+    far = !(fabsf(m * c.hi) < 32000.f && c.hi < 1e36f && 128.f / c.hi + fabsf(m) < 1e38f);
     zlow = far ? -3.4028234e38f : m - reach;
     e_ref = far ? 0 : (__float_as_int(fmaf(m, c.hi, EXP_MAGIC)) - EXP_MAGIC_BITS) >> 6;
   }
@@ -476,7 +476,7 @@ __device__ __forceinline__ bool reached(Goal goal, u64 want, u64 mass, uint32_t 
 }
 
 // The bin, from the top down, in which `want` is reached, counted on from `above` tokens of `above_mass`; the last bin
-// that is not empty where it is not.
+// that is not empty where it is not, -1 where all are empty.
 struct Histogram {
   int bin;
   uint32_t above, count;
@@ -664,7 +664,12 @@ __device__ __noinline__ Histogram find_bin(int level, uint32_t above, u64 above_
   S& s = smem<S>();
   const Bins& bins = s.bins[level];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) s.bin = s.last = -1;
+  if (threadIdx.x == 0) {
+    s.bin = s.last = -1;
+    s.bin_mass = s.bin_count = 0;
+    s.above_mass = above_mass;
+    s.above_count = above;
+  }
   // inclusive sums over the bins, four to a thread
   constexpr int OWN = SP_BINS / SP_THREADS;
   u64 m = 0;
@@ -746,6 +751,10 @@ __device__ __noinline__ Place descend(const T* row, Share part, Coarse coarse, u
     fill_fine<T, ALIGNED, S>(row, part, coarse, bin, lo, hi, weight);
     const int sh = bin_shift(lo, hi);
     h = find_bin<S>(1, p.above, p.above_mass, want, goal);
+    if (h.bin < 0) {  // none of the bin's tokens: no place
+      p.key = hi;
+      return p;
+    }
     hi -= (uint32_t)h.bin << sh;
     const uint32_t reach = (1u << sh) - 1u;
     if (hi - lo > reach) lo = hi - reach;
@@ -760,8 +769,9 @@ __device__ __noinline__ Place descend(const T* row, Share part, Coarse coarse, u
   }
 }
 
-// The id of the j-th token (from 1, by id) whose key is `key`, the last one where there are fewer; -1 in the blocks
-// of a cluster whose share does not hold it.
+// The id of the j-th token (from 1, by id) whose key is `key`, the last one where there are fewer, -1 where there is
+// none; ELSEWHERE in the blocks of a cluster that have nothing to say.
+constexpr int ELSEWHERE = -2;
 template <typename T, bool ALIGNED, int RANKS>
 __device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, uint32_t j) {
   Scratch& s = smem<Scratch>();
@@ -776,7 +786,7 @@ __device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, u
   for (int i = from; i < to; i += STEP) n += __popc(matches(i + lane * PER));
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   if (lane == 0) s.warp_count[warp] = n;
-  if (threadIdx.x == 0) s.bin = -1;
+  if (threadIdx.x == 0) s.bin = RANKS > 1 ? ELSEWHERE : -1;
   __syncthreads();
   uint32_t before = 0, all = 0;
   for (int w = 0; w < SP_WARPS; ++w) {
@@ -795,7 +805,8 @@ __device__ __noinline__ int find_token(const T* row, Share part, uint32_t key, u
     all = total;
     cluster_sync();
   }
-  if (j > all) j = all;
+  if (all == 0) return RANKS > 1 && cluster_rank() != 0 ? ELSEWHERE : -1;
+  j = min(max(j, 1u), all);
   if (before < j && j <= before + n) {
     uint32_t want = j - before;
     for (int i = from; i < to; i += STEP) {
@@ -1003,7 +1014,8 @@ __device__ __forceinline__ void sort_few(u64* a, int n, int id_bits, Bins& bins)
 }
 
 // The token (as in the lists) at which `want` is reached, of the tokens of coarse bin h.bin, the running sum up to and
-// with it, and its weight; the bin's last one where it is not.  False where the bin has more tokens than are sorted.
+// with it, and its weight; the bin's last one where it is not.  False where the bin has more tokens than are sorted, or
+// none.
 struct Cut {
   u64 token, mass, w;
 };
@@ -1054,7 +1066,7 @@ __device__ __noinline__ bool resolve(const T* row, Share part, Coarse coarse, Hi
     }
     cluster_sync();  // the other blocks' have been read
   }
-  if (n > SP_FEW) return false;
+  if (n < 1 || n > SP_FEW) return false;
   sort_few<T, OWN>(few, n, weight.id_bits, s.bins[1]);
   const int i0 = OWN * threadIdx.x;
   u64 run = 0;
@@ -1120,11 +1132,11 @@ __device__ __noinline__ void pick_by_keys(const T* row, Share part, Coarse coars
   if (p.w && p.above_mass <= want) j = (uint32_t)min((u64)j, (want - p.above_mass) / p.w + 1);
   if (p.key == key) j = min(j, equal);
   *token = find_token<T, ALIGNED, RANKS>(row, part, p.key, j);
-  *prob = share(p.w, mass);
+  *prob = p.w ? share(p.w, mass) : 0.f;
 }
 
-// Token and probability by searches over the whole row, by one block or a cluster (-1 in the blocks that do not hold
-// the token), or over a list that holds all tokens down to the last that can be drawn.
+// Token and probability by searches over the whole row, by one block or a cluster (ELSEWHERE in the blocks that do not
+// hold the token), or over a list that holds all tokens down to the last that can be drawn.
 template <typename T, bool ALIGNED, class S>
 __device__ __noinline__ void pick_by_search(const T* row, Share part, RowState r, Weights weight, int* token,
                                             float* prob) {
@@ -1143,7 +1155,7 @@ __device__ __noinline__ void pick_by_search(const T* row, Share part, RowState r
     if (r.w_min > cut.w) mass = mass_of_heavy<T, ALIGNED, S>(row, part, r.w_min, r.least, weight);
     found = search(draw_at(r.u, mass), ABOVE);
     if (found) {
-      *token = S::RANKS == 1 || cluster_rank() == 0 ? (int)~(uint32_t)cut.token : -1;
+      *token = S::RANKS == 1 || cluster_rank() == 0 ? (int)~(uint32_t)cut.token : ELSEWHERE;
       *prob = share(cut.w, mass);
       return;
     }
@@ -1558,7 +1570,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) k_sample_search(SampleArgs a, c
   float prob;
   pick_by_search<T, ALIGNED, SearchSmem>(static_cast<const T*>(a.logits) + n * a.ld,
                                          share_of_row<T, SS_RANKS>(a.vocab), r, weight, &token, &prob);
-  if (threadIdx.x == 0 && token >= 0) {
+  if (threadIdx.x == 0 && token != ELSEWHERE) {
     a.token[n] = token;
     if (a.prob) a.prob[n] = prob;
   }

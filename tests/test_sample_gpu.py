@@ -371,3 +371,23 @@ def test_without_probabilities_and_refusals():
         with pytest.raises(dh.DhError, match="INVALID_ARG"):
             dh.sample(z, u, **bad)
     assert dh.sample(z[:0], u[:0])[0].shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1.2e-38, 2e-38, 1e-37, 2.6e-37, 3e-37, 1.3e-36, 1.6e-36, 1e-34])
+def test_tiny_temperatures_of_searched_rows(T, dtype):
+    """Long flat rows whose logits and temperature lie near the smallest normal number: 64 steps of a weight's octave per
+    unit of logit pass fp32's range there.  (The tokens of one weight's step are thousands, and of one bin.)"""
+    V, N = 150016, 4
+    g = torch.Generator().manual_seed(31)
+    row = (2 * torch.randn(V, generator=g).double() * float(np.float32(T))).float().to(DT[dtype])
+    z = row.to(DEV).expand(N, V)
+    u = torch.rand(N, generator=g).to(DEV)
+    for s in [(T, 0, 1.0, 0.0), (T, 0, 0.95, 0.0), (T, 3000, 1.0, 0.0), (T, 20000, 0.9, 0.001), (T, 0, 1.0, 0.05)]:
+        token, _ = check(z, u, *s)
+        assert ((token >= 0) & (token < V)).all()
+    # and of one step's worth of values only, which are searched by their keys
+    z = torch.where(torch.arange(V) % 2 == 0, 1.0, 2.0).mul(float(np.float32(T)) / 512).to(DT[dtype]).to(DEV).expand(N, V)
+    for s in [(T, 0, 1.0, 0.0), (T, 0, 0.75, 0.0), (T, 100000, 1.0, 0.0)]:
+        token, _ = check(z, u, *s)
+        assert ((token >= 0) & (token < V)).all()
