@@ -16,6 +16,7 @@
 // Rows of more than NM_HELD columns are read again for each step instead, by k_norm_wide and
 // k_norm_backward_wide, and k_norm_columns sums their dw and db (10000 rows of 12288 bf16: 217 us and 453).
 #include <mutex>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -129,7 +130,8 @@ struct Ring {
     asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
     if constexpr (WORDS) __syncwarp();
   }
-  // Vector v of the row in slot s.
+  // Vector v of the row in slot s.  WHOLE: the warp's columns all lie within the row.
+  template <bool WHOLE = false>
   __device__ __forceinline__ uint4 get(const T* row, int s, int v) const {
     if constexpr (WORDS) {
       const int lane = threadIdx.x & 31;
@@ -138,7 +140,7 @@ struct Ring {
 #pragma unroll
       for (int e = 0; e < C::PER; ++e) {
         const int i = (v * C::PER + e) * 32 + lane;
-        if (i < held) {
+        if (WHOLE || i < held) {
           unsigned short x;
           asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + i * 2) : "memory");
           w[e / 2] |= (uint32_t)x << (16 * (e & 1));
@@ -254,36 +256,50 @@ __device__ __forceinline__ float pair_sum(f32x2 v) {
 
 constexpr int NF_STAGES = 3;  // 32768 rows of 5120 bf16: 104 us, 109 with 2, 103 with 4
 constexpr int NF_WARPS = 16;  // of a row, at most
-// Registers of a thread with NV vectors.
+// Registers of a thread with NV vectors.  With four, NF_TIGHT where they let more groups run (32768 rows of 5120: 4 groups
+// 103.6 us, 3 with 128 registers 106.6), else 128 (20000 rows of 8192: 2 groups of either kind 105 and 111).
 constexpr int norm_regs(int nv) { return nv == 1 ? 64 : nv == 2 ? 80 : 128; }
+constexpr int NF_TIGHT = 96;
+// Threads of a block that have an SM's registers to themselves: a quarter of them to each four warps' first one.
+constexpr int threads_by_regs(int regs) { return 65536 / 4 / 32 / regs * 128 < 1024 ? 65536 / 4 / 32 / regs * 128 : 1024; }
 
 // A block holds blockDim / width groups of `width` threads, each of which walks over rows of its own; the groups
 // share the parameters (SHARED: in shared memory).  Barriers are a group's.
-// Each thread takes its elements relative to the mean of its first vector (z = x - s): with at most NV vectors the
-// sum of z^2 is at most NV + 1 times that of the squares about the thread's own mean, so nothing is lost to a mean
-// far from 0 or to an outlier.  The threads' sums are joined relative to the shift of a warp's first lane, the
-// warps' relative to that of the first warp (the formulas of Chan, Golub and LeVeque).
-template <typename T, typename P, int NV, bool VEC, bool SHARED>
-__global__ void __maxnreg__(norm_regs(NV)) k_norm(NormArgs a, int width) {
+// A warp's sums are about the mean c of its threads' first eight elements each, the row's about the mean of up to four
+// warps' means (the formulas of Chan, Golub and LeVeque).  Of what is joined one part in four or more enters the value
+// that it is joined about, so the squares add up to about four times those about the mean at most, and nothing is lost
+// to a mean far from 0 or to outliers, wherever they stand.  (About the mean of a single thread's elements they add up to
+// d / 8 times an outlier's, which then cancels.)  x - c, which the result is taken from, is rounded by 2^-24 |c|: that
+// of an outlier's 256th part, less than the mean's own error allows.  Of means only differences and halves are added
+// up: equal elements have no deviation at all.  A warp that lies within the row (`whole`) needs no masks: 20000 rows of 5119 bf16 111 us, 129 with them.
+template <typename T, typename P, int NV, bool VEC, bool SHARED, int REGS>
+__global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
   using C = Cols<T, VEC, NV>;
   using S = SharedParams<T, P, VEC, NV>;
   constexpr int PER = C::PER, HALF = PER / 2;
+  constexpr int REF = PER == 4 && NV > 1 ? 2 : 1;  // vectors whose mean a warp's sums are about
   extern __shared__ __align__(16) unsigned char norm_smem[];
-  __shared__ float sh[2][32][4];
+  __shared__ __align__(16) float sh[2][32][4];  // of a warp: sum of x - c, c, sum of (x - c)^2
   const int group = threadIdx.x / width, groups = blockDim.x / width, me = threadIdx.x - group * width;
   const int warp = me >> 5, lane = me & 31, warps = width >> 5, warp0 = (threadIdx.x >> 5) - warp;
   const float inv_d = 1.f / (float)a.d;
-  // elements of this thread's first vector, of this thread, and of the warp whose sums this lane joins
+  // elements of this thread's first vectors, of this thread, and of the warp whose sums this lane joins (lanes `span`
+  // apart the same)
+  int span = 1;
+  while (span < warps) span *= 2;
+  const int peer = lane & (span - 1);
   int first = 0, mine = 0;
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
       mine += C::col(me, v, e) < a.d;
-      if (v == 0) first = mine;
+      if (v < REF) first = mine;
     }
   const float inv_first = first ? 1.f / (float)first : 0.f;
-  const float count = (float)mine, their_count = (float)min(max(a.d - (lane & 15) * C::WARP, 0), C::WARP);
+  const bool whole = (warp + 1) * C::WARP <= a.d;
+  const bool empty = __any_sync(0xFFFFFFFFu, first == 0);  // the row ends within the warp
+  const float their_count = (float)min(max(a.d - peer * C::WARP, 0), C::WARP);
   int turn = 0;
   const S w_shared(norm_smem), b_shared(norm_smem + S::bytes(width));
   const Ring<T, VEC, NV> ring(norm_smem + (SHARED ? 2 * S::bytes(width) : 0), me, a.d);
@@ -308,64 +324,95 @@ __global__ void __maxnreg__(norm_regs(NV)) k_norm(NormArgs a, int width) {
   for (; n < rows; n += step) {
     f32x2 z[NV][HALF];
     ring.template wait<NF_STAGES - 2>();
+    // the row to registers, the mean c of the warp's first vectors, and the sums of x - c and of its square
+    float c;
+    f32x2 d1[2] = {0, 0}, d2[2] = {0, 0};
+    auto take = [&](auto whole_warp) {
+      constexpr bool W = decltype(whole_warp)::value;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) unpack_pairs<T>(ring.get(row, stage, v), z[v]);
-    ring.fetch(next, n + (NF_STAGES - 1) * step < rows, stage == 0 ? NF_STAGES - 1 : stage - 1);
+      for (int v = 0; v < REF; ++v) unpack_pairs<T>(ring.template get<W>(row, stage, v), z[v]);
+      // past the row's end the elements are 0
+      f32x2 f = add2(z[0][0], z[0][1]);
+      if constexpr (HALF == 4) f = add2(f, add2(z[0][2], z[0][3]));
+      else if constexpr (REF == 2) f = add2(f, add2(z[1][0], z[1][1]));
+      c = pair_sum(f) * inv_first;
+      if (!W && empty) {
+        const float other = __shfl_sync(0xFFFFFFFFu, c, 0);
+        if (first == 0) c = other;
+      }
+      // (halves, so that equal ones stay what they are; each step while other loads are on their way)
+      auto mix = [&](int o) {
+        c *= 0.5f;
+        c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+      };
+      mix(16);
+#pragma unroll
+      for (int v = REF; v < NV; ++v) {
+        unpack_pairs<T>(ring.template get<W>(row, stage, v), z[v]);
+        mix(16 >> (v - REF + 1));
+      }
+      ring.fetch(next, n + (NF_STAGES - 1) * step < rows, stage == 0 ? NF_STAGES - 1 : stage - 1);
+#pragma unroll
+      for (int o = 16 >> (NV - REF + 1); o > 0; o >>= 1) mix(o);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        // and stay 0
+        const f32x2 shift = both(W || !VEC || v * PER < mine ? -c : 0.f);
+#pragma unroll
+        for (int e = 0; e < HALF; ++e) {
+          f32x2 t = add2(z[v][e], shift);
+          if constexpr (!VEC && !W) {
+            float p, q;
+            unpack2(t, p, q);
+            t = pack2(v * PER + 2 * e < mine ? p : 0.f, v * PER + 2 * e + 1 < mine ? q : 0.f);
+          }
+          z[v][e] = t;
+          d1[e & 1] = add2(d1[e & 1], t);
+          d2[e & 1] = fma2(t, t, d2[e & 1]);
+        }
+      }
+    };
+    if (!VEC && whole) take(std::true_type{});
+    else take(std::false_type{});
     next += x_step;
     row += x_step;
     stage = stage + 1 == NF_STAGES ? 0 : stage + 1;
-    // past the row's end the elements are 0
-    f32x2 f = add2(z[0][0], z[0][1]);
-    if constexpr (HALF == 4) f = add2(f, add2(z[0][2], z[0][3]));
-    const float s = pair_sum(f) * inv_first;
-    f32x2 d1[2] = {0, 0}, d2[2] = {0, 0};
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      // and stay 0
-      const f32x2 shift = both(!VEC || v * PER < mine ? -s : 0.f);
-#pragma unroll
-      for (int e = 0; e < HALF; ++e) {
-        f32x2 t = add2(z[v][e], shift);
-        if constexpr (!VEC) {
-          float p, q;
-          unpack2(t, p, q);
-          t = pack2(v * PER + 2 * e < mine ? p : 0.f, v * PER + 2 * e + 1 < mine ? q : 0.f);
-        }
-        z[v][e] = t;
-        d1[e & 1] = add2(d1[e & 1], t);
-        d2[e & 1] = fma2(t, t, d2[e & 1]);
-      }
-    }
-    // sums of x - c and of its square, c the first lane's shift
-    const float c = __shfl_sync(0xFFFFFFFFu, s, 0), r = s - c;
-    const float p1 = pair_sum(add2(d1[0], d1[1])), p2 = pair_sum(add2(d2[0], d2[1]));
-    float part = fold(fmaf(count, r, p1), fmaf(r, fmaf(count, r, 2.f * p1), p2), 16);
+    const float own = c;
+    float part = fold(pair_sum(add2(d1[0], d1[1])), pair_sum(add2(d2[0], d2[1])), 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
-    float c0 = c;
     if (warps > 1) {
       // lanes 0 and 16 have the warp's sums
-      if ((lane & 15) == 0) sh[turn][warp0 + warp][lane >> 4] = part;
-      if (lane == 1) sh[turn][warp0 + warp][2] = c;
+      if ((lane & 15) == 0) sh[turn][warp0 + warp][lane >> 3] = part;
+      if (lane == 1) sh[turn][warp0 + warp][1] = c;
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(width) : "memory");
-      c0 = sh[turn][warp0][2];
+      const float* q = sh[turn][warp0 + (peer < warps ? peer : 0)];
+      // means of four of the warps without the last, which may have few columns
+      auto mean_of = [&](int w) {
+        const float2 t = *reinterpret_cast<const float2*>(sh[turn][warp0 + w]);
+        return fmaf(t.x, 1.f / C::WARP, t.y);
+      };
+      const int most = warps - 1;
+      c = mean_of(0);
+      c += 0.25f * ((mean_of(most / 4) - c) + (mean_of(most / 2) - c) + (mean_of(most * 3 / 4) - c));
       part = 0.f;
-      if ((lane & 15) < warps) {
-        const float* q = sh[turn][warp0 + (lane & 15)];
-        const float g = q[2] - c0, k = their_count * g;
-        part = lane < 16 ? q[0] + k : fmaf(g, fmaf(2.f, q[0], k), q[1]);
+      if (peer < warps) {
+        const float g = q[1] - c, k = their_count * g;
+        part = lane < 16 ? q[0] + k : fmaf(g, fmaf(2.f, q[0], k), q[2]);
       }
       turn ^= 1;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+      for (int o = 8; o > 0; o >>= 1)
+        if (o < span) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
     }
     const float sum1 = __shfl_sync(0xFFFFFFFFu, part, 0), sum2 = __shfl_sync(0xFFFFFFFFu, part, 16);
     const float delta = sum1 * inv_d;
     float var = (sum2 - sum1 * delta) * inv_d;
     if (var < 0.f) var = 0.f;  // a NaN stays
     const float rs = 1.f / sqrtf(var + a.eps);
-    if (a.stats_out && me == 0) a.stats_out[n] = make_float2(c0 + delta, rs);
-    const f32x2 rstd = both(rs), back = both(((s - c0) - delta) * rs);
+    // the mean, rounded, and what that leaves out
+    if (a.stats_out && me == 0) a.stats_out[n] = make_float2(c + delta, rs);
+    const f32x2 rstd = both(rs), back = both(((own - c) - delta) * rs);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       f32x2 w[HALF], b[HALF];
@@ -733,13 +780,23 @@ cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
   const size_t ring = NF_STAGES * Ring<T, VEC, NV>::bytes(width);
   const size_t shared = 2 * SharedParams<T, P, VEC, NV>::bytes(width);
   if (few)
-    return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false>, (unsigned)a.N, (unsigned)width, ring, a, width);
-  long long groups = least(1024, 65536 / norm_regs(NV)) / width;
-  if (shared + ring * groups > SM_SMEM) groups = (SM_SMEM - (long long)shared) / (long long)ring;
-  groups = least(groups < 1 ? 1 : groups, 15);  // a barrier each
-  const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
-  return launch_ring(c, "norm", k_norm<T, P, NV, VEC, true>, grid, (unsigned)(width * groups), shared + ring * groups,
-                     a, width);
+    return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false, norm_regs(NV)>, (unsigned)a.N, (unsigned)width, ring, a,
+                       width);
+  const int barriers = width > 32 ? 15 : 32;  // one per group, but for rows of one warp
+  auto groups_by = [&](int regs) {
+    const long long fit = (SM_SMEM - (long long)shared) / (long long)ring;
+    const unsigned groups = least(least(threads_by_regs(regs) / width, barriers), fit);
+    return groups < 1 ? 1u : groups;
+  };
+  auto run = [&](auto kernel, unsigned groups) {
+    const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
+    return launch_ring(c, "norm", kernel, grid, (unsigned)width * groups, shared + ring * groups, a, width);
+  };
+  const unsigned groups = groups_by(norm_regs(NV));
+  if constexpr (NV == 4)
+    if (groups_by(NF_TIGHT) > groups)
+      return run(k_norm<T, P, NV, VEC, true, NF_TIGHT>, groups_by(NF_TIGHT));
+  return run(k_norm<T, P, NV, VEC, true, norm_regs(NV)>, groups);
 }
 
 template <typename T, typename P, bool VEC>

@@ -295,3 +295,22 @@ def test_refusals():
         dh.layer_norm_backward(x[1:], x[:3].clone(), stats[:3], grad_x=x[:3])
     with pytest.raises(TypeError, match="dtype"):
         dh.layer_norm(x.half())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [5, 700])
+@pytest.mark.parametrize("d", [1000, 1001, 5120, 8191, 8192, 9000])
+@pytest.mark.parametrize("value", [30.0, 1e3, 3e4, 1e15])
+def test_outliers(value, d, N, dtype):
+    """One element, a thread's first vector or a warp's columns far above the others: the sums are as exact wherever in
+    the row they stand, since they are taken about means, not about single elements."""
+    places = [[0], range(4), range(8), [d - 1], [512], [1024], range(256, 260), range(512), range(d - 5, d), [3, d // 2]]
+    for i, at in enumerate(places):
+        at = [c for c in at if c < d]
+        x = matrix(N, d, dtype, seed=i)
+        x[:, at] = x[:, at].sign() * value if i % 2 else value
+        w, b = params(d, dtype)
+        check_forward(x, w, b)
+    x = matrix(N, d, dtype, seed=20, ld=d + 3, base=1)  # off 16 bytes
+    x[:, :8] = value
+    check_forward(x, None, None)
