@@ -7,10 +7,13 @@ layer norm of the hidden rows, for training them together with the head (``disti
 Without gradients both may be captured into a CUDA graph.  A training step that is captured calls the four
 functions of ``binding`` instead: the backward pass that autograd would replay synchronises with the streams on
 which the leaves were used before, which a capture does not allow.
+
+There are no forward-mode derivatives: a tensor with a tangent is refused.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as dh
 
@@ -19,6 +22,12 @@ def _no_capture(name):
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError(f"{name} with gradients cannot be captured into a CUDA graph: use binding.{name} and "
                            f"binding.{name}_backward")
+
+
+def _no_tangents(name, *tensors):
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def _rows(t):
@@ -49,6 +58,7 @@ def embedding(table, tokens, *, scale=1.0):
         raise ValueError("table must be a CUDA tensor")
     if table.dim() != 2:
         raise ValueError("table must be [vocab, d]")
+    _no_tangents("embedding", table)
     flat = tokens.reshape(-1)
     if table.requires_grad and torch.is_grad_enabled():
         _no_capture("embed")
@@ -82,6 +92,7 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5):
     dtype)."""
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
+    _no_tangents("layer_norm", x, weight, bias)
     flat = _rows(x)
     given = [t for t in (x, weight, bias) if t is not None]
     if torch.is_grad_enabled() and any(t.requires_grad for t in given):

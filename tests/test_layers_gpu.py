@@ -257,3 +257,24 @@ def test_calls_on_two_streams_and_threads():
     for t in threads:
         t.join()
     assert not bad
+
+
+def test_forward_mode_is_refused():
+    """Tangents would be lost without a word: there is no forward-mode derivative."""
+    from torch.autograd import forward_ad
+    table, x = torch.randn(10, 16, device=DEV), torch.randn(4, 16, device=DEV)
+    w, tok = torch.ones(16, device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV)
+    calls = [lambda t: layers.embedding(t(table), tok), lambda t: layers.layer_norm(t(x)),
+             lambda t: layers.layer_norm(x, t(w)), lambda t: layers.layer_norm(x, w, t(w)),
+             lambda t: layers.layer_norm(t(x).t().contiguous().t(), w)]
+    for call in calls:
+        plain = call(lambda t: t)
+        with forward_ad.dual_level():
+            assert torch.equal(call(lambda t: t), plain)
+            for grad in (False, True):
+                for leaf in (False, True):
+                    dual = lambda t: forward_ad.make_dual(t.clone().requires_grad_(leaf), torch.ones_like(t))  # noqa: E731
+                    with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="forward"):
+                        call(dual)
+    with pytest.raises(NotImplementedError, match="forward"):
+        torch.func.jvp(lambda t: layers.layer_norm(t, w), (x,), (x,))
