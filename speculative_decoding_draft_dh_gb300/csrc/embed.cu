@@ -85,10 +85,12 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned unit
   const unsigned long long i0 = (unsigned long long)blockIdx.x * (EM_THREADS * VECS) + threadIdx.x;
   uint4 x[VECS];
   int row[VECS], at[VECS];
+  float by[VECS];  // the scale; 1 where padding is: its zeros stay zeros whatever the scale
 #pragma unroll
   for (int q = 0; q < VECS; ++q) {
     const unsigned long long i = i0 + q * EM_THREADS;
     row[q] = -1;
+    by[q] = 1.f;
     if (i < items) {
       const unsigned long long r = i / units;
       row[q] = (int)r;
@@ -97,6 +99,7 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned unit
       const int t = __ldg(a.tokens + r);
       x[q] = make_uint4(0u, 0u, 0u, 0u);
       if (t >= 0 && t < a.vocab) {
+        by[q] = a.scale;
         const T* from = table + (long long)t * a.src_ld;
         x[q] = VEC ? *reinterpret_cast<const uint4*>(from + at[q]) : load_piece(from, at[q], a.d);
       }
@@ -105,11 +108,11 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned unit
 #pragma unroll
   for (int q = 0; q < VECS; ++q) {
     if (row[q] < 0) continue;
-    if (a.scale != 1.f) {
+    if (by[q] != 1.f) {
       float z[PER];
       Elem<T>::unpack(x[q], z);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) z[e] *= a.scale;
+      for (int e = 0; e < PER; ++e) z[e] *= by[q];
       x[q] = round_vec<T>(z);
     }
     T* to = out + row[q] * a.dst_ld;

@@ -221,3 +221,20 @@ def test_refusals():
         dh.embed_backward(table[:4], tok, 10, grad_table=table)
     with pytest.raises(TypeError, match="dtype"):
         dh.embed(table.half(), tok)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [8, 1001, 5120])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -float("inf")])
+def test_padding_is_zeros_at_any_scale(scale, d, dtype):
+    V = 50
+    for N in (9, 20000):
+        table, tok = matrix(V, d, dtype, seed=1), tokens(N, V, "mixed", seed=2)
+        held = (tok >= 0) & (tok < V)
+        got = dh.embed(table, tok, scale=scale)
+        assert not got[~held].any() and not got[held].isfinite().any()
+        assert torch.equal(got[held].isnan(), forward(table, tok, scale)[held].isnan())
+    grad = dh.embed_backward(matrix(9, d, dtype, 3), tok[:9], V, scale=scale)
+    none = torch.ones(V, dtype=torch.bool, device=DEV)
+    none[tok[:9][held[:9]].long()] = False
+    assert not grad[none].any() and not grad[~none].isfinite().any()
