@@ -508,7 +508,9 @@ int dh_embed_backward(const void* grad_out, int64_t grad_stride, const int32_t* 
  * and with xhat = (x - mean) rstd, h = grad_out weight:
  *   grad_x = rstd (h - mean(h) - xhat mean(h xhat))
  *   grad_weight = sum over the rows of grad_out xhat,   grad_bias = sum over the rows of grad_out
- * Sums, statistics and products in fp32, each result rounded once to its type.  weight, bias: [d] of
+ * Sums, statistics and products in fp32, each result rounded once to its type; of grad_weight and
+ * grad_bias up to about N / 152 rows (d > 8192: 32) are added one after another, and what the last
+ * additions would round off is kept.  weight, bias: [d] of
  * param_dtype (DH_F32, or `dtype`), NULL for 1 and 0.  Infinite or NaN elements make their row NaN,
  * and the sums of the gradients that it enters; other rows are not affected.
  *

@@ -14,7 +14,7 @@
 // A thread keeps its columns over all rows that its group walks, so dw and db are summed in its registers;
 // blocks leave their sums in the workspace and a second kernel adds them in order.
 // Rows of more than NM_HELD columns are read again for each step instead, by k_norm_wide and
-// k_norm_backward_wide, and k_norm_columns sums their dw and db (10000 rows of 12288 bf16: 217 us and 453).
+// k_norm_backward_wide, and k_norm_columns sums their dw and db (10000 rows of 12288 bf16: 214 us and 433).
 #include <mutex>
 #include <type_traits>
 #include <utility>
@@ -684,29 +684,80 @@ __global__ void __launch_bounds__(NW_THREADS) k_norm_backward_wide(NormArgs a, b
   }
 }
 
-// dw and db of a tile of columns over a share of the rows.
-constexpr int NC_THREADS = 256;
+// A sum with what its additions round off (the exact error of a sum, by Knuth).
+struct LongSum {
+  float sum, rest;
+  __device__ __forceinline__ void add(float x) {
+    const float s = sum + x, b = s - sum;
+    rest += (sum - (s - b)) + (x - b);
+    sum = s;
+  }
+  __device__ __forceinline__ void add(const LongSum& o) {
+    add(o.sum);
+    rest += o.rest;
+  }
+  // (an infinite or NaN sum has no remainder)
+  __device__ __forceinline__ float value() const { return fabsf(sum) < INFINITY ? sum + rest : sum; }
+};
+
+// dw and db of a tile of columns over a share of the rows, NC_RUN of them at a time in one fp32 sum: a share of a million
+// rows of 65536 columns is 250000 rows, and their errors would add up.  The runs' sums wait in shared memory and four rows
+// are loaded ahead, so that all blocks of the grid run at once with 32 registers (the gradient of 10000 rows of 12288
+// bf16 433 us; 494 with a run unrolled by four, 653 with 40 registers).
+constexpr int NC_THREADS = 256, NC_BLOCKS = 8, NC_RUN = 32, NC_AHEAD = 4;
 template <typename T>
-__global__ void __launch_bounds__(NC_THREADS) k_norm_columns(NormArgs a) {
+__global__ void __launch_bounds__(NC_THREADS, NC_BLOCKS) k_norm_columns(NormArgs a) {
+  __shared__ LongSum sh[2][NC_THREADS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel follows
+  // the kernel that follows may be the gradient's, which may overwrite x or the gradient: it waits for this one to end
+  // before it touches memory
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int col = blockIdx.x * NC_THREADS + threadIdx.x;
   if (col >= a.d) return;
   const T* x = static_cast<const T*>(a.x) + col;
   const T* g = static_cast<const T*>(a.grad) + col;
-  float dw = 0.f, db = 0.f;
-  for (long long n = blockIdx.y; n < a.N; n += gridDim.y) {
-    const float2 st = __ldg(a.stats + n);
-    const float q = Elem<T>::to_f(g[n * a.grad_ld]);
-    dw = fmaf(q, (Elem<T>::to_f(x[n * a.ld]) - st.x) * st.y, dw);
-    db += q;
+  LongSum& w = sh[0][threadIdx.x];
+  LongSum& b = sh[1][threadIdx.x];
+  w = b = LongSum{0.f, 0.f};
+  const long long x_step = gridDim.y * a.ld, g_step = gridDim.y * a.grad_ld;
+  const float2* stats = a.stats + blockIdx.y;
+  x += blockIdx.y * a.ld;
+  g += blockIdx.y * a.grad_ld;
+  int left = (int)((a.N - blockIdx.y + gridDim.y - 1) / gridDim.y);  // (as many blocks as rows at most)
+  while (left > 0) {
+    float dw = 0.f, db = 0.f;
+    auto rows = [&](auto many) {
+      constexpr int R = decltype(many)::value;
+      float2 st[R];
+      float p[R], q[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        st[i] = __ldg(stats);
+        p[i] = Elem<T>::to_f(*x);
+        q[i] = Elem<T>::to_f(*g);
+        stats += gridDim.y;
+        x += x_step;
+        g += g_step;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        dw = fmaf(q[i], (p[i] - st[i].x) * st[i].y, dw);
+        db += q[i];
+      }
+    };
+    int n = min(left, NC_RUN);
+    left -= n;
+    for (; n >= NC_AHEAD; n -= NC_AHEAD) rows(std::integral_constant<int, NC_AHEAD>{});
+    for (; n > 0; --n) rows(std::integral_constant<int, 1>{});
+    w.add(dw);
+    b.add(db);
   }
   float* part = a.ws + (long long)blockIdx.y * 2 * a.part_ld;
-  part[col] = dw;
-  part[a.part_ld + col] = db;
+  part[col] = w.value();
+  part[a.part_ld + col] = b.value();
 }
 
-// The blocks' sums, added in a fixed order and rounded once.  They stand in the order of the threads' columns, nv
+// The blocks' sums, added in a fixed order, the last steps without loss, and rounded once.  They stand in the order of the threads' columns, nv
 // vectors of `per` of a thread and `width` threads (nv 0: in the order of the columns).
 constexpr int NJ_COLS = 32, NJ_ROWS = 32;
 template <typename P>
@@ -726,7 +777,14 @@ __global__ void __launch_bounds__(NJ_COLS * NJ_ROWS) k_norm_join(NormArgs a, int
   sh[row][lane] = s;
   __syncthreads();
   // warp r adds up column r: lane l has part l's sum
-  const float t = warp_sum(sh[lane][row]);
+  LongSum t = {sh[lane][row], 0.f};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LongSum other;
+    other.sum = __shfl_xor_sync(0xFFFFFFFFu, t.sum, o);
+    other.rest = __shfl_xor_sync(0xFFFFFFFFu, t.rest, o);
+    t.add(other);
+  }
   if (lane != 0) return;
   const int mine = blockIdx.x * NJ_COLS + row;
   int id = mine;
@@ -735,7 +793,7 @@ __global__ void __launch_bounds__(NJ_COLS * NJ_ROWS) k_norm_join(NormArgs a, int
     id = (thread >> 5) * (32 * nv * per) +
          (vec ? ((ve / per) * 32 + (thread & 31)) * per + ve % per : ve * 32 + (thread & 31));
   }
-  if (id < a.d) out[id] = Elem<P>::from_f(t);
+  if (id < a.d) out[id] = Elem<P>::from_f(t.value());
 }
 
 // Blocks that leave sums, at most: 2^22 columns of them, or 512.
@@ -884,7 +942,7 @@ cudaError_t pick_backward(const Ctx& c, NormArgs a) {
   } else {
     // the columns' sums first: the gradient may overwrite the rows
     if (sums) {
-      const int tiles = (a.d + NC_THREADS - 1) / NC_THREADS, shares = 8 * c.num_sms / tiles;
+      const int tiles = (a.d + NC_THREADS - 1) / NC_THREADS, shares = NC_BLOCKS * c.num_sms / tiles;
       join.parts = (int)least(a.N, least(norm_parts(a.d), shares < 1 ? 1 : shares));
       e = launch_pdl(c, "norm_columns", k_norm_columns<T>, dim3((unsigned)tiles, (unsigned)join.parts),
                      dim3(NC_THREADS), 0, a);

@@ -314,3 +314,18 @@ def test_outliers(value, d, N, dtype):
     x = matrix(N, d, dtype, seed=20, ld=d + 3, base=1)  # off 16 bytes
     x[:, :8] = value
     check_forward(x, None, None)
+
+
+def test_column_sums_over_many_rows():
+    """One row many times over (a row stride of 0), so that every column adds up equal terms and roundings do not cancel:
+    a share's rows are added 32 at a time in fp32 (31 roundings and the product's), those sums without further loss, and
+    a few more roundings lead to the result."""
+    for N, d, dtype in ((60000, 65536, "bf16"), (150000, 9001, "f32"), (150000, 8200, "bf16")):
+        x, g = matrix(1, d, dtype, 1), matrix(1, d, dtype, 2)
+        _, stats = dh.layer_norm(x, with_stats=True)
+        dx, dw, db = dh.layer_norm_backward(g.expand(N, d), x.expand(N, d), stats.repeat(N, 1), with_x=False,
+                                            param_dtype=torch.float32)
+        hat = (x.double() - stats[:, :1].double()) * stats[:, 1:].double()
+        for got, term in ((dw, g.double() * hat), (db, g.double())):
+            off = (got.double() - N * term[0]).abs() / (N * term[0].abs()).clamp(min=1e-30)
+            assert off.max() <= (32 + 8) * U, (N, d, dtype, off.max() / U)
