@@ -450,9 +450,11 @@ int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, co
  *   token_out[n] = the first token at which the running sum exceeds u[n] K
  *   prob_out[n]  = its w / K, the probability with which it is drawn
  * T = 0 takes the first token, with probability 1.  The same inputs give the same token.
- * - Weights are fixed-point numbers whose sums are exact: a running sum is off by about 2^-30 of
- *   itself, a single weight by 2^-28 (one as near as that to min-p's limit may fall on either side),
- *   and weights below about 2^-41 (2^-44 for a vocabulary of up to 2^18) of the largest count as 0.
+ * - Weights are fixed-point numbers whose sums are exact.  With f = 62 - ceil(log2(vocab)), at most 52
+ *   (44 for 2^18 ids, 41 for 2^21), a weight is off by about 2^-28 of itself and by up to 2^-(f+1) of the
+ *   row's largest (below that it counts as 0), a sum of n weights by 2^-28 of itself and n 2^-(f+1) of
+ *   the largest.  So a token 20 T below the largest logit has its weight and probability to 2^-16 for
+ *   2^18 ids, to 2^-13 for 2^21.  A weight as near as that to min-p's limit may fall on either side.
  * - A logit of -inf is never drawn.  A row with a NaN or +inf logit, or with nothing above -inf, has
  *   token -1 and probability 0; so has one whose temperature is not finite and >= 0 or whose u, top_p
  *   or min_p is NaN.  Other settings beyond their range count as the nearest end of it.

@@ -391,3 +391,48 @@ def test_tiny_temperatures_of_searched_rows(T, dtype):
     for s in [(T, 0, 1.0, 0.0), (T, 0, 0.75, 0.0), (T, 100000, 1.0, 0.0)]:
         token, _ = check(z, u, *s)
         assert ((token >= 0) & (token < V)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [151936, 1 << 21])
+@pytest.mark.parametrize("below", [15.0, 18.0, 21.0, 24.0, 28.0, "half a unit"])
+def test_unlikely_tokens(below, V, dtype):
+    """One likely token over a long tail, and uniforms that fall on the tail.  With f fraction bits a weight is off by
+    2^-27.5 of itself (the table's and the cubic's 2^-29 each, and a few of 2^-31) and half a unit, 2^-(f + 1) of the
+    largest; a sum of n by n times that.  So the token's own interval, widened by the sums' errors, has to hold
+    u K, and the probability is off by its weight's and the mass's errors and 2^-24."""
+    f = min(62 - (V - 1).bit_length(), 52)
+    rel, unit = 2.0 ** -27.5, 2.0 ** -(f + 1)
+    g = torch.Generator().manual_seed(V % 97 + 3)
+    for tail in ("equal", "spread"):
+        if below == "half a unit":  # equal logits whose weights are just under what counts
+            if tail == "spread":
+                continue
+            z = torch.full((V,), -float((f + 1) * np.log(2.0) + 0.004))
+        else:
+            z = torch.full((V,), -below)
+            if tail == "spread":
+                z += 0.3 * torch.randn(V, generator=g)
+        z[V // 3] = 0.0
+        z = z.to(DT[dtype])
+        row = z.double().numpy()
+        order = np.argsort(-row, kind="stable")
+        place = np.empty(V, dtype=np.int64)
+        place[order] = np.arange(V)
+        w = np.exp(row[order] - row[order[0]])
+        run = np.cumsum(w)
+        for k in (0, V // 2):
+            n = k or V
+            K = run[n - 1]
+            share = 1 - w[0] / K
+            u = torch.tensor(np.concatenate([1 - share * (np.arange(24) + 0.5) / 24, [0.3, 1 - 2.0 ** -24]]),
+                             dtype=torch.float32, device=DEV).clamp(max=1 - 2.0 ** -24)
+            token, prob = dh.sample(z.to(DEV).expand(len(u), V), u, top_k=k)
+            torch.cuda.synchronize()
+            for at, q, x in zip(token.tolist(), prob.tolist(), u.double().tolist()):
+                i = place[at]
+                assert 0 <= i < n
+                slack = 2 * rel * K + 2 * n * unit + 2 * unit
+                assert run[i] - w[i] - slack <= x * K <= run[i] + slack, (tail, k, i, x)
+                off = w[i] / K * (2 * rel + n * unit / K + 1.01 * 2.0 ** -24) + unit / K
+                assert abs(q - w[i] / K) <= 1.01 * off, (tail, k, i, q, w[i] / K)
