@@ -436,3 +436,21 @@ def test_unlikely_tokens(below, V, dtype):
                 assert run[i] - w[i] - slack <= x * K <= run[i] + slack, (tail, k, i, x)
                 off = w[i] / K * (2 * rel + n * unit / K + 1.01 * 2.0 ** -24) + unit / K
                 assert abs(q - w[i] / K) <= 1.01 * off, (tail, k, i, q, w[i] / K)
+
+
+def test_without_probabilities():
+    """prob_out NULL: the tokens of the call with probabilities, in a row that one block takes, in long rows with a top-k
+    for all, and where some rows are searched."""
+    lib = dh.load_library()
+    for V, N, k in ((500, 9, 0), (151936, 5, 30), (60000, 12, 0)):
+        z, u = rows(N, V, "bf16", seed=V)
+        if k == 0:
+            z[::2] = (0.5 * torch.randn(V, generator=torch.Generator().manual_seed(3))).bfloat16().to(DEV)
+        want, _ = dh.sample(z, u, temperature=1.5, top_k=k)
+        token = torch.full((N,), -7, dtype=torch.int32, device=DEV)
+        nbytes = lib.dh_sample_workspace(N, V, dh.BF16)
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=DEV)
+        status = lib.dh_sample(z.data_ptr(), z.stride(0), u.data_ptr(), None, None, None, None, 1.5, k, 1.0, 0.0, N, V,
+                               dh.BF16, token.data_ptr(), None, ws.data_ptr(), nbytes,
+                               torch.cuda.current_stream().cuda_stream)
+        assert status == 0 and torch.equal(token, want)
