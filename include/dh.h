@@ -462,7 +462,8 @@ int dh_reorder_states(const void* src, const int64_t* src_strides, void* dst, co
  * temperature, top_p, min_p fp32, top_k int32 [N]: device; NULL: the value *_all for every row, which
  * is checked on the host (temperature_all finite and >= 0, top_k_all >= 0, top_p_all and min_p_all in
  * [0, 1]).  logits `dtype`, rows row_stride elements apart (>= 0; any element alignment); u fp32 [N];
- * token_out int32 [N], prob_out fp32 [N] (may be NULL): device.  vocab <= DH_MAX_VOCAB,
+ * token_out int32 [N], prob_out fp32 [N] (may be NULL): device.  They must overlap neither each other
+ * nor what is read, but either may be u or a setting itself (same address).  vocab <= DH_MAX_VOCAB,
  * N <= 2^31 - 256.  Workspace: dh_sample_workspace bytes (0: NULL will do), 256-byte aligned, need not
  * be zeroed, not shared by calls that overlap in time.  N = 0 is a no-op.
  * ------------------------------------------------------------------------------------------- */
@@ -512,9 +513,10 @@ int dh_embed_backward(const void* grad_out, int64_t grad_stride, const int32_t* 
  *   grad_weight = sum over the rows of grad_out xhat,   grad_bias = sum over the rows of grad_out
  * Sums, statistics and products in fp32, each result rounded once to its type; of grad_weight and
  * grad_bias up to about N / 152 rows (d > 8192: 32) are added one after another, and what the last
- * additions would round off is kept.  weight, bias: [d] of
- * param_dtype (DH_F32, or `dtype`), NULL for 1 and 0.  Infinite or NaN elements make their row NaN,
- * and the sums of the gradients that it enters; other rows are not affected.
+ * additions would round off is kept.  (So deviations whose squares' sum passes fp32's range, 10^19 over
+ * the root of d and more, leave no variance to divide by.)  weight, bias: [d] of param_dtype (DH_F32, or
+ * `dtype`), NULL for 1 and 0.  Infinite or NaN elements make their row NaN, and the sums of the
+ * gradients that it enters; other rows are not affected.
  *
  * dh_layer_norm: stats_out fp32 [N x 2] (may be NULL).  y may be x itself (same address and stride).
  * dh_layer_norm_backward: from the stats of a forward call on the same x.  grad_x, grad_weight,
@@ -522,7 +524,7 @@ int dh_embed_backward(const void* grad_out, int64_t grad_stride, const int32_t* 
  * zeros of grad_weight and grad_bias.
  * Rows *_stride elements apart (any element alignment; rows read may overlap, rows written may not:
  * stride >= d); stats 8-byte aligned: all device.  Apart from the cases above what is written must
- * not overlap what is read.  The fastest are rows of whole 16-byte vectors that start on 16 bytes, of
+ * overlap neither what is read nor another result.  The fastest are rows of whole 16-byte vectors that start on 16 bytes, of
  * up to 8192 elements.  d <= DH_MAX_WIDTH, N <= 2^31 - 256, eps finite and >= 0.
  * Workspace (where grad_weight or grad_bias is wanted): dh_layer_norm_backward_workspace bytes,
  * 256-byte aligned, need not be zeroed, not shared by calls that overlap in time.  Results repeat bit

@@ -32,6 +32,20 @@ bool clash(const void* p, int64_t ps, const void* q, int64_t qs, int64_t n, int6
   return !(p == q && (ps == qs || n == 1)) && overlap(p, ps, n, q, qs, n, d, elem);
 }
 
+// Whether two arrays share memory (a null one none).
+bool shared(const void* p, uint64_t p_bytes, const void* q, uint64_t q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + q_bytes && b < a + p_bytes;
+}
+// Whether n rows of d elements at p share memory with an array; it may lie between two of them.
+bool touches(const void* p, int64_t ld, int64_t n, int64_t d, int elem, const void* q, uint64_t bytes) {
+  const uint64_t step = (uint64_t)ld * (uint64_t)elem, row = (uint64_t)d * (uint64_t)elem;
+  if (!shared(p, (uint64_t)(n - 1) * step + row, q, bytes)) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  if (b < a || step <= row) return true;
+  return (b - a) % step < row || (b - a) % step + bytes > step;
+}
+
 int done(cudaError_t e, const char* what) { return note_error(e, what) == cudaSuccess ? DH_OK : DH_ERR_CUDA; }
 
 }  // namespace
@@ -58,6 +72,16 @@ int dh_sample(const void* logits, int64_t row_stride, const float* u, const floa
   if (N == 0) return DH_OK;
   if (!logits || !u || !token_out) return DH_ERR_INVALID_ARG;
   if (!aligned_to(logits, elem_bytes(dtype))) return DH_ERR_UNSUPPORTED;
+  // a row's results may take the place of its uniform or of a setting: they are written when those have been read
+  const uint64_t each = 4ull * (uint64_t)N;
+  const void* const out[] = {token_out, prob_out};
+  const void* const per_row[] = {u, temperature, top_k, top_p, min_p};
+  if (shared(token_out, each, prob_out, each)) return DH_ERR_INVALID_ARG;
+  for (const void* o : out) {
+    if (touches(logits, row_stride, N, vocab, elem_bytes(dtype), o, each)) return DH_ERR_INVALID_ARG;
+    for (const void* r : per_row)
+      if (o != r && shared(o, each, r, each)) return DH_ERR_INVALID_ARG;
+  }
   const size_t need = dh_sample_workspace(N, vocab, dtype);
   if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return DH_ERR_WORKSPACE;
   Ctx c;
@@ -92,7 +116,9 @@ int dh_embed(const void* table, int64_t table_stride, const int32_t* tokens, int
   if (!table || !tokens || !out) return DH_ERR_INVALID_ARG;
   const int e = elem_bytes(dtype);
   if (!aligned_to(table, e) || !aligned_to(out, e)) return DH_ERR_UNSUPPORTED;
-  if (overlap(table, table_stride, vocab, out, out_stride, N, d, e)) return DH_ERR_INVALID_ARG;
+  if (overlap(table, table_stride, vocab, out, out_stride, N, d, e) ||
+      touches(out, out_stride, N, d, e, tokens, 4ull * (uint64_t)N))
+    return DH_ERR_INVALID_ARG;
   Ctx c;
   if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
   EmbedArgs a = {};
@@ -126,7 +152,9 @@ int dh_embed_backward(const void* grad_out, int64_t grad_stride, const int32_t* 
   if (!grad_table || (N > 0 && (!grad_out || !tokens))) return DH_ERR_INVALID_ARG;
   const int e = elem_bytes(dtype);
   if (!aligned_to(grad_table, e) || !aligned_to(grad_out, e)) return DH_ERR_UNSUPPORTED;
-  if (N > 0 && overlap(grad_out, grad_stride, N, grad_table, table_stride, vocab, d, e)) return DH_ERR_INVALID_ARG;
+  if (N > 0 && (overlap(grad_out, grad_stride, N, grad_table, table_stride, vocab, d, e) ||
+                touches(grad_table, table_stride, vocab, d, e, tokens, 4ull * (uint64_t)N)))
+    return DH_ERR_INVALID_ARG;
   const size_t need = dh_embed_backward_workspace(N, vocab, d, dtype);
   if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return DH_ERR_WORKSPACE;
   Ctx c;
@@ -171,7 +199,12 @@ int dh_layer_norm(const void* x, int64_t row_stride, const void* weight, const v
   if (!aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, pe) || !aligned_to(bias, pe) ||
       !aligned_to(stats_out, 8))
     return DH_ERR_UNSUPPORTED;
-  if (clash(x, row_stride, y, y_stride, N, d, e)) return DH_ERR_INVALID_ARG;
+  const uint64_t stats_bytes = 8ull * (uint64_t)N, param_bytes = (uint64_t)d * (uint64_t)pe;
+  if (clash(x, row_stride, y, y_stride, N, d, e) || touches(y, y_stride, N, d, e, weight, param_bytes) ||
+      touches(y, y_stride, N, d, e, bias, param_bytes) || touches(y, y_stride, N, d, e, stats_out, stats_bytes) ||
+      touches(x, row_stride, N, d, e, stats_out, stats_bytes) || shared(stats_out, stats_bytes, weight, param_bytes) ||
+      shared(stats_out, stats_bytes, bias, param_bytes))
+    return DH_ERR_INVALID_ARG;
   Ctx c;
   if (!get_ctx(stream, &c)) return DH_ERR_CUDA;
   NormArgs a = {};
@@ -209,6 +242,18 @@ int dh_layer_norm_backward(const void* grad_out, int64_t grad_stride, const void
   if (N > 0 && grad_x && (clash(grad_out, grad_stride, grad_x, grad_x_stride, N, d, e) ||
                           clash(x, row_stride, grad_x, grad_x_stride, N, d, e)))
     return DH_ERR_INVALID_ARG;
+  const uint64_t stats_bytes = 8ull * (uint64_t)N, param_bytes = (uint64_t)d * (uint64_t)pe;
+  if (N > 0 && (touches(grad_x, grad_x_stride, N, d, e, stats, stats_bytes) ||
+                touches(grad_x, grad_x_stride, N, d, e, weight, param_bytes)))
+    return DH_ERR_INVALID_ARG;
+  const void* const params[] = {grad_weight, grad_bias};
+  for (const void* p : params)
+    if (shared(p, param_bytes, weight, param_bytes) ||
+        (N > 0 && (touches(grad_out, grad_stride, N, d, e, p, param_bytes) ||
+                   touches(x, row_stride, N, d, e, p, param_bytes) || shared(p, param_bytes, stats, stats_bytes) ||
+                   touches(grad_x, grad_x_stride, N, d, e, p, param_bytes))))
+      return DH_ERR_INVALID_ARG;
+  if (shared(grad_weight, param_bytes, grad_bias, param_bytes)) return DH_ERR_INVALID_ARG;
   const bool sums = grad_weight || grad_bias;
   const size_t need = sums ? dh_layer_norm_backward_workspace(N, d, dtype) : 0;
   if (need && (!workspace || !aligned256(workspace) || ws_bytes < need)) return DH_ERR_WORKSPACE;

@@ -174,3 +174,47 @@ def test_binding_refuses_sizes_beyond_32_bits():
 def test_public_names(name):
     import speculative_decoding_draft_dh_gb300 as pkg
     assert callable(getattr(pkg, name))
+
+
+def test_results_that_share_memory_are_refused(lib):
+    """Small results (tokens, probabilities, statistics, parameters' gradients) over an input or one another.  The
+    accepted neighbours end at a later check, so that nothing is launched."""
+    A = [(i + 1) << 24 for i in range(12)]  # arrays far apart
+
+    def draw(N=4, ld=100002, z=A[0], u=A[1], T=A[2], k=A[3], p=A[4], m=A[5], tok=A[6], prob=A[7]):
+        return sample(lib, N=N, V=100000, ld=ld, z=z, u=u, tp=T, kp=k, pp=p, mp=m, tok=tok,
+                      prob=prob, ws=0)
+    assert draw() == WORKSPACE
+    assert draw(tok=A[7]) == draw(tok=A[7] + 12) == INVALID and draw(tok=A[7] + 16) == WORKSPACE
+    assert draw(tok=A[0] + 64) == draw(prob=A[0] + 64) == draw(prob=A[0] - 4) == INVALID
+    assert draw(prob=A[0] + 4 * 100000) == INVALID  # 2 elements between the rows, 4 probabilities
+    assert draw(prob=A[0] + 4 * 100000, ld=100016) == WORKSPACE  # they fit
+    for x in A[1:6]:
+        assert draw(tok=x) == draw(prob=x) == WORKSPACE
+        assert draw(tok=x + 4) == draw(prob=x - 12) == draw(prob=x + 12) == INVALID
+
+    def look(tok=A[0], out=A[1], os=64):
+        return lib.dh_embed(P(A[2]), 64, P(tok), 4, 1000, 64, binding.F32, F(1.0), P(out), os, None)
+    assert look(tok=A[1]) == look(tok=A[1] + 1000) == look(tok=A[1] - 8) == look(out=A[0] - 64) == INVALID
+
+    def grad(tok=A[0], out=A[1], ts=64):
+        return lib.dh_embed_backward(P(A[2]), 64, P(tok), 4, 1000, 64, binding.F32, F(1.0), 0, P(out), ts, P(0), 0,
+                                     None)
+    assert grad() == WORKSPACE and grad(tok=A[1] + 256) == INVALID
+    assert grad(tok=A[1] + 256, ts=72) == WORKSPACE and grad(tok=A[1] + 260, ts=68) == INVALID
+
+    def norm(y=A[1], w=A[2], b=A[3], st=A[4], eps=1e-5):
+        return lib.dh_layer_norm(P(A[0]), 64, P(w), P(b), 4, 64, binding.F32, binding.F32, F(eps), P(y), 64, P(st),
+                                 None)
+    for bad in (dict(w=A[1] + 512), dict(b=A[1] + 512), dict(st=A[0] + 8), dict(st=A[1] + 1000), dict(st=A[2] + 248),
+                dict(st=A[3] - 24), dict(y=A[4] - 1000)):
+        assert norm(**bad) == INVALID
+
+    def back(g=A[0], x=A[1], st=A[2], w=A[3], dx=A[4], dw=A[5], db=A[6], xs=64):
+        return lib.dh_layer_norm_backward(P(g), 64, P(x), xs, P(st), P(w), 4, 64, binding.F32, binding.F32, P(dx), 64,
+                                          P(dw), P(db), P(0), 0, None)
+    assert back() == back(dx=A[0]) == back(dx=A[1]) == WORKSPACE
+    for bad in (dict(dx=A[2]), dict(dx=A[3] - 800), dict(dw=A[0]), dict(dw=A[1] + 64), dict(db=A[2] + 24), dict(dw=A[3]),
+                dict(db=A[4] + 768), dict(db=A[5] + 128), dict(dw=A[6])):
+        assert back(**bad) == INVALID, bad
+    assert back(dw=A[1] + 256, xs=128) == WORKSPACE and back(dw=A[1] + 260, xs=128) == INVALID

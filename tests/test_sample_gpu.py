@@ -454,3 +454,22 @@ def test_without_probabilities():
                                dh.BF16, token.data_ptr(), None, ws.data_ptr(), nbytes,
                                torch.cuda.current_stream().cuda_stream)
         assert status == 0 and torch.equal(token, want)
+
+
+def test_results_in_the_place_of_settings():
+    """A row's token or probability over its own uniform or setting, searched rows and rows of one block among them."""
+    for V, N in ((400, 30), (60000, 30)):
+        z, u = rows(N, V, "bf16", seed=V)
+        z[::2] = (0.5 * torch.randn(V, generator=torch.Generator().manual_seed(3))).bfloat16().to(DEV)
+        at = torch.arange(N, device=DEV)
+        given = {"temperature": 0.7 + 0.1 * (at % 5).float(), "top_k": (at % 4 * 50).int(),
+                 "top_p": 1 - 0.05 * (at % 3).float(), "min_p": 0.001 * (at % 2).float()}
+        want = dh.sample(z, u, **given)
+        for name in ("u", "temperature", "top_p", "min_p", "top_k"):
+            kw = {k: t.clone() for k, t in given.items()}
+            uu = u.clone()
+            place = uu if name == "u" else kw[name]
+            out = {"token_out" if name == "top_k" else "prob_out": place}
+            token, prob = dh.sample(z, uu, **kw, **out)
+            assert torch.equal(token, want[0]) and torch.equal(prob, want[1])
+            assert place is (token if name == "top_k" else prob)
