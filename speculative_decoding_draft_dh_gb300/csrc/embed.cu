@@ -128,6 +128,7 @@ constexpr int TS_WARPS = TS_THREADS / 32;
 constexpr int TS_BITS = 9;   // at most, per pass
 constexpr int TS_ITEMS = 8;  // rows of 32 pairs of a warp at a time
 constexpr int TS_RANKS = 8;  // blocks of the cluster, at most
+constexpr int TS_FEW = 2048;  // tokens that one block sorts, at most
 
 // The lanes whose digit is this lane's, among those that have one.  By a ballot per bit: a match instruction takes
 // an SM many times as long (a sort of 32768 tokens 27 us with it).
@@ -438,7 +439,8 @@ __global__ void __launch_bounds__(32 * EJ_WARPS) k_embed_join(EmbedArgs a, GradP
   }
 }
 
-// Pairs per chunk: 64, fewer where that leaves SMs without a block.  (1001 columns of fp32, with 64, 16 and 8 in a
+// Pairs per chunk: 64, fewer where that leaves the 152 SMs with less than two blocks each.  (The workspace goes by it, whose
+// size is asked for without a device.)  (1001 columns of fp32, with 64, 16 and 8 in a
 // chunk: 2000 tokens 25, 17.1 and 16.5 us, 5000 tokens 29, 20.2 and 22.6, 20011 tokens 40.5, 44 and 54.)
 int chunk_of(int N) { return N >= 64 * 304 ? 64 : N >= 16 * 304 ? 16 : 8; }
 
@@ -492,8 +494,9 @@ cudaError_t launch_sort(const Ctx& c, const EmbedArgs& a, int passes, uint2* con
   static unsigned long long smem_done = 0;
   const cudaError_t e = allow_max_smem(k_token_sort<BITS>, c.device, &smem_done);
   if (e != cudaSuccess) return e;
-  // one block while a warp of it has no more pairs than it keeps in registers
-  const unsigned ranks = a.N > 32 * TS_WARPS * TS_ITEMS / 2 ? TS_RANKS : 1;
+  // one block for few tokens (gradients of 64 fp32 columns, 4096 rows: 1000 tokens 13.5 us, 15.3 by the cluster; 2000 tokens
+  // 15.9 and 16.0; 4000 tokens 21.5 and 17.1)
+  const unsigned ranks = a.N > TS_FEW ? TS_RANKS : 1;
   return launch_clusters(c, "token_sort", k_token_sort<BITS>, ranks, dim3(ranks), dim3(TS_THREADS),
                          (size_t)TS_WARPS * (1u << BITS) * 4, a.tokens, a.N, a.vocab, passes, buf[0], buf[1], present);
 }
