@@ -916,7 +916,8 @@ def _hidden_out(t, name, shape, dtype, dev):
 
 def embed(table, tokens, *, scale=1.0, out=None, stream=None):
     """scale * table[tokens] (dh_embed): table [vocab, d] (bf16 or fp32, rows may be strided), tokens int32 [N]; a
-    token outside the vocabulary (padding) has a row of zeros.  Returns [N, d] in the table's dtype."""
+    token outside the vocabulary (padding) has a row of zeros.  Returns [N, d] in the table's dtype.  Outside of
+    autograd: layers.embedding is the differentiable form."""
     lib = load_library()
     dt, index = _hidden(table, "table", None)
     vocab, d = table.shape
@@ -984,7 +985,8 @@ def _norm_params(x, index, weight, bias, dtype=None):
 def layer_norm(x, weight=None, bias=None, *, eps=1e-5, with_stats=False, out=None, stats_out=None, stream=None):
     """Layer norm of the rows x [N, d] (bf16 or fp32, rows may be strided; dh_layer_norm); weight and bias [d] in
     fp32 or x's dtype.  out may be x itself.  Returns (y in x's dtype, stats fp32 [N, 2] or None: each row's mean and
-    1 / sqrt(variance + eps), which the gradient takes)."""
+    1 / sqrt(variance + eps), which the gradient takes).  Outside of autograd, here and under the package's name:
+    layers.layer_norm is the differentiable form, which returns y alone."""
     lib = load_library()
     dt, index = _hidden(x, "x", None)
     N, d = x.shape

@@ -4,7 +4,7 @@
 // The bound is HBM: a row is read once and written once.  A row belongs to a group of threads, a vector of 16 bytes
 // each or up to four; a block's groups walk over rows of their own, with the next rows on their way in shared memory
 // while the present one is reduced in registers.  Once the memory is kept busy, the instructions count: they are
-// packed in pairs, and the parameters wait in shared memory as fp32.  32768 rows of 5120 bf16: forward 104 us
+// packed in pairs, and the parameters wait in shared memory as fp32.  32768 rows of 5120 bf16: forward 103 us
 // (671 MB, 6.5 TB/s), backward 173 (1.0 GB, 5.8 TB/s).  (The next rows in registers instead: 154 to 215 and 312 to 587;
 // the parameters by way of L1: up to 313 backward.)
 // Forward: the mean first, then the sums of x - mean and of its square, so that the variance loses nothing to a
@@ -254,7 +254,7 @@ __device__ __forceinline__ float pair_sum(f32x2 v) {
   return a + b;
 }
 
-constexpr int NF_STAGES = 3;  // 32768 rows of 5120 bf16: 104 us, 109 with 2, 103 with 4
+constexpr int NF_STAGES = 3;  // 32768 rows of 5120 bf16: 103 us, as with 2, 107 with 4
 constexpr int NF_WARPS = 16;  // of a row, at most
 // Registers of a thread with NV vectors.  With four, NF_TIGHT where they let more groups run (32768 rows of 5120: 4 groups
 // 103.6 us, 3 with 128 registers 106.6), else 128 (20000 rows of 8192: 2 groups of either kind 105 and 111).
@@ -271,7 +271,8 @@ constexpr int threads_by_regs(int regs) { return 65536 / 4 / 32 / regs * 128 < 1
 // to a mean far from 0 or to outliers, wherever they stand.  (About the mean of a single thread's elements they add up to
 // d / 8 times an outlier's, which then cancels.)  x - c, which the result is taken from, is rounded by 2^-24 |c|: that
 // of an outlier's 256th part, less than the mean's own error allows.  Of means only differences and halves are added
-// up: equal elements have no deviation at all.  A warp that lies within the row (`whole`) needs no masks: 20000 rows of 5119 bf16 111 us, 129 with them.
+// up: equal elements have no deviation at all.  A warp that lies within the row (`whole`) needs no masks: 20000 rows of
+// 5119 bf16 111 us, 129 with them.
 template <typename T, typename P, int NV, bool VEC, bool SHARED, int REGS>
 __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
   using C = Cols<T, VEC, NV>;
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(NW_THREADS) k_norm_wide(NormArgs a) {
 }
 
 template <typename T, typename P>
-__global__ void __launch_bounds__(NW_THREADS) k_norm_backward_wide(NormArgs a, bool sums) {
+__global__ void __launch_bounds__(NW_THREADS) k_norm_backward_wide(NormArgs a) {
   __shared__ float2 sh[2][32];
   int turn = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -861,12 +862,12 @@ template <typename T, typename P, bool VEC>
 cudaError_t run_norm(const Ctx& c, const NormArgs& a) {
   constexpr int PER = Elem<T>::PER16;
   const int nvec = (a.d + PER - 1) / PER;
-  // one row per block and no parameters in shared memory where there are few rows (5120 bf16: 8 rows 2.5 us, 3.6 as
-  // many rows are done; 304 rows 3.1 and 3.8; 608 rows 5.7 and 5.2)
+  // one row per block and no parameters in shared memory where there are few rows (5120 bf16: 8 rows 2.6 us, 4.0 as
+  // many rows are done; 304 rows 3.3 and 4.1; 608 rows 5.9 and 4.3)
   const bool few = a.N <= 2 * c.num_sms;
   if (nvec <= 32) return run_norm_nv<T, P, VEC, 1>(c, a, nvec, few);
   if (nvec <= 64 || (few && nvec <= 2 * 32 * NF_WARPS)) return run_norm_nv<T, P, VEC, 2>(c, a, nvec, few);
-  // (32768 rows of 5120 bf16 with 2 vectors per thread 121 us instead of 104, with 8 129)
+  // (32768 rows of 5120 bf16 with 2 vectors per thread 135 us instead of 103)
   return run_norm_nv<T, P, VEC, 4>(c, a, nvec, few);
 }
 
@@ -949,7 +950,7 @@ cudaError_t pick_backward(const Ctx& c, NormArgs a) {
     }
     if (e == cudaSuccess && a.y)
       e = launch_pdl(c, "norm_backward", k_norm_backward_wide<T, P>, dim3(least(a.N, 2LL * c.num_sms)),
-                     dim3(NW_THREADS), 0, a, sums);
+                     dim3(NW_THREADS), 0, a);
   }
   if (e != cudaSuccess || !sums) return e;
   return launch_pdl(c, "norm_join", k_norm_join<P>, dim3((unsigned)((a.part_ld + NJ_COLS - 1) / NJ_COLS), 2u),

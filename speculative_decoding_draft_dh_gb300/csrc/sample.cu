@@ -5,7 +5,7 @@
 // one at which the prefix's running sum of weights passes u times its mass.  So a token far down the order matters
 // only by its share of the row's mass, and that only where no top-k leaves it out.
 //   k_sample_scan   the one pass over the logits: the largest of every group of 16 vectors and, of rows whose mass
-//                   is needed, every segment's mass.  A warp takes a segment of 64 vectors, so that rows of any
+//                   is needed, every segment's mass.  A warp takes a segment of 128 vectors, so that rows of any
 //                   number fill the SMs.  Its bound is HBM (512 rows of 151936 bf16: 25 us, 156 MB at 6.2 TB/s);
 //                   with masses, the 25 instructions of a weight (72 us, the issue slots 74% full).
 //   k_sample_pick   a block per row.  A bound below which nothing can be drawn: the top_k-th largest group maximum,
@@ -339,8 +339,8 @@ struct SampleSmem : Scratch {
   };
   u64 list[SP_LIST];  // key << 32 | ~id: the order is that of these numbers, descending
 };
-// Blocks of a cluster: 512 flat rows 558 us, one 67, 512 rows at top-p 0.95 189; with 2 433, 81 and 194; with 8 1060,
-// 66 and 199.
+// Blocks of a cluster: 512 flat rows 534 us, one 61, 512 rows at top-p 0.95 154.  More rows at once would be faster with 2
+// (405, 86 and 166), one with 8 (1057, 56 and 225); a batch of which some rows are searched is the usual case.
 constexpr int SS_RANKS = 4;
 struct SearchSmem : Scratch {
   static constexpr int RANKS = SS_RANKS;
