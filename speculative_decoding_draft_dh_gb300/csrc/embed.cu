@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(EM_THREADS) k_embed(EmbedArgs a, unsigned unit
 #pragma unroll
   for (int q = 0; q < VECS; ++q) {
     if (row[q] < 0) continue;
-    if (by[q] != 1.f) {
+    if (a.scale != 1.f) {
       float z[PER];
       Elem<T>::unpack(x[q], z);
 #pragma unroll
