@@ -4,8 +4,8 @@
 // The bound is HBM: a row is read once and written once.  A row belongs to a group of threads, a vector of 16 bytes
 // each or up to four; a block's groups walk over rows of their own, with the next rows on their way in shared memory
 // while the present one is reduced in registers.  Once the memory is kept busy, the instructions count: they are
-// packed in pairs, and the parameters wait in shared memory as fp32.  32768 rows of 5120 bf16: forward 103 us
-// (671 MB, 6.5 TB/s), backward 173 (1.0 GB, 5.8 TB/s).  (The next rows in registers instead: 154 to 215 and 312 to 587;
+// packed in pairs, and the parameters wait in shared memory as fp32.  32768 rows of 5120 bf16: forward 102 us
+// (671 MB, 6.6 TB/s), backward 173 (1.0 GB, 5.8 TB/s).  (The next rows in registers instead: 154 to 215 and 312 to 587;
 // the parameters by way of L1: up to 313 backward.)
 // Forward: the mean first, then the sums of x - mean and of its square, so that the variance loses nothing to a
 // mean far from 0 (the two-pass form with the correction of Chan, Golub and LeVeque).
@@ -257,7 +257,7 @@ __device__ __forceinline__ float pair_sum(f32x2 v) {
 constexpr int NF_STAGES = 3;  // 32768 rows of 5120 bf16: 103 us, as with 2, 107 with 4
 constexpr int NF_WARPS = 16;  // of a row, at most
 // Registers of a thread with NV vectors.  With four, NF_TIGHT where they let more groups run (32768 rows of 5120: 4 groups
-// 103.6 us, 3 with 128 registers 106.6), else 128 (20000 rows of 8192: 2 groups of either kind 105 and 111).
+// 102 us, 3 with 128 registers 106), else 128 (20000 rows of 8192: 2 groups of either kind 104 and 111).
 constexpr int norm_regs(int nv) { return nv == 1 ? 64 : nv == 2 ? 80 : 128; }
 constexpr int NF_TIGHT = 96;
 // Threads of a block that have an SM's registers to themselves: a quarter of them to each four warps' first one.
@@ -269,11 +269,13 @@ constexpr int threads_by_regs(int regs) { return 65536 / 4 / 32 / regs * 128 < 1
 // warps' means (the formulas of Chan, Golub and LeVeque).  Of what is joined one part in four or more enters the value
 // that it is joined about, so the squares add up to about four times those about the mean at most, and nothing is lost
 // to a mean far from 0 or to outliers, wherever they stand.  (About the mean of a single thread's elements they add up to
-// d / 8 times an outlier's, which then cancels.)  x - c, which the result is taken from, is rounded by 2^-24 |c|: that
-// of an outlier's 256th part, less than the mean's own error allows.  Of means only differences and halves are added
-// up: equal elements have no deviation at all.  A warp that lies within the row (`whole`) needs no masks: 20000 rows of
-// 5119 bf16 111 us, 129 with them.
-template <typename T, typename P, int NV, bool VEC, bool SHARED, int REGS>
+// d / 8 times an outlier's, which then cancels.)  Of means only differences and halves are added up: equal elements have
+// no deviation at all.
+// x - c, which the result is taken from, is rounded by 2^-24 |c|: that of an outlier's 256th part, less than the mean's
+// own error allows.  But a warp that the row ends in may have few columns, of which c is mostly an outlier's: its result
+// is taken from x itself.  A warp that lies within the row (`whole`) needs no masks (20000 rows of 5119 bf16 111 us, 129
+// with them), and rows of whole vectors and WHOLE warps no choice (32768 rows of 5120 bf16 102 us, 110 with one).
+template <typename T, typename P, int NV, bool VEC, bool WHOLE, bool SHARED, int REGS>
 __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
   using C = Cols<T, VEC, NV>;
   using S = SharedParams<T, P, VEC, NV>;
@@ -298,7 +300,7 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
       if (v < REF) first = mine;
     }
   const float inv_first = first ? 1.f / (float)first : 0.f;
-  const bool whole = (warp + 1) * C::WARP <= a.d;
+  const bool whole = WHOLE || (warp + 1) * C::WARP <= a.d;
   const bool empty = __any_sync(0xFFFFFFFFu, first == 0);  // the row ends within the warp
   const float their_count = (float)min(max(a.d - peer * C::WARP, 0), C::WARP);
   int turn = 0;
@@ -357,7 +359,7 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
       for (int o = 16 >> (NV - REF + 1); o > 0; o >>= 1) mix(o);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        // and stay 0
+        // and count for nothing
         const f32x2 shift = both(W || !VEC || v * PER < mine ? -c : 0.f);
 #pragma unroll
         for (int e = 0; e < HALF; ++e) {
@@ -367,18 +369,15 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
             unpack2(t, p, q);
             t = pack2(v * PER + 2 * e < mine ? p : 0.f, v * PER + 2 * e + 1 < mine ? q : 0.f);
           }
-          z[v][e] = t;
+          if constexpr (VEC || W) z[v][e] = t;
           d1[e & 1] = add2(d1[e & 1], t);
           d2[e & 1] = fma2(t, t, d2[e & 1]);
         }
       }
     };
-    if (!VEC && whole) take(std::true_type{});
-    else take(std::false_type{});
-    next += x_step;
-    row += x_step;
-    stage = stage + 1 == NF_STAGES ? 0 : stage + 1;
-    const float own = c;
+    if (WHOLE || (!VEC && whole)) take(std::true_type{});
+    else if constexpr (!WHOLE) take(std::false_type{});
+    float own = c;  // what has been taken from z, or, of a warp that the row ends in, will be
     float part = fold(pair_sum(add2(d1[0], d1[1])), pair_sum(add2(d2[0], d2[1])), 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
@@ -412,8 +411,19 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
     if (var < 0.f) var = 0.f;  // a NaN stays
     const float rs = 1.f / sqrtf(var + a.eps);
     // the mean, rounded, and what that leaves out
-    if (a.stats_out && me == 0) a.stats_out[n] = make_float2(c + delta, rs);
-    const f32x2 rstd = both(rs), back = both(((own - c) - delta) * rs);
+    const float mean = c + delta, rest = (c - mean) + delta;  // rounded, and what that leaves out
+    if (a.stats_out && me == 0) a.stats_out[n] = make_float2(mean, rs);
+    if (!whole) {
+      // (the row's slot is filled again in the next round)
+      own = mean;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (VEC) unpack_pairs<T>(ring.get(row, stage, v), z[v]);
+#pragma unroll
+        for (int e = 0; e < HALF; ++e) z[v][e] = add2(z[v][e], both(-mean));
+      }
+    }
+    const f32x2 rstd = both(rs), back = both(((own - mean) - rest) * rs);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       f32x2 w[HALF], b[HALF];
@@ -435,6 +445,9 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
       C::store(out, me, v, a.d, round_pairs<T>(z[v]));
     }
     out += y_step;
+    next += x_step;
+    row += x_step;
+    stage = stage + 1 == NF_STAGES ? 0 : stage + 1;
   }
 }
 
@@ -839,7 +852,7 @@ cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
   const size_t ring = NF_STAGES * Ring<T, VEC, NV>::bytes(width);
   const size_t shared = 2 * SharedParams<T, P, VEC, NV>::bytes(width);
   if (few)
-    return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false, norm_regs(NV)>, (unsigned)a.N, (unsigned)width, ring, a,
+    return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false, false, norm_regs(NV)>, (unsigned)a.N, (unsigned)width, ring, a,
                        width);
   const int barriers = width > 32 ? 15 : 32;  // one per group, but for rows of one warp
   auto groups_by = [&](int regs) {
@@ -851,11 +864,16 @@ cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
     const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
     return launch_ring(c, "norm", kernel, grid, (unsigned)width * groups, shared + ring * groups, a, width);
   };
-  const unsigned groups = groups_by(norm_regs(NV));
-  if constexpr (NV == 4)
-    if (groups_by(NF_TIGHT) > groups)
-      return run(k_norm<T, P, NV, VEC, true, NF_TIGHT>, groups_by(NF_TIGHT));
-  return run(k_norm<T, P, NV, VEC, true, norm_regs(NV)>, groups);
+  auto run_whole = [&](auto whole) {
+    constexpr bool W = decltype(whole)::value;
+    const unsigned groups = groups_by(norm_regs(NV));
+    if constexpr (NV == 4)
+      if (groups_by(NF_TIGHT) > groups) return run(k_norm<T, P, NV, VEC, W, true, NF_TIGHT>, groups_by(NF_TIGHT));
+    return run(k_norm<T, P, NV, VEC, W, true, norm_regs(NV)>, groups);
+  };
+  if constexpr (VEC)
+    if (a.d % Cols<T, VEC, NV>::WARP == 0) return run_whole(std::true_type{});
+  return run_whole(std::false_type{});
 }
 
 template <typename T, typename P, bool VEC>

@@ -329,3 +329,15 @@ def test_column_sums_over_many_rows():
         for got, term in ((dw, g.double() * hat), (db, g.double())):
             off = (got.double() - N * term[0]).abs() / (N * term[0].abs()).clamp(min=1e-30)
             assert off.max() <= (32 + 8) * U, (N, d, dtype, off.max() / U)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [3, 700])
+@pytest.mark.parametrize("d,k", [(7714, 8), (5656, 8), (7200, 2), (7711, 3), (1032, 4), (4104, 8), (545, 16)])
+def test_outliers_in_a_short_last_warp(d, k, N, dtype):
+    """The last columns are all that some warp has, and most of them are outliers."""
+    for i, value in enumerate((3e3, 1e6, -1e9)):
+        for ld, base in ((d, 0), (d + 1, 0), (d, 2)):
+            x = matrix(N, d, dtype, i, ld, base)
+            x[:, d - k:] = value
+            check_forward(x, None, None)
