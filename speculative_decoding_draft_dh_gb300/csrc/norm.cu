@@ -263,6 +263,10 @@ constexpr int NF_TIGHT = 96;
 // Threads of a block that have an SM's registers to themselves: a quarter of them to each four warps' first one.
 constexpr int threads_by_regs(int regs) { return 65536 / 4 / 32 / regs * 128 < 1024 ? 65536 / 4 / 32 / regs * 128 : 1024; }
 
+// How a row ends: with a whole warp, within a warp that has eight elements of each thread or more (or is the only one, so
+// that its c is no further out than the row's own deviations allow), or within a warp that has less.
+enum RowEnd { WHOLE, LONG, SHORT };
+
 // A block holds blockDim / width groups of `width` threads, each of which walks over rows of its own; the groups
 // share the parameters (SHARED: in shared memory).  Barriers are a group's.
 // A warp's sums are about the mean c of its threads' first eight elements each, the row's about the mean of up to four
@@ -272,10 +276,11 @@ constexpr int threads_by_regs(int regs) { return 65536 / 4 / 32 / regs * 128 < 1
 // d / 8 times an outlier's, which then cancels.)  Of means only differences and halves are added up: equal elements have
 // no deviation at all.
 // x - c, which the result is taken from, is rounded by 2^-24 |c|: that of an outlier's 256th part, less than the mean's
-// own error allows.  But a warp that the row ends in may have few columns, of which c is mostly an outlier's: its result
-// is taken from x itself.  A warp that lies within the row (`whole`) needs no masks (20000 rows of 5119 bf16 111 us, 129
-// with them), and rows of whole vectors and WHOLE warps no choice (32768 rows of 5120 bf16 102 us, 110 with one).
-template <typename T, typename P, int NV, bool VEC, bool WHOLE, bool SHARED, int REGS>
+// own error allows.  But a warp that the row ends in may have less than those eight of each thread, and c is mostly an
+// outlier's: its result is taken from x itself (a choice that costs 32768 rows of 5120 bf16 8 us of 110).
+// Warps and vectors that lie within the row are read and summed without masks in rows off 16 bytes (20000 rows of 8191
+// bf16 166 us, 200 with masks, 182 with those of the last warp only; of 2047 42 and 51).
+template <typename T, typename P, int NV, bool VEC, RowEnd END, bool SHARED, int REGS>
 __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
   using C = Cols<T, VEC, NV>;
   using S = SharedParams<T, P, VEC, NV>;
@@ -300,7 +305,8 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
       if (v < REF) first = mine;
     }
   const float inv_first = first ? 1.f / (float)first : 0.f;
-  const bool whole = WHOLE || (warp + 1) * C::WARP <= a.d;
+  const bool whole = (warp + 1) * C::WARP <= a.d;
+  const int inside = (a.d - warp * C::WARP) / (32 * PER);  // vectors of the warp that lie within the row
   const bool empty = __any_sync(0xFFFFFFFFu, first == 0);  // the row ends within the warp
   const float their_count = (float)min(max(a.d - peer * C::WARP, 0), C::WARP);
   int turn = 0;
@@ -332,8 +338,13 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
     f32x2 d1[2] = {0, 0}, d2[2] = {0, 0};
     auto take = [&](auto whole_warp) {
       constexpr bool W = decltype(whole_warp)::value;
+      // (vectors that lie within the row need no masks)
+      auto get = [&](int v) {
+        if (W || VEC || v < inside) unpack_pairs<T>(ring.template get<true>(row, stage, v), z[v]);
+        else unpack_pairs<T>(ring.template get<false>(row, stage, v), z[v]);
+      };
 #pragma unroll
-      for (int v = 0; v < REF; ++v) unpack_pairs<T>(ring.template get<W>(row, stage, v), z[v]);
+      for (int v = 0; v < REF; ++v) get(v);
       // past the row's end the elements are 0
       f32x2 f = add2(z[0][0], z[0][1]);
       if constexpr (HALF == 4) f = add2(f, add2(z[0][2], z[0][3]));
@@ -351,7 +362,7 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
       mix(16);
 #pragma unroll
       for (int v = REF; v < NV; ++v) {
-        unpack_pairs<T>(ring.template get<W>(row, stage, v), z[v]);
+        get(v);
         mix(16 >> (v - REF + 1));
       }
       ring.fetch(next, n + (NF_STAGES - 1) * step < rows, stage == 0 ? NF_STAGES - 1 : stage - 1);
@@ -361,23 +372,27 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
       for (int v = 0; v < NV; ++v) {
         // and count for nothing
         const f32x2 shift = both(W || !VEC || v * PER < mine ? -c : 0.f);
+        auto terms = [&](auto masked) {
 #pragma unroll
-        for (int e = 0; e < HALF; ++e) {
-          f32x2 t = add2(z[v][e], shift);
-          if constexpr (!VEC && !W) {
-            float p, q;
-            unpack2(t, p, q);
-            t = pack2(v * PER + 2 * e < mine ? p : 0.f, v * PER + 2 * e + 1 < mine ? q : 0.f);
+          for (int e = 0; e < HALF; ++e) {
+            f32x2 t = add2(z[v][e], shift);
+            if constexpr (decltype(masked)::value) {
+              float p, q;
+              unpack2(t, p, q);
+              t = pack2(v * PER + 2 * e < mine ? p : 0.f, v * PER + 2 * e + 1 < mine ? q : 0.f);
+            }
+            if constexpr (END != SHORT || VEC || W) z[v][e] = t;
+            d1[e & 1] = add2(d1[e & 1], t);
+            d2[e & 1] = fma2(t, t, d2[e & 1]);
           }
-          if constexpr (VEC || W) z[v][e] = t;
-          d1[e & 1] = add2(d1[e & 1], t);
-          d2[e & 1] = fma2(t, t, d2[e & 1]);
-        }
+        };
+        if (W || VEC || v < inside) terms(std::false_type{});
+        else if (v == inside) terms(std::true_type{});
       }
     };
-    if (WHOLE || (!VEC && whole)) take(std::true_type{});
-    else if constexpr (!WHOLE) take(std::false_type{});
-    float own = c;  // what has been taken from z, or, of a warp that the row ends in, will be
+    if (END == WHOLE || (!VEC && whole)) take(std::true_type{});
+    else if constexpr (END != WHOLE) take(std::false_type{});
+    float own = c;  // what has been taken from z, or will be
     float part = fold(pair_sum(add2(d1[0], d1[1])), pair_sum(add2(d2[0], d2[1])), 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
@@ -413,7 +428,7 @@ __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
     // the mean, rounded, and what that leaves out
     const float mean = c + delta, rest = (c - mean) + delta;  // rounded, and what that leaves out
     if (a.stats_out && me == 0) a.stats_out[n] = make_float2(mean, rs);
-    if (!whole) {
+    if (END == SHORT && !whole) {
       // (the row's slot is filled again in the next round)
       own = mean;
 #pragma unroll
@@ -851,9 +866,6 @@ cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
   const int width = round32((nvec + NV - 1) / NV);
   const size_t ring = NF_STAGES * Ring<T, VEC, NV>::bytes(width);
   const size_t shared = 2 * SharedParams<T, P, VEC, NV>::bytes(width);
-  if (few)
-    return launch_ring(c, "norm", k_norm<T, P, NV, VEC, false, false, norm_regs(NV)>, (unsigned)a.N, (unsigned)width, ring, a,
-                       width);
   const int barriers = width > 32 ? 15 : 32;  // one per group, but for rows of one warp
   auto groups_by = [&](int regs) {
     const long long fit = (SM_SMEM - (long long)shared) / (long long)ring;
@@ -864,16 +876,22 @@ cudaError_t run_norm_nv(const Ctx& c, const NormArgs& a, int nvec, bool few) {
     const unsigned grid = least(((long long)a.N + groups - 1) / groups, c.num_sms);
     return launch_ring(c, "norm", kernel, grid, (unsigned)width * groups, shared + ring * groups, a, width);
   };
-  auto run_whole = [&](auto whole) {
-    constexpr bool W = decltype(whole)::value;
+  auto pick = [&](auto end) {
+    constexpr RowEnd S = decltype(end)::value;
+    if (few)
+      return launch_ring(c, "norm", k_norm<T, P, NV, VEC, S, false, norm_regs(NV)>, (unsigned)a.N, (unsigned)width,
+                         ring, a, width);
     const unsigned groups = groups_by(norm_regs(NV));
     if constexpr (NV == 4)
-      if (groups_by(NF_TIGHT) > groups) return run(k_norm<T, P, NV, VEC, W, true, NF_TIGHT>, groups_by(NF_TIGHT));
-    return run(k_norm<T, P, NV, VEC, W, true, norm_regs(NV)>, groups);
+      if (groups_by(NF_TIGHT) > groups) return run(k_norm<T, P, NV, VEC, S, true, NF_TIGHT>, groups_by(NF_TIGHT));
+    return run(k_norm<T, P, NV, VEC, S, true, norm_regs(NV)>, groups);
   };
-  if constexpr (VEC)
-    if (a.d % Cols<T, VEC, NV>::WARP == 0) return run_whole(std::true_type{});
-  return run_whole(std::false_type{});
+  const int last = a.d % Cols<T, VEC, NV>::WARP;  // columns of a warp that the row ends in
+  if constexpr (NV > 1)
+    if (width > 32 && last > 0 && last < 8 * 32) return pick(std::integral_constant<RowEnd, SHORT>{});
+  if constexpr (VEC && NV == 4)
+    if (last == 0) return pick(std::integral_constant<RowEnd, WHOLE>{});
+  return pick(std::integral_constant<RowEnd, LONG>{});
 }
 
 template <typename T, typename P, bool VEC>
