@@ -439,9 +439,9 @@ __global__ void __launch_bounds__(32 * EJ_WARPS) k_embed_join(EmbedArgs a, GradP
   }
 }
 
-// Pairs per chunk: 64, fewer where that leaves the 152 SMs with less than two blocks each.  (The workspace goes by it, whose
-// size is asked for without a device.)  (1001 columns of fp32, with 64, 16 and 8 in a
-// chunk: 2000 tokens 25, 17.1 and 16.5 us, 5000 tokens 29, 20.2 and 22.6, 20011 tokens 40.5, 44 and 54.)
+// Pairs per chunk: 64, fewer where that leaves the 152 SMs with less than two chunks each.  (The workspace goes by it,
+// whose size is asked for without a device.)  1001 columns of fp32, with 64, 16 and 8 in a chunk: 2000 tokens 25, 17.1
+// and 16.5 us, 5000 tokens 29, 20.2 and 22.6, 20011 tokens 40.5, 44 and 54.
 int chunk_of(int N) { return N >= 64 * 304 ? 64 : N >= 16 * 304 ? 16 : 8; }
 
 // Columns of a part, whole tiles of either type.

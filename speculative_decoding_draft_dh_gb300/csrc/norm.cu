@@ -256,30 +256,32 @@ __device__ __forceinline__ float pair_sum(f32x2 v) {
 
 constexpr int NF_STAGES = 3;  // 32768 rows of 5120 bf16: 103 us, as with 2, 107 with 4
 constexpr int NF_WARPS = 16;  // of a row, at most
-// Registers of a thread with NV vectors.  With four, NF_TIGHT where they let more groups run (32768 rows of 5120: 4 groups
-// 102 us, 3 with 128 registers 106), else 128 (20000 rows of 8192: 2 groups of either kind 104 and 111).
+// Registers of a thread with NV vectors.  With four, NF_TIGHT where they let more groups run (32768 rows of 5120: 4
+// groups 102 us, 3 with 128 registers 106), else 128 (20000 rows of 8192: 2 groups of either kind 104 and 111).
 constexpr int norm_regs(int nv) { return nv == 1 ? 64 : nv == 2 ? 80 : 128; }
 constexpr int NF_TIGHT = 96;
 // Threads of a block that have an SM's registers to themselves: a quarter of them to each four warps' first one.
-constexpr int threads_by_regs(int regs) { return 65536 / 4 / 32 / regs * 128 < 1024 ? 65536 / 4 / 32 / regs * 128 : 1024; }
+constexpr int threads_by_regs(int regs) {
+  return 65536 / 4 / 32 / regs * 128 < 1024 ? 65536 / 4 / 32 / regs * 128 : 1024;
+}
 
-// How a row ends: with a whole warp, within a warp that has eight elements of each thread or more (or is the only one, so
-// that its c is no further out than the row's own deviations allow), or within a warp that has less.
+// How a row ends: with a whole warp, within a warp that has eight elements of each thread or more (or is the only
+// one, so that its c is no further out than the row's own deviations allow), or within a warp that has less.
 enum RowEnd { WHOLE, LONG, SHORT };
 
 // A block holds blockDim / width groups of `width` threads, each of which walks over rows of its own; the groups
 // share the parameters (SHARED: in shared memory).  Barriers are a group's.
-// A warp's sums are about the mean c of its threads' first eight elements each, the row's about the mean of up to four
-// warps' means (the formulas of Chan, Golub and LeVeque).  Of what is joined one part in four or more enters the value
-// that it is joined about, so the squares add up to about four times those about the mean at most, and nothing is lost
-// to a mean far from 0 or to outliers, wherever they stand.  (About the mean of a single thread's elements they add up to
-// d / 8 times an outlier's, which then cancels.)  Of means only differences and halves are added up: equal elements have
-// no deviation at all.
-// x - c, which the result is taken from, is rounded by 2^-24 |c|: that of an outlier's 256th part, less than the mean's
-// own error allows.  But a warp that the row ends in may have less than those eight of each thread, and c is mostly an
-// outlier's: its result is taken from x itself (a choice that costs 32768 rows of 5120 bf16 8 us of 110).
-// Warps and vectors that lie within the row are read and summed without masks in rows off 16 bytes (20000 rows of 8191
-// bf16 166 us, 200 with masks, 182 with those of the last warp only; of 2047 42 and 51).
+// A warp's sums are about the mean c of its threads' first eight elements each, the row's about the mean of up to
+// four warps' means (the formulas of Chan, Golub and LeVeque).  Of what is joined one part in four or more enters
+// the value that it is joined about, so the squares add up to about four times those about the mean at most, and
+// nothing is lost to a mean far from 0 or to outliers, wherever they stand.  (About the mean of a single thread's
+// elements they add up to d / 8 times an outlier's, which then cancels.)  Of means only differences and halves are
+// added up: equal elements have no deviation at all.
+// x - c, which the result is taken from, is rounded by 2^-24 |c|: that of an outlier's 256th part, less than the
+// mean's own error allows.  But a warp that the row ends in may have less than those eight of each thread, and c is
+// mostly an outlier's: its result is taken from x itself (a choice that costs 32768 rows of 5120 bf16 8 us of 110).
+// Warps and vectors that lie within the row are read and summed without masks in rows off 16 bytes (20000 rows of
+// 8191 bf16 166 us, 200 with masks, 182 with those of the last warp only; of 2047 42 and 51).
 template <typename T, typename P, int NV, bool VEC, RowEnd END, bool SHARED, int REGS>
 __global__ void __maxnreg__(REGS) k_norm(NormArgs a, int width) {
   using C = Cols<T, VEC, NV>;
@@ -729,10 +731,10 @@ struct LongSum {
   __device__ __forceinline__ float value() const { return fabsf(sum) < INFINITY ? sum + rest : sum; }
 };
 
-// dw and db of a tile of columns over a share of the rows, NC_RUN of them at a time in one fp32 sum: a share of a million
-// rows of 65536 columns is 250000 rows, and their errors would add up.  The runs' sums wait in shared memory and four rows
-// are loaded ahead, so that all blocks of the grid run at once with 32 registers (the gradient of 10000 rows of 12288
-// bf16 433 us; 494 with a run unrolled by four, 653 with 40 registers).
+// dw and db of a tile of columns over a share of the rows, NC_RUN of them at a time in one fp32 sum: a share of a
+// million rows of 65536 columns is 250000 rows, and their errors would add up.  The runs' sums wait in shared memory
+// and four rows are loaded ahead, so that all blocks of the grid run at once with 32 registers (the gradient of
+// 10000 rows of 12288 bf16 433 us; 494 with a run unrolled by four, 653 with 40 registers).
 constexpr int NC_THREADS = 256, NC_BLOCKS = 8, NC_RUN = 32, NC_AHEAD = 4;
 template <typename T>
 __global__ void __launch_bounds__(NC_THREADS, NC_BLOCKS) k_norm_columns(NormArgs a) {
@@ -786,8 +788,8 @@ __global__ void __launch_bounds__(NC_THREADS, NC_BLOCKS) k_norm_columns(NormArgs
   part[a.part_ld + col] = b.value();
 }
 
-// The blocks' sums, added in a fixed order, the last steps without loss, and rounded once.  They stand in the order of the threads' columns, nv
-// vectors of `per` of a thread and `width` threads (nv 0: in the order of the columns).
+// The blocks' sums, added in a fixed order, the last steps without loss, and rounded once.  They stand in the order
+// of the threads' columns, nv vectors of `per` of a thread and `width` threads (nv 0: in the order of the columns).
 constexpr int NJ_COLS = 32, NJ_ROWS = 32;
 template <typename P>
 __global__ void __launch_bounds__(NJ_COLS * NJ_ROWS) k_norm_join(NormArgs a, int parts, int width, int nv, int per,
