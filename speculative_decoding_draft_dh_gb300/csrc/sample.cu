@@ -23,10 +23,11 @@
 //
 // Which token a uniform falls on hangs on the running sums, so the weights exp((z - max)/T) are integers: fixed
 // point with `frac` fraction bits relative to a power of two near the largest, frac = 62 - log2(vocab) (52 at most),
-// so that a row's masses fit 64 bits.  Their sums are exact, whatever their order; what is rounded is each weight, by
-// half a unit of 2^-frac of the largest (for 2^18 ids half the weight of a token 30 T below the largest logit) and by about
-// 2^-28 of itself.  2^(z c), c = log2(e)/T, is taken as 2^(k/64) 2^r with k the rounded 64 z c: 2^(k/64) from a table, exact to 2^-29, and 2^r - 1, |r| < 2^-7 + 2^-9,
-// by a cubic in fp32 whose rounding is below 2^-29 of the weight; c in two floats, so that z c is exact to 2^-31.
+// so that a row's masses fit 64 bits.  Their sums are exact, whatever their order; what is rounded is each weight,
+// by half a unit of 2^-frac of the largest (for 2^18 ids half the weight of a token 30 T below the largest logit)
+// and by about 2^-28 of itself.  2^(z c), c = log2(e)/T, is taken as 2^(k/64) 2^r with k the rounded 64 z c:
+// 2^(k/64) from a table, exact to 2^-29, and 2^r - 1, |r| < 2^-7 + 2^-9, by a cubic in fp32 whose rounding is below
+// 2^-29 of the weight; c in two floats, so that z c is exact to 2^-31.
 #include "layers.cuh"
 #include "rows.cuh"
 
